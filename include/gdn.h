@@ -327,6 +327,100 @@ int gdn_segment_fold(const void* k, const void* v, const float* g, const float* 
                      int chunk, int n_segments, void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * Single-token forms: one token per row, the row's state updated in place.
+ * Per row r, value head j (key head kh = j / (Hv/Hk)) and state h:
+ *   gdn_delta_step   h <- exp(g) (I - beta k k^T) h + beta k v^T,  o = h^T q
+ *                    (one token of gdn_chunk_fwd's recurrence);
+ *   gdn_decay_step   h <- exp(decay) h + k v^T,                   o = h^T q
+ *                    (one token of gdn_decay_fwd's recurrence).
+ * q, k [R, Hk, d_k] and v [R, Hv, d_v] bf16; g, beta [R, Hv] fp32; decay [Hv]
+ * fp32 (the log-decay of each head); state [n_slots, Hv, d_k, d_v] fp32, read
+ * and written; o [R, Hv, d_v] bf16.  Row r works on state slots[r] (int32;
+ * NULL: state r).  A slot outside [0, n_slots) marks a row without a state (a
+ * padded batch entry): its output is zero and no state is touched.  Two rows
+ * with one slot give that state an undefined value.
+ * q_stride, k_stride, v_stride: elements from a row to the next (at least
+ * H * 128, a multiple of 8), so that q, k and v may be parts of one buffer.
+ * No workspace.
+ */
+int gdn_delta_step(const void* q, const void* k, const void* v, const float* g, const float* beta,
+                   float* state, const int* slots, void* o, int R, int n_slots, int Hk, int Hv,
+                   int d_k, int d_v, long long q_stride, long long k_stride, long long v_stride,
+                   void* stream);
+int gdn_decay_step(const void* q, const void* k, const void* v, const float* decay, float* state,
+                   const int* slots, void* o, int R, int n_slots, int Hk, int Hv, int d_k, int d_v,
+                   long long q_stride, long long k_stride, long long v_stride, void* stream);
+
+/*
+ * Linear attention with a decay for each head, over packed sequences.  Per
+ * sequence and value head j (key head kh = j / (Hv/Hk)), w = decay[j] <= 0:
+ *     h_t = exp(w) h_{t-1} + k_t v_t^T,   o_t = h_t^T q_t,   h_{-1} = h0,   hT = h_{T-1}.
+ * The decays are constants of the model: no gradient of them is formed.
+ * q, k [total, Hk, d_k], v [total, Hv, d_v] bf16 (strides as for the
+ * single-token forms); decay [Hv] fp32; h0, hT [n_seqs, Hv, d_k, d_v] fp32
+ * (NULL = zero / not written); o [total, Hv, d_v] bf16.  Sequence s holds the
+ * rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1 (int32 [n_seqs + 1] on the device,
+ * ascending from 0 to total; lengths of zero are allowed); NULL = n_seqs
+ * sequences of total / n_seqs rows.  max_seqlen: the longest sequence's length
+ * or an upper bound of it; it sizes the split of long sequences over the SMs
+ * (a value that is too small costs speed, not correctness).
+ * Backward: the forward's inputs, the output cotangent dO [total, Hv, d_v]
+ * (bf16, contiguous) and dhT (fp32, NULL = zero); writes dq, dk [total, Hk, d_k]
+ * (bf16, summed over the value heads of each key head), dv [total, Hv, d_v]
+ * (bf16) and dh0 (fp32, NULL = not written).  Nothing is saved by the forward.
+ * A sequence's results depend on its own rows alone, whatever the rows beside
+ * it hold.  ws: at least gdn_decay_workspace_bytes(backward, ...) bytes, whose
+ * first word is the status word of the bounded waits (gdn_workspace_status).
+ */
+size_t gdn_decay_workspace_bytes(int backward, int n_seqs, int total, int max_seqlen, int Hk,
+                                 int Hv, int d_k, int d_v);
+int gdn_decay_fwd(const void* q, const void* k, const void* v, const float* decay, const float* h0,
+                  const int* cu_seqlens, void* o, float* hT, int n_seqs, int total, int max_seqlen,
+                  int Hk, int Hv, int d_k, int d_v, long long q_stride, long long k_stride,
+                  long long v_stride, void* ws, size_t ws_bytes, void* stream);
+int gdn_decay_bwd(const void* q, const void* k, const void* v, const float* decay, const float* h0,
+                  const void* dO, const float* dhT, const int* cu_seqlens, void* dq, void* dk,
+                  void* dv, float* dh0, int n_seqs, int total, int max_seqlen, int Hk, int Hv,
+                  int d_k, int d_v, long long q_stride, long long k_stride, long long v_stride,
+                  void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Causal softmax attention over packed sequences with grouped heads (key head
+ * h / (Hq/Hk) for query head h).  In a sequence of n queries and m keys, query i
+ * sees the keys j <= i + m - n (the last query sees all of them):
+ *     o_i = sum_j p_ij v_j,   p_ij = exp(scale q_i . k_j - lse_i),   lse_i = log sum_j exp(..).
+ * n = m is a prompt, n < m a prompt or single tokens continuing m - n cached
+ * keys.  A query that sees no key (n > m, or m = 0) has o = 0, lse = -inf and
+ * passes no gradient.
+ * q, o [total_q, Hq, d], k, v [total_k, Hk, d] bf16, d = 128, Hq a multiple of
+ * Hk, at most 128 query heads to a key head (q_stride, k_stride, v_stride as for
+ * the single-token forms); lse [total_q, Hq] fp32 (NULL = not written);
+ * scale > 0.  cu_q, cu_k: int32 [n_seqs + 1] on the device, ascending from 0 to
+ * total_q / total_k (NULL: equal lengths).  k_len: int32 [n_seqs] (NULL: all),
+ * the used rows of each sequence's keys, for caches of fixed capacity; rows past
+ * it may hold anything.  max_k: the longest sequence's keys or an upper bound; it
+ * sizes the split of the keys over the SMs (a value that is too small costs
+ * speed, not correctness).
+ * Backward: the forward's inputs (without k_len), o and lse, and the output
+ * cotangent dO [total_q, Hq, d] (bf16, contiguous); writes dq [total_q, Hq, d]
+ * and dk, dv [total_k, Hk, d] (bf16, summed over the query heads of each key
+ * head).  Sums have a fixed order: equal calls give equal results.
+ * ws: at least gdn_attn_workspace_bytes(backward, ...) bytes, whose first word is
+ * the status word of the bounded waits (gdn_workspace_status).
+ */
+size_t gdn_attn_workspace_bytes(int backward, int n_seqs, int total_q, int total_k, int max_k,
+                                int Hq, int Hk, int d);
+int gdn_attn_fwd(const void* q, const void* k, const void* v, const int* cu_q, const int* cu_k,
+                 const int* k_len, void* o, float* lse, int n_seqs, int total_q, int total_k,
+                 int max_k, int Hq, int Hk, int d, float scale, long long q_stride,
+                 long long k_stride, long long v_stride, void* ws, size_t ws_bytes, void* stream);
+int gdn_attn_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                 const void* dO, const int* cu_q, const int* cu_k, void* dq, void* dk, void* dv,
+                 int n_seqs, int total_q, int total_k, int Hq, int Hk, int d, float scale,
+                 long long q_stride, long long k_stride, long long v_stride, void* ws,
+                 size_t ws_bytes, void* stream);
+
+/*
  * Debug export of the per-chunk UT quantities, for tests.  For every
  * (b, value head j, chunk c), in [B, Hv, N, ...] order with N = ceil(T/chunk):
  *   S_out [.., chunk, chunk] fp32  S = tril(diag(beta) (K K^T * decay), -1)

@@ -96,6 +96,23 @@ def lib():
         L.gdn_chunk_fwd_noalloc.restype = I
         L.gdn_noalloc_status.argtypes = [P]
         L.gdn_noalloc_status.restype = I
+        LL = ctypes.c_longlong
+        L.gdn_delta_step.argtypes = [P] * 8 + [I] * 6 + [LL] * 3 + [P]
+        L.gdn_delta_step.restype = I
+        L.gdn_decay_step.argtypes = [P] * 7 + [I] * 6 + [LL] * 3 + [P]
+        L.gdn_decay_step.restype = I
+        L.gdn_decay_workspace_bytes.argtypes = [I] * 8
+        L.gdn_decay_workspace_bytes.restype = Z
+        L.gdn_decay_fwd.argtypes = [P] * 8 + [I] * 7 + [LL] * 3 + [P, Z, P]
+        L.gdn_decay_fwd.restype = I
+        L.gdn_decay_bwd.argtypes = [P] * 12 + [I] * 7 + [LL] * 3 + [P, Z, P]
+        L.gdn_decay_bwd.restype = I
+        L.gdn_attn_workspace_bytes.argtypes = [I] * 8
+        L.gdn_attn_workspace_bytes.restype = Z
+        L.gdn_attn_fwd.argtypes = [P] * 8 + [I] * 7 + [ctypes.c_float] + [LL] * 3 + [P, Z, P]
+        L.gdn_attn_fwd.restype = I
+        L.gdn_attn_bwd.argtypes = [P] * 11 + [I] * 6 + [ctypes.c_float] + [LL] * 3 + [P, Z, P]
+        L.gdn_attn_bwd.restype = I
         L.gdn_selftest_wait_timeout.argtypes = [ctypes.c_longlong, P, P]
         L.gdn_selftest_wait_timeout.restype = I
         _lib = L
@@ -351,6 +368,235 @@ def segment_fold(k, v, g, beta, n_segments: int = 1, *, chunk: int = 128, want_A
     return A, Bm
 
 
+def _check_rows(t, name, H, d, n=None):
+    """bf16 rows [.., H, d] whose heads and columns are contiguous; the tokens may
+    be further apart (a part of a wider buffer).  Returns the elements between
+    tokens."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() < 3 or tuple(t.shape[-2:]) != (H, d) or (n is not None and t.numel() != n * H * d):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
+                         f"{'' if n is None else str(n) + ' '}rows of ({H}, {d})")
+    if t.numel() == 0:
+        return H * d
+    if t.stride(-1) != 1 or (H > 1 and t.stride(-2) != d):
+        raise ValueError(f"{name} must have contiguous heads and columns")
+    # the row dimensions as one: each is the next one's whole extent
+    shape, strides = [], []
+    for n_i, s_i in zip(t.shape[:-2], t.stride()[:-2]):
+        if n_i > 1:
+            shape.append(n_i)
+            strides.append(s_i)
+    for i in range(len(shape) - 1):
+        if strides[i] != shape[i + 1] * strides[i + 1]:
+            raise ValueError(f"{name} must have rows a constant stride apart")
+    stride = strides[-1] if strides else H * d
+    if stride < H * d or stride % 8:
+        raise ValueError(f"{name} must have rows at least {H * d} elements apart, by a multiple of 8")
+    return stride
+
+
+def _step(name, q, k, v, gates, state, slots, o):
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k, v must be [R, H, D]")
+    R, Hk, dk = k.shape
+    Hv, dv = v.shape[1:]
+    strides = [_check_rows(q, "q", Hk, dk, R), _check_rows(k, "k", Hk, dk, R),
+               _check_rows(v, "v", Hv, dv, R)]
+    if state.dim() != 4:
+        raise ValueError("state must be [slots, Hv, d_k, d_v]")
+    _check(state, "state", torch.float32, (state.shape[0], Hv, dk, dv))
+    _check(slots, "slots", torch.int32, (R,))
+    if slots is None and state.shape[0] < R:
+        raise ValueError(f"{R} rows need as many states, got {state.shape[0]}")
+    if o is None:
+        o = torch.empty((R, Hv, dv), dtype=torch.bfloat16, device=q.device)
+    _check(o, "o", torch.bfloat16, (R, Hv, dv))
+    rc = getattr(lib(), name)(_ptr(q), _ptr(k), _ptr(v), *[_ptr(g) for g in gates], _ptr(state),
+                              _ptr(slots), _ptr(o), R, state.shape[0], Hk, Hv, dk, dv, *strides,
+                              _stream(q.device))
+    if rc != GDN_OK:
+        raise GDNError(rc, name)
+    return o
+
+
+def delta_step(q, k, v, g, beta, state, slots=None, *, o=None) -> torch.Tensor:
+    """One token per row of the gated delta rule: q, k [R, Hk, 128], v [R, Hv, 128]
+    (bf16), g, beta [R, Hv]; state [n, Hv, 128, 128] (fp32) is updated in place.
+    slots: int32 [R], the state of each row (None: row r's state is r); a
+    negative slot is a padded row, whose output is zero.  Returns o [R, Hv, 128]."""
+    _check(g, "g", torch.float32, tuple(v.shape[:2]))
+    _check(beta, "beta", torch.float32, tuple(v.shape[:2]))
+    return _step("gdn_delta_step", q, k, v, (g, beta), state, slots, o)
+
+
+def decay_step(q, k, v, decay, state, slots=None, *, o=None) -> torch.Tensor:
+    """One token per row of linear attention with a decay for each head (decay
+    [Hv], the log-decays); otherwise as delta_step."""
+    _check(decay, "decay", torch.float32, tuple(v.shape[1:2]))
+    return _step("gdn_decay_step", q, k, v, (decay,), state, slots, o)
+
+
+def decay_workspace_bytes(backward, n_seqs, total, max_seqlen, Hk, Hv, dk=128, dv=128) -> int:
+    return int(lib().gdn_decay_workspace_bytes(int(backward), n_seqs, total, max_seqlen, Hk, Hv, dk,
+                                               dv))
+
+
+def _decay_dims(q, k, v, decay, cu_seqlens, max_seqlen):
+    """Packed [total, H, D] with cu_seqlens, or [B, T, H, D] without."""
+    if cu_seqlens is not None:
+        if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+            raise ValueError("q, k, v must be [total, H, D] with cu_seqlens")
+        _check(cu_seqlens, "cu_seqlens", torch.int32)
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+            raise ValueError("cu_seqlens must hold the sequences' starts and the total")
+        n, total = cu_seqlens.numel() - 1, k.shape[0]
+        longest = total if max_seqlen is None else int(max_seqlen)
+    else:
+        if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
+            raise ValueError("q, k, v must be [B, T, H, D] without cu_seqlens")
+        n, longest = k.shape[:2]
+        total = n * longest
+    Hk, dk = k.shape[-2:]
+    Hv, dv = v.shape[-2:]
+    if q.shape != k.shape or v.shape[:-2] != k.shape[:-2]:
+        raise ValueError(f"q, k, v have shapes {tuple(q.shape)}, {tuple(k.shape)}, {tuple(v.shape)}")
+    strides = [_check_rows(q, "q", Hk, dk, total), _check_rows(k, "k", Hk, dk, total),
+               _check_rows(v, "v", Hv, dv, total)]
+    _check(decay, "decay", torch.float32, (Hv,))
+    return n, total, longest, Hk, Hv, dk, dv, strides
+
+
+def decay_fwd(q, k, v, decay, h0=None, *, cu_seqlens=None, max_seqlen=None, want_hT: bool = True,
+              o=None, hT=None, workspace=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Linear attention with a decay for each head (decay [Hv], the log-decays,
+    <= 0): S_t = exp(decay) S_{t-1} + k_t v_t^T, o_t = S_t^T q_t.  q, k, v are
+    [B, T, H, 128], or with cu_seqlens (int32, on the device) packed sequences
+    [total, H, 128]; max_seqlen then bounds the longest one (it only steers how
+    the work is split).  h0 [n, Hv, 128, 128].  Returns (o, hT)."""
+    n, total, longest, Hk, Hv, dk, dv, strides = _decay_dims(q, k, v, decay, cu_seqlens, max_seqlen)
+    dev = q.device
+    _check(h0, "h0", torch.float32, (n, Hv, dk, dv))
+    if o is None:
+        o = torch.empty(v.shape, dtype=torch.bfloat16, device=dev)
+    _check(o, "o", torch.bfloat16, tuple(v.shape))
+    if want_hT and hT is None:
+        hT = torch.empty((n, Hv, dk, dv), dtype=torch.float32, device=dev)
+    _check(hT, "hT", torch.float32, (n, Hv, dk, dv))
+    ws = _workspace(decay_workspace_bytes(0, n, total, longest, Hk, Hv, dk, dv), dev, workspace)
+    rc = lib().gdn_decay_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(h0), _ptr(cu_seqlens),
+                             _ptr(o), _ptr(hT), n, total, longest, Hk, Hv, dk, dv, *strides,
+                             _ptr(ws), ws.numel(), _stream(dev))
+    if rc != GDN_OK:
+        raise GDNError(rc, "gdn_decay_fwd")
+    return o, hT
+
+
+def decay_bwd(q, k, v, decay, h0, dO, dhT=None, *, cu_seqlens=None, max_seqlen=None,
+              want_dh0: bool = True, workspace=None):
+    """Backward of decay_fwd.  Returns (dq, dk, dv, dh0); dq and dk are summed over
+    the value heads that share a key head."""
+    n, total, longest, Hk, Hv, dk, dv, strides = _decay_dims(q, k, v, decay, cu_seqlens, max_seqlen)
+    dev = q.device
+    _check(h0, "h0", torch.float32, (n, Hv, dk, dv))
+    _check(dO, "dO", torch.bfloat16, tuple(v.shape))
+    _check(dhT, "dhT", torch.float32, (n, Hv, dk, dv))
+    dq = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+    dk_ = torch.empty(k.shape, dtype=torch.bfloat16, device=dev)
+    dv_ = torch.empty(v.shape, dtype=torch.bfloat16, device=dev)
+    dh0 = torch.empty((n, Hv, dk, dv), dtype=torch.float32, device=dev) if want_dh0 else None
+    ws = _workspace(decay_workspace_bytes(1, n, total, longest, Hk, Hv, dk, dv), dev, workspace)
+    rc = lib().gdn_decay_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(h0), _ptr(dO), _ptr(dhT),
+                             _ptr(cu_seqlens), _ptr(dq), _ptr(dk_), _ptr(dv_), _ptr(dh0), n, total,
+                             longest, Hk, Hv, dk, dv, *strides, _ptr(ws), ws.numel(), _stream(dev))
+    if rc != GDN_OK:
+        raise GDNError(rc, "gdn_decay_bwd")
+    return dq, dk_, dv_, dh0
+
+
+def attn_workspace_bytes(backward, n_seqs, total_q, total_k, max_k, Hq, Hk, d=128) -> int:
+    return int(lib().gdn_attn_workspace_bytes(int(backward), n_seqs, total_q, total_k, max_k, Hq, Hk,
+                                              d))
+
+
+def _attn_dims(q, k, v, cu_q, cu_k, scale):
+    """Packed [total, H, D] with cu_q and cu_k, or [B, T, H, D] without."""
+    if (cu_q is None) != (cu_k is None):
+        raise ValueError("cu_q and cu_k go together")
+    dims = 4 if cu_q is None else 3
+    if q.dim() != dims or k.dim() != dims or v.dim() != dims:
+        raise ValueError("q, k, v must be [B, T, H, D], or [total, H, D] with cu_q and cu_k")
+    if cu_q is not None:
+        for name, t in (("cu_q", cu_q), ("cu_k", cu_k)):
+            _check(t, name, torch.int32)
+        if cu_q.dim() != 1 or cu_q.numel() < 1 or cu_q.shape != cu_k.shape:
+            raise ValueError("cu_q and cu_k must hold as many starts and the total")
+        n, total_q, total_k = cu_q.numel() - 1, q.shape[0], k.shape[0]
+    else:
+        if q.shape[0] != k.shape[0]:
+            raise ValueError(f"q has {q.shape[0]} sequences, k {k.shape[0]}")
+        n, total_q, total_k = q.shape[0], q.shape[0] * q.shape[1], k.shape[0] * k.shape[1]
+    Hq, d = q.shape[-2:]
+    Hk = k.shape[-2]
+    if v.shape != k.shape or k.shape[-1] != d:
+        raise ValueError(f"q, k, v have shapes {tuple(q.shape)}, {tuple(k.shape)}, {tuple(v.shape)}")
+    strides = [_check_rows(q, "q", Hq, d, total_q), _check_rows(k, "k", Hk, d, total_k),
+               _check_rows(v, "v", Hk, d, total_k)]
+    return n, total_q, total_k, Hq, Hk, d, d ** -0.5 if scale is None else float(scale), strides
+
+
+def attn_fwd(q, k, v, *, cu_q=None, cu_k=None, k_len=None, max_q=None, max_k=None, scale=None,
+             want_lse: bool = True, o=None, lse=None, workspace=None
+             ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Causal softmax attention with grouped heads: q [total_q, Hq, 128], k, v
+    [total_k, Hk, 128] hold packed sequences that start at cu_q and cu_k (int32,
+    on the device), or are [B, T, H, 128] without them.  The last query of a
+    sequence sees all of its keys, each one before it one key fewer; k_len
+    (int32) gives the used rows of caches with a fixed capacity.  max_q and
+    max_k bound the lengths (they only steer how the work is split).  scale
+    defaults to 1 / sqrt(128).  Returns (o, lse), lse [.., Hq] in fp32."""
+    n, total_q, total_k, Hq, Hk, d, scale, strides = _attn_dims(q, k, v, cu_q, cu_k, scale)
+    dev = q.device
+    _check(k_len, "k_len", torch.int32, (n,))
+    longest = int(max_k) if max_k is not None else (k.shape[1] if cu_k is None else total_k)
+    if o is None:
+        o = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+    _check(o, "o", torch.bfloat16, tuple(q.shape))
+    if want_lse and lse is None:
+        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
+    _check(lse, "lse", torch.float32, tuple(q.shape[:-1]))
+    ws = _workspace(attn_workspace_bytes(0, n, total_q, total_k, longest, Hq, Hk, d), dev, workspace)
+    rc = lib().gdn_attn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_q), _ptr(cu_k), _ptr(k_len), _ptr(o),
+                            _ptr(lse), n, total_q, total_k, longest, Hq, Hk, d, scale, *strides,
+                            _ptr(ws), ws.numel(), _stream(dev))
+    if rc != GDN_OK:
+        raise GDNError(rc, "gdn_attn_fwd")
+    return o, lse
+
+
+def attn_bwd(q, k, v, o, lse, dO, *, cu_q=None, cu_k=None, max_q=None, max_k=None, scale=None,
+             workspace=None):
+    """Backward of attn_fwd (without k_len).  Returns (dq, dk, dv); dk and dv are
+    summed over the query heads that share a key head."""
+    n, total_q, total_k, Hq, Hk, d, scale, strides = _attn_dims(q, k, v, cu_q, cu_k, scale)
+    dev = q.device
+    _check(o, "o", torch.bfloat16, tuple(q.shape))
+    _check(dO, "dO", torch.bfloat16, tuple(q.shape))
+    _check(lse, "lse", torch.float32, tuple(q.shape[:-1]))
+    dq = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+    dk = torch.empty(k.shape, dtype=torch.bfloat16, device=dev)
+    dv = torch.empty(v.shape, dtype=torch.bfloat16, device=dev)
+    ws = _workspace(attn_workspace_bytes(1, n, total_q, total_k, 0, Hq, Hk, d), dev, workspace)
+    rc = lib().gdn_attn_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dO), _ptr(cu_q),
+                            _ptr(cu_k), _ptr(dq), _ptr(dk), _ptr(dv), n, total_q, total_k, Hq, Hk, d,
+                            scale, *strides, _ptr(ws), ws.numel(), _stream(dev))
+    if rc != GDN_OK:
+        raise GDNError(rc, "gdn_attn_bwd")
+    return dq, dk, dv
+
+
 def debug_ut(k, v, g, beta, chunk: int = 128, tiles: bool = False):
     """Per-chunk S, T (fp32) and w, u (bf16), each [B, Hv, N, chunk, .].
 
@@ -406,4 +652,5 @@ def selftest_wait_timeout(limit_ns: int, status: torch.Tensor) -> int:
 __all__ = ["build", "lib", "chunk_fwd", "chunk_bwd", "layer_fwd", "layer_bwd",
            "layer_workspace_bytes", "saved_bytes", "affine_compose", "segment_fold", "debug_ut",
            "fwd_workspace_bytes", "bwd_workspace_bytes", "default_segments", "GDNError",
-           "header_functions", "workspace_status", "selftest_wait_timeout"]
+           "header_functions", "delta_step", "decay_step", "decay_fwd", "decay_bwd",
+           "decay_workspace_bytes", "attn_fwd", "attn_bwd", "attn_workspace_bytes", "workspace_status", "selftest_wait_timeout"]

@@ -1,0 +1,304 @@
+// gdn_attn_fwd.cu -- causal softmax attention over packed sequences, grouped heads.
+//
+//   o_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = e^{scale q_i . k_j - max},  j <= i + keys - queries
+//
+// One pass over the keys with a running maximum and sum per row.  A CTA holds
+// two query tiles of 128 rows (gdn_attn.cuh) and streams K and V tiles of 128
+// keys through a ring of five 32 KiB slots.  S = Q K^T and O += P V are tcgen05
+// products with fp32 accumulators in tensor memory (S and O of both tiles: 4 x
+// 128 columns); P goes back to tensor memory as a bf16 A operand over the half
+// of S that its row has already been read from.  Four warps own a tile, one
+// thread a row, so the row's maximum and sum need no exchange.  The two tiles
+// alternate: while one's softmax runs, the other's products do.
+//
+// The running maximum is only raised when a row's new one is larger by more than
+// 8 in base 2 (p then stays below 2^8, exact in scale for bf16 and fp32), which
+// after the first tiles is rare: O is rescaled in tensor memory by the row's own
+// thread, between the product that wrote it and the next one.
+//
+// Few rows over many keys (single tokens over a cache): the keys are split over
+// CTAs, each writes its own normalised output and log-sum in fp32, and a second
+// kernel joins them.
+//
+// Bound: the two products, 1024 cycles per 128 x 128 tile pair at the tensor
+// rate, for prompts; HBM (k and v once) for single tokens.
+#include <limits.h>
+
+#include "gdn_attn.cuh"
+
+namespace gdn {
+
+namespace {
+
+using namespace attn;
+
+constexpr int NSLOT = 5;
+constexpr int FWD_THREADS = 256 + 64;
+constexpr float RAISE = 8.f;  // base-2 headroom before the running maximum is raised
+
+struct FwdSmem {
+  unsigned char q[2][TILE];
+  unsigned char slot[NSLOT][TILE];
+  uint64_t full[NSLOT], empty[NSLOT];
+  uint64_t barQ[2], barS[2], barP[2], barO[2];
+  uint32_t tmem;
+};
+
+__global__ void __launch_bounds__(FWD_THREADS, 1) k_attn_fwd(const __grid_constant__ AttnArgs a) {
+  extern __shared__ unsigned char raw[];
+  FwdSmem& sm = *reinterpret_cast<FwdSmem*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait();
+  pdl_release();
+  const int G = a.Hq / a.Hk, TT = CH / G;  // tokens to a tile
+  // a sequence's last tiles, which see the most keys, start first
+  const int kh = blockIdx.x % a.Hk, split = blockIdx.y;
+  const int2 at = find_tile(a.cu_q, a.n_seqs, a.total_q, 2 * TT, (int)((gridDim.x - 1 - blockIdx.x) / a.Hk));
+  if (at.x < 0) return;
+  const Seq sq = seq_of(a, at.x);
+  const int off = sq.kl - sq.ql;
+  const int tok0 = at.y * 2 * TT;
+  if (tok0 >= sq.ql) return;
+  // key tiles [kb, kb + n[w]) of tile w
+  int n[2];
+  const int kb = split * a.split_tiles, most = split == a.n_splits - 1 ? INT_MAX : a.split_tiles;
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const int first = tok0 + w * TT, last = min(first + TT, sq.ql) - 1;
+    const int keys = last >= first ? min(sq.kl, last + off + 1) : 0;
+    n[w] = max(0, min((max(keys, 0) + CH - 1) / CH - kb, most));
+  }
+  const int nmax = max(n[0], n[1]);
+  const float sc = a.scale * LOG2E;
+
+  if (tid == 0) {
+    for (int k = 0; k < NSLOT; ++k) {
+      tc::mbar_init(&sm.full[k], 1);
+      tc::mbar_init(&sm.empty[k], 1);
+    }
+    for (int w = 0; w < 2; ++w) {
+      tc::mbar_init(&sm.barQ[w], 1);
+      tc::mbar_init(&sm.barS[w], 1);
+      tc::mbar_init(&sm.barO[w], 1);
+      tc::mbar_init(&sm.barP[w], 128);
+    }
+    tc::mbar_fence_init();
+  }
+  if (warp == 0) tc::alloc(&sm.tmem, 512);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tS = sm.tmem, tO = sm.tmem + 256;
+  tc::Wait w;
+  const int nt = 2 * nmax;  // ring tiles: K, V of every key tile
+
+  if (warp == 9) {
+    if (lane == 0 && nmax > 0) {
+      for (int x = 0; x < 2; ++x)
+        if (n[x] > 0) load_group(sm.q[x], &a.q, kh, G, sq.q0 + tok0 + x * TT, &sm.barQ[x]);
+      for (int t = 0; t < nt && w.ok; ++t) {
+        const int k = t % NSLOT;
+        if (t >= NSLOT) w.on(&sm.empty[k], t / NSLOT - 1);
+        if (!w.ok) break;
+        load_rows(sm.slot[k], (t & 1) ? &a.v : &a.k, kh, sq.k0 + (kb + t / 2) * CH, &sm.full[k]);
+      }
+      if (w.ok)  // no copy is in flight when the CTA ends
+        for (int t = max(0, nt - NSLOT); t < nt; ++t) w.on(&sm.full[t % NSLOT], t / NSLOT);
+      else
+        for (int k = 0; k < NSLOT; ++k) tc::mbar_wait_sleep(&sm.full[k], 0, 4000000LL);
+    }
+  } else if (warp == 8) {
+    if (lane == 0 && nmax > 0) {
+      auto slot = [&](int t) { return smem_u32(sm.slot[t % NSLOT]); };
+      auto arrived = [&](int t) { w.on(&sm.full[t % NSLOT], t / NSLOT); };
+      auto release = [&](int t) {
+        if (t + NSLOT < nt) tc::commit(&sm.empty[t % NSLOT]);
+      };
+      auto scores = [&](int x, int i) {  // S of tile x = Q K^T
+        tc::gemm128(tS + 128 * x, smem_u32(sm.q[x]), false, slot(2 * i), false, false);
+        tc::commit(&sm.barS[x]);
+      };
+      arrived(0);
+      for (int x = 0; x < 2; ++x)
+        if (n[x] > 0) {
+          w.on(&sm.barQ[x], 0);
+          scores(x, 0);
+        }
+      release(0);
+      for (int i = 0; i < nmax; ++i) {
+        arrived(2 * i + 1);
+        if (i + 1 < nmax) arrived(2 * i + 2);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (i < n[x]) {
+            w.on(&sm.barP[x], i);
+            tc::fence_after();
+            tc::gemm_ts_bmn(tO + 128 * x, tS + 128 * x, slot(2 * i + 1), i > 0);
+            if (i + 1 == n[x]) tc::commit(&sm.barO[x]);
+          }
+          if (x == 1) release(2 * i + 1);
+          if (i + 1 < n[x]) scores(x, i + 1);
+        }
+        if (i + 1 < nmax) release(2 * i + 2);
+      }
+    }
+  } else {
+    const int x = warp >> 2, r = 32 * (warp & 3) + lane;
+    const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t S = tS + 128 * x + lane_base, O = tO + 128 * x + lane_base;
+    const int tok = tok0 + x * TT + r / G;
+    const bool valid = r < TT * G && tok < sq.ql;
+    const int lim = valid ? tok + off : -1;  // the last key that the row sees
+    const bool any = __any_sync(0xffffffffu, valid);
+    float m = -INFINITY, l = 0.f;
+    for (int i = 0; i < n[x]; ++i) {
+      const int key0 = (kb + i) * CH;
+      w.warp_on(&sm.barS[x], i);
+      tc::fence_after();
+      if (any) {
+        float v[128];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) tc::ld32(S + 32 * g, *reinterpret_cast<float(*)[32]>(v + 32 * g));
+        if (key0 + CH - 1 > lim) {
+#pragma unroll
+          for (int j = 0; j < 128; ++j) v[j] = key0 + j <= lim ? v[j] : -INFINITY;
+        }
+        float mt[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+        for (int j = 4; j < 128; j += 4) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) mt[c] = fmaxf(mt[c], v[j + c]);
+        }
+        const float mn = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3]));
+        // raise the maximum (a first one counts); O is idle: this S was issued after the last P V
+        if (__any_sync(0xffffffffu, mn > m && (mn - m) * sc > RAISE)) {
+          const float to = fmaxf(m, mn);
+          const float f = m == to ? 1.f : ex2((m - to) * sc);  // 0 for a first maximum
+          m = to;
+          l *= f;
+          if (i > 0) {
+#pragma unroll 1
+            for (int g = 0; g < 4; ++g) {
+              float y[32];
+              tc::ld32(O + 32 * g, y);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) y[j] *= f;
+              tc::st32(O + 32 * g, y);
+            }
+            tc::wait_st();
+          }
+        }
+        const float ms = m == -INFINITY ? 0.f : m * sc;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          float p[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            p[j] = ex2(v[32 * g + j] * sc - ms);
+            sum[j & 3] += p[j];
+          }
+          tc::st16_bf16(S + 16 * g, p);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      }
+      if (key0 + CH > sq.kl) {  // rows past the keys: whatever they hold, they count as zero
+        const int t = 2 * i + 1;
+        w.warp_on(&sm.full[t % NSLOT], t / NSLOT);
+        zero_rows(sm.slot[t % NSLOT], sq.kl - key0, tid & 127, 128);
+        tc::fence_proxy_async();
+      }
+      tc::wait_st();
+      tc::fence_before();
+      tc::mbar_arrive(&sm.barP[x]);
+    }
+    if (n[x] > 0) w.warp_on(&sm.barO[x], 0);
+    tc::fence_after();
+    if (any) {
+      const long row = ((long)sq.q0 + tok) * a.Hq + kh * G + r % G;
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float lse = l > 0.f ? m * a.scale + logf(l) : -INFINITY;
+#pragma unroll 1
+      for (int g = 0; g < 4; ++g) {
+        float y[32];
+        if (n[x] > 0) {
+          tc::ld32(O + 32 * g, y);
+        }
+        if (valid) {
+          if (n[x] == 0 || l == 0.f) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) y[j] = 0.f;
+          }
+          if (a.n_splits == 1) {
+            store32(a.o + row * HD + 32 * g, y, inv);
+          } else if (l > 0.f) {  // (the join reads a part only where its lse is finite)
+            float* d = a.part + ((long)split * a.total_q * a.Hq + row) * HD + 32 * g;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              *reinterpret_cast<float4*>(d + 4 * j) =
+                  make_float4(inv * y[4 * j], inv * y[4 * j + 1], inv * y[4 * j + 2], inv * y[4 * j + 3]);
+          }
+        }
+        __syncwarp();
+      }
+      if (valid) {
+        if (a.n_splits > 1)
+          a.part_lse[(long)split * a.total_q * a.Hq + row] = lse;
+        else if (a.lse)
+          a.lse[row] = lse;
+      }
+    }
+    tc::fence_before();
+  }
+  if (!w.ok && a.status) atomicOr(a.status, 1);
+  __syncthreads();
+  tc::fence_after();
+  if (warp == 0) tc::dealloc(sm.tmem, 512);
+}
+
+// Joins the splits of a row: o = sum_s e^{lse_s - lse} o_s.  One warp per row.
+__global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ AttnArgs a) {
+  pdl_wait();
+  pdl_release();
+  const long rows = (long)a.total_q * a.Hq, row = (long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= rows) return;
+  float top = -INFINITY;
+  for (int s = lane; s < a.n_splits; s += 32) top = fmaxf(top, a.part_lse[s * rows + row]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  float total = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
+  if (top > -INFINITY)
+    for (int s = 0; s < a.n_splits; ++s) {
+      const float l = a.part_lse[s * rows + row];
+      if (l == -INFINITY) continue;
+      const float f = expf(l - top);
+      const float4 p = *reinterpret_cast<const float4*>(a.part + (s * rows + row) * HD + 4 * lane);
+      total += f;
+      y[0] += f * p.x;
+      y[1] += f * p.y;
+      y[2] += f * p.z;
+      y[3] += f * p.w;
+    }
+  const float inv = total > 0.f ? 1.f / total : 0.f;
+  *reinterpret_cast<uint2*>(a.o + row * HD + 4 * lane) =
+      make_uint2(pack_bf16(inv * y[0], inv * y[1]), pack_bf16(inv * y[2], inv * y[3]));
+  if (a.lse && lane == 0) a.lse[row] = total > 0.f ? top + logf(total) : -INFINITY;
+}
+
+}  // namespace
+
+cudaError_t launch_attn_fwd(const AttnArgs& a, cudaStream_t s) {
+  constexpr size_t smem = sizeof(FwdSmem) + 1024;
+  static_assert(smem <= 227 * 1024, "shared memory");
+  cudaError_t e = cudaFuncSetAttribute(k_attn_fwd, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  const int K = 2 * (CH / (a.Hq / a.Hk));
+  const dim3 grid((unsigned)a.Hk * (unsigned)(a.total_q / K + a.n_seqs), (unsigned)a.n_splits);
+  e = launch_pdl(k_attn_fwd, grid, dim3(FWD_THREADS), smem, s, a);
+  if (e != cudaSuccess || a.n_splits == 1) return e;
+  const long rows = (long)a.total_q * a.Hq;
+  return launch_pdl(k_attn_join, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, a);
+}
+
+}  // namespace gdn

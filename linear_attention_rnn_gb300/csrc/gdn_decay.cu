@@ -1,0 +1,582 @@
+// gdn_decay.cu -- linear attention with a decay for each head, over packed
+// sequences: S_t = e^w S_{t-1} + k_t v_t^T, o_t = S_t^T q_t, forward and backward.
+//
+// One operation does all of it.  With rows a, b, c of 128 values and a state X,
+//     out_t = sum_{s <= t} e^{w (t - s)} (a_t . b_s) c_s + (decayed X0)^T a_t,
+// the forward is (a, b, c) = (q, k, v) with X0 = h0, and the gradients are
+//     dq:  (dO, v, k),  X0 = h0^T,   forwards in time,
+//     dv:  (k, q, dO),  X0 = dhT,    backwards in time (s >= t),
+//     dk:  (v, dO, q),  X0 = dhT^T,  backwards in time;
+// the state that the dv pass ends with is dh0.  dq and dk of a key head are sums
+// over its value heads.
+//
+// Chunks of 128 tokens (n valid in a sequence's last one), rows i and columns j
+// of a chunk, per chunk:
+//     out = diag(f) A X + ((A B^T) o M) C,    X <- e^{w n} X + B^T diag(e) C
+//   forwards:  M_ij = e^{w (i - j)}, j <= i;  f_i = e^{w (i + 1)};  e_j = e^{w (n - 1 - j)}
+//   backwards: M_ij = e^{w (j - i)}, j >= i;  f_i = e^{w (n - 1 - i)};  e_j = e^{w (j + 1)}
+// (every exponent that is used is <= 0, so nothing overflows for any w <= 0).
+//
+// k_decay, one CTA per (pass, sequence, head, segment): five tcgen05 products of
+// 128^3 per chunk, accumulators in tensor memory (P = A B^T, O1 = A X, O2 = P C,
+// X: 4 x 128 columns).  X stays in tensor memory in fp32 for the whole segment;
+// it is scaled there and rounded to bf16 only as the operand of A X.  B^T diag(e)
+// C has to keep the state's fp32: the rows of B are scaled in fp32 and split
+// into two bf16 terms (hi in place, lo beside it), two products.  The masked P
+// goes back to tensor memory as a bf16 A operand.  Warps 0-3 mask P, 4-7 carry
+// the state, 8-11 write the output, 12-15 scale B; one thread issues the
+// products, one the TMA loads (a ring of five 32 KiB tiles, three to a chunk).
+//
+// With few sequences and heads the SMs are filled by segments: k_decay_fold
+// forms each segment's own X (rows weighted to the segment's end, so that its
+// chunks accumulate in tensor memory without a rescale), k_decay_prefix turns
+// them into entering states, and k_decay starts every segment from its own.
+//
+// Bound: HBM (each of q, k, v, o once: 128 KiB per chunk and head, 2.9 us of an
+// SM's share of the measured copy rate; the five products take 1.4 us).
+#include "gdn_kernels.cuh"
+#include "gdn_tc05.cuh"
+
+namespace gdn {
+
+namespace {
+
+constexpr uint32_t TILE = CH * HD * 2;  // a [128 x 128] bf16 tile
+constexpr int NSLOT = 5;
+constexpr int WALK_THREADS = 16 * 32 + 64;
+constexpr int FOLD_SLOTS = 6;
+constexpr int FOLD_THREADS = 256 + 64;
+
+struct Range {
+  int start, len;
+};
+// sequence s of the packed rows (cu null: equal lengths), held inside [0, total]
+__device__ __forceinline__ Range seq_range(const int* cu, int s, int T, int total) {
+  Range r;
+  if (cu) {
+    const int a = min(max(cu[s], 0), total), b = min(max(cu[s + 1], a), total);
+    r.start = a;
+    r.len = b - a;
+  } else {
+    r.start = s * T;
+    r.len = T;
+  }
+  return r;
+}
+
+// Segment slots.  Sequence s has the slots first_slot(s) .. first_slot(s + 1) - 1,
+// at least as many as it has segments of K = 128 seg_chunks tokens and at most
+// one more than total / K over all sequences together, so that neither grids
+// nor states grow with sequences x longest sequence.
+__device__ __forceinline__ int first_slot(const int* cu, int s, int T, int total, int K) {
+  return (cu ? min(max(cu[s], 0), total) : s * T) / K + s;
+}
+// Sequence and segment of a slot, by all threads of the block together (sequence
+// -1: none).  With one segment to a sequence a slot is a sequence.
+__device__ __forceinline__ int2 find_segment(const int* cu, int n_seqs, int T, int total, int seg_chunks, int nseg,
+                                             int slot) {
+  if (nseg == 1) return make_int2(slot, 0);
+  __shared__ int2 found;
+  if (threadIdx.x == 0) found = make_int2(-1, 0);
+  __syncthreads();
+  const int K = seg_chunks * CH;
+  for (int s = threadIdx.x; s < n_seqs; s += blockDim.x) {
+    const int a = first_slot(cu, s, T, total, K);
+    if (slot >= a && slot < first_slot(cu, s + 1, T, total, K)) found = make_int2(s, slot - a);
+  }
+  __syncthreads();
+  return found;
+}
+
+// Rows of an SW128 tile scaled by f (rows at or past n: zero), split into hi
+// (in place) and lo; this thread's row r, 16-byte chunks j0 .. j0 + nj - 1.
+__device__ __forceinline__ void scale_row(unsigned char* tile, unsigned char* lo, int r, int j0, int nj, float f,
+                                          bool valid) {
+  for (int j = j0; j < j0 + nj; ++j) {
+    const uint32_t off = tc::sw128_chunk(r, j, CH);
+    uint4 u = *reinterpret_cast<const uint4*>(tile + off), h, l;
+    uint32_t* up = reinterpret_cast<uint32_t*>(&u);
+    uint32_t* hp = reinterpret_cast<uint32_t*>(&h);
+    uint32_t* lp = reinterpret_cast<uint32_t*>(&l);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = unpack_bf16(up[i]);
+      split_bf16(valid ? f * x.x : 0.f, valid ? f * x.y : 0.f, hp[i], lp[i]);
+    }
+    *reinterpret_cast<uint4*>(tile + off) = h;
+    *reinterpret_cast<uint4*>(lo + off) = l;
+  }
+}
+__device__ __forceinline__ void zero_row(unsigned char* tile, int r, int j0, int nj) {
+  for (int j = j0; j < j0 + nj; ++j)
+    *reinterpret_cast<uint4*>(tile + tc::sw128_chunk(r, j, CH)) = make_uint4(0u, 0u, 0u, 0u);
+}
+
+__device__ __forceinline__ void load_tile(unsigned char* dst, const CUtensorMap* m, int head, int row, uint64_t* bar) {
+  tc::arrive_expect_tx(bar, TILE);
+  tc::tma_load_3d(dst, m, 0, head, row, bar);
+  tc::tma_load_3d(dst + TILE / 2, m, 64, head, row, bar);
+}
+
+// ---- the chunk walk ----------------------------------------------------------------
+struct WalkSmem {
+  unsigned char slot[NSLOT][TILE];
+  unsigned char lo[TILE];   // second term of the scaled B rows
+  unsigned char X[TILE];    // the entering state in bf16, [128 (b) rows x 128 (c)]
+  float tab[CH];            // e^{w d}
+  uint64_t full[NSLOT], empty[NSLOT];
+  uint64_t barP, barPm, barK, barS, barX, barO, barOf;
+  uint32_t tmem;
+};
+
+__global__ void __launch_bounds__(WALK_THREADS, 1) k_decay(const __grid_constant__ DecayArgs a) {
+  extern __shared__ unsigned char raw[];
+  WalkSmem& sm = *reinterpret_cast<WalkSmem*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int G = a.Hv / a.Hk;
+  pdl_wait();
+  pdl_release();
+
+  // pass, then segment, sequence and head of this CTA
+  int u = blockIdx.x, ri = 0;
+  for (; ri < a.n_roles - 1; ++ri) {
+    const int units = a.slots * (a.role[ri].shared ? a.Hk : a.Hv);
+    if (u < units) break;
+    u -= units;
+  }
+  const DecayRole& R = a.role[ri];
+  const int heads = R.shared ? a.Hk : a.Hv, loops = R.shared ? G : 1;
+  const int hd = u % heads, slot = u / heads;
+  const int2 at = find_segment(a.cu, a.n_seqs, a.T, a.total, a.seg_chunks, a.nseg, slot);
+  const int s = at.x, seg = at.y;
+  if (s < 0) return;
+  const Range q = seq_range(a.cu, s, a.T, a.total);
+  const int nch = (q.len + CH - 1) / CH;
+  const int cb = seg * a.seg_chunks, ce = a.nseg == 1 ? nch : min(nch, cb + a.seg_chunks), nc = ce - cb;
+  const bool rev = R.rev;
+  if (nc <= 0) {  // an empty sequence ends in the state that it began with
+    if (seg == 0 && R.xT) {
+      const long o = ((long)s * a.Hv + hd) * HD * HD;
+      for (int i = tid; i < HD * HD; i += WALK_THREADS) R.xT[o + i] = R.x0 ? R.x0[o + i] : 0.f;
+    }
+    return;
+  }
+  const int n_it = loops * nc;
+  auto chunk_of = [&](int it) { return rev ? ce - 1 - it % nc : cb + it % nc; };
+  auto head_of = [&](int it) { return R.shared ? hd * G + it / nc : hd; };  // value head
+  auto rows_of = [&](int c) { return min(CH, q.len - c * CH); };
+
+  if (tid == 0) {
+    for (int k = 0; k < NSLOT; ++k) {
+      tc::mbar_init(&sm.full[k], 1);
+      tc::mbar_init(&sm.empty[k], 1);
+    }
+    tc::mbar_init(&sm.barP, 1);
+    tc::mbar_init(&sm.barX, 1);
+    tc::mbar_init(&sm.barO, 1);
+    tc::mbar_init(&sm.barPm, 128);
+    tc::mbar_init(&sm.barK, 128);
+    tc::mbar_init(&sm.barS, 128);
+    tc::mbar_init(&sm.barOf, 128);
+    tc::mbar_fence_init();
+  }
+  if (warp == 0) tc::alloc(&sm.tmem, 512);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tP = sm.tmem, tO1 = tP + 128, tO2 = tP + 256, tX = tP + 384;
+  tc::Wait w;
+
+  if (warp == 17) {  // ---- TMA: tiles b, a, c of every chunk, in the order consumed
+    if (lane == 0) {
+      const int nt = 3 * n_it;
+      for (int t = 0; t < nt && w.ok; ++t) {
+        const int k = t % NSLOT, it = t / 3, kind = t % 3, row = q.start + chunk_of(it) * CH;
+        if (t >= NSLOT) w.on(&sm.empty[k], (t / NSLOT - 1));
+        if (!w.ok) break;
+        const int j = head_of(it), jk = j / G;
+        const CUtensorMap* m = kind == 0 ? &R.b : kind == 1 ? &R.a : &R.c;
+        const int per_v = kind == 0 ? R.hb : kind == 1 ? R.ha : R.hc;
+        load_tile(sm.slot[k], m, per_v ? j : jk, row, &sm.full[k]);
+      }
+      // no copy is in flight when the CTA ends
+      if (w.ok)
+        for (int t = max(0, nt - NSLOT); t < nt; ++t) w.on(&sm.full[t % NSLOT], t / NSLOT);
+      else
+        for (int k = 0; k < NSLOT; ++k) tc::mbar_wait_sleep(&sm.full[k], 0, 4000000LL);
+    }
+  } else if (warp == 16) {  // ---- products
+    if (lane == 0) {
+      const int nt = 3 * n_it;
+      auto slot = [&](int t) { return smem_u32(sm.slot[t % NSLOT]); };
+      auto arrived = [&](int t) { w.on(&sm.full[t % NSLOT], t / NSLOT); };
+      auto release = [&](int t) {
+        if (t + NSLOT < nt) tc::commit(&sm.empty[t % NSLOT]);
+      };
+      auto scores = [&](int it) {  // P = A B^T
+        arrived(3 * it);
+        arrived(3 * it + 1);
+        tc::gemm128(tP, slot(3 * it + 1), false, slot(3 * it), false, false);
+        tc::commit(&sm.barP);
+      };
+      scores(0);
+      for (int it = 0; it < n_it; ++it) {
+        const int tb = 3 * it, ta = tb + 1, tcc = tb + 2;
+        w.on(&sm.barS, it);
+        if (it > 0) w.on(&sm.barOf, it - 1);
+        tc::fence_after();
+        tc::gemm128(tO1, slot(ta), false, smem_u32(sm.X), true, false);  // A X
+        release(ta);
+        w.on(&sm.barK, it);
+        arrived(tcc);
+        tc::fence_after();
+        tc::gemm128(tX, slot(tb), true, slot(tcc), true, true);          // X += B'^T C
+        tc::gemm128(tX, smem_u32(sm.lo), true, slot(tcc), true, true);
+        tc::commit(&sm.barX);
+        release(tb);
+        w.on(&sm.barPm, it);
+        tc::fence_after();
+        tc::gemm_ts_bmn(tO2, tP, slot(tcc), false);                      // P C
+        release(tcc);
+        tc::commit(&sm.barO);
+        if (it + 1 < n_it) scores(it + 1);
+      }
+    }
+  } else {
+    const int grp = warp >> 2, r = 32 * (warp & 3) + lane;   // TMEM lane = row r
+    const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
+    if (grp == 0) {  // ---- mask and decay of the scores
+      for (int it = 0; it < n_it; ++it) {
+        if (it % nc == 0) {  // a new head: its table of decays
+          asm volatile("bar.sync 1, 128;" ::: "memory");
+          sm.tab[r] = expf(a.decay[head_of(it)] * (float)r);
+          asm volatile("bar.sync 1, 128;" ::: "memory");
+        }
+        const int n = rows_of(chunk_of(it));
+        w.warp_on(&sm.barP, it);
+        tc::fence_after();
+#pragma unroll 1
+        for (int g = 0; g < 4; ++g) {
+          float v[32];
+          tc::ld32(tP + lane_base + 32 * g, v);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const int j = 32 * g + i, d = rev ? j - r : r - j;
+            v[i] = (d >= 0 && j < n) ? v[i] * sm.tab[d & (CH - 1)] : 0.f;
+          }
+          tc::st16_bf16(tP + lane_base + 16 * g, v);  // (columns already read)
+        }
+        tc::wait_st();
+        tc::fence_before();
+        tc::mbar_arrive(&sm.barPm);
+      }
+    } else if (grp == 1) {  // ---- the state: bf16 image of X, X <- e^{w n} X
+      for (int it = 0; it < n_it; ++it) {
+        const int j = head_of(it);
+        const float keep = expf(a.decay[j] * (float)rows_of(chunk_of(it)));
+        if (it > 0) {
+          w.warp_on(&sm.barX, it - 1);
+          tc::fence_after();
+        }
+        const bool first = it % nc == 0;
+        const long sh = (long)s * a.Hv + j;
+        const float* x0 = R.xseg ? R.xseg + ((long)slot * a.Hv + j) * HD * HD
+                                 : (R.x0 ? R.x0 + sh * HD * HD : nullptr);
+#pragma unroll 1
+        for (int g = 0; g < 4; ++g) {
+          float v[32];
+          if (!first) {
+            tc::ld32(tX + lane_base + 32 * g, v);
+          } else if (!x0) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0.f;
+          } else if (R.xt) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = x0[(32 * g + i) * HD + r];
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 f = *reinterpret_cast<const float4*>(x0 + r * HD + 32 * g + 4 * i);
+              v[4 * i] = f.x;
+              v[4 * i + 1] = f.y;
+              v[4 * i + 2] = f.z;
+              v[4 * i + 3] = f.w;
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint4 o;
+            o.x = pack_bf16(v[8 * c], v[8 * c + 1]);
+            o.y = pack_bf16(v[8 * c + 2], v[8 * c + 3]);
+            o.z = pack_bf16(v[8 * c + 4], v[8 * c + 5]);
+            o.w = pack_bf16(v[8 * c + 6], v[8 * c + 7]);
+            *reinterpret_cast<uint4*>(sm.X + tc::sw128_chunk(r, 4 * g + c, CH)) = o;
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] *= keep;
+          tc::st32(tX + lane_base + 32 * g, v);
+        }
+        tc::wait_st();
+        tc::fence_before();
+        tc::fence_proxy_async();
+        tc::mbar_arrive(&sm.barS);
+      }
+      if (R.xT) {  // (one segment: with more, the prefix has written the final state)
+        w.warp_on(&sm.barX, n_it - 1);
+        tc::fence_after();
+        float* dst = R.xT + ((long)s * a.Hv + hd) * HD * HD + r * HD;
+#pragma unroll 1
+        for (int g = 0; g < 4; ++g) {
+          float v[32];
+          tc::ld32(tX + lane_base + 32 * g, v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<float4*>(dst + 32 * g + 4 * i) =
+                make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        }
+        tc::fence_before();
+      }
+    } else if (grp == 2) {  // ---- output rows
+      const int Ho = R.shared ? a.Hk : a.Hv;
+      for (int it = 0; it < n_it; ++it) {
+        const int c = chunk_of(it), n = rows_of(c);
+        const float f = expf(a.decay[head_of(it)] * (float)(rev ? max(n - 1 - r, 0) : r + 1));
+        const bool sum = loops > 1, firsth = it < nc, lasth = it >= n_it - nc;
+        const long row = (long)q.start + (long)c * CH + r;
+        bf16* dst = R.out + (row * Ho + hd) * HD;
+        // running sums over the value heads, [head][4-column group][row]: this thread's own
+        float4* acc = sum ? reinterpret_cast<float4*>(R.acc) + (long)hd * 32 * a.total + row : nullptr;
+        w.warp_on(&sm.barO, it);
+        tc::fence_after();
+#pragma unroll 1
+        for (int g = 0; g < 4; ++g) {
+          float x[32], y[32];
+          tc::ld32(tO1 + lane_base + 32 * g, x);
+          tc::ld32(tO2 + lane_base + 32 * g, y);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] = f * x[i] + y[i];
+          if (sum && !firsth && r < n) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 p = acc[(long)(8 * g + i) * a.total];
+              x[4 * i] += p.x;
+              x[4 * i + 1] += p.y;
+              x[4 * i + 2] += p.z;
+              x[4 * i + 3] += p.w;
+            }
+          }
+          if (r >= n) {
+          } else if (sum && !lasth) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              acc[(long)(8 * g + i) * a.total] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint4 o;
+              o.x = pack_bf16(x[8 * i], x[8 * i + 1]);
+              o.y = pack_bf16(x[8 * i + 2], x[8 * i + 3]);
+              o.z = pack_bf16(x[8 * i + 4], x[8 * i + 5]);
+              o.w = pack_bf16(x[8 * i + 6], x[8 * i + 7]);
+              *reinterpret_cast<uint4*>(dst + 32 * g + 8 * i) = o;
+            }
+          }
+          __syncwarp();
+        }
+        tc::fence_before();
+        tc::mbar_arrive(&sm.barOf);
+      }
+    } else {  // ---- B' = diag(e) B in two bf16 terms; rows past the sequence's end are cleared
+      for (int it = 0; it < n_it; ++it) {
+        const int n = rows_of(chunk_of(it));
+        const float wd = a.decay[head_of(it)];
+        const int tb = 3 * it, tcc = tb + 2;
+        w.warp_on(&sm.full[tb % NSLOT], tb / NSLOT);
+        w.warp_on(&sm.barP, it);  // (A B^T, which reads the raw tile, has completed)
+        const float e = expf(wd * (float)(rev ? r + 1 : max(n - 1 - r, 0)));
+        scale_row(sm.slot[tb % NSLOT], sm.lo, r, 0, 16, e, r < n);
+        if (n < CH) {
+          w.warp_on(&sm.full[tcc % NSLOT], tcc / NSLOT);
+          if (r >= n) zero_row(sm.slot[tcc % NSLOT], r, 0, 16);
+        }
+        tc::fence_proxy_async();
+        tc::mbar_arrive(&sm.barK);
+      }
+    }
+  }
+  if (!w.ok && a.status) atomicOr(a.status, 1);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (warp == 0) tc::dealloc(sm.tmem, 512);
+}
+
+// ---- segments ----------------------------------------------------------------------
+struct FoldSmem {
+  unsigned char slot[FOLD_SLOTS][TILE];
+  unsigned char lo[TILE];
+  uint64_t full[FOLD_SLOTS], empty[FOLD_SLOTS];
+  uint64_t barK, barM;
+  uint32_t tmem;
+};
+
+__global__ void __launch_bounds__(FOLD_THREADS, 1) k_decay_fold(const __grid_constant__ DecayFoldArgs a) {
+  extern __shared__ unsigned char raw[];
+  FoldSmem& sm = *reinterpret_cast<FoldSmem*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int G = a.Hv / a.Hk;
+  pdl_wait();
+  pdl_release();
+  const int j = blockIdx.x % a.Hv, slot = blockIdx.x / a.Hv;
+  const int2 at = find_segment(a.cu, a.n_seqs, a.T, a.total, a.seg_chunks, a.nseg, slot);
+  const int s = at.x, seg = at.y;
+  if (s < 0) return;
+  const DecayFoldRole& R = a.role[blockIdx.y];
+  const Range q = seq_range(a.cu, s, a.T, a.total);
+  const int nch = (q.len + CH - 1) / CH;
+  const int cb = seg * a.seg_chunks, ce = min(nch, cb + a.seg_chunks), nc = ce - cb;
+  if (nc <= 0) return;
+  // the segment that the walk ends with matters only for the final state
+  if (!R.last && (R.rev ? cb == 0 : ce == nch)) return;
+  const int end = min(q.len, ce * CH);  // one past the segment's last token
+
+  if (tid == 0) {
+    for (int k = 0; k < FOLD_SLOTS; ++k) {
+      tc::mbar_init(&sm.full[k], 1);
+      tc::mbar_init(&sm.empty[k], 1);
+    }
+    tc::mbar_init(&sm.barK, 256);
+    tc::mbar_init(&sm.barM, 1);
+    tc::mbar_fence_init();
+  }
+  if (warp == 0) tc::alloc(&sm.tmem, 128);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tX = sm.tmem;
+  tc::Wait w;
+  if (warp == 9) {
+    if (lane == 0) {
+      const int nt = 2 * nc;
+      for (int t = 0; t < nt && w.ok; ++t) {
+        const int k = t % FOLD_SLOTS;
+        if (t >= FOLD_SLOTS) w.on(&sm.empty[k], t / FOLD_SLOTS - 1);
+        if (!w.ok) break;
+        load_tile(sm.slot[k], (t & 1) ? &R.c : &R.b, (t & 1) ? j : j / G, q.start + (cb + t / 2) * CH, &sm.full[k]);
+      }
+      if (w.ok)
+        for (int t = max(0, nt - FOLD_SLOTS); t < nt; ++t) w.on(&sm.full[t % FOLD_SLOTS], t / FOLD_SLOTS);
+      else
+        for (int k = 0; k < FOLD_SLOTS; ++k) tc::mbar_wait_sleep(&sm.full[k], 0, 4000000LL);
+    }
+  } else if (warp == 8) {
+    if (lane == 0) {
+      for (int i = 0; i < nc; ++i) {
+        const int tb = 2 * i, tcc = tb + 1;
+        w.on(&sm.barK, i);
+        w.on(&sm.full[tcc % FOLD_SLOTS], tcc / FOLD_SLOTS);
+        tc::fence_after();
+        const uint32_t c = smem_u32(sm.slot[tcc % FOLD_SLOTS]);
+        tc::gemm128(tX, smem_u32(sm.slot[tb % FOLD_SLOTS]), true, c, true, i > 0);
+        tc::gemm128(tX, smem_u32(sm.lo), true, c, true, true);
+        if (tb + FOLD_SLOTS < 2 * nc) tc::commit(&sm.empty[tb % FOLD_SLOTS]);
+        if (tcc + FOLD_SLOTS < 2 * nc) tc::commit(&sm.empty[tcc % FOLD_SLOTS]);
+        tc::commit(&sm.barM);
+      }
+    }
+  } else {
+    const int r = tid & 127, j0 = 8 * (tid >> 7);
+    const float wd = a.decay[j];
+    for (int i = 0; i < nc; ++i) {
+      const int t0 = (cb + i) * CH + r, n = min(CH, q.len - (cb + i) * CH);
+      const int tb = 2 * i, tcc = tb + 1;
+      // weight to the segment's end (forwards) or to its start (backwards)
+      const float e = expf(wd * (float)(R.rev ? t0 - cb * CH + 1 : max(end - 1 - t0, 0)));
+      if (i > 0) w.warp_on(&sm.barM, i - 1);  // (the second term of the chunk before has been read)
+      w.warp_on(&sm.full[tb % FOLD_SLOTS], tb / FOLD_SLOTS);
+      scale_row(sm.slot[tb % FOLD_SLOTS], sm.lo, r, j0, 8, e, r < n);
+      if (n < CH) {
+        w.warp_on(&sm.full[tcc % FOLD_SLOTS], tcc / FOLD_SLOTS);
+        if (r >= n) zero_row(sm.slot[tcc % FOLD_SLOTS], r, j0, 8);
+      }
+      tc::fence_proxy_async();
+      tc::mbar_arrive(&sm.barK);
+    }
+    w.warp_on(&sm.barM, nc - 1);
+    tc::fence_after();
+    const int row = 32 * (warp & 3) + lane, g0 = 2 * (warp >> 2);
+    const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
+    float* dst = R.x + ((long)slot * a.Hv + j) * HD * HD + row * HD;
+#pragma unroll 1
+    for (int g = g0; g < g0 + 2; ++g) {
+      float v[32];
+      tc::ld32(tX + lane_base + 32 * g, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        *reinterpret_cast<float4*>(dst + 32 * g + 4 * i) =
+            make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    }
+    tc::fence_before();
+  }
+  if (!w.ok && a.status) atomicOr(a.status, 1);
+  __syncthreads();
+  tc::fence_after();
+  if (warp == 0) tc::dealloc(sm.tmem, 128);
+}
+
+// Entering states from the segments' own ones, in place, and the final state:
+// run <- X0;  per segment in the pass's order: x <- run, run <- e^{w len} run + x.
+__global__ void __launch_bounds__(256) k_decay_prefix(const __grid_constant__ DecayFoldArgs a) {
+  pdl_wait();
+  pdl_release();
+  const int j = blockIdx.x % a.Hv, s = blockIdx.x / a.Hv;
+  const DecayFoldRole& R = a.role[blockIdx.z];
+  const Range q = seq_range(a.cu, s, a.T, a.total);
+  const int nch = (q.len + CH - 1) / CH, nseg = (nch + a.seg_chunks - 1) / a.seg_chunks;
+  const long sh = (long)s * a.Hv + j;
+  const int e = 4 * (blockIdx.y * 256 + threadIdx.x);  // 16 blocks cover the state
+  const float wd = a.decay[j];
+  const int slot0 = first_slot(a.cu, s, a.T, a.total, a.seg_chunks * CH);
+  float4 run = R.x0 ? *reinterpret_cast<const float4*>(R.x0 + sh * HD * HD + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i < nseg; ++i) {
+    const int seg = R.rev ? nseg - 1 - i : i;
+    float4* p = reinterpret_cast<float4*>(R.x + ((long)(slot0 + seg) * a.Hv + j) * HD * HD + e);
+    const bool need = R.last || i + 1 < nseg;  // (the last one's own state is not formed otherwise)
+    const float4 x = need ? *p : make_float4(0.f, 0.f, 0.f, 0.f);
+    *p = run;
+    const int len = min(q.len, (seg + 1) * a.seg_chunks * CH) - seg * a.seg_chunks * CH;
+    const float keep = expf(wd * (float)len);
+    run = make_float4(keep * run.x + x.x, keep * run.y + x.y, keep * run.z + x.z, keep * run.w + x.w);
+  }
+  if (R.last) *reinterpret_cast<float4*>(R.last + sh * HD * HD + e) = run;
+}
+
+template <typename K>
+cudaError_t set_smem(K k, size_t bytes) {
+  return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+}  // namespace
+
+cudaError_t launch_decay(const DecayArgs& a, cudaStream_t s) {
+  constexpr size_t smem = sizeof(WalkSmem) + 1024;
+  static_assert(smem <= 227 * 1024, "shared memory");
+  cudaError_t e = set_smem(k_decay, smem);
+  if (e != cudaSuccess) return e;
+  long units = 0;
+  for (int i = 0; i < a.n_roles; ++i) units += (long)a.slots * (a.role[i].shared ? a.Hk : a.Hv);
+  return launch_pdl(k_decay, dim3((unsigned)units), dim3(WALK_THREADS), smem, s, a);
+}
+
+cudaError_t launch_decay_fold(const DecayFoldArgs& a, cudaStream_t s) {
+  constexpr size_t smem = sizeof(FoldSmem) + 1024;
+  static_assert(smem <= 227 * 1024, "shared memory");
+  cudaError_t e = set_smem(k_decay_fold, smem);
+  if (e != cudaSuccess) return e;
+  const unsigned sh = (unsigned)((long)a.n_seqs * a.Hv);
+  e = launch_pdl(k_decay_fold, dim3((unsigned)a.slots * (unsigned)a.Hv, (unsigned)a.n_roles), dim3(FOLD_THREADS), smem, s, a);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k_decay_prefix, dim3(sh, HD * HD / 1024, (unsigned)a.n_roles), dim3(256), 0, s, a);
+}
+
+}  // namespace gdn

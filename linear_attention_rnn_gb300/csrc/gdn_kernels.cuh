@@ -140,6 +140,84 @@ struct GradArgs {
   int B, T, Hk, Hv, NC;
 };
 
+// Single-token forms (gdn_step.cu): rows r = 0 .. R - 1, state slot slots[r] (null: r).
+struct StepArgs {
+  const bf16* q;
+  const bf16* k;
+  const bf16* v;
+  const float* g;      // log-gate: [R][Hv] with beta (the delta rule), [Hv] without
+  const float* beta;   // [R][Hv]; null: linear attention with a decay for each head
+  float* state;        // [n_slots][Hv][HD][HD], updated in place
+  const int* slots;
+  bf16* o;             // [R][Hv][HD]
+  long R, n_slots;
+  long sq, sk, sv;     // elements between rows
+  int Hk, Hv;
+};
+
+// Linear attention with a decay for each head (gdn_decay.cu): one pass of the
+// chunk walk over rows a, b, c with entering state X0.
+struct DecayRole {
+  CUtensorMap a, b, c;  // rows [total][H][HD], boxes of 64 columns x 1 head x 128 rows
+  int ha, hb, hc;       // 1: a head for each value head; 0: shared by a group
+  int rev;              // 1: backwards in time
+  int xt;               // 1: X0 and the segments' states are stored transposed
+  int shared;           // 1: the output is one head for a group, summed over its value heads
+  const float* x0;      // [n_seqs][Hv][HD][HD] (nullable = 0)
+  const float* xseg;    // entering states [slots][Hv][HD][HD] (null with one segment)
+  float* xT;            // final state (one segment only, nullable)
+  float* acc;           // running sums [Hk][HD / 4][total][4] (shared, Hv > Hk)
+  bf16* out;
+};
+struct DecayArgs {
+  DecayRole role[3];
+  const float* decay;  // [Hv]
+  const int* cu;       // [n_seqs + 1] (null: T rows to each sequence)
+  int* status;
+  int n_roles, n_seqs, total, T, Hk, Hv;
+  int nseg, seg_chunks;  // most segments of a sequence, chunks to a segment
+  int slots;             // segment slots: n_seqs with nseg = 1, else total / (128 seg_chunks) + n_seqs
+};
+struct DecayFoldRole {
+  CUtensorMap b, c;    // b: shared heads, c: value heads
+  int rev;
+  const float* x0;     // (nullable = 0)
+  float* x;            // [slots][Hv][HD][HD]: own states, then entering states
+  float* last;         // final state (nullable)
+};
+struct DecayFoldArgs {
+  DecayFoldRole role[2];
+  const float* decay;
+  const int* cu;
+  int* status;
+  int n_roles, n_seqs, total, T, Hk, Hv;
+  int nseg, seg_chunks;  // most segments of a sequence, chunks to a segment
+  int slots;             // segment slots: n_seqs with nseg = 1, else total / (128 seg_chunks) + n_seqs
+};
+
+// Causal softmax attention over packed sequences (gdn_attn_fwd.cu, gdn_attn_bwd.cu).
+struct AttnArgs {
+  CUtensorMap q, k, v;  // q: boxes of 64 columns x a group's heads x 128 / G tokens; k, v: x 1 head x 128 rows
+  CUtensorMap dO;       // as q (backward)
+  const int* cu_q;      // [n_seqs + 1] (null: equal lengths), cu_k alike
+  const int* cu_k;
+  const int* k_len;     // [n_seqs] used rows of each sequence's keys (nullable; forward)
+  bf16* o;              // [total_q][Hq][HD]
+  float* lse;           // [total_q][Hq] (forward: nullable)
+  float* part;          // [n_splits][total_q][Hq][HD]
+  float* part_lse;      // [n_splits][total_q][Hq]
+  const bf16* dOp;      // backward: dO and o as plain rows, delta = dO . o
+  const bf16* op;
+  float* delta;         // [total_q][Hq]
+  bf16* dq;
+  bf16* dk;
+  bf16* dv;
+  int* status;
+  float scale;
+  int n_seqs, total_q, total_k, Hq, Hk;
+  int split_tiles, n_splits;  // key tiles to a split
+};
+
 // Launches kernel k with programmatic stream serialization: its CTAs may start
 // (and run up to their pdl_wait) while the previous kernel in the stream ends.
 template <typename... KArgs, typename... Args>
@@ -176,6 +254,13 @@ cudaError_t launch_l2norm_bwd(const bf16* x, const bf16* dy, bf16* dx, long rows
 cudaError_t launch_out_gate(const bf16* o, const bf16* z, bf16* y, long rows, cudaStream_t s);
 cudaError_t launch_out_gate_bwd(const bf16* o, const bf16* z, const bf16* dy, bf16* dO, bf16* dz, long rows,
                                 cudaStream_t s);
+cudaError_t launch_step(const StepArgs& a, cudaStream_t s);
+cudaError_t launch_decay(const DecayArgs& a, cudaStream_t s);
+// the segments' own states and the prefix over them (two launches)
+cudaError_t launch_decay_fold(const DecayFoldArgs& a, cudaStream_t s);
+cudaError_t launch_attn_fwd(const AttnArgs& a, cudaStream_t s);
+// dO . o per row, then the gradients of k and v, then that of q
+cudaError_t launch_attn_bwd(const AttnArgs& a, cudaStream_t s);
 // (A, B) = (I, 0) for n [HD x HD] fp32 pairs (A nullable).
 cudaError_t launch_identity_pairs(float* A, float* Bv, long n, cudaStream_t s);
 cudaError_t launch_grads(const GradArgs& a, cudaStream_t s);

@@ -1,0 +1,482 @@
+// gdn_ops.cu -- the extern "C" boundary of the operators around the chunked rule
+// (include/gdn.h): the single-token forms, linear attention with a decay for
+// each head, and causal softmax attention.  Arguments are checked on the host before anything is enqueued.
+#include <stdint.h>
+#include <string.h>
+
+#include "gdn.h"
+#include "gdn_kernels.cuh"
+#include "gdn_tmap.cuh"
+
+using namespace gdn;
+
+namespace {
+
+constexpr size_t ALIGN = 256;
+inline size_t up(size_t x) { return (x + ALIGN - 1) / ALIGN * ALIGN; }
+inline bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+int cuda_status(cudaError_t e) { return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA; }
+
+template <typename T>
+T* at(void* ws, size_t off) {
+  return reinterpret_cast<T*>(static_cast<char*>(ws) + off);
+}
+
+int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
+    sms = 152;
+  return sms;
+}
+
+// rows of H heads, `stride` elements apart: whole 16-byte pieces that do not overlap
+inline bool row_stride_ok(long long stride, int H) { return stride >= (long long)H * HD && stride % 8 == 0; }
+
+// ---- linear attention with a decay for each head -----------------------------------
+struct DecayPlan {
+  int nseg, seg_chunks, slots;
+  size_t status, xf, xr, accq, acck, total;
+};
+
+// Segments.  One CTA walks a segment of a head; without segments a call keeps
+// n_seqs Hv of them busy, for as long as the longest sequence takes.  With
+// segments each chunk of k and v is read twice (the fold) and two more kernels
+// start.  The estimate, in chunks of the walk: rounds of CTAs over the SMs, a
+// start of 2 per CTA, a fold at half a chunk's time, 4 for the two launches.
+DecayPlan decay_plan(int backward, int n_seqs, int total, int max_seqlen, int Hk, int Hv) {
+  DecayPlan p;
+  memset(&p, 0, sizeof p);
+  const long longest = max_seqlen < total ? max_seqlen : total;
+  const long nch = (longest + CH - 1) / CH;
+  p.nseg = 1;
+  p.seg_chunks = nch > 0 ? (int)nch : 1;
+  const double sms = sm_count();
+  // sequences that are about as long as the longest one
+  const double full = nch > 0 ? (double)total / (double)(longest > 0 ? longest : 1) : 1.0;
+  const double heads = (full < 1.0 ? 1.0 : full) * Hv * (backward ? 3.0 : 1.0);
+  double best = 1e300;
+  for (long k = 1; k <= nch && k <= 128; ++k) {
+    const long L = (nch + k - 1) / k;
+    const long segs = (nch + L - 1) / L;
+    const double rounds = (double)(long)((heads * segs + sms - 1.0) / sms);
+    double t = rounds * (L + 2.0);
+    if (segs > 1) t += rounds * (backward ? 0.67 : 1.0) * (0.5 * L + 1.0) + 4.0;
+    if (t < best * 0.97) {
+      best = t;
+      p.nseg = (int)segs;
+      p.seg_chunks = (int)L;
+    }
+  }
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off += up(bytes);
+    return o;
+  };
+  p.status = take(sizeof(int));
+  p.slots = n_seqs + (p.nseg > 1 ? total / (p.seg_chunks * CH) : 0);
+  const size_t states = p.nseg > 1 ? (size_t)p.slots * Hv * HD * HD * sizeof(float) : 0;
+  p.xf = take(states);
+  if (backward) {
+    p.xr = take(states);
+    const size_t acc = Hv > Hk ? (size_t)total * Hk * HD * sizeof(float) : 0;
+    p.accq = take(acc);
+    p.acck = take(acc);
+  }
+  p.total = off;
+  return p;
+}
+
+int decay_check(int n_seqs, int total, int max_seqlen, int Hk, int Hv, int d_k, int d_v, const int* cu, long long sq,
+                long long sk, long long sv) {
+  if (n_seqs < 0 || total < 0 || max_seqlen < 0 || Hk <= 0 || Hv <= 0 || Hv % Hk != 0) return GDN_ERR_ARG;
+  if (d_k != HD || d_v != HD) return GDN_ERR_SHAPE;
+  if (!cu && n_seqs > 0 && total % n_seqs != 0) return GDN_ERR_ARG;
+  // (blocks of the three passes in one grid dimension)
+  if (((long long)n_seqs + total / CH) * Hv > (1LL << 29)) return GDN_ERR_ARG;
+  if (!row_stride_ok(sq, Hk) || !row_stride_ok(sk, Hk) || !row_stride_ok(sv, Hv)) return GDN_ERR_ARG;
+  return GDN_OK;
+}
+
+// ---- causal softmax attention ---------------------------------------------------------
+struct AttnPlan {
+  int split_tiles, n_splits;
+  size_t status, part, part_lse, delta, total;
+};
+
+// Key splits of the forward.  A CTA holds 256 / G tokens of one key head; calls
+// with fewer of them than two to an SM, over more than 8 key tiles, are split
+// into four CTAs to an SM (by the longest sequence, so that ragged lengths
+// leave fewer of them with work), of 8 key tiles or more.
+AttnPlan attn_plan(int backward, int n_seqs, int total_q, int max_k, int Hq, int Hk) {
+  AttnPlan p;
+  memset(&p, 0, sizeof p);
+  const long tiles = ((long)max_k + CH - 1) / CH;
+  const long ctas = ((long)total_q / (2 * (CH / (Hq / Hk))) + n_seqs) * Hk;
+  const long sms = sm_count();
+  p.split_tiles = tiles > 0 ? (int)tiles : 1;
+  p.n_splits = 1;
+  if (!backward && ctas < 2 * sms && tiles > 8) {
+    long per = (ctas * tiles + 4 * sms - 1) / (4 * sms);
+    if (per < 8) per = 8;
+    p.split_tiles = (int)per;
+    p.n_splits = (int)((tiles + per - 1) / per);
+  }
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off += up(bytes);
+    return o;
+  };
+  p.status = take(sizeof(int));
+  const size_t rows = (size_t)total_q * Hq;
+  if (backward) {
+    p.delta = take(rows * sizeof(float));
+  } else if (p.n_splits > 1) {
+    p.part = take(rows * p.n_splits * HD * sizeof(float));
+    p.part_lse = take(rows * p.n_splits * sizeof(float));
+  }
+  p.total = off;
+  return p;
+}
+
+int attn_check(int n_seqs, int total_q, int total_k, int max_k, int Hq, int Hk, int d, const int* cu_q,
+               const int* cu_k, float scale, long long sq, long long sk, long long sv) {
+  if (n_seqs < 0 || total_q < 0 || total_k < 0 || max_k < 0 || Hq <= 0 || Hk <= 0 || Hq % Hk != 0) return GDN_ERR_ARG;
+  if (d != HD || Hq / Hk > CH) return GDN_ERR_SHAPE;
+  if (!(scale > 0.f) || scale > 1e30f) return GDN_ERR_ARG;
+  if (n_seqs > 0 && ((!cu_q && total_q % n_seqs != 0) || (!cu_k && total_k % n_seqs != 0))) return GDN_ERR_ARG;
+  if (!row_stride_ok(sq, Hq) || !row_stride_ok(sk, Hk) || !row_stride_ok(sv, Hk)) return GDN_ERR_ARG;
+  // (blocks of one launch in one grid dimension)
+  const long long tiles = (long long)total_q / (CH / (Hq / Hk)) + total_k / CH + n_seqs;
+  if (tiles * Hk > (1LL << 30) || (long long)total_q * Hq > (1LL << 33)) return GDN_ERR_ARG;
+  return GDN_OK;
+}
+
+// Tensor maps and the arguments that both directions share.
+int attn_args(AttnArgs& a, const void* q, const void* k, const void* v, const int* cu_q, const int* cu_k, int n_seqs,
+              int total_q, int total_k, int Hq, int Hk, float scale, long long sq, long long sk, long long sv) {
+  memset(&a, 0, sizeof a);
+  a.cu_q = cu_q;
+  a.cu_k = cu_k;
+  a.scale = scale;
+  a.n_seqs = n_seqs;
+  a.total_q = total_q;
+  a.total_k = total_k;
+  a.Hq = Hq;
+  a.Hk = Hk;
+  const int G = Hq / Hk;
+  if (!tmap_rows(&a.q, q, total_q, Hq, HD, (uint64_t)sq * 2, G, CH / G)) return GDN_ERR_CUDA;
+  if (total_k == 0) return GDN_OK;  // (no key tile is ever loaded)
+  if (!tmap_rows(&a.k, k, total_k, Hk, HD, (uint64_t)sk * 2, 1, CH) ||
+      !tmap_rows(&a.v, v, total_k, Hk, HD, (uint64_t)sv * 2, 1, CH))
+    return GDN_ERR_CUDA;
+  return GDN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+static int step(const void* q, const void* k, const void* v, const float* g, const float* beta, float* state,
+                const int* slots, void* o, int R, int n_slots, int Hk, int Hv, int d_k, int d_v, long long sq,
+                long long sk, long long sv, void* stream) {
+  if (R < 0 || n_slots < 0 || Hk <= 0 || Hv <= 0 || Hv % Hk != 0) return GDN_ERR_ARG;
+  if (d_k != HD || d_v != HD) return GDN_ERR_SHAPE;
+  if ((long long)R * Hv > (1LL << 28)) return GDN_ERR_ARG;  // four blocks to a state, one grid dimension
+  if (R == 0) return GDN_OK;
+  if (!q || !k || !v || !g || !state || !o) return GDN_ERR_ARG;
+  if (!row_stride_ok(sq, Hk) || !row_stride_ok(sk, Hk) || !row_stride_ok(sv, Hv)) return GDN_ERR_ARG;
+  const void* ptrs[] = {q, k, v, g, beta, state, o};
+  for (const void* p : ptrs)
+    if (p && !aligned(p, 16)) return GDN_ERR_ARG;
+  if (!aligned(slots, 4)) return GDN_ERR_ARG;
+  StepArgs a;
+  a.q = static_cast<const bf16*>(q);
+  a.k = static_cast<const bf16*>(k);
+  a.v = static_cast<const bf16*>(v);
+  a.g = g;
+  a.beta = beta;
+  a.state = state;
+  a.slots = slots;
+  a.o = static_cast<bf16*>(o);
+  a.R = R;
+  a.n_slots = n_slots;
+  a.sq = sq;
+  a.sk = sk;
+  a.sv = sv;
+  a.Hk = Hk;
+  a.Hv = Hv;
+  return cuda_status(launch_step(a, static_cast<cudaStream_t>(stream)));
+}
+
+int gdn_delta_step(const void* q, const void* k, const void* v, const float* g, const float* beta, float* state,
+                   const int* slots, void* o, int R, int n_slots, int Hk, int Hv, int d_k, int d_v,
+                   long long q_stride, long long k_stride, long long v_stride, void* stream) {
+  if (R > 0 && !beta) return GDN_ERR_ARG;
+  return step(q, k, v, g, beta, state, slots, o, R, n_slots, Hk, Hv, d_k, d_v, q_stride, k_stride, v_stride, stream);
+}
+
+int gdn_decay_step(const void* q, const void* k, const void* v, const float* decay, float* state, const int* slots,
+                   void* o, int R, int n_slots, int Hk, int Hv, int d_k, int d_v, long long q_stride,
+                   long long k_stride, long long v_stride, void* stream) {
+  return step(q, k, v, decay, nullptr, state, slots, o, R, n_slots, Hk, Hv, d_k, d_v, q_stride, k_stride, v_stride,
+              stream);
+}
+
+size_t gdn_decay_workspace_bytes(int backward, int n_seqs, int total, int max_seqlen, int Hk, int Hv, int d_k,
+                                 int d_v) {
+  if (decay_check(n_seqs, total, max_seqlen, Hk, Hv, d_k, d_v, reinterpret_cast<const int*>(4), (long long)Hk * HD,
+                  (long long)Hk * HD, (long long)Hv * HD) != GDN_OK)
+    return 0;
+  return decay_plan(backward != 0, n_seqs, total, max_seqlen, Hk, Hv).total;
+}
+
+// No rows at all: every sequence ends in the state that it began with.
+static int pass_state(const float* x0, float* xT, int n_seqs, int Hv, cudaStream_t s) {
+  if (!xT) return GDN_OK;
+  const size_t bytes = (size_t)n_seqs * Hv * HD * HD * sizeof(float);
+  return cuda_status(x0 ? cudaMemcpyAsync(xT, x0, bytes, cudaMemcpyDeviceToDevice, s)
+                        : cudaMemsetAsync(xT, 0, bytes, s));
+}
+
+int gdn_decay_fwd(const void* q, const void* k, const void* v, const float* decay, const float* h0,
+                  const int* cu_seqlens, void* o, float* hT, int n_seqs, int total, int max_seqlen, int Hk, int Hv,
+                  int d_k, int d_v, long long q_stride, long long k_stride, long long v_stride, void* ws,
+                  size_t ws_bytes, void* stream) {
+  int rc = decay_check(n_seqs, total, max_seqlen, Hk, Hv, d_k, d_v, cu_seqlens, q_stride, k_stride, v_stride);
+  if (rc) return rc;
+  const void* ptrs[] = {q, k, v, h0, o, hT, ws};
+  for (const void* p : ptrs)
+    if (p && !aligned(p, 16)) return GDN_ERR_ARG;
+  if (!aligned(decay, 4) || !aligned(cu_seqlens, 4)) return GDN_ERR_ARG;
+  if (n_seqs == 0) return GDN_OK;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (total == 0) return pass_state(h0, hT, n_seqs, Hv, s);
+  if (!q || !k || !v || !decay || !o) return GDN_ERR_ARG;
+  const DecayPlan p = decay_plan(0, n_seqs, total, max_seqlen, Hk, Hv);
+  if (!ws || ws_bytes < p.total) return GDN_ERR_WORKSPACE;
+  DecayArgs a;
+  memset(&a, 0, sizeof a);
+  a.decay = decay;
+  a.cu = cu_seqlens;
+  a.status = at<int>(ws, p.status);
+  a.n_seqs = n_seqs;
+  a.total = total;
+  a.T = total / n_seqs;
+  a.Hk = Hk;
+  a.Hv = Hv;
+  a.nseg = p.nseg;
+  a.seg_chunks = p.seg_chunks;
+  a.slots = p.slots;
+  a.n_roles = 1;
+  DecayRole& r = a.role[0];
+  if (!tmap_rows(&r.a, q, total, Hk, HD, (uint64_t)q_stride * 2, 1, CH) ||
+      !tmap_rows(&r.b, k, total, Hk, HD, (uint64_t)k_stride * 2, 1, CH) ||
+      !tmap_rows(&r.c, v, total, Hv, HD, (uint64_t)v_stride * 2, 1, CH))
+    return GDN_ERR_CUDA;
+  r.hc = 1;
+  r.x0 = h0;
+  r.out = static_cast<bf16*>(o);
+  if ((rc = cuda_status(cudaMemsetAsync(a.status, 0, sizeof(int), s)))) return rc;
+  if (p.nseg > 1) {
+    float* x = at<float>(ws, p.xf);
+    DecayFoldArgs f;
+    memset(&f, 0, sizeof f);
+    f.decay = decay;
+    f.cu = cu_seqlens;
+    f.status = a.status;
+    f.n_roles = 1;
+    f.n_seqs = n_seqs;
+    f.total = total;
+    f.T = a.T;
+    f.Hk = Hk;
+    f.Hv = Hv;
+    f.nseg = p.nseg;
+    f.seg_chunks = p.seg_chunks;
+    f.slots = p.slots;
+    f.role[0].b = r.b;
+    f.role[0].c = r.c;
+    f.role[0].x0 = h0;
+    f.role[0].x = x;
+    f.role[0].last = hT;
+    if ((rc = cuda_status(launch_decay_fold(f, s)))) return rc;
+    r.xseg = x;
+  } else {
+    r.xT = hT;
+  }
+  return cuda_status(launch_decay(a, s));
+}
+
+int gdn_decay_bwd(const void* q, const void* k, const void* v, const float* decay, const float* h0, const void* dO,
+                  const float* dhT, const int* cu_seqlens, void* dq, void* dk, void* dv, float* dh0, int n_seqs,
+                  int total, int max_seqlen, int Hk, int Hv, int d_k, int d_v, long long q_stride,
+                  long long k_stride, long long v_stride, void* ws, size_t ws_bytes, void* stream) {
+  int rc = decay_check(n_seqs, total, max_seqlen, Hk, Hv, d_k, d_v, cu_seqlens, q_stride, k_stride, v_stride);
+  if (rc) return rc;
+  const void* ptrs[] = {q, k, v, h0, dO, dhT, dq, dk, dv, dh0, ws};
+  for (const void* p : ptrs)
+    if (p && !aligned(p, 16)) return GDN_ERR_ARG;
+  if (!aligned(decay, 4) || !aligned(cu_seqlens, 4)) return GDN_ERR_ARG;
+  if (n_seqs == 0) return GDN_OK;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (total == 0) return pass_state(dhT, dh0, n_seqs, Hv, s);
+  if (!q || !k || !v || !decay || !dO || !dq || !dk || !dv) return GDN_ERR_ARG;
+  const DecayPlan p = decay_plan(1, n_seqs, total, max_seqlen, Hk, Hv);
+  if (!ws || ws_bytes < p.total) return GDN_ERR_WORKSPACE;
+  DecayArgs a;
+  memset(&a, 0, sizeof a);
+  a.decay = decay;
+  a.cu = cu_seqlens;
+  a.status = at<int>(ws, p.status);
+  a.n_seqs = n_seqs;
+  a.total = total;
+  a.T = total / n_seqs;
+  a.Hk = Hk;
+  a.Hv = Hv;
+  a.nseg = p.nseg;
+  a.seg_chunks = p.seg_chunks;
+  a.slots = p.slots;
+  a.n_roles = 3;
+  CUtensorMap mq, mk, mv, md;
+  if (!tmap_rows(&mq, q, total, Hk, HD, (uint64_t)q_stride * 2, 1, CH) ||
+      !tmap_rows(&mk, k, total, Hk, HD, (uint64_t)k_stride * 2, 1, CH) ||
+      !tmap_rows(&mv, v, total, Hv, HD, (uint64_t)v_stride * 2, 1, CH) ||
+      !tmap_rows(&md, dO, total, Hv, HD, (uint64_t)Hv * HD * 2, 1, CH))
+    return GDN_ERR_CUDA;
+  // the longest CTAs first: dq and dk walk a group's value heads one behind another
+  DecayRole &rq = a.role[0], &rk = a.role[1], &rv = a.role[2];
+  rq.a = md, rq.b = mv, rq.c = mk;
+  rq.ha = rq.hb = 1;
+  rq.xt = 1;
+  rq.shared = 1;
+  rq.x0 = h0;
+  rq.acc = Hv > Hk ? at<float>(ws, p.accq) : nullptr;
+  rq.out = static_cast<bf16*>(dq);
+  rk.a = mv, rk.b = md, rk.c = mq;
+  rk.ha = rk.hb = 1;
+  rk.rev = 1;
+  rk.xt = 1;
+  rk.shared = 1;
+  rk.x0 = dhT;
+  rk.acc = Hv > Hk ? at<float>(ws, p.acck) : nullptr;
+  rk.out = static_cast<bf16*>(dk);
+  rv.a = mk, rv.b = mq, rv.c = md;
+  rv.hc = 1;
+  rv.rev = 1;
+  rv.x0 = dhT;
+  rv.out = static_cast<bf16*>(dv);
+  if ((rc = cuda_status(cudaMemsetAsync(a.status, 0, sizeof(int), s)))) return rc;
+  if (p.nseg > 1) {
+    DecayFoldArgs f;
+    memset(&f, 0, sizeof f);
+    f.decay = decay;
+    f.cu = cu_seqlens;
+    f.status = a.status;
+    f.n_roles = 2;
+    f.n_seqs = n_seqs;
+    f.total = total;
+    f.T = a.T;
+    f.Hk = Hk;
+    f.Hv = Hv;
+    f.nseg = p.nseg;
+    f.seg_chunks = p.seg_chunks;
+    f.slots = p.slots;
+    f.role[0].b = mk;
+    f.role[0].c = mv;
+    f.role[0].x0 = h0;
+    f.role[0].x = at<float>(ws, p.xf);
+    f.role[1].b = mq;
+    f.role[1].c = md;
+    f.role[1].rev = 1;
+    f.role[1].x0 = dhT;
+    f.role[1].x = at<float>(ws, p.xr);
+    f.role[1].last = dh0;
+    if ((rc = cuda_status(launch_decay_fold(f, s)))) return rc;
+    rq.xseg = f.role[0].x;
+    rk.xseg = rv.xseg = f.role[1].x;
+  } else {
+    rv.xT = dh0;
+  }
+  return cuda_status(launch_decay(a, s));
+}
+
+size_t gdn_attn_workspace_bytes(int backward, int n_seqs, int total_q, int total_k, int max_k, int Hq, int Hk,
+                                int d) {
+  const int* some = reinterpret_cast<const int*>(4);
+  if (attn_check(n_seqs, total_q, total_k, max_k, Hq, Hk, d, some, some, 1.f, (long long)Hq * HD, (long long)Hk * HD,
+                 (long long)Hk * HD) != GDN_OK)
+    return 0;
+  return attn_plan(backward != 0, n_seqs, total_q, max_k < total_k ? max_k : total_k, Hq, Hk).total;
+}
+
+int gdn_attn_fwd(const void* q, const void* k, const void* v, const int* cu_q, const int* cu_k, const int* k_len,
+                 void* o, float* lse, int n_seqs, int total_q, int total_k, int max_k, int Hq, int Hk, int d,
+                 float scale, long long q_stride, long long k_stride, long long v_stride, void* ws, size_t ws_bytes,
+                 void* stream) {
+  int rc = attn_check(n_seqs, total_q, total_k, max_k, Hq, Hk, d, cu_q, cu_k, scale, q_stride, k_stride, v_stride);
+  if (rc) return rc;
+  const void* ptrs[] = {q, k, v, o, ws};
+  for (const void* p : ptrs)
+    if (p && !aligned(p, 16)) return GDN_ERR_ARG;
+  if (!aligned(cu_q, 4) || !aligned(cu_k, 4) || !aligned(k_len, 4) || !aligned(lse, 4)) return GDN_ERR_ARG;
+  if (n_seqs == 0 || total_q == 0) return GDN_OK;
+  if (!q || !o || (total_k > 0 && (!k || !v))) return GDN_ERR_ARG;
+  const AttnPlan p = attn_plan(0, n_seqs, total_q, max_k < total_k ? max_k : total_k, Hq, Hk);
+  if (!ws || ws_bytes < p.total) return GDN_ERR_WORKSPACE;
+  AttnArgs a;
+  if ((rc = attn_args(a, q, k, v, cu_q, cu_k, n_seqs, total_q, total_k, Hq, Hk, scale, q_stride, k_stride, v_stride)))
+    return rc;
+  a.k_len = k_len;
+  a.o = static_cast<bf16*>(o);
+  a.lse = lse;
+  a.status = at<int>(ws, p.status);
+  a.split_tiles = p.split_tiles;
+  a.n_splits = p.n_splits;
+  a.part = at<float>(ws, p.part);
+  a.part_lse = at<float>(ws, p.part_lse);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if ((rc = cuda_status(cudaMemsetAsync(a.status, 0, sizeof(int), s)))) return rc;
+  return cuda_status(launch_attn_fwd(a, s));
+}
+
+int gdn_attn_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dO,
+                 const int* cu_q, const int* cu_k, void* dq, void* dk, void* dv, int n_seqs, int total_q, int total_k,
+                 int Hq, int Hk, int d, float scale, long long q_stride, long long k_stride, long long v_stride,
+                 void* ws, size_t ws_bytes, void* stream) {
+  int rc = attn_check(n_seqs, total_q, total_k, 0, Hq, Hk, d, cu_q, cu_k, scale, q_stride, k_stride, v_stride);
+  if (rc) return rc;
+  const void* ptrs[] = {q, k, v, o, dO, dq, dk, dv, ws};
+  for (const void* p : ptrs)
+    if (p && !aligned(p, 16)) return GDN_ERR_ARG;
+  if (!aligned(cu_q, 4) || !aligned(cu_k, 4) || !aligned(lse, 4)) return GDN_ERR_ARG;
+  if (n_seqs == 0) return GDN_OK;
+  if (total_q > 0 && (!q || !o || !lse || !dO || !dq)) return GDN_ERR_ARG;
+  if (total_k > 0 && (!k || !v || !dk || !dv)) return GDN_ERR_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (total_q == 0 || total_k == 0) {  // no pair of a query and a key: zero gradients
+    const size_t nq = (size_t)total_q * Hq * HD * sizeof(bf16), nk = (size_t)total_k * Hk * HD * sizeof(bf16);
+    if (nq && (rc = cuda_status(cudaMemsetAsync(dq, 0, nq, s)))) return rc;
+    if (nk && (rc = cuda_status(cudaMemsetAsync(dk, 0, nk, s)))) return rc;
+    return nk ? cuda_status(cudaMemsetAsync(dv, 0, nk, s)) : GDN_OK;
+  }
+  const AttnPlan p = attn_plan(1, n_seqs, total_q, total_k, Hq, Hk);
+  if (!ws || ws_bytes < p.total) return GDN_ERR_WORKSPACE;
+  AttnArgs a;
+  if ((rc = attn_args(a, q, k, v, cu_q, cu_k, n_seqs, total_q, total_k, Hq, Hk, scale, q_stride, k_stride, v_stride)))
+    return rc;
+  if (!tmap_rows(&a.dO, dO, total_q, Hq, HD, (uint64_t)Hq * HD * 2, Hq / Hk, CH / (Hq / Hk))) return GDN_ERR_CUDA;
+  a.lse = const_cast<float*>(lse);
+  a.dOp = static_cast<const bf16*>(dO);
+  a.op = static_cast<const bf16*>(o);
+  a.delta = at<float>(ws, p.delta);
+  a.dq = static_cast<bf16*>(dq);
+  a.dk = static_cast<bf16*>(dk);
+  a.dv = static_cast<bf16*>(dv);
+  a.status = at<int>(ws, p.status);
+  if ((rc = cuda_status(cudaMemsetAsync(a.status, 0, sizeof(int), s)))) return rc;
+  return cuda_status(launch_attn_bwd(a, s));
+}
+
+}  // extern "C"

@@ -359,5 +359,67 @@ __device__ __forceinline__ uint32_t sw64_chunk(int r, int j) {
   return (uint32_t)(r * 64 + ((j ^ ((r >> 1) & 3)) << 4));
 }
 
+// 3-D tiled load (columns, head, token)
+__device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+      "%3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// A thread's bounded waits on mbarriers (the phase of parity p & 1): once one has
+// given up, the later ones return at once, and ok says so.  warp_on is for
+// waits that all 32 lanes make, and brings them together again before the
+// warp-wide instructions that follow.
+struct Wait {
+  bool ok = true;
+  __device__ __forceinline__ void on(uint64_t* bar, uint32_t p) {
+    if (ok) ok = mbar_wait_sleep(bar, p & 1u);
+  }
+  __device__ __forceinline__ void warp_on(uint64_t* bar, uint32_t p) {
+    on(bar, p);
+    __syncwarp();
+  }
+};
+
+// ---- A operand in tensor memory ----------------------------------------------------
+// The [128 x K] bf16 A operand: row m is TMEM lane m, and each 32-bit column
+// holds two consecutive K elements (the lower one in the low half), so a
+// K = 16 step reads 8 columns.
+__device__ __forceinline__ void mma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t db, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(db), "r"(idesc), "r"(accumulate));
+}
+// D[128 x 128] (+)= A B, A in tensor memory (K = 128: 64 columns), B a [128 (K)
+// rows x 128] SW128 tile read MN-major (as gemm_bmn_k128)
+__device__ __forceinline__ void gemm_ts_bmn(uint32_t tmem_d, uint32_t tmem_a, uint32_t b_smem,
+                                            bool accumulate_first) {
+  const uint32_t idesc = idesc_bf16(128, 128) | (1u << 16);
+  const uint64_t db0 = desc_sw128_mn(b_smem, 128u * 128u);
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    mma_ts(tmem_d, tmem_a + 8u * (uint32_t)k, db0 + (((uint32_t)k * 2048u) >> 4), idesc,
+           (k > 0 || accumulate_first) ? 1u : 0u);
+}
+// 32 values as 16 packed bf16 columns of this thread's TMEM lane (complete after wait_st)
+__device__ __forceinline__ void st16_bf16(uint32_t taddr, const float (&v)[32]) {
+  uint32_t r[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) r[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
 }  // namespace tc
 }  // namespace gdn

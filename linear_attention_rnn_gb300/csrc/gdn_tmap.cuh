@@ -84,4 +84,20 @@ inline bool tmap_heads_box(CUtensorMap* m, const void* base, int B, int T, int H
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// bf16 rows [N][H][D] whose tokens are token_bytes apart (a multiple of 16);
+// box = 64 columns of box_heads heads over box_tokens tokens (128-byte
+// swizzle), tokens past N read as zero.
+inline bool tmap_rows(CUtensorMap* m, const void* base, uint64_t N, int H, int D, uint64_t token_bytes,
+                      uint32_t box_heads, uint32_t box_tokens) {
+  auto enc = tmap_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)N};
+  cuuint64_t strides[2] = {(cuuint64_t)D * 2, token_bytes};
+  cuuint32_t box[3] = {64, box_heads, box_tokens};
+  cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace gdn
