@@ -120,11 +120,13 @@ def lib():
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-def _stream(device) -> ctypes.c_void_p:
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+def _stream(device) -> int:
+    """The raw handle of the device's current stream (without the Stream object
+    that torch.cuda.current_stream builds, 2 us of a single-token call)."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _check(t, name, dtype, shape=None):
@@ -136,7 +138,7 @@ def _check(t, name, dtype, shape=None):
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
@@ -372,6 +374,9 @@ def _check_rows(t, name, H, d, n=None):
     """bf16 rows [.., H, d] whose heads and columns are contiguous; the tokens may
     be further apart (a part of a wider buffer).  Returns the elements between
     tokens."""
+    if (t.dtype is torch.bfloat16 and t.is_cuda and t.is_contiguous() and t.dim() > 2
+            and t.shape[-2:] == (H, d) and (n is None or t.numel() == n * H * d)):
+        return H * d
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != torch.bfloat16:

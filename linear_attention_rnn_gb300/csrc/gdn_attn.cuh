@@ -99,17 +99,5 @@ __device__ __forceinline__ void store32(bf16* dst, const float (&v)[32], float f
   }
 }
 
-// D (+)= A B with A a bf16 operand in tensor memory whose first 64 K-values lie at
-// column 0 and last 64 at column 64 (each half written over the fp32 half that
-// its writers read), B a [128 (K) rows x 128] tile
-__device__ __forceinline__ void gemm_ts_halves(uint32_t d, uint32_t ta, uint32_t b_smem, bool accumulate_first) {
-  const uint32_t idesc = tc::idesc_bf16(128, 128) | (1u << 16);
-  const uint64_t db0 = tc::desc_sw128_mn(b_smem, 128u * 128u);
-#pragma unroll
-  for (int k = 0; k < 8; ++k)
-    tc::mma_ts(d, ta + 64u * (uint32_t)(k >> 2) + 8u * (uint32_t)(k & 3), db0 + (((uint32_t)k * 2048u) >> 4), idesc,
-               (k > 0 || accumulate_first) ? 1u : 0u);
-}
-
 }  // namespace attn
 }  // namespace gdn

@@ -2,8 +2,8 @@
 //
 // With p_ij = e^{scale q_i . k_j - lse_i} (recomputed), dp_ij = dO_i . v_j and
 // delta_i = dO_i . o_i:
-//     ds_ij = scale p_ij (dp_ij - delta_i),
-//     dv_j = sum_i p_ij dO_i,   dk_j = sum_i ds_ij q_i,   dq_i = sum_j ds_ij k_j.
+//     ds_ij = p_ij (dp_ij - delta_i),
+//     dv_j = sum_i p_ij dO_i,   dk_j = scale sum_i ds_ij q_i,   dq_i = scale sum_j ds_ij k_j.
 //
 // Two kernels, so that every gradient is summed in one CTA, in a fixed order,
 // without atomics (seven products per tile pair instead of five):
@@ -35,6 +35,7 @@ constexpr int Q_SLOTS = 5;   // K, V of two key tiles and a half
 __global__ void __launch_bounds__(256) k_attn_delta(const __grid_constant__ AttnArgs a) {
   pdl_wait();
   pdl_release();
+  clear_status(a.status);
   const long rows = (long)a.total_q * a.Hq, row = (long)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (row >= rows) return;
@@ -51,8 +52,9 @@ __global__ void __launch_bounds__(256) k_attn_delta(const __grid_constant__ Attn
 struct KvSmem {
   unsigned char k[TILE], v[TILE];
   unsigned char slot[KV_SLOTS][TILE];
-  float lse[2][CH], delta[2][CH];
-  int lim[2][CH];
+  alignas(16) float lse[2][CH];  // of the query rows: lse in base 2, delta, the last key seen
+  alignas(16) float delta[2][CH];
+  alignas(16) int lim[2][CH];
   uint64_t full[KV_SLOTS], empty[KV_SLOTS];
   uint64_t barKV, barS, barD, barP, barDs, barEnd;
   uint32_t tmem;
@@ -61,7 +63,7 @@ struct KvSmem {
 __global__ void __launch_bounds__(BWD_THREADS, 1) k_attn_dkv(const __grid_constant__ AttnArgs a) {
   extern __shared__ unsigned char raw[];
   KvSmem& sm = *reinterpret_cast<KvSmem*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tc::warp_index();
   pdl_wait();
   pdl_release();
   const int G = a.Hq / a.Hk, TT = CH / G;
@@ -119,38 +121,39 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) k_attn_dkv(const __grid_consta
       }
     }
   } else if (warp == 8) {
-    if (lane == 0 && n > 0) {
+    const uint32_t lead = tc::elect_leader();
+    if (n > 0) {
       auto slot = [&](int t) { return smem_u32(sm.slot[t % KV_SLOTS]); };
-      auto arrived = [&](int t) { w.on(&sm.full[t % KV_SLOTS], t / KV_SLOTS); };
+      auto arrived = [&](int t) { w.warp_on(&sm.full[t % KV_SLOTS], t / KV_SLOTS); };
       auto release = [&](int t) {
-        if (t + KV_SLOTS < nt) tc::commit(&sm.empty[t % KV_SLOTS]);
+        if (t + KV_SLOTS < nt) tc::commit_by(lead, &sm.empty[t % KV_SLOTS]);
       };
       auto scores = [&](int i) {
         arrived(2 * i);
-        tc::gemm128(tS, smem_u32(sm.k), false, slot(2 * i), false, false);
-        tc::commit(&sm.barS);
+        tc::gemm128_by<false, false>(lead, tS, smem_u32(sm.k), slot(2 * i), false);
+        tc::commit_by(lead, &sm.barS);
       };
       auto dscores = [&](int i) {
         arrived(2 * i + 1);
-        tc::gemm128(tP, smem_u32(sm.v), false, slot(2 * i + 1), false, false);
-        tc::commit(&sm.barD);
+        tc::gemm128_by<false, false>(lead, tP, smem_u32(sm.v), slot(2 * i + 1), false);
+        tc::commit_by(lead, &sm.barD);
       };
-      w.on(&sm.barKV, 0);
+      w.warp_on(&sm.barKV, 0);
       scores(0);
       dscores(0);
       for (int i = 0; i < n; ++i) {
-        w.on(&sm.barP, i);
+        w.warp_on(&sm.barP, i);
         tc::fence_after();
-        gemm_ts_halves(tV, tS, slot(2 * i + 1), i > 0);  // dV += P^T dO
+        tc::gemm_ts_by<true>(lead, tV, tS, slot(2 * i + 1), i > 0);  // dV += P^T dO
         if (i + 1 < n) scores(i + 1);
-        w.on(&sm.barDs, i);
+        w.warp_on(&sm.barDs, i);
         tc::fence_after();
-        gemm_ts_halves(tK, tP, slot(2 * i), i > 0);      // dK += dS^T Q
+        tc::gemm_ts_by<true>(lead, tK, tP, slot(2 * i), i > 0);      // dK += dS^T Q
         release(2 * i);
         release(2 * i + 1);
         if (i + 1 < n) dscores(i + 1);
       }
-      tc::commit(&sm.barEnd);
+      tc::commit_by(lead, &sm.barEnd);
     }
   } else {
     const int g0 = warp >> 2, r = 32 * (warp & 3) + lane;  // key row r, columns 64 g0 .. 64 g0 + 63
@@ -158,36 +161,56 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) k_attn_dkv(const __grid_consta
     const uint32_t S = tS + lane_base + 64 * g0, P = tP + lane_base + 64 * g0;
     const int key = key0 + r;
     const float sc = a.scale * LOG2E;
-    // what a query row needs: the last key that it sees, lse (base 2), delta
-    auto load_cols = [&](int i) {
-      if (tid < CH) {
-        const int tok = (first + i) * TT + tid / G;
-        const bool ok = tid < TT * G && tok < sq.ql;
-        const long row = ((long)sq.q0 + tok) * a.Hq + kh * G + tid % G;
-        sm.lim[i & 1][tid] = ok ? tok + off : -1;
-        sm.lse[i & 1][tid] = ok ? a.lse[row] * LOG2E : 0.f;
-        sm.delta[i & 1][tid] = ok ? a.delta[row] : 0.f;
-      }
+    // Per query row (a column here): lse (base 2), delta and the last key that it
+    // sees, read from global memory two tiles ahead, written to shared memory one ahead.
+    float c_lse = 0.f, c_delta = 0.f;
+    int c_lim = -1;
+    auto fetch_cols = [&](int i) {
+      const int tok = (first + i) * TT + tid / G;
+      const bool ok = tid < TT * G && tok < sq.ql;
+      const long row = ((long)sq.q0 + tok) * a.Hq + kh * G + tid % G;
+      c_lim = ok ? tok + off : -1;
+      c_lse = ok ? a.lse[row] : 0.f;
+      c_delta = ok ? a.delta[row] : 0.f;
     };
-    if (n > 0) load_cols(0);
+    auto put_cols = [&](int i) {
+      sm.lim[i & 1][tid] = c_lim;
+      sm.lse[i & 1][tid] = c_lse * LOG2E;
+      sm.delta[i & 1][tid] = c_delta;
+    };
+    if (n > 0 && tid < CH) {
+      fetch_cols(0);
+      put_cols(0);
+      fetch_cols(1);
+    }
     asm volatile("bar.sync 1, 256;" ::: "memory");
     for (int i = 0; i < n; ++i) {
-      if (i + 1 < n) load_cols(i + 1);
       const int b = i & 1;
       const int tok0 = (first + i) * TT, live = min(sq.ql - tok0, TT) * G;  // rows of tokens that exist
       const bool whole = live == CH && key0 + CH - 1 <= tok0 + off;         // every row sees every key
+      const float4* c_l = reinterpret_cast<const float4*>(sm.lse[b] + 64 * g0);
+      const float4* c_d = reinterpret_cast<const float4*>(sm.delta[b] + 64 * g0);
+      const int4* c_m = reinterpret_cast<const int4*>(sm.lim[b] + 64 * g0);
       float p[64];
       w.warp_on(&sm.barS, i);
       tc::fence_after();
+      tc::ld64(S, p);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float(&v)[32] = *reinterpret_cast<float(*)[32]>(p + 32 * h);
-        tc::ld32(S + 32 * h, v);
+      for (int j = 0; j < 16; ++j) {
+        const float4 l = c_l[j];
+        p[4 * j] = ex2(p[4 * j] * sc - l.x);
+        p[4 * j + 1] = ex2(p[4 * j + 1] * sc - l.y);
+        p[4 * j + 2] = ex2(p[4 * j + 2] * sc - l.z);
+        p[4 * j + 3] = ex2(p[4 * j + 3] * sc - l.w);
+      }
+      if (!whole) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const int c = 64 * g0 + 32 * h + j;
-          const float e = ex2(v[j] * sc - sm.lse[b][c]);
-          v[j] = whole || key <= sm.lim[b][c] ? e : 0.f;
+        for (int j = 0; j < 16; ++j) {
+          const int4 m = c_m[j];
+          p[4 * j] = key <= m.x ? p[4 * j] : 0.f;
+          p[4 * j + 1] = key <= m.y ? p[4 * j + 1] : 0.f;
+          p[4 * j + 2] = key <= m.z ? p[4 * j + 2] : 0.f;
+          p[4 * j + 3] = key <= m.w ? p[4 * j + 3] : 0.f;
         }
       }
 #pragma unroll
@@ -204,20 +227,28 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) k_attn_dkv(const __grid_consta
       tc::wait_st();
       tc::fence_before();
       tc::mbar_arrive(&sm.barP);
+      if (tid < CH && i + 1 < n) {
+        put_cols(i + 1);
+        fetch_cols(i + 2);
+      }
       w.warp_on(&sm.barD, i);
       tc::fence_after();
+      float v[64];
+      tc::ld64(P, v);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float v[32];
-        tc::ld32(P + 32 * h, v);
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const int c = 64 * g0 + 32 * h + j;
-          const float q = p[32 * h + j];
-          v[j] = whole || key <= sm.lim[b][c] ? q * (v[j] - sm.delta[b][c]) * a.scale : 0.f;
-        }
-        tc::st16_bf16(P + 16 * h, v);
+      for (int j = 0; j < 16; ++j) {
+        const float4 d = c_d[j];
+        v[4 * j] = p[4 * j] * (v[4 * j] - d.x);
+        v[4 * j + 1] = p[4 * j + 1] * (v[4 * j + 1] - d.y);
+        v[4 * j + 2] = p[4 * j + 2] * (v[4 * j + 2] - d.z);
+        v[4 * j + 3] = p[4 * j + 3] * (v[4 * j + 3] - d.w);
       }
+      if (!whole) {  // (a masked dP may be anything, NaN too)
+#pragma unroll
+        for (int j = 0; j < 64; ++j) v[j] = p[j] == 0.f ? 0.f : v[j];
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) tc::st16_bf16(P + 16 * h, *reinterpret_cast<float(*)[32]>(v + 32 * h));
       tc::wait_st();
       tc::fence_before();
       tc::mbar_arrive(&sm.barDs);
@@ -235,7 +266,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) k_attn_dkv(const __grid_consta
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = 0.f;
       }
-      if (key < sq.kl) store32((g0 ? a.dk : a.dv) + row * HD + 32 * h, v, 1.f);
+      if (key < sq.kl) store32((g0 ? a.dk : a.dv) + row * HD + 32 * h, v, g0 ? a.scale : 1.f);
       __syncwarp();
     }
     tc::fence_before();
@@ -258,7 +289,7 @@ struct QSmem {
 __global__ void __launch_bounds__(BWD_THREADS, 1) k_attn_dq(const __grid_constant__ AttnArgs a) {
   extern __shared__ unsigned char raw[];
   QSmem& sm = *reinterpret_cast<QSmem*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tc::warp_index();
   pdl_wait();
   pdl_release();
   const int G = a.Hq / a.Hk, TT = CH / G;
@@ -313,35 +344,36 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) k_attn_dq(const __grid_constan
       }
     }
   } else if (warp == 8) {
-    if (lane == 0 && n > 0) {
+    const uint32_t lead = tc::elect_leader();
+    if (n > 0) {
       auto slot = [&](int t) { return smem_u32(sm.slot[t % Q_SLOTS]); };
-      auto arrived = [&](int t) { w.on(&sm.full[t % Q_SLOTS], t / Q_SLOTS); };
+      auto arrived = [&](int t) { w.warp_on(&sm.full[t % Q_SLOTS], t / Q_SLOTS); };
       auto release = [&](int t) {
-        if (t + Q_SLOTS < nt) tc::commit(&sm.empty[t % Q_SLOTS]);
+        if (t + Q_SLOTS < nt) tc::commit_by(lead, &sm.empty[t % Q_SLOTS]);
       };
       auto scores = [&](int i) {
         arrived(2 * i);
-        tc::gemm128(tS + 128 * (i & 1), smem_u32(sm.q), false, slot(2 * i), false, false);
-        tc::commit(&sm.barS);
+        tc::gemm128_by<false, false>(lead, tS + 128 * (i & 1), smem_u32(sm.q), slot(2 * i), false);
+        tc::commit_by(lead, &sm.barS);
       };
       auto dscores = [&](int i) {
         arrived(2 * i + 1);
-        tc::gemm128(tP, smem_u32(sm.dO), false, slot(2 * i + 1), false, false);
+        tc::gemm128_by<false, false>(lead, tP, smem_u32(sm.dO), slot(2 * i + 1), false);
         release(2 * i + 1);
-        tc::commit(&sm.barD);
+        tc::commit_by(lead, &sm.barD);
       };
-      w.on(&sm.barQ, 0);
+      w.warp_on(&sm.barQ, 0);
       scores(0);
       dscores(0);
       for (int i = 0; i < n; ++i) {
         if (i + 1 < n) scores(i + 1);  // (its buffer's last S was read before dS i - 1 was signalled)
-        w.on(&sm.barDs, i);
+        w.warp_on(&sm.barDs, i);
         tc::fence_after();
-        gemm_ts_halves(tQ, tP, slot(2 * i), i > 0);  // dQ += dS K
+        tc::gemm_ts_by<true>(lead, tQ, tP, slot(2 * i), i > 0);  // dQ += dS K
         release(2 * i);
         if (i + 1 < n) dscores(i + 1);
       }
-      tc::commit(&sm.barEnd);
+      tc::commit_by(lead, &sm.barEnd);
     }
   } else {
     const int g0 = warp >> 2, r = 32 * (warp & 3) + lane;  // query row r, columns 64 g0 .. 64 g0 + 63
@@ -360,13 +392,9 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) k_attn_dq(const __grid_constan
       float p[64];
       w.warp_on(&sm.barS, i);
       tc::fence_after();
+      tc::ld64(S, p);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float(&v)[32] = *reinterpret_cast<float(*)[32]>(p + 32 * h);
-        tc::ld32(S + 32 * h, v);
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = ex2(v[j] * sc - lse);
-      }
+      for (int j = 0; j < 64; ++j) p[j] = ex2(p[j] * sc - lse);
       if (key0 + CH > sq.kl) {  // rows past the keys: whatever they hold, they count as zero
         const int t = 2 * i;
         w.warp_on(&sm.full[t % Q_SLOTS], t / Q_SLOTS);
@@ -375,17 +403,16 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) k_attn_dq(const __grid_constan
       }
       w.warp_on(&sm.barD, i);
       tc::fence_after();
+      float v[64];
+      tc::ld64(P, v);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float v[32];
-        tc::ld32(P + 32 * h, v);
+      for (int j = 0; j < 64; ++j) v[j] = p[j] * (v[j] - delta);
+      if (!whole) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float d = p[32 * h + j] * (v[j] - delta) * a.scale;
-          v[j] = whole || key0 + 64 * g0 + 32 * h + j <= lim ? d : 0.f;
-        }
-        tc::st16_bf16(P + 16 * h, v);
+        for (int j = 0; j < 64; ++j) v[j] = key0 + 64 * g0 + j <= lim ? v[j] : 0.f;
       }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) tc::st16_bf16(P + 16 * h, *reinterpret_cast<float(*)[32]>(v + 32 * h));
       tc::wait_st();
       tc::fence_before();
       tc::mbar_arrive(&sm.barDs);
@@ -401,7 +428,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) k_attn_dq(const __grid_constan
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = 0.f;
       }
-      if (valid) store32(a.dq + row * HD + 64 * g0 + 32 * h, v, 1.f);
+      if (valid) store32(a.dq + row * HD + 64 * g0 + 32 * h, v, a.scale);
       __syncwarp();
     }
     tc::fence_before();

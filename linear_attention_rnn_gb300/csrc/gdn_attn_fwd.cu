@@ -47,9 +47,10 @@ struct FwdSmem {
 __global__ void __launch_bounds__(FWD_THREADS, 1) k_attn_fwd(const __grid_constant__ AttnArgs a) {
   extern __shared__ unsigned char raw[];
   FwdSmem& sm = *reinterpret_cast<FwdSmem*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tc::warp_index();
   pdl_wait();
   pdl_release();
+  if (blockIdx.y == 0) clear_status(a.status);
   const int G = a.Hq / a.Hk, TT = CH / G;  // tokens to a tile
   // a sequence's last tiles, which see the most keys, start first
   const int kh = blockIdx.x % a.Hk, split = blockIdx.y;
@@ -108,20 +109,21 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) k_attn_fwd(const __grid_consta
         for (int k = 0; k < NSLOT; ++k) tc::mbar_wait_sleep(&sm.full[k], 0, 4000000LL);
     }
   } else if (warp == 8) {
-    if (lane == 0 && nmax > 0) {
+    const uint32_t lead = tc::elect_leader();
+    if (nmax > 0) {
       auto slot = [&](int t) { return smem_u32(sm.slot[t % NSLOT]); };
-      auto arrived = [&](int t) { w.on(&sm.full[t % NSLOT], t / NSLOT); };
+      auto arrived = [&](int t) { w.warp_on(&sm.full[t % NSLOT], t / NSLOT); };
       auto release = [&](int t) {
-        if (t + NSLOT < nt) tc::commit(&sm.empty[t % NSLOT]);
+        if (t + NSLOT < nt) tc::commit_by(lead, &sm.empty[t % NSLOT]);
       };
       auto scores = [&](int x, int i) {  // S of tile x = Q K^T
-        tc::gemm128(tS + 128 * x, smem_u32(sm.q[x]), false, slot(2 * i), false, false);
-        tc::commit(&sm.barS[x]);
+        tc::gemm128_by<false, false>(lead, tS + 128 * x, smem_u32(sm.q[x]), slot(2 * i), false);
+        tc::commit_by(lead, &sm.barS[x]);
       };
       arrived(0);
       for (int x = 0; x < 2; ++x)
         if (n[x] > 0) {
-          w.on(&sm.barQ[x], 0);
+          w.warp_on(&sm.barQ[x], 0);
           scores(x, 0);
         }
       release(0);
@@ -131,10 +133,10 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) k_attn_fwd(const __grid_consta
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           if (i < n[x]) {
-            w.on(&sm.barP[x], i);
+            w.warp_on(&sm.barP[x], i);
             tc::fence_after();
-            tc::gemm_ts_bmn(tO + 128 * x, tS + 128 * x, slot(2 * i + 1), i > 0);
-            if (i + 1 == n[x]) tc::commit(&sm.barO[x]);
+            tc::gemm_ts_by<false>(lead, tO + 128 * x, tS + 128 * x, slot(2 * i + 1), i > 0);
+            if (i + 1 == n[x]) tc::commit_by(lead, &sm.barO[x]);
           }
           if (x == 1) release(2 * i + 1);
           if (i + 1 < n[x]) scores(x, i + 1);

@@ -17,15 +17,15 @@
 //   backwards: M_ij = e^{w (j - i)}, j >= i;  f_i = e^{w (n - 1 - i)};  e_j = e^{w (j + 1)}
 // (every exponent that is used is <= 0, so nothing overflows for any w <= 0).
 //
-// k_decay, one CTA per (pass, sequence, head, segment): five tcgen05 products of
-// 128^3 per chunk, accumulators in tensor memory (P = A B^T, O1 = A X, O2 = P C,
+// k_decay, one CTA per (pass, sequence, head, segment): five (six) tcgen05 products
+// of 128^3 per chunk, accumulators in tensor memory (P = A B^T, O1 = A X, O2 = P C,
 // X: 4 x 128 columns).  X stays in tensor memory in fp32 for the whole segment;
 // it is scaled there and rounded to bf16 only as the operand of A X.  B^T diag(e)
 // C has to keep the state's fp32: the rows of B are scaled in fp32 and split
-// into two bf16 terms (hi in place, lo beside it), two products.  The masked P
-// goes back to tensor memory as a bf16 A operand.  Warps 0-3 mask P, 4-7 carry
-// the state, 8-11 write the output, 12-15 scale B; one thread issues the
-// products, one the TMA loads (a ring of five 32 KiB tiles, three to a chunk).
+// into bf16 terms (the first in place, one or two beside it), a product each.  The masked P
+// goes back to tensor memory as a bf16 A operand.  Warps 0-7 mask P and
+// write the output, 8-15 carry the state and scale B; one thread issues the
+// products, one the TMA loads (a ring of five or four 32 KiB tiles, three to a chunk).
 //
 // With few sequences and heads the SMs are filled by segments: k_decay_fold
 // forms each segment's own X (rows weighted to the segment's end, so that its
@@ -42,9 +42,9 @@ namespace gdn {
 namespace {
 
 constexpr uint32_t TILE = CH * HD * 2;  // a [128 x 128] bf16 tile
-constexpr int NSLOT = 5;
-constexpr int WALK_THREADS = 16 * 32 + 64;
-constexpr int FOLD_SLOTS = 6;
+constexpr int WALK_THREADS = 16 * 32 + 96;
+constexpr int FOLD_SLOTS = 5;
+constexpr int FOLD_TERMS = 3;
 constexpr int FOLD_THREADS = 256 + 64;
 
 struct Range {
@@ -88,23 +88,43 @@ __device__ __forceinline__ int2 find_segment(const int* cu, int n_seqs, int T, i
   return found;
 }
 
-// Rows of an SW128 tile scaled by f (rows at or past n: zero), split into hi
-// (in place) and lo; this thread's row r, 16-byte chunks j0 .. j0 + nj - 1.
-__device__ __forceinline__ void scale_row(unsigned char* tile, unsigned char* lo, int r, int j0, int nj, float f,
-                                          bool valid) {
-  for (int j = j0; j < j0 + nj; ++j) {
-    const uint32_t off = tc::sw128_chunk(r, j, CH);
-    uint4 u = *reinterpret_cast<const uint4*>(tile + off), h, l;
-    uint32_t* up = reinterpret_cast<uint32_t*>(&u);
-    uint32_t* hp = reinterpret_cast<uint32_t*>(&h);
-    uint32_t* lp = reinterpret_cast<uint32_t*>(&l);
+// Rows of an SW128 tile scaled by f and split into TERMS bf16 terms, the first in
+// place, the others in the tiles at `rest`; this thread's row r, 16-byte chunks
+// j0 .. j0 + NJ - 1.  The leading terms are the value's upper 16 bits as they
+// stand (the remainder is then exact), the last one is rounded: 8 bits more of
+// the fp32 product per term, at a permute, two ands and a subtraction per pair.
+// A row that is not `valid` (past the sequence's end) becomes zero, whatever it
+// holds.
+template <int TERMS, int NJ>
+__device__ __forceinline__ void scale_row(unsigned char* tile, unsigned char* rest, int r, int j0, float f, bool valid) {
+  const uint32_t keep = valid ? 0xffffffffu : 0u;
+#pragma unroll 1
+  for (int j = j0; j < j0 + NJ; j += 4) {
+    uint4 u[4];  // four loads in flight
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 x = unpack_bf16(up[i]);
-      split_bf16(valid ? f * x.x : 0.f, valid ? f * x.y : 0.f, hp[i], lp[i]);
+    for (int c = 0; c < 4; ++c) u[c] = *reinterpret_cast<const uint4*>(tile + tc::sw128_chunk(r, j + c, CH));
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint32_t off = tc::sw128_chunk(r, j + c, CH);
+      const uint32_t up[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
+      uint32_t o[TERMS][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t w = up[i] & keep;
+        float x = f * __uint_as_float(w << 16), y = f * __uint_as_float(w & 0xffff0000u);
+#pragma unroll
+        for (int t = 0; t < TERMS - 1; ++t) {
+          o[t][i] = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+          x -= __uint_as_float(__float_as_uint(x) & 0xffff0000u);
+          y -= __uint_as_float(__float_as_uint(y) & 0xffff0000u);
+        }
+        o[TERMS - 1][i] = pack_bf16(x, y);
+      }
+#pragma unroll
+      for (int t = 0; t < TERMS; ++t)
+        *reinterpret_cast<uint4*>((t == 0 ? tile : rest + (t - 1) * TILE) + off) =
+            make_uint4(o[t][0], o[t][1], o[t][2], o[t][3]);
     }
-    *reinterpret_cast<uint4*>(tile + off) = h;
-    *reinterpret_cast<uint4*>(lo + off) = l;
   }
 }
 __device__ __forceinline__ void zero_row(unsigned char* tile, int r, int j0, int nj) {
@@ -119,50 +139,30 @@ __device__ __forceinline__ void load_tile(unsigned char* dst, const CUtensorMap*
 }
 
 // ---- the chunk walk ----------------------------------------------------------------
+// TERMS: bf16 terms of the scaled B rows.  Two leave an error of some 1e-5 in the
+// state, far below the rounding of the output's operands; a final state that is
+// returned in fp32 takes three, at a ring slot's cost.
+template <int TERMS>
 struct WalkSmem {
+  static constexpr int NSLOT = 7 - TERMS;
   unsigned char slot[NSLOT][TILE];
-  unsigned char lo[TILE];   // second term of the scaled B rows
-  unsigned char X[TILE];    // the entering state in bf16, [128 (b) rows x 128 (c)]
-  float tab[CH];            // e^{w d}
+  unsigned char rest[TERMS - 1][TILE];  // further terms of the scaled B rows
+  unsigned char X[TILE];                // the entering state in bf16, [128 (b) rows x 128 (c)]
+  alignas(16) float tab[CH];            // e^{w d}
   uint64_t full[NSLOT], empty[NSLOT];
-  uint64_t barP, barPm, barK, barS, barX, barO, barOf;
+  uint64_t barP, barPm, barK, barS, barX, barO, barOf, barSt;
   uint32_t tmem;
 };
 
-__global__ void __launch_bounds__(WALK_THREADS, 1) k_decay(const __grid_constant__ DecayArgs a) {
-  extern __shared__ unsigned char raw[];
-  WalkSmem& sm = *reinterpret_cast<WalkSmem*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int G = a.Hv / a.Hk;
-  pdl_wait();
-  pdl_release();
-
-  // pass, then segment, sequence and head of this CTA
-  int u = blockIdx.x, ri = 0;
-  for (; ri < a.n_roles - 1; ++ri) {
-    const int units = a.slots * (a.role[ri].shared ? a.Hk : a.Hv);
-    if (u < units) break;
-    u -= units;
-  }
-  const DecayRole& R = a.role[ri];
-  const int heads = R.shared ? a.Hk : a.Hv, loops = R.shared ? G : 1;
-  const int hd = u % heads, slot = u / heads;
-  const int2 at = find_segment(a.cu, a.n_seqs, a.T, a.total, a.seg_chunks, a.nseg, slot);
-  const int s = at.x, seg = at.y;
-  if (s < 0) return;
-  const Range q = seq_range(a.cu, s, a.T, a.total);
-  const int nch = (q.len + CH - 1) / CH;
-  const int cb = seg * a.seg_chunks, ce = a.nseg == 1 ? nch : min(nch, cb + a.seg_chunks), nc = ce - cb;
-  const bool rev = R.rev;
-  if (nc <= 0) {  // an empty sequence ends in the state that it began with
-    if (seg == 0 && R.xT) {
-      const long o = ((long)s * a.Hv + hd) * HD * HD;
-      for (int i = tid; i < HD * HD; i += WALK_THREADS) R.xT[o + i] = R.x0 ? R.x0[o + i] : 0.f;
-    }
-    return;
-  }
+// One CTA's walk over the chunks [cb, ce) of head hd in sequence s (rows q); REV: backwards.
+template <int TERMS, bool REV>
+__device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, WalkSmem<TERMS>& sm, const Range q, int s,
+                                     int slot_id, int hd, int cb, int ce, int nch) {
+  constexpr int NSLOT = WalkSmem<TERMS>::NSLOT;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tc::warp_index();
+  const int G = a.Hv / a.Hk, loops = R.shared ? G : 1, nc = ce - cb;
   const int n_it = loops * nc;
-  auto chunk_of = [&](int it) { return rev ? ce - 1 - it % nc : cb + it % nc; };
+  auto chunk_of = [&](int it) { return REV ? ce - 1 - it % nc : cb + it % nc; };
   auto head_of = [&](int it) { return R.shared ? hd * G + it / nc : hd; };  // value head
   auto rows_of = [&](int c) { return min(CH, q.len - c * CH); };
 
@@ -174,10 +174,11 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_decay(const __grid_constant
     tc::mbar_init(&sm.barP, 1);
     tc::mbar_init(&sm.barX, 1);
     tc::mbar_init(&sm.barO, 1);
-    tc::mbar_init(&sm.barPm, 128);
-    tc::mbar_init(&sm.barK, 128);
-    tc::mbar_init(&sm.barS, 128);
-    tc::mbar_init(&sm.barOf, 128);
+    tc::mbar_init(&sm.barPm, 256);
+    tc::mbar_init(&sm.barK, 256);
+    tc::mbar_init(&sm.barS, 256);
+    tc::mbar_init(&sm.barOf, 256);
+    tc::mbar_init(&sm.barSt, 256);
     tc::mbar_fence_init();
   }
   if (warp == 0) tc::alloc(&sm.tmem, 512);
@@ -187,7 +188,28 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_decay(const __grid_constant
   const uint32_t tP = sm.tmem, tO1 = tP + 128, tO2 = tP + 256, tX = tP + 384;
   tc::Wait w;
 
-  if (warp == 17) {  // ---- TMA: tiles b, a, c of every chunk, in the order consumed
+  // whether chunk `it`'s output rows are stored as a tile: a whole chunk of the last head summed
+  auto whole = [&](int it) { return it >= n_it - nc && rows_of(chunk_of(it)) == CH; };
+
+  if (warp == 18) {  // ---- output tiles: staged in the slot of the chunk's C, which O has consumed
+    if (lane == 0) {
+      for (int it = 0; it < n_it && w.ok; ++it) {
+        const int t = 3 * it + 2;
+        w.on(&sm.barSt, it);
+        if (!w.ok) break;
+        if (whole(it)) {
+          const unsigned char* tile = sm.slot[t % NSLOT];
+          const int row = q.start + chunk_of(it) * CH;
+          tc::tma_store_3d(&R.o, 0, hd, row, tile);
+          tc::tma_store_3d(&R.o, 64, hd, row, tile + TILE / 2);
+          tc::bulk_commit();
+          tc::bulk_wait_read();
+        }
+        if (t + NSLOT < 3 * n_it) tc::mbar_arrive(&sm.empty[t % NSLOT]);
+      }
+      tc::bulk_wait();
+    }
+  } else if (warp == 17) {  // ---- TMA: tiles a, b, c of every chunk, in the order consumed
     if (lane == 0) {
       const int nt = 3 * n_it;
       for (int t = 0; t < nt && w.ok; ++t) {
@@ -195,8 +217,8 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_decay(const __grid_constant
         if (t >= NSLOT) w.on(&sm.empty[k], (t / NSLOT - 1));
         if (!w.ok) break;
         const int j = head_of(it), jk = j / G;
-        const CUtensorMap* m = kind == 0 ? &R.b : kind == 1 ? &R.a : &R.c;
-        const int per_v = kind == 0 ? R.hb : kind == 1 ? R.ha : R.hc;
+        const CUtensorMap* m = kind == 0 ? &R.a : kind == 1 ? &R.b : &R.c;
+        const int per_v = kind == 0 ? R.ha : kind == 1 ? R.hb : R.hc;
         load_tile(sm.slot[k], m, per_v ? j : jk, row, &sm.full[k]);
       }
       // no copy is in flight when the CTA ends
@@ -206,153 +228,69 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_decay(const __grid_constant
         for (int k = 0; k < NSLOT; ++k) tc::mbar_wait_sleep(&sm.full[k], 0, 4000000LL);
     }
   } else if (warp == 16) {  // ---- products
-    if (lane == 0) {
-      const int nt = 3 * n_it;
-      auto slot = [&](int t) { return smem_u32(sm.slot[t % NSLOT]); };
-      auto arrived = [&](int t) { w.on(&sm.full[t % NSLOT], t / NSLOT); };
-      auto release = [&](int t) {
-        if (t + NSLOT < nt) tc::commit(&sm.empty[t % NSLOT]);
-      };
-      auto scores = [&](int it) {  // P = A B^T
-        arrived(3 * it);
-        arrived(3 * it + 1);
-        tc::gemm128(tP, slot(3 * it + 1), false, slot(3 * it), false, false);
-        tc::commit(&sm.barP);
-      };
-      scores(0);
-      for (int it = 0; it < n_it; ++it) {
-        const int tb = 3 * it, ta = tb + 1, tcc = tb + 2;
-        w.on(&sm.barS, it);
-        if (it > 0) w.on(&sm.barOf, it - 1);
-        tc::fence_after();
-        tc::gemm128(tO1, slot(ta), false, smem_u32(sm.X), true, false);  // A X
-        release(ta);
-        w.on(&sm.barK, it);
-        arrived(tcc);
-        tc::fence_after();
-        tc::gemm128(tX, slot(tb), true, slot(tcc), true, true);          // X += B'^T C
-        tc::gemm128(tX, smem_u32(sm.lo), true, slot(tcc), true, true);
-        tc::commit(&sm.barX);
-        release(tb);
-        w.on(&sm.barPm, it);
-        tc::fence_after();
-        tc::gemm_ts_bmn(tO2, tP, slot(tcc), false);                      // P C
-        release(tcc);
-        tc::commit(&sm.barO);
-        if (it + 1 < n_it) scores(it + 1);
-      }
+    const uint32_t lead = tc::elect_leader();
+    const int nt = 3 * n_it;
+    auto slot = [&](int t) { return smem_u32(sm.slot[t % NSLOT]); };
+    auto arrived = [&](int t) { w.warp_on(&sm.full[t % NSLOT], t / NSLOT); };
+    auto release = [&](int t) {
+      if (t + NSLOT < nt) tc::commit_by(lead, &sm.empty[t % NSLOT]);
+    };
+    auto scores = [&](int it) {  // P = A B^T
+      arrived(3 * it);
+      arrived(3 * it + 1);
+      tc::gemm128_by<false, false>(lead, tP, slot(3 * it), slot(3 * it + 1), false);
+      tc::commit_by(lead, &sm.barP);
+    };
+    scores(0);
+    for (int it = 0; it < n_it; ++it) {
+      const int ta = 3 * it, tb = ta + 1, tcc = ta + 2;
+      w.warp_on(&sm.barS, it);
+      if (it > 0) w.warp_on(&sm.barOf, it - 1);
+      tc::fence_after();
+      tc::gemm128_by<false, true>(lead, tO1, slot(ta), smem_u32(sm.X), false);  // A X
+      release(ta);
+      w.warp_on(&sm.barK, it);
+      arrived(tcc);
+      tc::fence_after();
+      tc::gemm128_by<true, true>(lead, tX, slot(tb), slot(tcc), true);  // X += B'^T C
+#pragma unroll
+      for (int t = 0; t < TERMS - 1; ++t) tc::gemm128_by<true, true>(lead, tX, smem_u32(sm.rest[t]), slot(tcc), true);
+      tc::commit_by(lead, &sm.barX);
+      release(tb);
+      w.warp_on(&sm.barPm, it);
+      tc::fence_after();
+      tc::gemm_ts_by<true>(lead, tO2, tP, slot(tcc), false);  // P C
+      tc::commit_by(lead, &sm.barO);
+      if (it + 1 < n_it) scores(it + 1);
     }
   } else {
-    const int grp = warp >> 2, r = 32 * (warp & 3) + lane;   // TMEM lane = row r
-    const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
-    if (grp == 0) {  // ---- mask and decay of the scores
-      for (int it = 0; it < n_it; ++it) {
-        if (it % nc == 0) {  // a new head: its table of decays
-          asm volatile("bar.sync 1, 128;" ::: "memory");
-          sm.tab[r] = expf(a.decay[head_of(it)] * (float)r);
-          asm volatile("bar.sync 1, 128;" ::: "memory");
-        }
-        const int n = rows_of(chunk_of(it));
-        w.warp_on(&sm.barP, it);
-        tc::fence_after();
-#pragma unroll 1
-        for (int g = 0; g < 4; ++g) {
-          float v[32];
-          tc::ld32(tP + lane_base + 32 * g, v);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int j = 32 * g + i, d = rev ? j - r : r - j;
-            v[i] = (d >= 0 && j < n) ? v[i] * sm.tab[d & (CH - 1)] : 0.f;
-          }
-          tc::st16_bf16(tP + lane_base + 16 * g, v);  // (columns already read)
-        }
-        tc::wait_st();
-        tc::fence_before();
-        tc::mbar_arrive(&sm.barPm);
-      }
-    } else if (grp == 1) {  // ---- the state: bf16 image of X, X <- e^{w n} X
-      for (int it = 0; it < n_it; ++it) {
-        const int j = head_of(it);
-        const float keep = expf(a.decay[j] * (float)rows_of(chunk_of(it)));
-        if (it > 0) {
-          w.warp_on(&sm.barX, it - 1);
-          tc::fence_after();
-        }
-        const bool first = it % nc == 0;
-        const long sh = (long)s * a.Hv + j;
-        const float* x0 = R.xseg ? R.xseg + ((long)slot * a.Hv + j) * HD * HD
-                                 : (R.x0 ? R.x0 + sh * HD * HD : nullptr);
-#pragma unroll 1
-        for (int g = 0; g < 4; ++g) {
-          float v[32];
-          if (!first) {
-            tc::ld32(tX + lane_base + 32 * g, v);
-          } else if (!x0) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0.f;
-          } else if (R.xt) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = x0[(32 * g + i) * HD + r];
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float4 f = *reinterpret_cast<const float4*>(x0 + r * HD + 32 * g + 4 * i);
-              v[4 * i] = f.x;
-              v[4 * i + 1] = f.y;
-              v[4 * i + 2] = f.z;
-              v[4 * i + 3] = f.w;
-            }
-          }
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint4 o;
-            o.x = pack_bf16(v[8 * c], v[8 * c + 1]);
-            o.y = pack_bf16(v[8 * c + 2], v[8 * c + 3]);
-            o.z = pack_bf16(v[8 * c + 4], v[8 * c + 5]);
-            o.w = pack_bf16(v[8 * c + 6], v[8 * c + 7]);
-            *reinterpret_cast<uint4*>(sm.X + tc::sw128_chunk(r, 4 * g + c, CH)) = o;
-          }
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] *= keep;
-          tc::st32(tX + lane_base + 32 * g, v);
-        }
-        tc::wait_st();
-        tc::fence_before();
-        tc::fence_proxy_async();
-        tc::mbar_arrive(&sm.barS);
-      }
-      if (R.xT) {  // (one segment: with more, the prefix has written the final state)
-        w.warp_on(&sm.barX, n_it - 1);
-        tc::fence_after();
-        float* dst = R.xT + ((long)s * a.Hv + hd) * HD * HD + r * HD;
-#pragma unroll 1
-        for (int g = 0; g < 4; ++g) {
-          float v[32];
-          tc::ld32(tX + lane_base + 32 * g, v);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<float4*>(dst + 32 * g + 4 * i) =
-                make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-        }
-        tc::fence_before();
-      }
-    } else if (grp == 2) {  // ---- output rows
-      const int Ho = R.shared ? a.Hk : a.Hv;
-      for (int it = 0; it < n_it; ++it) {
+    // Eight warps for the scores and the output, eight for the state and the scaled
+    // rows: thread (r, half) has row r = TMEM lane r and 64 of its 128 columns.
+    const int half = (warp >> 2) & 1, r = 32 * (warp & 3) + lane;
+    const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16, cols = lane_base + 64 * half;
+    float wd = 0.f;
+    if (warp < 8) {
+      const int own = warp & 3, Ho = R.shared ? a.Hk : a.Hv;
+      // O of chunk `it`, whose products have been issued
+      auto output = [&](int it) {
         const int c = chunk_of(it), n = rows_of(c);
-        const float f = expf(a.decay[head_of(it)] * (float)(rev ? max(n - 1 - r, 0) : r + 1));
+        const float f = expf(wd * (float)(REV ? max(n - 1 - r, 0) : r + 1));
         const bool sum = loops > 1, firsth = it < nc, lasth = it >= n_it - nc;
         const long row = (long)q.start + (long)c * CH + r;
-        bf16* dst = R.out + (row * Ho + hd) * HD;
+        bf16* dst = R.out + (row * Ho + hd) * HD + 64 * half;
         // running sums over the value heads, [head][4-column group][row]: this thread's own
-        float4* acc = sum ? reinterpret_cast<float4*>(R.acc) + (long)hd * 32 * a.total + row : nullptr;
+        float4* acc = sum ? reinterpret_cast<float4*>(R.acc) + ((long)hd * 32 + 16 * half) * a.total + row : nullptr;
         w.warp_on(&sm.barO, it);
         tc::fence_after();
 #pragma unroll 1
-        for (int g = 0; g < 4; ++g) {
+        for (int g = 0; g < 2; ++g) {
           float x[32], y[32];
-          tc::ld32(tO1 + lane_base + 32 * g, x);
-          tc::ld32(tO2 + lane_base + 32 * g, y);
+          tc::ld32(tO1 + cols + 32 * g, x);
+          tc::ld32(tO2 + cols + 32 * g, y);
+          if (g == 1) {
+            tc::fence_before();
+            tc::mbar_arrive(&sm.barOf);
+          }
 #pragma unroll
           for (int i = 0; i < 32; ++i) x[i] = f * x[i] + y[i];
           if (sum && !firsth && r < n) {
@@ -365,7 +303,18 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_decay(const __grid_constant
               x[4 * i + 3] += p.w;
             }
           }
-          if (r >= n) {
+          if (whole(it)) {
+            unsigned char* tile = sm.slot[(3 * it + 2) % NSLOT];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint4 o;
+              o.x = pack_bf16(x[8 * i], x[8 * i + 1]);
+              o.y = pack_bf16(x[8 * i + 2], x[8 * i + 3]);
+              o.z = pack_bf16(x[8 * i + 4], x[8 * i + 5]);
+              o.w = pack_bf16(x[8 * i + 6], x[8 * i + 7]);
+              *reinterpret_cast<uint4*>(tile + tc::sw128_chunk(r, 8 * half + 4 * g + i, CH)) = o;
+            }
+          } else if (r >= n) {
           } else if (sum && !lasth) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -383,24 +332,147 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_decay(const __grid_constant
           }
           __syncwarp();
         }
+        tc::fence_proxy_async();
+        tc::mbar_arrive(&sm.barSt);
+      };
+      for (int it = 0; it < n_it; ++it) {
+        if (it > 0) output(it - 1);
+        if (it % nc == 0) {  // a new head: its table of decays
+          wd = a.decay[head_of(it)];
+          asm volatile("bar.sync 1, 256;" ::: "memory");
+          if (half == 0) sm.tab[r] = expf(wd * (float)r);
+          asm volatile("bar.sync 1, 256;" ::: "memory");
+        }
+        const int n = rows_of(chunk_of(it));
+        w.warp_on(&sm.barP, it);
+        tc::fence_after();
+        // Of the four 32 x 32 blocks of a warp's rows, those on the far side of the
+        // diagonal are zero, those on the near side have the factor
+        // e^{w |i - j|} = (to the block's edge) * (from the edge), both <= 1.
+#pragma unroll 1
+        for (int h = 4 * half; h < 4 * half + 4; ++h) {  // 16 columns at a time
+          const int g = h >> 1, j0 = 16 * h;
+          float v[16];
+          if (REV ? g < own : g > own) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = 0.f;
+          } else {
+            tc::ld16(tP + lane_base + j0, v);
+            if (g == own) {
+              const int d0 = REV ? j0 - r : r - j0;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const int d = REV ? d0 + i : d0 - i;
+                v[i] = d >= 0 ? v[i] * sm.tab[d & 31] : 0.f;
+              }
+            } else {
+              const float edge = sm.tab[REV ? 32 * g - r : r - 32 * g - 31];
+              const float* t = sm.tab + (REV ? j0 & 16 : 16 - (j0 & 16));
+#pragma unroll
+              for (int i = 0; i < 16; i += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(t + (REV ? i : 12 - i));
+                v[i] *= edge * (REV ? f.x : f.w);
+                v[i + 1] *= edge * (REV ? f.y : f.z);
+                v[i + 2] *= edge * (REV ? f.z : f.y);
+                v[i + 3] *= edge * (REV ? f.w : f.x);
+              }
+            }
+            if (REV && j0 + 16 > n) {  // (forwards, rows of tokens see tokens only)
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] = j0 + i < n ? v[i] : 0.f;
+            }
+          }
+          tc::st8_bf16(tP + cols + 8 * (h & 3), v);  // (columns of this half that were read already)
+        }
+        tc::wait_st();
         tc::fence_before();
-        tc::mbar_arrive(&sm.barOf);
+        tc::mbar_arrive(&sm.barPm);
       }
-    } else {  // ---- B' = diag(e) B in two bf16 terms; rows past the sequence's end are cleared
+      output(n_it - 1);
+    } else {
+      const float* x0 = nullptr;
+      float keep = 1.f;
       for (int it = 0; it < n_it; ++it) {
         const int n = rows_of(chunk_of(it));
-        const float wd = a.decay[head_of(it)];
-        const int tb = 3 * it, tcc = tb + 2;
+        const bool first = it % nc == 0;
+        if (first) {
+          const int j = head_of(it);
+          const long sh = (long)s * a.Hv + j;
+          wd = a.decay[j];
+          x0 = R.xseg ? R.xseg + ((long)slot_id * a.Hv + j) * HD * HD : (R.x0 ? R.x0 + sh * HD * HD : nullptr);
+        }
+        keep = expf(wd * (float)n);
+        // ---- the state: bf16 image of X, X <- e^{w n} X
+        if (it > 0) {
+          w.warp_on(&sm.barX, it - 1);
+          tc::fence_after();
+        }
+#pragma unroll 1
+        for (int g = 0; g < 2; ++g) {
+          const int c0 = 64 * half + 32 * g;
+          float v[32];
+          if (!first) {
+            tc::ld32(tX + cols + 32 * g, v);
+          } else if (!x0) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0.f;
+          } else if (R.xt) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = x0[(c0 + i) * HD + r];
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 f = *reinterpret_cast<const float4*>(x0 + r * HD + c0 + 4 * i);
+              v[4 * i] = f.x;
+              v[4 * i + 1] = f.y;
+              v[4 * i + 2] = f.z;
+              v[4 * i + 3] = f.w;
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint4 o;
+            o.x = pack_bf16(v[8 * c], v[8 * c + 1]);
+            o.y = pack_bf16(v[8 * c + 2], v[8 * c + 3]);
+            o.z = pack_bf16(v[8 * c + 4], v[8 * c + 5]);
+            o.w = pack_bf16(v[8 * c + 6], v[8 * c + 7]);
+            *reinterpret_cast<uint4*>(sm.X + tc::sw128_chunk(r, 8 * half + 4 * g + c, CH)) = o;
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] *= keep;
+          tc::st32(tX + cols + 32 * g, v);
+        }
+        tc::wait_st();
+        tc::fence_before();
+        tc::fence_proxy_async();
+        tc::mbar_arrive(&sm.barS);
+        // ---- B' = diag(e) B in bf16 terms; rows past the sequence's end are cleared
+        const int tb = 3 * it + 1, tcc = tb + 1;
+        const float e = expf(wd * (float)(REV ? r + 1 : max(n - 1 - r, 0)));
         w.warp_on(&sm.full[tb % NSLOT], tb / NSLOT);
         w.warp_on(&sm.barP, it);  // (A B^T, which reads the raw tile, has completed)
-        const float e = expf(wd * (float)(rev ? r + 1 : max(n - 1 - r, 0)));
-        scale_row(sm.slot[tb % NSLOT], sm.lo, r, 0, 16, e, r < n);
+        scale_row<TERMS, 8>(sm.slot[tb % NSLOT], sm.rest[0], r, 8 * half, e, r < n);
         if (n < CH) {
           w.warp_on(&sm.full[tcc % NSLOT], tcc / NSLOT);
-          if (r >= n) zero_row(sm.slot[tcc % NSLOT], r, 0, 16);
+          if (r >= n) zero_row(sm.slot[tcc % NSLOT], r, 8 * half, 8);
         }
         tc::fence_proxy_async();
         tc::mbar_arrive(&sm.barK);
+      }
+      if (R.xT) {  // (one segment: with more, the prefix has written the final state)
+        w.warp_on(&sm.barX, n_it - 1);
+        tc::fence_after();
+        float* dst = R.xT + ((long)s * a.Hv + hd) * HD * HD + r * HD + 64 * half;
+#pragma unroll 1
+        for (int g = 0; g < 2; ++g) {
+          float v[32];
+          tc::ld32(tX + cols + 32 * g, v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<float4*>(dst + 32 * g + 4 * i) =
+                make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        }
+        tc::fence_before();
       }
     }
   }
@@ -411,10 +483,48 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_decay(const __grid_constant
   if (warp == 0) tc::dealloc(sm.tmem, 512);
 }
 
+template <int TERMS>
+__global__ void __launch_bounds__(WALK_THREADS, 1) k_decay(const __grid_constant__ DecayArgs a) {
+  extern __shared__ unsigned char raw[];
+  WalkSmem<TERMS>& sm = *reinterpret_cast<WalkSmem<TERMS>*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
+  const int tid = threadIdx.x;
+  pdl_wait();
+  pdl_release();
+  if (a.nseg == 1) clear_status(a.status);
+
+  // pass, then segment, sequence and head of this CTA
+  int u = blockIdx.x, ri = 0;
+  for (; ri < a.n_roles - 1; ++ri) {
+    const int units = a.slots * (a.role[ri].shared ? a.Hk : a.Hv);
+    if (u < units) break;
+    u -= units;
+  }
+  const DecayRole& R = a.role[ri];
+  const int heads = R.shared ? a.Hk : a.Hv;
+  const int hd = u % heads, slot = u / heads;
+  const int2 at = find_segment(a.cu, a.n_seqs, a.T, a.total, a.seg_chunks, a.nseg, slot);
+  const int s = at.x, seg = at.y;
+  if (s < 0) return;
+  const Range q = seq_range(a.cu, s, a.T, a.total);
+  const int nch = (q.len + CH - 1) / CH;
+  const int cb = seg * a.seg_chunks, ce = a.nseg == 1 ? nch : min(nch, cb + a.seg_chunks), nc = ce - cb;
+  if (nc <= 0) {  // an empty sequence ends in the state that it began with
+    if (seg == 0 && R.xT) {
+      const long o = ((long)s * a.Hv + hd) * HD * HD;
+      for (int i = tid; i < HD * HD; i += WALK_THREADS) R.xT[o + i] = R.x0 ? R.x0[o + i] : 0.f;
+    }
+    return;
+  }
+  if (R.rev)
+    walk<TERMS, true>(a, R, sm, q, s, slot, hd, cb, ce, nch);
+  else
+    walk<TERMS, false>(a, R, sm, q, s, slot, hd, cb, ce, nch);
+}
+
 // ---- segments ----------------------------------------------------------------------
 struct FoldSmem {
   unsigned char slot[FOLD_SLOTS][TILE];
-  unsigned char lo[TILE];
+  unsigned char rest[FOLD_TERMS - 1][TILE];  // further terms of the scaled B rows
   uint64_t full[FOLD_SLOTS], empty[FOLD_SLOTS];
   uint64_t barK, barM;
   uint32_t tmem;
@@ -423,10 +533,11 @@ struct FoldSmem {
 __global__ void __launch_bounds__(FOLD_THREADS, 1) k_decay_fold(const __grid_constant__ DecayFoldArgs a) {
   extern __shared__ unsigned char raw[];
   FoldSmem& sm = *reinterpret_cast<FoldSmem*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tc::warp_index();
   const int G = a.Hv / a.Hk;
   pdl_wait();
   pdl_release();
+  if (blockIdx.y == 0) clear_status(a.status);
   const int j = blockIdx.x % a.Hv, slot = blockIdx.x / a.Hv;
   const int2 at = find_segment(a.cu, a.n_seqs, a.T, a.total, a.seg_chunks, a.nseg, slot);
   const int s = at.x, seg = at.y;
@@ -470,19 +581,19 @@ __global__ void __launch_bounds__(FOLD_THREADS, 1) k_decay_fold(const __grid_con
         for (int k = 0; k < FOLD_SLOTS; ++k) tc::mbar_wait_sleep(&sm.full[k], 0, 4000000LL);
     }
   } else if (warp == 8) {
-    if (lane == 0) {
-      for (int i = 0; i < nc; ++i) {
-        const int tb = 2 * i, tcc = tb + 1;
-        w.on(&sm.barK, i);
-        w.on(&sm.full[tcc % FOLD_SLOTS], tcc / FOLD_SLOTS);
-        tc::fence_after();
-        const uint32_t c = smem_u32(sm.slot[tcc % FOLD_SLOTS]);
-        tc::gemm128(tX, smem_u32(sm.slot[tb % FOLD_SLOTS]), true, c, true, i > 0);
-        tc::gemm128(tX, smem_u32(sm.lo), true, c, true, true);
-        if (tb + FOLD_SLOTS < 2 * nc) tc::commit(&sm.empty[tb % FOLD_SLOTS]);
-        if (tcc + FOLD_SLOTS < 2 * nc) tc::commit(&sm.empty[tcc % FOLD_SLOTS]);
-        tc::commit(&sm.barM);
-      }
+    const uint32_t lead = tc::elect_leader();
+    for (int i = 0; i < nc; ++i) {
+      const int tb = 2 * i, tcc = tb + 1;
+      w.warp_on(&sm.barK, i);
+      w.warp_on(&sm.full[tcc % FOLD_SLOTS], tcc / FOLD_SLOTS);
+      tc::fence_after();
+      const uint32_t c = smem_u32(sm.slot[tcc % FOLD_SLOTS]);
+      tc::gemm128_by<true, true>(lead, tX, smem_u32(sm.slot[tb % FOLD_SLOTS]), c, i > 0);
+#pragma unroll
+      for (int t = 0; t < FOLD_TERMS - 1; ++t) tc::gemm128_by<true, true>(lead, tX, smem_u32(sm.rest[t]), c, true);
+      if (tb + FOLD_SLOTS < 2 * nc) tc::commit_by(lead, &sm.empty[tb % FOLD_SLOTS]);
+      if (tcc + FOLD_SLOTS < 2 * nc) tc::commit_by(lead, &sm.empty[tcc % FOLD_SLOTS]);
+      tc::commit_by(lead, &sm.barM);
     }
   } else {
     const int r = tid & 127, j0 = 8 * (tid >> 7);
@@ -494,7 +605,7 @@ __global__ void __launch_bounds__(FOLD_THREADS, 1) k_decay_fold(const __grid_con
       const float e = expf(wd * (float)(R.rev ? t0 - cb * CH + 1 : max(end - 1 - t0, 0)));
       if (i > 0) w.warp_on(&sm.barM, i - 1);  // (the second term of the chunk before has been read)
       w.warp_on(&sm.full[tb % FOLD_SLOTS], tb / FOLD_SLOTS);
-      scale_row(sm.slot[tb % FOLD_SLOTS], sm.lo, r, j0, 8, e, r < n);
+      scale_row<FOLD_TERMS, 8>(sm.slot[tb % FOLD_SLOTS], sm.rest[0], r, j0, e, r < n);
       if (n < CH) {
         w.warp_on(&sm.full[tcc % FOLD_SLOTS], tcc / FOLD_SLOTS);
         if (r >= n) zero_row(sm.slot[tcc % FOLD_SLOTS], r, j0, 8);
@@ -538,15 +649,26 @@ __global__ void __launch_bounds__(256) k_decay_prefix(const __grid_constant__ De
   const float wd = a.decay[j];
   const int slot0 = first_slot(a.cu, s, a.T, a.total, a.seg_chunks * CH);
   float4 run = R.x0 ? *reinterpret_cast<const float4*>(R.x0 + sh * HD * HD + e) : make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i = 0; i < nseg; ++i) {
-    const int seg = R.rev ? nseg - 1 - i : i;
-    float4* p = reinterpret_cast<float4*>(R.x + ((long)(slot0 + seg) * a.Hv + j) * HD * HD + e);
-    const bool need = R.last || i + 1 < nseg;  // (the last one's own state is not formed otherwise)
-    const float4 x = need ? *p : make_float4(0.f, 0.f, 0.f, 0.f);
-    *p = run;
-    const int len = min(q.len, (seg + 1) * a.seg_chunks * CH) - seg * a.seg_chunks * CH;
-    const float keep = expf(wd * (float)len);
-    run = make_float4(keep * run.x + x.x, keep * run.y + x.y, keep * run.z + x.z, keep * run.w + x.w);
+  constexpr int AHEAD = 4;  // loads in flight
+  for (int i0 = 0; i0 < nseg; i0 += AHEAD) {
+    float4 x[AHEAD];
+    float4* p[AHEAD];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      const int i = i0 + k, seg = R.rev ? nseg - 1 - i : i;
+      p[k] = reinterpret_cast<float4*>(R.x + ((long)(slot0 + seg) * a.Hv + j) * HD * HD + e);
+      x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < nseg && (R.last || i + 1 < nseg)) x[k] = *p[k];  // (the last one's own is not formed otherwise)
+    }
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      const int i = i0 + k, seg = R.rev ? nseg - 1 - i : i;
+      if (i >= nseg) break;
+      *p[k] = run;
+      const int len = min(q.len, (seg + 1) * a.seg_chunks * CH) - seg * a.seg_chunks * CH;
+      const float keep = expf(wd * (float)len);
+      run = make_float4(keep * run.x + x[k].x, keep * run.y + x[k].y, keep * run.z + x[k].z, keep * run.w + x[k].w);
+    }
   }
   if (R.last) *reinterpret_cast<float4*>(R.last + sh * HD * HD + e) = run;
 }
@@ -558,14 +680,21 @@ cudaError_t set_smem(K k, size_t bytes) {
 
 }  // namespace
 
-cudaError_t launch_decay(const DecayArgs& a, cudaStream_t s) {
-  constexpr size_t smem = sizeof(WalkSmem) + 1024;
+template <int TERMS>
+static cudaError_t launch_walk(const DecayArgs& a, cudaStream_t s) {
+  constexpr size_t smem = sizeof(WalkSmem<TERMS>) + 1024;
   static_assert(smem <= 227 * 1024, "shared memory");
-  cudaError_t e = set_smem(k_decay, smem);
+  cudaError_t e = set_smem(k_decay<TERMS>, smem);
   if (e != cudaSuccess) return e;
   long units = 0;
   for (int i = 0; i < a.n_roles; ++i) units += (long)a.slots * (a.role[i].shared ? a.Hk : a.Hv);
-  return launch_pdl(k_decay, dim3((unsigned)units), dim3(WALK_THREADS), smem, s, a);
+  return launch_pdl(k_decay<TERMS>, dim3((unsigned)units), dim3(WALK_THREADS), smem, s, a);
+}
+
+cudaError_t launch_decay(const DecayArgs& a, cudaStream_t s) {
+  bool last = false;
+  for (int i = 0; i < a.n_roles; ++i) last = last || a.role[i].xT;
+  return last ? launch_walk<3>(a, s) : launch_walk<2>(a, s);
 }
 
 cudaError_t launch_decay_fold(const DecayFoldArgs& a, cudaStream_t s) {

@@ -158,7 +158,7 @@ struct StepArgs {
 // Linear attention with a decay for each head (gdn_decay.cu): one pass of the
 // chunk walk over rows a, b, c with entering state X0.
 struct DecayRole {
-  CUtensorMap a, b, c;  // rows [total][H][HD], boxes of 64 columns x 1 head x 128 rows
+  CUtensorMap a, b, c, o;  // rows [total][H][HD], boxes of 64 columns x 1 head x 128 rows
   int ha, hb, hc;       // 1: a head for each value head; 0: shared by a group
   int rev;              // 1: backwards in time
   int xt;               // 1: X0 and the segments' states are stored transposed
@@ -217,6 +217,13 @@ struct AttnArgs {
   int n_seqs, total_q, total_k, Hq, Hk;
   int split_tiles, n_splits;  // key tiles to a split
 };
+
+// The status word of a call, cleared by the first block of its first kernel: that
+// block starts with the first blocks of the call, and a wait gives up only a
+// second after its own block has started.
+__device__ __forceinline__ void clear_status(int* status) {
+  if (status && blockIdx.x == 0 && threadIdx.x == 0) *status = 0;
+}
 
 // Launches kernel k with programmatic stream serialization: its CTAs may start
 // (and run up to their pdl_wait) while the previous kernel in the stream ends.

@@ -274,12 +274,12 @@ int gdn_decay_fwd(const void* q, const void* k, const void* v, const float* deca
   DecayRole& r = a.role[0];
   if (!tmap_rows(&r.a, q, total, Hk, HD, (uint64_t)q_stride * 2, 1, CH) ||
       !tmap_rows(&r.b, k, total, Hk, HD, (uint64_t)k_stride * 2, 1, CH) ||
-      !tmap_rows(&r.c, v, total, Hv, HD, (uint64_t)v_stride * 2, 1, CH))
+      !tmap_rows(&r.c, v, total, Hv, HD, (uint64_t)v_stride * 2, 1, CH) ||
+      !tmap_rows(&r.o, o, total, Hv, HD, (uint64_t)Hv * HD * 2, 1, CH))
     return GDN_ERR_CUDA;
   r.hc = 1;
   r.x0 = h0;
   r.out = static_cast<bf16*>(o);
-  if ((rc = cuda_status(cudaMemsetAsync(a.status, 0, sizeof(int), s)))) return rc;
   if (p.nseg > 1) {
     float* x = at<float>(ws, p.xf);
     DecayFoldArgs f;
@@ -367,7 +367,10 @@ int gdn_decay_bwd(const void* q, const void* k, const void* v, const float* deca
   rv.rev = 1;
   rv.x0 = dhT;
   rv.out = static_cast<bf16*>(dv);
-  if ((rc = cuda_status(cudaMemsetAsync(a.status, 0, sizeof(int), s)))) return rc;
+  if (!tmap_rows(&rq.o, dq, total, Hk, HD, (uint64_t)Hk * HD * 2, 1, CH) ||
+      !tmap_rows(&rk.o, dk, total, Hk, HD, (uint64_t)Hk * HD * 2, 1, CH) ||
+      !tmap_rows(&rv.o, dv, total, Hv, HD, (uint64_t)Hv * HD * 2, 1, CH))
+    return GDN_ERR_CUDA;
   if (p.nseg > 1) {
     DecayFoldArgs f;
     memset(&f, 0, sizeof f);
@@ -437,7 +440,6 @@ int gdn_attn_fwd(const void* q, const void* k, const void* v, const int* cu_q, c
   a.part = at<float>(ws, p.part);
   a.part_lse = at<float>(ws, p.part_lse);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if ((rc = cuda_status(cudaMemsetAsync(a.status, 0, sizeof(int), s)))) return rc;
   return cuda_status(launch_attn_fwd(a, s));
 }
 
@@ -475,7 +477,6 @@ int gdn_attn_bwd(const void* q, const void* k, const void* v, const void* o, con
   a.dk = static_cast<bf16*>(dk);
   a.dv = static_cast<bf16*>(dv);
   a.status = at<int>(ws, p.status);
-  if ((rc = cuda_status(cudaMemsetAsync(a.status, 0, sizeof(int), s)))) return rc;
   return cuda_status(launch_attn_bwd(a, s));
 }
 

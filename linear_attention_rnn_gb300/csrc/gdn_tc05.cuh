@@ -127,6 +127,27 @@ __device__ __forceinline__ void ld16(uint32_t taddr, float (&v)[16]) {
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// 64 consecutive fp32 columns of this thread's TMEM lane, both loads in flight at once
+__device__ __forceinline__ void ld64(uint32_t taddr, float (&v)[64]) {
+  uint32_t r[64];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t* p = r + 32 * h;
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+        "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(p[0]), "=r"(p[1]), "=r"(p[2]), "=r"(p[3]), "=r"(p[4]), "=r"(p[5]), "=r"(p[6]),
+          "=r"(p[7]), "=r"(p[8]), "=r"(p[9]), "=r"(p[10]), "=r"(p[11]), "=r"(p[12]), "=r"(p[13]),
+          "=r"(p[14]), "=r"(p[15]), "=r"(p[16]), "=r"(p[17]), "=r"(p[18]), "=r"(p[19]), "=r"(p[20]),
+          "=r"(p[21]), "=r"(p[22]), "=r"(p[23]), "=r"(p[24]), "=r"(p[25]), "=r"(p[26]), "=r"(p[27]),
+          "=r"(p[28]), "=r"(p[29]), "=r"(p[30]), "=r"(p[31])
+        : "r"(taddr + 32u * (uint32_t)h));
+  }
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
+}
+
 // ---- mbarriers --------------------------------------------------------------------
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count));
@@ -367,6 +388,11 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int x, 
       "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
 }
+__device__ __forceinline__ void tma_store_3d(const void* tmap, int x, int y, int z, const void* src) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(tmap), "r"(x),
+               "r"(y), "r"(z), "r"(smem_u32(src))
+               : "memory");
+}
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
@@ -390,23 +416,68 @@ struct Wait {
 // The [128 x K] bf16 A operand: row m is TMEM lane m, and each 32-bit column
 // holds two consecutive K elements (the lower one in the low half), so a
 // K = 16 step reads 8 columns.
-__device__ __forceinline__ void mma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t db, uint32_t idesc,
+// ---- products issued by a whole warp ------------------------------------------------
+// The warp runs the issuing code together and one lane (`leader`, the same one
+// throughout) issues: addresses and descriptors are then uniform over the warp,
+// and the compiler keeps them in uniform registers, where tcgen05.mma reads them.
+// Issued from a branch that one lane takes, each MMA first moves its operands
+// there, which costs more time than a K = 16 step of 128 x 128 takes.
+__device__ __forceinline__ int warp_index() {  // threadIdx.x / 32, known to be uniform
+  return __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
+}
+__device__ __forceinline__ uint32_t elect_leader() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}\n" : "=r"(p));
+  return p;
+}
+__device__ __forceinline__ void mma_by(uint32_t leader, uint32_t tmem_d, uint64_t da, uint64_t db, uint32_t idesc,
                                        uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(tmem_d),
-      "r"(tmem_a), "l"(db), "r"(idesc), "r"(accumulate));
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(tmem_d),
+      "l"(da), "l"(db), "r"(idesc), "r"(accumulate), "r"(leader));
 }
-// D[128 x 128] (+)= A B, A in tensor memory (K = 128: 64 columns), B a [128 (K)
-// rows x 128] SW128 tile read MN-major (as gemm_bmn_k128)
-__device__ __forceinline__ void gemm_ts_bmn(uint32_t tmem_d, uint32_t tmem_a, uint32_t b_smem,
-                                            bool accumulate_first) {
+__device__ __forceinline__ void mma_ts_by(uint32_t leader, uint32_t tmem_d, uint32_t tmem_a, uint64_t db,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(db), "r"(idesc), "r"(accumulate), "r"(leader));
+}
+__device__ __forceinline__ void commit_by(uint32_t leader, uint64_t* mbar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(smem_u32(mbar)),
+      "r"(leader)
+      : "memory");
+}
+// gemm128 by a warp: D[128 x 128] (+)= A B^T of SW128 tiles, each K-major or MN-major
+template <bool A_MN, bool B_MN>
+__device__ __forceinline__ void gemm128_by(uint32_t leader, uint32_t tmem_d, uint32_t a_smem, uint32_t b_smem,
+                                           bool accumulate_first) {
+  const uint32_t idesc = idesc_bf16(128, 128) | (A_MN ? (1u << 15) : 0u) | (B_MN ? (1u << 16) : 0u);
+  const uint64_t da0 = A_MN ? desc_sw128_mn(a_smem, 128u * 128u) : desc_sw128(a_smem);
+  const uint64_t db0 = B_MN ? desc_sw128_mn(b_smem, 128u * 128u) : desc_sw128(b_smem);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const uint32_t kmaj = (uint32_t)(k >> 2) * 128u * 128u + (uint32_t)(k & 3) * 32u;
+    mma_by(leader, tmem_d, da0 + ((A_MN ? (uint32_t)k * 2048u : kmaj) >> 4),
+           db0 + ((B_MN ? (uint32_t)k * 2048u : kmaj) >> 4), idesc, (k > 0 || accumulate_first) ? 1u : 0u);
+  }
+}
+// A bf16 operand in tensor memory (K = 128) times a [128 (K) rows x 128] tile read
+// MN-major, by a warp.  SPLIT: the operand's last 64 K-values begin at column 64,
+// not 32 (each half then lies over the fp32 half that its writers have read).
+template <bool SPLIT>
+__device__ __forceinline__ void gemm_ts_by(uint32_t leader, uint32_t tmem_d, uint32_t tmem_a, uint32_t b_smem,
+                                           bool accumulate_first) {
   const uint32_t idesc = idesc_bf16(128, 128) | (1u << 16);
   const uint64_t db0 = desc_sw128_mn(b_smem, 128u * 128u);
 #pragma unroll
   for (int k = 0; k < 8; ++k)
-    mma_ts(tmem_d, tmem_a + 8u * (uint32_t)k, db0 + (((uint32_t)k * 2048u) >> 4), idesc,
-           (k > 0 || accumulate_first) ? 1u : 0u);
+    mma_ts_by(leader, tmem_d, tmem_a + (SPLIT ? 64u : 32u) * (uint32_t)(k >> 2) + 8u * (uint32_t)(k & 3),
+              db0 + (((uint32_t)k * 2048u) >> 4), idesc, (k > 0 || accumulate_first) ? 1u : 0u);
 }
 // 32 values as 16 packed bf16 columns of this thread's TMEM lane (complete after wait_st)
 __device__ __forceinline__ void st16_bf16(uint32_t taddr, const float (&v)[32]) {
@@ -419,6 +490,16 @@ __device__ __forceinline__ void st16_bf16(uint32_t taddr, const float (&v)[32]) 
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
       "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+
+// 16 values as 8 packed bf16 columns of this thread's TMEM lane (complete after wait_st)
+__device__ __forceinline__ void st8_bf16(uint32_t taddr, const float (&v)[16]) {
+  uint32_t r[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 }  // namespace tc
