@@ -40,7 +40,7 @@ struct FwdSmem {
   unsigned char q[2][TILE];
   unsigned char slot[NSLOT][TILE];
   uint64_t full[NSLOT], empty[NSLOT];
-  uint64_t barQ[2], barS[2], barP[2], barO[2];
+  uint64_t barQ[2], barS[2], barP[2][2], barO[2];  // barP: the halves of P
   uint32_t tmem;
 };
 
@@ -60,7 +60,9 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) k_attn_fwd(const __grid_consta
   const int off = sq.kl - sq.ql;
   const int tok0 = at.y * 2 * TT;
   if (tok0 >= sq.ql) return;
-  // key tiles [kb, kb + n[w]) of tile w
+  // Key tiles from kb on: n[0] and n[1] of the two query tiles.  A single query
+  // tile of a split call is held by both groups of warps, each with every second
+  // key tile (`dual`).
   int n[2];
   const int kb = split * a.split_tiles, most = split == a.n_splits - 1 ? INT_MAX : a.split_tiles;
 #pragma unroll
@@ -69,7 +71,12 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) k_attn_fwd(const __grid_consta
     const int keys = last >= first ? min(sq.kl, last + off + 1) : 0;
     n[w] = max(0, min((max(keys, 0) + CH - 1) / CH - kb, most));
   }
-  const int nmax = max(n[0], n[1]);
+  const bool dual = a.n_splits > 1 && tok0 + TT >= sq.ql;
+  const int nmax = max(n[0], n[1]);  // key tiles that are loaded
+  if (dual) {
+    n[1] = nmax / 2;
+    n[0] = nmax - n[1];
+  }
   const float sc = a.scale * LOG2E;
 
   if (tid == 0) {
@@ -81,7 +88,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) k_attn_fwd(const __grid_consta
       tc::mbar_init(&sm.barQ[w], 1);
       tc::mbar_init(&sm.barS[w], 1);
       tc::mbar_init(&sm.barO[w], 1);
-      tc::mbar_init(&sm.barP[w], 128);
+      tc::mbar_init(&sm.barP[w][0], 128);
+      tc::mbar_init(&sm.barP[w][1], 128);
     }
     tc::mbar_fence_init();
   }
@@ -95,7 +103,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) k_attn_fwd(const __grid_consta
 
   if (warp == 9) {
     if (lane == 0 && nmax > 0) {
-      for (int x = 0; x < 2; ++x)
+      for (int x = 0; x < (dual ? 1 : 2); ++x)
         if (n[x] > 0) load_group(sm.q[x], &a.q, kh, G, sq.q0 + tok0 + x * TT, &sm.barQ[x]);
       for (int t = 0; t < nt && w.ok; ++t) {
         const int k = t % NSLOT;
@@ -116,62 +124,95 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) k_attn_fwd(const __grid_consta
       auto release = [&](int t) {
         if (t + NSLOT < nt) tc::commit_by(lead, &sm.empty[t % NSLOT]);
       };
-      auto scores = [&](int x, int i) {  // S of tile x = Q K^T
-        tc::gemm128_by<false, false>(lead, tS + 128 * x, smem_u32(sm.q[x]), slot(2 * i), false);
+      auto scores = [&](int x, int q, int i) {  // S of group x = Q K^T of key tile i
+        tc::gemm128_by<false, false>(lead, tS + 128 * x, smem_u32(sm.q[q]), slot(2 * i), false);
         tc::commit_by(lead, &sm.barS[x]);
       };
-      arrived(0);
-      for (int x = 0; x < 2; ++x)
-        if (n[x] > 0) {
-          w.warp_on(&sm.barQ[x], 0);
-          scores(x, 0);
-        }
-      release(0);
-      for (int i = 0; i < nmax; ++i) {
-        arrived(2 * i + 1);
-        if (i + 1 < nmax) arrived(2 * i + 2);
+      // O of group x += P V of key tile i, the group's j-th; P arrives by halves
+      auto values = [&](int x, int i, int j) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (i < n[x]) {
-            w.warp_on(&sm.barP[x], i);
-            tc::fence_after();
-            tc::gemm_ts_by<false>(lead, tO + 128 * x, tS + 128 * x, slot(2 * i + 1), i > 0);
-            if (i + 1 == n[x]) tc::commit_by(lead, &sm.barO[x]);
-          }
-          if (x == 1) release(2 * i + 1);
-          if (i + 1 < n[x]) scores(x, i + 1);
+        for (int h = 0; h < 2; ++h) {
+          w.warp_on(&sm.barP[x][h], j);
+          tc::fence_after();
+          tc::gemm_ts64_by(lead, tO + 128 * x, tS + 128 * x + 32 * h, slot(2 * i + 1) + 8192 * h, j > 0 || h > 0);
         }
-        if (i + 1 < nmax) release(2 * i + 2);
+        if (j + 1 == n[x]) tc::commit_by(lead, &sm.barO[x]);
+      };
+      if (n[0] > 0) w.warp_on(&sm.barQ[0], 0);  // (early rows may see no key)
+      arrived(0);
+      if (dual) {
+        scores(0, 0, 0);
+        release(0);
+        if (nmax > 1) {
+          arrived(2);
+          scores(1, 0, 1);
+          release(2);
+        }
+        for (int i = 0; i < nmax; ++i) {
+          arrived(2 * i + 1);
+          values(i & 1, i, i >> 1);
+          release(2 * i + 1);
+          if (i + 2 < nmax) {
+            arrived(2 * i + 4);
+            scores(i & 1, 0, i + 2);
+            release(2 * i + 4);
+          }
+        }
+      } else {
+        if (n[0] > 0) scores(0, 0, 0);
+        if (n[1] > 0) {
+          w.warp_on(&sm.barQ[1], 0);
+          scores(1, 1, 0);
+        }
+        release(0);
+        for (int i = 0; i < nmax; ++i) {
+          arrived(2 * i + 1);
+          if (i + 1 < nmax) arrived(2 * i + 2);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (i < n[x]) values(x, i, i);
+            if (x == 1) release(2 * i + 1);
+            if (i + 1 < n[x]) scores(x, x, i + 1);
+          }
+          if (i + 1 < nmax) release(2 * i + 2);
+        }
       }
     }
   } else {
     const int x = warp >> 2, r = 32 * (warp & 3) + lane;
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t S = tS + 128 * x + lane_base, O = tO + 128 * x + lane_base;
-    const int tok = tok0 + x * TT + r / G;
+    const int tok = tok0 + (dual ? 0 : x * TT) + r / G;
     const bool valid = r < TT * G && tok < sq.ql;
     const int lim = valid ? tok + off : -1;  // the last key that the row sees
     const bool any = __any_sync(0xffffffffu, valid);
     float m = -INFINITY, l = 0.f;
     for (int i = 0; i < n[x]; ++i) {
-      const int key0 = (kb + i) * CH;
+      const int tile = dual ? 2 * i + x : i;  // of the CTA's key tiles
+      const int key0 = (kb + tile) * CH;
+      if (key0 + CH > sq.kl) {  // rows past the keys: whatever they hold, they count as zero
+        const int t = 2 * tile + 1;
+        w.warp_on(&sm.full[t % NSLOT], t / NSLOT);
+        zero_rows(sm.slot[t % NSLOT], sq.kl - key0, tid & 127, 128);
+        tc::fence_proxy_async();
+      }
       w.warp_on(&sm.barS[x], i);
       tc::fence_after();
       if (any) {
         float v[128];
-#pragma unroll
-        for (int g = 0; g < 4; ++g) tc::ld32(S + 32 * g, *reinterpret_cast<float(*)[32]>(v + 32 * g));
+        tc::ld64(S, *reinterpret_cast<float(*)[64]>(v));
+        tc::ld64(S + 64, *reinterpret_cast<float(*)[64]>(v + 64));
         if (key0 + CH - 1 > lim) {
 #pragma unroll
           for (int j = 0; j < 128; ++j) v[j] = key0 + j <= lim ? v[j] : -INFINITY;
         }
         float mt[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-        for (int j = 4; j < 128; j += 4) {
+        for (int j = 4; j < 124; j += 8) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) mt[c] = fmaxf(mt[c], v[j + c]);
+          for (int c = 0; c < 4; ++c) mt[c] = tc::max3(mt[c], v[j + c], v[j + 4 + c]);
         }
-        const float mn = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3]));
+        const float mn = fmaxf(tc::max3(mt[0], mt[1], fmaxf(v[124], v[125])), tc::max3(mt[2], mt[3], fmaxf(v[126], v[127])));
         // raise the maximum (a first one counts); O is idle: this S was issued after the last P V
         if (__any_sync(0xffffffffu, mn > m && (mn - m) * sc > RAISE)) {
           const float to = fmaxf(m, mn);
@@ -190,29 +231,32 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) k_attn_fwd(const __grid_consta
             tc::wait_st();
           }
         }
-        const float ms = m == -INFINITY ? 0.f : m * sc;
+        const float ms = m == -INFINITY ? 0.f : -m * sc;
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          float p[32];
+        for (int h = 0; h < 2; ++h) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            p[j] = ex2(v[32 * g + j] * sc - ms);
-            sum[j & 3] += p[j];
+          for (int g = 0; g < 2; ++g) {
+            float(&p)[32] = *reinterpret_cast<float(*)[32]>(v + 64 * h + 32 * g);
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              tc::fma2(p[j], p[j + 1], sc, sc, ms);
+              p[j] = ex2(p[j]);
+              p[j + 1] = ex2(p[j + 1]);
+              tc::add2(sum[j & 2], sum[(j & 2) + 1], p[j], p[j + 1]);
+            }
+            tc::st16_bf16(S + 32 * h + 16 * g, p);
           }
-          tc::st16_bf16(S + 16 * g, p);
+          tc::wait_st();
+          tc::fence_before();
+          tc::mbar_arrive(&sm.barP[x][h]);
         }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      } else {
+        tc::fence_before();
+        tc::mbar_arrive(&sm.barP[x][0]);
+        tc::mbar_arrive(&sm.barP[x][1]);
       }
-      if (key0 + CH > sq.kl) {  // rows past the keys: whatever they hold, they count as zero
-        const int t = 2 * i + 1;
-        w.warp_on(&sm.full[t % NSLOT], t / NSLOT);
-        zero_rows(sm.slot[t % NSLOT], sq.kl - key0, tid & 127, 128);
-        tc::fence_proxy_async();
-      }
-      tc::wait_st();
-      tc::fence_before();
-      tc::mbar_arrive(&sm.barP[x]);
     }
     if (n[x] > 0) w.warp_on(&sm.barO[x], 0);
     tc::fence_after();
@@ -234,7 +278,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) k_attn_fwd(const __grid_consta
           if (a.n_splits == 1) {
             store32(a.o + row * HD + 32 * g, y, inv);
           } else if (l > 0.f) {  // (the join reads a part only where its lse is finite)
-            float* d = a.part + ((long)split * a.total_q * a.Hq + row) * HD + 32 * g;
+            float* d = a.part + ((long)(2 * split + x) * a.total_q * a.Hq + row) * HD + 32 * g;
 #pragma unroll
             for (int j = 0; j < 8; ++j)
               *reinterpret_cast<float4*>(d + 4 * j) =
@@ -244,10 +288,13 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) k_attn_fwd(const __grid_consta
         __syncwarp();
       }
       if (valid) {
-        if (a.n_splits > 1)
-          a.part_lse[(long)split * a.total_q * a.Hq + row] = lse;
-        else if (a.lse)
+        if (a.n_splits > 1) {
+          // (two parts to a split; a query tile that one group holds alone leaves the other empty)
+          if (!dual) a.part_lse[(long)(2 * split + 1 - x) * a.total_q * a.Hq + row] = -INFINITY;
+          a.part_lse[(long)(2 * split + x) * a.total_q * a.Hq + row] = lse;
+        } else if (a.lse) {
           a.lse[row] = lse;
+        }
       }
     }
     tc::fence_before();
@@ -266,12 +313,12 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ AttnA
   const int lane = threadIdx.x & 31;
   if (row >= rows) return;
   float top = -INFINITY;
-  for (int s = lane; s < a.n_splits; s += 32) top = fmaxf(top, a.part_lse[s * rows + row]);
+  for (int s = lane; s < 2 * a.n_splits; s += 32) top = fmaxf(top, a.part_lse[s * rows + row]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   float total = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
   if (top > -INFINITY)
-    for (int s = 0; s < a.n_splits; ++s) {
+    for (int s = 0; s < 2 * a.n_splits; ++s) {
       const float l = a.part_lse[s * rows + row];
       if (l == -INFINITY) continue;
       const float f = expf(l - top);

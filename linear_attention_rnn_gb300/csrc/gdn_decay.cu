@@ -90,16 +90,15 @@ __device__ __forceinline__ int2 find_segment(const int* cu, int n_seqs, int T, i
 
 // Rows of an SW128 tile scaled by f and split into TERMS bf16 terms, the first in
 // place, the others in the tiles at `rest`; this thread's row r, 16-byte chunks
-// j0 .. j0 + NJ - 1.  The leading terms are the value's upper 16 bits as they
+// j .. j + 3.  The leading terms are the value's upper 16 bits as they
 // stand (the remainder is then exact), the last one is rounded: 8 bits more of
 // the fp32 product per term, at a permute, two ands and a subtraction per pair.
 // A row that is not `valid` (past the sequence's end) becomes zero, whatever it
 // holds.
-template <int TERMS, int NJ>
-__device__ __forceinline__ void scale_row(unsigned char* tile, unsigned char* rest, int r, int j0, float f, bool valid) {
+template <int TERMS>
+__device__ __forceinline__ void scale_row(unsigned char* tile, unsigned char* rest, int r, int j, float f, bool valid) {
   const uint32_t keep = valid ? 0xffffffffu : 0u;
-#pragma unroll 1
-  for (int j = j0; j < j0 + NJ; j += 4) {
+  {
     uint4 u[4];  // four loads in flight
 #pragma unroll
     for (int c = 0; c < 4; ++c) u[c] = *reinterpret_cast<const uint4*>(tile + tc::sw128_chunk(r, j + c, CH));
@@ -150,7 +149,7 @@ struct WalkSmem {
   unsigned char X[TILE];                // the entering state in bf16, [128 (b) rows x 128 (c)]
   alignas(16) float tab[CH];            // e^{w d}
   uint64_t full[NSLOT], empty[NSLOT];
-  uint64_t barP, barPm, barK, barS, barX, barO, barOf, barSt;
+  uint64_t barP, barPm, barK[2], barS, barX, barO, barOf, barSt;
   uint32_t tmem;
 };
 
@@ -175,7 +174,8 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
     tc::mbar_init(&sm.barX, 1);
     tc::mbar_init(&sm.barO, 1);
     tc::mbar_init(&sm.barPm, 256);
-    tc::mbar_init(&sm.barK, 256);
+    tc::mbar_init(&sm.barK[0], 256);
+    tc::mbar_init(&sm.barK[1], 256);
     tc::mbar_init(&sm.barS, 256);
     tc::mbar_init(&sm.barOf, 256);
     tc::mbar_init(&sm.barSt, 256);
@@ -249,12 +249,16 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
       tc::fence_after();
       tc::gemm128_by<false, true>(lead, tO1, slot(ta), smem_u32(sm.X), false);  // A X
       release(ta);
-      w.warp_on(&sm.barK, it);
       arrived(tcc);
-      tc::fence_after();
-      tc::gemm128_by<true, true>(lead, tX, slot(tb), slot(tcc), true);  // X += B'^T C
 #pragma unroll
-      for (int t = 0; t < TERMS - 1; ++t) tc::gemm128_by<true, true>(lead, tX, smem_u32(sm.rest[t]), slot(tcc), true);
+      for (int h = 0; h < 2; ++h) {  // X += B'^T C, 64 tokens at a time
+        w.warp_on(&sm.barK[h], it);
+        tc::fence_after();
+        const uint32_t c = slot(tcc) + 8192 * h;
+        tc::gemm_rows64_by(lead, tX, slot(tb) + 8192 * h, c, true);
+#pragma unroll
+        for (int t = 0; t < TERMS - 1; ++t) tc::gemm_rows64_by(lead, tX, smem_u32(sm.rest[t]) + 8192 * h, c, true);
+      }
       tc::commit_by(lead, &sm.barX);
       release(tb);
       w.warp_on(&sm.barPm, it);
@@ -448,16 +452,18 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
         tc::mbar_arrive(&sm.barS);
         // ---- B' = diag(e) B in bf16 terms; rows past the sequence's end are cleared
         const int tb = 3 * it + 1, tcc = tb + 1;
-        const float e = expf(wd * (float)(REV ? r + 1 : max(n - 1 - r, 0)));
         w.warp_on(&sm.full[tb % NSLOT], tb / NSLOT);
+        if (n < CH) w.warp_on(&sm.full[tcc % NSLOT], tcc / NSLOT);
         w.warp_on(&sm.barP, it);  // (A B^T, which reads the raw tile, has completed)
-        scale_row<TERMS, 8>(sm.slot[tb % NSLOT], sm.rest[0], r, 8 * half, e, r < n);
-        if (n < CH) {
-          w.warp_on(&sm.full[tcc % NSLOT], tcc / NSLOT);
-          if (r >= n) zero_row(sm.slot[tcc % NSLOT], r, 8 * half, 8);
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {  // 64 rows at a time, four threads to a row
+          const int i = 64 * h + (tid & 63), j = 4 * ((tid >> 6) & 3);
+          const float e = expf(wd * (float)(REV ? i + 1 : max(n - 1 - i, 0)));
+          scale_row<TERMS>(sm.slot[tb % NSLOT], sm.rest[0], i, j, e, i < n);
+          if (i >= n) zero_row(sm.slot[tcc % NSLOT], i, j, 4);
+          tc::fence_proxy_async();
+          tc::mbar_arrive(&sm.barK[h]);
         }
-        tc::fence_proxy_async();
-        tc::mbar_arrive(&sm.barK);
       }
       if (R.xT) {  // (one segment: with more, the prefix has written the final state)
         w.warp_on(&sm.barX, n_it - 1);
@@ -526,7 +532,7 @@ struct FoldSmem {
   unsigned char slot[FOLD_SLOTS][TILE];
   unsigned char rest[FOLD_TERMS - 1][TILE];  // further terms of the scaled B rows
   uint64_t full[FOLD_SLOTS], empty[FOLD_SLOTS];
-  uint64_t barK, barM;
+  uint64_t barK[2], barM[2];
   uint32_t tmem;
 };
 
@@ -556,8 +562,10 @@ __global__ void __launch_bounds__(FOLD_THREADS, 1) k_decay_fold(const __grid_con
       tc::mbar_init(&sm.full[k], 1);
       tc::mbar_init(&sm.empty[k], 1);
     }
-    tc::mbar_init(&sm.barK, 256);
-    tc::mbar_init(&sm.barM, 1);
+    for (int h = 0; h < 2; ++h) {
+      tc::mbar_init(&sm.barK[h], 256);
+      tc::mbar_init(&sm.barM[h], 1);
+    }
     tc::mbar_fence_init();
   }
   if (warp == 0) tc::alloc(&sm.tmem, 128);
@@ -584,36 +592,43 @@ __global__ void __launch_bounds__(FOLD_THREADS, 1) k_decay_fold(const __grid_con
     const uint32_t lead = tc::elect_leader();
     for (int i = 0; i < nc; ++i) {
       const int tb = 2 * i, tcc = tb + 1;
-      w.warp_on(&sm.barK, i);
       w.warp_on(&sm.full[tcc % FOLD_SLOTS], tcc / FOLD_SLOTS);
-      tc::fence_after();
-      const uint32_t c = smem_u32(sm.slot[tcc % FOLD_SLOTS]);
-      tc::gemm128_by<true, true>(lead, tX, smem_u32(sm.slot[tb % FOLD_SLOTS]), c, i > 0);
 #pragma unroll
-      for (int t = 0; t < FOLD_TERMS - 1; ++t) tc::gemm128_by<true, true>(lead, tX, smem_u32(sm.rest[t]), c, true);
-      if (tb + FOLD_SLOTS < 2 * nc) tc::commit_by(lead, &sm.empty[tb % FOLD_SLOTS]);
-      if (tcc + FOLD_SLOTS < 2 * nc) tc::commit_by(lead, &sm.empty[tcc % FOLD_SLOTS]);
-      tc::commit_by(lead, &sm.barM);
+      for (int h = 0; h < 2; ++h) {
+        w.warp_on(&sm.barK[h], i);
+        tc::fence_after();
+        const uint32_t c = smem_u32(sm.slot[tcc % FOLD_SLOTS]) + 8192 * h;
+        tc::gemm_rows64_by(lead, tX, smem_u32(sm.slot[tb % FOLD_SLOTS]) + 8192 * h, c, i > 0 || h > 0);
+#pragma unroll
+        for (int t = 0; t < FOLD_TERMS - 1; ++t)
+          tc::gemm_rows64_by(lead, tX, smem_u32(sm.rest[t]) + 8192 * h, c, true);
+        if (h == 1) {
+          if (tb + FOLD_SLOTS < 2 * nc) tc::commit_by(lead, &sm.empty[tb % FOLD_SLOTS]);
+          if (tcc + FOLD_SLOTS < 2 * nc) tc::commit_by(lead, &sm.empty[tcc % FOLD_SLOTS]);
+        }
+        tc::commit_by(lead, &sm.barM[h]);
+      }
     }
   } else {
-    const int r = tid & 127, j0 = 8 * (tid >> 7);
+    const int j0 = 4 * (tid >> 6);  // 64 rows at a time, four threads to a row
     const float wd = a.decay[j];
     for (int i = 0; i < nc; ++i) {
-      const int t0 = (cb + i) * CH + r, n = min(CH, q.len - (cb + i) * CH);
-      const int tb = 2 * i, tcc = tb + 1;
-      // weight to the segment's end (forwards) or to its start (backwards)
-      const float e = expf(wd * (float)(R.rev ? t0 - cb * CH + 1 : max(end - 1 - t0, 0)));
-      if (i > 0) w.warp_on(&sm.barM, i - 1);  // (the second term of the chunk before has been read)
+      const int n = min(CH, q.len - (cb + i) * CH), tb = 2 * i, tcc = tb + 1;
       w.warp_on(&sm.full[tb % FOLD_SLOTS], tb / FOLD_SLOTS);
-      scale_row<FOLD_TERMS, 8>(sm.slot[tb % FOLD_SLOTS], sm.rest[0], r, j0, e, r < n);
-      if (n < CH) {
-        w.warp_on(&sm.full[tcc % FOLD_SLOTS], tcc / FOLD_SLOTS);
-        if (r >= n) zero_row(sm.slot[tcc % FOLD_SLOTS], r, j0, 8);
+      if (n < CH) w.warp_on(&sm.full[tcc % FOLD_SLOTS], tcc / FOLD_SLOTS);
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        const int r = 64 * h + (tid & 63), t0 = (cb + i) * CH + r;
+        // weight to the segment's end (forwards) or to its start (backwards)
+        const float e = expf(wd * (float)(R.rev ? t0 - cb * CH + 1 : max(end - 1 - t0, 0)));
+        if (i > 0) w.warp_on(&sm.barM[h], i - 1);  // (these rows' further terms have been read)
+        scale_row<FOLD_TERMS>(sm.slot[tb % FOLD_SLOTS], sm.rest[0], r, j0, e, r < n);
+        if (r >= n) zero_row(sm.slot[tcc % FOLD_SLOTS], r, j0, 4);
+        tc::fence_proxy_async();
+        tc::mbar_arrive(&sm.barK[h]);
       }
-      tc::fence_proxy_async();
-      tc::mbar_arrive(&sm.barK);
     }
-    w.warp_on(&sm.barM, nc - 1);
+    w.warp_on(&sm.barM[1], nc - 1);
     tc::fence_after();
     const int row = 32 * (warp & 3) + lane, g0 = 2 * (warp >> 2);
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;

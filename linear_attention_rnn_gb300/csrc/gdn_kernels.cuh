@@ -204,8 +204,8 @@ struct AttnArgs {
   const int* k_len;     // [n_seqs] used rows of each sequence's keys (nullable; forward)
   bf16* o;              // [total_q][Hq][HD]
   float* lse;           // [total_q][Hq] (forward: nullable)
-  float* part;          // [n_splits][total_q][Hq][HD]
-  float* part_lse;      // [n_splits][total_q][Hq]
+  float* part;          // [2 n_splits][total_q][Hq][HD]
+  float* part_lse;      // [2 n_splits][total_q][Hq]
   const bf16* dOp;      // backward: dO and o as plain rows, delta = dO . o
   const bf16* op;
   float* delta;         // [total_q][Hq]

@@ -134,8 +134,8 @@ AttnPlan attn_plan(int backward, int n_seqs, int total_q, int max_k, int Hq, int
   if (backward) {
     p.delta = take(rows * sizeof(float));
   } else if (p.n_splits > 1) {
-    p.part = take(rows * p.n_splits * HD * sizeof(float));
-    p.part_lse = take(rows * p.n_splits * sizeof(float));
+    p.part = take(rows * 2 * p.n_splits * HD * sizeof(float));
+    p.part_lse = take(rows * 2 * p.n_splits * sizeof(float));
   }
   p.total = off;
   return p;

@@ -466,6 +466,17 @@ __device__ __forceinline__ void gemm128_by(uint32_t leader, uint32_t tmem_d, uin
            db0 + ((B_MN ? (uint32_t)k * 2048u : kmaj) >> 4), idesc, (k > 0 || accumulate_first) ? 1u : 0u);
   }
 }
+// D[128 x 128] (+)= A^T B over 64 of the K rows: A and B are rows of [128 (K) x 128]
+// tiles, from the row that the addresses point to (a multiple of 8)
+__device__ __forceinline__ void gemm_rows64_by(uint32_t leader, uint32_t tmem_d, uint32_t a_smem, uint32_t b_smem,
+                                               bool accumulate_first) {
+  const uint32_t idesc = idesc_bf16(128, 128) | (1u << 15) | (1u << 16);
+  const uint64_t da0 = desc_sw128_mn(a_smem, 128u * 128u), db0 = desc_sw128_mn(b_smem, 128u * 128u);
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    mma_by(leader, tmem_d, da0 + (((uint32_t)k * 2048u) >> 4), db0 + (((uint32_t)k * 2048u) >> 4), idesc,
+           (k > 0 || accumulate_first) ? 1u : 0u);
+}
 // A bf16 operand in tensor memory (K = 128) times a [128 (K) rows x 128] tile read
 // MN-major, by a warp.  SPLIT: the operand's last 64 K-values begin at column 64,
 // not 32 (each half then lies over the fp32 half that its writers have read).
@@ -500,6 +511,37 @@ __device__ __forceinline__ void st8_bf16(uint32_t taddr, const float (&v)[16]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
+}
+
+// 64 of the K-values: A in tensor memory from tmem_a on (32 columns), B from the row
+// of its tile that b_smem points to, by a warp
+__device__ __forceinline__ void gemm_ts64_by(uint32_t leader, uint32_t tmem_d, uint32_t tmem_a, uint32_t b_smem,
+                                             bool accumulate_first) {
+  const uint32_t idesc = idesc_bf16(128, 128) | (1u << 16);
+  const uint64_t db0 = desc_sw128_mn(b_smem, 128u * 128u);
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    mma_ts_by(leader, tmem_d, tmem_a + 8u * (uint32_t)k, db0 + (((uint32_t)k * 2048u) >> 4), idesc,
+              (k > 0 || accumulate_first) ? 1u : 0u);
+}
+
+// ---- pairs of fp32 values (one instruction for two) ------------------------------------
+__device__ __forceinline__ void fma2(float& x, float& y, float a, float b, float c) {  // x, y <- x a + c, y b + c
+  asm("{\n\t.reg .b64 p, q, r;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tmov.b64 r, {%4, %4};\n\t"
+      "fma.rn.f32x2 p, p, q, r;\n\tmov.b64 {%0, %1}, p;\n\t}\n"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b), "f"(c));
+}
+__device__ __forceinline__ void add2(float& x, float& y, float a, float b) {  // x += a, y += b
+  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\t"
+      "add.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}\n"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 }  // namespace tc
