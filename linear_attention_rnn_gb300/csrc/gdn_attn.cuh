@@ -40,25 +40,51 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs& a, int s) {
   return r;
 }
 
-// Tile slots: sequence s has the slots first_slot(s) .. first_slot(s + 1) - 1, at
-// least as many as it has tiles of K rows and at most one more than total / K
-// over all sequences together.
-__device__ __forceinline__ int first_slot(const int* cu, int s, int each, int total, int K) {
-  return (cu ? min(max(cu[s], 0), total) : s * each) / K + s;
-}
-// Sequence and tile of a slot, by all threads of the block together (sequence
-// -1: none).
-__device__ __forceinline__ int2 find_tile(const int* cu, int n_seqs, int total, int K, int slot) {
-  __shared__ int2 found;
-  if (threadIdx.x == 0) found = make_int2(-1, 0);
-  __syncthreads();
-  const int each = total / n_seqs;
-  for (int s = threadIdx.x; s < n_seqs; s += blockDim.x) {
-    const int a = first_slot(cu, s, each, total, K);
-    if (slot >= a && slot < first_slot(cu, s + 1, each, total, K)) found = make_int2(s, slot - a);
+// The rank-th tile of all sequences' tiles of K rows, those with the highest index
+// in their sequence first (the work of a tile grows with it, and CTAs start in
+// order of rank); sequence -1: there are fewer.  cu null: `each` rows to a
+// sequence.  Every warp finds it for itself: a lane counts for every 32nd
+// sequence, and the index of rank's tile is found by bisection.
+__device__ __forceinline__ int2 find_tile(const int* cu, int n_seqs, int total, int K, int rank) {
+  const int lane = threadIdx.x & 31, each = total / n_seqs;
+  auto tiles = [&](int s) {
+    int len = each;
+    if (cu) {
+      const int a = min(max(cu[s], 0), total);
+      len = min(max(cu[s + 1], a), total) - a;
+    }
+    return (len + K - 1) / K;
+  };
+  const int n0 = lane < n_seqs ? tiles(lane) : 0;  // (the first 32 stay in registers)
+  auto count_above = [&](int t) {                  // tiles of index t or more
+    int c = max(n0 - t, 0);
+    for (int s = lane + 32; s < n_seqs; s += 32) c += max(tiles(s) - t, 0);
+    return __reduce_add_sync(0xffffffffu, c);
+  };
+  int most = n0;
+  for (int s = lane + 32; s < n_seqs; s += 32) most = max(most, tiles(s));
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (rank >= count_above(0)) return make_int2(-1, 0);
+  int lo = 0, hi = most;  // count_above(lo) > rank >= count_above(hi)
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (count_above(mid) > rank)
+      lo = mid;
+    else
+      hi = mid;
   }
-  __syncthreads();
-  return found;
+  int k = rank - count_above(lo + 1);  // the k-th sequence that has a tile lo
+  for (int s0 = 0; s0 < n_seqs; s0 += 32) {
+    const bool has = s0 + lane < n_seqs && (s0 ? tiles(s0 + lane) : n0) > lo;
+    unsigned m = __ballot_sync(0xffffffffu, has);
+    const int c = __popc(m);
+    if (k < c) {
+      for (; k > 0; --k) m &= m - 1;
+      return make_int2(s0 + __ffs((int)m) - 1, lo);
+    }
+    k -= c;
+  }
+  return make_int2(-1, 0);
 }
 
 // 128 rows of one head

@@ -5,13 +5,13 @@
 //     ds_ij = p_ij (dp_ij - delta_i),
 //     dv_j = sum_i p_ij dO_i,   dk_j = scale sum_i ds_ij q_i,   dq_i = scale sum_j ds_ij k_j.
 //
-// Two kernels, so that every gradient is summed in one CTA, in a fixed order,
+// Two kinds of CTAs, so that every gradient is summed in one CTA, in a fixed order,
 // without atomics (seven products per tile pair instead of five):
-//   k_attn_dkv  one CTA per 128 keys and key head, over the query tiles that see
+//   dkv   one CTA per 128 keys and key head, over the query tiles that see
 //               them: S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q.  A query
 //               tile holds all heads of the group, so the sum over them is part
 //               of the product.
-//   k_attn_dq   one CTA per query tile, over the key tiles: S = Q K^T, dP = dO V^T,
+//   dq    one CTA per query tile, over the key tiles: S = Q K^T, dP = dO V^T,
 //               dQ += dS K.
 // Accumulators in tensor memory, P and dS as bf16 A operands there too (each
 // half over the fp32 half that its own four warps have read).  Eight compute
@@ -31,28 +31,41 @@ constexpr int BWD_THREADS = 256 + 64;
 constexpr int KV_SLOTS = 4;  // Q, dO of two query tiles
 constexpr int Q_SLOTS = 5;   // K, V of two key tiles and a half
 
-// ---- delta_i = dO_i . o_i, one warp per row ----------------------------------------------
+// ---- delta_i = dO_i . o_i: half a warp to a row, four rows in flight ------------------
+constexpr int DELTA_ROWS = 64;  // rows per block of 256 threads
 __global__ void __launch_bounds__(256) k_attn_delta(const __grid_constant__ AttnArgs a) {
   pdl_wait();
   pdl_release();
   clear_status(a.status);
-  const long rows = (long)a.total_q * a.Hq, row = (long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (row >= rows) return;
-  const uint2 x = *reinterpret_cast<const uint2*>(a.dOp + row * HD + 4 * lane);
-  const uint2 y = *reinterpret_cast<const uint2*>(a.op + row * HD + 4 * lane);
-  const float2 x0 = unpack_bf16(x.x), x1 = unpack_bf16(x.y), y0 = unpack_bf16(y.x), y1 = unpack_bf16(y.y);
-  float d = x0.x * y0.x + x0.y * y0.y + x1.x * y1.x + x1.y * y1.y;
+  const long rows = (long)a.total_q * a.Hq, row0 = (long)blockIdx.x * DELTA_ROWS + (threadIdx.x >> 4);
+  const int c = 8 * (threadIdx.x & 15);
+  uint4 x[4], y[4];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-  if (lane == 0) a.delta[row] = d;
+  for (int k = 0; k < 4; ++k) {
+    const long row = min(row0 + 16 * k, rows - 1);
+    x[k] = *reinterpret_cast<const uint4*>(a.dOp + row * HD + c);
+    y[k] = *reinterpret_cast<const uint4*>(a.op + row * HD + c);
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t u[4] = {x[k].x, x[k].y, x[k].z, x[k].w}, v[4] = {y[k].x, y[k].y, y[k].z, y[k].w};
+    float d = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 p = unpack_bf16(u[i]), q = unpack_bf16(v[i]);
+      d += p.x * q.x + p.y * q.y;
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+    if ((threadIdx.x & 15) == 0 && row0 + 16 * k < rows) a.delta[row0 + 16 * k] = d;
+  }
 }
 
 // ---- dK, dV -------------------------------------------------------------------------
 struct KvSmem {
   unsigned char k[TILE], v[TILE];
   unsigned char slot[KV_SLOTS][TILE];
-  alignas(16) float lse[2][CH];  // of the query rows: lse in base 2, delta, the last key seen
+  alignas(16) float lse[2][CH];  // of the query rows: -lse in base 2, delta, the last key seen
   alignas(16) float delta[2][CH];
   alignas(16) int lim[2][CH];
   uint64_t full[KV_SLOTS], empty[KV_SLOTS];
@@ -60,19 +73,16 @@ struct KvSmem {
   uint32_t tmem;
 };
 
-__global__ void __launch_bounds__(BWD_THREADS, 1) k_attn_dkv(const __grid_constant__ AttnArgs a) {
-  extern __shared__ unsigned char raw[];
+__device__ __forceinline__ void dkv(const AttnArgs& a, unsigned char* raw, int block) {
   KvSmem& sm = *reinterpret_cast<KvSmem*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
   const int tid = threadIdx.x, lane = tid & 31, warp = tc::warp_index();
-  pdl_wait();
-  pdl_release();
   const int G = a.Hq / a.Hk, TT = CH / G;
-  const int kh = blockIdx.x % a.Hk;
-  const int2 at = find_tile(a.cu_k, a.n_seqs, a.total_k, CH, (int)(blockIdx.x / a.Hk));
+  const int kh = block % a.Hk;
+  const int2 at = find_tile(a.cu_k, a.n_seqs, a.total_k, CH, block / a.Hk);
   if (at.x < 0) return;
   const Seq sq = seq_of(a, at.x);
-  const int key0 = at.y * CH, off = sq.kl - sq.ql;
-  if (key0 >= sq.kl) return;
+  // (a sequence's first keys are seen by the most queries: index 0 is its last tile)
+  const int key0 = ((sq.kl + CH - 1) / CH - 1 - at.y) * CH, off = sq.kl - sq.ql;
   const int first = max(0, key0 - off) / TT;                 // first query tile that sees key0
   const int n = max(0, (sq.ql + TT - 1) / TT - first);
 
@@ -175,7 +185,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) k_attn_dkv(const __grid_consta
     };
     auto put_cols = [&](int i) {
       sm.lim[i & 1][tid] = c_lim;
-      sm.lse[i & 1][tid] = c_lse * LOG2E;
+      sm.lse[i & 1][tid] = -c_lse * LOG2E;
       sm.delta[i & 1][tid] = c_delta;
     };
     if (n > 0 && tid < CH) {
@@ -198,10 +208,10 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) k_attn_dkv(const __grid_consta
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
         const float4 l = c_l[j];
-        p[4 * j] = ex2(p[4 * j] * sc - l.x);
-        p[4 * j + 1] = ex2(p[4 * j + 1] * sc - l.y);
-        p[4 * j + 2] = ex2(p[4 * j + 2] * sc - l.z);
-        p[4 * j + 3] = ex2(p[4 * j + 3] * sc - l.w);
+        p[4 * j] = ex2(p[4 * j] * sc + l.x);
+        p[4 * j + 1] = ex2(p[4 * j + 1] * sc + l.y);
+        p[4 * j + 2] = ex2(p[4 * j + 2] * sc + l.z);
+        p[4 * j + 3] = ex2(p[4 * j + 3] * sc + l.w);
       }
       if (!whole) {
 #pragma unroll
@@ -286,16 +296,12 @@ struct QSmem {
   uint32_t tmem;
 };
 
-__global__ void __launch_bounds__(BWD_THREADS, 1) k_attn_dq(const __grid_constant__ AttnArgs a) {
-  extern __shared__ unsigned char raw[];
+__device__ __forceinline__ void dq(const AttnArgs& a, unsigned char* raw, int block) {
   QSmem& sm = *reinterpret_cast<QSmem*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
   const int tid = threadIdx.x, lane = tid & 31, warp = tc::warp_index();
-  pdl_wait();
-  pdl_release();
   const int G = a.Hq / a.Hk, TT = CH / G;
-  // a sequence's last tiles, which see the most keys, start first
-  const int kh = blockIdx.x % a.Hk;
-  const int2 at = find_tile(a.cu_q, a.n_seqs, a.total_q, TT, (int)((gridDim.x - 1 - blockIdx.x) / a.Hk));
+  const int kh = block % a.Hk;
+  const int2 at = find_tile(a.cu_q, a.n_seqs, a.total_q, TT, block / a.Hk);
   if (at.x < 0) return;
   const Seq sq = seq_of(a, at.x);
   const int tok0 = at.y * TT, off = sq.kl - sq.ql;
@@ -439,26 +445,31 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) k_attn_dq(const __grid_constan
   if (warp == 0) tc::dealloc(sm.tmem, 512);
 }
 
-template <typename K>
-cudaError_t set_smem(K k, size_t bytes) {
-  return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+// Both in one launch: the dkv CTAs, whose longest ones are few and long, start
+// first, and the dq CTAs fill the SMs beside and after them.
+__global__ void __launch_bounds__(BWD_THREADS, 1) k_attn_bwd(const __grid_constant__ AttnArgs a, int kv_blocks) {
+  extern __shared__ unsigned char raw[];
+  pdl_wait();
+  pdl_release();
+  if ((int)blockIdx.x < kv_blocks)
+    dkv(a, raw, (int)blockIdx.x);
+  else
+    dq(a, raw, (int)blockIdx.x - kv_blocks);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_bwd(const AttnArgs& a, cudaStream_t s) {
-  constexpr size_t kv = sizeof(KvSmem) + 1024, qs = sizeof(QSmem) + 1024;
-  static_assert(kv <= 227 * 1024 && qs <= 227 * 1024, "shared memory");
-  cudaError_t e = set_smem(k_attn_dkv, kv);
-  if (e == cudaSuccess) e = set_smem(k_attn_dq, qs);
+  constexpr size_t smem = (sizeof(KvSmem) > sizeof(QSmem) ? sizeof(KvSmem) : sizeof(QSmem)) + 1024;
+  static_assert(smem <= 227 * 1024, "shared memory");
+  cudaError_t e = cudaFuncSetAttribute(k_attn_bwd, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   const int TT = CH / (a.Hq / a.Hk);
   const long rows = (long)a.total_q * a.Hq;
-  e = launch_pdl(k_attn_delta, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, a);
+  e = launch_pdl(k_attn_delta, dim3((unsigned)((rows + DELTA_ROWS - 1) / DELTA_ROWS)), dim3(256), 0, s, a);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(k_attn_dkv, dim3((unsigned)a.Hk * (unsigned)(a.total_k / CH + a.n_seqs)), dim3(BWD_THREADS), kv, s, a);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(k_attn_dq, dim3((unsigned)a.Hk * (unsigned)(a.total_q / TT + a.n_seqs)), dim3(BWD_THREADS), qs, s, a);
+  const int kv = a.Hk * (a.total_k / CH + a.n_seqs), q = a.Hk * (a.total_q / TT + a.n_seqs);
+  return launch_pdl(k_attn_bwd, dim3((unsigned)(kv + q)), dim3(BWD_THREADS), smem, s, a, kv);
 }
 
 }  // namespace gdn

@@ -52,9 +52,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) k_attn_fwd(const __grid_consta
   pdl_release();
   if (blockIdx.y == 0) clear_status(a.status);
   const int G = a.Hq / a.Hk, TT = CH / G;  // tokens to a tile
-  // a sequence's last tiles, which see the most keys, start first
   const int kh = blockIdx.x % a.Hk, split = blockIdx.y;
-  const int2 at = find_tile(a.cu_q, a.n_seqs, a.total_q, 2 * TT, (int)((gridDim.x - 1 - blockIdx.x) / a.Hk));
+  const int2 at = find_tile(a.cu_q, a.n_seqs, a.total_q, 2 * TT, (int)(blockIdx.x / a.Hk));
   if (at.x < 0) return;
   const Seq sq = seq_of(a, at.x);
   const int off = sq.kl - sq.ql;
