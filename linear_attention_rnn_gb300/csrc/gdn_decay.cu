@@ -25,7 +25,7 @@
 // into bf16 terms (the first in place, one or two beside it), a product each.  The masked P
 // goes back to tensor memory as a bf16 A operand.  Warps 0-7 mask P and
 // write the output, 8-15 carry the state and scale B; one thread issues the
-// products, one the TMA loads (a ring of five or four 32 KiB tiles, three to a chunk).
+// products, one the TMA loads (a ring of five 32 KiB tiles, three to a chunk).
 //
 // With few sequences and heads the SMs are filled by segments: k_decay_fold
 // forms each segment's own X (rows weighted to the segment's end, so that its
@@ -71,22 +71,26 @@ __device__ __forceinline__ Range seq_range(const int* cu, int s, int T, int tota
 __device__ __forceinline__ int first_slot(const int* cu, int s, int T, int total, int K) {
   return (cu ? min(max(cu[s], 0), total) : s * T) / K + s;
 }
-// Sequence and segment of a slot, by all threads of the block together (sequence
-// -1: none).  With one segment to a sequence a slot is a sequence.
+// Sequence and segment of a slot, found by every warp for itself (sequence -1:
+// none).  With one segment to a sequence a slot is a sequence.
 __device__ __forceinline__ int2 find_segment(const int* cu, int n_seqs, int T, int total, int seg_chunks, int nseg,
                                              int slot) {
   if (nseg == 1) return make_int2(slot, 0);
-  __shared__ int2 found;
-  if (threadIdx.x == 0) found = make_int2(-1, 0);
-  __syncthreads();
-  const int K = seg_chunks * CH;
-  for (int s = threadIdx.x; s < n_seqs; s += blockDim.x) {
-    const int a = first_slot(cu, s, T, total, K);
-    if (slot >= a && slot < first_slot(cu, s + 1, T, total, K)) found = make_int2(s, slot - a);
+  const int K = seg_chunks * CH, lane = threadIdx.x & 31;
+  for (int s0 = 0; s0 < n_seqs; s0 += 32) {
+    const int s = min(s0 + lane, n_seqs - 1), a = first_slot(cu, s, T, total, K);
+    const unsigned m = __ballot_sync(0xffffffffu, slot >= a && slot < first_slot(cu, s + 1, T, total, K));
+    if (m) {
+      const int l = __ffs((int)m) - 1;
+      return make_int2(min(s0 + l, n_seqs - 1), slot - __shfl_sync(0xffffffffu, a, l));
+    }
   }
-  __syncthreads();
-  return found;
+  return make_int2(-1, 0);
 }
+
+// The states of segments lie in the workspace so that lanes with consecutive rows
+// touch consecutive addresses: float4 (row r, columns 4 g .. 4 g + 3) at g * 128 + r.
+__device__ __forceinline__ int seg_index(int r, int c) { return ((c >> 2) * HD + r) * 4 + (c & 3); }
 
 // Rows of an SW128 tile scaled by f and split into TERMS bf16 terms, the first in
 // place, the others in the tiles at `rest`; this thread's row r, 16-byte chunks
@@ -95,7 +99,8 @@ __device__ __forceinline__ int2 find_segment(const int* cu, int n_seqs, int T, i
 // the fp32 product per term, at a permute, two ands and a subtraction per pair.
 // A row that is not `valid` (past the sequence's end) becomes zero, whatever it
 // holds.
-template <int TERMS>
+// The tiles at `rest` have REST_ROWS rows (64: one for both halves of the tile).
+template <int TERMS, int REST_ROWS>
 __device__ __forceinline__ void scale_row(unsigned char* tile, unsigned char* rest, int r, int j, float f, bool valid) {
   const uint32_t keep = valid ? 0xffffffffu : 0u;
   {
@@ -121,7 +126,9 @@ __device__ __forceinline__ void scale_row(unsigned char* tile, unsigned char* re
       }
 #pragma unroll
       for (int t = 0; t < TERMS; ++t)
-        *reinterpret_cast<uint4*>((t == 0 ? tile : rest + (t - 1) * TILE) + off) =
+        *reinterpret_cast<uint4*>(t == 0 ? tile + off
+                                         : rest + (t - 1) * REST_ROWS * 256 +
+                                               tc::sw128_chunk(r & (REST_ROWS - 1), j + c, REST_ROWS)) =
             make_uint4(o[t][0], o[t][1], o[t][2], o[t][3]);
     }
   }
@@ -138,40 +145,97 @@ __device__ __forceinline__ void load_tile(unsigned char* dst, const CUtensorMap*
 }
 
 // ---- the chunk walk ----------------------------------------------------------------
-// TERMS: bf16 terms of the scaled B rows.  Two leave an error of some 1e-5 in the
-// state, far below the rounding of the output's operands; a final state that is
-// returned in fp32 takes three, at a ring slot's cost.
-template <int TERMS>
+// Room for the further terms of the scaled B rows.  Two terms leave an error of
+// some 1e-5 in the state, far below the rounding of the output's operands; a
+// final state that is returned in fp32 takes three, whose two further tiles
+// hold 64 rows at a time (the second half waits for the first one's products:
+// 0.35 us of a chunk, where a ring slot less cost 1.5).
+constexpr int NSLOT = 5;
 struct WalkSmem {
-  static constexpr int NSLOT = 7 - TERMS;
   unsigned char slot[NSLOT][TILE];
-  unsigned char rest[TERMS - 1][TILE];  // further terms of the scaled B rows
+  unsigned char rest[TILE];
   unsigned char X[TILE];                // the entering state in bf16, [128 (b) rows x 128 (c)]
   alignas(16) float tab[CH];            // e^{w d}
   uint64_t full[NSLOT], empty[NSLOT];
-  uint64_t barP, barPm, barK[2], barS, barX, barO, barOf, barSt;
+  uint64_t barP, barPm, barK[2], barH, barS, barX, barO, barOf, barSt;
   uint32_t tmem;
 };
 
+// Row r, columns c0 .. c0 + 31 of the state that the walk begins with, by the state's
+// 256 threads together (c0 of a thread: its half's 0 or 32).  Rows of a caller's
+// state go through shared memory (`stage`, 32 KiB), so that a warp reads whole
+// lines of it.
+__device__ __forceinline__ void first_state(const DecayRole& R, unsigned char* stage, const float* x0, int r, int c0,
+                                            float (&v)[32]) {
+  if (!x0) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = 0.f;
+  } else if (R.xseg && !R.xt) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+      const float4 f = *reinterpret_cast<const float4*>(x0 + seg_index(r, c0 + i));
+      v[i] = f.x;
+      v[i + 1] = f.y;
+      v[i + 2] = f.z;
+      v[i + 3] = f.w;
+    }
+  } else if (R.xt) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = x0[R.xseg ? seg_index(c0 + i, r) : (c0 + i) * HD + r];
+  } else {
+    // columns c, c + 64 of the pass (c = 0 .. 31, or 32 .. 63): 128 rows x 2 x 128 bytes
+    const int t = threadIdx.x & 255, cc = c0 & 63;
+    float4 f[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int i = t + 256 * k, row = i >> 4, p = i & 15;  // 16-byte piece p of the row's two
+      f[k] = *reinterpret_cast<const float4*>(x0 + row * HD + (p >> 3) * 64 + cc + 4 * (p & 7));
+    }
+    asm volatile("bar.sync 2, 256;" ::: "memory");  // (the pass before has been read)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int i = t + 256 * k, row = i >> 4, p = i & 15;
+      *reinterpret_cast<float4*>(stage + row * 256 + ((p ^ (row & 7)) << 4)) = f[k];
+    }
+    asm volatile("bar.sync 2, 256;" ::: "memory");
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int p = 8 * (c0 >> 6) + k;
+      const float4 x = *reinterpret_cast<const float4*>(stage + r * 256 + ((p ^ (r & 7)) << 4));
+      v[4 * k] = x.x;
+      v[4 * k + 1] = x.y;
+      v[4 * k + 2] = x.z;
+      v[4 * k + 3] = x.w;
+    }
+  }
+}
+
 // One CTA's walk over the chunks [cb, ce) of head hd in sequence s (rows q); REV: backwards.
-template <int TERMS, bool REV>
-__device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, WalkSmem<TERMS>& sm, const Range q, int s,
+template <int TERMS, bool SUM, bool REV>
+__device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, WalkSmem& sm, const Range q, int s,
                                      int slot_id, int hd, int cb, int ce, int nch) {
-  constexpr int NSLOT = WalkSmem<TERMS>::NSLOT;
   const int tid = threadIdx.x, lane = tid & 31, warp = tc::warp_index();
-  const int G = a.Hv / a.Hk, loops = R.shared ? G : 1, nc = ce - cb;
+  const int G = a.Hv / a.Hk, loops = SUM ? G : 1, nc = ce - cb;
   const int n_it = loops * nc;
   auto chunk_of = [&](int it) { return REV ? ce - 1 - it % nc : cb + it % nc; };
-  auto head_of = [&](int it) { return R.shared ? hd * G + it / nc : hd; };  // value head
+  auto head_of = [&](int it) { return SUM ? hd * G + it / nc : hd; };  // value head
   auto rows_of = [&](int c) { return min(CH, q.len - c * CH); };
 
-  if (tid == 0) {
+  auto load = [&](int t) {  // tile t (a, b, c of every chunk) into its slot
+    const int it = t / 3, kind = t % 3, row = q.start + chunk_of(it) * CH, j = head_of(it);
+    const CUtensorMap* m = kind == 0 ? &R.a : kind == 1 ? &R.b : &R.c;
+    const int per_v = kind == 0 ? R.ha : kind == 1 ? R.hb : R.hc;
+    load_tile(sm.slot[t % NSLOT], m, per_v ? j : j / G, row, &sm.full[t % NSLOT]);
+  };
+  const int nt = 3 * n_it;
+  if (warp == 17 && lane == 0) {
     for (int k = 0; k < NSLOT; ++k) {
       tc::mbar_init(&sm.full[k], 1);
       tc::mbar_init(&sm.empty[k], 1);
     }
     tc::mbar_init(&sm.barP, 1);
     tc::mbar_init(&sm.barX, 1);
+    tc::mbar_init(&sm.barH, 1);
     tc::mbar_init(&sm.barO, 1);
     tc::mbar_init(&sm.barPm, 256);
     tc::mbar_init(&sm.barK[0], 256);
@@ -180,6 +244,10 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
     tc::mbar_init(&sm.barOf, 256);
     tc::mbar_init(&sm.barSt, 256);
     tc::mbar_fence_init();
+    // The first tiles are requested at once.  After the prefix kernel q, k, v and dO
+    // are complete already: it starts no dependent before its own wait is over,
+    // and that is for the fold, which read them.
+    for (int t = 0; t < min(nt, NSLOT); ++t) load(t);
   }
   if (warp == 0) tc::alloc(&sm.tmem, 512);
   tc::fence_before();
@@ -211,15 +279,9 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
     }
   } else if (warp == 17) {  // ---- TMA: tiles a, b, c of every chunk, in the order consumed
     if (lane == 0) {
-      const int nt = 3 * n_it;
-      for (int t = 0; t < nt && w.ok; ++t) {
-        const int k = t % NSLOT, it = t / 3, kind = t % 3, row = q.start + chunk_of(it) * CH;
-        if (t >= NSLOT) w.on(&sm.empty[k], (t / NSLOT - 1));
-        if (!w.ok) break;
-        const int j = head_of(it), jk = j / G;
-        const CUtensorMap* m = kind == 0 ? &R.a : kind == 1 ? &R.b : &R.c;
-        const int per_v = kind == 0 ? R.ha : kind == 1 ? R.hb : R.hc;
-        load_tile(sm.slot[k], m, per_v ? j : jk, row, &sm.full[k]);
+      for (int t = NSLOT; t < nt && w.ok; ++t) {
+        w.on(&sm.empty[t % NSLOT], t / NSLOT - 1);
+        if (w.ok) load(t);
       }
       // no copy is in flight when the CTA ends
       if (w.ok)
@@ -229,7 +291,6 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
     }
   } else if (warp == 16) {  // ---- products
     const uint32_t lead = tc::elect_leader();
-    const int nt = 3 * n_it;
     auto slot = [&](int t) { return smem_u32(sm.slot[t % NSLOT]); };
     auto arrived = [&](int t) { w.warp_on(&sm.full[t % NSLOT], t / NSLOT); };
     auto release = [&](int t) {
@@ -256,8 +317,13 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
         tc::fence_after();
         const uint32_t c = slot(tcc) + 8192 * h;
         tc::gemm_rows64_by(lead, tX, slot(tb) + 8192 * h, c, true);
-#pragma unroll
-        for (int t = 0; t < TERMS - 1; ++t) tc::gemm_rows64_by(lead, tX, smem_u32(sm.rest[t]) + 8192 * h, c, true);
+        if (TERMS == 2) {
+          tc::gemm_rows64_by(lead, tX, smem_u32(sm.rest) + 8192 * h, c, true);
+        } else {
+          tc::gemm_rows64_by<64>(lead, tX, smem_u32(sm.rest), c, true);
+          tc::gemm_rows64_by<64>(lead, tX, smem_u32(sm.rest) + TILE / 2, c, true);
+          if (h == 0) tc::commit_by(lead, &sm.barH);
+        }
       }
       tc::commit_by(lead, &sm.barX);
       release(tb);
@@ -279,62 +345,86 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
       auto output = [&](int it) {
         const int c = chunk_of(it), n = rows_of(c);
         const float f = expf(wd * (float)(REV ? max(n - 1 - r, 0) : r + 1));
-        const bool sum = loops > 1, firsth = it < nc, lasth = it >= n_it - nc;
+        const bool tile = whole(it);
         const long row = (long)q.start + (long)c * CH + r;
         bf16* dst = R.out + (row * Ho + hd) * HD + 64 * half;
-        // running sums over the value heads, [head][4-column group][row]: this thread's own
-        float4* acc = sum ? reinterpret_cast<float4*>(R.acc) + ((long)hd * 32 + 16 * half) * a.total + row : nullptr;
-        w.warp_on(&sm.barO, it);
-        tc::fence_after();
+        unsigned char* staged = sm.slot[(3 * it + 2) % NSLOT];
+        auto put = [&](int j, const float* x) {  // columns 8 j .. 8 j + 7 of the half
+          const uint4 o = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                                     pack_bf16(x[6], x[7]));
+          if (tile)
+            *reinterpret_cast<uint4*>(staged + tc::sw128_chunk(r, 8 * half + j, CH)) = o;
+          else if (r < n)
+            *reinterpret_cast<uint4*>(dst + 8 * j) = o;
+        };
+        if constexpr (!SUM) {
+          w.warp_on(&sm.barO, it);
+          tc::fence_after();
 #pragma unroll 1
-        for (int g = 0; g < 2; ++g) {
-          float x[32], y[32];
-          tc::ld32(tO1 + cols + 32 * g, x);
-          tc::ld32(tO2 + cols + 32 * g, y);
-          if (g == 1) {
-            tc::fence_before();
-            tc::mbar_arrive(&sm.barOf);
-          }
-#pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = f * x[i] + y[i];
-          if (sum && !firsth && r < n) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float4 p = acc[(long)(8 * g + i) * a.total];
-              x[4 * i] += p.x;
-              x[4 * i + 1] += p.y;
-              x[4 * i + 2] += p.z;
-              x[4 * i + 3] += p.w;
+          for (int g = 0; g < 2; ++g) {
+            float x[32], y[32];
+            tc::ld32(tO1 + cols + 32 * g, x);
+            tc::ld32(tO2 + cols + 32 * g, y);
+            if (g == 1) {
+              tc::fence_before();
+              tc::mbar_arrive(&sm.barOf);
             }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = f * x[i] + y[i];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) put(4 * g + i, x + 8 * i);
+            __syncwarp();
           }
-          if (whole(it)) {
-            unsigned char* tile = sm.slot[(3 * it + 2) % NSLOT];
+        } else {
+          // running sums over the value heads, [head][4-column group][row], this thread's
+          // own; 32 columns of them are requested before the products are waited for
+          const bool add = it >= nc && r < n, last = it >= n_it - nc;
+          float4* acc = reinterpret_cast<float4*>(R.acc) + ((long)hd * 32 + 16 * half) * a.total + row;
+          float4 p[8];
+          auto request = [&](int g) {
+            if (add) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint4 o;
-              o.x = pack_bf16(x[8 * i], x[8 * i + 1]);
-              o.y = pack_bf16(x[8 * i + 2], x[8 * i + 3]);
-              o.z = pack_bf16(x[8 * i + 4], x[8 * i + 5]);
-              o.w = pack_bf16(x[8 * i + 6], x[8 * i + 7]);
-              *reinterpret_cast<uint4*>(tile + tc::sw128_chunk(r, 8 * half + 4 * g + i, CH)) = o;
+              for (int i = 0; i < 8; ++i) p[i] = acc[(long)(8 * g + i) * a.total];
             }
-          } else if (r >= n) {
-          } else if (sum && !lasth) {
+          };
+          request(0);
+          w.warp_on(&sm.barO, it);
+          tc::fence_after();
+#pragma unroll 1
+          for (int g = 0; g < 2; ++g) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              acc[(long)(8 * g + i) * a.total] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-          } else {
+            for (int h = 0; h < 2; ++h) {
+              float x[16], y[16];
+              tc::ld16(tO1 + cols + 32 * g + 16 * h, x);
+              tc::ld16(tO2 + cols + 32 * g + 16 * h, y);
+              if (g == 1 && h == 1) {
+                tc::fence_before();
+                tc::mbar_arrive(&sm.barOf);
+              }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint4 o;
-              o.x = pack_bf16(x[8 * i], x[8 * i + 1]);
-              o.y = pack_bf16(x[8 * i + 2], x[8 * i + 3]);
-              o.z = pack_bf16(x[8 * i + 4], x[8 * i + 5]);
-              o.w = pack_bf16(x[8 * i + 6], x[8 * i + 7]);
-              *reinterpret_cast<uint4*>(dst + 32 * g + 8 * i) = o;
+              for (int i = 0; i < 16; ++i) x[i] = f * x[i] + y[i];
+              if (add) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  x[4 * i] += p[4 * h + i].x;
+                  x[4 * i + 1] += p[4 * h + i].y;
+                  x[4 * i + 2] += p[4 * h + i].z;
+                  x[4 * i + 3] += p[4 * h + i].w;
+                }
+              }
+              if (last) {
+                put(4 * g + 2 * h, x);
+                put(4 * g + 2 * h + 1, x + 8);
+              } else if (r < n) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  acc[(long)(8 * g + 4 * h + i) * a.total] =
+                      make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+              }
+              __syncwarp();
             }
+            if (g == 0) request(1);
           }
-          __syncwarp();
         }
         tc::fence_proxy_async();
         tc::mbar_arrive(&sm.barSt);
@@ -404,6 +494,10 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
           const long sh = (long)s * a.Hv + j;
           wd = a.decay[j];
           x0 = R.xseg ? R.xseg + ((long)slot_id * a.Hv + j) * HD * HD : (R.x0 ? R.x0 + sh * HD * HD : nullptr);
+          if (it == 0 && a.nseg > 1 && !a.beside) {  // the entering states come from the kernel before
+            pdl_wait();
+            pdl_release();
+          }
         }
         keep = expf(wd * (float)n);
         // ---- the state: bf16 image of X, X <- e^{w n} X
@@ -411,28 +505,20 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
           w.warp_on(&sm.barX, it - 1);
           tc::fence_after();
         }
+        if (first) {
+#pragma unroll 1
+          for (int g = 0; g < 2; ++g) {
+            float v[32];
+            first_state(R, sm.rest, x0, r, 64 * half + 32 * g, v);
+            tc::st32(tX + cols + 32 * g, v);
+          }
+          tc::wait_st();
+          asm volatile("bar.sync 2, 256;" ::: "memory");  // (the staged state has been read)
+        }
 #pragma unroll 1
         for (int g = 0; g < 2; ++g) {
-          const int c0 = 64 * half + 32 * g;
           float v[32];
-          if (!first) {
-            tc::ld32(tX + cols + 32 * g, v);
-          } else if (!x0) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0.f;
-          } else if (R.xt) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = x0[(c0 + i) * HD + r];
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float4 f = *reinterpret_cast<const float4*>(x0 + r * HD + c0 + 4 * i);
-              v[4 * i] = f.x;
-              v[4 * i + 1] = f.y;
-              v[4 * i + 2] = f.z;
-              v[4 * i + 3] = f.w;
-            }
-          }
+          tc::ld32(tX + cols + 32 * g, v);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint4 o;
@@ -459,7 +545,8 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
         for (int h = 0; h < 2; ++h) {  // 64 rows at a time, four threads to a row
           const int i = 64 * h + (tid & 63), j = 4 * ((tid >> 6) & 3);
           const float e = expf(wd * (float)(REV ? i + 1 : max(n - 1 - i, 0)));
-          scale_row<TERMS>(sm.slot[tb % NSLOT], sm.rest[0], i, j, e, i < n);
+          if (TERMS == 3 && h == 1) w.warp_on(&sm.barH, it);  // (the first half's further terms have been read)
+          scale_row<TERMS, TERMS == 2 ? CH : 64>(sm.slot[tb % NSLOT], sm.rest, i, j, e, i < n);
           if (i >= n) zero_row(sm.slot[tcc % NSLOT], i, j, 4);
           tc::fence_proxy_async();
           tc::mbar_arrive(&sm.barK[h]);
@@ -489,14 +576,14 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
   if (warp == 0) tc::dealloc(sm.tmem, 512);
 }
 
-template <int TERMS>
-__global__ void __launch_bounds__(WALK_THREADS, 1) k_decay(const __grid_constant__ DecayArgs a) {
-  extern __shared__ unsigned char raw[];
-  WalkSmem<TERMS>& sm = *reinterpret_cast<WalkSmem<TERMS>*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
+template <int TERMS, bool SUM>
+__device__ __forceinline__ void walk_block(const DecayArgs& a, WalkSmem& sm) {
   const int tid = threadIdx.x;
-  pdl_wait();
-  pdl_release();
-  if (a.nseg == 1) clear_status(a.status);
+  if (a.nseg == 1 && !a.beside) {  // (with segments, only the entering states wait for the kernel before)
+    pdl_wait();
+    pdl_release();
+    clear_status(a.status);
+  }
 
   // pass, then segment, sequence and head of this CTA
   int u = blockIdx.x, ri = 0;
@@ -522,9 +609,18 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) k_decay(const __grid_constant
     return;
   }
   if (R.rev)
-    walk<TERMS, true>(a, R, sm, q, s, slot, hd, cb, ce, nch);
+    walk<TERMS, SUM, true>(a, R, sm, q, s, slot, hd, cb, ce, nch);
   else
-    walk<TERMS, false>(a, R, sm, q, s, slot, hd, cb, ce, nch);
+    walk<TERMS, SUM, false>(a, R, sm, q, s, slot, hd, cb, ce, nch);
+}
+
+// TERMS = 3 where final states are returned in fp32; SUM: an output head is the sum
+// over a group's value heads.
+template <int TERMS, bool SUM>
+__global__ void __launch_bounds__(WALK_THREADS, 1) k_decay(const __grid_constant__ DecayArgs a) {
+  extern __shared__ unsigned char raw[];
+  walk_block<TERMS, SUM>(a, *reinterpret_cast<WalkSmem*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u)));
+  if (blockIdx.x == 0) pdl_wait();  // the grid ends after the one before it, whatever its CTAs had to do
 }
 
 // ---- segments ----------------------------------------------------------------------
@@ -557,7 +653,12 @@ __global__ void __launch_bounds__(FOLD_THREADS, 1) k_decay_fold(const __grid_con
   if (!R.last && (R.rev ? cb == 0 : ce == nch)) return;
   const int end = min(q.len, ce * CH);  // one past the segment's last token
 
-  if (tid == 0) {
+  auto load = [&](int t) {
+    load_tile(sm.slot[t % FOLD_SLOTS], (t & 1) ? &R.c : &R.b, (t & 1) ? j : j / G, q.start + (cb + t / 2) * CH,
+              &sm.full[t % FOLD_SLOTS]);
+  };
+  const int nt = 2 * nc;
+  if (warp == 9 && lane == 0) {
     for (int k = 0; k < FOLD_SLOTS; ++k) {
       tc::mbar_init(&sm.full[k], 1);
       tc::mbar_init(&sm.empty[k], 1);
@@ -567,6 +668,7 @@ __global__ void __launch_bounds__(FOLD_THREADS, 1) k_decay_fold(const __grid_con
       tc::mbar_init(&sm.barM[h], 1);
     }
     tc::mbar_fence_init();
+    for (int t = 0; t < min(nt, FOLD_SLOTS); ++t) load(t);
   }
   if (warp == 0) tc::alloc(&sm.tmem, 128);
   tc::fence_before();
@@ -576,12 +678,9 @@ __global__ void __launch_bounds__(FOLD_THREADS, 1) k_decay_fold(const __grid_con
   tc::Wait w;
   if (warp == 9) {
     if (lane == 0) {
-      const int nt = 2 * nc;
-      for (int t = 0; t < nt && w.ok; ++t) {
-        const int k = t % FOLD_SLOTS;
-        if (t >= FOLD_SLOTS) w.on(&sm.empty[k], t / FOLD_SLOTS - 1);
-        if (!w.ok) break;
-        load_tile(sm.slot[k], (t & 1) ? &R.c : &R.b, (t & 1) ? j : j / G, q.start + (cb + t / 2) * CH, &sm.full[k]);
+      for (int t = FOLD_SLOTS; t < nt && w.ok; ++t) {
+        w.on(&sm.empty[t % FOLD_SLOTS], t / FOLD_SLOTS - 1);
+        if (w.ok) load(t);
       }
       if (w.ok)
         for (int t = max(0, nt - FOLD_SLOTS); t < nt; ++t) w.on(&sm.full[t % FOLD_SLOTS], t / FOLD_SLOTS);
@@ -622,7 +721,7 @@ __global__ void __launch_bounds__(FOLD_THREADS, 1) k_decay_fold(const __grid_con
         // weight to the segment's end (forwards) or to its start (backwards)
         const float e = expf(wd * (float)(R.rev ? t0 - cb * CH + 1 : max(end - 1 - t0, 0)));
         if (i > 0) w.warp_on(&sm.barM[h], i - 1);  // (these rows' further terms have been read)
-        scale_row<FOLD_TERMS>(sm.slot[tb % FOLD_SLOTS], sm.rest[0], r, j0, e, r < n);
+        scale_row<FOLD_TERMS, CH>(sm.slot[tb % FOLD_SLOTS], sm.rest[0], r, j0, e, r < n);
         if (r >= n) zero_row(sm.slot[tcc % FOLD_SLOTS], r, j0, 4);
         tc::fence_proxy_async();
         tc::mbar_arrive(&sm.barK[h]);
@@ -632,14 +731,14 @@ __global__ void __launch_bounds__(FOLD_THREADS, 1) k_decay_fold(const __grid_con
     tc::fence_after();
     const int row = 32 * (warp & 3) + lane, g0 = 2 * (warp >> 2);
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
-    float* dst = R.x + ((long)slot * a.Hv + j) * HD * HD + row * HD;
+    float* dst = R.x + ((long)slot * a.Hv + j) * HD * HD;
 #pragma unroll 1
     for (int g = g0; g < g0 + 2; ++g) {
       float v[32];
       tc::ld32(tX + lane_base + 32 * g, v);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        *reinterpret_cast<float4*>(dst + 32 * g + 4 * i) =
+        *reinterpret_cast<float4*>(dst + seg_index(row, 32 * g + 4 * i)) =
             make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
     }
     tc::fence_before();
@@ -660,10 +759,11 @@ __global__ void __launch_bounds__(256) k_decay_prefix(const __grid_constant__ De
   const Range q = seq_range(a.cu, s, a.T, a.total);
   const int nch = (q.len + CH - 1) / CH, nseg = (nch + a.seg_chunks - 1) / a.seg_chunks;
   const long sh = (long)s * a.Hv + j;
-  const int e = 4 * (blockIdx.y * 256 + threadIdx.x);  // 16 blocks cover the state
+  const int e = 4 * (blockIdx.y * 256 + threadIdx.x);  // 16 blocks cover the state, in the segments' order
+  const int e0 = ((e >> 2) & (HD - 1)) * HD + 4 * (e >> 9);  // the same place in a caller's state
   const float wd = a.decay[j];
   const int slot0 = first_slot(a.cu, s, a.T, a.total, a.seg_chunks * CH);
-  float4 run = R.x0 ? *reinterpret_cast<const float4*>(R.x0 + sh * HD * HD + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 run = R.x0 ? *reinterpret_cast<const float4*>(R.x0 + sh * HD * HD + e0) : make_float4(0.f, 0.f, 0.f, 0.f);
   constexpr int AHEAD = 4;  // loads in flight
   for (int i0 = 0; i0 < nseg; i0 += AHEAD) {
     float4 x[AHEAD];
@@ -685,7 +785,7 @@ __global__ void __launch_bounds__(256) k_decay_prefix(const __grid_constant__ De
       run = make_float4(keep * run.x + x[k].x, keep * run.y + x[k].y, keep * run.z + x[k].z, keep * run.w + x[k].w);
     }
   }
-  if (R.last) *reinterpret_cast<float4*>(R.last + sh * HD * HD + e) = run;
+  if (R.last) *reinterpret_cast<float4*>(R.last + sh * HD * HD + e0) = run;
 }
 
 template <typename K>
@@ -695,21 +795,21 @@ cudaError_t set_smem(K k, size_t bytes) {
 
 }  // namespace
 
-template <int TERMS>
+template <int TERMS, bool SUM>
 static cudaError_t launch_walk(const DecayArgs& a, cudaStream_t s) {
-  constexpr size_t smem = sizeof(WalkSmem<TERMS>) + 1024;
+  constexpr size_t smem = sizeof(WalkSmem) + 1024;
   static_assert(smem <= 227 * 1024, "shared memory");
-  cudaError_t e = set_smem(k_decay<TERMS>, smem);
+  cudaError_t e = set_smem(k_decay<TERMS, SUM>, smem);
   if (e != cudaSuccess) return e;
   long units = 0;
   for (int i = 0; i < a.n_roles; ++i) units += (long)a.slots * (a.role[i].shared ? a.Hk : a.Hv);
-  return launch_pdl(k_decay<TERMS>, dim3((unsigned)units), dim3(WALK_THREADS), smem, s, a);
+  return launch_pdl(k_decay<TERMS, SUM>, dim3((unsigned)units), dim3(WALK_THREADS), smem, s, a);
 }
 
 cudaError_t launch_decay(const DecayArgs& a, cudaStream_t s) {
-  bool last = false;
-  for (int i = 0; i < a.n_roles; ++i) last = last || a.role[i].xT;
-  return last ? launch_walk<3>(a, s) : launch_walk<2>(a, s);
+  const bool sum = a.Hv > a.Hk && a.role[0].shared;
+  if (a.role[0].xT) return launch_walk<3, false>(a, s);
+  return sum ? launch_walk<2, true>(a, s) : launch_walk<2, false>(a, s);
 }
 
 cudaError_t launch_decay_fold(const DecayFoldArgs& a, cudaStream_t s) {

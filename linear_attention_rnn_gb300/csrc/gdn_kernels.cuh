@@ -177,6 +177,7 @@ struct DecayArgs {
   int n_roles, n_seqs, total, T, Hk, Hv;
   int nseg, seg_chunks;  // most segments of a sequence, chunks to a segment
   int slots;             // segment slots: n_seqs with nseg = 1, else total / (128 seg_chunks) + n_seqs
+  int beside;            // the launch before it is another walk of the same call, which it need not wait for
 };
 struct DecayFoldRole {
   CUtensorMap b, c;    // b: shared heads, c: value heads
@@ -262,6 +263,7 @@ cudaError_t launch_out_gate(const bf16* o, const bf16* z, bf16* y, long rows, cu
 cudaError_t launch_out_gate_bwd(const bf16* o, const bf16* z, const bf16* dy, bf16* dO, bf16* dz, long rows,
                                 cudaStream_t s);
 cudaError_t launch_step(const StepArgs& a, cudaStream_t s);
+// (all roles shared, or none; a final state in the first role or in none)
 cudaError_t launch_decay(const DecayArgs& a, cudaStream_t s);
 // the segments' own states and the prefix over them (two launches)
 cudaError_t launch_decay_fold(const DecayFoldArgs& a, cudaStream_t s);

@@ -39,11 +39,19 @@ struct DecayPlan {
   size_t status, xf, xr, accq, acck, total;
 };
 
-// Segments.  One CTA walks a segment of a head; without segments a call keeps
-// n_seqs Hv of them busy, for as long as the longest sequence takes.  With
-// segments each chunk of k and v is read twice (the fold) and two more kernels
-// start.  The estimate, in chunks of the walk: rounds of CTAs over the SMs, a
-// start of 2 per CTA, a fold at half a chunk's time, 4 for the two launches.
+// Segments.  One CTA walks a segment of a head (of a group's heads one behind
+// another for dq and dk); without segments a call takes as long as its longest
+// sequence however few CTAs there are.  With segments k and v (q and dO) are read
+// twice, and two more kernels start.  The estimate, in chunks of the walk (2.7 us
+// measured): equal CTAs run in rounds over the SMs, CTAs of mixed lengths take
+// their average and a part of the longest one's; a CTA starts in 1.5, the fold
+// takes half a chunk's time, the two launches together 4.
+double decay_rounds(double ctas, double longest, double sms, bool mixed) {
+  if (ctas <= sms) return longest;
+  if (mixed) return ctas * longest / sms + 0.3 * longest;
+  return (double)(long)((ctas + sms - 1.0) / sms) * longest;
+}
+
 DecayPlan decay_plan(int backward, int n_seqs, int total, int max_seqlen, int Hk, int Hv) {
   DecayPlan p;
   memset(&p, 0, sizeof p);
@@ -51,17 +59,19 @@ DecayPlan decay_plan(int backward, int n_seqs, int total, int max_seqlen, int Hk
   const long nch = (longest + CH - 1) / CH;
   p.nseg = 1;
   p.seg_chunks = nch > 0 ? (int)nch : 1;
-  const double sms = sm_count();
-  // sequences that are about as long as the longest one
-  const double full = nch > 0 ? (double)total / (double)(longest > 0 ? longest : 1) : 1.0;
-  const double heads = (full < 1.0 ? 1.0 : full) * Hv * (backward ? 3.0 : 1.0);
+  const double sms = sm_count(), G = (double)Hv / Hk;
+  const double all = (double)total / CH + 0.5 * n_seqs;  // chunks of all sequences
   double best = 1e300;
   for (long k = 1; k <= nch && k <= 128; ++k) {
-    const long L = (nch + k - 1) / k;
-    const long segs = (nch + L - 1) / L;
-    const double rounds = (double)(long)((heads * segs + sms - 1.0) / sms);
-    double t = rounds * (L + 2.0);
-    if (segs > 1) t += rounds * (backward ? 0.67 : 1.0) * (0.5 * L + 1.0) + 4.0;
+    const double L = (double)((nch + k - 1) / k);
+    const long segs = (nch + (long)L - 1) / (long)L;
+    // segments that are as long as L
+    const double parts = n_seqs == 1 ? (double)segs : k == 1 ? all / L : all / L + 0.25 * (n_seqs - 1);
+    const bool mixed = n_seqs > 1 || backward;
+    // backward: Hv CTAs of a segment for dv, Hk that are G times as long for dq and for dk
+    double t = backward ? decay_rounds(parts * 3.0 * Hk, G * L + 1.5, sms, mixed)
+                        : decay_rounds(parts * Hv, L + 1.5, sms, mixed);
+    if (segs > 1) t += decay_rounds(parts * Hv * (backward ? 2.0 : 1.0), 0.5 * L + 1.5, sms, mixed) + 4.0;
     if (t < best * 0.97) {
       best = t;
       p.nseg = (int)segs;
@@ -338,15 +348,16 @@ int gdn_decay_bwd(const void* q, const void* k, const void* v, const float* deca
   a.nseg = p.nseg;
   a.seg_chunks = p.seg_chunks;
   a.slots = p.slots;
-  a.n_roles = 3;
+  a.n_roles = 2;
   CUtensorMap mq, mk, mv, md;
   if (!tmap_rows(&mq, q, total, Hk, HD, (uint64_t)q_stride * 2, 1, CH) ||
       !tmap_rows(&mk, k, total, Hk, HD, (uint64_t)k_stride * 2, 1, CH) ||
       !tmap_rows(&mv, v, total, Hv, HD, (uint64_t)v_stride * 2, 1, CH) ||
       !tmap_rows(&md, dO, total, Hv, HD, (uint64_t)Hv * HD * 2, 1, CH))
     return GDN_ERR_CUDA;
-  // the longest CTAs first: dq and dk walk a group's value heads one behind another
-  DecayRole &rq = a.role[0], &rk = a.role[1], &rv = a.role[2];
+  // dq and dk, whose CTAs walk a group's value heads one behind another, then dv beside them
+  DecayArgs b = a;
+  DecayRole &rq = a.role[0], &rk = a.role[1], &rv = b.role[0];
   rq.a = md, rq.b = mv, rq.c = mk;
   rq.ha = rq.hb = 1;
   rq.xt = 1;
@@ -402,7 +413,10 @@ int gdn_decay_bwd(const void* q, const void* k, const void* v, const float* deca
   } else {
     rv.xT = dh0;
   }
-  return cuda_status(launch_decay(a, s));
+  if ((rc = cuda_status(launch_decay(a, s)))) return rc;
+  b.n_roles = 1;
+  b.beside = 1;
+  return cuda_status(launch_decay(b, s));
 }
 
 size_t gdn_attn_workspace_bytes(int backward, int n_seqs, int total_q, int total_k, int max_k, int Hq, int Hk,
