@@ -102,35 +102,38 @@ __device__ __forceinline__ int seg_index(int r, int c) { return ((c >> 2) * HD +
 // The tiles at `rest` have REST_ROWS rows (64: one for both halves of the tile).
 template <int TERMS, int REST_ROWS>
 __device__ __forceinline__ void scale_row(unsigned char* tile, unsigned char* rest, int r, int j, float f, bool valid) {
-  const uint32_t keep = valid ? 0xffffffffu : 0u;
-  {
-    uint4 u[4];  // four loads in flight
+  uint4 u[4];  // four loads in flight
 #pragma unroll
-    for (int c = 0; c < 4; ++c) u[c] = *reinterpret_cast<const uint4*>(tile + tc::sw128_chunk(r, j + c, CH));
+  for (int c = 0; c < 4; ++c) u[c] = *reinterpret_cast<const uint4*>(tile + tc::sw128_chunk(r, j + c, CH));
+  if (!valid) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const uint32_t off = tc::sw128_chunk(r, j + c, CH);
-      const uint32_t up[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
-      uint32_t o[TERMS][4];
+    for (int c = 0; c < 4; ++c) u[c] = make_uint4(0u, 0u, 0u, 0u);
+  }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t w = up[i] & keep;
-        float x = f * __uint_as_float(w << 16), y = f * __uint_as_float(w & 0xffff0000u);
+  for (int c = 0; c < 4; ++c) {
+    const uint32_t up[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
+    uint32_t o[TERMS][4];
 #pragma unroll
-        for (int t = 0; t < TERMS - 1; ++t) {
-          o[t][i] = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
-          x -= __uint_as_float(__float_as_uint(x) & 0xffff0000u);
-          y -= __uint_as_float(__float_as_uint(y) & 0xffff0000u);
-        }
-        o[TERMS - 1][i] = pack_bf16(x, y);
+    for (int i = 0; i < 4; ++i) {
+      float x = __uint_as_float(up[i] << 16), y = __uint_as_float(up[i] & 0xffff0000u);
+      tc::mul2(x, y, f, f);
+#pragma unroll
+      for (int t = 0; t < TERMS - 1; ++t) {
+        o[t][i] = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+        float hx = __uint_as_float(__float_as_uint(x) & 0xffff0000u);
+        float hy = __uint_as_float(__float_as_uint(y) & 0xffff0000u);
+        tc::axpy2(hx, hy, -1.f, x, y);
+        x = hx;
+        y = hy;
       }
-#pragma unroll
-      for (int t = 0; t < TERMS; ++t)
-        *reinterpret_cast<uint4*>(t == 0 ? tile + off
-                                         : rest + (t - 1) * REST_ROWS * 256 +
-                                               tc::sw128_chunk(r & (REST_ROWS - 1), j + c, REST_ROWS)) =
-            make_uint4(o[t][0], o[t][1], o[t][2], o[t][3]);
+      o[TERMS - 1][i] = pack_bf16(x, y);
     }
+#pragma unroll
+    for (int t = 0; t < TERMS; ++t)
+      *reinterpret_cast<uint4*>(t == 0 ? tile + tc::sw128_chunk(r, j + c, CH)
+                                       : rest + (t - 1) * REST_ROWS * 256 +
+                                             tc::sw128_chunk(r & (REST_ROWS - 1), j + c, REST_ROWS)) =
+          make_uint4(o[t][0], o[t][1], o[t][2], o[t][3]);
   }
 }
 __device__ __forceinline__ void zero_row(unsigned char* tile, int r, int j0, int nj) {
@@ -370,7 +373,7 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
               tc::mbar_arrive(&sm.barOf);
             }
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = f * x[i] + y[i];
+            for (int i = 0; i < 32; i += 2) tc::axpy2(x[i], x[i + 1], f, y[i], y[i + 1]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) put(4 * g + i, x + 8 * i);
             __syncwarp();
@@ -402,7 +405,7 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
                 tc::mbar_arrive(&sm.barOf);
               }
 #pragma unroll
-              for (int i = 0; i < 16; ++i) x[i] = f * x[i] + y[i];
+              for (int i = 0; i < 16; i += 2) tc::axpy2(x[i], x[i + 1], f, y[i], y[i + 1]);
               if (add) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -465,10 +468,10 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
 #pragma unroll
               for (int i = 0; i < 16; i += 4) {
                 const float4 f = *reinterpret_cast<const float4*>(t + (REV ? i : 12 - i));
-                v[i] *= edge * (REV ? f.x : f.w);
-                v[i + 1] *= edge * (REV ? f.y : f.z);
-                v[i + 2] *= edge * (REV ? f.z : f.y);
-                v[i + 3] *= edge * (REV ? f.w : f.x);
+                tc::mul2(v[i], v[i + 1], edge, edge);
+                tc::mul2(v[i + 2], v[i + 3], edge, edge);
+                tc::mul2(v[i], v[i + 1], REV ? f.x : f.w, REV ? f.y : f.z);
+                tc::mul2(v[i + 2], v[i + 3], REV ? f.z : f.y, REV ? f.w : f.x);
               }
             }
             if (REV && j0 + 16 > n) {  // (forwards, rows of tokens see tokens only)
@@ -529,7 +532,7 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
             *reinterpret_cast<uint4*>(sm.X + tc::sw128_chunk(r, 8 * half + 4 * g + c, CH)) = o;
           }
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] *= keep;
+          for (int i = 0; i < 32; i += 2) tc::mul2(v[i], v[i + 1], keep, keep);
           tc::st32(tX + cols + 32 * g, v);
         }
         tc::wait_st();

@@ -540,6 +540,19 @@ __device__ __forceinline__ void add2(float& x, float& y, float a, float b) {  //
       : "+f"(x), "+f"(y)
       : "f"(a), "f"(b));
 }
+__device__ __forceinline__ void mul2(float& x, float& y, float a, float b) {  // x *= a, y *= b
+  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\t"
+      "mul.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}\n"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
+// x <- f x + a, y <- f y + b
+__device__ __forceinline__ void axpy2(float& x, float& y, float f, float a, float b) {
+  asm("{\n\t.reg .b64 p, q, r;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %2};\n\tmov.b64 r, {%3, %4};\n\t"
+      "fma.rn.f32x2 p, p, q, r;\n\tmov.b64 {%0, %1}, p;\n\t}\n"
+      : "+f"(x), "+f"(y)
+      : "f"(f), "f"(a), "f"(b));
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
