@@ -138,7 +138,7 @@ def _check(t, name, dtype, shape=None):
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and t.shape != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
@@ -374,9 +374,8 @@ def _check_rows(t, name, H, d, n=None):
     """bf16 rows [.., H, d] whose heads and columns are contiguous; the tokens may
     be further apart (a part of a wider buffer).  Returns the elements between
     tokens."""
-    if (t.dtype is torch.bfloat16 and t.is_cuda and t.is_contiguous() and t.dim() > 2
-            and t.shape[-2:] == (H, d) and (n is None or t.numel() == n * H * d)):
-        return H * d
+    if t.dtype is torch.bfloat16 and t.is_cuda and t.is_contiguous() and t.shape == (n, H, d):
+        return H * d  # (the usual case, at a third of what the checks below take)
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != torch.bfloat16:
@@ -407,23 +406,28 @@ def _step(name, q, k, v, gates, state, slots, o):
     if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
         raise ValueError("q, k, v must be [R, H, D]")
     R, Hk, dk = k.shape
-    Hv, dv = v.shape[1:]
-    strides = [_check_rows(q, "q", Hk, dk, R), _check_rows(k, "k", Hk, dk, R),
-               _check_rows(v, "v", Hv, dv, R)]
+    _, Hv, dv = v.shape
+    sq = _check_rows(q, "q", Hk, dk, R)
+    sk = _check_rows(k, "k", Hk, dk, R)
+    sv = _check_rows(v, "v", Hv, dv, R)
     if state.dim() != 4:
         raise ValueError("state must be [slots, Hv, d_k, d_v]")
-    _check(state, "state", torch.float32, (state.shape[0], Hv, dk, dv))
-    _check(slots, "slots", torch.int32, (R,))
-    if slots is None and state.shape[0] < R:
-        raise ValueError(f"{R} rows need as many states, got {state.shape[0]}")
+    n = state.shape[0]
+    _check(state, "state", torch.float32, (n, Hv, dk, dv))
+    if slots is not None:
+        _check(slots, "slots", torch.int32, (R,))
+        slots = slots.data_ptr()
+    elif n < R:
+        raise ValueError(f"{R} rows need as many states, got {n}")
     if o is None:
-        o = torch.empty((R, Hv, dv), dtype=torch.bfloat16, device=q.device)
-    _check(o, "o", torch.bfloat16, (R, Hv, dv))
-    rc = getattr(lib(), name)(_ptr(q), _ptr(k), _ptr(v), *[_ptr(g) for g in gates], _ptr(state),
-                              _ptr(slots), _ptr(o), R, state.shape[0], Hk, Hv, dk, dv, *strides,
-                              _stream(q.device))
+        o = torch.empty_like(v, memory_format=torch.contiguous_format)
+    else:
+        _check(o, "o", torch.bfloat16, (R, Hv, dv))
+    rc = name(q.data_ptr(), k.data_ptr(), v.data_ptr(), *gates, state.data_ptr(), slots,
+              o.data_ptr(), R, n, Hk, Hv, dk, dv, sq, sk, sv,
+              torch._C._cuda_getCurrentRawStream(q.device.index))
     if rc != GDN_OK:
-        raise GDNError(rc, name)
+        raise GDNError(rc, name.__name__)
     return o
 
 
@@ -432,16 +436,17 @@ def delta_step(q, k, v, g, beta, state, slots=None, *, o=None) -> torch.Tensor:
     (bf16), g, beta [R, Hv]; state [n, Hv, 128, 128] (fp32) is updated in place.
     slots: int32 [R], the state of each row (None: row r's state is r); a
     negative slot is a padded row, whose output is zero.  Returns o [R, Hv, 128]."""
-    _check(g, "g", torch.float32, tuple(v.shape[:2]))
-    _check(beta, "beta", torch.float32, tuple(v.shape[:2]))
-    return _step("gdn_delta_step", q, k, v, (g, beta), state, slots, o)
+    rows = v.shape[:2]
+    _check(g, "g", torch.float32, rows)
+    _check(beta, "beta", torch.float32, rows)
+    return _step(lib().gdn_delta_step, q, k, v, (g.data_ptr(), beta.data_ptr()), state, slots, o)
 
 
 def decay_step(q, k, v, decay, state, slots=None, *, o=None) -> torch.Tensor:
     """One token per row of linear attention with a decay for each head (decay
     [Hv], the log-decays); otherwise as delta_step."""
-    _check(decay, "decay", torch.float32, tuple(v.shape[1:2]))
-    return _step("gdn_decay_step", q, k, v, (decay,), state, slots, o)
+    _check(decay, "decay", torch.float32, v.shape[1:2])
+    return _step(lib().gdn_decay_step, q, k, v, (decay.data_ptr(),), state, slots, o)
 
 
 def decay_workspace_bytes(backward, n_seqs, total, max_seqlen, Hk, Hv, dk=128, dv=128) -> int:

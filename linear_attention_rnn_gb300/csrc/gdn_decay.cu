@@ -22,7 +22,7 @@
 // X: 4 x 128 columns).  X stays in tensor memory in fp32 for the whole segment;
 // it is scaled there and rounded to bf16 only as the operand of A X.  B^T diag(e)
 // C has to keep the state's fp32: the rows of B are scaled in fp32 and split
-// into bf16 terms (the first in place, one or two beside it), a product each.  The masked P
+// into bf16 terms, a product each.  The masked P
 // goes back to tensor memory as a bf16 A operand.  Warps 0-7 mask P and
 // write the output, 8-15 carry the state and scale B; one thread issues the
 // products, one the TMA loads (a ring of five 32 KiB tiles, three to a chunk).
@@ -92,25 +92,25 @@ __device__ __forceinline__ int2 find_segment(const int* cu, int n_seqs, int T, i
 // touch consecutive addresses: float4 (row r, columns 4 g .. 4 g + 3) at g * 128 + r.
 __device__ __forceinline__ int seg_index(int r, int c) { return ((c >> 2) * HD + r) * 4 + (c & 3); }
 
-// Rows of an SW128 tile scaled by f and split into TERMS bf16 terms, the first in
-// place, the others in the tiles at `rest`; this thread's row r, 16-byte chunks
-// j .. j + 3.  The leading terms are the value's upper 16 bits as they
-// stand (the remainder is then exact), the last one is rounded: 8 bits more of
-// the fp32 product per term, at a permute, two ands and a subtraction per pair.
-// A row that is not `valid` (past the sequence's end) becomes zero, whatever it
-// holds.
-// The tiles at `rest` have REST_ROWS rows (64: one for both halves of the tile).
-template <int TERMS, int REST_ROWS>
-__device__ __forceinline__ void scale_row(unsigned char* tile, unsigned char* rest, int r, int j, float f, bool valid) {
-  uint4 u[4];  // four loads in flight
+// Row r of an SW128 tile scaled by f and split into TERMS bf16 terms, 16-byte chunks
+// j .. j + NJ - 1.  Term 0 goes to `first` and the others to the tiles at `rest`,
+// row r % ROWS of tiles with ROWS rows (`first` = the tile itself, 128 rows: in
+// place).  The leading terms are the value's upper 16 bits as they stand (the
+// remainder is then exact), the last one is rounded: 8 bits more of the fp32
+// product per term, at a permute, two ands and half a multiply-add per pair.  A
+// row that is not `valid` (past the sequence's end) becomes zero, whatever it holds.
+template <int TERMS, int NJ, int ROWS>
+__device__ __forceinline__ void scale_row(const unsigned char* tile, unsigned char* first, unsigned char* rest, int r,
+                                          int j, float f, bool valid) {
+  uint4 u[NJ];  // all loads in flight at once
 #pragma unroll
-  for (int c = 0; c < 4; ++c) u[c] = *reinterpret_cast<const uint4*>(tile + tc::sw128_chunk(r, j + c, CH));
+  for (int c = 0; c < NJ; ++c) u[c] = *reinterpret_cast<const uint4*>(tile + tc::sw128_chunk(r, j + c, CH));
   if (!valid) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) u[c] = make_uint4(0u, 0u, 0u, 0u);
+    for (int c = 0; c < NJ; ++c) u[c] = make_uint4(0u, 0u, 0u, 0u);
   }
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
+  for (int c = 0; c < NJ; ++c) {
     const uint32_t up[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
     uint32_t o[TERMS][4];
 #pragma unroll
@@ -128,11 +128,10 @@ __device__ __forceinline__ void scale_row(unsigned char* tile, unsigned char* re
       }
       o[TERMS - 1][i] = pack_bf16(x, y);
     }
+    const uint32_t at = tc::sw128_chunk(r & (ROWS - 1), j + c, ROWS);
 #pragma unroll
     for (int t = 0; t < TERMS; ++t)
-      *reinterpret_cast<uint4*>(t == 0 ? tile + tc::sw128_chunk(r, j + c, CH)
-                                       : rest + (t - 1) * REST_ROWS * 256 +
-                                             tc::sw128_chunk(r & (REST_ROWS - 1), j + c, REST_ROWS)) =
+      *reinterpret_cast<uint4*>((t == 0 ? first : rest + (t - 1) * ROWS * 256) + at) =
           make_uint4(o[t][0], o[t][1], o[t][2], o[t][3]);
   }
 }
@@ -148,19 +147,17 @@ __device__ __forceinline__ void load_tile(unsigned char* dst, const CUtensorMap*
 }
 
 // ---- the chunk walk ----------------------------------------------------------------
-// Room for the further terms of the scaled B rows.  Two terms leave an error of
-// some 1e-5 in the state, far below the rounding of the output's operands; a
-// final state that is returned in fp32 takes three, whose two further tiles
-// hold 64 rows at a time (the second half waits for the first one's products:
-// 0.35 us of a chunk, where a ring slot less cost 1.5).
+// B' = diag(e) B enters X += B'^T C in two bf16 terms, which leave an error of some
+// 1e-5 in the state, far below the rounding of the output's operands (a final
+// state that is returned in fp32 comes from k_decay_fold, in three).
 constexpr int NSLOT = 5;
 struct WalkSmem {
   unsigned char slot[NSLOT][TILE];
-  unsigned char rest[TILE];
+  unsigned char lo[TILE];               // second term of the scaled B rows (the first one in place)
   unsigned char X[TILE];                // the entering state in bf16, [128 (b) rows x 128 (c)]
   alignas(16) float tab[CH];            // e^{w d}
   uint64_t full[NSLOT], empty[NSLOT];
-  uint64_t barP, barPm, barK[2], barH, barS, barX, barO, barOf, barSt;
+  uint64_t barP, barPm, barK[2], barS, barX, barO, barOf, barSt;
   uint32_t tmem;
 };
 
@@ -188,17 +185,20 @@ __device__ __forceinline__ void first_state(const DecayRole& R, unsigned char* s
   } else {
     // columns c, c + 64 of the pass (c = 0 .. 31, or 32 .. 63): 128 rows x 2 x 128 bytes
     const int t = threadIdx.x & 255, cc = c0 & 63;
-    float4 f[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int i = t + 256 * k, row = i >> 4, p = i & 15;  // 16-byte piece p of the row's two
-      f[k] = *reinterpret_cast<const float4*>(x0 + row * HD + (p >> 3) * 64 + cc + 4 * (p & 7));
-    }
     asm volatile("bar.sync 2, 256;" ::: "memory");  // (the pass before has been read)
+#pragma unroll 1
+    for (int k = 0; k < 8; k += 2) {
+      float4 f[2];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int i = t + 256 * k, row = i >> 4, p = i & 15;
-      *reinterpret_cast<float4*>(stage + row * 256 + ((p ^ (row & 7)) << 4)) = f[k];
+      for (int l = 0; l < 2; ++l) {
+        const int i = t + 256 * (k + l), row = i >> 4, p = i & 15;  // 16-byte piece p of the row's two
+        f[l] = *reinterpret_cast<const float4*>(x0 + row * HD + (p >> 3) * 64 + cc + 4 * (p & 7));
+      }
+#pragma unroll
+      for (int l = 0; l < 2; ++l) {
+        const int i = t + 256 * (k + l), row = i >> 4, p = i & 15;
+        *reinterpret_cast<float4*>(stage + row * 256 + ((p ^ (row & 7)) << 4)) = f[l];
+      }
     }
     asm volatile("bar.sync 2, 256;" ::: "memory");
 #pragma unroll
@@ -214,9 +214,9 @@ __device__ __forceinline__ void first_state(const DecayRole& R, unsigned char* s
 }
 
 // One CTA's walk over the chunks [cb, ce) of head hd in sequence s (rows q); REV: backwards.
-template <int TERMS, bool SUM, bool REV>
+template <bool SUM, bool REV>
 __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, WalkSmem& sm, const Range q, int s,
-                                     int slot_id, int hd, int cb, int ce, int nch) {
+                                     int slot_id, int hd, int cb, int ce) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tc::warp_index();
   const int G = a.Hv / a.Hk, loops = SUM ? G : 1, nc = ce - cb;
   const int n_it = loops * nc;
@@ -238,7 +238,6 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
     }
     tc::mbar_init(&sm.barP, 1);
     tc::mbar_init(&sm.barX, 1);
-    tc::mbar_init(&sm.barH, 1);
     tc::mbar_init(&sm.barO, 1);
     tc::mbar_init(&sm.barPm, 256);
     tc::mbar_init(&sm.barK[0], 256);
@@ -319,14 +318,8 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
         w.warp_on(&sm.barK[h], it);
         tc::fence_after();
         const uint32_t c = slot(tcc) + 8192 * h;
-        tc::gemm_rows64_by(lead, tX, slot(tb) + 8192 * h, c, true);
-        if (TERMS == 2) {
-          tc::gemm_rows64_by(lead, tX, smem_u32(sm.rest) + 8192 * h, c, true);
-        } else {
-          tc::gemm_rows64_by<64>(lead, tX, smem_u32(sm.rest), c, true);
-          tc::gemm_rows64_by<64>(lead, tX, smem_u32(sm.rest) + TILE / 2, c, true);
-          if (h == 0) tc::commit_by(lead, &sm.barH);
-        }
+        tc::gemm_rows_by<64, 128>(lead, tX, slot(tb) + 8192 * h, c, true);
+        tc::gemm_rows_by<64, 128>(lead, tX, smem_u32(sm.lo) + 8192 * h, c, true);
       }
       tc::commit_by(lead, &sm.barX);
       release(tb);
@@ -512,7 +505,7 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
 #pragma unroll 1
           for (int g = 0; g < 2; ++g) {
             float v[32];
-            first_state(R, sm.rest, x0, r, 64 * half + 32 * g, v);
+            first_state(R, sm.lo, x0, r, 64 * half + 32 * g, v);
             tc::st32(tX + cols + 32 * g, v);
           }
           tc::wait_st();
@@ -548,27 +541,11 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
         for (int h = 0; h < 2; ++h) {  // 64 rows at a time, four threads to a row
           const int i = 64 * h + (tid & 63), j = 4 * ((tid >> 6) & 3);
           const float e = expf(wd * (float)(REV ? i + 1 : max(n - 1 - i, 0)));
-          if (TERMS == 3 && h == 1) w.warp_on(&sm.barH, it);  // (the first half's further terms have been read)
-          scale_row<TERMS, TERMS == 2 ? CH : 64>(sm.slot[tb % NSLOT], sm.rest, i, j, e, i < n);
+          scale_row<2, 4, CH>(sm.slot[tb % NSLOT], sm.slot[tb % NSLOT], sm.lo, i, j, e, i < n);
           if (i >= n) zero_row(sm.slot[tcc % NSLOT], i, j, 4);
           tc::fence_proxy_async();
           tc::mbar_arrive(&sm.barK[h]);
         }
-      }
-      if (R.xT) {  // (one segment: with more, the prefix has written the final state)
-        w.warp_on(&sm.barX, n_it - 1);
-        tc::fence_after();
-        float* dst = R.xT + ((long)s * a.Hv + hd) * HD * HD + r * HD + 64 * half;
-#pragma unroll 1
-        for (int g = 0; g < 2; ++g) {
-          float v[32];
-          tc::ld32(tX + cols + 32 * g, v);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<float4*>(dst + 32 * g + 4 * i) =
-                make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-        }
-        tc::fence_before();
       }
     }
   }
@@ -579,14 +556,14 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
   if (warp == 0) tc::dealloc(sm.tmem, 512);
 }
 
-template <int TERMS, bool SUM>
+template <bool SUM>
 __device__ __forceinline__ void walk_block(const DecayArgs& a, WalkSmem& sm) {
-  const int tid = threadIdx.x;
   if (a.nseg == 1 && !a.beside) {  // (with segments, only the entering states wait for the kernel before)
     pdl_wait();
     pdl_release();
     clear_status(a.status);
   }
+  if (a.beside == 2) pdl_release();  // (a third kernel beside the two)
 
   // pass, then segment, sequence and head of this CTA
   int u = blockIdx.x, ri = 0;
@@ -604,25 +581,18 @@ __device__ __forceinline__ void walk_block(const DecayArgs& a, WalkSmem& sm) {
   const Range q = seq_range(a.cu, s, a.T, a.total);
   const int nch = (q.len + CH - 1) / CH;
   const int cb = seg * a.seg_chunks, ce = a.nseg == 1 ? nch : min(nch, cb + a.seg_chunks), nc = ce - cb;
-  if (nc <= 0) {  // an empty sequence ends in the state that it began with
-    if (seg == 0 && R.xT) {
-      const long o = ((long)s * a.Hv + hd) * HD * HD;
-      for (int i = tid; i < HD * HD; i += WALK_THREADS) R.xT[o + i] = R.x0 ? R.x0[o + i] : 0.f;
-    }
-    return;
-  }
+  if (nc <= 0) return;
   if (R.rev)
-    walk<TERMS, SUM, true>(a, R, sm, q, s, slot, hd, cb, ce, nch);
+    walk<SUM, true>(a, R, sm, q, s, slot, hd, cb, ce);
   else
-    walk<TERMS, SUM, false>(a, R, sm, q, s, slot, hd, cb, ce, nch);
+    walk<SUM, false>(a, R, sm, q, s, slot, hd, cb, ce);
 }
 
-// TERMS = 3 where final states are returned in fp32; SUM: an output head is the sum
-// over a group's value heads.
-template <int TERMS, bool SUM>
+// SUM: an output head is the sum over a group's value heads.
+template <bool SUM>
 __global__ void __launch_bounds__(WALK_THREADS, 1) k_decay(const __grid_constant__ DecayArgs a) {
   extern __shared__ unsigned char raw[];
-  walk_block<TERMS, SUM>(a, *reinterpret_cast<WalkSmem*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u)));
+  walk_block<SUM>(a, *reinterpret_cast<WalkSmem*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u)));
   if (blockIdx.x == 0) pdl_wait();  // the grid ends after the one before it, whatever its CTAs had to do
 }
 
@@ -635,14 +605,14 @@ struct FoldSmem {
   uint32_t tmem;
 };
 
-__global__ void __launch_bounds__(FOLD_THREADS, 1) k_decay_fold(const __grid_constant__ DecayFoldArgs a) {
-  extern __shared__ unsigned char raw[];
-  FoldSmem& sm = *reinterpret_cast<FoldSmem*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
+__device__ __forceinline__ void fold_block(const DecayFoldArgs& a, FoldSmem& sm) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tc::warp_index();
   const int G = a.Hv / a.Hk;
-  pdl_wait();
-  pdl_release();
-  if (blockIdx.y == 0) clear_status(a.status);
+  if (!a.beside) {
+    pdl_wait();
+    pdl_release();
+    if (blockIdx.y == 0) clear_status(a.status);
+  }
   const int j = blockIdx.x % a.Hv, slot = blockIdx.x / a.Hv;
   const int2 at = find_segment(a.cu, a.n_seqs, a.T, a.total, a.seg_chunks, a.nseg, slot);
   const int s = at.x, seg = at.y;
@@ -650,8 +620,13 @@ __global__ void __launch_bounds__(FOLD_THREADS, 1) k_decay_fold(const __grid_con
   const DecayFoldRole& R = a.role[blockIdx.y];
   const Range q = seq_range(a.cu, s, a.T, a.total);
   const int nch = (q.len + CH - 1) / CH;
-  const int cb = seg * a.seg_chunks, ce = min(nch, cb + a.seg_chunks), nc = ce - cb;
-  if (nc <= 0) return;
+  const int cb = seg * a.seg_chunks, ce = a.nseg == 1 ? nch : min(nch, cb + a.seg_chunks), nc = ce - cb;
+  const long sh = (long)s * a.Hv + j;
+  if (nc <= 0) {
+    if (a.nseg == 1)  // an empty sequence ends in the state that it began with
+      for (int i = tid; i < HD * HD; i += FOLD_THREADS) R.last[sh * HD * HD + i] = R.x0 ? R.x0[sh * HD * HD + i] : 0.f;
+    return;
+  }
   // the segment that the walk ends with matters only for the final state
   if (!R.last && (R.rev ? cb == 0 : ce == nch)) return;
   const int end = min(q.len, ce * CH);  // one past the segment's last token
@@ -700,10 +675,10 @@ __global__ void __launch_bounds__(FOLD_THREADS, 1) k_decay_fold(const __grid_con
         w.warp_on(&sm.barK[h], i);
         tc::fence_after();
         const uint32_t c = smem_u32(sm.slot[tcc % FOLD_SLOTS]) + 8192 * h;
-        tc::gemm_rows64_by(lead, tX, smem_u32(sm.slot[tb % FOLD_SLOTS]) + 8192 * h, c, i > 0 || h > 0);
+        tc::gemm_rows_by<64, 128>(lead, tX, smem_u32(sm.slot[tb % FOLD_SLOTS]) + 8192 * h, c, i > 0 || h > 0);
 #pragma unroll
         for (int t = 0; t < FOLD_TERMS - 1; ++t)
-          tc::gemm_rows64_by(lead, tX, smem_u32(sm.rest[t]) + 8192 * h, c, true);
+          tc::gemm_rows_by<64, 128>(lead, tX, smem_u32(sm.rest[t]) + 8192 * h, c, true);
         if (h == 1) {
           if (tb + FOLD_SLOTS < 2 * nc) tc::commit_by(lead, &sm.empty[tb % FOLD_SLOTS]);
           if (tcc + FOLD_SLOTS < 2 * nc) tc::commit_by(lead, &sm.empty[tcc % FOLD_SLOTS]);
@@ -724,7 +699,7 @@ __global__ void __launch_bounds__(FOLD_THREADS, 1) k_decay_fold(const __grid_con
         // weight to the segment's end (forwards) or to its start (backwards)
         const float e = expf(wd * (float)(R.rev ? t0 - cb * CH + 1 : max(end - 1 - t0, 0)));
         if (i > 0) w.warp_on(&sm.barM[h], i - 1);  // (these rows' further terms have been read)
-        scale_row<FOLD_TERMS, CH>(sm.slot[tb % FOLD_SLOTS], sm.rest[0], r, j0, e, r < n);
+        scale_row<FOLD_TERMS, 4, CH>(sm.slot[tb % FOLD_SLOTS], sm.slot[tb % FOLD_SLOTS], sm.rest[0], r, j0, e, r < n);
         if (r >= n) zero_row(sm.slot[tcc % FOLD_SLOTS], r, j0, 4);
         tc::fence_proxy_async();
         tc::mbar_arrive(&sm.barK[h]);
@@ -734,15 +709,24 @@ __global__ void __launch_bounds__(FOLD_THREADS, 1) k_decay_fold(const __grid_con
     tc::fence_after();
     const int row = 32 * (warp & 3) + lane, g0 = 2 * (warp >> 2);
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
-    float* dst = R.x + ((long)slot * a.Hv + j) * HD * HD;
+    // with one segment this is the final state but for the initial one's share
+    const float keep = expf(wd * (float)q.len);
+    const float* x0 = a.nseg == 1 && R.x0 ? R.x0 + sh * HD * HD : nullptr;
+    float* dst = a.nseg == 1 ? R.last + sh * HD * HD : R.x + ((long)slot * a.Hv + j) * HD * HD;
 #pragma unroll 1
     for (int g = g0; g < g0 + 2; ++g) {
       float v[32];
       tc::ld32(tX + lane_base + 32 * g, v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        *reinterpret_cast<float4*>(dst + seg_index(row, 32 * g + 4 * i)) =
-            make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+      for (int i = 0; i < 32; i += 4) {
+        const int c = 32 * g + i;
+        float4 o = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        if (x0) {
+          const float4 x = *reinterpret_cast<const float4*>(x0 + row * HD + c);
+          o = make_float4(o.x + keep * x.x, o.y + keep * x.y, o.z + keep * x.z, o.w + keep * x.w);
+        }
+        *reinterpret_cast<float4*>(dst + (a.nseg == 1 ? row * HD + c : seg_index(row, c))) = o;
+      }
     }
     tc::fence_before();
   }
@@ -750,6 +734,14 @@ __global__ void __launch_bounds__(FOLD_THREADS, 1) k_decay_fold(const __grid_con
   __syncthreads();
   tc::fence_after();
   if (warp == 0) tc::dealloc(sm.tmem, 128);
+}
+
+// A segment's own state; with one segment to a sequence the final state itself,
+// formed beside the walk (in three bf16 terms: an error of 1e-7 of the sums' sizes).
+__global__ void __launch_bounds__(FOLD_THREADS, 1) k_decay_fold(const __grid_constant__ DecayFoldArgs a) {
+  extern __shared__ unsigned char raw[];
+  fold_block(a, *reinterpret_cast<FoldSmem*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u)));
+  if (blockIdx.x == 0 && blockIdx.y == 0) pdl_wait();  // (as the walk)
 }
 
 // Entering states from the segments' own ones, in place, and the final state:
@@ -798,21 +790,19 @@ cudaError_t set_smem(K k, size_t bytes) {
 
 }  // namespace
 
-template <int TERMS, bool SUM>
+template <bool SUM>
 static cudaError_t launch_walk(const DecayArgs& a, cudaStream_t s) {
   constexpr size_t smem = sizeof(WalkSmem) + 1024;
   static_assert(smem <= 227 * 1024, "shared memory");
-  cudaError_t e = set_smem(k_decay<TERMS, SUM>, smem);
+  cudaError_t e = set_smem(k_decay<SUM>, smem);
   if (e != cudaSuccess) return e;
   long units = 0;
   for (int i = 0; i < a.n_roles; ++i) units += (long)a.slots * (a.role[i].shared ? a.Hk : a.Hv);
-  return launch_pdl(k_decay<TERMS, SUM>, dim3((unsigned)units), dim3(WALK_THREADS), smem, s, a);
+  return launch_pdl(k_decay<SUM>, dim3((unsigned)units), dim3(WALK_THREADS), smem, s, a);
 }
 
 cudaError_t launch_decay(const DecayArgs& a, cudaStream_t s) {
-  const bool sum = a.Hv > a.Hk && a.role[0].shared;
-  if (a.role[0].xT) return launch_walk<3, false>(a, s);
-  return sum ? launch_walk<2, true>(a, s) : launch_walk<2, false>(a, s);
+  return a.Hv > a.Hk && a.role[0].shared ? launch_walk<true>(a, s) : launch_walk<false>(a, s);
 }
 
 cudaError_t launch_decay_fold(const DecayFoldArgs& a, cudaStream_t s) {
@@ -822,7 +812,7 @@ cudaError_t launch_decay_fold(const DecayFoldArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const unsigned sh = (unsigned)((long)a.n_seqs * a.Hv);
   e = launch_pdl(k_decay_fold, dim3((unsigned)a.slots * (unsigned)a.Hv, (unsigned)a.n_roles), dim3(FOLD_THREADS), smem, s, a);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || a.nseg == 1) return e;
   return launch_pdl(k_decay_prefix, dim3(sh, HD * HD / 1024, (unsigned)a.n_roles), dim3(256), 0, s, a);
 }
 

@@ -165,7 +165,6 @@ struct DecayRole {
   int shared;           // 1: the output is one head for a group, summed over its value heads
   const float* x0;      // [n_seqs][Hv][HD][HD] (nullable = 0)
   const float* xseg;    // entering states [slots][Hv][HD][HD] (null with one segment)
-  float* xT;            // final state (one segment only, nullable)
   float* acc;           // running sums [Hk][HD / 4][total][4] (shared, Hv > Hk)
   bf16* out;
 };
@@ -177,7 +176,8 @@ struct DecayArgs {
   int n_roles, n_seqs, total, T, Hk, Hv;
   int nseg, seg_chunks;  // most segments of a sequence, chunks to a segment
   int slots;             // segment slots: n_seqs with nseg = 1, else total / (128 seg_chunks) + n_seqs
-  int beside;            // the launch before it is another walk of the same call, which it need not wait for
+  int beside;            // the launch before it is another walk of the same call, which it need not wait
+                         //   for (2: and a fold of the call follows, which need not wait for it)
 };
 struct DecayFoldRole {
   CUtensorMap b, c;    // b: shared heads, c: value heads
@@ -194,6 +194,7 @@ struct DecayFoldArgs {
   int n_roles, n_seqs, total, T, Hk, Hv;
   int nseg, seg_chunks;  // most segments of a sequence, chunks to a segment
   int slots;             // segment slots: n_seqs with nseg = 1, else total / (128 seg_chunks) + n_seqs
+  int beside;            // as DecayArgs
 };
 
 // Causal softmax attention over packed sequences (gdn_attn_fwd.cu, gdn_attn_bwd.cu).
@@ -263,9 +264,10 @@ cudaError_t launch_out_gate(const bf16* o, const bf16* z, bf16* y, long rows, cu
 cudaError_t launch_out_gate_bwd(const bf16* o, const bf16* z, const bf16* dy, bf16* dO, bf16* dz, long rows,
                                 cudaStream_t s);
 cudaError_t launch_step(const StepArgs& a, cudaStream_t s);
-// (all roles shared, or none; a final state in the first role or in none)
+// (all roles shared, or none)
 cudaError_t launch_decay(const DecayArgs& a, cudaStream_t s);
-// the segments' own states and the prefix over them (two launches)
+// the segments' own states and the prefix over them (two launches); with one segment
+// to a sequence the final state alone (one launch)
 cudaError_t launch_decay_fold(const DecayFoldArgs& a, cudaStream_t s);
 cudaError_t launch_attn_fwd(const AttnArgs& a, cudaStream_t s);
 // dO . o per row, then the gradients of k and v, then that of q

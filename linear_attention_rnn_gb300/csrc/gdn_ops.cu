@@ -98,6 +98,23 @@ DecayPlan decay_plan(int backward, int n_seqs, int total, int max_seqlen, int Hk
   return p;
 }
 
+DecayFoldArgs fold_args(const DecayArgs& a) {
+  DecayFoldArgs f;
+  memset(&f, 0, sizeof f);
+  f.decay = a.decay;
+  f.cu = a.cu;
+  f.status = a.status;
+  f.n_seqs = a.n_seqs;
+  f.total = a.total;
+  f.T = a.T;
+  f.Hk = a.Hk;
+  f.Hv = a.Hv;
+  f.nseg = a.nseg;
+  f.seg_chunks = a.seg_chunks;
+  f.slots = a.slots;
+  return f;
+}
+
 int decay_check(int n_seqs, int total, int max_seqlen, int Hk, int Hv, int d_k, int d_v, const int* cu, long long sq,
                 long long sk, long long sv) {
   if (n_seqs < 0 || total < 0 || max_seqlen < 0 || Hk <= 0 || Hv <= 0 || Hv % Hk != 0) return GDN_ERR_ARG;
@@ -290,33 +307,21 @@ int gdn_decay_fwd(const void* q, const void* k, const void* v, const float* deca
   r.hc = 1;
   r.x0 = h0;
   r.out = static_cast<bf16*>(o);
+  DecayFoldArgs f = fold_args(a);
+  f.n_roles = 1;
+  f.role[0].b = r.b;
+  f.role[0].c = r.c;
+  f.role[0].x0 = h0;
+  f.role[0].last = hT;
   if (p.nseg > 1) {
-    float* x = at<float>(ws, p.xf);
-    DecayFoldArgs f;
-    memset(&f, 0, sizeof f);
-    f.decay = decay;
-    f.cu = cu_seqlens;
-    f.status = a.status;
-    f.n_roles = 1;
-    f.n_seqs = n_seqs;
-    f.total = total;
-    f.T = a.T;
-    f.Hk = Hk;
-    f.Hv = Hv;
-    f.nseg = p.nseg;
-    f.seg_chunks = p.seg_chunks;
-    f.slots = p.slots;
-    f.role[0].b = r.b;
-    f.role[0].c = r.c;
-    f.role[0].x0 = h0;
-    f.role[0].x = x;
-    f.role[0].last = hT;
+    f.role[0].x = at<float>(ws, p.xf);
     if ((rc = cuda_status(launch_decay_fold(f, s)))) return rc;
-    r.xseg = x;
-  } else {
-    r.xT = hT;
+    r.xseg = f.role[0].x;
+    return cuda_status(launch_decay(a, s));
   }
-  return cuda_status(launch_decay(a, s));
+  if ((rc = cuda_status(launch_decay(a, s))) || !hT) return rc;
+  f.beside = 1;
+  return cuda_status(launch_decay_fold(f, s));
 }
 
 int gdn_decay_bwd(const void* q, const void* k, const void* v, const float* decay, const float* h0, const void* dO,
@@ -382,41 +387,33 @@ int gdn_decay_bwd(const void* q, const void* k, const void* v, const float* deca
       !tmap_rows(&rk.o, dk, total, Hk, HD, (uint64_t)Hk * HD * 2, 1, CH) ||
       !tmap_rows(&rv.o, dv, total, Hv, HD, (uint64_t)Hv * HD * 2, 1, CH))
     return GDN_ERR_CUDA;
+  DecayFoldArgs f = fold_args(a);
+  DecayFoldRole &ff = f.role[0], &fr = f.role[1];
+  ff.b = mk;
+  ff.c = mv;
+  ff.x0 = h0;
+  fr.b = mq;
+  fr.c = md;
+  fr.rev = 1;
+  fr.x0 = dhT;
+  fr.last = dh0;
   if (p.nseg > 1) {
-    DecayFoldArgs f;
-    memset(&f, 0, sizeof f);
-    f.decay = decay;
-    f.cu = cu_seqlens;
-    f.status = a.status;
     f.n_roles = 2;
-    f.n_seqs = n_seqs;
-    f.total = total;
-    f.T = a.T;
-    f.Hk = Hk;
-    f.Hv = Hv;
-    f.nseg = p.nseg;
-    f.seg_chunks = p.seg_chunks;
-    f.slots = p.slots;
-    f.role[0].b = mk;
-    f.role[0].c = mv;
-    f.role[0].x0 = h0;
-    f.role[0].x = at<float>(ws, p.xf);
-    f.role[1].b = mq;
-    f.role[1].c = md;
-    f.role[1].rev = 1;
-    f.role[1].x0 = dhT;
-    f.role[1].x = at<float>(ws, p.xr);
-    f.role[1].last = dh0;
+    ff.x = at<float>(ws, p.xf);
+    fr.x = at<float>(ws, p.xr);
     if ((rc = cuda_status(launch_decay_fold(f, s)))) return rc;
-    rq.xseg = f.role[0].x;
-    rk.xseg = rv.xseg = f.role[1].x;
-  } else {
-    rv.xT = dh0;
+    rq.xseg = ff.x;
+    rk.xseg = rv.xseg = fr.x;
   }
+  const bool last = p.nseg == 1 && dh0;  // the final state in a kernel of its own, beside the walks
   if ((rc = cuda_status(launch_decay(a, s)))) return rc;
   b.n_roles = 1;
-  b.beside = 1;
-  return cuda_status(launch_decay(b, s));
+  b.beside = last ? 2 : 1;
+  if ((rc = cuda_status(launch_decay(b, s))) || !last) return rc;
+  f.n_roles = 1;
+  f.role[0] = fr;
+  f.beside = 1;
+  return cuda_status(launch_decay_fold(f, s));
 }
 
 size_t gdn_attn_workspace_bytes(int backward, int n_seqs, int total_q, int total_k, int max_k, int Hq, int Hk,

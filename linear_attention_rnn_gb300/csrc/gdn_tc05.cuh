@@ -466,16 +466,16 @@ __device__ __forceinline__ void gemm128_by(uint32_t leader, uint32_t tmem_d, uin
            db0 + ((B_MN ? (uint32_t)k * 2048u : kmaj) >> 4), idesc, (k > 0 || accumulate_first) ? 1u : 0u);
   }
 }
-// D[128 x 128] (+)= A^T B over 64 of the K rows: A and B are rows of [K x 128] tiles,
-// from the row that the addresses point to (a multiple of 8); A's tile has
-// A_ROWS rows, B's 128
-template <int A_ROWS = 128>
-__device__ __forceinline__ void gemm_rows64_by(uint32_t leader, uint32_t tmem_d, uint32_t a_smem, uint32_t b_smem,
-                                               bool accumulate_first) {
+// D[128 x 128] (+)= A^T B over K rows: A and B are rows of [rows x 128] tiles, from
+// the row that the addresses point to (a multiple of 8); A's tile has A_ROWS
+// rows, B's 128
+template <int K, int A_ROWS>
+__device__ __forceinline__ void gemm_rows_by(uint32_t leader, uint32_t tmem_d, uint32_t a_smem, uint32_t b_smem,
+                                             bool accumulate_first) {
   const uint32_t idesc = idesc_bf16(128, 128) | (1u << 15) | (1u << 16);
   const uint64_t da0 = desc_sw128_mn(a_smem, A_ROWS * 128u), db0 = desc_sw128_mn(b_smem, 128u * 128u);
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
+  for (int k = 0; k < K / 16; ++k)
     mma_by(leader, tmem_d, da0 + (((uint32_t)k * 2048u) >> 4), db0 + (((uint32_t)k * 2048u) >> 4), idesc,
            (k > 0 || accumulate_first) ? 1u : 0u);
 }
