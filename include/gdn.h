@@ -370,7 +370,8 @@ int gdn_decay_step(const void* q, const void* k, const void* v, const float* dec
  * (bf16) and dh0 (fp32, NULL = not written).  Nothing is saved by the forward.
  * A sequence's results depend on its own rows alone, whatever the rows beside
  * it hold.  ws: at least gdn_decay_workspace_bytes(backward, ...) bytes, whose
- * first word is the status word of the bounded waits (gdn_workspace_status).
+ * first word is the status word of the bounded waits (gdn_workspace_status);
+ * where that is all (256 bytes), ws may be NULL, and no status is kept.
  */
 size_t gdn_decay_workspace_bytes(int backward, int n_seqs, int total, int max_seqlen, int Hk,
                                  int Hv, int d_k, int d_v);
@@ -406,7 +407,8 @@ int gdn_decay_bwd(const void* q, const void* k, const void* v, const float* deca
  * and dk, dv [total_k, Hk, d] (bf16, summed over the query heads of each key
  * head).  Sums have a fixed order: equal calls give equal results.
  * ws: at least gdn_attn_workspace_bytes(backward, ...) bytes, whose first word is
- * the status word of the bounded waits (gdn_workspace_status).
+ * the status word of the bounded waits (gdn_workspace_status); where that is all
+ * (256 bytes), ws may be NULL, and no status is kept.
  */
 size_t gdn_attn_workspace_bytes(int backward, int n_seqs, int total_q, int total_k, int max_k,
                                 int Hq, int Hk, int d);

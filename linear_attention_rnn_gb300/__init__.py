@@ -9,6 +9,7 @@ first call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 from typing import Optional, Tuple
@@ -37,7 +38,9 @@ class GDNError(RuntimeError):
 
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile libgdn.so in-tree (nvcc, sm_103a)."""
+    this = globals()["build"]
     from .build import build as _build
+    globals()["build"] = this  # (importing the submodule of that name replaces it)
     return _build(force=force, verbose=verbose)
 
 
@@ -402,6 +405,20 @@ def _check_rows(t, name, H, d, n=None):
     return stride
 
 
+_STATUS_BYTES = 256  # a workspace that holds the status word alone may be left out
+
+
+def _scratch(nbytes, device, ws):
+    """(pointer, bytes) of the caller's workspace, or of one allocated here."""
+    if ws is None:
+        if nbytes <= _STATUS_BYTES:
+            return None, 0, None
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    elif ws.numel() * ws.element_size() < nbytes:
+        raise ValueError("workspace too small")
+    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
+
+
 def _step(name, q, k, v, gates, state, slots, o):
     if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
         raise ValueError("q, k, v must be [R, H, D]")
@@ -449,6 +466,7 @@ def decay_step(q, k, v, decay, state, slots=None, *, o=None) -> torch.Tensor:
     return _step(lib().gdn_decay_step, q, k, v, (decay.data_ptr(),), state, slots, o)
 
 
+@functools.lru_cache(maxsize=256)
 def decay_workspace_bytes(backward, n_seqs, total, max_seqlen, Hk, Hv, dk=128, dv=128) -> int:
     return int(lib().gdn_decay_workspace_bytes(int(backward), n_seqs, total, max_seqlen, Hk, Hv, dk,
                                                dv))
@@ -495,10 +513,11 @@ def decay_fwd(q, k, v, decay, h0=None, *, cu_seqlens=None, max_seqlen=None, want
     if want_hT and hT is None:
         hT = torch.empty((n, Hv, dk, dv), dtype=torch.float32, device=dev)
     _check(hT, "hT", torch.float32, (n, Hv, dk, dv))
-    ws = _workspace(decay_workspace_bytes(0, n, total, longest, Hk, Hv, dk, dv), dev, workspace)
+    wp, wn, ws = _scratch(decay_workspace_bytes(0, n, total, longest, Hk, Hv, dk, dv), dev,
+                          workspace)  # (ws: kept alive over the call)
     rc = lib().gdn_decay_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(h0), _ptr(cu_seqlens),
                              _ptr(o), _ptr(hT), n, total, longest, Hk, Hv, dk, dv, *strides,
-                             _ptr(ws), ws.numel(), _stream(dev))
+                             wp, wn, _stream(dev))
     if rc != GDN_OK:
         raise GDNError(rc, "gdn_decay_fwd")
     return o, hT
@@ -517,15 +536,17 @@ def decay_bwd(q, k, v, decay, h0, dO, dhT=None, *, cu_seqlens=None, max_seqlen=N
     dk_ = torch.empty(k.shape, dtype=torch.bfloat16, device=dev)
     dv_ = torch.empty(v.shape, dtype=torch.bfloat16, device=dev)
     dh0 = torch.empty((n, Hv, dk, dv), dtype=torch.float32, device=dev) if want_dh0 else None
-    ws = _workspace(decay_workspace_bytes(1, n, total, longest, Hk, Hv, dk, dv), dev, workspace)
+    wp, wn, ws = _scratch(decay_workspace_bytes(1, n, total, longest, Hk, Hv, dk, dv), dev,
+                          workspace)  # (ws: kept alive over the call)
     rc = lib().gdn_decay_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(h0), _ptr(dO), _ptr(dhT),
                              _ptr(cu_seqlens), _ptr(dq), _ptr(dk_), _ptr(dv_), _ptr(dh0), n, total,
-                             longest, Hk, Hv, dk, dv, *strides, _ptr(ws), ws.numel(), _stream(dev))
+                             longest, Hk, Hv, dk, dv, *strides, wp, wn, _stream(dev))
     if rc != GDN_OK:
         raise GDNError(rc, "gdn_decay_bwd")
     return dq, dk_, dv_, dh0
 
 
+@functools.lru_cache(maxsize=256)
 def attn_workspace_bytes(backward, n_seqs, total_q, total_k, max_k, Hq, Hk, d=128) -> int:
     return int(lib().gdn_attn_workspace_bytes(int(backward), n_seqs, total_q, total_k, max_k, Hq, Hk,
                                               d))
@@ -577,10 +598,11 @@ def attn_fwd(q, k, v, *, cu_q=None, cu_k=None, k_len=None, max_q=None, max_k=Non
     if want_lse and lse is None:
         lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
     _check(lse, "lse", torch.float32, tuple(q.shape[:-1]))
-    ws = _workspace(attn_workspace_bytes(0, n, total_q, total_k, longest, Hq, Hk, d), dev, workspace)
+    wp, wn, ws = _scratch(attn_workspace_bytes(0, n, total_q, total_k, longest, Hq, Hk, d), dev,
+                          workspace)  # (ws: kept alive over the call)
     rc = lib().gdn_attn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_q), _ptr(cu_k), _ptr(k_len), _ptr(o),
                             _ptr(lse), n, total_q, total_k, longest, Hq, Hk, d, scale, *strides,
-                            _ptr(ws), ws.numel(), _stream(dev))
+                            wp, wn, _stream(dev))
     if rc != GDN_OK:
         raise GDNError(rc, "gdn_attn_fwd")
     return o, lse
@@ -598,10 +620,11 @@ def attn_bwd(q, k, v, o, lse, dO, *, cu_q=None, cu_k=None, max_q=None, max_k=Non
     dq = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
     dk = torch.empty(k.shape, dtype=torch.bfloat16, device=dev)
     dv = torch.empty(v.shape, dtype=torch.bfloat16, device=dev)
-    ws = _workspace(attn_workspace_bytes(1, n, total_q, total_k, 0, Hq, Hk, d), dev, workspace)
+    wp, wn, ws = _scratch(attn_workspace_bytes(1, n, total_q, total_k, 0, Hq, Hk, d), dev,
+                          workspace)  # (ws: kept alive over the call)
     rc = lib().gdn_attn_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dO), _ptr(cu_q),
                             _ptr(cu_k), _ptr(dq), _ptr(dk), _ptr(dv), n, total_q, total_k, Hq, Hk, d,
-                            scale, *strides, _ptr(ws), ws.numel(), _stream(dev))
+                            scale, *strides, wp, wn, _stream(dev))
     if rc != GDN_OK:
         raise GDNError(rc, "gdn_attn_bwd")
     return dq, dk, dv

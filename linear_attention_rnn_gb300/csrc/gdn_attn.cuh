@@ -107,6 +107,27 @@ __device__ __forceinline__ void zero_rows(unsigned char* tile, int from, int t, 
     *reinterpret_cast<uint4*>(tile + tc::sw128_chunk(i >> 4, i & 15, CH)) = make_uint4(0u, 0u, 0u, 0u);
 }
 
+// 32 columns (c0 ..) of row r, times f, into an SW128 tile that a tensor map stores
+__device__ __forceinline__ void stage32(unsigned char* tile, int r, int c0, const float (&v)[32], float f) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint4 o;
+    o.x = pack_bf16(f * v[8 * i], f * v[8 * i + 1]);
+    o.y = pack_bf16(f * v[8 * i + 2], f * v[8 * i + 3]);
+    o.z = pack_bf16(f * v[8 * i + 4], f * v[8 * i + 5]);
+    o.w = pack_bf16(f * v[8 * i + 6], f * v[8 * i + 7]);
+    *reinterpret_cast<uint4*>(tile + tc::sw128_chunk(r, (c0 >> 3) + i, CH)) = o;
+  }
+}
+// The staged tile's two halves to (head, row) of a map, by one thread, which waits
+// until they have been read.
+__device__ __forceinline__ void store_tile(const CUtensorMap* m, int head, int row, const unsigned char* tile) {
+  tc::tma_store_3d(m, 0, head, row, tile);
+  tc::tma_store_3d(m, 64, head, row, tile + TILE / 2);
+  tc::bulk_commit();
+  tc::bulk_wait_read();
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

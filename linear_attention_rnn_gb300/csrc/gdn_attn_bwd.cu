@@ -86,7 +86,12 @@ __device__ __forceinline__ void dkv(const AttnArgs& a, unsigned char* raw, int b
   const int first = max(0, key0 - off) / TT;                 // first query tile that sees key0
   const int n = max(0, (sq.ql + TT - 1) / TT - first);
 
-  if (tid == 0) {
+  const int nt = 2 * n;
+  auto load = [&](int t) {
+    load_group(sm.slot[t % KV_SLOTS], (t & 1) ? &a.dO : &a.q, kh, G, sq.q0 + (first + t / 2) * TT,
+               &sm.full[t % KV_SLOTS]);
+  };
+  if (warp == 9 && lane == 0) {
     for (int k = 0; k < KV_SLOTS; ++k) {
       tc::mbar_init(&sm.full[k], 1);
       tc::mbar_init(&sm.empty[k], 1);
@@ -98,6 +103,14 @@ __device__ __forceinline__ void dkv(const AttnArgs& a, unsigned char* raw, int b
     tc::mbar_init(&sm.barP, 256);
     tc::mbar_init(&sm.barDs, 256);
     tc::mbar_fence_init();
+    if (n > 0) {  // the first loads at once
+      tc::arrive_expect_tx(&sm.barKV, 2 * TILE);
+      for (int h = 0; h < 2; ++h) {
+        tc::tma_load_3d(sm.k + h * (TILE / 2), &a.k, 64 * h, kh, sq.k0 + key0, &sm.barKV);
+        tc::tma_load_3d(sm.v + h * (TILE / 2), &a.v, 64 * h, kh, sq.k0 + key0, &sm.barKV);
+      }
+      for (int t = 0; t < min(nt, KV_SLOTS); ++t) load(t);
+    }
   }
   if (warp == 0) tc::alloc(&sm.tmem, 512);
   if (TT * G < CH)  // rows that no load writes, but the products over rows read
@@ -108,20 +121,12 @@ __device__ __forceinline__ void dkv(const AttnArgs& a, unsigned char* raw, int b
   tc::fence_after();
   const uint32_t tS = sm.tmem, tP = tS + 128, tV = tS + 256, tK = tS + 384;
   tc::Wait w;
-  const int nt = 2 * n;
 
   if (warp == 9) {
     if (lane == 0 && n > 0) {
-      tc::arrive_expect_tx(&sm.barKV, 2 * TILE);
-      for (int h = 0; h < 2; ++h) {
-        tc::tma_load_3d(sm.k + h * (TILE / 2), &a.k, 64 * h, kh, sq.k0 + key0, &sm.barKV);
-        tc::tma_load_3d(sm.v + h * (TILE / 2), &a.v, 64 * h, kh, sq.k0 + key0, &sm.barKV);
-      }
-      for (int t = 0; t < nt && w.ok; ++t) {
-        const int k = t % KV_SLOTS;
-        if (t >= KV_SLOTS) w.on(&sm.empty[k], t / KV_SLOTS - 1);
-        if (!w.ok) break;
-        load_group(sm.slot[k], (t & 1) ? &a.dO : &a.q, kh, G, sq.q0 + (first + t / 2) * TT, &sm.full[k]);
+      for (int t = KV_SLOTS; t < nt && w.ok; ++t) {
+        w.on(&sm.empty[t % KV_SLOTS], t / KV_SLOTS - 1);
+        if (w.ok) load(t);
       }
       if (w.ok) {
         w.on(&sm.barKV, 0);
@@ -266,9 +271,13 @@ __device__ __forceinline__ void dkv(const AttnArgs& a, unsigned char* raw, int b
     }
     if (n > 0) w.warp_on(&sm.barEnd, 0);
     tc::fence_after();
+    // warps 0-3 write dV, 4-7 dK: a whole tile through V's or K's place in shared memory
+    // (the last products have read them) and one TMA store, else row by row
     const long row = ((long)sq.k0 + key) * a.Hk + kh;
+    const bool tile = key0 + CH <= sq.kl;
+    unsigned char* staged = g0 ? sm.k : sm.v;
 #pragma unroll 1
-    for (int h = 0; h < 4; ++h) {  // warps 0-3 write dV, 4-7 dK
+    for (int h = 0; h < 4; ++h) {
       float v[32];
       if (n > 0) {
         tc::ld32((g0 ? tK : tV) + lane_base + 32 * h, v);
@@ -276,8 +285,16 @@ __device__ __forceinline__ void dkv(const AttnArgs& a, unsigned char* raw, int b
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = 0.f;
       }
-      if (key < sq.kl) store32((g0 ? a.dk : a.dv) + row * HD + 32 * h, v, g0 ? a.scale : 1.f);
+      if (tile)
+        stage32(staged, r, 32 * h, v, g0 ? a.scale : 1.f);
+      else if (key < sq.kl)
+        store32((g0 ? a.dk : a.dv) + row * HD + 32 * h, v, g0 ? a.scale : 1.f);
       __syncwarp();
+    }
+    if (tile) {
+      tc::fence_proxy_async();
+      asm volatile("bar.sync %0, 128;" ::"r"(2 + g0) : "memory");
+      if ((tid & 127) == 0) store_tile(g0 ? &a.mdk : &a.mdv, kh, sq.k0 + key0, staged);
     }
     tc::fence_before();
   }
@@ -292,7 +309,9 @@ struct QSmem {
   unsigned char q[TILE], dO[TILE];
   unsigned char slot[Q_SLOTS][TILE];
   uint64_t full[Q_SLOTS], empty[Q_SLOTS];
-  uint64_t barQ, barS, barD, barDs, barEnd;
+  // barS: of even and odd key tiles.  S runs one tile ahead of its readers, so a
+  // barrier for both could complete two phases before a late one has seen the first.
+  uint64_t barQ, barS[2], barD, barDs, barEnd;
   uint32_t tmem;
 };
 
@@ -309,17 +328,30 @@ __device__ __forceinline__ void dq(const AttnArgs& a, unsigned char* raw, int bl
   const int keys = max(0, min(sq.kl, min(tok0 + TT, sq.ql) + off));
   const int n = (keys + CH - 1) / CH;
 
-  if (tid == 0) {
+  const int nt = 2 * n;
+  auto load = [&](int t) {
+    load_rows(sm.slot[t % Q_SLOTS], (t & 1) ? &a.v : &a.k, kh, sq.k0 + (t / 2) * CH, &sm.full[t % Q_SLOTS]);
+  };
+  if (warp == 9 && lane == 0) {
     for (int k = 0; k < Q_SLOTS; ++k) {
       tc::mbar_init(&sm.full[k], 1);
       tc::mbar_init(&sm.empty[k], 1);
     }
     tc::mbar_init(&sm.barQ, 1);
-    tc::mbar_init(&sm.barS, 1);
+    tc::mbar_init(&sm.barS[0], 1);
+    tc::mbar_init(&sm.barS[1], 1);
     tc::mbar_init(&sm.barD, 1);
     tc::mbar_init(&sm.barEnd, 1);
     tc::mbar_init(&sm.barDs, 256);
     tc::mbar_fence_init();
+    if (n > 0) {  // the first loads at once
+      tc::arrive_expect_tx(&sm.barQ, 2u * 2u * 128u * (uint32_t)(TT * G));
+      for (int h = 0; h < 2; ++h) {
+        tc::tma_load_3d(sm.q + h * (TILE / 2), &a.q, 64 * h, kh * G, sq.q0 + tok0, &sm.barQ);
+        tc::tma_load_3d(sm.dO + h * (TILE / 2), &a.dO, 64 * h, kh * G, sq.q0 + tok0, &sm.barQ);
+      }
+      for (int t = 0; t < min(nt, Q_SLOTS); ++t) load(t);
+    }
   }
   if (warp == 0) tc::alloc(&sm.tmem, 512);
   tc::fence_before();
@@ -327,20 +359,12 @@ __device__ __forceinline__ void dq(const AttnArgs& a, unsigned char* raw, int bl
   tc::fence_after();
   const uint32_t tS = sm.tmem, tP = tS + 256, tQ = tS + 384;  // S of even and odd key tiles at 0 and 128
   tc::Wait w;
-  const int nt = 2 * n;
 
   if (warp == 9) {
     if (lane == 0 && n > 0) {
-      tc::arrive_expect_tx(&sm.barQ, 2u * 2u * 128u * (uint32_t)(TT * G));
-      for (int h = 0; h < 2; ++h) {
-        tc::tma_load_3d(sm.q + h * (TILE / 2), &a.q, 64 * h, kh * G, sq.q0 + tok0, &sm.barQ);
-        tc::tma_load_3d(sm.dO + h * (TILE / 2), &a.dO, 64 * h, kh * G, sq.q0 + tok0, &sm.barQ);
-      }
-      for (int t = 0; t < nt && w.ok; ++t) {
-        const int k = t % Q_SLOTS;
-        if (t >= Q_SLOTS) w.on(&sm.empty[k], t / Q_SLOTS - 1);
-        if (!w.ok) break;
-        load_rows(sm.slot[k], (t & 1) ? &a.v : &a.k, kh, sq.k0 + (t / 2) * CH, &sm.full[k]);
+      for (int t = Q_SLOTS; t < nt && w.ok; ++t) {
+        w.on(&sm.empty[t % Q_SLOTS], t / Q_SLOTS - 1);
+        if (w.ok) load(t);
       }
       if (w.ok) {
         w.on(&sm.barQ, 0);
@@ -360,7 +384,7 @@ __device__ __forceinline__ void dq(const AttnArgs& a, unsigned char* raw, int bl
       auto scores = [&](int i) {
         arrived(2 * i);
         tc::gemm128_by<false, false>(lead, tS + 128 * (i & 1), smem_u32(sm.q), slot(2 * i), false);
-        tc::commit_by(lead, &sm.barS);
+        tc::commit_by(lead, &sm.barS[i & 1]);
       };
       auto dscores = [&](int i) {
         arrived(2 * i + 1);
@@ -396,7 +420,7 @@ __device__ __forceinline__ void dq(const AttnArgs& a, unsigned char* raw, int bl
       const bool whole = key0 + CH - 1 <= lim;
       const uint32_t S = tS + 128 * (i & 1) + lane_base + 64 * g0;
       float p[64];
-      w.warp_on(&sm.barS, i);
+      w.warp_on(&sm.barS[i & 1], i >> 1);
       tc::fence_after();
       tc::ld64(S, p);
 #pragma unroll
@@ -425,6 +449,7 @@ __device__ __forceinline__ void dq(const AttnArgs& a, unsigned char* raw, int bl
     }
     if (n > 0) w.warp_on(&sm.barEnd, 0);
     tc::fence_after();
+    const bool tile = tok0 + TT <= sq.ql;  // (as dkv: through Q's place)
 #pragma unroll 1
     for (int h = 0; h < 2; ++h) {
       float v[32];
@@ -434,8 +459,16 @@ __device__ __forceinline__ void dq(const AttnArgs& a, unsigned char* raw, int bl
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = 0.f;
       }
-      if (valid) store32(a.dq + row * HD + 64 * g0 + 32 * h, v, a.scale);
+      if (tile)
+        stage32(sm.q, r, 64 * g0 + 32 * h, v, a.scale);
+      else if (valid)
+        store32(a.dq + row * HD + 64 * g0 + 32 * h, v, a.scale);
       __syncwarp();
+    }
+    if (tile) {
+      tc::fence_proxy_async();
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (tid == 0) store_tile(&a.mo, kh * G, sq.q0 + tok0, sm.q);
     }
     tc::fence_before();
   }

@@ -78,7 +78,11 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) k_attn_fwd(const __grid_consta
   }
   const float sc = a.scale * LOG2E;
 
-  if (tid == 0) {
+  const int nt = 2 * nmax;  // ring tiles: K, V of every key tile
+  auto load = [&](int t) {
+    load_rows(sm.slot[t % NSLOT], (t & 1) ? &a.v : &a.k, kh, sq.k0 + (kb + t / 2) * CH, &sm.full[t % NSLOT]);
+  };
+  if (warp == 9 && lane == 0) {
     for (int k = 0; k < NSLOT; ++k) {
       tc::mbar_init(&sm.full[k], 1);
       tc::mbar_init(&sm.empty[k], 1);
@@ -91,6 +95,9 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) k_attn_fwd(const __grid_consta
       tc::mbar_init(&sm.barP[w][1], 128);
     }
     tc::mbar_fence_init();
+    for (int x = 0; x < (dual ? 1 : 2); ++x)  // the first loads at once
+      if (n[x] > 0) load_group(sm.q[x], &a.q, kh, G, sq.q0 + tok0 + x * TT, &sm.barQ[x]);
+    for (int t = 0; t < min(nt, NSLOT); ++t) load(t);
   }
   if (warp == 0) tc::alloc(&sm.tmem, 512);
   tc::fence_before();
@@ -98,17 +105,12 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) k_attn_fwd(const __grid_consta
   tc::fence_after();
   const uint32_t tS = sm.tmem, tO = sm.tmem + 256;
   tc::Wait w;
-  const int nt = 2 * nmax;  // ring tiles: K, V of every key tile
 
   if (warp == 9) {
     if (lane == 0 && nmax > 0) {
-      for (int x = 0; x < (dual ? 1 : 2); ++x)
-        if (n[x] > 0) load_group(sm.q[x], &a.q, kh, G, sq.q0 + tok0 + x * TT, &sm.barQ[x]);
-      for (int t = 0; t < nt && w.ok; ++t) {
-        const int k = t % NSLOT;
-        if (t >= NSLOT) w.on(&sm.empty[k], t / NSLOT - 1);
-        if (!w.ok) break;
-        load_rows(sm.slot[k], (t & 1) ? &a.v : &a.k, kh, sq.k0 + (kb + t / 2) * CH, &sm.full[k]);
+      for (int t = NSLOT; t < nt && w.ok; ++t) {
+        w.on(&sm.empty[t % NSLOT], t / NSLOT - 1);
+        if (w.ok) load(t);
       }
       if (w.ok)  // no copy is in flight when the CTA ends
         for (int t = max(0, nt - NSLOT); t < nt; ++t) w.on(&sm.full[t % NSLOT], t / NSLOT);
@@ -259,6 +261,10 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) k_attn_fwd(const __grid_consta
     }
     if (n[x] > 0) w.warp_on(&sm.barO[x], 0);
     tc::fence_after();
+    // a whole tile leaves through shared memory (the Q tile, which the last scores have
+    // read) and one TMA store, rows of a part of one from their own threads
+    const int first = tok0 + (dual ? 0 : x * TT);
+    const bool tile = a.n_splits == 1 && first + TT <= sq.ql;
     if (any) {
       const long row = ((long)sq.q0 + tok) * a.Hq + kh * G + r % G;
       const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -274,7 +280,9 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) k_attn_fwd(const __grid_consta
 #pragma unroll
             for (int j = 0; j < 32; ++j) y[j] = 0.f;
           }
-          if (a.n_splits == 1) {
+          if (tile) {
+            stage32(sm.q[x], r, 32 * g, y, inv);
+          } else if (a.n_splits == 1) {
             store32(a.o + row * HD + 32 * g, y, inv);
           } else if (l > 0.f) {  // (the join reads a part only where its lse is finite)
             float* d = a.part + ((long)(2 * split + x) * a.total_q * a.Hq + row) * HD + 32 * g;
@@ -295,6 +303,11 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) k_attn_fwd(const __grid_consta
           a.lse[row] = lse;
         }
       }
+    }
+    if (tile) {
+      tc::fence_proxy_async();
+      asm volatile("bar.sync %0, 128;" ::"r"(1 + x) : "memory");
+      if ((tid & 127) == 0) store_tile(&a.mo, kh * G, sq.q0 + first, sm.q[x]);
     }
     tc::fence_before();
   }

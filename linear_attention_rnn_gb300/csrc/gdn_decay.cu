@@ -157,7 +157,9 @@ struct WalkSmem {
   unsigned char X[TILE];                // the entering state in bf16, [128 (b) rows x 128 (c)]
   alignas(16) float tab[CH];            // e^{w d}
   uint64_t full[NSLOT], empty[NSLOT];
-  uint64_t barP, barPm, barK[2], barS, barX, barO, barOf, barSt;
+  // barSt: of even and odd chunks.  The storing thread may be a chunk behind the
+  // writers; the slot that it frees keeps them from getting two ahead.
+  uint64_t barP, barPm, barK[2], barS, barX, barO, barOf, barSt[2];
   uint32_t tmem;
 };
 
@@ -244,7 +246,8 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
     tc::mbar_init(&sm.barK[1], 256);
     tc::mbar_init(&sm.barS, 256);
     tc::mbar_init(&sm.barOf, 256);
-    tc::mbar_init(&sm.barSt, 256);
+    tc::mbar_init(&sm.barSt[0], 256);
+    tc::mbar_init(&sm.barSt[1], 256);
     tc::mbar_fence_init();
     // The first tiles are requested at once.  After the prefix kernel q, k, v and dO
     // are complete already: it starts no dependent before its own wait is over,
@@ -265,7 +268,7 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
     if (lane == 0) {
       for (int it = 0; it < n_it && w.ok; ++it) {
         const int t = 3 * it + 2;
-        w.on(&sm.barSt, it);
+        w.on(&sm.barSt[it & 1], it >> 1);
         if (!w.ok) break;
         if (whole(it)) {
           const unsigned char* tile = sm.slot[t % NSLOT];
@@ -423,7 +426,7 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
           }
         }
         tc::fence_proxy_async();
-        tc::mbar_arrive(&sm.barSt);
+        tc::mbar_arrive(&sm.barSt[it & 1]);
       };
       for (int it = 0; it < n_it; ++it) {
         if (it > 0) output(it - 1);
@@ -648,7 +651,7 @@ __device__ __forceinline__ void fold_block(const DecayFoldArgs& a, FoldSmem& sm)
     tc::mbar_fence_init();
     for (int t = 0; t < min(nt, FOLD_SLOTS); ++t) load(t);
   }
-  if (warp == 0) tc::alloc(&sm.tmem, 128);
+  if (warp == 0) tc::alloc(&sm.tmem, 512);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -675,10 +678,13 @@ __device__ __forceinline__ void fold_block(const DecayFoldArgs& a, FoldSmem& sm)
         w.warp_on(&sm.barK[h], i);
         tc::fence_after();
         const uint32_t c = smem_u32(sm.slot[tcc % FOLD_SLOTS]) + 8192 * h;
-        tc::gemm_rows_by<64, 128>(lead, tX, smem_u32(sm.slot[tb % FOLD_SLOTS]) + 8192 * h, c, i > 0 || h > 0);
+        // The tensor cores' fp32 sums lose a little at every step: the first terms of
+        // even and odd chunks and the small further terms have sums of their own.
+        const uint32_t t0 = tX + 128 * (i & 1), t1 = tX + 256 + 128 * (i & 1);
+        tc::gemm_rows_by<64, 128>(lead, t0, smem_u32(sm.slot[tb % FOLD_SLOTS]) + 8192 * h, c, i > 1 || h > 0);
 #pragma unroll
         for (int t = 0; t < FOLD_TERMS - 1; ++t)
-          tc::gemm_rows_by<64, 128>(lead, tX, smem_u32(sm.rest[t]) + 8192 * h, c, true);
+          tc::gemm_rows_by<64, 128>(lead, t1, smem_u32(sm.rest[t]) + 8192 * h, c, i > 1 || h > 0 || t > 0);
         if (h == 1) {
           if (tb + FOLD_SLOTS < 2 * nc) tc::commit_by(lead, &sm.empty[tb % FOLD_SLOTS]);
           if (tcc + FOLD_SLOTS < 2 * nc) tc::commit_by(lead, &sm.empty[tcc % FOLD_SLOTS]);
@@ -716,7 +722,15 @@ __device__ __forceinline__ void fold_block(const DecayFoldArgs& a, FoldSmem& sm)
 #pragma unroll 1
     for (int g = g0; g < g0 + 2; ++g) {
       float v[32];
-      tc::ld32(tX + lane_base + 32 * g, v);
+      tc::ld32(tX + 256 + lane_base + 32 * g, v);
+#pragma unroll 1
+      for (int k = 384; k >= 0; k -= 128) {  // the small sums first; odd chunks' where there were any
+        if (k == 256 || (k & 128 && nc == 1)) continue;
+        float y[32];
+        tc::ld32(tX + k + lane_base + 32 * g, y);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] += y[i];
+      }
 #pragma unroll
       for (int i = 0; i < 32; i += 4) {
         const int c = 32 * g + i;
@@ -733,7 +747,7 @@ __device__ __forceinline__ void fold_block(const DecayFoldArgs& a, FoldSmem& sm)
   if (!w.ok && a.status) atomicOr(a.status, 1);
   __syncthreads();
   tc::fence_after();
-  if (warp == 0) tc::dealloc(sm.tmem, 128);
+  if (warp == 0) tc::dealloc(sm.tmem, 512);
 }
 
 // A segment's own state; with one segment to a sequence the final state itself,

@@ -201,6 +201,7 @@ struct DecayFoldArgs {
 struct AttnArgs {
   CUtensorMap q, k, v;  // q: boxes of 64 columns x a group's heads x 128 / G tokens; k, v: x 1 head x 128 rows
   CUtensorMap dO;       // as q (backward)
+  CUtensorMap mo, mdk, mdv;  // outputs: o or dq as q (plain rows), dk and dv as k
   const int* cu_q;      // [n_seqs + 1] (null: equal lengths), cu_k alike
   const int* cu_k;
   const int* k_len;     // [n_seqs] used rows of each sequence's keys (nullable; forward)

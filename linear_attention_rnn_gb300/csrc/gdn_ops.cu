@@ -33,6 +33,12 @@ int sm_count() {
 // rows of H heads, `stride` elements apart: whole 16-byte pieces that do not overlap
 inline bool row_stride_ok(long long stride, int H) { return stride >= (long long)H * HD && stride % 8 == 0; }
 
+// A workspace that would hold the status word alone may be left out.
+constexpr size_t STATUS_BYTES = ALIGN;
+inline bool workspace_ok(const void* ws, size_t ws_bytes, size_t need) {
+  return ws ? ws_bytes >= need : need <= STATUS_BYTES;
+}
+
 // ---- linear attention with a decay for each head -----------------------------------
 struct DecayPlan {
   int nseg, seg_chunks, slots;
@@ -283,12 +289,12 @@ int gdn_decay_fwd(const void* q, const void* k, const void* v, const float* deca
   if (total == 0) return pass_state(h0, hT, n_seqs, Hv, s);
   if (!q || !k || !v || !decay || !o) return GDN_ERR_ARG;
   const DecayPlan p = decay_plan(0, n_seqs, total, max_seqlen, Hk, Hv);
-  if (!ws || ws_bytes < p.total) return GDN_ERR_WORKSPACE;
+  if (!workspace_ok(ws, ws_bytes, p.total)) return GDN_ERR_WORKSPACE;
   DecayArgs a;
   memset(&a, 0, sizeof a);
   a.decay = decay;
   a.cu = cu_seqlens;
-  a.status = at<int>(ws, p.status);
+  a.status = ws ? at<int>(ws, p.status) : nullptr;
   a.n_seqs = n_seqs;
   a.total = total;
   a.T = total / n_seqs;
@@ -339,12 +345,12 @@ int gdn_decay_bwd(const void* q, const void* k, const void* v, const float* deca
   if (total == 0) return pass_state(dhT, dh0, n_seqs, Hv, s);
   if (!q || !k || !v || !decay || !dO || !dq || !dk || !dv) return GDN_ERR_ARG;
   const DecayPlan p = decay_plan(1, n_seqs, total, max_seqlen, Hk, Hv);
-  if (!ws || ws_bytes < p.total) return GDN_ERR_WORKSPACE;
+  if (!workspace_ok(ws, ws_bytes, p.total)) return GDN_ERR_WORKSPACE;
   DecayArgs a;
   memset(&a, 0, sizeof a);
   a.decay = decay;
   a.cu = cu_seqlens;
-  a.status = at<int>(ws, p.status);
+  a.status = ws ? at<int>(ws, p.status) : nullptr;
   a.n_seqs = n_seqs;
   a.total = total;
   a.T = total / n_seqs;
@@ -438,14 +444,15 @@ int gdn_attn_fwd(const void* q, const void* k, const void* v, const int* cu_q, c
   if (n_seqs == 0 || total_q == 0) return GDN_OK;
   if (!q || !o || (total_k > 0 && (!k || !v))) return GDN_ERR_ARG;
   const AttnPlan p = attn_plan(0, n_seqs, total_q, max_k < total_k ? max_k : total_k, Hq, Hk);
-  if (!ws || ws_bytes < p.total) return GDN_ERR_WORKSPACE;
+  if (!workspace_ok(ws, ws_bytes, p.total)) return GDN_ERR_WORKSPACE;
   AttnArgs a;
   if ((rc = attn_args(a, q, k, v, cu_q, cu_k, n_seqs, total_q, total_k, Hq, Hk, scale, q_stride, k_stride, v_stride)))
     return rc;
+  if (!tmap_rows(&a.mo, o, total_q, Hq, HD, (uint64_t)Hq * HD * 2, Hq / Hk, CH / (Hq / Hk))) return GDN_ERR_CUDA;
   a.k_len = k_len;
   a.o = static_cast<bf16*>(o);
   a.lse = lse;
-  a.status = at<int>(ws, p.status);
+  a.status = ws ? at<int>(ws, p.status) : nullptr;
   a.split_tiles = p.split_tiles;
   a.n_splits = p.n_splits;
   a.part = at<float>(ws, p.part);
@@ -475,11 +482,15 @@ int gdn_attn_bwd(const void* q, const void* k, const void* v, const void* o, con
     return nk ? cuda_status(cudaMemsetAsync(dv, 0, nk, s)) : GDN_OK;
   }
   const AttnPlan p = attn_plan(1, n_seqs, total_q, total_k, Hq, Hk);
-  if (!ws || ws_bytes < p.total) return GDN_ERR_WORKSPACE;
+  if (!workspace_ok(ws, ws_bytes, p.total)) return GDN_ERR_WORKSPACE;
   AttnArgs a;
   if ((rc = attn_args(a, q, k, v, cu_q, cu_k, n_seqs, total_q, total_k, Hq, Hk, scale, q_stride, k_stride, v_stride)))
     return rc;
-  if (!tmap_rows(&a.dO, dO, total_q, Hq, HD, (uint64_t)Hq * HD * 2, Hq / Hk, CH / (Hq / Hk))) return GDN_ERR_CUDA;
+  if (!tmap_rows(&a.dO, dO, total_q, Hq, HD, (uint64_t)Hq * HD * 2, Hq / Hk, CH / (Hq / Hk)) ||
+      !tmap_rows(&a.mo, dq, total_q, Hq, HD, (uint64_t)Hq * HD * 2, Hq / Hk, CH / (Hq / Hk)) ||
+      !tmap_rows(&a.mdk, dk, total_k, Hk, HD, (uint64_t)Hk * HD * 2, 1, CH) ||
+      !tmap_rows(&a.mdv, dv, total_k, Hk, HD, (uint64_t)Hk * HD * 2, 1, CH))
+    return GDN_ERR_CUDA;
   a.lse = const_cast<float*>(lse);
   a.dOp = static_cast<const bf16*>(dO);
   a.op = static_cast<const bf16*>(o);
@@ -487,7 +498,7 @@ int gdn_attn_bwd(const void* q, const void* k, const void* v, const void* o, con
   a.dq = static_cast<bf16*>(dq);
   a.dk = static_cast<bf16*>(dk);
   a.dv = static_cast<bf16*>(dv);
-  a.status = at<int>(ws, p.status);
+  a.status = ws ? at<int>(ws, p.status) : nullptr;
   return cuda_status(launch_attn_bwd(a, s));
 }
 

@@ -18,6 +18,7 @@ def delta_step(q, k, v, g, beta, state, slots):
     """(o, state): one token per row of the gated delta rule (rows with a slot
     below 0 have no state and give zero)."""
     q, k, v, g, beta, state = map(_d, (q, k, v, g, beta, state))
+    state = state.clone()
     G = v.shape[1] // k.shape[1]
     o = torch.zeros_like(v)
     for r, s in enumerate(slots):
@@ -33,6 +34,7 @@ def delta_step(q, k, v, g, beta, state, slots):
 
 def decay_step(q, k, v, decay, state, slots):
     q, k, v, decay, state = map(_d, (q, k, v, decay, state))
+    state = state.clone()
     G = v.shape[1] // k.shape[1]
     o = torch.zeros_like(v)
     for r, s in enumerate(slots):
