@@ -509,10 +509,12 @@ def decay_fwd(q, k, v, decay, h0=None, *, cu_seqlens=None, max_seqlen=None, want
     _check(h0, "h0", torch.float32, (n, Hv, dk, dv))
     if o is None:
         o = torch.empty(v.shape, dtype=torch.bfloat16, device=dev)
-    _check(o, "o", torch.bfloat16, tuple(v.shape))
-    if want_hT and hT is None:
+    else:
+        _check(o, "o", torch.bfloat16, v.shape)
+    if hT is not None:
+        _check(hT, "hT", torch.float32, (n, Hv, dk, dv))
+    elif want_hT:
         hT = torch.empty((n, Hv, dk, dv), dtype=torch.float32, device=dev)
-    _check(hT, "hT", torch.float32, (n, Hv, dk, dv))
     wp, wn, ws = _scratch(decay_workspace_bytes(0, n, total, longest, Hk, Hv, dk, dv), dev,
                           workspace)  # (ws: kept alive over the call)
     rc = lib().gdn_decay_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(h0), _ptr(cu_seqlens),
@@ -594,10 +596,12 @@ def attn_fwd(q, k, v, *, cu_q=None, cu_k=None, k_len=None, max_q=None, max_k=Non
     longest = int(max_k) if max_k is not None else (k.shape[1] if cu_k is None else total_k)
     if o is None:
         o = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
-    _check(o, "o", torch.bfloat16, tuple(q.shape))
-    if want_lse and lse is None:
+    else:
+        _check(o, "o", torch.bfloat16, q.shape)
+    if lse is not None:
+        _check(lse, "lse", torch.float32, q.shape[:-1])
+    elif want_lse:
         lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
-    _check(lse, "lse", torch.float32, tuple(q.shape[:-1]))
     wp, wn, ws = _scratch(attn_workspace_bytes(0, n, total_q, total_k, longest, Hq, Hk, d), dev,
                           workspace)  # (ws: kept alive over the call)
     rc = lib().gdn_attn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_q), _ptr(cu_k), _ptr(k_len), _ptr(o),

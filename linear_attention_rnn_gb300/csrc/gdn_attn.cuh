@@ -19,43 +19,56 @@ constexpr float LOG2E = 1.4426950408889634f;
 struct Seq {
   int q0, ql, k0, kl;  // first row and rows of q, first row and used rows of k
 };
-// (held inside the tensors whatever the arrays say)
-__device__ __forceinline__ Seq seq_of(const AttnArgs& a, int s) {
+// Sequence s of n_seqs over `total` rows (cu null: equal lengths), as (first row,
+// rows), held inside the tensor whatever the array says.
+__device__ __forceinline__ int2 rows_of(const int* cu, int s, int n_seqs, int total) {
+  if (!cu) return make_int2(s * (total / n_seqs), total / n_seqs);
+  const int a = min(max(cu[s], 0), total);
+  return make_int2(a, min(max(cu[s + 1], a), total) - a);
+}
+// Both sides of the first 32 sequences, one to a lane, read at the kernel's start,
+// where one trip to memory fetches them all.
+struct Lanes {
+  int2 q, k;
+  int used;
+};
+__device__ __forceinline__ Lanes read_lanes(const AttnArgs& a) {
+  const int s = min((int)(threadIdx.x & 31), a.n_seqs - 1);
+  Lanes l;
+  l.q = rows_of(a.cu_q, s, a.n_seqs, a.total_q);
+  l.k = rows_of(a.cu_k, s, a.n_seqs, a.total_k);
+  l.used = a.k_len ? min(max(a.k_len[s], 0), l.k.y) : l.k.y;
+  return l;
+}
+__device__ __forceinline__ Seq seq_of(const AttnArgs& a, const Lanes& l, int s) {
+  int2 q, k;
+  int used;
+  if (s < 32) {
+    q = make_int2(__shfl_sync(0xffffffffu, l.q.x, s), __shfl_sync(0xffffffffu, l.q.y, s));
+    k = make_int2(__shfl_sync(0xffffffffu, l.k.x, s), 0);
+    used = __shfl_sync(0xffffffffu, l.used, s);
+  } else {
+    q = rows_of(a.cu_q, s, a.n_seqs, a.total_q);
+    k = rows_of(a.cu_k, s, a.n_seqs, a.total_k);
+    used = a.k_len ? min(max(a.k_len[s], 0), k.y) : k.y;
+  }
   Seq r;
-  if (a.cu_q) {
-    r.q0 = min(max(a.cu_q[s], 0), a.total_q);
-    r.ql = min(max(a.cu_q[s + 1], r.q0), a.total_q) - r.q0;
-  } else {
-    r.ql = a.total_q / a.n_seqs;
-    r.q0 = s * r.ql;
-  }
-  if (a.cu_k) {
-    r.k0 = min(max(a.cu_k[s], 0), a.total_k);
-    r.kl = min(max(a.cu_k[s + 1], r.k0), a.total_k) - r.k0;
-  } else {
-    r.kl = a.total_k / a.n_seqs;
-    r.k0 = s * r.kl;
-  }
-  if (a.k_len) r.kl = min(max(a.k_len[s], 0), r.kl);
+  r.q0 = q.x;
+  r.ql = q.y;
+  r.k0 = k.x;
+  r.kl = used;
   return r;
 }
 
 // The rank-th tile of all sequences' tiles of K rows, those with the highest index
 // in their sequence first (the work of a tile grows with it, and CTAs start in
-// order of rank); sequence -1: there are fewer.  cu null: `each` rows to a
-// sequence.  Every warp finds it for itself: a lane counts for every 32nd
-// sequence, and the index of rank's tile is found by bisection.
-__device__ __forceinline__ int2 find_tile(const int* cu, int n_seqs, int total, int K, int rank) {
-  const int lane = threadIdx.x & 31, each = total / n_seqs;
-  auto tiles = [&](int s) {
-    int len = each;
-    if (cu) {
-      const int a = min(max(cu[s], 0), total);
-      len = min(max(cu[s + 1], a), total) - a;
-    }
-    return (len + K - 1) / K;
-  };
-  const int n0 = lane < n_seqs ? tiles(lane) : 0;  // (the first 32 stay in registers)
+// order of rank); sequence -1: there are fewer.  Every warp finds it for itself: a
+// lane counts for every 32nd sequence (lane_rows: its first one's rows), and the
+// index of rank's tile is found by bisection.
+__device__ __forceinline__ int2 find_tile(const int* cu, int lane_rows, int n_seqs, int total, int K, int rank) {
+  const int lane = threadIdx.x & 31;
+  auto tiles = [&](int s) { return (rows_of(cu, s, n_seqs, total).y + K - 1) / K; };
+  const int n0 = lane < n_seqs ? (lane_rows + K - 1) / K : 0;  // (the first 32 stay in registers)
   auto count_above = [&](int t) {                  // tiles of index t or more
     int c = max(n0 - t, 0);
     for (int s = lane + 32; s < n_seqs; s += 32) c += max(tiles(s) - t, 0);

@@ -78,9 +78,10 @@ __device__ __forceinline__ void dkv(const AttnArgs& a, unsigned char* raw, int b
   const int tid = threadIdx.x, lane = tid & 31, warp = tc::warp_index();
   const int G = a.Hq / a.Hk, TT = CH / G;
   const int kh = block % a.Hk;
-  const int2 at = find_tile(a.cu_k, a.n_seqs, a.total_k, CH, block / a.Hk);
+  const Lanes lanes = read_lanes(a);
+  const int2 at = find_tile(a.cu_k, lanes.k.y, a.n_seqs, a.total_k, CH, block / a.Hk);
   if (at.x < 0) return;
-  const Seq sq = seq_of(a, at.x);
+  const Seq sq = seq_of(a, lanes, at.x);
   // (a sequence's first keys are seen by the most queries: index 0 is its last tile)
   const int key0 = ((sq.kl + CH - 1) / CH - 1 - at.y) * CH, off = sq.kl - sq.ql;
   const int first = max(0, key0 - off) / TT;                 // first query tile that sees key0
@@ -320,9 +321,10 @@ __device__ __forceinline__ void dq(const AttnArgs& a, unsigned char* raw, int bl
   const int tid = threadIdx.x, lane = tid & 31, warp = tc::warp_index();
   const int G = a.Hq / a.Hk, TT = CH / G;
   const int kh = block % a.Hk;
-  const int2 at = find_tile(a.cu_q, a.n_seqs, a.total_q, TT, block / a.Hk);
+  const Lanes lanes = read_lanes(a);
+  const int2 at = find_tile(a.cu_q, lanes.q.y, a.n_seqs, a.total_q, TT, block / a.Hk);
   if (at.x < 0) return;
-  const Seq sq = seq_of(a, at.x);
+  const Seq sq = seq_of(a, lanes, at.x);
   const int tok0 = at.y * TT, off = sq.kl - sq.ql;
   if (tok0 >= sq.ql) return;
   const int keys = max(0, min(sq.kl, min(tok0 + TT, sq.ql) + off));

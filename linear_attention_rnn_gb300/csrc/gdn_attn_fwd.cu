@@ -33,7 +33,13 @@ namespace {
 using namespace attn;
 
 constexpr int NSLOT = 5;
-constexpr int FWD_THREADS = 256 + 64;
+// Three groups of four warps: two of softmax, one whose first two warps issue and
+// load.  At 384 threads a block may have 168 registers a thread; the third group
+// hands most of its own over (2 x 208 + 88 = 3 x 168), and a softmax row's 128
+// values stay in registers.
+constexpr int FWD_THREADS = 384;
+constexpr int REGS_LAUNCH = 168, REGS_SOFTMAX = 208, REGS_ISSUE = 88;
+static_assert(2 * REGS_SOFTMAX + REGS_ISSUE <= 3 * REGS_LAUNCH, "the groups' registers come from the block's");
 constexpr float RAISE = 8.f;  // base-2 headroom before the running maximum is raised
 
 struct FwdSmem {
@@ -53,9 +59,10 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) k_attn_fwd(const __grid_consta
   if (blockIdx.y == 0) clear_status(a.status);
   const int G = a.Hq / a.Hk, TT = CH / G;  // tokens to a tile
   const int kh = blockIdx.x % a.Hk, split = blockIdx.y;
-  const int2 at = find_tile(a.cu_q, a.n_seqs, a.total_q, 2 * TT, (int)(blockIdx.x / a.Hk));
+  const Lanes lanes = read_lanes(a);
+  const int2 at = find_tile(a.cu_q, lanes.q.y, a.n_seqs, a.total_q, 2 * TT, (int)(blockIdx.x / a.Hk));
   if (at.x < 0) return;
-  const Seq sq = seq_of(a, at.x);
+  const Seq sq = seq_of(a, lanes, at.x);
   const int off = sq.kl - sq.ql;
   const int tok0 = at.y * 2 * TT;
   if (tok0 >= sq.ql) return;
@@ -106,6 +113,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) k_attn_fwd(const __grid_consta
   const uint32_t tS = sm.tmem, tO = sm.tmem + 256;
   tc::Wait w;
 
+  if (warp >= 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_ISSUE));
   if (warp == 9) {
     if (lane == 0 && nmax > 0) {
       for (int t = NSLOT; t < nt && w.ok; ++t) {
@@ -179,7 +188,9 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) k_attn_fwd(const __grid_consta
         }
       }
     }
+  }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
     const int x = warp >> 2, r = 32 * (warp & 3) + lane;
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t S = tS + 128 * x + lane_base, O = tO + 128 * x + lane_base;
@@ -354,6 +365,10 @@ cudaError_t launch_attn_fwd(const AttnArgs& a, cudaStream_t s) {
   static_assert(smem <= 227 * 1024, "shared memory");
   cudaError_t e = cudaFuncSetAttribute(k_attn_fwd, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
+  // (the register hand-over waits for ever where the block was launched with fewer)
+  cudaFuncAttributes fa;
+  if ((e = cudaFuncGetAttributes(&fa, k_attn_fwd)) != cudaSuccess) return e;
+  if (fa.numRegs < REGS_LAUNCH) return cudaErrorInvalidConfiguration;
   const int K = 2 * (CH / (a.Hq / a.Hk));
   const dim3 grid((unsigned)a.Hk * (unsigned)(a.total_q / K + a.n_seqs), (unsigned)a.n_splits);
   e = launch_pdl(k_attn_fwd, grid, dim3(FWD_THREADS), smem, s, a);

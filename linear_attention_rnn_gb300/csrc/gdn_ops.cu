@@ -138,23 +138,26 @@ struct AttnPlan {
   size_t status, part, part_lse, delta, total;
 };
 
-// Key splits of the forward.  A CTA holds 256 / G tokens of one key head; calls
-// with fewer of them than two to an SM, over more than 8 key tiles, are split
-// into four CTAs to an SM (by the longest sequence, so that ragged lengths
-// leave fewer of them with work), of 8 key tiles or more.
+// Key splits of the forward.  A CTA holds 256 / G tokens of one key head.  The
+// estimate, in key tiles of a CTA (0.8 us measured): the work of all CTAs over the
+// SMs, contexts being 0.6 of the longest one on average, most of the longest
+// CTA's behind it, 6 for a CTA's start and end, 4 for the join.
 AttnPlan attn_plan(int backward, int n_seqs, int total_q, int max_k, int Hq, int Hk) {
   AttnPlan p;
   memset(&p, 0, sizeof p);
   const long tiles = ((long)max_k + CH - 1) / CH;
-  const long ctas = ((long)total_q / (2 * (CH / (Hq / Hk))) + n_seqs) * Hk;
-  const long sms = sm_count();
+  const double ctas = (double)((long)total_q / (2 * (CH / (Hq / Hk))) + n_seqs) * Hk, sms = sm_count();
   p.split_tiles = tiles > 0 ? (int)tiles : 1;
   p.n_splits = 1;
-  if (!backward && ctas < 2 * sms && tiles > 8) {
-    long per = (ctas * tiles + 4 * sms - 1) / (4 * sms);
-    if (per < 8) per = 8;
-    p.split_tiles = (int)per;
-    p.n_splits = (int)((tiles + per - 1) / per);
+  double best = 1e300;
+  for (long k = 1; !backward && k <= 64 && 4 * k <= tiles + 3; ++k) {
+    const long per = (tiles + k - 1) / k, splits = (tiles + per - 1) / per;
+    const double t = ctas * (0.6 * tiles + 6.0 * splits) / sms + 0.8 * (per + 6.0) + (splits > 1 ? 4.0 : 0.0);
+    if (t < best * 0.97) {
+      best = t;
+      p.split_tiles = (int)per;
+      p.n_splits = (int)splits;
+    }
   }
   size_t off = 0;
   auto take = [&](size_t bytes) {
