@@ -215,22 +215,40 @@ __device__ __forceinline__ void first_state(const DecayRole& R, unsigned char* s
   }
 }
 
+// Waits (bounded, by a whole warp) until the flag is `value` or more and what was
+// written before it can be read.
+__device__ __forceinline__ bool wait_flag(const int* flag, int value) {
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) {
+    const long long t0 = clock64();
+    for (int v = 0;;) {
+      asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(flag) : "memory");
+      if (v >= value) break;
+      if (clock64() - t0 > tc::WAIT_LIMIT_CYCLES) {
+        ok = false;
+        break;
+      }
+      __nanosleep(100);
+    }
+  }
+  return __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+}
+
 // One CTA's walk over the chunks [cb, ce) of head hd in sequence s (rows q); REV: backwards.
 template <bool SUM, bool REV>
 __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, WalkSmem& sm, const Range q, int s,
                                      int slot_id, int hd, int cb, int ce) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tc::warp_index();
-  const int G = a.Hv / a.Hk, loops = SUM ? G : 1, nc = ce - cb;
-  const int n_it = loops * nc;
-  auto chunk_of = [&](int it) { return REV ? ce - 1 - it % nc : cb + it % nc; };
-  auto head_of = [&](int it) { return SUM ? hd * G + it / nc : hd; };  // value head
+  const int n_it = ce - cb, G = a.Hv / a.Hk, kh = hd / G;
+  const int g = hd - kh * G, ho = R.shared ? kh : hd;  // place in the group, output head
+  auto chunk_of = [&](int it) { return REV ? ce - 1 - it : cb + it; };
   auto rows_of = [&](int c) { return min(CH, q.len - c * CH); };
 
   auto load = [&](int t) {  // tile t (a, b, c of every chunk) into its slot
-    const int it = t / 3, kind = t % 3, row = q.start + chunk_of(it) * CH, j = head_of(it);
+    const int kind = t % 3, row = q.start + chunk_of(t / 3) * CH;
     const CUtensorMap* m = kind == 0 ? &R.a : kind == 1 ? &R.b : &R.c;
     const int per_v = kind == 0 ? R.ha : kind == 1 ? R.hb : R.hc;
-    load_tile(sm.slot[t % NSLOT], m, per_v ? j : j / G, row, &sm.full[t % NSLOT]);
+    load_tile(sm.slot[t % NSLOT], m, per_v ? hd : kh, row, &sm.full[t % NSLOT]);
   };
   const int nt = 3 * n_it;
   if (warp == 17 && lane == 0) {
@@ -261,8 +279,8 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
   const uint32_t tP = sm.tmem, tO1 = tP + 128, tO2 = tP + 256, tX = tP + 384;
   tc::Wait w;
 
-  // whether chunk `it`'s output rows are stored as a tile: a whole chunk of the last head summed
-  auto whole = [&](int it) { return it >= n_it - nc && rows_of(chunk_of(it)) == CH; };
+  // whether chunk `it`'s output rows are stored as a tile: a whole chunk, of the last head summed
+  auto whole = [&](int it) { return (!SUM || g == G - 1) && rows_of(chunk_of(it)) == CH; };
 
   if (warp == 18) {  // ---- output tiles: staged in the slot of the chunk's C, which O has consumed
     if (lane == 0) {
@@ -273,8 +291,8 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
         if (whole(it)) {
           const unsigned char* tile = sm.slot[t % NSLOT];
           const int row = q.start + chunk_of(it) * CH;
-          tc::tma_store_3d(&R.o, 0, hd, row, tile);
-          tc::tma_store_3d(&R.o, 64, hd, row, tile + TILE / 2);
+          tc::tma_store_3d(&R.o, 0, ho, row, tile);
+          tc::tma_store_3d(&R.o, 64, ho, row, tile + TILE / 2);
           tc::bulk_commit();
           tc::bulk_wait_read();
         }
@@ -337,7 +355,7 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
     // rows: thread (r, half) has row r = TMEM lane r and 64 of its 128 columns.
     const int half = (warp >> 2) & 1, r = 32 * (warp & 3) + lane;
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16, cols = lane_base + 64 * half;
-    float wd = 0.f;
+    const float wd = a.decay[hd];
     if (warp < 8) {
       const int own = warp & 3, Ho = R.shared ? a.Hk : a.Hv;
       // O of chunk `it`, whose products have been issued
@@ -346,7 +364,7 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
         const float f = expf(wd * (float)(REV ? max(n - 1 - r, 0) : r + 1));
         const bool tile = whole(it);
         const long row = (long)q.start + (long)c * CH + r;
-        bf16* dst = R.out + (row * Ho + hd) * HD + 64 * half;
+        bf16* dst = R.out + (row * Ho + ho) * HD + 64 * half;
         unsigned char* staged = sm.slot[(3 * it + 2) % NSLOT];
         auto put = [&](int j, const float* x) {  // columns 8 j .. 8 j + 7 of the half
           const uint4 o = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
@@ -375,28 +393,31 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
             __syncwarp();
           }
         } else {
-          // running sums over the value heads, [head][4-column group][row], this thread's
-          // own; 32 columns of them are requested before the products are waited for
-          const bool add = it >= nc && r < n, last = it >= n_it - nc;
-          float4* acc = reinterpret_cast<float4*>(R.acc) + ((long)hd * 32 + 16 * half) * a.total + row;
-          float4 p[8];
-          auto request = [&](int g) {
+          // The sum over the value heads runs from CTA to CTA, [head][4-column group][row]
+          // in the workspace: the warp of one CTA that holds these rows and columns writes
+          // its sum, and a flag of its own says so to the same warp of the next one.
+          const bool add = g > 0 && r < n, last = g == G - 1;
+          float4* acc = reinterpret_cast<float4*>(R.acc) + ((long)kh * 32 + 16 * half) * a.total + row;
+          int* flag = R.flags + ((long)kh * (a.total / CH + a.n_seqs) + first_slot(a.cu, s, a.T, a.total, CH) + c) * 8 + warp;
+          if (g > 0) w.ok = wait_flag(flag, g) && w.ok;
+          float4 p[8];  // 32 columns of it are requested before the products are waited for
+          auto request = [&](int k) {
             if (add) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) p[i] = acc[(long)(8 * g + i) * a.total];
+              for (int i = 0; i < 8; ++i) p[i] = acc[(long)(8 * k + i) * a.total];
             }
           };
           request(0);
           w.warp_on(&sm.barO, it);
           tc::fence_after();
 #pragma unroll 1
-          for (int g = 0; g < 2; ++g) {
+          for (int k = 0; k < 2; ++k) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               float x[16], y[16];
-              tc::ld16(tO1 + cols + 32 * g + 16 * h, x);
-              tc::ld16(tO2 + cols + 32 * g + 16 * h, y);
-              if (g == 1 && h == 1) {
+              tc::ld16(tO1 + cols + 32 * k + 16 * h, x);
+              tc::ld16(tO2 + cols + 32 * k + 16 * h, y);
+              if (k == 1 && h == 1) {
                 tc::fence_before();
                 tc::mbar_arrive(&sm.barOf);
               }
@@ -412,30 +433,30 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
                 }
               }
               if (last) {
-                put(4 * g + 2 * h, x);
-                put(4 * g + 2 * h + 1, x + 8);
+                put(4 * k + 2 * h, x);
+                put(4 * k + 2 * h + 1, x + 8);
               } else if (r < n) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                  acc[(long)(8 * g + 4 * h + i) * a.total] =
+                  acc[(long)(8 * k + 4 * h + i) * a.total] =
                       make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
               }
               __syncwarp();
             }
-            if (g == 0) request(1);
+            if (k == 0) request(1);
+          }
+          if (!last) {
+            __syncwarp();
+            if (lane == 0) asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(flag), "r"(g + 1) : "memory");
           }
         }
         tc::fence_proxy_async();
         tc::mbar_arrive(&sm.barSt[it & 1]);
       };
+      if (half == 0) sm.tab[r] = expf(wd * (float)r);
+      asm volatile("bar.sync 1, 256;" ::: "memory");
       for (int it = 0; it < n_it; ++it) {
         if (it > 0) output(it - 1);
-        if (it % nc == 0) {  // a new head: its table of decays
-          wd = a.decay[head_of(it)];
-          asm volatile("bar.sync 1, 256;" ::: "memory");
-          if (half == 0) sm.tab[r] = expf(wd * (float)r);
-          asm volatile("bar.sync 1, 256;" ::: "memory");
-        }
         const int n = rows_of(chunk_of(it));
         w.warp_on(&sm.barP, it);
         tc::fence_after();
@@ -483,36 +504,27 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
       }
       output(n_it - 1);
     } else {
-      const float* x0 = nullptr;
-      float keep = 1.f;
+      if (a.nseg > 1 && !a.beside) {  // the entering states come from the kernel before
+        pdl_wait();
+        pdl_release();
+      }
+      const float* x0 = R.xseg ? R.xseg + ((long)slot_id * a.Hv + hd) * HD * HD
+                               : (R.x0 ? R.x0 + ((long)s * a.Hv + hd) * HD * HD : nullptr);
+#pragma unroll 1
+      for (int k = 0; k < 2; ++k) {
+        float v[32];
+        first_state(R, sm.lo, x0, r, 64 * half + 32 * k, v);
+        tc::st32(tX + cols + 32 * k, v);
+      }
+      tc::wait_st();
+      asm volatile("bar.sync 2, 256;" ::: "memory");  // (the staged state has been read)
       for (int it = 0; it < n_it; ++it) {
         const int n = rows_of(chunk_of(it));
-        const bool first = it % nc == 0;
-        if (first) {
-          const int j = head_of(it);
-          const long sh = (long)s * a.Hv + j;
-          wd = a.decay[j];
-          x0 = R.xseg ? R.xseg + ((long)slot_id * a.Hv + j) * HD * HD : (R.x0 ? R.x0 + sh * HD * HD : nullptr);
-          if (it == 0 && a.nseg > 1 && !a.beside) {  // the entering states come from the kernel before
-            pdl_wait();
-            pdl_release();
-          }
-        }
-        keep = expf(wd * (float)n);
+        const float keep = expf(wd * (float)n);
         // ---- the state: bf16 image of X, X <- e^{w n} X
         if (it > 0) {
           w.warp_on(&sm.barX, it - 1);
           tc::fence_after();
-        }
-        if (first) {
-#pragma unroll 1
-          for (int g = 0; g < 2; ++g) {
-            float v[32];
-            first_state(R, sm.lo, x0, r, 64 * half + 32 * g, v);
-            tc::st32(tX + cols + 32 * g, v);
-          }
-          tc::wait_st();
-          asm volatile("bar.sync 2, 256;" ::: "memory");  // (the staged state has been read)
         }
 #pragma unroll 1
         for (int g = 0; g < 2; ++g) {
@@ -571,27 +583,27 @@ __device__ __forceinline__ void walk_block(const DecayArgs& a, WalkSmem& sm) {
   // pass, then segment, sequence and head of this CTA
   int u = blockIdx.x, ri = 0;
   for (; ri < a.n_roles - 1; ++ri) {
-    const int units = a.slots * (a.role[ri].shared ? a.Hk : a.Hv);
+    const int units = a.slots * a.Hv;
     if (u < units) break;
     u -= units;
   }
   const DecayRole& R = a.role[ri];
-  const int heads = R.shared ? a.Hk : a.Hv;
-  const int hd = u % heads, slot = u / heads;
+  const int hd = u % a.Hv, slot = u / a.Hv;  // (a group's heads side by side, in the order of their sum)
   const int2 at = find_segment(a.cu, a.n_seqs, a.T, a.total, a.seg_chunks, a.nseg, slot);
   const int s = at.x, seg = at.y;
   if (s < 0) return;
   const Range q = seq_range(a.cu, s, a.T, a.total);
   const int nch = (q.len + CH - 1) / CH;
-  const int cb = seg * a.seg_chunks, ce = a.nseg == 1 ? nch : min(nch, cb + a.seg_chunks), nc = ce - cb;
-  if (nc <= 0) return;
+  const int cb = seg * a.seg_chunks, ce = a.nseg == 1 ? nch : min(nch, cb + a.seg_chunks);
+  if (cb >= ce) return;
   if (R.rev)
     walk<SUM, true>(a, R, sm, q, s, slot, hd, cb, ce);
   else
     walk<SUM, false>(a, R, sm, q, s, slot, hd, cb, ce);
 }
 
-// SUM: an output head is the sum over a group's value heads.
+// SUM: an output head is the sum over a group's value heads, whose CTAs run side by
+// side, each one a chunk or so behind the one before it.
 template <bool SUM>
 __global__ void __launch_bounds__(WALK_THREADS, 1) k_decay(const __grid_constant__ DecayArgs a) {
   extern __shared__ unsigned char raw[];
@@ -810,8 +822,7 @@ static cudaError_t launch_walk(const DecayArgs& a, cudaStream_t s) {
   static_assert(smem <= 227 * 1024, "shared memory");
   cudaError_t e = set_smem(k_decay<SUM>, smem);
   if (e != cudaSuccess) return e;
-  long units = 0;
-  for (int i = 0; i < a.n_roles; ++i) units += (long)a.slots * (a.role[i].shared ? a.Hk : a.Hv);
+  const long units = (long)a.n_roles * a.slots * a.Hv;
   return launch_pdl(k_decay<SUM>, dim3((unsigned)units), dim3(WALK_THREADS), smem, s, a);
 }
 

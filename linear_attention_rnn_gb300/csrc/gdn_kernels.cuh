@@ -166,6 +166,7 @@ struct DecayRole {
   const float* x0;      // [n_seqs][Hv][HD][HD] (nullable = 0)
   const float* xseg;    // entering states [slots][Hv][HD][HD] (null with one segment)
   float* acc;           // running sums [Hk][HD / 4][total][4] (shared, Hv > Hk)
+  int* flags;           // their heads so far [Hk][total / 128 + n_seqs][8], zero at the start
   bf16* out;
 };
 struct DecayArgs {

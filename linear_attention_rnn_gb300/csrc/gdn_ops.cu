@@ -42,11 +42,11 @@ inline bool workspace_ok(const void* ws, size_t ws_bytes, size_t need) {
 // ---- linear attention with a decay for each head -----------------------------------
 struct DecayPlan {
   int nseg, seg_chunks, slots;
-  size_t status, xf, xr, accq, acck, total;
+  size_t status, xf, xr, accq, acck, flags, flag_bytes, total;
 };
 
-// Segments.  One CTA walks a segment of a head (of a group's heads one behind
-// another for dq and dk); without segments a call takes as long as its longest
+// Segments.  One CTA walks a segment of a head (three of them in the backward, for
+// dq, dk and dv); without segments a call takes as long as its longest
 // sequence however few CTAs there are.  With segments k and v (q and dO) are read
 // twice, and two more kernels start.  The estimate, in chunks of the walk (2.7 us
 // measured): equal CTAs run in rounds over the SMs, CTAs of mixed lengths take
@@ -65,7 +65,7 @@ DecayPlan decay_plan(int backward, int n_seqs, int total, int max_seqlen, int Hk
   const long nch = (longest + CH - 1) / CH;
   p.nseg = 1;
   p.seg_chunks = nch > 0 ? (int)nch : 1;
-  const double sms = sm_count(), G = (double)Hv / Hk;
+  const double sms = sm_count();
   const double all = (double)total / CH + 0.5 * n_seqs;  // chunks of all sequences
   double best = 1e300;
   for (long k = 1; k <= nch && k <= 128; ++k) {
@@ -74,9 +74,7 @@ DecayPlan decay_plan(int backward, int n_seqs, int total, int max_seqlen, int Hk
     // segments that are as long as L
     const double parts = n_seqs == 1 ? (double)segs : k == 1 ? all / L : all / L + 0.25 * (n_seqs - 1);
     const bool mixed = n_seqs > 1 || backward;
-    // backward: Hv CTAs of a segment for dv, Hk that are G times as long for dq and for dk
-    double t = backward ? decay_rounds(parts * 3.0 * Hk, G * L + 1.5, sms, mixed)
-                        : decay_rounds(parts * Hv, L + 1.5, sms, mixed);
+    double t = decay_rounds(parts * Hv * (backward ? 3.0 : 1.0), L + 1.5, sms, mixed);
     if (segs > 1) t += decay_rounds(parts * Hv * (backward ? 2.0 : 1.0), 0.5 * L + 1.5, sms, mixed) + 4.0;
     if (t < best * 0.97) {
       best = t;
@@ -99,6 +97,8 @@ DecayPlan decay_plan(int backward, int n_seqs, int total, int max_seqlen, int Hk
     const size_t acc = Hv > Hk ? (size_t)total * Hk * HD * sizeof(float) : 0;
     p.accq = take(acc);
     p.acck = take(acc);
+    p.flag_bytes = Hv > Hk ? (size_t)Hk * (total / CH + n_seqs) * 8 * sizeof(int) : 0;  // of dq or dk
+    p.flags = take(2 * p.flag_bytes);
   }
   p.total = off;
   return p;
@@ -369,7 +369,7 @@ int gdn_decay_bwd(const void* q, const void* k, const void* v, const float* deca
       !tmap_rows(&mv, v, total, Hv, HD, (uint64_t)v_stride * 2, 1, CH) ||
       !tmap_rows(&md, dO, total, Hv, HD, (uint64_t)Hv * HD * 2, 1, CH))
     return GDN_ERR_CUDA;
-  // dq and dk, whose CTAs walk a group's value heads one behind another, then dv beside them
+  // dq and dk, then dv beside them
   DecayArgs b = a;
   DecayRole &rq = a.role[0], &rk = a.role[1], &rv = b.role[0];
   rq.a = md, rq.b = mv, rq.c = mk;
@@ -377,7 +377,11 @@ int gdn_decay_bwd(const void* q, const void* k, const void* v, const float* deca
   rq.xt = 1;
   rq.shared = 1;
   rq.x0 = h0;
-  rq.acc = Hv > Hk ? at<float>(ws, p.accq) : nullptr;
+  if (Hv > Hk) {
+    rq.acc = at<float>(ws, p.accq);
+    rq.flags = at<int>(ws, p.flags);
+    if ((rc = cuda_status(cudaMemsetAsync(rq.flags, 0, 2 * p.flag_bytes, s)))) return rc;
+  }
   rq.out = static_cast<bf16*>(dq);
   rk.a = mv, rk.b = md, rk.c = mq;
   rk.ha = rk.hb = 1;
@@ -385,7 +389,10 @@ int gdn_decay_bwd(const void* q, const void* k, const void* v, const float* deca
   rk.xt = 1;
   rk.shared = 1;
   rk.x0 = dhT;
-  rk.acc = Hv > Hk ? at<float>(ws, p.acck) : nullptr;
+  if (Hv > Hk) {
+    rk.acc = at<float>(ws, p.acck);
+    rk.flags = rq.flags + p.flag_bytes / sizeof(int);
+  }
   rk.out = static_cast<bf16*>(dk);
   rv.a = mk, rv.b = mq, rv.c = md;
   rv.hc = 1;
