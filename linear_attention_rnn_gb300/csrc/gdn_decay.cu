@@ -72,11 +72,22 @@ __device__ __forceinline__ int first_slot(const int* cu, int s, int T, int total
   return (cu ? min(max(cu[s], 0), total) : s * T) / K + s;
 }
 // Sequence and segment of a slot, found by every warp for itself (sequence -1:
-// none).  With one segment to a sequence a slot is a sequence.
+// none).  With one segment to a sequence a slot is a sequence, the longest first
+// (of 32 at most: CTAs start in order of slots, and the long ones decide when a
+// call ends).
 __device__ __forceinline__ int2 find_segment(const int* cu, int n_seqs, int T, int total, int seg_chunks, int nseg,
                                              int slot) {
-  if (nseg == 1) return make_int2(slot, 0);
   const int K = seg_chunks * CH, lane = threadIdx.x & 31;
+  if (nseg == 1) {
+    if (n_seqs == 1 || n_seqs > 32 || !cu) return make_int2(slot, 0);
+    const int len = seq_range(cu, min(lane, n_seqs - 1), T, total).len;
+    int longer = 0;
+    for (int k = 0; k < n_seqs; ++k) {
+      const int l = __shfl_sync(0xffffffffu, len, k);
+      longer += l > len || (l == len && k < lane);
+    }
+    return make_int2(__ffs((int)__ballot_sync(0xffffffffu, lane < n_seqs && longer == slot)) - 1, 0);
+  }
   for (int s0 = 0; s0 < n_seqs; s0 += 32) {
     const int s = min(s0 + lane, n_seqs - 1), a = first_slot(cu, s, T, total, K);
     const unsigned m = __ballot_sync(0xffffffffu, slot >= a && slot < first_slot(cu, s + 1, T, total, K));
