@@ -34,7 +34,7 @@ constexpr int Q_SLOTS = 5;   // K, V of two key tiles and a half
 // ---- delta_i = dO_i . o_i: half a warp to a row, four rows in flight ------------------
 constexpr int DELTA_ROWS = 64;  // rows per block of 256 threads
 __global__ void __launch_bounds__(256) k_attn_delta(const __grid_constant__ AttnArgs a) {
-  pdl_wait();
+  pdl_wait();  // (before it lets the next kernel start, which reads its inputs without a wait)
   pdl_release();
   clear_status(a.status);
   const long rows = (long)a.total_q * a.Hq, row0 = (long)blockIdx.x * DELTA_ROWS + (threadIdx.x >> 4);
@@ -194,6 +194,8 @@ __device__ __forceinline__ void dkv(const AttnArgs& a, unsigned char* raw, int b
       sm.lse[i & 1][tid] = -c_lse * LOG2E;
       sm.delta[i & 1][tid] = c_delta;
     };
+    pdl_wait();  // (delta, from the kernel before; everything else was complete when it began)
+    pdl_release();
     if (n > 0 && tid < CH) {
       fetch_cols(0);
       put_cols(0);
@@ -416,6 +418,8 @@ __device__ __forceinline__ void dq(const AttnArgs& a, unsigned char* raw, int bl
     const long row = ((long)sq.q0 + tok) * a.Hq + kh * G + r % G;
     const int lim = valid ? tok + off : -1;
     const float sc = a.scale * LOG2E;
+    pdl_wait();  // (as dkv)
+    pdl_release();
     const float lse = valid ? a.lse[row] * LOG2E : 0.f, delta = valid ? a.delta[row] : 0.f;
     for (int i = 0; i < n; ++i) {
       const int key0 = i * CH;
@@ -484,12 +488,11 @@ __device__ __forceinline__ void dq(const AttnArgs& a, unsigned char* raw, int bl
 // first, and the dq CTAs fill the SMs beside and after them.
 __global__ void __launch_bounds__(BWD_THREADS, 1) k_attn_bwd(const __grid_constant__ AttnArgs a, int kv_blocks) {
   extern __shared__ unsigned char raw[];
-  pdl_wait();
-  pdl_release();
   if ((int)blockIdx.x < kv_blocks)
     dkv(a, raw, (int)blockIdx.x);
   else
     dq(a, raw, (int)blockIdx.x - kv_blocks);
+  if (blockIdx.x == 0) pdl_wait();  // the grid ends after the one before it, whatever its CTAs had to do
 }
 
 }  // namespace
