@@ -355,7 +355,8 @@ int gdn_decay_step(const void* q, const void* k, const void* v, const float* dec
  * Linear attention with a decay for each head, over packed sequences.  Per
  * sequence and value head j (key head kh = j / (Hv/Hk)), w = decay[j] <= 0:
  *     h_t = exp(w) h_{t-1} + k_t v_t^T,   o_t = h_t^T q_t,   h_{-1} = h0,   hT = h_{T-1}.
- * The decays are constants of the model: no gradient of them is formed.
+ * (minus infinity: only the newest row is kept).  The decays are constants of the
+ * model: no gradient of them is formed.
  * q, k [total, Hk, d_k], v [total, Hv, d_v] bf16 (strides as for the
  * single-token forms); decay [Hv] fp32; h0, hT [n_seqs, Hv, d_k, d_v] fp32
  * (NULL = zero / not written); o [total, Hv, d_v] bf16.  Sequence s holds the

@@ -64,6 +64,13 @@ __device__ __forceinline__ Range seq_range(const int* cu, int s, int T, int tota
   return r;
 }
 
+// A head's log-decay: minus infinity (nothing is kept) as a number, so that it times a
+// distance of zero is zero.
+__device__ __forceinline__ float log_decay(const float* decay, int j) {
+  const float w = decay[j];
+  return w == -INFINITY ? -1e30f : w;
+}
+
 // Segment slots.  Sequence s has the slots first_slot(s) .. first_slot(s + 1) - 1,
 // at least as many as it has segments of K = 128 seg_chunks tokens and at most
 // one more than total / K over all sequences together, so that neither grids
@@ -366,7 +373,7 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
     // rows: thread (r, half) has row r = TMEM lane r and 64 of its 128 columns.
     const int half = (warp >> 2) & 1, r = 32 * (warp & 3) + lane;
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16, cols = lane_base + 64 * half;
-    const float wd = a.decay[hd];
+    const float wd = log_decay(a.decay, hd);
     if (warp < 8) {
       const int own = warp & 3, Ho = R.shared ? a.Hk : a.Hv;
       // O of chunk `it`, whose products have been issued
@@ -717,7 +724,7 @@ __device__ __forceinline__ void fold_block(const DecayFoldArgs& a, FoldSmem& sm)
     }
   } else {
     const int j0 = 4 * (tid >> 6);  // 64 rows at a time, four threads to a row
-    const float wd = a.decay[j];
+    const float wd = log_decay(a.decay, j);
     for (int i = 0; i < nc; ++i) {
       const int n = min(CH, q.len - (cb + i) * CH), tb = 2 * i, tcc = tb + 1;
       w.warp_on(&sm.full[tb % FOLD_SLOTS], tb / FOLD_SLOTS);
@@ -793,7 +800,7 @@ __global__ void __launch_bounds__(256) k_decay_prefix(const __grid_constant__ De
   const long sh = (long)s * a.Hv + j;
   const int e = 4 * (blockIdx.y * 256 + threadIdx.x);  // 16 blocks cover the state, in the segments' order
   const int e0 = ((e >> 2) & (HD - 1)) * HD + 4 * (e >> 9);  // the same place in a caller's state
-  const float wd = a.decay[j];
+  const float wd = log_decay(a.decay, j);
   const int slot0 = first_slot(a.cu, s, a.T, a.total, a.seg_chunks * CH);
   float4 run = R.x0 ? *reinterpret_cast<const float4*>(R.x0 + sh * HD * HD + e0) : make_float4(0.f, 0.f, 0.f, 0.f);
   constexpr int AHEAD = 4;  // loads in flight
