@@ -664,8 +664,11 @@ __device__ __forceinline__ void fold_block(const DecayFoldArgs& a, FoldSmem& sm)
   if (!R.last && (R.rev ? cb == 0 : ce == nch)) return;
   const int end = min(q.len, ce * CH);  // one past the segment's last token
 
+  // in the order of growing weights: the fp32 sums of the tensor cores lose a little of
+  // whatever is added to a larger sum
+  auto chunk_of = [&](int i) { return R.rev ? ce - 1 - i : cb + i; };
   auto load = [&](int t) {
-    load_tile(sm.slot[t % FOLD_SLOTS], (t & 1) ? &R.c : &R.b, (t & 1) ? j : j / G, q.start + (cb + t / 2) * CH,
+    load_tile(sm.slot[t % FOLD_SLOTS], (t & 1) ? &R.c : &R.b, (t & 1) ? j : j / G, q.start + chunk_of(t / 2) * CH,
               &sm.full[t % FOLD_SLOTS]);
   };
   const int nt = 2 * nc;
@@ -687,6 +690,14 @@ __device__ __forceinline__ void fold_block(const DecayFoldArgs& a, FoldSmem& sm)
   tc::fence_after();
   const uint32_t tX = sm.tmem;
   tc::Wait w;
+  const float wd = log_decay(a.decay, j);
+  // The third terms of chunk i's rows (2^-17 of their size) are for the final state
+  // alone, and only where the chunk has a weight of 2^-8 or more in it: beyond that
+  // they are below the fp32 rounding of sums of newer rows as large.
+  auto third = [&](int i) {
+    const int newer = R.rev ? chunk_of(i) * CH : max(q.len - (chunk_of(i) + 1) * CH, 0);
+    return R.last && wd * (float)newer > -5.55f;
+  };
   if (warp == 9) {
     if (lane == 0) {
       for (int t = FOLD_SLOTS; t < nt && w.ok; ++t) {
@@ -712,9 +723,8 @@ __device__ __forceinline__ void fold_block(const DecayFoldArgs& a, FoldSmem& sm)
         // even and odd chunks and the small further terms have sums of their own.
         const uint32_t t0 = tX + 128 * (i & 1), t1 = tX + 256 + 128 * (i & 1);
         tc::gemm_rows_by<64, 128>(lead, t0, smem_u32(sm.slot[tb % FOLD_SLOTS]) + 8192 * h, c, i > 1 || h > 0);
-#pragma unroll
-        for (int t = 0; t < FOLD_TERMS - 1; ++t)
-          tc::gemm_rows_by<64, 128>(lead, t1, smem_u32(sm.rest[t]) + 8192 * h, c, i > 1 || h > 0 || t > 0);
+        tc::gemm_rows_by<64, 128>(lead, t1, smem_u32(sm.rest[0]) + 8192 * h, c, i > 1 || h > 0);
+        if (third(i)) tc::gemm_rows_by<64, 128>(lead, t1, smem_u32(sm.rest[1]) + 8192 * h, c, true);
         if (h == 1) {
           if (tb + FOLD_SLOTS < 2 * nc) tc::commit_by(lead, &sm.empty[tb % FOLD_SLOTS]);
           if (tcc + FOLD_SLOTS < 2 * nc) tc::commit_by(lead, &sm.empty[tcc % FOLD_SLOTS]);
@@ -724,18 +734,21 @@ __device__ __forceinline__ void fold_block(const DecayFoldArgs& a, FoldSmem& sm)
     }
   } else {
     const int j0 = 4 * (tid >> 6);  // 64 rows at a time, four threads to a row
-    const float wd = log_decay(a.decay, j);
     for (int i = 0; i < nc; ++i) {
-      const int n = min(CH, q.len - (cb + i) * CH), tb = 2 * i, tcc = tb + 1;
+      const int n = min(CH, q.len - chunk_of(i) * CH), tb = 2 * i, tcc = tb + 1;
       w.warp_on(&sm.full[tb % FOLD_SLOTS], tb / FOLD_SLOTS);
       if (n < CH) w.warp_on(&sm.full[tcc % FOLD_SLOTS], tcc / FOLD_SLOTS);
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
-        const int r = 64 * h + (tid & 63), t0 = (cb + i) * CH + r;
+        const int r = 64 * h + (tid & 63), t0 = chunk_of(i) * CH + r;
         // weight to the segment's end (forwards) or to its start (backwards)
         const float e = expf(wd * (float)(R.rev ? t0 - cb * CH + 1 : max(end - 1 - t0, 0)));
         if (i > 0) w.warp_on(&sm.barM[h], i - 1);  // (these rows' further terms have been read)
-        scale_row<FOLD_TERMS, 4, CH>(sm.slot[tb % FOLD_SLOTS], sm.slot[tb % FOLD_SLOTS], sm.rest[0], r, j0, e, r < n);
+        unsigned char* b = sm.slot[tb % FOLD_SLOTS];
+        if (third(i))
+          scale_row<3, 4, CH>(b, b, sm.rest[0], r, j0, e, r < n);
+        else
+          scale_row<2, 4, CH>(b, b, sm.rest[0], r, j0, e, r < n);
         if (r >= n) zero_row(sm.slot[tcc % FOLD_SLOTS], r, j0, 4);
         tc::fence_proxy_async();
         tc::mbar_arrive(&sm.barK[h]);
