@@ -174,6 +174,7 @@ struct WalkSmem {
   unsigned char lo[TILE];               // second term of the scaled B rows (the first one in place)
   unsigned char X[TILE];                // the entering state in bf16, [128 (b) rows x 128 (c)]
   alignas(16) float tab[CH];            // e^{w d}
+  alignas(16) float col[2][32];         // e^{w (31 - d)}, e^{-w d}
   uint64_t full[NSLOT], empty[NSLOT];
   // barSt: of even and odd chunks.  The storing thread may be a chunk behind the
   // writers; the slot that it frees keeps them from getting two ahead.
@@ -207,15 +208,15 @@ __device__ __forceinline__ void first_state(const DecayRole& R, unsigned char* s
     const int t = threadIdx.x & 255, cc = c0 & 63;
     asm volatile("bar.sync 2, 256;" ::: "memory");  // (the pass before has been read)
 #pragma unroll 1
-    for (int k = 0; k < 8; k += 2) {
-      float4 f[2];
+    for (int k = 0; k < 8; k += 8) {
+      float4 f[8];
 #pragma unroll
-      for (int l = 0; l < 2; ++l) {
+      for (int l = 0; l < 8; ++l) {
         const int i = t + 256 * (k + l), row = i >> 4, p = i & 15;  // 16-byte piece p of the row's two
         f[l] = *reinterpret_cast<const float4*>(x0 + row * HD + (p >> 3) * 64 + cc + 4 * (p & 7));
       }
 #pragma unroll
-      for (int l = 0; l < 2; ++l) {
+      for (int l = 0; l < 8; ++l) {
         const int i = t + 256 * (k + l), row = i >> 4, p = i & 15;
         *reinterpret_cast<float4*>(stage + row * 256 + ((p ^ (row & 7)) << 4)) = f[l];
       }
@@ -298,7 +299,11 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
   tc::Wait w;
 
   // whether chunk `it`'s output rows are stored as a tile: a whole chunk, of the last head summed
-  auto whole = [&](int it) { return (!SUM || g == G - 1) && rows_of(chunk_of(it)) == CH; };
+  auto flag_of = [&](int c) {
+    return R.flags + (long)kh * (a.total / CH + a.n_seqs) + first_slot(a.cu, s, a.T, a.total, CH) + c;
+  };
+  const bool adds = SUM && R.shared && g > 0, last = !SUM || !R.shared || g == G - 1;
+  auto whole = [&](int it) { return last && rows_of(chunk_of(it)) == CH; };
 
   if (warp == 18) {  // ---- output tiles: staged in the slot of the chunk's C, which O has consumed
     if (lane == 0) {
@@ -315,6 +320,10 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
           tc::bulk_wait_read();
         }
         if (t + NSLOT < 3 * n_it) tc::mbar_arrive(&sm.empty[t % NSLOT]);
+        // the chunk's sums are in memory: the flag says so to the next head's CTA (from
+        // here, where the wait for the writes holds up nobody else)
+        if (!last)
+          asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(flag_of(chunk_of(it))), "r"(g + 1) : "memory");
       }
       tc::bulk_wait();
     }
@@ -412,66 +421,64 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
           }
         } else {
           // The sum over the value heads runs from CTA to CTA, [head][4-column group][row]
-          // in the workspace: the warp of one CTA that holds these rows and columns writes
-          // its sum, and a flag of its own says so to the same warp of the next one.
-          const bool add = g > 0 && r < n, last = g == G - 1;
+          // in the workspace; a flag per chunk says how many heads are in it.
+          const bool add = adds && r < n;
           float4* acc = reinterpret_cast<float4*>(R.acc) + ((long)kh * 32 + 16 * half) * a.total + row;
-          int* flag = R.flags + ((long)kh * (a.total / CH + a.n_seqs) + first_slot(a.cu, s, a.T, a.total, CH) + c) * 8 + warp;
-          if (g > 0) w.ok = wait_flag(flag, g) && w.ok;
-          float4 p[8];  // 32 columns of it are requested before the products are waited for
+          if (adds) w.ok = wait_flag(flag_of(c), g) && w.ok;
+          float4 p[2][4];  // 32 columns of it are on their way at any time
           auto request = [&](int k) {
             if (add) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) p[i] = acc[(long)(8 * k + i) * a.total];
+              for (int i = 0; i < 4; ++i) p[k & 1][i] = acc[(long)(4 * k + i) * a.total];
             }
           };
           request(0);
+          request(1);
           w.warp_on(&sm.barO, it);
           tc::fence_after();
-#pragma unroll 1
-          for (int k = 0; k < 2; ++k) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float x[16], y[16];
-              tc::ld16(tO1 + cols + 32 * k + 16 * h, x);
-              tc::ld16(tO2 + cols + 32 * k + 16 * h, y);
-              if (k == 1 && h == 1) {
-                tc::fence_before();
-                tc::mbar_arrive(&sm.barOf);
-              }
-#pragma unroll
-              for (int i = 0; i < 16; i += 2) tc::axpy2(x[i], x[i + 1], f, y[i], y[i + 1]);
-              if (add) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  x[4 * i] += p[4 * h + i].x;
-                  x[4 * i + 1] += p[4 * h + i].y;
-                  x[4 * i + 2] += p[4 * h + i].z;
-                  x[4 * i + 3] += p[4 * h + i].w;
-                }
-              }
-              if (last) {
-                put(4 * k + 2 * h, x);
-                put(4 * k + 2 * h + 1, x + 8);
-              } else if (r < n) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  acc[(long)(8 * k + 4 * h + i) * a.total] =
-                      make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-              }
-              __syncwarp();
+          for (int k = 0; k < 4; ++k) {
+            float x[16], y[16];
+            tc::ld16(tO1 + cols + 16 * k, x);
+            tc::ld16(tO2 + cols + 16 * k, y);
+            if (k == 3) {
+              tc::fence_before();
+              tc::mbar_arrive(&sm.barOf);
             }
-            if (k == 0) request(1);
-          }
-          if (!last) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) tc::axpy2(x[i], x[i + 1], f, y[i], y[i + 1]);
+            if (add) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                x[4 * i] += p[k & 1][i].x;
+                x[4 * i + 1] += p[k & 1][i].y;
+                x[4 * i + 2] += p[k & 1][i].z;
+                x[4 * i + 3] += p[k & 1][i].w;
+              }
+            }
+            if (k < 2) request(k + 2);
+            if (last) {
+              put(2 * k, x);
+              put(2 * k + 1, x + 8);
+            } else if (r < n) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                acc[(long)(4 * k + i) * a.total] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+            }
             __syncwarp();
-            if (lane == 0) asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(flag), "r"(g + 1) : "memory");
           }
         }
         tc::fence_proxy_async();
         tc::mbar_arrive(&sm.barSt[it & 1]);
       };
-      if (half == 0) sm.tab[r] = expf(wd * (float)r);
+      if (half == 0) {
+        sm.tab[r] = expf(wd * (float)r);
+        if (r < 32) {
+          sm.col[0][r] = expf(wd * (float)(31 - r));
+          sm.col[1][r] = expf(-wd * (float)r);
+        }
+      }
+      const bool mild = wd > -2.5f;  // (e^{-31 w} is a number, and far from fp32's largest)
       asm volatile("bar.sync 1, 256;" ::: "memory");
       for (int it = 0; it < n_it; ++it) {
         if (it > 0) output(it - 1);
@@ -479,8 +486,9 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
         w.warp_on(&sm.barP, it);
         tc::fence_after();
         // Of the four 32 x 32 blocks of a warp's rows, those on the far side of the
-        // diagonal are zero, those on the near side have the factor
-        // e^{w |i - j|} = (to the block's edge) * (from the edge), both <= 1.
+        // diagonal are zero, those on the near side have the factor e^{w |i - j|} = (to
+        // the block's edge) * (from the edge), both <= 1.  On the diagonal block it is
+        // e^{w i} * e^{-w j} from the block's corner, unless the second one could overflow.
 #pragma unroll 1
         for (int h = 4 * half; h < 4 * half + 4; ++h) {  // 16 columns at a time
           const int g = h >> 1, j0 = 16 * h;
@@ -490,24 +498,26 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
             for (int i = 0; i < 16; ++i) v[i] = 0.f;
           } else {
             tc::ld16(tP + lane_base + j0, v);
-            if (g == own) {
-              const int d0 = REV ? j0 - r : r - j0;
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const int d = REV ? d0 + i : d0 - i;
-                v[i] = d >= 0 ? v[i] * sm.tab[d & 31] : 0.f;
-              }
-            } else {
-              const float edge = sm.tab[REV ? 32 * g - r : r - 32 * g - 31];
-              const float* t = sm.tab + (REV ? j0 & 16 : 16 - (j0 & 16));
+            if (g != own || mild) {
+              const float edge = REV ? (g == own ? sm.col[1][lane] : sm.tab[32 * g - r])
+                                     : sm.tab[g == own ? lane : r - 32 * g - 31];
+              const float* col = (REV ? sm.tab : sm.col[g == own]) + (j0 & 16);
 #pragma unroll
               for (int i = 0; i < 16; i += 4) {
-                const float4 f = *reinterpret_cast<const float4*>(t + (REV ? i : 12 - i));
+                const float4 f = *reinterpret_cast<const float4*>(col + i);
                 tc::mul2(v[i], v[i + 1], edge, edge);
                 tc::mul2(v[i + 2], v[i + 3], edge, edge);
-                tc::mul2(v[i], v[i + 1], REV ? f.x : f.w, REV ? f.y : f.z);
-                tc::mul2(v[i + 2], v[i + 3], REV ? f.z : f.y, REV ? f.w : f.x);
+                tc::mul2(v[i], v[i + 1], f.x, f.y);
+                tc::mul2(v[i + 2], v[i + 3], f.z, f.w);
               }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] *= sm.tab[max(REV ? j0 + i - r : r - j0 - i, 0)];
+            }
+            if (g == own) {
+              const int d0 = r - j0;  // column of the diagonal
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] = (REV ? i >= d0 : i <= d0) ? v[i] : 0.f;
             }
             if (REV && j0 + 16 > n) {  // (forwards, rows of tokens see tokens only)
 #pragma unroll
@@ -522,7 +532,7 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
       }
       output(n_it - 1);
     } else {
-      if (a.nseg > 1 && !a.beside) {  // the entering states come from the kernel before
+      if (a.nseg > 1) {  // the entering states come from the kernel before
         pdl_wait();
         pdl_release();
       }
@@ -596,17 +606,10 @@ __device__ __forceinline__ void walk_block(const DecayArgs& a, WalkSmem& sm) {
     pdl_release();
     clear_status(a.status);
   }
-  if (a.beside == 2) pdl_release();  // (a third kernel beside the two)
-
-  // pass, then segment, sequence and head of this CTA
-  int u = blockIdx.x, ri = 0;
-  for (; ri < a.n_roles - 1; ++ri) {
-    const int units = a.slots * a.Hv;
-    if (u < units) break;
-    u -= units;
-  }
+  // This CTA's sequence (or segment), pass and head: the longest sequences' CTAs of all
+  // passes come first, a group's heads side by side in the order of their sum.
+  const int hd = blockIdx.x % a.Hv, u = blockIdx.x / a.Hv, ri = u % a.n_roles, slot = u / a.n_roles;
   const DecayRole& R = a.role[ri];
-  const int hd = u % a.Hv, slot = u / a.Hv;  // (a group's heads side by side, in the order of their sum)
   const int2 at = find_segment(a.cu, a.n_seqs, a.T, a.total, a.seg_chunks, a.nseg, slot);
   const int s = at.x, seg = at.y;
   if (s < 0) return;

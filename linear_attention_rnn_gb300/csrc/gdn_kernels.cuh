@@ -166,7 +166,7 @@ struct DecayRole {
   const float* x0;      // [n_seqs][Hv][HD][HD] (nullable = 0)
   const float* xseg;    // entering states [slots][Hv][HD][HD] (null with one segment)
   float* acc;           // running sums [Hk][HD / 4][total][4] (shared, Hv > Hk)
-  int* flags;           // their heads so far [Hk][total / 128 + n_seqs][8], zero at the start
+  int* flags;           // their heads so far [Hk][total / 128 + n_seqs], zero at the start
   bf16* out;
 };
 struct DecayArgs {
@@ -177,8 +177,7 @@ struct DecayArgs {
   int n_roles, n_seqs, total, T, Hk, Hv;
   int nseg, seg_chunks;  // most segments of a sequence, chunks to a segment
   int slots;             // segment slots: n_seqs with nseg = 1, else total / (128 seg_chunks) + n_seqs
-  int beside;            // the launch before it is another walk of the same call, which it need not wait
-                         //   for (2: and a fold of the call follows, which need not wait for it)
+  int beside;            // the launch before it is the call's fold, which it need not wait for
 };
 struct DecayFoldRole {
   CUtensorMap b, c;    // b: shared heads, c: value heads
@@ -195,7 +194,7 @@ struct DecayFoldArgs {
   int n_roles, n_seqs, total, T, Hk, Hv;
   int nseg, seg_chunks;  // most segments of a sequence, chunks to a segment
   int slots;             // segment slots: n_seqs with nseg = 1, else total / (128 seg_chunks) + n_seqs
-  int beside;            // as DecayArgs
+  int beside;            // the launch before it is the call's walk, which it need not wait for
 };
 
 // Causal softmax attention over packed sequences (gdn_attn_fwd.cu, gdn_attn_bwd.cu).

@@ -97,7 +97,7 @@ DecayPlan decay_plan(int backward, int n_seqs, int total, int max_seqlen, int Hk
     const size_t acc = Hv > Hk ? (size_t)total * Hk * HD * sizeof(float) : 0;
     p.accq = take(acc);
     p.acck = take(acc);
-    p.flag_bytes = Hv > Hk ? (size_t)Hk * (total / CH + n_seqs) * 8 * sizeof(int) : 0;  // of dq or dk
+    p.flag_bytes = Hv > Hk ? (size_t)Hk * (total / CH + n_seqs) * sizeof(int) : 0;  // of dq or dk
     p.flags = take(2 * p.flag_bytes);
   }
   p.total = off;
@@ -362,16 +362,14 @@ int gdn_decay_bwd(const void* q, const void* k, const void* v, const float* deca
   a.nseg = p.nseg;
   a.seg_chunks = p.seg_chunks;
   a.slots = p.slots;
-  a.n_roles = 2;
+  a.n_roles = 3;
   CUtensorMap mq, mk, mv, md;
   if (!tmap_rows(&mq, q, total, Hk, HD, (uint64_t)q_stride * 2, 1, CH) ||
       !tmap_rows(&mk, k, total, Hk, HD, (uint64_t)k_stride * 2, 1, CH) ||
       !tmap_rows(&mv, v, total, Hv, HD, (uint64_t)v_stride * 2, 1, CH) ||
       !tmap_rows(&md, dO, total, Hv, HD, (uint64_t)Hv * HD * 2, 1, CH))
     return GDN_ERR_CUDA;
-  // dq and dk, then dv beside them
-  DecayArgs b = a;
-  DecayRole &rq = a.role[0], &rk = a.role[1], &rv = b.role[0];
+  DecayRole &rq = a.role[0], &rk = a.role[1], &rv = a.role[2];
   rq.a = md, rq.b = mv, rq.c = mk;
   rq.ha = rq.hb = 1;
   rq.xt = 1;
@@ -421,15 +419,15 @@ int gdn_decay_bwd(const void* q, const void* k, const void* v, const float* deca
     rq.xseg = ff.x;
     rk.xseg = rv.xseg = fr.x;
   }
-  const bool last = p.nseg == 1 && dh0;  // the final state in a kernel of its own, beside the walks
-  if ((rc = cuda_status(launch_decay(a, s)))) return rc;
-  b.n_roles = 1;
-  b.beside = last ? 2 : 1;
-  if ((rc = cuda_status(launch_decay(b, s))) || !last) return rc;
-  f.n_roles = 1;
-  f.role[0] = fr;
-  f.beside = 1;
-  return cuda_status(launch_decay_fold(f, s));
+  if (p.nseg == 1 && dh0) {
+    // The final state in a kernel of its own, beside the walk.  It goes first: its CTAs
+    // are short, and behind the walk's they would start only when the last of those has.
+    f.n_roles = 1;
+    f.role[0] = fr;
+    if ((rc = cuda_status(launch_decay_fold(f, s)))) return rc;
+    a.beside = 1;
+  }
+  return cuda_status(launch_decay(a, s));
 }
 
 size_t gdn_attn_workspace_bytes(int backward, int n_seqs, int total_q, int total_k, int max_k, int Hq, int Hk,
