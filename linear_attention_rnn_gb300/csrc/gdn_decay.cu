@@ -270,6 +270,10 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
     load_tile(sm.slot[t % NSLOT], m, per_v ? hd : kh, row, &sm.full[t % NSLOT]);
   };
   const int nt = 3 * n_it;
+  const float* x0 = R.xseg ? R.xseg + ((long)slot_id * a.Hv + hd) * HD * HD
+                           : (R.x0 ? R.x0 + ((long)s * a.Hv + hd) * HD * HD : nullptr);
+  if (!R.xseg && x0 && tid < HD * HD / 32)  // on its way to L2 while the CTA sets up
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(x0 + 32 * tid));
   if (warp == 17 && lane == 0) {
     for (int k = 0; k < NSLOT; ++k) {
       tc::mbar_init(&sm.full[k], 1);
@@ -536,8 +540,6 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
         pdl_wait();
         pdl_release();
       }
-      const float* x0 = R.xseg ? R.xseg + ((long)slot_id * a.Hv + hd) * HD * HD
-                               : (R.x0 ? R.x0 + ((long)s * a.Hv + hd) * HD * HD : nullptr);
 #pragma unroll 1
       for (int k = 0; k < 2; ++k) {
         float v[32];
