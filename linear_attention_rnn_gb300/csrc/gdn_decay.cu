@@ -662,7 +662,10 @@ __device__ __forceinline__ void fold_block(const DecayFoldArgs& a, FoldSmem& sm)
   const long sh = (long)s * a.Hv + j;
   if (nc <= 0) {
     if (a.nseg == 1)  // an empty sequence ends in the state that it began with
-      for (int i = tid; i < HD * HD; i += FOLD_THREADS) R.last[sh * HD * HD + i] = R.x0 ? R.x0[sh * HD * HD + i] : 0.f;
+#pragma unroll 4
+      for (int i = 4 * tid; i < HD * HD; i += 4 * FOLD_THREADS)
+        *reinterpret_cast<float4*>(R.last + sh * HD * HD + i) =
+            R.x0 ? __ldg(reinterpret_cast<const float4*>(R.x0 + sh * HD * HD + i)) : make_float4(0.f, 0.f, 0.f, 0.f);
     return;
   }
   // the segment that the walk ends with matters only for the final state
@@ -677,6 +680,10 @@ __device__ __forceinline__ void fold_block(const DecayFoldArgs& a, FoldSmem& sm)
               &sm.full[t % FOLD_SLOTS]);
   };
   const int nt = 2 * nc;
+  if (a.nseg == 1 && R.x0 && tid < HD * HD / 64) {  // on its way to L2 meanwhile
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(R.x0 + sh * HD * HD + 64 * tid));
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(R.x0 + sh * HD * HD + 64 * tid + 32));
+  }
   if (warp == 9 && lane == 0) {
     for (int k = 0; k < FOLD_SLOTS; ++k) {
       tc::mbar_init(&sm.full[k], 1);
@@ -763,10 +770,11 @@ __device__ __forceinline__ void fold_block(const DecayFoldArgs& a, FoldSmem& sm)
     tc::fence_after();
     const int row = 32 * (warp & 3) + lane, g0 = 2 * (warp >> 2);
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
-    // with one segment this is the final state but for the initial one's share
-    const float keep = expf(wd * (float)q.len);
-    const float* x0 = a.nseg == 1 && R.x0 ? R.x0 + sh * HD * HD : nullptr;
-    float* dst = a.nseg == 1 ? R.last + sh * HD * HD : R.x + ((long)slot * a.Hv + j) * HD * HD;
+    // With one segment this is the final state but for the initial one's share: through
+    // shared memory (the tiles are done with), so that a warp touches whole rows.
+    float* dst = R.x + ((long)slot * a.Hv + j) * HD * HD;
+    unsigned char* staged = sm.slot[0];
+    auto place = [&](int r, int c4) { return reinterpret_cast<float4*>(staged + r * 512 + ((c4 ^ (r & 7)) << 4)); };
 #pragma unroll 1
     for (int g = g0; g < g0 + 2; ++g) {
       float v[32];
@@ -782,12 +790,27 @@ __device__ __forceinline__ void fold_block(const DecayFoldArgs& a, FoldSmem& sm)
 #pragma unroll
       for (int i = 0; i < 32; i += 4) {
         const int c = 32 * g + i;
-        float4 o = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-        if (x0) {
-          const float4 x = *reinterpret_cast<const float4*>(x0 + row * HD + c);
-          o = make_float4(o.x + keep * x.x, o.y + keep * x.y, o.z + keep * x.z, o.w + keep * x.w);
+        *(a.nseg == 1 ? place(row, c >> 2) : reinterpret_cast<float4*>(dst + seg_index(row, c))) =
+            make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+      }
+    }
+    if (a.nseg == 1) {
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      const float keep = expf(wd * (float)q.len);
+      const float* x0 = R.x0 ? R.x0 + sh * HD * HD + 4 * lane : nullptr;
+      float* out = R.last + sh * HD * HD + 4 * lane;
+#pragma unroll 1
+      for (int r0 = warp; r0 < HD; r0 += 64) {
+        float4 x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          x[k] = x0 ? __ldg(reinterpret_cast<const float4*>(x0 + (r0 + 8 * k) * HD)) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float4 o = *place(r0 + 8 * k, lane);
+          *reinterpret_cast<float4*>(out + (r0 + 8 * k) * HD) =
+              make_float4(o.x + keep * x[k].x, o.y + keep * x[k].y, o.z + keep * x[k].z, o.w + keep * x[k].w);
         }
-        *reinterpret_cast<float4*>(dst + (a.nseg == 1 ? row * HD + c : seg_index(row, c))) = o;
       }
     }
     tc::fence_before();
