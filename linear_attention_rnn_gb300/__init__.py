@@ -1,5 +1,11 @@
 """GB300 (sm_103a) chunked Gated DeltaNet -- Python binding of libgdn.
 
+Beside the chunked rule (chunk_fwd, chunk_bwd, the layer and the segment calls) there
+are the operators that a stack with other mixers and a decoding loop need:
+delta_step, one token per row of the gated delta rule; decay_fwd, decay_bwd and
+decay_step, linear attention with a decay for each head; attn_fwd and attn_bwd,
+causal softmax attention with grouped heads, over packed sequences or caches.
+
 Thin marshalling over the C ABI in include/gdn.h: shape/dtype checks,
 allocation of outputs and workspace with torch, and the ctypes call on the
 current CUDA stream.  Every step of the computation runs in the library's

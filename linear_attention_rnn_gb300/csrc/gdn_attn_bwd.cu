@@ -18,7 +18,15 @@
 // warps hold a tile, 64 columns to a thread.  While they form dS, the tensor
 // cores run the next S; while they form P, the last gradient product.
 //
-// Bound: the tensor rate (7 x 512 cycles per pair of 128 x 128 tiles).
+// Roundings: P and dS become bf16 once, as operands, and so does every result; delta
+// takes the forward's rounded o, as the caller has it.  A gradient's error against 64 bits
+// is then 2.5e-3 to 2.9e-3 in the 2-norm (rounding the result alone: 1.7e-3); scores, lse,
+// delta and all sums are fp32.
+//
+// Bound: the tensor rate (7 x 512 cycles per pair of 128 x 128 tiles).  Measured on a
+// GB300, 4096 + 2048 + 1000 + 977 + 71 packed tokens, 16 query and 4 key heads: 230 us,
+// the tensor pipe busy for 0.62 of it; delta 14 us; with the forward 329 us.  Two CTAs
+// for the heaviest key tiles were slower (245 us): the SMs are busy to the end as it is.
 #include "gdn_attn.cuh"
 
 namespace gdn {

@@ -11,7 +11,9 @@
 // across the block once, and written once.
 //
 // Bound: HBM.  A state is 64 KiB read and 64 KiB written against 1.3 KiB of
-// everything else and 5 to 9 operations per element.  A block of 128 threads
+// everything else and 5 to 9 operations per element.  Measured on a GB300, 32 heads:
+// 256 rows 156 us (decay) and 512 rows 310 us (delta), 6.9 TB/s, 1.02 of the rate of
+// a plain copy; one row 4 us, a launch's and a memory round trip's latency.  A block of 128 threads
 // holds 32 columns (one 128-byte line of each of the 128 rows), 32 values to a
 // thread, all of its loads in flight at once; four blocks share a state.  Small
 // blocks make the loads of a single row spread over 4 Hv SMs (128 at 32 heads)
