@@ -33,7 +33,8 @@
 // forms each segment's own X (rows weighted to the segment's end, so that its
 // chunks accumulate in tensor memory without a rescale), k_decay_prefix turns
 // them into entering states, and k_decay starts every segment from its own.  With
-// one segment to a sequence the fold forms the final states, beside the walk.
+// one segment to a sequence the fold forms the final states, beside the walk (in a
+// launch of its own, or, in short calls, in the walk's: k_decay_small).
 //
 // Bound: shared memory.  A product whose operands both lie there reads 64 KiB in the
 // 512 cycles that it takes, all of an SM's 128 bytes per cycle; with the loads, the
@@ -41,7 +42,7 @@
 // 4600 cycles, and takes 4800 to 5800 (2.4 to 2.9 us); the fold's 2300 (two terms) take
 // 2600.  Measured on a GB300, 16 key and 32 value heads: 65536 tokens in 485 us (fold
 // 151, prefix 8, walk 310; the bytes alone 238), 4096 tokens in 49 us (19, 6, 32; 15);
-// forward and backward of 4096 + 2500 + 1000 + 595 + 1 packed tokens in 278 us (walks 90
+// forward and backward of 4096 + 2500 + 1000 + 595 + 1 packed tokens in 277 us (walks 90
 // and 158, the longest sequence's 32 chunks deciding the first one; the bytes alone 87).
 #include "gdn_kernels.cuh"
 #include "gdn_tc05.cuh"
@@ -610,40 +611,7 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
   if (warp == 0) tc::dealloc(sm.tmem, 512);
 }
 
-template <bool SUM>
-__device__ __forceinline__ void walk_block(const DecayArgs& a, WalkSmem& sm) {
-  if (a.nseg == 1 && !a.beside) {  // (with segments, only the entering states wait for the kernel before)
-    pdl_wait();
-    pdl_release();
-    clear_status(a.status);
-  }
-  // This CTA's sequence (or segment), pass and head: the longest sequences' CTAs of all
-  // passes come first, a group's heads side by side in the order of their sum.
-  const int hd = blockIdx.x % a.Hv, u = blockIdx.x / a.Hv, ri = u % a.n_roles, slot = u / a.n_roles;
-  const DecayRole& R = a.role[ri];
-  const int2 at = find_segment(a.cu, a.n_seqs, a.T, a.total, a.seg_chunks, a.nseg, slot);
-  const int s = at.x, seg = at.y;
-  if (s < 0) return;
-  const Range q = seq_range(a.cu, s, a.T, a.total);
-  const int nch = (q.len + CH - 1) / CH;
-  const int cb = seg * a.seg_chunks, ce = a.nseg == 1 ? nch : min(nch, cb + a.seg_chunks);
-  if (cb >= ce) return;
-  if (R.rev)
-    walk<SUM, true>(a, R, sm, q, s, slot, hd, cb, ce);
-  else
-    walk<SUM, false>(a, R, sm, q, s, slot, hd, cb, ce);
-}
-
-// SUM: an output head is the sum over a group's value heads, whose CTAs run side by
-// side, each one a chunk or so behind the one before it.
-template <bool SUM>
-__global__ void __launch_bounds__(WALK_THREADS, 1) k_decay(const __grid_constant__ DecayArgs a) {
-  extern __shared__ unsigned char raw[];
-  walk_block<SUM>(a, *reinterpret_cast<WalkSmem*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u)));
-  if (blockIdx.x == 0) pdl_wait();  // the grid ends after the one before it, whatever its CTAs had to do
-}
-
-// ---- segments ----------------------------------------------------------------------
+// ---- segments and final states ----------------------------------------------------------------------
 struct FoldSmem {
   unsigned char slot[FOLD_SLOTS][TILE];
   unsigned char rest[FOLD_TERMS - 1][TILE];  // further terms of the scaled B rows
@@ -652,19 +620,13 @@ struct FoldSmem {
   uint32_t tmem;
 };
 
-__device__ __forceinline__ void fold_block(const DecayFoldArgs& a, FoldSmem& sm) {
+// The first ten warps of a block: 0-7 scale, 8 issues the products, 9 loads.
+__device__ __forceinline__ void fold_block(const DecayFoldArgs& a, const DecayFoldRole& R, FoldSmem& sm, int slot, int j) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tc::warp_index();
   const int G = a.Hv / a.Hk;
-  if (!a.beside) {
-    pdl_wait();
-    pdl_release();
-    if (blockIdx.y == 0) clear_status(a.status);
-  }
-  const int j = blockIdx.x % a.Hv, slot = blockIdx.x / a.Hv;
   const int2 at = find_segment(a.cu, a.n_seqs, a.T, a.total, a.seg_chunks, a.nseg, slot);
   const int s = at.x, seg = at.y;
   if (s < 0) return;
-  const DecayFoldRole& R = a.role[blockIdx.y];
   const Range q = seq_range(a.cu, s, a.T, a.total);
   const int nch = (q.len + CH - 1) / CH;
   const int cb = seg * a.seg_chunks, ce = a.nseg == 1 ? nch : min(nch, cb + a.seg_chunks), nc = ce - cb;
@@ -672,7 +634,7 @@ __device__ __forceinline__ void fold_block(const DecayFoldArgs& a, FoldSmem& sm)
   if (nc <= 0) {
     if (a.nseg == 1)  // an empty sequence ends in the state that it began with
 #pragma unroll 4
-      for (int i = 4 * tid; i < HD * HD; i += 4 * FOLD_THREADS)
+      for (int i = 4 * tid; i < HD * HD; i += 4 * (int)blockDim.x)
         *reinterpret_cast<float4*>(R.last + sh * HD * HD + i) =
             R.x0 ? __ldg(reinterpret_cast<const float4*>(R.x0 + sh * HD * HD + i)) : make_float4(0.f, 0.f, 0.f, 0.f);
     return;
@@ -753,7 +715,7 @@ __device__ __forceinline__ void fold_block(const DecayFoldArgs& a, FoldSmem& sm)
         tc::commit_by(lead, &sm.barM[h]);
       }
     }
-  } else {
+  } else if (warp < 8) {
     const int j0 = 4 * (tid >> 6);  // 64 rows at a time, four threads to a row
     for (int i = 0; i < nc; ++i) {
       const int n = min(CH, q.len - chunk_of(i) * CH), tb = 2 * i, tcc = tb + 1;
@@ -830,12 +792,63 @@ __device__ __forceinline__ void fold_block(const DecayFoldArgs& a, FoldSmem& sm)
   if (warp == 0) tc::dealloc(sm.tmem, 512);
 }
 
-// A segment's own state; with one segment to a sequence the final state itself,
-// formed beside the walk (in three bf16 terms: an error of 1e-7 of the sums' sizes).
+// The segments' own states; with one segment to a sequence the final states, beside the
+// walk (in three bf16 terms: an error of 1e-7 of the sums' sizes).
 __global__ void __launch_bounds__(FOLD_THREADS, 1) k_decay_fold(const __grid_constant__ DecayFoldArgs a) {
   extern __shared__ unsigned char raw[];
-  fold_block(a, *reinterpret_cast<FoldSmem*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u)));
-  if (blockIdx.x == 0 && blockIdx.y == 0) pdl_wait();  // (as the walk)
+  if (!a.beside) {
+    pdl_wait();
+    pdl_release();
+    if (blockIdx.y == 0) clear_status(a.status);
+  }
+  fold_block(a, a.role[blockIdx.y], *reinterpret_cast<FoldSmem*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u)),
+             blockIdx.x / a.Hv, blockIdx.x % a.Hv);
+  if (blockIdx.x == 0 && blockIdx.y == 0) pdl_wait();  // the grid ends after the one before it
+}
+
+// The walks of all passes.  SUM: an output head is the sum over a group's value heads,
+// whose CTAs run side by side, each one a chunk or so behind the one before it.  FOLD:
+// and the final states, from CTAs beside them (f.n_roles of them a sequence and head).
+template <bool SUM, bool FOLD>
+__device__ __forceinline__ void decay_block(const DecayArgs& a, const DecayFoldArgs* f) {
+  extern __shared__ unsigned char raw[];
+  unsigned char* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  if (a.nseg == 1 && !a.beside) {  // (with segments, only the entering states wait for the kernel before)
+    pdl_wait();
+    pdl_release();
+    clear_status(a.status);
+  }
+  // This CTA's sequence (or segment), pass and head: the longest sequences' CTAs of all
+  // passes come first, a group's heads side by side in the order of their sum.
+  const int hd = blockIdx.x % a.Hv, u = blockIdx.x / a.Hv, kinds = a.n_roles + (FOLD ? f->n_roles : 0);
+  const int ri = u % kinds, slot = u / kinds;
+  if constexpr (FOLD) {
+    if (ri >= a.n_roles) {
+      fold_block(*f, f->role[ri - a.n_roles], *reinterpret_cast<FoldSmem*>(smem), slot, hd);
+      return;
+    }
+  }
+  const DecayRole& R = a.role[ri];
+  WalkSmem& sm = *reinterpret_cast<WalkSmem*>(smem);
+  const int2 at = find_segment(a.cu, a.n_seqs, a.T, a.total, a.seg_chunks, a.nseg, slot);
+  if (at.x < 0) return;
+  const Range q = seq_range(a.cu, at.x, a.T, a.total);
+  const int nch = (q.len + CH - 1) / CH, cb = at.y * a.seg_chunks, ce = a.nseg == 1 ? nch : min(nch, cb + a.seg_chunks);
+  if (cb >= ce) return;
+  if (R.rev)
+    walk<SUM, true>(a, R, sm, q, at.x, slot, hd, cb, ce);
+  else
+    walk<SUM, false>(a, R, sm, q, at.x, slot, hd, cb, ce);
+}
+template <bool SUM>
+__global__ void __launch_bounds__(WALK_THREADS, 1) k_decay(const __grid_constant__ DecayArgs a) {
+  decay_block<SUM, false>(a, nullptr);
+  if (blockIdx.x == 0) pdl_wait();  // the grid ends after the one before it, whatever its CTAs had to do
+}
+template <bool SUM>
+__global__ void __launch_bounds__(WALK_THREADS, 1) k_decay_small(const __grid_constant__ DecayArgs a,
+                                                                 const __grid_constant__ DecayFoldArgs f) {
+  decay_block<SUM, true>(a, &f);
 }
 
 // Entering states from the segments' own ones, in place, and the final state:
@@ -885,17 +898,18 @@ cudaError_t set_smem(K k, size_t bytes) {
 }  // namespace
 
 template <bool SUM>
-static cudaError_t launch_walk(const DecayArgs& a, cudaStream_t s) {
-  constexpr size_t smem = sizeof(WalkSmem) + 1024;
+static cudaError_t launch_walk(const DecayArgs& a, const DecayFoldArgs& f, cudaStream_t s) {
+  constexpr size_t smem = (sizeof(WalkSmem) > sizeof(FoldSmem) ? sizeof(WalkSmem) : sizeof(FoldSmem)) + 1024;
   static_assert(smem <= 227 * 1024, "shared memory");
-  cudaError_t e = set_smem(k_decay<SUM>, smem);
+  const cudaError_t e = f.n_roles ? set_smem(k_decay_small<SUM>, smem) : set_smem(k_decay<SUM>, smem);
   if (e != cudaSuccess) return e;
-  const long units = (long)a.n_roles * a.slots * a.Hv;
-  return launch_pdl(k_decay<SUM>, dim3((unsigned)units), dim3(WALK_THREADS), smem, s, a);
+  const dim3 grid((unsigned)((long)(a.n_roles + f.n_roles) * a.slots * a.Hv)), block(WALK_THREADS);
+  return f.n_roles ? launch_pdl(k_decay_small<SUM>, grid, block, smem, s, a, f)
+                   : launch_pdl(k_decay<SUM>, grid, block, smem, s, a);
 }
 
-cudaError_t launch_decay(const DecayArgs& a, cudaStream_t s) {
-  return a.Hv > a.Hk && a.role[0].shared ? launch_walk<true>(a, s) : launch_walk<false>(a, s);
+cudaError_t launch_decay(const DecayArgs& a, const DecayFoldArgs& f, cudaStream_t s) {
+  return a.Hv > a.Hk && a.role[0].shared ? launch_walk<true>(a, f, s) : launch_walk<false>(a, f, s);
 }
 
 cudaError_t launch_decay_fold(const DecayFoldArgs& a, cudaStream_t s) {

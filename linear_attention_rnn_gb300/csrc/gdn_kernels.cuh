@@ -266,7 +266,7 @@ cudaError_t launch_out_gate_bwd(const bf16* o, const bf16* z, const bf16* dy, bf
                                 cudaStream_t s);
 cudaError_t launch_step(const StepArgs& a, cudaStream_t s);
 // (all roles shared, or none)
-cudaError_t launch_decay(const DecayArgs& a, cudaStream_t s);
+cudaError_t launch_decay(const DecayArgs& a, const DecayFoldArgs& f, cudaStream_t s);
 // the segments' own states and the prefix over them (two launches); with one segment
 // to a sequence the final state alone (one launch)
 cudaError_t launch_decay_fold(const DecayFoldArgs& a, cudaStream_t s);

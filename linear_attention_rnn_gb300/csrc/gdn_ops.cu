@@ -104,6 +104,15 @@ DecayPlan decay_plan(int backward, int n_seqs, int total, int max_seqlen, int Hk
   return p;
 }
 
+// Final states without segments.  Where every CTA of the call finds an SM at once and
+// sequences are short, they are formed in the walk's own launch: the two codes in one
+// kernel cost the walk up to a tenth of its time, a launch costs the host some 4 us
+// (forwards, 2 to 4 sequences of 2 to 6 chunks: 19-23 us against 24-26; of 8 and 16
+// chunks: 28 and 51 us against 27 and 47).
+bool one_launch(const DecayArgs& a) {
+  return a.seg_chunks <= 6 && (long)(a.n_roles + 1) * a.slots * a.Hv <= sm_count();
+}
+
 DecayFoldArgs fold_args(const DecayArgs& a) {
   DecayFoldArgs f;
   memset(&f, 0, sizeof f);
@@ -126,8 +135,8 @@ int decay_check(int n_seqs, int total, int max_seqlen, int Hk, int Hv, int d_k, 
   if (n_seqs < 0 || total < 0 || max_seqlen < 0 || Hk <= 0 || Hv <= 0 || Hv % Hk != 0) return GDN_ERR_ARG;
   if (d_k != HD || d_v != HD) return GDN_ERR_SHAPE;
   if (!cu && n_seqs > 0 && total % n_seqs != 0) return GDN_ERR_ARG;
-  // (blocks of the three passes in one grid dimension)
-  if (((long long)n_seqs + total / CH) * Hv > (1LL << 29)) return GDN_ERR_ARG;
+  // (blocks of the three passes and the final state in one grid dimension)
+  if (((long long)n_seqs + total / CH) * Hv >= (1LL << 29)) return GDN_ERR_ARG;
   if (!row_stride_ok(sq, Hk) || !row_stride_ok(sk, Hk) || !row_stride_ok(sv, Hv)) return GDN_ERR_ARG;
   return GDN_OK;
 }
@@ -326,9 +335,11 @@ int gdn_decay_fwd(const void* q, const void* k, const void* v, const float* deca
     f.role[0].x = at<float>(ws, p.xf);
     if ((rc = cuda_status(launch_decay_fold(f, s)))) return rc;
     r.xseg = f.role[0].x;
-    return cuda_status(launch_decay(a, s));
   }
-  if ((rc = cuda_status(launch_decay(a, s))) || !hT) return rc;
+  const int last = p.nseg == 1 && hT;
+  f.n_roles = last && one_launch(a);
+  if ((rc = cuda_status(launch_decay(a, f, s))) || !last || f.n_roles) return rc;
+  f.n_roles = 1;
   f.beside = 1;
   return cuda_status(launch_decay_fold(f, s));
 }
@@ -419,15 +430,17 @@ int gdn_decay_bwd(const void* q, const void* k, const void* v, const float* deca
     rq.xseg = ff.x;
     rk.xseg = rv.xseg = fr.x;
   }
-  if (p.nseg == 1 && dh0) {
-    // The final state in a kernel of its own, beside the walk.  It goes first: its CTAs
-    // are short, and behind the walk's they would start only when the last of those has.
-    f.n_roles = 1;
-    f.role[0] = fr;
+  const int last = p.nseg == 1 && dh0;
+  f.role[0] = fr;
+  f.n_roles = last;
+  if (last && !one_launch(a)) {
+    // ahead of the walk: its CTAs are short, and behind the walk's they would start
+    // only when the last of those has
     if ((rc = cuda_status(launch_decay_fold(f, s)))) return rc;
     a.beside = 1;
+    f.n_roles = 0;
   }
-  return cuda_status(launch_decay(a, s));
+  return cuda_status(launch_decay(a, f, s));
 }
 
 size_t gdn_attn_workspace_bytes(int backward, int n_seqs, int total_q, int total_k, int max_k, int Hq, int Hk,
