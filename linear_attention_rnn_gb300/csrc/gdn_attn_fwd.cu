@@ -16,7 +16,7 @@
 // after the first tiles is rare: O is rescaled in tensor memory by the row's own
 // thread, between the product that wrote it and the next one.
 //
-// Few rows over many keys (single tokens over a cache): the keys are split over
+// Few rows over many keys (a prompt's part over a cache): the keys are split over
 // CTAs, each writes its own normalised output and log-sum in fp32, and a second
 // kernel joins them.
 //
@@ -26,8 +26,7 @@
 // x 128 exponentials, 1024 cycles of the SM's four units, which the other tile's
 // products have to hide).  Packed prompts of 0 to 3000 tokens (4 key heads): 64 us,
 // 1.06 PFLOP/s; the start of a CTA, its diagonal tiles and the last round are the rest.
-// Single tokens: HBM (k and v once).  32 caches of 1 to 16214 rows, 4 key heads: 102 us,
-// 5.2 TB/s, 0.77 of a copy's rate: CTAs of up to 32 key tiles in two uneven rounds.
+// (Calls with few rows to a sequence: gdn_attn_split.cu.)
 #include <limits.h>
 
 #include "gdn_attn.cuh"
@@ -342,12 +341,12 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ AttnA
   const int lane = threadIdx.x & 31;
   if (row >= rows) return;
   float top = -INFINITY;
-  for (int s = lane; s < 2 * a.n_splits; s += 32) top = fmaxf(top, a.part_lse[s * rows + row]);
+  for (int s = lane; s < a.n_parts; s += 32) top = fmaxf(top, a.part_lse[s * rows + row]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   float total = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
   if (top > -INFINITY)
-    for (int s = 0; s < 2 * a.n_splits; ++s) {
+    for (int s = 0; s < a.n_parts; ++s) {
       const float l = a.part_lse[s * rows + row];
       if (l == -INFINITY) continue;
       const float f = expf(l - top);
@@ -378,7 +377,10 @@ cudaError_t launch_attn_fwd(const AttnArgs& a, cudaStream_t s) {
   const int K = 2 * (CH / (a.Hq / a.Hk));
   const dim3 grid((unsigned)a.Hk * (unsigned)(a.total_q / K + a.n_seqs), (unsigned)a.n_splits);
   e = launch_pdl(k_attn_fwd, grid, dim3(FWD_THREADS), smem, s, a);
-  if (e != cudaSuccess || a.n_splits == 1) return e;
+  return e != cudaSuccess || a.n_splits == 1 ? e : launch_attn_join(a, s);
+}
+
+cudaError_t launch_attn_join(const AttnArgs& a, cudaStream_t s) {
   const long rows = (long)a.total_q * a.Hq;
   return launch_pdl(k_attn_join, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, a);
 }

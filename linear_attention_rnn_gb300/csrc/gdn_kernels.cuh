@@ -207,8 +207,8 @@ struct AttnArgs {
   const int* k_len;     // [n_seqs] used rows of each sequence's keys (nullable; forward)
   bf16* o;              // [total_q][Hq][HD]
   float* lse;           // [total_q][Hq] (forward: nullable)
-  float* part;          // [2 n_splits][total_q][Hq][HD]
-  float* part_lse;      // [2 n_splits][total_q][Hq]
+  float* part;          // [n_parts][total_q][Hq][HD]
+  float* part_lse;      // [n_parts][total_q][Hq]
   const bf16* dOp;      // backward: dO and o as plain rows, delta = dO . o
   const bf16* op;
   float* delta;         // [total_q][Hq]
@@ -219,6 +219,7 @@ struct AttnArgs {
   float scale;
   int n_seqs, total_q, total_k, Hq, Hk;
   int split_tiles, n_splits;  // key tiles to a split
+  int n_parts;                // 2 to a split (k_attn_fwd) or 1 (k_attn_split)
 };
 
 // The status word of a call, cleared by the first block of its first kernel: that
@@ -271,6 +272,8 @@ cudaError_t launch_decay(const DecayArgs& a, const DecayFoldArgs& f, cudaStream_
 // to a sequence the final state alone (one launch)
 cudaError_t launch_decay_fold(const DecayFoldArgs& a, cudaStream_t s);
 cudaError_t launch_attn_fwd(const AttnArgs& a, cudaStream_t s);
+cudaError_t launch_attn_split(const AttnArgs& a, cudaStream_t s);  // keys in maps of 64 rows
+cudaError_t launch_attn_join(const AttnArgs& a, cudaStream_t s);
 // dO . o per row, then the gradients of k and v, then that of q
 cudaError_t launch_attn_bwd(const AttnArgs& a, cudaStream_t s);
 // (A, B) = (I, 0) for n [HD x HD] fp32 pairs (A nullable).

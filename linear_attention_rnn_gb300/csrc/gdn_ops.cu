@@ -143,14 +143,24 @@ int decay_check(int n_seqs, int total, int max_seqlen, int Hk, int Hv, int d_k, 
 
 // ---- causal softmax attention ---------------------------------------------------------
 struct AttnPlan {
-  int split_tiles, n_splits;
+  int few, split_tiles, n_splits, n_parts;
   size_t status, part, part_lse, delta, total;
 };
 
-// Key splits of the forward.  A CTA holds 256 / G tokens of one key head.  The
-// estimate, in key tiles of a CTA (0.8 us measured): the work of all CTAs over the
-// SMs, contexts being 0.6 of the longest one on average, most of the longest
-// CTA's behind it, 6 for a CTA's start and end, 4 for the join.
+// The forward's kernel and its key splits.
+//
+// Calls with one query tile to a sequence on average (tokens over caches, short
+// prompts) take k_attn_split, two CTAs to an SM: 32 caches of up to 16214 rows 94 us
+// against 103 in k_attn_fwd, 256 of 1024 102 against 136, 64 prompts of 100 tokens 22
+// against 32.  Its estimate, in us: memory's time for all keys (64 KiB per key tile and
+// head, contexts being 0.8 of the longest one on average), or what one CTA takes by
+// itself (1.6 a key tile, measured), 10 for each round of CTAs, 9 and 0.2 a split for
+// the join and its launch.
+//
+// Else a CTA of k_attn_fwd holds 256 / G tokens of one key head.  The estimate, in key
+// tiles of a CTA (0.8 us measured): the work of all CTAs over the SMs, contexts being
+// 0.6 of the longest one on average, most of the longest CTA's behind it, 6 for a CTA's
+// start and end, 4 for the join.
 AttnPlan attn_plan(int backward, int n_seqs, int total_q, int max_k, int Hq, int Hk) {
   AttnPlan p;
   memset(&p, 0, sizeof p);
@@ -159,7 +169,22 @@ AttnPlan attn_plan(int backward, int n_seqs, int total_q, int max_k, int Hq, int
   p.split_tiles = tiles > 0 ? (int)tiles : 1;
   p.n_splits = 1;
   double best = 1e300;
-  for (long k = 1; !backward && k <= 64 && 4 * k <= tiles + 3; ++k) {
+  p.few = !backward && tiles > 0 && total_q <= (long)n_seqs * (CH / (Hq / Hk));
+  if (p.few) {
+    const double heads = (double)Hk * n_seqs, all = 0.0097 * 0.8 * heads * tiles;
+    for (long k = 1; k <= 64 && k <= tiles; ++k) {
+      const long per = (tiles + k - 1) / k, splits = (tiles + per - 1) / per;
+      const double rounds = (double)(long)(heads * splits / (2.0 * sms) + 0.999);
+      const double t = (all + 0.4 * per > 1.6 * per ? all + 0.4 * per : 1.6 * per) + 10.0 * (rounds > 1.0 ? rounds : 1.0) +
+                       (splits > 1 ? 9.0 + 0.2 * splits : 0.0);
+      if (t < best) {
+        best = t;
+        p.split_tiles = (int)per;
+        p.n_splits = (int)splits;
+      }
+    }
+  }
+  for (long k = 1; !backward && !p.few && k <= 64 && 4 * k <= tiles + 3; ++k) {
     const long per = (tiles + k - 1) / k, splits = (tiles + per - 1) / per;
     const double t = ctas * (0.6 * tiles + 6.0 * splits) / sms + 0.8 * (per + 6.0) + (splits > 1 ? 4.0 : 0.0);
     if (t < best * 0.97) {
@@ -179,8 +204,9 @@ AttnPlan attn_plan(int backward, int n_seqs, int total_q, int max_k, int Hq, int
   if (backward) {
     p.delta = take(rows * sizeof(float));
   } else if (p.n_splits > 1) {
-    p.part = take(rows * 2 * p.n_splits * HD * sizeof(float));
-    p.part_lse = take(rows * 2 * p.n_splits * sizeof(float));
+    p.n_parts = p.few ? p.n_splits : 2 * p.n_splits;
+    p.part = take(rows * p.n_parts * HD * sizeof(float));
+    p.part_lse = take(rows * p.n_parts * sizeof(float));
   }
   p.total = off;
   return p;
@@ -201,7 +227,8 @@ int attn_check(int n_seqs, int total_q, int total_k, int max_k, int Hq, int Hk, 
 
 // Tensor maps and the arguments that both directions share.
 int attn_args(AttnArgs& a, const void* q, const void* k, const void* v, const int* cu_q, const int* cu_k, int n_seqs,
-              int total_q, int total_k, int Hq, int Hk, float scale, long long sq, long long sk, long long sv) {
+              int total_q, int total_k, int Hq, int Hk, float scale, long long sq, long long sk, long long sv,
+              int key_rows = CH) {
   memset(&a, 0, sizeof a);
   a.cu_q = cu_q;
   a.cu_k = cu_k;
@@ -214,8 +241,8 @@ int attn_args(AttnArgs& a, const void* q, const void* k, const void* v, const in
   const int G = Hq / Hk;
   if (!tmap_rows(&a.q, q, total_q, Hq, HD, (uint64_t)sq * 2, G, CH / G)) return GDN_ERR_CUDA;
   if (total_k == 0) return GDN_OK;  // (no key tile is ever loaded)
-  if (!tmap_rows(&a.k, k, total_k, Hk, HD, (uint64_t)sk * 2, 1, CH) ||
-      !tmap_rows(&a.v, v, total_k, Hk, HD, (uint64_t)sv * 2, 1, CH))
+  if (!tmap_rows(&a.k, k, total_k, Hk, HD, (uint64_t)sk * 2, 1, key_rows) ||
+      !tmap_rows(&a.v, v, total_k, Hk, HD, (uint64_t)sv * 2, 1, key_rows))
     return GDN_ERR_CUDA;
   return GDN_OK;
 }
@@ -467,7 +494,8 @@ int gdn_attn_fwd(const void* q, const void* k, const void* v, const int* cu_q, c
   const AttnPlan p = attn_plan(0, n_seqs, total_q, max_k < total_k ? max_k : total_k, Hq, Hk);
   if (!workspace_ok(ws, ws_bytes, p.total)) return GDN_ERR_WORKSPACE;
   AttnArgs a;
-  if ((rc = attn_args(a, q, k, v, cu_q, cu_k, n_seqs, total_q, total_k, Hq, Hk, scale, q_stride, k_stride, v_stride)))
+  if ((rc = attn_args(a, q, k, v, cu_q, cu_k, n_seqs, total_q, total_k, Hq, Hk, scale, q_stride, k_stride, v_stride,
+                      p.few ? CH / 2 : CH)))
     return rc;
   if (!tmap_rows(&a.mo, o, total_q, Hq, HD, (uint64_t)Hq * HD * 2, Hq / Hk, CH / (Hq / Hk))) return GDN_ERR_CUDA;
   a.k_len = k_len;
@@ -476,10 +504,11 @@ int gdn_attn_fwd(const void* q, const void* k, const void* v, const int* cu_q, c
   a.status = ws ? at<int>(ws, p.status) : nullptr;
   a.split_tiles = p.split_tiles;
   a.n_splits = p.n_splits;
+  a.n_parts = p.n_parts;
   a.part = at<float>(ws, p.part);
   a.part_lse = at<float>(ws, p.part_lse);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return cuda_status(launch_attn_fwd(a, s));
+  return cuda_status(p.few ? launch_attn_split(a, s) : launch_attn_fwd(a, s));
 }
 
 int gdn_attn_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dO,

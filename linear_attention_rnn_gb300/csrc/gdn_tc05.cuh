@@ -515,12 +515,23 @@ __device__ __forceinline__ void st8_bf16(uint32_t taddr, const float (&v)[16]) {
                : "memory");
 }
 
+// D[128 x 64] = A B^T of K-major SW128 tiles of 128 and 64 rows, by a warp
+__device__ __forceinline__ void gemm128x64_by(uint32_t leader, uint32_t tmem_d, uint32_t a_smem, uint32_t b_smem) {
+  const uint64_t da0 = desc_sw128(a_smem), db0 = desc_sw128(b_smem);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const uint32_t in = (uint32_t)(k & 3) * 32u, half = (uint32_t)(k >> 2);
+    mma_by(leader, tmem_d, da0 + ((half * 128u * 128u + in) >> 4), db0 + ((half * 64u * 128u + in) >> 4),
+           idesc_bf16(128, 64), k > 0 ? 1u : 0u);
+  }
+}
 // 64 of the K-values: A in tensor memory from tmem_a on (32 columns), B from the row
-// of its tile that b_smem points to, by a warp
+// of its tile (of ROWS rows) that b_smem points to, by a warp
+template <int ROWS = 128>
 __device__ __forceinline__ void gemm_ts64_by(uint32_t leader, uint32_t tmem_d, uint32_t tmem_a, uint32_t b_smem,
                                              bool accumulate_first) {
   const uint32_t idesc = idesc_bf16(128, 128) | (1u << 16);
-  const uint64_t db0 = desc_sw128_mn(b_smem, 128u * 128u);
+  const uint64_t db0 = desc_sw128_mn(b_smem, ROWS * 128u);
 #pragma unroll
   for (int k = 0; k < 4; ++k)
     mma_ts_by(leader, tmem_d, tmem_a + 8u * (uint32_t)k, db0 + (((uint32_t)k * 2048u) >> 4), idesc,
