@@ -149,10 +149,10 @@ struct AttnPlan {
 
 // The forward's kernel and its key splits.
 //
-// Calls with one query tile to a sequence on average (tokens over caches, short
-// prompts) take k_attn_split, two CTAs to an SM: 32 caches of up to 16214 rows 94 us
-// against 103 in k_attn_fwd, 256 of 1024 102 against 136, 64 prompts of 100 tokens 22
-// against 32.  Its estimate, in us: memory's time for all keys (64 KiB per key tile and
+// Calls with one query tile to a sequence on average (tokens over caches) or at most five
+// key tiles (short prompts) take k_attn_split, two CTAs to an SM: 32 caches of up to
+// 16214 rows 94 us against 103 in k_attn_fwd, 256 of 1024 102 against 136, 64 prompts of
+// 100 tokens 22 against 32, 8 of 600 25 against 28, but 8 of 1000 52 against 47.  Its estimate, in us: memory's time for all keys (64 KiB per key tile and
 // head, contexts being 0.8 of the longest one on average), or what one CTA takes by
 // itself (1.6 a key tile, measured), 10 for each round of CTAs, 9 and 0.2 a split for
 // the join and its launch.
@@ -169,7 +169,7 @@ AttnPlan attn_plan(int backward, int n_seqs, int total_q, int max_k, int Hq, int
   p.split_tiles = tiles > 0 ? (int)tiles : 1;
   p.n_splits = 1;
   double best = 1e300;
-  p.few = !backward && tiles > 0 && total_q <= (long)n_seqs * (CH / (Hq / Hk));
+  p.few = !backward && tiles > 0 && (total_q <= (long)n_seqs * (CH / (Hq / Hk)) || tiles <= 5);
   if (p.few) {
     const double heads = (double)Hk * n_seqs, all = 0.0097 * 0.8 * heads * tiles;
     for (long k = 1; k <= 64 && k <= tiles; ++k) {
