@@ -19,10 +19,9 @@
 // cores run the next S; while they form P, the last gradient product.
 //
 // Roundings: P and dS become bf16 once, as operands, and so does every result; delta
-// takes the forward's rounded o, as the caller has it.  A gradient's error against 64 bits
-// is then 2.3e-3 to 2.9e-3 in the 2-norm (rounding the result alone: 1.7e-3), of dq and dk
-// up to 7e-3 where all sequences have two or three tokens and dP - delta cancels; scores,
-// lse, delta and all sums are fp32.
+// takes the forward's rounded o, as the caller has it, where a row sees more than EARLY
+// keys.  A gradient's error against 64 bits is then 2.3e-3 to 2.5e-3 in the 2-norm
+// (rounding the result alone: 1.7e-3); scores, lse, delta and all sums are fp32.
 //
 // Bound: the tensor rate (7 x 512 cycles per pair of 128 x 128 tiles).  Measured on a
 // GB300, 4096 + 2048 + 1000 + 977 + 71 packed tokens, 16 query and 4 key heads: 230 us,
@@ -41,12 +40,69 @@ constexpr int KV_SLOTS = 4;  // Q, dO of two query tiles
 constexpr int Q_SLOTS = 5;   // K, V of two key tiles and a half
 
 // ---- delta_i = dO_i . o_i: half a warp to a row, four rows in flight ------------------
+// The caller's o is rounded to bf16, which shows in the gradients of rows that see few
+// keys (their dP - delta is largest, and cancels most).  For rows with up to EARLY keys
+// delta is therefore formed as sum_j p_ij dp_ij: one pass over a sequence's first keys, by
+// blocks of their own, first in the grid.  It brings the error of dq and dk against 64
+// bits from 2.5e-3 to 2.4e-3 in the 2-norm, of sequences of two or three tokens from 7e-3
+// to 2.5e-3, and costs 2 us of 323 (16 keys: 2.38e-3, and 3 to 6 us).
 constexpr int DELTA_ROWS = 64;  // rows per block of 256 threads
-__global__ void __launch_bounds__(256) k_attn_delta(const __grid_constant__ AttnArgs a) {
+constexpr int EARLY = 8;
+constexpr int EARLY_BLOCKS = 65536;  // at most
+
+__device__ __forceinline__ float dot8(const uint4& x, const uint4& y) {
+  const uint32_t u[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w};
+  float d = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = unpack_bf16(u[i]), q = unpack_bf16(v[i]);
+    d += p.x * q.x + p.y * q.y;
+  }
+  return d;
+}
+__device__ __forceinline__ float sum16(float d, unsigned mask) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) d += __shfl_xor_sync(mask, d, o);
+  return d;
+}
+
+// Rows (sequence, keys seen - 1, head), half a warp to each
+__device__ __forceinline__ void early_delta(const AttnArgs& a, int early_blocks) {
+  const int G = a.Hq / a.Hk, c = 8 * (threadIdx.x & 15);
+  const unsigned half = 0xffffu << (threadIdx.x & 16);
+  const long all = (long)a.n_seqs * EARLY * a.Hq;
+  for (long i = (long)blockIdx.x * 16 + (threadIdx.x >> 4); i < all; i += 16L * early_blocks) {
+    const int head = (int)(i % a.Hq), vis = (int)(i / a.Hq % EARLY), s = (int)(i / a.Hq / EARLY);
+    const int2 q = rows_of(a.cu_q, s, a.n_seqs, a.total_q), k = rows_of(a.cu_k, s, a.n_seqs, a.total_k);
+    const int t = vis - (k.y - q.y);
+    if (t < 0 || t >= q.y || vis >= k.y) continue;
+    const long row = ((long)q.x + t) * a.Hq + head;
+    const uint4 x = *reinterpret_cast<const uint4*>(a.pq + ((long)q.x + t) * a.sq + head * HD + c);
+    const uint4 y = *reinterpret_cast<const uint4*>(a.dOp + row * HD + c);
+    const bf16* kp = a.pk + (long)k.x * a.sk + head / G * HD + c;
+    const bf16* vp = a.pv + (long)k.x * a.sv + head / G * HD + c;
+    const float lse = a.lse[row] * LOG2E, sc = a.scale * LOG2E;
+    float d = 0.f;
+#pragma unroll 4
+    for (int j = 0; j <= vis; ++j) {
+      const float z = sum16(dot8(x, *reinterpret_cast<const uint4*>(kp + j * a.sk)), half);
+      const float dp = sum16(dot8(y, *reinterpret_cast<const uint4*>(vp + j * a.sv)), half);
+      d += ex2(z * sc - lse) * dp;
+    }
+    if ((threadIdx.x & 15) == 0) a.delta[row] = d;
+  }
+}
+
+__global__ void __launch_bounds__(256, 4) k_attn_delta(const __grid_constant__ AttnArgs a, int early_blocks) {
   pdl_wait();  // (before it lets the next kernel start, which reads its inputs without a wait)
   pdl_release();
   clear_status(a.status);
-  const long rows = (long)a.total_q * a.Hq, row0 = (long)blockIdx.x * DELTA_ROWS + (threadIdx.x >> 4);
+  if ((int)blockIdx.x < early_blocks) {
+    early_delta(a, early_blocks);
+    return;
+  }
+  const long rows = (long)a.total_q * a.Hq;
+  const long row0 = (long)((int)blockIdx.x - early_blocks) * DELTA_ROWS + (threadIdx.x >> 4);
   const int c = 8 * (threadIdx.x & 15);
   uint4 x[4], y[4];
 #pragma unroll
@@ -55,18 +111,24 @@ __global__ void __launch_bounds__(256) k_attn_delta(const __grid_constant__ Attn
     x[k] = *reinterpret_cast<const uint4*>(a.dOp + row * HD + c);
     y[k] = *reinterpret_cast<const uint4*>(a.op + row * HD + c);
   }
+  // whether the four rows are early_delta's, a row to a lane, while they are on their way
+  const int tok = (int)(min(row0 + 16 * (threadIdx.x & 3), rows - 1) / a.Hq);
+  int s = a.cu_q ? 0 : tok / (a.total_q / a.n_seqs);
+  if (a.cu_q)
+    for (int hi = a.n_seqs; hi - s > 1;) {  // the last sequence that begins at tok or before
+      const int mid = (s + hi) >> 1;
+      if (a.cu_q[mid] <= tok)
+        s = mid;
+      else
+        hi = mid;
+    }
+  const int2 q = rows_of(a.cu_q, s, a.n_seqs, a.total_q), kk = rows_of(a.cu_k, s, a.n_seqs, a.total_k);
+  const int vis = tok - q.x + kk.y - q.y;
+  const unsigned skip = __ballot_sync(0xffffffffu, vis >= 0 && vis < EARLY) >> (threadIdx.x & 16);
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const uint32_t u[4] = {x[k].x, x[k].y, x[k].z, x[k].w}, v[4] = {y[k].x, y[k].y, y[k].z, y[k].w};
-    float d = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 p = unpack_bf16(u[i]), q = unpack_bf16(v[i]);
-      d += p.x * q.x + p.y * q.y;
-    }
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-    if ((threadIdx.x & 15) == 0 && row0 + 16 * k < rows) a.delta[row0 + 16 * k] = d;
+    const float d = sum16(dot8(x[k], y[k]), 0xffffffffu);
+    if ((threadIdx.x & 15) == 0 && row0 + 16 * k < rows && !(skip >> k & 1)) a.delta[row0 + 16 * k] = d;
   }
 }
 
@@ -513,7 +575,9 @@ cudaError_t launch_attn_bwd(const AttnArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int TT = CH / (a.Hq / a.Hk);
   const long rows = (long)a.total_q * a.Hq;
-  e = launch_pdl(k_attn_delta, dim3((unsigned)((rows + DELTA_ROWS - 1) / DELTA_ROWS)), dim3(256), 0, s, a);
+  const long early_rows = (long)a.n_seqs * EARLY * a.Hq;
+  const int early = (int)((early_rows + 15) / 16 < EARLY_BLOCKS ? (early_rows + 15) / 16 : EARLY_BLOCKS);
+  e = launch_pdl(k_attn_delta, dim3((unsigned)((rows + DELTA_ROWS - 1) / DELTA_ROWS + early)), dim3(256), 0, s, a, early);
   if (e != cudaSuccess) return e;
   const int kv = a.Hk * (a.total_k / CH + a.n_seqs), q = a.Hk * (a.total_q / TT + a.n_seqs);
   return launch_pdl(k_attn_bwd, dim3((unsigned)(kv + q)), dim3(BWD_THREADS), smem, s, a, kv);

@@ -211,6 +211,8 @@ struct AttnArgs {
   float* part_lse;      // [n_parts][total_q][Hq]
   const bf16* dOp;      // backward: dO and o as plain rows, delta = dO . o
   const bf16* op;
+  const bf16 *pq, *pk, *pv;  // and q, k, v, elements between their rows
+  long sq, sk, sv;
   float* delta;         // [total_q][Hq]
   bf16* dq;
   bf16* dk;

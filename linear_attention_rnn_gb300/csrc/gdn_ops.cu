@@ -544,6 +544,12 @@ int gdn_attn_bwd(const void* q, const void* k, const void* v, const void* o, con
   a.lse = const_cast<float*>(lse);
   a.dOp = static_cast<const bf16*>(dO);
   a.op = static_cast<const bf16*>(o);
+  a.pq = static_cast<const bf16*>(q);
+  a.pk = static_cast<const bf16*>(k);
+  a.pv = static_cast<const bf16*>(v);
+  a.sq = q_stride;
+  a.sk = k_stride;
+  a.sv = v_stride;
   a.delta = at<float>(ws, p.delta);
   a.dq = static_cast<bf16*>(dq);
   a.dk = static_cast<bf16*>(dk);
