@@ -393,7 +393,8 @@ int gdn_decay_bwd(const void* q, const void* k, const void* v, const float* deca
  *     o_i = sum_j p_ij v_j,   p_ij = exp(scale q_i . k_j - lse_i),   lse_i = log sum_j exp(..).
  * n = m is a prompt, n < m a prompt or single tokens continuing m - n cached
  * keys.  A query that sees no key (n > m, or m = 0) has o = 0, lse = -inf and
- * passes no gradient.
+ * passes no gradient.  One that sees a score of NaN or plus infinity (or one too large
+ * for fp32) has o and lse NaN, however the keys are split.
  * q, o [total_q, Hq, d], k, v [total_k, Hk, d] bf16, d = 128, Hq a multiple of
  * Hk, at most 128 query heads to a key head (q_stride, k_stride, v_stride as for
  * the single-token forms); lse [total_q, Hq] fp32 (NULL = not written);

@@ -28,6 +28,7 @@
 // 1.06 PFLOP/s; the start of a CTA, its diagonal tiles and the last round are the rest.
 // (Calls with few rows to a sequence: gdn_attn_split.cu.)
 #include <limits.h>
+#include <math.h>
 
 #include "gdn_attn.cuh"
 
@@ -283,8 +284,9 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) k_attn_fwd(const __grid_consta
     const bool tile = a.n_splits == 1 && first + TT <= sq.ql;
     if (any) {
       const long row = ((long)sq.q0 + tok) * a.Hq + kh * G + r % G;
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      const float lse = l > 0.f ? m * a.scale + logf(l) : -INFINITY;
+      // (a sum of zero: the row sees no key; one of NaN is neither greater nor equal, and goes on)
+      const float inv = l != 0.f ? 1.f / l : 0.f;
+      const float lse = l != 0.f ? m * a.scale + logf(l) : -INFINITY;
 #pragma unroll 1
       for (int g = 0; g < 4; ++g) {
         float y[32];
@@ -300,7 +302,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) k_attn_fwd(const __grid_consta
             stage32(sm.q[x], r, 32 * g, y, inv);
           } else if (a.n_splits == 1) {
             store32(a.o + row * HD + 32 * g, y, inv);
-          } else if (l > 0.f) {  // (the join reads a part only where its lse is finite)
+          } else if (l != 0.f) {  // (the join reads no part whose lse is minus infinity)
             float* d = a.part + ((long)(2 * split + x) * a.total_q * a.Hq + row) * HD + 32 * g;
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -333,7 +335,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) k_attn_fwd(const __grid_consta
   if (warp == 0) tc::dealloc(sm.tmem, 512);
 }
 
-// Joins the splits of a row: o = sum_s e^{lse_s - lse} o_s.  One warp per row.
+// Joins the splits of a row: o = sum_s e^{lse_s - lse} o_s.  One warp per row.  A part of
+// NaN makes the row NaN, as it would be in one piece.
 __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ AttnArgs a) {
   pdl_wait();
   pdl_release();
@@ -341,11 +344,17 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ AttnA
   const int lane = threadIdx.x & 31;
   if (row >= rows) return;
   float top = -INFINITY;
-  for (int s = lane; s < a.n_parts; s += 32) top = fmaxf(top, a.part_lse[s * rows + row]);
+  bool nan = false;  // (which fmaxf passes over)
+  for (int s = lane; s < a.n_parts; s += 32) {
+    const float l = a.part_lse[s * rows + row];
+    nan |= isnan(l);
+    top = fmaxf(top, l);
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (__any_sync(0xffffffffu, nan)) top = NAN;
   float total = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
-  if (top > -INFINITY)
+  if (top != -INFINITY)
     for (int s = 0; s < a.n_parts; ++s) {
       const float l = a.part_lse[s * rows + row];
       if (l == -INFINITY) continue;
@@ -357,10 +366,10 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ AttnA
       y[2] += f * p.z;
       y[3] += f * p.w;
     }
-  const float inv = total > 0.f ? 1.f / total : 0.f;
+  const float inv = total != 0.f ? 1.f / total : 0.f;
   *reinterpret_cast<uint2*>(a.o + row * HD + 4 * lane) =
       make_uint2(pack_bf16(inv * y[0], inv * y[1]), pack_bf16(inv * y[2], inv * y[3]));
-  if (a.lse && lane == 0) a.lse[row] = total > 0.f ? top + logf(total) : -INFINITY;
+  if (a.lse && lane == 0) a.lse[row] = total != 0.f ? top + logf(total) : -INFINITY;
 }
 
 }  // namespace

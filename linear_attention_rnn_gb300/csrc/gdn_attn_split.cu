@@ -201,7 +201,8 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 2) k_attn_split(const __grid_co
     tc::fence_after();
     if (any) {
       const long row = ((long)sq.q0 + tok) * a.Hq + kh * G + r % G, part = (long)split * a.total_q * a.Hq + row;
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      // (a sum of zero: the row sees no key; one of NaN is neither greater nor equal, and goes on)
+      const float inv = l != 0.f ? 1.f / l : 0.f;
 #pragma unroll 1
       for (int g = 0; g < 4; ++g) {
         float y[32];
@@ -214,7 +215,7 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 2) k_attn_split(const __grid_co
             for (int j = 0; j < 32; ++j) y[j] = 0.f;
           }
           store32(a.o + row * HD + 32 * g, y, inv);
-        } else if (valid && l > 0.f) {  // (the join reads a part only where its lse is finite)
+        } else if (valid && l != 0.f) {  // (the join reads no part whose lse is minus infinity)
           float* d = a.part + part * HD + 32 * g;
 #pragma unroll
           for (int j = 0; j < 8; ++j)
@@ -223,7 +224,7 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 2) k_attn_split(const __grid_co
         }
         __syncwarp();
       }
-      const float lse = l > 0.f ? m * a.scale + logf(l) : -INFINITY;
+      const float lse = l != 0.f ? m * a.scale + logf(l) : -INFINITY;
       if (valid && a.n_splits > 1) a.part_lse[part] = lse;
       if (valid && a.n_splits == 1 && a.lse) a.lse[row] = lse;
     }
