@@ -492,7 +492,7 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
           sm.col[1][r] = expf(-wd * (float)r);
         }
       }
-      const bool mild = wd > -2.5f;  // (e^{-31 w} is a number, and far from fp32's largest)
+      const bool mild = wd > -2.5f;  // (e^{-31 w} and e^{31 w} are normal fp32 numbers)
       asm volatile("bar.sync 1, 256;" ::: "memory");
       for (int it = 0; it < n_it; ++it) {
         if (it > 0) output(it - 1);
@@ -502,7 +502,8 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
         // Of the four 32 x 32 blocks of a warp's rows, those on the far side of the
         // diagonal are zero, those on the near side have the factor e^{w |i - j|} = (to
         // the block's edge) * (from the edge), both <= 1.  On the diagonal block it is
-        // e^{w i} * e^{-w j} from the block's corner, unless the second one could overflow.
+        // e^{w i} * e^{-w j} from the block's corner, unless one of them could leave fp32's
+        // range.  The scores meet the finished factor only: they may be of any size.
 #pragma unroll 1
         for (int h = 4 * half; h < 4 * half + 4; ++h) {  // 16 columns at a time
           const int g = h >> 1, j0 = 16 * h;
@@ -518,9 +519,9 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
               const float* col = (REV ? sm.tab : sm.col[g == own]) + (j0 & 16);
 #pragma unroll
               for (int i = 0; i < 16; i += 4) {
-                const float4 f = *reinterpret_cast<const float4*>(col + i);
-                tc::mul2(v[i], v[i + 1], edge, edge);
-                tc::mul2(v[i + 2], v[i + 3], edge, edge);
+                float4 f = *reinterpret_cast<const float4*>(col + i);
+                tc::mul2(f.x, f.y, edge, edge);  // (the factor first: it is at most 1, its parts may not be)
+                tc::mul2(f.z, f.w, edge, edge);
                 tc::mul2(v[i], v[i + 1], f.x, f.y);
                 tc::mul2(v[i + 2], v[i + 3], f.z, f.w);
               }
