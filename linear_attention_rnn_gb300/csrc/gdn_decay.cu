@@ -675,13 +675,9 @@ __device__ __forceinline__ void fold_block(const DecayFoldArgs& a, const DecayFo
   const uint32_t tX = sm.tmem;
   tc::Wait w;
   const float wd = log_decay(a.decay, j);
-  // The third terms of chunk i's rows (2^-17 of their size) are for the final state
-  // alone, and only where the chunk has a weight of 2^-8 or more in it: beyond that
-  // they are below the fp32 rounding of sums of newer rows as large.
-  auto third = [&](int i) {
-    const int newer = R.rev ? chunk_of(i) * CH : max(q.len - (chunk_of(i) + 1) * CH, 0);
-    return R.last && wd * (float)newer > -5.55f;
-  };
+  // The rows' third terms (2^-17 of their size) are for the final state alone.  All of its
+  // chunks have them: an old one's may be all that is left in it, where newer rows are zero.
+  const bool third = R.last;
   if (warp == 9) {
     if (lane == 0) {
       for (int t = FOLD_SLOTS; t < nt && w.ok; ++t) {
@@ -708,7 +704,7 @@ __device__ __forceinline__ void fold_block(const DecayFoldArgs& a, const DecayFo
         const uint32_t t0 = tX + 128 * (i & 1), t1 = tX + 256 + 128 * (i & 1);
         tc::gemm_rows_by<64, 128>(lead, t0, smem_u32(sm.slot[tb % FOLD_SLOTS]) + 8192 * h, c, i > 1 || h > 0);
         tc::gemm_rows_by<64, 128>(lead, t1, smem_u32(sm.rest[0]) + 8192 * h, c, i > 1 || h > 0);
-        if (third(i)) tc::gemm_rows_by<64, 128>(lead, t1, smem_u32(sm.rest[1]) + 8192 * h, c, true);
+        if (third) tc::gemm_rows_by<64, 128>(lead, t1, smem_u32(sm.rest[1]) + 8192 * h, c, true);
         if (h == 1) {
           if (tb + FOLD_SLOTS < 2 * nc) tc::commit_by(lead, &sm.empty[tb % FOLD_SLOTS]);
           if (tcc + FOLD_SLOTS < 2 * nc) tc::commit_by(lead, &sm.empty[tcc % FOLD_SLOTS]);
@@ -729,7 +725,7 @@ __device__ __forceinline__ void fold_block(const DecayFoldArgs& a, const DecayFo
         const float e = expf(wd * (float)(R.rev ? t0 - cb * CH + 1 : max(end - 1 - t0, 0)));
         if (i > 0) w.warp_on(&sm.barM[h], i - 1);  // (these rows' further terms have been read)
         unsigned char* b = sm.slot[tb % FOLD_SLOTS];
-        if (third(i))
+        if (third)
           scale_row<3, 4, CH>(b, b, sm.rest[0], r, j0, e, r < n);
         else
           scale_row<2, 4, CH>(b, b, sm.rest[0], r, j0, e, r < n);
