@@ -365,6 +365,8 @@ int gdn_decay_step(const void* q, const void* k, const void* v, const float* dec
  * sequences of total / n_seqs rows.  max_seqlen: the longest sequence's length
  * or an upper bound of it; it sizes the split of long sequences over the SMs
  * (a value that is too small costs speed, not correctness).
+ * Outputs must not overlap inputs, with one exception: hT may be h0 (and dh0 may
+ * be dhT), the states then being replaced.  States that overlap otherwise are refused.
  * Backward: the forward's inputs, the output cotangent dO [total, Hv, d_v]
  * (bf16, contiguous) and dhT (fp32, NULL = zero); writes dq, dk [total, Hk, d_k]
  * (bf16, summed over the value heads of each key head), dv [total, Hv, d_v]

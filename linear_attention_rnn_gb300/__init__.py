@@ -509,7 +509,8 @@ def decay_fwd(q, k, v, decay, h0=None, *, cu_seqlens=None, max_seqlen=None, want
     <= 0): S_t = exp(decay) S_{t-1} + k_t v_t^T, o_t = S_t^T q_t.  q, k, v are
     [B, T, H, 128], or with cu_seqlens (int32, on the device) packed sequences
     [total, H, 128]; max_seqlen then bounds the longest one (it only steers how
-    the work is split).  h0 [n, Hv, 128, 128].  Returns (o, hT)."""
+    the work is split).  h0 [n, Hv, 128, 128].  hT may be h0 itself, the states then
+    being replaced; otherwise outputs must not overlap inputs.  Returns (o, hT)."""
     n, total, longest, Hk, Hv, dk, dv, strides = _decay_dims(q, k, v, decay, cu_seqlens, max_seqlen)
     dev = q.device
     _check(h0, "h0", torch.float32, (n, Hv, dk, dv))

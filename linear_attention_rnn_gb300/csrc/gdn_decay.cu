@@ -637,7 +637,7 @@ __device__ __forceinline__ void fold_block(const DecayFoldArgs& a, const DecayFo
 #pragma unroll 4
       for (int i = 4 * tid; i < HD * HD; i += 4 * (int)blockDim.x)
         *reinterpret_cast<float4*>(R.last + sh * HD * HD + i) =
-            R.x0 ? __ldg(reinterpret_cast<const float4*>(R.x0 + sh * HD * HD + i)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            R.x0 ? *reinterpret_cast<const float4*>(R.x0 + sh * HD * HD + i) : make_float4(0.f, 0.f, 0.f, 0.f);
     return;
   }
   // the segment that the walk ends with matters only for the final state
@@ -765,6 +765,7 @@ __device__ __forceinline__ void fold_block(const DecayFoldArgs& a, const DecayFo
     if (a.nseg == 1) {
       asm volatile("bar.sync 1, 256;" ::: "memory");
       const float keep = expf(wd * (float)q.len);
+      // (both may be one state: an element is read and written by the same thread)
       const float* x0 = R.x0 ? R.x0 + sh * HD * HD + 4 * lane : nullptr;
       float* out = R.last + sh * HD * HD + 4 * lane;
 #pragma unroll 1
@@ -772,7 +773,7 @@ __device__ __forceinline__ void fold_block(const DecayFoldArgs& a, const DecayFo
         float4 x[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          x[k] = x0 ? __ldg(reinterpret_cast<const float4*>(x0 + (r0 + 8 * k) * HD)) : make_float4(0.f, 0.f, 0.f, 0.f);
+          x[k] = x0 ? *reinterpret_cast<const float4*>(x0 + (r0 + 8 * k) * HD) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const float4 o = *place(r0 + 8 * k, lane);
@@ -796,7 +797,7 @@ __global__ void __launch_bounds__(FOLD_THREADS, 1) k_decay_fold(const __grid_con
   if (!a.beside) {
     pdl_wait();
     pdl_release();
-    if (blockIdx.y == 0) clear_status(a.status);
+    if (blockIdx.y == 0 && !a.behind) clear_status(a.status);  // (its call's first kernel)
   }
   fold_block(a, a.role[blockIdx.y], *reinterpret_cast<FoldSmem*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u)),
              blockIdx.x / a.Hv, blockIdx.x % a.Hv);

@@ -195,6 +195,7 @@ struct DecayFoldArgs {
   int nseg, seg_chunks;  // most segments of a sequence, chunks to a segment
   int slots;             // segment slots: n_seqs with nseg = 1, else total / (128 seg_chunks) + n_seqs
   int beside;            // the launch before it is the call's walk, which it need not wait for
+  int behind;            // the launch before it is the call's walk, which reads the states that it writes
 };
 
 // Causal softmax attention over packed sequences (gdn_attn_fwd.cu, gdn_attn_bwd.cu).

@@ -113,6 +113,13 @@ bool one_launch(const DecayArgs& a) {
   return a.seg_chunks <= 6 && (long)(a.n_roles + 1) * a.slots * a.Hv <= sm_count();
 }
 
+// Whether two states' buffers of `bytes` share any of them.
+inline bool overlap(const void* a, const void* b, size_t bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && (x < y ? y - x : x - y) < bytes;
+}
+inline size_t state_bytes(int n_seqs, int Hv) { return (size_t)n_seqs * Hv * HD * HD * sizeof(float); }
+
 DecayFoldArgs fold_args(const DecayArgs& a) {
   DecayFoldArgs f;
   memset(&f, 0, sizeof f);
@@ -307,8 +314,8 @@ size_t gdn_decay_workspace_bytes(int backward, int n_seqs, int total, int max_se
 
 // No rows at all: every sequence ends in the state that it began with.
 static int pass_state(const float* x0, float* xT, int n_seqs, int Hv, cudaStream_t s) {
-  if (!xT) return GDN_OK;
-  const size_t bytes = (size_t)n_seqs * Hv * HD * HD * sizeof(float);
+  if (!xT || xT == x0) return GDN_OK;
+  const size_t bytes = state_bytes(n_seqs, Hv);
   return cuda_status(x0 ? cudaMemcpyAsync(xT, x0, bytes, cudaMemcpyDeviceToDevice, s)
                         : cudaMemsetAsync(xT, 0, bytes, s));
 }
@@ -323,6 +330,7 @@ int gdn_decay_fwd(const void* q, const void* k, const void* v, const float* deca
   for (const void* p : ptrs)
     if (p && !aligned(p, 16)) return GDN_ERR_ARG;
   if (!aligned(decay, 4) || !aligned(cu_seqlens, 4)) return GDN_ERR_ARG;
+  if (hT != h0 && overlap(hT, h0, state_bytes(n_seqs, Hv))) return GDN_ERR_ARG;
   if (n_seqs == 0) return GDN_OK;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (total == 0) return pass_state(h0, hT, n_seqs, Hv, s);
@@ -363,11 +371,15 @@ int gdn_decay_fwd(const void* q, const void* k, const void* v, const float* deca
     if ((rc = cuda_status(launch_decay_fold(f, s)))) return rc;
     r.xseg = f.role[0].x;
   }
-  const int last = p.nseg == 1 && hT;
-  f.n_roles = last && one_launch(a);
+  // The final states, with one segment.  Written over the entering ones they come behind
+  // the walk, which reads those; else beside it.  (With segments the prefix kernel reads
+  // each value before it writes it, and the walk reads the workspace.)
+  const bool last = p.nseg == 1 && hT, in_place = hT && hT == h0;
+  f.n_roles = last && !in_place && one_launch(a);
   if ((rc = cuda_status(launch_decay(a, f, s))) || !last || f.n_roles) return rc;
   f.n_roles = 1;
-  f.beside = 1;
+  f.beside = !in_place;
+  f.behind = in_place;
   return cuda_status(launch_decay_fold(f, s));
 }
 
@@ -381,6 +393,8 @@ int gdn_decay_bwd(const void* q, const void* k, const void* v, const float* deca
   for (const void* p : ptrs)
     if (p && !aligned(p, 16)) return GDN_ERR_ARG;
   if (!aligned(decay, 4) || !aligned(cu_seqlens, 4)) return GDN_ERR_ARG;
+  if (dh0 != dhT && overlap(dh0, dhT, state_bytes(n_seqs, Hv))) return GDN_ERR_ARG;
+  if (overlap(dh0, h0, state_bytes(n_seqs, Hv))) return GDN_ERR_ARG;
   if (n_seqs == 0) return GDN_OK;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (total == 0) return pass_state(dhT, dh0, n_seqs, Hv, s);
@@ -457,17 +471,20 @@ int gdn_decay_bwd(const void* q, const void* k, const void* v, const float* deca
     rq.xseg = ff.x;
     rk.xseg = rv.xseg = fr.x;
   }
-  const int last = p.nseg == 1 && dh0;
+  const bool last = p.nseg == 1 && dh0, in_place = dh0 && dh0 == dhT;  // (as in the forward)
   f.role[0] = fr;
-  f.n_roles = last;
-  if (last && !one_launch(a)) {
+  f.n_roles = last && !in_place;
+  if (f.n_roles && !one_launch(a)) {
     // ahead of the walk: its CTAs are short, and behind the walk's they would start
     // only when the last of those has
     if ((rc = cuda_status(launch_decay_fold(f, s)))) return rc;
     a.beside = 1;
     f.n_roles = 0;
   }
-  return cuda_status(launch_decay(a, f, s));
+  if ((rc = cuda_status(launch_decay(a, f, s))) || !last || !in_place) return rc;
+  f.n_roles = 1;
+  f.behind = 1;
+  return cuda_status(launch_decay_fold(f, s));
 }
 
 size_t gdn_attn_workspace_bytes(int backward, int n_seqs, int total_q, int total_k, int max_k, int Hq, int Hk,
