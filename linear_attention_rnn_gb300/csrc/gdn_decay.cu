@@ -260,6 +260,7 @@ __device__ __forceinline__ bool wait_flag(const int* flag, int value) {
       __nanosleep(100);
     }
   }
+  __syncwarp();  // (lane 0's acquire holds for the other lanes' reads; a shuffle orders none)
   return __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
 }
 

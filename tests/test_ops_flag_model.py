@@ -1,0 +1,54 @@
+"""The flags that pass the decay backward's running sums from one head's CTA to the next, on the CPU.
+
+The operations that a warp makes around a flag are read from the kernel's source and run in a
+model of what the memory model promises: a lane knows of another CTA's writes through its own
+acquire, or through a barrier with a lane that knows of them; a shuffle passes a value on and
+orders nothing.
+"""
+import os
+import re
+
+SOURCE = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "linear_attention_rnn_gb300", "csrc",
+                      "gdn_decay.cu")
+
+
+def body(name):
+    """The text between the braces of function `name`."""
+    with open(SOURCE) as f:
+        s = f.read()
+    at = s.index("{", re.search(r"\b%s\(" % name, s).end())
+    depth, i = 0, at
+    while True:
+        depth += {"{": 1, "}": -1}.get(s[i], 0)
+        if depth == 0:
+            return s[at:i + 1]
+        i += 1
+
+
+# ---- order ----------------------------------------------------------------------------------
+
+def operations(text):
+    """Acquires, barriers and shuffles in the order of the text."""
+    return re.findall(r"ld\.acquire|__syncwarp|__shfl_sync", text)
+
+
+def knowing_lanes(ops):
+    """Lanes that know, behind `ops`, of what the flag's writer wrote before it (lane 0 alone acquires)."""
+    knows = [False] * 32
+    for op in ops:
+        if op == "ld.acquire":
+            knows[0] = True
+        elif op == "__syncwarp":
+            knows = [any(knows)] * 32
+    return sum(knows)
+
+
+def test_every_lane_may_read_behind_a_flag():
+    ops = operations(body("wait_flag"))
+    assert ops.count("ld.acquire") == 1
+    assert knowing_lanes(ops) == 32
+
+
+def test_a_shuffle_alone_orders_nothing():
+    assert knowing_lanes(["ld.acquire", "__shfl_sync"]) == 1
+    assert knowing_lanes(["__syncwarp", "ld.acquire"]) == 1
