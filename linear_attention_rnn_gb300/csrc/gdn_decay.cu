@@ -245,10 +245,10 @@ __device__ __forceinline__ void first_state(const DecayRole& R, unsigned char* s
 }
 
 // Waits (bounded, by a whole warp) until the flag is `value` or more and what was
-// written before it can be read.
-__device__ __forceinline__ bool wait_flag(const int* flag, int value) {
-  bool ok = true;
-  if ((threadIdx.x & 31) == 0) {
+// written before it can be read.  Where a wait of the warp has given up before (lane 0's
+// `ok` says so), at once, so that a walk without its flags ends within one limit, not one to a chunk.
+__device__ __forceinline__ bool wait_flag(const int* flag, int value, bool ok) {
+  if (ok && (threadIdx.x & 31) == 0) {
     const long long t0 = clock64();
     for (int v = 0;;) {
       asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(flag) : "memory");
@@ -439,7 +439,7 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
           // in the workspace; a flag per chunk says how many heads are in it.
           const bool add = adds && r < n;
           float4* acc = reinterpret_cast<float4*>(R.acc) + ((long)kh * 32 + 16 * half) * a.total + row;
-          if (adds) w.ok = wait_flag(flag_of(c), g) && w.ok;
+          if (adds) w.ok = wait_flag(flag_of(c), g, w.ok) && w.ok;
           float4 p[2][4];  // 32 columns of it are on their way at any time
           auto request = [&](int k) {
             if (add) {

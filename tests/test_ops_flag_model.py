@@ -52,3 +52,26 @@ def test_every_lane_may_read_behind_a_flag():
 def test_a_shuffle_alone_orders_nothing():
     assert knowing_lanes(["ld.acquire", "__shfl_sync"]) == 1
     assert knowing_lanes(["__syncwarp", "ld.acquire"]) == 1
+
+
+# ---- bounds ---------------------------------------------------------------------------------
+
+def waits_on_flags_that_nobody_sets(call, wait, chunks):
+    """How often a warp waits for its whole limit over a walk's chunks: the call passes on whether a wait has
+    given up before, and the wait's loop asks for it first."""
+    guarded = "w.ok" in re.search(r"wait_flag\((.*)\)", call).group(1) and re.search(r"\bif \([^;{]*\bok\b", wait)
+    ok, waits = True, 0
+    for _ in range(chunks):
+        if ok or not guarded:
+            waits += 1
+            ok = False
+    return waits
+
+
+def test_a_walk_waits_for_one_limit_at_most():
+    call = re.search(r"w\.ok = [^;]*wait_flag\([^;]*;", body("walk")).group(0)
+    assert waits_on_flags_that_nobody_sets(call, body("wait_flag"), 512) == 1
+
+
+def test_a_wait_that_does_not_ask_repeats_its_limit():
+    assert waits_on_flags_that_nobody_sets("w.ok = wait_flag(flag, g) && w.ok;", "{ if (lane == 0) loop; }", 512) == 512
