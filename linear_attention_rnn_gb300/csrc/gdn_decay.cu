@@ -818,8 +818,17 @@ __device__ __forceinline__ void decay_block(const DecayArgs& a, const DecayFoldA
     clear_status(a.status);
   }
   // This CTA's sequence (or segment), pass and head: the longest sequences' CTAs of all
-  // passes come first, a group's heads side by side in the order of their sum.
-  const int hd = blockIdx.x % a.Hv, u = blockIdx.x / a.Hv, kinds = a.n_roles + (FOLD ? f->n_roles : 0);
+  // passes come first, a group's heads side by side in the order of their sum.  Where a CTA
+  // waits for the head before its own, places are handed out in the order of starts: that
+  // head's CTA is then running or done, whatever order the CTAs of a grid start in.
+  int place = (int)blockIdx.x;
+  if constexpr (SUM) {
+    __shared__ int started;
+    if (threadIdx.x == 0) started = atomicAdd(a.ticket, 1);
+    __syncthreads();
+    place = started;
+  }
+  const int hd = place % a.Hv, u = place / a.Hv, kinds = a.n_roles + (FOLD ? f->n_roles : 0);
   const int ri = u % kinds, slot = u / kinds;
   if constexpr (FOLD) {
     if (ri >= a.n_roles) {

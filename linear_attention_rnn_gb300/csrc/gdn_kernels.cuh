@@ -178,6 +178,7 @@ struct DecayArgs {
   int nseg, seg_chunks;  // most segments of a sequence, chunks to a segment
   int slots;             // segment slots: n_seqs with nseg = 1, else total / (128 seg_chunks) + n_seqs
   int beside;            // the launch before it is the call's fold, which it need not wait for
+  int* ticket;           // CTAs started so far, zero at the start (sums over value heads; else null)
 };
 struct DecayFoldRole {
   CUtensorMap b, c;    // b: shared heads, c: value heads

@@ -98,7 +98,7 @@ DecayPlan decay_plan(int backward, int n_seqs, int total, int max_seqlen, int Hk
     p.accq = take(acc);
     p.acck = take(acc);
     p.flag_bytes = Hv > Hk ? (size_t)Hk * (total / CH + n_seqs) * sizeof(int) : 0;  // of dq or dk
-    p.flags = take(2 * p.flag_bytes);
+    p.flags = take(2 * p.flag_bytes + (p.flag_bytes ? sizeof(int) : 0));  // and the count of started CTAs
   }
   p.total = off;
   return p;
@@ -430,7 +430,8 @@ int gdn_decay_bwd(const void* q, const void* k, const void* v, const float* deca
   if (Hv > Hk) {
     rq.acc = at<float>(ws, p.accq);
     rq.flags = at<int>(ws, p.flags);
-    if ((rc = cuda_status(cudaMemsetAsync(rq.flags, 0, 2 * p.flag_bytes, s)))) return rc;
+    a.ticket = rq.flags + 2 * p.flag_bytes / sizeof(int);
+    if ((rc = cuda_status(cudaMemsetAsync(rq.flags, 0, 2 * p.flag_bytes + sizeof(int), s)))) return rc;
   }
   rq.out = static_cast<bf16*>(dq);
   rk.a = mv, rk.b = md, rk.c = mq;

@@ -6,6 +6,7 @@ acquire, or through a barrier with a lane that knows of them; a shuffle passes a
 orders nothing.
 """
 import os
+import random
 import re
 
 SOURCE = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "linear_attention_rnn_gb300", "csrc",
@@ -75,3 +76,48 @@ def test_a_walk_waits_for_one_limit_at_most():
 
 def test_a_wait_that_does_not_ask_repeats_its_limit():
     assert waits_on_flags_that_nobody_sets("w.ok = wait_flag(flag, g) && w.ok;", "{ if (lane == 0) loop; }", 512) == 512
+
+
+# ---- places -----------------------------------------------------------------------------------
+
+def run_cta_order(order, places_by, sms, group, chunks=3):
+    """CTAs start in `order`, one to an SM, and stay until they are done; the CTA at a place waits, chunk by chunk, for
+    the place before it of its group.  places_by: "index" (a CTA's own) or "counter" (the next one when it starts).
+    True if all of them end."""
+    waiting, counter, running, done = list(order), 0, {}, {}
+    while True:
+        while waiting and len(running) < sms:
+            cta = waiting.pop(0)
+            place = cta if places_by == "index" else counter
+            counter += 1
+            running[place] = 0
+        if not running:
+            return not waiting
+        before = dict(running)
+        for place, c in before.items():
+            ahead = done.get(place - 1, running.get(place - 1, 0))
+            if place % group == 0 or ahead > c:
+                running[place] = c + 1
+        for place in [p for p, c in running.items() if c == chunks]:
+            done[place] = running.pop(place)
+        if running == before:
+            return False
+
+
+def places_of_the_kernel():
+    text = body("decay_block")
+    place = re.search(r"const int hd = (\w+(?:\.\w+)?) % a\.Hv", text).group(1)
+    return "index" if place == "blockIdx.x" else "counter" if re.search(r"atomicAdd\(a\.ticket, 1\)", text) else None
+
+
+def test_sums_pass_on_in_any_order_of_starts():
+    rnd = random.Random(1)
+    for _ in range(200):
+        n, group = 24, rnd.choice([2, 3, 4, 8])
+        order = rnd.sample(range(n), n)
+        assert run_cta_order(order, places_of_the_kernel(), rnd.choice([1, 2, 5, 16]), group)
+
+
+def test_places_by_index_need_starts_in_order():
+    assert run_cta_order(range(24), "index", 2, 4)
+    assert not run_cta_order(reversed(range(24)), "index", 2, 4)
