@@ -33,6 +33,7 @@ STATUS = {0: "GDN_OK", -1: "GDN_ERR_ARG", -2: "GDN_ERR_SHAPE", -3: "GDN_ERR_WORK
           -4: "GDN_ERR_CUDA", -5: "GDN_ERR_TIMEOUT", -6: "GDN_ERR_UNSUPPORTED"}
 
 _lib = None
+_several_devices = True  # whether operands can be on different ones; lib() finds out
 
 
 class GDNError(RuntimeError):
@@ -58,7 +59,7 @@ def header_functions():
 
 
 def lib():
-    global _lib
+    global _lib, _several_devices
     if _lib is None:
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(
@@ -124,6 +125,7 @@ def lib():
         L.gdn_attn_bwd.restype = I
         L.gdn_selftest_wait_timeout.argtypes = [ctypes.c_longlong, P, P]
         L.gdn_selftest_wait_timeout.restype = I
+        _several_devices = torch.cuda.device_count() > 1
         _lib = L
     return _lib
 
@@ -411,6 +413,26 @@ def _check_rows(t, name, H, d, n=None):
     return stride
 
 
+def _check_devices(q, *operands):
+    """All operands on q's device, which is the current one (a kernel is launched there).
+    For machines with several devices; with one it would only take time."""
+    for t in operands:
+        if t is not None and t.device != q.device:
+            raise ValueError(f"operands are on {q.device} and {t.device}")
+    if torch.cuda.current_device() != q.device.index:
+        raise ValueError(f"operands are on {q.device}, which is not the current device")
+
+
+def _current_device() -> int:
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -1
+
+
+@functools.lru_cache(maxsize=256)
+def _planned_bytes(name, device, *sizes) -> int:
+    """A workspace's size by the library's plan, which counts the current device's SMs."""
+    return int(getattr(lib(), name)(*sizes))
+
+
 _STATUS_BYTES = 256  # a workspace that holds the status word alone may be left out
 
 
@@ -420,6 +442,8 @@ def _scratch(nbytes, device, ws):
         if nbytes <= _STATUS_BYTES:
             return None, 0, None
         ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    elif not (ws.is_cuda and ws.is_contiguous()):
+        raise ValueError("workspace must be a contiguous CUDA tensor")
     elif ws.numel() * ws.element_size() < nbytes:
         raise ValueError("workspace too small")
     return ws.data_ptr(), ws.numel() * ws.element_size(), ws
@@ -439,15 +463,16 @@ def _step(name, q, k, v, gates, state, slots, o):
     _check(state, "state", torch.float32, (n, Hv, dk, dv))
     if slots is not None:
         _check(slots, "slots", torch.int32, (R,))
-        slots = slots.data_ptr()
     elif n < R:
         raise ValueError(f"{R} rows need as many states, got {n}")
     if o is None:
         o = torch.empty_like(v, memory_format=torch.contiguous_format)
     else:
         _check(o, "o", torch.bfloat16, (R, Hv, dv))
-    rc = name(q.data_ptr(), k.data_ptr(), v.data_ptr(), *gates, state.data_ptr(), slots,
-              o.data_ptr(), R, n, Hk, Hv, dk, dv, sq, sk, sv,
+    if _several_devices:
+        _check_devices(q, k, v, state, slots, o)
+    rc = name(q.data_ptr(), k.data_ptr(), v.data_ptr(), *gates,
+              state.data_ptr(), _ptr(slots), o.data_ptr(), R, n, Hk, Hv, dk, dv, sq, sk, sv,
               torch._C._cuda_getCurrentRawStream(q.device.index))
     if rc != GDN_OK:
         raise GDNError(rc, name.__name__)
@@ -462,6 +487,8 @@ def delta_step(q, k, v, g, beta, state, slots=None, *, o=None) -> torch.Tensor:
     rows = v.shape[:2]
     _check(g, "g", torch.float32, rows)
     _check(beta, "beta", torch.float32, rows)
+    if _several_devices:
+        _check_devices(q, g, beta)
     return _step(lib().gdn_delta_step, q, k, v, (g.data_ptr(), beta.data_ptr()), state, slots, o)
 
 
@@ -469,13 +496,14 @@ def decay_step(q, k, v, decay, state, slots=None, *, o=None) -> torch.Tensor:
     """One token per row of linear attention with a decay for each head (decay
     [Hv], the log-decays); otherwise as delta_step."""
     _check(decay, "decay", torch.float32, v.shape[1:2])
+    if _several_devices:
+        _check_devices(q, decay)
     return _step(lib().gdn_decay_step, q, k, v, (decay.data_ptr(),), state, slots, o)
 
 
-@functools.lru_cache(maxsize=256)
 def decay_workspace_bytes(backward, n_seqs, total, max_seqlen, Hk, Hv, dk=128, dv=128) -> int:
-    return int(lib().gdn_decay_workspace_bytes(int(backward), n_seqs, total, max_seqlen, Hk, Hv, dk,
-                                               dv))
+    return _planned_bytes("gdn_decay_workspace_bytes", _current_device(), int(backward), n_seqs,
+                          total, max_seqlen, Hk, Hv, dk, dv)
 
 
 def _decay_dims(q, k, v, decay, cu_seqlens, max_seqlen):
@@ -522,8 +550,10 @@ def decay_fwd(q, k, v, decay, h0=None, *, cu_seqlens=None, max_seqlen=None, want
         _check(hT, "hT", torch.float32, (n, Hv, dk, dv))
     elif want_hT:
         hT = torch.empty((n, Hv, dk, dv), dtype=torch.float32, device=dev)
-    wp, wn, ws = _scratch(decay_workspace_bytes(0, n, total, longest, Hk, Hv, dk, dv), dev,
-                          workspace)  # (ws: kept alive over the call)
+    if _several_devices:
+        _check_devices(q, k, v, decay, h0, cu_seqlens, o, hT, workspace)
+    wp, wn, ws = _scratch(_planned_bytes("gdn_decay_workspace_bytes", dev.index, 0, n, total, longest,
+                                         Hk, Hv, dk, dv), dev, workspace)  # (ws: kept alive over the call)
     rc = lib().gdn_decay_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(h0), _ptr(cu_seqlens),
                              _ptr(o), _ptr(hT), n, total, longest, Hk, Hv, dk, dv, *strides,
                              wp, wn, _stream(dev))
@@ -545,8 +575,10 @@ def decay_bwd(q, k, v, decay, h0, dO, dhT=None, *, cu_seqlens=None, max_seqlen=N
     dk_ = torch.empty(k.shape, dtype=torch.bfloat16, device=dev)
     dv_ = torch.empty(v.shape, dtype=torch.bfloat16, device=dev)
     dh0 = torch.empty((n, Hv, dk, dv), dtype=torch.float32, device=dev) if want_dh0 else None
-    wp, wn, ws = _scratch(decay_workspace_bytes(1, n, total, longest, Hk, Hv, dk, dv), dev,
-                          workspace)  # (ws: kept alive over the call)
+    if _several_devices:
+        _check_devices(q, k, v, decay, h0, dO, dhT, cu_seqlens, workspace)
+    wp, wn, ws = _scratch(_planned_bytes("gdn_decay_workspace_bytes", dev.index, 1, n, total, longest,
+                                         Hk, Hv, dk, dv), dev, workspace)  # (ws: kept alive over the call)
     rc = lib().gdn_decay_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(h0), _ptr(dO), _ptr(dhT),
                              _ptr(cu_seqlens), _ptr(dq), _ptr(dk_), _ptr(dv_), _ptr(dh0), n, total,
                              longest, Hk, Hv, dk, dv, *strides, wp, wn, _stream(dev))
@@ -555,10 +587,9 @@ def decay_bwd(q, k, v, decay, h0, dO, dhT=None, *, cu_seqlens=None, max_seqlen=N
     return dq, dk_, dv_, dh0
 
 
-@functools.lru_cache(maxsize=256)
 def attn_workspace_bytes(backward, n_seqs, total_q, total_k, max_k, Hq, Hk, d=128) -> int:
-    return int(lib().gdn_attn_workspace_bytes(int(backward), n_seqs, total_q, total_k, max_k, Hq, Hk,
-                                              d))
+    return _planned_bytes("gdn_attn_workspace_bytes", _current_device(), int(backward), n_seqs,
+                          total_q, total_k, max_k, Hq, Hk, d)
 
 
 def _attn_dims(q, k, v, cu_q, cu_k, scale):
@@ -609,8 +640,10 @@ def attn_fwd(q, k, v, *, cu_q=None, cu_k=None, k_len=None, max_q=None, max_k=Non
         _check(lse, "lse", torch.float32, q.shape[:-1])
     elif want_lse:
         lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
-    wp, wn, ws = _scratch(attn_workspace_bytes(0, n, total_q, total_k, longest, Hq, Hk, d), dev,
-                          workspace)  # (ws: kept alive over the call)
+    if _several_devices:
+        _check_devices(q, k, v, cu_q, cu_k, k_len, o, lse, workspace)
+    wp, wn, ws = _scratch(_planned_bytes("gdn_attn_workspace_bytes", dev.index, 0, n, total_q, total_k,
+                                         longest, Hq, Hk, d), dev, workspace)  # (ws: kept alive over the call)
     rc = lib().gdn_attn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_q), _ptr(cu_k), _ptr(k_len), _ptr(o),
                             _ptr(lse), n, total_q, total_k, longest, Hq, Hk, d, scale, *strides,
                             wp, wn, _stream(dev))
@@ -631,8 +664,10 @@ def attn_bwd(q, k, v, o, lse, dO, *, cu_q=None, cu_k=None, max_q=None, max_k=Non
     dq = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
     dk = torch.empty(k.shape, dtype=torch.bfloat16, device=dev)
     dv = torch.empty(v.shape, dtype=torch.bfloat16, device=dev)
-    wp, wn, ws = _scratch(attn_workspace_bytes(1, n, total_q, total_k, 0, Hq, Hk, d), dev,
-                          workspace)  # (ws: kept alive over the call)
+    if _several_devices:
+        _check_devices(q, k, v, o, lse, dO, cu_q, cu_k, workspace)
+    wp, wn, ws = _scratch(_planned_bytes("gdn_attn_workspace_bytes", dev.index, 1, n, total_q, total_k, 0,
+                                         Hq, Hk, d), dev, workspace)  # (ws: kept alive over the call)
     rc = lib().gdn_attn_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dO), _ptr(cu_q),
                             _ptr(cu_k), _ptr(dq), _ptr(dk), _ptr(dv), n, total_q, total_k, Hq, Hk, d,
                             scale, *strides, wp, wn, _stream(dev))
