@@ -217,12 +217,12 @@ __device__ __forceinline__ void dkv(const AttnArgs& a, unsigned char* raw, int b
       };
       auto scores = [&](int i) {
         arrived(2 * i);
-        tc::gemm128_by<false, false>(lead, tS, smem_u32(sm.k), slot(2 * i), false);
+        tc::gemm128_by<false>(lead, tS, smem_u32(sm.k), slot(2 * i), false);
         tc::commit_by(lead, &sm.barS);
       };
       auto dscores = [&](int i) {
         arrived(2 * i + 1);
-        tc::gemm128_by<false, false>(lead, tP, smem_u32(sm.v), slot(2 * i + 1), false);
+        tc::gemm128_by<false>(lead, tP, smem_u32(sm.v), slot(2 * i + 1), false);
         tc::commit_by(lead, &sm.barD);
       };
       w.warp_on(&sm.barKV, 0);
@@ -231,11 +231,11 @@ __device__ __forceinline__ void dkv(const AttnArgs& a, unsigned char* raw, int b
       for (int i = 0; i < n; ++i) {
         w.warp_on(&sm.barP, i);
         tc::fence_after();
-        tc::gemm_ts_by<true>(lead, tV, tS, slot(2 * i + 1), i > 0);  // dV += P^T dO
+        tc::gemm_ts_by(lead, tV, tS, slot(2 * i + 1), i > 0);  // dV += P^T dO
         if (i + 1 < n) scores(i + 1);
         w.warp_on(&sm.barDs, i);
         tc::fence_after();
-        tc::gemm_ts_by<true>(lead, tK, tP, slot(2 * i), i > 0);      // dK += dS^T Q
+        tc::gemm_ts_by(lead, tK, tP, slot(2 * i), i > 0);      // dK += dS^T Q
         release(2 * i);
         release(2 * i + 1);
         if (i + 1 < n) dscores(i + 1);
@@ -458,12 +458,12 @@ __device__ __forceinline__ void dq(const AttnArgs& a, unsigned char* raw, int bl
       };
       auto scores = [&](int i) {
         arrived(2 * i);
-        tc::gemm128_by<false, false>(lead, tS + 128 * (i & 1), smem_u32(sm.q), slot(2 * i), false);
+        tc::gemm128_by<false>(lead, tS + 128 * (i & 1), smem_u32(sm.q), slot(2 * i), false);
         tc::commit_by(lead, &sm.barS[i & 1]);
       };
       auto dscores = [&](int i) {
         arrived(2 * i + 1);
-        tc::gemm128_by<false, false>(lead, tP, smem_u32(sm.dO), slot(2 * i + 1), false);
+        tc::gemm128_by<false>(lead, tP, smem_u32(sm.dO), slot(2 * i + 1), false);
         release(2 * i + 1);
         tc::commit_by(lead, &sm.barD);
       };
@@ -474,7 +474,7 @@ __device__ __forceinline__ void dq(const AttnArgs& a, unsigned char* raw, int bl
         if (i + 1 < n) scores(i + 1);  // (its buffer's last S was read before dS i - 1 was signalled)
         w.warp_on(&sm.barDs, i);
         tc::fence_after();
-        tc::gemm_ts_by<true>(lead, tQ, tP, slot(2 * i), i > 0);  // dQ += dS K
+        tc::gemm_ts_by(lead, tQ, tP, slot(2 * i), i > 0);  // dQ += dS K
         release(2 * i);
         if (i + 1 < n) dscores(i + 1);
       }

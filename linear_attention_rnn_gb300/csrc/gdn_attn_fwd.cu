@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) k_attn_fwd(const __grid_consta
         if (t + NSLOT < nt) tc::commit_by(lead, &sm.empty[t % NSLOT]);
       };
       auto scores = [&](int x, int q, int i) {  // S of group x = Q K^T of key tile i
-        tc::gemm128_by<false, false>(lead, tS + 128 * x, smem_u32(sm.q[q]), slot(2 * i), false);
+        tc::gemm128_by<false>(lead, tS + 128 * x, smem_u32(sm.q[q]), slot(2 * i), false);
         tc::commit_by(lead, &sm.barS[x]);
       };
       // O of group x += P V of key tile i, the group's j-th; P arrives by halves

@@ -121,24 +121,22 @@ __device__ __forceinline__ int2 find_segment(const int* cu, int n_seqs, int T, i
 __device__ __forceinline__ int seg_index(int r, int c) { return ((c >> 2) * HD + r) * 4 + (c & 3); }
 
 // Row r of an SW128 tile scaled by f and split into TERMS bf16 terms, 16-byte chunks
-// j .. j + NJ - 1.  Term 0 goes to `first` and the others to the tiles at `rest`,
-// row r % ROWS of tiles with ROWS rows (`first` = the tile itself, 128 rows: in
-// place).  The leading terms are the value's upper 16 bits as they stand (the
+// j .. j + 3: term 0 in place, the others to the same place of the tiles at `rest`.
+// The leading terms are the value's upper 16 bits as they stand (the
 // remainder is then exact), the last one is rounded: 8 bits more of the fp32
 // product per term, at a permute, two ands and half a multiply-add per pair.  A
 // row that is not `valid` (past the sequence's end) becomes zero, whatever it holds.
-template <int TERMS, int NJ, int ROWS>
-__device__ __forceinline__ void scale_row(const unsigned char* tile, unsigned char* first, unsigned char* rest, int r,
-                                          int j, float f, bool valid) {
-  uint4 u[NJ];  // all loads in flight at once
+template <int TERMS>
+__device__ __forceinline__ void scale_row(unsigned char* tile, unsigned char* rest, int r, int j, float f, bool valid) {
+  uint4 u[4];  // all loads in flight at once
 #pragma unroll
-  for (int c = 0; c < NJ; ++c) u[c] = *reinterpret_cast<const uint4*>(tile + tc::sw128_chunk(r, j + c, CH));
+  for (int c = 0; c < 4; ++c) u[c] = *reinterpret_cast<const uint4*>(tile + tc::sw128_chunk(r, j + c, CH));
   if (!valid) {
 #pragma unroll
-    for (int c = 0; c < NJ; ++c) u[c] = make_uint4(0u, 0u, 0u, 0u);
+    for (int c = 0; c < 4; ++c) u[c] = make_uint4(0u, 0u, 0u, 0u);
   }
 #pragma unroll
-  for (int c = 0; c < NJ; ++c) {
+  for (int c = 0; c < 4; ++c) {
     const uint32_t up[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
     uint32_t o[TERMS][4];
 #pragma unroll
@@ -156,10 +154,10 @@ __device__ __forceinline__ void scale_row(const unsigned char* tile, unsigned ch
       }
       o[TERMS - 1][i] = pack_bf16(x, y);
     }
-    const uint32_t at = tc::sw128_chunk(r & (ROWS - 1), j + c, ROWS);
+    const uint32_t at = tc::sw128_chunk(r, j + c, CH);
 #pragma unroll
     for (int t = 0; t < TERMS; ++t)
-      *reinterpret_cast<uint4*>((t == 0 ? first : rest + (t - 1) * ROWS * 256) + at) =
+      *reinterpret_cast<uint4*>((t == 0 ? tile : rest + (t - 1) * TILE) + at) =
           make_uint4(o[t][0], o[t][1], o[t][2], o[t][3]);
   }
 }
@@ -217,19 +215,16 @@ __device__ __forceinline__ void first_state(const DecayRole& R, unsigned char* s
     // columns c, c + 64 of the pass (c = 0 .. 31, or 32 .. 63): 128 rows x 2 x 128 bytes
     const int t = threadIdx.x & 255, cc = c0 & 63;
     asm volatile("bar.sync 2, 256;" ::: "memory");  // (the pass before has been read)
-#pragma unroll 1
-    for (int k = 0; k < 8; k += 8) {
-      float4 f[8];
+    float4 f[8];
 #pragma unroll
-      for (int l = 0; l < 8; ++l) {
-        const int i = t + 256 * (k + l), row = i >> 4, p = i & 15;  // 16-byte piece p of the row's two
-        f[l] = *reinterpret_cast<const float4*>(x0 + row * HD + (p >> 3) * 64 + cc + 4 * (p & 7));
-      }
+    for (int l = 0; l < 8; ++l) {
+      const int i = t + 256 * l, row = i >> 4, p = i & 15;  // 16-byte piece p of the row's two
+      f[l] = *reinterpret_cast<const float4*>(x0 + row * HD + (p >> 3) * 64 + cc + 4 * (p & 7));
+    }
 #pragma unroll
-      for (int l = 0; l < 8; ++l) {
-        const int i = t + 256 * (k + l), row = i >> 4, p = i & 15;
-        *reinterpret_cast<float4*>(stage + row * 256 + ((p ^ (row & 7)) << 4)) = f[l];
-      }
+    for (int l = 0; l < 8; ++l) {
+      const int i = t + 256 * l, row = i >> 4, p = i & 15;
+      *reinterpret_cast<float4*>(stage + row * 256 + ((p ^ (row & 7)) << 4)) = f[l];
     }
     asm volatile("bar.sync 2, 256;" ::: "memory");
 #pragma unroll
@@ -364,7 +359,7 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
     auto scores = [&](int it) {  // P = A B^T
       arrived(3 * it);
       arrived(3 * it + 1);
-      tc::gemm128_by<false, false>(lead, tP, slot(3 * it), slot(3 * it + 1), false);
+      tc::gemm128_by<false>(lead, tP, slot(3 * it), slot(3 * it + 1), false);
       tc::commit_by(lead, &sm.barP);
     };
     scores(0);
@@ -373,7 +368,7 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
       w.warp_on(&sm.barS, it);
       if (it > 0) w.warp_on(&sm.barOf, it - 1);
       tc::fence_after();
-      tc::gemm128_by<false, true>(lead, tO1, slot(ta), smem_u32(sm.X), false);  // A X
+      tc::gemm128_by<true>(lead, tO1, slot(ta), smem_u32(sm.X), false);  // A X
       release(ta);
       arrived(tcc);
 #pragma unroll
@@ -381,14 +376,14 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
         w.warp_on(&sm.barK[h], it);
         tc::fence_after();
         const uint32_t c = slot(tcc) + 8192 * h;
-        tc::gemm_rows_by<64, 128>(lead, tX, slot(tb) + 8192 * h, c, true);
-        tc::gemm_rows_by<64, 128>(lead, tX, smem_u32(sm.lo) + 8192 * h, c, true);
+        tc::gemm_rows_by<64>(lead, tX, slot(tb) + 8192 * h, c, true);
+        tc::gemm_rows_by<64>(lead, tX, smem_u32(sm.lo) + 8192 * h, c, true);
       }
       tc::commit_by(lead, &sm.barX);
       release(tb);
       w.warp_on(&sm.barPm, it);
       tc::fence_after();
-      tc::gemm_ts_by<true>(lead, tO2, tP, slot(tcc), false);  // P C
+      tc::gemm_ts_by(lead, tO2, tP, slot(tcc), false);  // P C
       tc::commit_by(lead, &sm.barO);
       if (it + 1 < n_it) scores(it + 1);
     }
@@ -598,7 +593,7 @@ __device__ __forceinline__ void walk(const DecayArgs& a, const DecayRole& R, Wal
         for (int h = 0; h < 2; ++h) {  // 64 rows at a time, four threads to a row
           const int i = 64 * h + (tid & 63), j = 4 * ((tid >> 6) & 3);
           const float e = expf(wd * (float)(REV ? i + 1 : max(n - 1 - i, 0)));
-          scale_row<2, 4, CH>(sm.slot[tb % NSLOT], sm.slot[tb % NSLOT], sm.lo, i, j, e, i < n);
+          scale_row<2>(sm.slot[tb % NSLOT], sm.lo, i, j, e, i < n);
           if (i >= n) zero_row(sm.slot[tcc % NSLOT], i, j, 4);
           tc::fence_proxy_async();
           tc::mbar_arrive(&sm.barK[h]);
@@ -703,9 +698,9 @@ __device__ __forceinline__ void fold_block(const DecayFoldArgs& a, const DecayFo
         // The tensor cores' fp32 sums lose a little at every step: the first terms of
         // even and odd chunks and the small further terms have sums of their own.
         const uint32_t t0 = tX + 128 * (i & 1), t1 = tX + 256 + 128 * (i & 1);
-        tc::gemm_rows_by<64, 128>(lead, t0, smem_u32(sm.slot[tb % FOLD_SLOTS]) + 8192 * h, c, i > 1 || h > 0);
-        tc::gemm_rows_by<64, 128>(lead, t1, smem_u32(sm.rest[0]) + 8192 * h, c, i > 1 || h > 0);
-        if (third) tc::gemm_rows_by<64, 128>(lead, t1, smem_u32(sm.rest[1]) + 8192 * h, c, true);
+        tc::gemm_rows_by<64>(lead, t0, smem_u32(sm.slot[tb % FOLD_SLOTS]) + 8192 * h, c, i > 1 || h > 0);
+        tc::gemm_rows_by<64>(lead, t1, smem_u32(sm.rest[0]) + 8192 * h, c, i > 1 || h > 0);
+        if (third) tc::gemm_rows_by<64>(lead, t1, smem_u32(sm.rest[1]) + 8192 * h, c, true);
         if (h == 1) {
           if (tb + FOLD_SLOTS < 2 * nc) tc::commit_by(lead, &sm.empty[tb % FOLD_SLOTS]);
           if (tcc + FOLD_SLOTS < 2 * nc) tc::commit_by(lead, &sm.empty[tcc % FOLD_SLOTS]);
@@ -727,9 +722,9 @@ __device__ __forceinline__ void fold_block(const DecayFoldArgs& a, const DecayFo
         if (i > 0) w.warp_on(&sm.barM[h], i - 1);  // (these rows' further terms have been read)
         unsigned char* b = sm.slot[tb % FOLD_SLOTS];
         if (third)
-          scale_row<3, 4, CH>(b, b, sm.rest[0], r, j0, e, r < n);
+          scale_row<3>(b, sm.rest[0], r, j0, e, r < n);
         else
-          scale_row<2, 4, CH>(b, b, sm.rest[0], r, j0, e, r < n);
+          scale_row<2>(b, sm.rest[0], r, j0, e, r < n);
         if (r >= n) zero_row(sm.slot[tcc % FOLD_SLOTS], r, j0, 4);
         tc::fence_proxy_async();
         tc::mbar_arrive(&sm.barK[h]);

@@ -412,10 +412,6 @@ struct Wait {
   }
 };
 
-// ---- A operand in tensor memory ----------------------------------------------------
-// The [128 x K] bf16 A operand: row m is TMEM lane m, and each 32-bit column
-// holds two consecutive K elements (the lower one in the low half), so a
-// K = 16 step reads 8 columns.
 // ---- products issued by a whole warp ------------------------------------------------
 // The warp runs the issuing code together and one lane (`leader`, the same one
 // throughout) issues: addresses and descriptors are then uniform over the warp,
@@ -452,44 +448,48 @@ __device__ __forceinline__ void commit_by(uint32_t leader, uint64_t* mbar) {
       "r"(leader)
       : "memory");
 }
-// gemm128 by a warp: D[128 x 128] (+)= A B^T of SW128 tiles, each K-major or MN-major
-template <bool A_MN, bool B_MN>
+// gemm128 by a warp: D[128 x 128] (+)= A B^T of SW128 tiles, A K-major, B K-major or MN-major
+template <bool B_MN>
 __device__ __forceinline__ void gemm128_by(uint32_t leader, uint32_t tmem_d, uint32_t a_smem, uint32_t b_smem,
                                            bool accumulate_first) {
-  const uint32_t idesc = idesc_bf16(128, 128) | (A_MN ? (1u << 15) : 0u) | (B_MN ? (1u << 16) : 0u);
-  const uint64_t da0 = A_MN ? desc_sw128_mn(a_smem, 128u * 128u) : desc_sw128(a_smem);
+  const uint32_t idesc = idesc_bf16(128, 128) | (B_MN ? (1u << 16) : 0u);
+  const uint64_t da0 = desc_sw128(a_smem);
   const uint64_t db0 = B_MN ? desc_sw128_mn(b_smem, 128u * 128u) : desc_sw128(b_smem);
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const uint32_t kmaj = (uint32_t)(k >> 2) * 128u * 128u + (uint32_t)(k & 3) * 32u;
-    mma_by(leader, tmem_d, da0 + ((A_MN ? (uint32_t)k * 2048u : kmaj) >> 4),
-           db0 + ((B_MN ? (uint32_t)k * 2048u : kmaj) >> 4), idesc, (k > 0 || accumulate_first) ? 1u : 0u);
+    mma_by(leader, tmem_d, da0 + (kmaj >> 4), db0 + ((B_MN ? (uint32_t)k * 2048u : kmaj) >> 4), idesc,
+           (k > 0 || accumulate_first) ? 1u : 0u);
   }
 }
-// D[128 x 128] (+)= A^T B over K rows: A and B are rows of [rows x 128] tiles, from
-// the row that the addresses point to (a multiple of 8); A's tile has A_ROWS
-// rows, B's 128
-template <int K, int A_ROWS>
+// D[128 x 128] (+)= A^T B over K rows: A and B are rows of [128 x 128] tiles, from
+// the row that the addresses point to (a multiple of 8)
+template <int K>
 __device__ __forceinline__ void gemm_rows_by(uint32_t leader, uint32_t tmem_d, uint32_t a_smem, uint32_t b_smem,
                                              bool accumulate_first) {
   const uint32_t idesc = idesc_bf16(128, 128) | (1u << 15) | (1u << 16);
-  const uint64_t da0 = desc_sw128_mn(a_smem, A_ROWS * 128u), db0 = desc_sw128_mn(b_smem, 128u * 128u);
+  const uint64_t da0 = desc_sw128_mn(a_smem, 128u * 128u), db0 = desc_sw128_mn(b_smem, 128u * 128u);
 #pragma unroll
   for (int k = 0; k < K / 16; ++k)
     mma_by(leader, tmem_d, da0 + (((uint32_t)k * 2048u) >> 4), db0 + (((uint32_t)k * 2048u) >> 4), idesc,
            (k > 0 || accumulate_first) ? 1u : 0u);
 }
+
+// ---- A operand in tensor memory ----------------------------------------------------
+// The [128 x K] bf16 A operand: row m is TMEM lane m, and each 32-bit column
+// holds two consecutive K elements (the lower one in the low half), so a
+// K = 16 step reads 8 columns.
+
 // A bf16 operand in tensor memory (K = 128) times a [128 (K) rows x 128] tile read
-// MN-major, by a warp.  SPLIT: the operand's last 64 K-values begin at column 64,
-// not 32 (each half then lies over the fp32 half that its writers have read).
-template <bool SPLIT>
+// MN-major, by a warp.  The operand's last 64 K-values begin at column 64 (each half
+// lies over the fp32 half that its writers have read).
 __device__ __forceinline__ void gemm_ts_by(uint32_t leader, uint32_t tmem_d, uint32_t tmem_a, uint32_t b_smem,
                                            bool accumulate_first) {
   const uint32_t idesc = idesc_bf16(128, 128) | (1u << 16);
   const uint64_t db0 = desc_sw128_mn(b_smem, 128u * 128u);
 #pragma unroll
   for (int k = 0; k < 8; ++k)
-    mma_ts_by(leader, tmem_d, tmem_a + (SPLIT ? 64u : 32u) * (uint32_t)(k >> 2) + 8u * (uint32_t)(k & 3),
+    mma_ts_by(leader, tmem_d, tmem_a + 64u * (uint32_t)(k >> 2) + 8u * (uint32_t)(k & 3),
               db0 + (((uint32_t)k * 2048u) >> 4), idesc, (k > 0 || accumulate_first) ? 1u : 0u);
 }
 // 32 values as 16 packed bf16 columns of this thread's TMEM lane (complete after wait_st)
