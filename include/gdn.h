@@ -374,7 +374,8 @@ int gdn_decay_step(const void* q, const void* k, const void* v, const float* dec
  * A sequence's results depend on its own rows alone, whatever the rows beside
  * it hold.  ws: at least gdn_decay_workspace_bytes(backward, ...) bytes, whose
  * first word is the status word of the bounded waits (gdn_workspace_status);
- * where that is all (256 bytes), ws may be NULL, and no status is kept.
+ * where that is all (256 bytes), ws may be NULL, and no status is kept.  A call without
+ * rows starts no kernel and leaves that word as it was.
  */
 size_t gdn_decay_workspace_bytes(int backward, int n_seqs, int total, int max_seqlen, int Hk,
                                  int Hv, int d_k, int d_v);
@@ -404,15 +405,16 @@ int gdn_decay_bwd(const void* q, const void* k, const void* v, const float* deca
  * total_q / total_k (NULL: equal lengths).  k_len: int32 [n_seqs] (NULL: all),
  * the used rows of each sequence's keys, for caches of fixed capacity; rows past
  * it may hold anything.  max_k: the longest sequence's keys or an upper bound; it
- * sizes the split of the keys over the SMs (a value that is too small costs
- * speed, not correctness).
+ * sizes the split of the keys over the SMs (a value that is too small, or much too
+ * large, costs speed, not correctness).  Outputs must not overlap inputs.
  * Backward: the forward's inputs (without k_len), o and lse, and the output
  * cotangent dO [total_q, Hq, d] (bf16, contiguous); writes dq [total_q, Hq, d]
  * and dk, dv [total_k, Hk, d] (bf16, summed over the query heads of each key
  * head).  Sums have a fixed order: equal calls give equal results.
  * ws: at least gdn_attn_workspace_bytes(backward, ...) bytes, whose first word is
  * the status word of the bounded waits (gdn_workspace_status); where that is all
- * (256 bytes), ws may be NULL, and no status is kept.
+ * (256 bytes), ws may be NULL, and no status is kept.  A call without queries, and a
+ * backward without keys, starts no kernel and leaves that word as it was.
  */
 size_t gdn_attn_workspace_bytes(int backward, int n_seqs, int total_q, int total_k, int max_k,
                                 int Hq, int Hk, int d);

@@ -427,7 +427,7 @@ def _current_device() -> int:
     return torch.cuda.current_device() if torch.cuda.is_initialized() else -1
 
 
-@functools.lru_cache(maxsize=256)
+@functools.lru_cache(maxsize=512)
 def _planned_bytes(name, device, *sizes) -> int:
     """A workspace's size by the library's plan, which counts the current device's SMs."""
     return int(getattr(lib(), name)(*sizes))
@@ -625,9 +625,11 @@ def attn_fwd(q, k, v, *, cu_q=None, cu_k=None, k_len=None, max_q=None, max_k=Non
     [total_k, Hk, 128] hold packed sequences that start at cu_q and cu_k (int32,
     on the device), or are [B, T, H, 128] without them.  The last query of a
     sequence sees all of its keys, each one before it one key fewer; k_len
-    (int32) gives the used rows of caches with a fixed capacity.  max_q and
-    max_k bound the lengths (they only steer how the work is split).  scale
-    defaults to 1 / sqrt(128).  Returns (o, lse), lse [.., Hq] in fp32."""
+    (int32) gives the used rows of caches with a fixed capacity.  max_k bounds the
+    keys of a sequence and steers how they are split over the SMs (packed keys without
+    it are split as if one sequence had all of them); max_q is accepted beside it and
+    changes nothing.  scale defaults to 1 / sqrt(128).  Returns (o, lse), lse [.., Hq]
+    in fp32."""
     n, total_q, total_k, Hq, Hk, d, scale, strides = _attn_dims(q, k, v, cu_q, cu_k, scale)
     dev = q.device
     _check(k_len, "k_len", torch.int32, (n,))
@@ -655,7 +657,8 @@ def attn_fwd(q, k, v, *, cu_q=None, cu_k=None, k_len=None, max_q=None, max_k=Non
 def attn_bwd(q, k, v, o, lse, dO, *, cu_q=None, cu_k=None, max_q=None, max_k=None, scale=None,
              workspace=None):
     """Backward of attn_fwd (without k_len).  Returns (dq, dk, dv); dk and dv are
-    summed over the query heads that share a key head."""
+    summed over the query heads that share a key head.  max_q and max_k are accepted
+    as there and change nothing."""
     n, total_q, total_k, Hq, Hk, d, scale, strides = _attn_dims(q, k, v, cu_q, cu_k, scale)
     dev = q.device
     _check(o, "o", torch.bfloat16, tuple(q.shape))

@@ -24,9 +24,9 @@
 // (rounding the result alone: 1.7e-3); scores, lse, delta and all sums are fp32.
 //
 // Bound: the tensor rate (7 x 512 cycles per pair of 128 x 128 tiles).  Measured on a
-// GB300, 4096 + 2048 + 1000 + 977 + 71 packed tokens, 16 query and 4 key heads: 230 us,
-// the tensor pipe busy for 0.62 of it; delta 14 us; with the forward 329 us.  Two CTAs
-// for the heaviest key tiles were slower (245 us): the SMs are busy to the end as it is.
+// GB300, 4096 + 2048 + 1000 + 977 + 71 packed tokens, 16 query and 4 key heads: 236 us,
+// the tensor pipe busy for 0.62 of it; delta 15 us; with the forward 334 us.  Two CTAs
+// for the heaviest key tiles were slower (by 15 us): the SMs are busy to the end as it is.
 #include "gdn_attn.cuh"
 
 namespace gdn {

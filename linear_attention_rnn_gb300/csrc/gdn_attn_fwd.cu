@@ -21,11 +21,12 @@
 // kernel joins them.
 //
 // Bound: the two products, 1024 cycles per 128 x 128 tile pair at the tensor rate, for
-// long prompts: 16384 tokens, 16 query and 2 key heads, in 650 us on a GB300, 1.69
-// PFLOP/s, 0.89 of a large library product's rate (beside the products a pair takes 128
+// long prompts: 16384 tokens, 16 query and 2 key heads, in 658 us on a GB300, 1.67
+// PFLOP/s, 0.88 of a large library product's rate (beside the products a pair takes 128
 // x 128 exponentials, 1024 cycles of the SM's four units, which the other tile's
 // products have to hide).  Packed prompts of 0 to 3000 tokens (4 key heads): 64 us,
-// 1.06 PFLOP/s; the start of a CTA, its diagonal tiles and the last round are the rest.
+// 1.05 PFLOP/s; the starts and ends of CTAs (some 5 us each, 3.5 CTAs to an SM), diagonal
+// tiles and the last round are the rest.
 // (Calls with few rows to a sequence: gdn_attn_split.cu.)
 #include <limits.h>
 #include <math.h>

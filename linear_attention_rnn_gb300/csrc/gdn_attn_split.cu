@@ -14,7 +14,7 @@
 // S buffer is enough: softmax, P V and the next S take some 1500 cycles a tile, and two
 // CTAs need one each in 2100 to take in what memory gives an SM.  Measured on a GB300, one
 // token each: 32 caches of 4096 rows, 16 heads without groups, 166 us, 6.5 TB/s, 0.96 of a
-// copy's rate; 32 caches of 1 to 16214 rows, 4 key heads, 94 us, 0.83 of it (unequal CTAs).
+// copy's rate; 32 caches of 1 to 16214 rows, 4 key heads, 95 us, 0.82 of it (unequal CTAs).
 #include "gdn_attn.cuh"
 
 namespace gdn {

@@ -40,10 +40,11 @@
 // 512 cycles that it takes, all of an SM's 128 bytes per cycle; with the loads, the
 // scaled rows, X's image and the staged output a chunk of the walk moves 576 KiB,
 // 4600 cycles, and takes 4800 to 5800 (2.4 to 2.9 us); the fold's 2300 (two terms) take
-// 2600.  Measured on a GB300, 16 key and 32 value heads: 65536 tokens in 485 us (fold
-// 151, prefix 8, walk 310; the bytes alone 238), 4096 tokens in 49 us (19, 6, 32; 15);
-// forward and backward of 4096 + 2500 + 1000 + 595 + 1 packed tokens in 277 us (walks 90
-// and 158, the longest sequence's 32 chunks deciding the first one; the bytes alone 87).
+// 2600, its 3100 where a final state needs three about 3050.  Measured on a GB300, 16 key and
+// 32 value heads: 65536 tokens in 504 to 520 us (fold 177, prefix 10, walk 316; the bytes
+// alone 238), 4096 tokens in 50 us (21, 7, 35, partly overlapped; 15); forward and backward of
+// 4096 + 2500 + 1000 + 595 + 1 packed tokens in 280 us (walks 94 and 159, the longest
+// sequence's 32 chunks deciding the first one; the bytes alone 87).
 #include "gdn_kernels.cuh"
 #include "gdn_tc05.cuh"
 

@@ -51,7 +51,8 @@ struct DecayPlan {
 // twice, and two more kernels start.  The estimate, in chunks of the walk (2.7 us
 // measured): equal CTAs run in rounds over the SMs, CTAs of mixed lengths take
 // their average and a part of the longest one's; a CTA starts in 1.5, the fold
-// takes half a chunk's time, the two launches together 4.
+// takes half a chunk's time (0.57 with the third terms of a final state, which the
+// estimate leaves out), the two launches together 4.
 double decay_rounds(double ctas, double longest, double sms, bool mixed) {
   if (ctas <= sms) return longest;
   if (mixed) return ctas * longest / sms + 0.3 * longest;
@@ -159,10 +160,11 @@ struct AttnPlan {
 // Calls with one query tile to a sequence on average (tokens over caches) or at most five
 // key tiles (short prompts) take k_attn_split, two CTAs to an SM: 32 caches of up to
 // 16214 rows 94 us against 103 in k_attn_fwd, 256 of 1024 102 against 136, 64 prompts of
-// 100 tokens 22 against 32, 8 of 600 25 against 28, but 8 of 1000 52 against 47.  Its estimate, in us: memory's time for all keys (64 KiB per key tile and
-// head, contexts being 0.8 of the longest one on average), or what one CTA takes by
-// itself (1.6 a key tile, measured), 10 for each round of CTAs, 9 and 0.2 a split for
-// the join and its launch.
+// 100 tokens 22 against 32, 8 of 600 25 against 28, but 8 of 1000 52 against 47.  (The
+// average is all that is known here: a long prompt among many single tokens goes the same way.)
+// Its estimate, in us: memory's time for all keys (64 KiB per key tile and head, contexts
+// being 0.8 of the longest one on average), or what one CTA takes by itself (1.6 a key
+// tile, measured), 10 for each round of CTAs, 9 and 0.2 a split for the join and its launch.
 //
 // Else a CTA of k_attn_fwd holds 256 / G tokens of one key head.  The estimate, in key
 // tiles of a CTA (0.8 us measured): the work of all CTAs over the SMs, contexts being

@@ -167,8 +167,8 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
 }
 // Every wait of this library's kernels gives up after this many SM cycles
 // (about one second at the GB300's 2.07 GHz, longer at lower clocks).  A wait
-// is for a TMA copy, an MMA or a handshake inside one CTA, normally
-// microseconds.
+// is for a TMA copy, an MMA, a handshake inside one CTA or (decay backward) the
+// sums of another, normally microseconds.
 constexpr long long WAIT_LIMIT_CYCLES = 2000000000LL;
 // Waits for the phase with the given parity to complete; gives up after
 // limit_cycles SM cycles and returns false (the caller records an error).
