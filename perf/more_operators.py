@@ -222,7 +222,6 @@ def prepare(case, seed):
         s["vp"] = normal(total, page, Hk, D).to(bf)
         s["to"] = table(kept, sum(-(-m // page) for m in kl))
         s["weights"] = torch.exp(2.0 * normal(total, Hk, page))
-        s["max_k"] = max(kl)
         return s
     ql, Hq = _ints(case["q"]), case["Hq"]
     s["cu"] = ints([0] + ql).cumsum(0).to(torch.int32)
@@ -268,7 +267,7 @@ def _run_own(s):
         return _without_none({"q": qo, "k": ko, "dq": dq, "dk": dk, "dwq": dwq, "dwk": dwk})
     if op == "evict":
         n = gdn.cache_evict(s["kp"], s["vp"], s["weights"], s["table"], s["len"], s["budget"], recent=s["recent"],
-                            to_table=s["to"], max_k=s["max_k"])
+                            to_table=s["to"])
         return {"len": n, "k_pages": s["kp"], "v_pages": s["vp"], "weights": s["weights"]}
     at = dict(cu_q=s["cu"], max_q=s["max_q"], max_k=s["max_k"])
     if op == "weigh":
