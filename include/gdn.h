@@ -429,6 +429,124 @@ int gdn_attn_bwd(const void* q, const void* k, const void* v, const void* o, con
                  size_t ws_bytes, void* stream);
 
 /*
+ * Norms of query and key heads with the position rotation in the same pass.  Per
+ * token t and head x [d] of q (weight q_weight) or k (k_weight):
+ *     n = x w / sqrt(mean(x^2) + eps)          (no weight: n = x),
+ *     y = n with its pairs j < n_pairs turned by
+ *         positions[pair_axis[j]][t] * inv_freq[j]  radians:
+ *         (a, b) -> (a cos - b sin, b cos + a sin).
+ * Pair j is (n_j, n_{j + n_pairs}), or with interleaved != 0 (n_{2j}, n_{2j + 1});
+ * values behind the first 2 n_pairs keep theirs.  n_pairs is a multiple of 8, at most
+ * d / 2 (0: no rotation; positions and inv_freq may then be NULL).  positions: int32
+ * [n_axes, n] on the device (several axes: time, height, width); inv_freq: fp32
+ * [n_pairs] on the device, finite; pair_axis: n_pairs bytes on the HOST, each below
+ * n_axes (NULL with one axis).  The angle's fraction of a turn is formed in 64 bits:
+ * positions of any size keep it.  q, q_out [n, Hq, d], k, k_out [n, Hk, d] bf16, d =
+ * 128, with strides between tokens as for the single-token forms; weights fp32 [d],
+ * 16-byte aligned; squares and sums in fp32 (values beyond 1e18 overflow them).
+ * q_out may be q, and k_out k, with equal strides; otherwise outputs must not overlap
+ * inputs.
+ * Backward: dq_out, dk_out are the cotangents of q_out and k_out, dq and dk those of q
+ * and k (dq may be dq_out, dk may be dk_out, with equal strides).  q and k are the
+ * forward's inputs, not read (and may be NULL) without a weight.  dq_weight, dk_weight:
+ * fp32 [d], sums over tokens and heads in a fixed order (NULL: not wanted); they need
+ * ws, of gdn_rope_workspace_bytes bytes.  Without them ws may be NULL.  No kernel of
+ * these calls waits, and ws has no status word.
+ *
+ * gdn_rope_append is the forward that writes the keys, and the values v [n, Hk, d] as
+ * they are, into a cache of n_pages pages of page_size rows each: token t into row
+ * slots[t] % page_size of page slots[t] / page_size (slots: int32 [n] on the device;
+ * a slot outside the cache is a padded token's, which is not written; two tokens must
+ * not share one).  q_out is written for every token.
+ *
+ * Pages: k_pages, v_pages hold n_pages x page_size rows of Hk heads, bf16, at element
+ * offset  page * strides->page + row * strides->row + head * strides->head, each stride
+ * a multiple of 8, at least d; page_size a multiple of 16.
+ */
+typedef struct {
+  long long page, row, head;
+} gdn_page_strides;
+
+int gdn_rope_fwd(const void* q, const void* k, const float* q_weight, const float* k_weight,
+                 const int* positions, const float* inv_freq, const unsigned char* pair_axis,
+                 void* q_out, void* k_out, int n, int Hq, int Hk, int d, int n_axes, int n_pairs,
+                 int interleaved, float eps, long long q_stride, long long k_stride,
+                 long long qo_stride, long long ko_stride, void* stream);
+size_t gdn_rope_workspace_bytes(int n, int Hq, int Hk, int d);
+int gdn_rope_bwd(const void* q, const void* k, const float* q_weight, const float* k_weight,
+                 const int* positions, const float* inv_freq, const unsigned char* pair_axis,
+                 const void* dq_out, const void* dk_out, void* dq, void* dk, float* dq_weight,
+                 float* dk_weight, int n, int Hq, int Hk, int d, int n_axes, int n_pairs,
+                 int interleaved, float eps, long long q_stride, long long k_stride,
+                 long long dqo_stride, long long dko_stride, long long dq_stride,
+                 long long dk_stride, void* ws, size_t ws_bytes, void* stream);
+int gdn_rope_append(const void* q, const void* k, const void* v, const float* q_weight,
+                    const float* k_weight, const int* positions, const float* inv_freq,
+                    const unsigned char* pair_axis, void* q_out, void* k_pages, void* v_pages,
+                    const int* slots, int n, int n_pages, int page_size, int Hq, int Hk, int d,
+                    int n_axes, int n_pairs, int interleaved, float eps, long long q_stride,
+                    long long k_stride, long long v_stride, long long qo_stride,
+                    const gdn_page_strides* k_strides, const gdn_page_strides* v_strides,
+                    void* stream);
+
+/*
+ * Softmax attention of new tokens over a paged cache: gdn_attn_fwd whose sequence s has
+ * its key and value rows in pages.  Row j lies in page page_table[s][j / page_size] at
+ * row j % page_size of k_pages and v_pages (layout: gdn_page_strides above); k_len[s]
+ * rows are used, the new tokens' own among them (gdn_rope_append writes them), so that
+ * the last query sees all of them, each one before it one fewer.  page_table: int32
+ * [n_seqs, max_pages] on the device, table_stride entries between sequences; an entry
+ * outside 0 .. n_pages - 1 is an absent page, whose keys nobody sees (a row that sees no
+ * other has o = 0, lse = -inf).  k_len is held within max_pages * page_size (at most
+ * 2^30).  Rows past k_len may hold anything.  Sequences may share pages.  q [total_q, Hq,
+ * d], cu_q, o, lse, scale, max_k, status and non-finite scores as for gdn_attn_fwd; ws of
+ * gdn_attn_workspace_bytes(0, n_seqs, total_q, max_pages * page_size, max_k, Hq, Hk, d).
+ *
+ * gdn_attn_paged_weights adds to each key the attention weight that it receives from the
+ * same queries,
+ *     weights[page][kh][row] += sum exp(scale q_i . k_j - lse_i)
+ * over the queries i that see key j and the query heads of key head kh, with lse
+ * [total_q, Hq] as gdn_attn_paged returned it (a row with lse = -inf adds nothing).
+ * weights: fp32 [n_pages, Hk, page_size], contiguous.  A sequence's sum is formed in a
+ * fixed order and added at once; where sequences share a page, or a table names one twice,
+ * each adds its own, in no fixed order.  max_k bounds the keys of a sequence (a value that
+ * is too small costs speed, not correctness).  ws: 256 bytes whose first word is the status
+ * word, or NULL.  A call that has nothing to add starts no kernel.
+ *
+ * gdn_cache_evict drops the lightest keys.  Per sequence and key head the last min(recent,
+ * budget) keys stay and of the others those with the largest weights, budget in all; of
+ * equal weights the lowest index stays, NaN weighs least.  What stays moves in its order
+ * into rows 0, 1, .. of the sequence's target pages to_table [n_seqs, to_pages] (int32,
+ * to_stride entries between sequences, with to_pages * page_size rows for min(budget,
+ * max_pages * page_size) keys): keys, values and weights.  to_table NULL or page_table:
+ * the sequence's own pages, in place.  Other rows keep what they hold.  new_len [n_seqs] receives
+ * the keys that stay of each sequence (the same for all heads); it must not be k_len.
+ * Keys on absent pages never stay; a row whose target page is absent is not written.  In
+ * place, sequences must not share pages; otherwise no target page may hold a key of any
+ * sequence of the call.  ws: gdn_cache_evict_workspace_bytes(n_seqs, max_pages *
+ * page_size, budget, Hk) bytes, without a status word (no kernel of it waits).
+ */
+int gdn_attn_paged(const void* q, const void* k_pages, const void* v_pages, const int* page_table,
+                   const int* k_len, const int* cu_q, void* o, float* lse, int n_seqs, int total_q,
+                   int max_k, int n_pages, int page_size, int max_pages, int Hq, int Hk, int d,
+                   float scale, long long q_stride, const gdn_page_strides* k_strides,
+                   const gdn_page_strides* v_strides, long long table_stride, void* ws,
+                   size_t ws_bytes, void* stream);
+int gdn_attn_paged_weights(const void* q, const void* k_pages, const float* lse,
+                           const int* page_table, const int* k_len, const int* cu_q, float* weights,
+                           int n_seqs, int total_q, int max_k, int n_pages, int page_size,
+                           int max_pages, int Hq, int Hk, int d, float scale, long long q_stride,
+                           const gdn_page_strides* k_strides, long long table_stride, void* ws,
+                           size_t ws_bytes, void* stream);
+size_t gdn_cache_evict_workspace_bytes(int n_seqs, int max_rows, int budget, int Hk);
+int gdn_cache_evict(void* k_pages, void* v_pages, float* weights, const int* page_table,
+                    const int* to_table, const int* k_len, int* new_len, int n_seqs, int n_pages,
+                    int page_size, int max_pages, int to_pages, int Hk, int d, int budget,
+                    int recent, const gdn_page_strides* k_strides, const gdn_page_strides* v_strides,
+                    long long table_stride, long long to_stride, void* ws, size_t ws_bytes,
+                    void* stream);
+
+/*
  * Debug export of the per-chunk UT quantities, for tests.  For every
  * (b, value head j, chunk c), in [B, Hv, N, ...] order with N = ceil(T/chunk):
  *   S_out [.., chunk, chunk] fp32  S = tril(diag(beta) (K K^T * decay), -1)

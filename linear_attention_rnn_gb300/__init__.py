@@ -4,7 +4,10 @@ Beside the chunked rule (chunk_fwd, chunk_bwd, the layer and the segment calls) 
 are the operators that a stack with other mixers and a decoding loop need:
 delta_step, one token per row of the gated delta rule; decay_fwd, decay_bwd and
 decay_step, linear attention with a decay for each head; attn_fwd and attn_bwd,
-causal softmax attention with grouped heads, over packed sequences or caches.
+causal softmax attention with grouped heads, over packed sequences or caches.  Around
+softmax attention: rope_fwd and rope_bwd, norms of query and key heads with the position
+rotation; for serving from a paged cache rope_append, which writes the turned keys into
+its pages, attn_paged, attn_paged_weights and cache_evict.
 
 Thin marshalling over the C ABI in include/gdn.h: shape/dtype checks,
 allocation of outputs and workspace with torch, and the ctypes call on the
@@ -123,6 +126,23 @@ def lib():
         L.gdn_attn_fwd.restype = I
         L.gdn_attn_bwd.argtypes = [P] * 11 + [I] * 6 + [ctypes.c_float] + [LL] * 3 + [P, Z, P]
         L.gdn_attn_bwd.restype = I
+        F = ctypes.c_float
+        L.gdn_rope_fwd.argtypes = [P] * 9 + [I] * 7 + [F] + [LL] * 4 + [P]
+        L.gdn_rope_fwd.restype = I
+        L.gdn_rope_workspace_bytes.argtypes = [I] * 4
+        L.gdn_rope_workspace_bytes.restype = Z
+        L.gdn_rope_bwd.argtypes = [P] * 13 + [I] * 7 + [F] + [LL] * 6 + [P, Z, P]
+        L.gdn_rope_bwd.restype = I
+        L.gdn_rope_append.argtypes = [P] * 12 + [I] * 9 + [F] + [LL] * 4 + [P] * 3
+        L.gdn_rope_append.restype = I
+        L.gdn_attn_paged.argtypes = [P] * 8 + [I] * 9 + [F, LL, P, P, LL, P, Z, P]
+        L.gdn_attn_paged.restype = I
+        L.gdn_attn_paged_weights.argtypes = [P] * 7 + [I] * 9 + [F, LL, P, LL, P, Z, P]
+        L.gdn_attn_paged_weights.restype = I
+        L.gdn_cache_evict_workspace_bytes.argtypes = [I] * 4
+        L.gdn_cache_evict_workspace_bytes.restype = Z
+        L.gdn_cache_evict.argtypes = [P] * 7 + [I] * 9 + [P, P, LL, LL, P, Z, P]
+        L.gdn_cache_evict.restype = I
         L.gdn_selftest_wait_timeout.argtypes = [ctypes.c_longlong, P, P]
         L.gdn_selftest_wait_timeout.restype = I
         _several_devices = torch.cuda.device_count() > 1
@@ -679,6 +699,306 @@ def attn_bwd(q, k, v, o, lse, dO, *, cu_q=None, cu_k=None, max_q=None, max_k=Non
     return dq, dk, dv
 
 
+# ---- heads' norms and rotation, and the paged cache that they feed -----------------------
+class _PageStrides(ctypes.Structure):
+    _fields_ = [("page", ctypes.c_longlong), ("row", ctypes.c_longlong), ("head", ctypes.c_longlong)]
+
+
+@functools.lru_cache(maxsize=256)
+def _page_layout(shape, strides):
+    """The C struct of a cache's strides (a dimension of one element has any)."""
+    st = [max(shape[3], 8) if n <= 1 else s for n, s in zip(shape[:3], strides[:3])]
+    return _PageStrides(st[0], st[1], st[2])
+
+
+def _check_pages(t, name, Hk=None, like=None):
+    """A cache [pages, page_size, Hk, d] in bf16 whose rows of d values are contiguous and
+    lie multiples of 8 elements apart; returns its strides as the C struct."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype is not torch.bfloat16:
+        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 4 or (Hk is not None and t.shape[2] != Hk):
+        raise ValueError(f"{name} must be [pages, page_size, {'Hk' if Hk is None else Hk}, d], got {tuple(t.shape)}")
+    if like is not None and t.shape != like.shape:
+        raise ValueError(f"k_pages and v_pages have shapes {tuple(like.shape)} and {tuple(t.shape)}")
+    d = t.shape[3]
+    strides = t.stride()
+    if t.numel():
+        if strides[3] != 1:
+            raise ValueError(f"{name} must have contiguous rows")
+        for n, s in zip(t.shape[:3], strides[:3]):
+            if n > 1 and (s < d or s % 8):
+                raise ValueError(f"{name} must have rows at least {d} elements apart, by multiples of 8")
+        return _page_layout(t.shape, strides)
+    return _page_layout(t.shape, (d, d, d, 1))
+
+
+def _check_table(t, name, n):
+    """int32 [n, pages] whose rows are contiguous; returns (pages, entries between rows)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype is not torch.int32:
+        raise ValueError(f"{name} must be {torch.int32}, got {t.dtype}")
+    if t.dim() != 2 or t.shape[0] != n:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({n}, pages)")
+    m = t.shape[1]
+    if t.numel() and ((m > 1 and t.stride(1) != 1) or (n > 1 and t.stride(0) < m)):
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    return m, (t.stride(0) if t.numel() and n > 1 else m)
+
+
+@functools.lru_cache(maxsize=64)
+def _pair_axes(pair_axis, n_pairs):
+    if pair_axis is None:
+        return None
+    if len(pair_axis) != n_pairs or not all(0 <= a < 256 for a in pair_axis):
+        raise ValueError(f"pair_axis must name an axis for each of the {n_pairs} pairs")
+    return bytes(pair_axis)
+
+
+def _rope_dims(q, k, positions, inv_freq, q_weight, k_weight, pair_axis):
+    """Rows [n, H, d] or [B, T, H, d]; returns the sizes and the row strides of q and k."""
+    if q.dim() < 3 or k.dim() != q.dim() or q.shape[:-2] != k.shape[:-2] or q.shape[-1] != k.shape[-1]:
+        raise ValueError(f"q and k must be [.., H, d] with equal rows, got {tuple(q.shape)} and {tuple(k.shape)}")
+    Hq, d = q.shape[-2:]
+    Hk = k.shape[-2]
+    n = q.shape[:-2].numel()
+    sq, sk = _check_rows(q, "q", Hq, d, n), _check_rows(k, "k", Hk, d, n)
+    _check(q_weight, "q_weight", torch.float32, (d,))
+    _check(k_weight, "k_weight", torch.float32, (d,))
+    axes, pairs = 1, 0
+    if inv_freq is not None:
+        _check(inv_freq, "inv_freq", torch.float32)
+        if inv_freq.dim() != 1:
+            raise ValueError("inv_freq must hold a frequency for each pair")
+        pairs = inv_freq.numel()
+        if positions is None:
+            raise ValueError("inv_freq needs positions")
+        _check(positions, "positions", torch.int32)
+        rows = q.shape[:-2]
+        if positions.shape != rows:
+            if positions.dim() != len(rows) + 1 or positions.shape[1:] != rows or positions.shape[0] < 1:
+                raise ValueError(f"positions has shape {tuple(positions.shape)}, expected {tuple(rows)} "
+                                 f"or an axis more in front")
+            axes = positions.shape[0]
+    if pair_axis is not None and pair_axis.__class__ is not tuple:
+        pair_axis = tuple(int(x) for x in pair_axis)
+    return n, Hq, Hk, d, axes, pairs, _pair_axes(pair_axis, pairs), sq, sk
+
+
+def _rows_out(t, name, like, n, H, d):
+    """An output's rows: contiguous ones made here, or the caller's (a part of a wider buffer)."""
+    if t is None:
+        return torch.empty(like.shape, dtype=torch.bfloat16, device=like.device), H * d
+    if t.shape != like.shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(like.shape)}")
+    return t, _check_rows(t, name, H, d, n)
+
+
+def rope_fwd(q, k, positions, inv_freq, *, q_weight=None, k_weight=None, eps: float = 1e-6, pair_axis=None,
+             interleaved: bool = False, q_out=None, k_out=None):
+    """Norms of query and key heads with the position rotation in the same pass: every head
+    x of q [.., Hq, 128] and k [.., Hk, 128] becomes x w / sqrt(mean(x^2) + eps) (without
+    its weight, fp32 [128], it stays x), then each of its first P pairs turns by
+    positions[pair_axis[j]] * inv_freq[j].  inv_freq: fp32 [P], P a multiple of 8 up to 64
+    (None: no rotation); positions: int32, the rows' shape, or [axes, ..] with pair_axis, a
+    sequence of P axis numbers (time, height, width).  Pair j is (j, j + P), or
+    (2j, 2j + 1) if interleaved.  q_out and k_out may be q and k.  Returns (q_out, k_out)."""
+    n, Hq, Hk, d, axes, pairs, table, sq, sk = _rope_dims(q, k, positions, inv_freq, q_weight, k_weight, pair_axis)
+    q_out, so = _rows_out(q_out, "q_out", q, n, Hq, d)
+    k_out, sko = _rows_out(k_out, "k_out", k, n, Hk, d)
+    if _several_devices:
+        _check_devices(q, k, positions, inv_freq, q_weight, k_weight, q_out, k_out)
+    rc = lib().gdn_rope_fwd(q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight), _ptr(positions),
+                            _ptr(inv_freq), table, q_out.data_ptr(), k_out.data_ptr(), n, Hq, Hk, d, axes, pairs,
+                            interleaved, eps, sq, sk, so, sko, _stream(q.device))
+    if rc != GDN_OK:
+        raise GDNError(rc, "gdn_rope_fwd")
+    return q_out, k_out
+
+
+def rope_workspace_bytes(n, Hq, Hk, d=128) -> int:
+    return _planned_bytes("gdn_rope_workspace_bytes", _current_device(), n, Hq, Hk, d)
+
+
+def rope_bwd(q, k, positions, inv_freq, dq_out, dk_out, *, q_weight=None, k_weight=None, eps: float = 1e-6,
+             pair_axis=None, interleaved: bool = False, dq=None, dk=None, workspace=None):
+    """Backward of rope_fwd: q and k are its inputs, dq_out and dk_out the cotangents of its
+    outputs (dq may be dq_out, dk may be dk_out).  Returns (dq, dk, dq_weight, dk_weight), the
+    last two in fp32 (None without the weight)."""
+    n, Hq, Hk, d, axes, pairs, table, sq, sk = _rope_dims(q, k, positions, inv_freq, q_weight, k_weight, pair_axis)
+    if dq_out.shape != q.shape or dk_out.shape != k.shape:
+        raise ValueError(f"dq_out and dk_out have shapes {tuple(dq_out.shape)} and {tuple(dk_out.shape)}, expected "
+                         f"{tuple(q.shape)} and {tuple(k.shape)}")
+    sg, sgk = _check_rows(dq_out, "dq_out", Hq, d, n), _check_rows(dk_out, "dk_out", Hk, d, n)
+    dq, so = _rows_out(dq, "dq", q, n, Hq, d)
+    dk, sko = _rows_out(dk, "dk", k, n, Hk, d)
+    dev = q.device
+    dqw = torch.empty(d, dtype=torch.float32, device=dev) if q_weight is not None else None
+    dkw = torch.empty(d, dtype=torch.float32, device=dev) if k_weight is not None else None
+    if _several_devices:
+        _check_devices(q, k, positions, inv_freq, q_weight, k_weight, dq_out, dk_out, dq, dk, workspace)
+    need = 0 if dqw is None and dkw is None else _planned_bytes("gdn_rope_workspace_bytes", dev.index, n, Hq, Hk, d)
+    wp, wn, ws = _scratch_all(need, dev, workspace)  # (ws: kept alive over the call)
+    rc = lib().gdn_rope_bwd(q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight), _ptr(positions),
+                            _ptr(inv_freq), table, dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+                            _ptr(dqw), _ptr(dkw), n, Hq, Hk, d, axes, pairs, interleaved, eps, sq, sk, sg, sgk, so, sko,
+                            wp, wn, _stream(dev))
+    if rc != GDN_OK:
+        raise GDNError(rc, "gdn_rope_bwd")
+    return dq, dk, dqw, dkw
+
+
+def rope_append(q, k, v, positions, inv_freq, k_pages, v_pages, slots, *, q_weight=None, k_weight=None,
+                eps: float = 1e-6, pair_axis=None, interleaved: bool = False, q_out=None) -> torch.Tensor:
+    """rope_fwd of new tokens whose keys, and values v [.., Hk, 128] as they are, go into a
+    cache: k_pages and v_pages [pages, page_size, Hk, 128] (any strides that are multiples of
+    8; page_size a multiple of 16).  slots: int32, the rows' shape; token t goes to page
+    slots[t] // page_size, row slots[t] % page_size, and nowhere if that is outside the cache (a
+    padded token).  Returns q_out."""
+    n, Hq, Hk, d, axes, pairs, table, sq, sk = _rope_dims(q, k, positions, inv_freq, q_weight, k_weight, pair_axis)
+    if v.shape != k.shape:
+        raise ValueError(f"k and v have shapes {tuple(k.shape)} and {tuple(v.shape)}")
+    sv = _check_rows(v, "v", Hk, d, n)
+    ks = _check_pages(k_pages, "k_pages", Hk)
+    vs = _check_pages(v_pages, "v_pages", Hk, k_pages)
+    _check(slots, "slots", torch.int32, q.shape[:-2])
+    q_out, so = _rows_out(q_out, "q_out", q, n, Hq, d)
+    if _several_devices:
+        _check_devices(q, k, v, positions, inv_freq, q_weight, k_weight, k_pages, v_pages, slots, q_out)
+    rc = lib().gdn_rope_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(q_weight), _ptr(k_weight),
+                               _ptr(positions), _ptr(inv_freq), table, q_out.data_ptr(), k_pages.data_ptr(),
+                               v_pages.data_ptr(), slots.data_ptr(), n, k_pages.shape[0], k_pages.shape[1], Hq, Hk, d,
+                               axes, pairs, interleaved, eps, sq, sk, sv, so, ctypes.byref(ks), ctypes.byref(vs),
+                               _stream(q.device))
+    if rc != GDN_OK:
+        raise GDNError(rc, "gdn_rope_append")
+    return q_out
+
+
+def _scratch_all(nbytes, device, ws):
+    """As _scratch, for workspaces without a status word: none is made where none is needed."""
+    if ws is None and nbytes:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return _scratch(nbytes, device, ws)
+
+
+def _paged_dims(q, k_pages, page_table, k_len, cu_q, max_k, scale):
+    """New tokens packed [total, H, D] with cu_q, or [B, T, H, D] without, over pages."""
+    if q.dim() != (4 if cu_q is None else 3):
+        raise ValueError("q must be [B, T, H, D], or [total, H, D] with cu_q")
+    if cu_q is not None:
+        _check(cu_q, "cu_q", torch.int32)
+        if cu_q.dim() != 1 or cu_q.numel() < 1:
+            raise ValueError("cu_q must hold the sequences' starts and the total")
+        n, total = cu_q.numel() - 1, q.shape[0]
+    else:
+        n, total = q.shape[0], q.shape[0] * q.shape[1]
+    Hq, d = q.shape[-2:]
+    sq = _check_rows(q, "q", Hq, d, total)
+    ks = _check_pages(k_pages, "k_pages")
+    if k_pages.shape[3] != d:
+        raise ValueError(f"q and k_pages have heads of {d} and {k_pages.shape[3]}")
+    P, page, Hk = k_pages.shape[:3]
+    pages, st = _check_table(page_table, "page_table", n)
+    _check(k_len, "k_len", torch.int32, (n,))
+    if k_len is None:
+        raise ValueError("k_len must give the used rows of every sequence")
+    longest = pages * page if max_k is None else int(max_k)
+    return n, total, longest, P, page, pages, Hq, Hk, d, d ** -0.5 if scale is None else float(scale), sq, ks, st
+
+
+def attn_paged(q, k_pages, v_pages, page_table, k_len, *, cu_q=None, max_q=None, max_k=None, scale=None,
+               want_lse: bool = True, o=None, lse=None, workspace=None
+               ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """attn_fwd of new tokens over a paged cache: q [total_q, Hq, 128] with cu_q, or [B, T, Hq,
+    128]; k_pages, v_pages [pages, page_size, Hk, 128] as for rope_append; page_table int32
+    [n, ..], the pages of each sequence (an entry outside the cache is an absent page, whose
+    keys nobody sees); k_len int32 [n], their used rows, the new tokens' own among them.  max_k
+    bounds them and steers how they are split over the SMs (without it: the table's rows).  Returns (o, lse)."""
+    n, total, longest, P, page, pages, Hq, Hk, d, scale, sq, ks, st = _paged_dims(q, k_pages, page_table, k_len, cu_q,
+                                                                                  max_k, scale)
+    vs = _check_pages(v_pages, "v_pages", Hk, k_pages)
+    dev = q.device
+    if o is None:
+        o = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+    else:
+        _check(o, "o", torch.bfloat16, q.shape)
+    if lse is not None:
+        _check(lse, "lse", torch.float32, q.shape[:-1])
+    elif want_lse:
+        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
+    if _several_devices:
+        _check_devices(q, k_pages, v_pages, page_table, k_len, cu_q, o, lse, workspace)
+    wp, wn, ws = _scratch(_planned_bytes("gdn_attn_workspace_bytes", dev.index, 0, n, total, pages * page, longest,
+                                         Hq, Hk, d), dev, workspace)  # (ws: kept alive over the call)
+    rc = lib().gdn_attn_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
+                              k_len.data_ptr(), _ptr(cu_q), o.data_ptr(), _ptr(lse), n, total, longest, P, page, pages,
+                              Hq, Hk, d, scale, sq, ctypes.byref(ks), ctypes.byref(vs), st, wp, wn, _stream(dev))
+    if rc != GDN_OK:
+        raise GDNError(rc, "gdn_attn_paged")
+    return o, lse
+
+
+def attn_paged_weights(q, k_pages, lse, page_table, k_len, weights, *, cu_q=None, max_q=None, max_k=None, scale=None,
+                       workspace=None) -> torch.Tensor:
+    """Adds to weights [pages, Hk, page_size] (fp32) the attention weight that each cached key
+    receives from the queries of an attn_paged call (its q, pages, table and lengths, and its
+    lse), summed over them and over the query heads of each key head.  Returns weights."""
+    n, total, longest, P, page, pages, Hq, Hk, d, scale, sq, ks, st = _paged_dims(q, k_pages, page_table, k_len, cu_q,
+                                                                                  max_k, scale)
+    _check(lse, "lse", torch.float32, q.shape[:-1])
+    _check(weights, "weights", torch.float32, (P, Hk, page))
+    if _several_devices:
+        _check_devices(q, k_pages, lse, page_table, k_len, weights, cu_q, workspace)
+    wp, wn, ws = _scratch(_STATUS_BYTES, q.device, workspace)
+    rc = lib().gdn_attn_paged_weights(q.data_ptr(), k_pages.data_ptr(), lse.data_ptr(), page_table.data_ptr(),
+                                      k_len.data_ptr(), _ptr(cu_q), weights.data_ptr(), n, total, longest, P, page,
+                                      pages, Hq, Hk, d, scale, sq, ctypes.byref(ks), st, wp, wn, _stream(q.device))
+    if rc != GDN_OK:
+        raise GDNError(rc, "gdn_attn_paged_weights")
+    return weights
+
+
+def cache_evict_workspace_bytes(n_seqs, max_rows, budget, Hk) -> int:
+    return int(lib().gdn_cache_evict_workspace_bytes(n_seqs, max_rows, budget, Hk))
+
+
+def cache_evict(k_pages, v_pages, weights, page_table, k_len, budget: int, *, recent: int = 0, to_table=None,
+                new_len=None, workspace=None) -> torch.Tensor:
+    """Drops the lightest keys of a paged cache: of each sequence and key head the last `recent`
+    keys stay and of the others those with the largest weights [pages, Hk, page_size] (ties: the
+    lowest index), `budget` in all.  What stays moves in its order, with its values and weights, to
+    the first rows of the pages that to_table [n, ..] lists (None: the sequence's own, in place;
+    they must not be shared then, and other target pages must hold no key of the call).  Returns the
+    new lengths, int32 [n] (new_len, if given; it must not be k_len)."""
+    ks = _check_pages(k_pages, "k_pages")
+    P, page, Hk, d = k_pages.shape
+    vs = _check_pages(v_pages, "v_pages", Hk, k_pages)
+    _check(weights, "weights", torch.float32, (P, Hk, page))
+    if k_len.dim() != 1:
+        raise ValueError("k_len must give the used rows of every sequence")
+    n = k_len.shape[0]
+    _check(k_len, "k_len", torch.int32)
+    pages, st = _check_table(page_table, "page_table", n)
+    to_pages, sto = _check_table(to_table, "to_table", n) if to_table is not None else (0, 0)
+    if new_len is None:
+        new_len = torch.empty(n, dtype=torch.int32, device=k_len.device)
+    else:
+        _check(new_len, "new_len", torch.int32, (n,))
+    if _several_devices:
+        _check_devices(k_pages, v_pages, weights, page_table, k_len, to_table, new_len, workspace)
+    wp, wn, ws = _scratch_all(cache_evict_workspace_bytes(n, pages * page, int(budget), Hk), k_len.device, workspace)
+    rc = lib().gdn_cache_evict(k_pages.data_ptr(), v_pages.data_ptr(), weights.data_ptr(), page_table.data_ptr(),
+                               _ptr(to_table), k_len.data_ptr(), new_len.data_ptr(), n, P, page, pages, to_pages, Hk, d,
+                               int(budget), int(recent), ctypes.byref(ks), ctypes.byref(vs), st, sto, wp, wn,
+                               _stream(k_len.device))
+    if rc != GDN_OK:
+        raise GDNError(rc, "gdn_cache_evict")
+    return new_len
+
+
 def debug_ut(k, v, g, beta, chunk: int = 128, tiles: bool = False):
     """Per-chunk S, T (fp32) and w, u (bf16), each [B, Hv, N, chunk, .].
 
@@ -735,4 +1055,6 @@ __all__ = ["build", "lib", "chunk_fwd", "chunk_bwd", "layer_fwd", "layer_bwd",
            "layer_workspace_bytes", "saved_bytes", "affine_compose", "segment_fold", "debug_ut",
            "fwd_workspace_bytes", "bwd_workspace_bytes", "default_segments", "GDNError",
            "header_functions", "delta_step", "decay_step", "decay_fwd", "decay_bwd",
-           "decay_workspace_bytes", "attn_fwd", "attn_bwd", "attn_workspace_bytes", "workspace_status", "selftest_wait_timeout"]
+           "decay_workspace_bytes", "attn_fwd", "attn_bwd", "attn_workspace_bytes", "rope_fwd", "rope_bwd",
+           "rope_workspace_bytes", "rope_append", "attn_paged", "attn_paged_weights", "cache_evict",
+           "cache_evict_workspace_bytes", "workspace_status", "selftest_wait_timeout"]

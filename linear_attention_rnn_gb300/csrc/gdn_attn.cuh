@@ -32,11 +32,14 @@ struct Lanes {
   int2 q, k;
   int used;
 };
+__device__ __forceinline__ int2 keys_of(const AttnArgs& a, int s) {
+  return a.table ? make_int2(0, a.pages.capacity) : rows_of(a.cu_k, s, a.n_seqs, a.total_k);
+}
 __device__ __forceinline__ Lanes read_lanes(const AttnArgs& a) {
   const int s = min((int)(threadIdx.x & 31), a.n_seqs - 1);
   Lanes l;
   l.q = rows_of(a.cu_q, s, a.n_seqs, a.total_q);
-  l.k = rows_of(a.cu_k, s, a.n_seqs, a.total_k);
+  l.k = keys_of(a, s);
   l.used = a.k_len ? min(max(a.k_len[s], 0), l.k.y) : l.k.y;
   return l;
 }
@@ -49,7 +52,7 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs& a, const Lanes& l, int s) 
     used = __shfl_sync(0xffffffffu, l.used, s);
   } else {
     q = rows_of(a.cu_q, s, a.n_seqs, a.total_q);
-    k = rows_of(a.cu_k, s, a.n_seqs, a.total_k);
+    k = keys_of(a, s);
     used = a.k_len ? min(max(a.k_len[s], 0), k.y) : k.y;
   }
   Seq r;
@@ -113,6 +116,49 @@ __device__ __forceinline__ void load_group(unsigned char* dst, const CUtensorMap
   tc::tma_load_3d(dst, m, 0, kh * G, tok, bar);
   tc::tma_load_3d(dst + TILE / 2, m, 64, kh * G, tok, bar);
 }
+
+// ---- keys in pages ----------------------------------------------------------------
+// A tile of KEYS rows of a sequence is loaded piece by piece: `box` rows, the largest
+// power of two that divides the page size (at most KEYS), lie in one page.  Pieces are
+// shared out to the lanes of the loading warp, which reads a tile's table entries ahead
+// of its slot.  An entry that names no page, and a piece behind the keys, reads as zeros
+// (the map's fill for page -1).
+template <int KEYS>
+struct Paged {
+  const int* row;  // the sequence's part of the table
+  int kl;
+  __device__ __forceinline__ Paged(const AttnArgs& a, int seq, int keys)
+      : row(a.table + (long)seq * a.pages.table_stride), kl(keys) {}
+  // the page of this lane's piece of the tile from key0 on (-1: none)
+  __device__ __forceinline__ int entry(const PageArgs& p, int key0) const {
+    const int lane = threadIdx.x & 31, key = key0 + lane * p.box;
+    if (lane >= KEYS / p.box || key >= kl) return -1;
+    const int e = row[key / p.page];
+    return (unsigned)e < (unsigned)p.n_pages ? e : -1;
+  }
+  // by a whole warp
+  __device__ __forceinline__ void load(const PageArgs& p, unsigned char* dst, const CUtensorMap* m, int head, int key0,
+                                       int entry, uint64_t* bar) const {
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) tc::arrive_expect_tx(bar, KEYS * HD * 2);
+    __syncwarp();
+    if (lane < KEYS / p.box) {
+      const int y = (key0 + lane * p.box) % p.page;
+      unsigned char* d = dst + lane * p.box * 128;
+      tc::tma_load_4d(d, m, 0, head, y, entry, bar);
+      tc::tma_load_4d(d + KEYS * 128, m, 64, head, y, entry, bar);
+    }
+  }
+  // one bit for every 16 keys of the tile from key0 on whose page is absent, the same in all
+  // lanes; ask() reads the table, absent() a tile later so that nobody waits for it
+  __device__ __forceinline__ int ask(const PageArgs& p, int key0) const {
+    const int lane = threadIdx.x & 31, key = key0 + lane * 16;
+    return lane < KEYS / 16 && key < kl ? row[key / p.page] : 0;
+  }
+  __device__ __forceinline__ uint32_t absent(const PageArgs& p, int asked) const {
+    return __ballot_sync(0xffffffffu, (unsigned)asked >= (unsigned)p.n_pages);
+  }
+};
 
 // Zeros in rows [from, 128) of an SW128 tile, by `nthreads` threads.
 __device__ __forceinline__ void zero_rows(unsigned char* tile, int from, int t, int nthreads) {

@@ -199,6 +199,14 @@ struct DecayFoldArgs {
   int behind;            // the launch before it is the call's walk, which reads the states that it writes
 };
 
+// A cache in pages.
+struct PageArgs {
+  int page, n_pages;  // rows of a page, pages
+  int box;            // rows of a load (divides page and the key tile)
+  int capacity;       // rows that a sequence's part of the table covers
+  long table_stride;  // entries between sequences
+};
+
 // Causal softmax attention over packed sequences (gdn_attn_fwd.cu, gdn_attn_bwd.cu).
 struct AttnArgs {
   CUtensorMap q, k, v;  // q: boxes of 64 columns x a group's heads x 128 / G tokens; k, v: x 1 head x 128 rows
@@ -207,6 +215,8 @@ struct AttnArgs {
   const int* cu_q;      // [n_seqs + 1] (null: equal lengths), cu_k alike
   const int* cu_k;
   const int* k_len;     // [n_seqs] used rows of each sequence's keys (nullable; forward)
+  const int* table;     // keys in pages: [n_seqs][..] pages (null: packed keys; forward), k and v
+  PageArgs pages;       //   then have boxes of 64 columns x 1 head x pages.box rows x 1 page
   bf16* o;              // [total_q][Hq][HD]
   float* lse;           // [total_q][Hq] (forward: nullable)
   float* part;          // [n_parts][total_q][Hq][HD]
@@ -224,6 +234,57 @@ struct AttnArgs {
   int n_seqs, total_q, total_k, Hq, Hk;
   int split_tiles, n_splits;  // key tiles to a split
   int n_parts;                // 2 to a split (k_attn_fwd) or 1 (k_attn_split)
+};
+
+// The weight that attention gives to each key in pages (gdn_weigh.cu).
+struct WeighArgs {
+  AttnArgs at;          // q, k, cu_q, k_len, table and sizes
+  const float* lse;     // [total_q][Hq]
+  float* weights;       // [n_pages][Hk][page], added to
+  int few;              // tokens over caches: the kernel that streams keys
+  int key_tiles;        // many queries: key tiles of a sequence, foreseen; few: key tiles to a split
+  int n_splits;         // few
+};
+
+// Eviction of the lightest keys from pages (gdn_evict.cu).
+struct EvictArgs {
+  bf16* k;
+  bf16* v;
+  float* weights;       // [n_pages][Hk][page]
+  const int* table;     // [n_seqs][..] pages of the sequences
+  const int* to;        // [n_seqs][..] target pages (null: the sequences' own)
+  const int* k_len;
+  int* new_len;         // [n_seqs]
+  int* list;            // [n_seqs][Hk][keep] keys that stay
+  PageArgs pages;       // (box unused)
+  long to_stride;       // entries between sequences
+  long sk_page, sk_row, sk_head, sv_page, sv_row, sv_head;  // elements
+  int n_seqs, Hk, budget, recent;
+  int keep;             // most keys that stay: the smaller of budget and the table's rows
+};
+
+// Norms and rotation of heads (gdn_rope.cu): the rows of q, of k or of v (v: copied into pages).
+struct RopePart {
+  const bf16* x;        // [n][H][HD], sx elements between tokens
+  const bf16* g;        // backward: the cotangent of the turned rows
+  bf16* y;              // forward: the turned rows; backward: dx
+  const float* w;       // [HD] (null: no norm)
+  float* dw;            // backward (nullable)
+  long sx, sg, sy;      // elements between tokens (paged y: between pages)
+  long sy_row, sy_head; // paged y: between a page's rows, between heads
+  int H, turned, paged;
+  int tokens, blocks;   // tokens of a block, blocks of this part
+};
+struct RopeArgs {
+  RopePart part[3];
+  const int* pos;       // [axes][n]
+  const float* freq;    // [P]
+  const int* slots;     // [n] rows of the cache (paged parts)
+  float* partial;       // [blocks][HD] (backward with weights)
+  long n, cache_rows;
+  int page, P, interleaved;
+  float eps;
+  unsigned char axis[HD / 2];
 };
 
 // The status word of a call, cleared by the first block of its first kernel: that
@@ -275,6 +336,12 @@ cudaError_t launch_decay(const DecayArgs& a, const DecayFoldArgs& f, cudaStream_
 // the segments' own states and the prefix over them (two launches); with one segment
 // to a sequence the final state alone (one launch)
 cudaError_t launch_decay_fold(const DecayFoldArgs& a, cudaStream_t s);
+cudaError_t launch_weigh(const WeighArgs& a, cudaStream_t s);
+// the keys that stay and their lengths, then the copies
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s);
+int rope_tokens(int H);  // tokens that a block takes of a part with H heads
+cudaError_t launch_rope_fwd(const RopeArgs& a, cudaStream_t s);
+cudaError_t launch_rope_bwd(const RopeArgs& a, cudaStream_t s);
 cudaError_t launch_attn_fwd(const AttnArgs& a, cudaStream_t s);
 cudaError_t launch_attn_split(const AttnArgs& a, cudaStream_t s);  // keys in maps of 64 rows
 cudaError_t launch_attn_join(const AttnArgs& a, cudaStream_t s);

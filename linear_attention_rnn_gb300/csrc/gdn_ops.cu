@@ -5,39 +5,13 @@
 #include <string.h>
 
 #include "gdn.h"
+#include "gdn_host.cuh"
 #include "gdn_kernels.cuh"
 #include "gdn_tmap.cuh"
 
 using namespace gdn;
 
 namespace {
-
-constexpr size_t ALIGN = 256;
-inline size_t up(size_t x) { return (x + ALIGN - 1) / ALIGN * ALIGN; }
-inline bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-int cuda_status(cudaError_t e) { return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA; }
-
-template <typename T>
-T* at(void* ws, size_t off) {
-  return reinterpret_cast<T*>(static_cast<char*>(ws) + off);
-}
-
-int sm_count() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
-    sms = 152;
-  return sms;
-}
-
-// rows of H heads, `stride` elements apart: whole 16-byte pieces that do not overlap
-inline bool row_stride_ok(long long stride, int H) { return stride >= (long long)H * HD && stride % 8 == 0; }
-
-// A workspace that would hold the status word alone may be left out.
-constexpr size_t STATUS_BYTES = ALIGN;
-inline bool workspace_ok(const void* ws, size_t ws_bytes, size_t need) {
-  return ws ? ws_bytes >= need : need <= STATUS_BYTES;
-}
 
 // ---- linear attention with a decay for each head -----------------------------------
 struct DecayPlan {
@@ -249,7 +223,7 @@ int attn_args(AttnArgs& a, const void* q, const void* k, const void* v, const in
   a.Hk = Hk;
   const int G = Hq / Hk;
   if (!tmap_rows(&a.q, q, total_q, Hq, HD, (uint64_t)sq * 2, G, CH / G)) return GDN_ERR_CUDA;
-  if (total_k == 0) return GDN_OK;  // (no key tile is ever loaded)
+  if (total_k == 0 || !k) return GDN_OK;  // (no key tile is ever loaded, or pages are)
   if (!tmap_rows(&a.k, k, total_k, Hk, HD, (uint64_t)sk * 2, 1, key_rows) ||
       !tmap_rows(&a.v, v, total_k, Hk, HD, (uint64_t)sv * 2, 1, key_rows))
     return GDN_ERR_CUDA;
@@ -529,6 +503,189 @@ int gdn_attn_fwd(const void* q, const void* k, const void* v, const int* cu_q, c
   a.part_lse = at<float>(ws, p.part_lse);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return cuda_status(p.few ? launch_attn_split(a, s) : launch_attn_fwd(a, s));
+}
+
+// Keys in pages: the argument checks and arguments that the attention over them and the
+// weights of its keys share.
+static int paged_check(int n_seqs, int total_q, int max_k, int n_pages, int page_size, int max_pages, int Hq, int Hk,
+                       int d, const int* cu_q, const int* table, long long table_stride, const int* k_len, float scale,
+                       long long sq, const gdn_page_strides* ks) {
+  int rc = attn_check(n_seqs, total_q, 0, max_k, Hq, Hk, d, cu_q, k_len, scale, sq, (long long)Hk * HD,
+                      (long long)Hk * HD);
+  if (rc || (rc = pages_check(n_pages, page_size))) return rc;
+  if (max_pages < 0 || table_stride < max_pages || (long long)max_pages * page_size > (1LL << 30)) return GDN_ERR_ARG;
+  if (!page_strides_ok(ks)) return GDN_ERR_ARG;
+  if (!aligned(cu_q, 4) || !aligned(table, 4) || !aligned(k_len, 4)) return GDN_ERR_ARG;
+  return GDN_OK;
+}
+
+static PageArgs page_args(int n_pages, int page_size, int max_pages, long long table_stride, int tile) {
+  PageArgs p;
+  p.page = page_size;
+  p.n_pages = n_pages;
+  p.box = tile;
+  while (page_size % p.box != 0) p.box /= 2;  // (16 divides it)
+  p.capacity = n_pages > 0 ? max_pages * page_size : 0;
+  p.table_stride = table_stride;
+  return p;
+}
+
+int gdn_attn_paged(const void* q, const void* k_pages, const void* v_pages, const int* page_table, const int* k_len,
+                   const int* cu_q, void* o, float* lse, int n_seqs, int total_q, int max_k, int n_pages, int page_size,
+                   int max_pages, int Hq, int Hk, int d, float scale, long long q_stride,
+                   const gdn_page_strides* k_strides, const gdn_page_strides* v_strides, long long table_stride,
+                   void* ws, size_t ws_bytes, void* stream) {
+  int rc = paged_check(n_seqs, total_q, max_k, n_pages, page_size, max_pages, Hq, Hk, d, cu_q, page_table, table_stride,
+                       k_len, scale, q_stride, k_strides);
+  if (rc) return rc;
+  if (!page_strides_ok(v_strides)) return GDN_ERR_ARG;
+  const void* ptrs[] = {q, k_pages, v_pages, o, ws};
+  for (const void* p : ptrs)
+    if (p && !aligned(p, 16)) return GDN_ERR_ARG;
+  if (!aligned(lse, 4)) return GDN_ERR_ARG;
+  if (n_seqs == 0 || total_q == 0) return GDN_OK;
+  if (!q || !o || !page_table || !k_len || (n_pages > 0 && (!k_pages || !v_pages))) return GDN_ERR_ARG;
+  const long long capacity = (long long)max_pages * page_size;
+  const AttnPlan p = attn_plan(0, n_seqs, total_q, max_k < capacity ? max_k : (int)capacity, Hq, Hk);
+  if (!workspace_ok(ws, ws_bytes, p.total)) return GDN_ERR_WORKSPACE;
+  AttnArgs a;
+  if ((rc = attn_args(a, q, nullptr, nullptr, cu_q, nullptr, n_seqs, total_q, 0, Hq, Hk, scale, q_stride,
+                      (long long)Hk * HD, (long long)Hk * HD)))
+    return rc;
+  a.table = page_table;
+  a.pages = page_args(n_pages, page_size, max_pages, table_stride, p.few ? CH / 2 : CH);
+  if (!tmap_rows(&a.mo, o, total_q, Hq, HD, (uint64_t)Hq * HD * 2, Hq / Hk, CH / (Hq / Hk))) return GDN_ERR_CUDA;
+  if (n_pages > 0 &&  // (without pages no tile is ever loaded)
+      (!tmap_pages(&a.k, k_pages, n_pages, page_size, Hk, HD, (uint64_t)k_strides->page * 2, (uint64_t)k_strides->row * 2,
+                   (uint64_t)k_strides->head * 2, a.pages.box) ||
+       !tmap_pages(&a.v, v_pages, n_pages, page_size, Hk, HD, (uint64_t)v_strides->page * 2, (uint64_t)v_strides->row * 2,
+                   (uint64_t)v_strides->head * 2, a.pages.box)))
+    return GDN_ERR_CUDA;
+  a.k_len = k_len;
+  a.o = static_cast<bf16*>(o);
+  a.lse = lse;
+  a.status = ws ? at<int>(ws, p.status) : nullptr;
+  a.split_tiles = p.split_tiles;
+  a.n_splits = p.n_splits;
+  a.n_parts = p.n_parts;
+  a.part = at<float>(ws, p.part);
+  a.part_lse = at<float>(ws, p.part_lse);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return cuda_status(p.few ? launch_attn_split(a, s) : launch_attn_fwd(a, s));
+}
+
+// The weights' kernel and its share of the keys.  Few rows to a sequence (one query tile
+// on average): two CTAs to an SM stream the keys of a sequence and head; with fewer such
+// pairs than that the keys are split.  A split's start and end take some 3 us, in which
+// an SM would take in 32 key tiles of 32 KiB: a split has at least 4 tiles.
+static void weigh_plan(WeighArgs& w, int max_k) {
+  const AttnArgs& a = w.at;
+  const long tiles = ((long)max_k + CH - 1) / CH, heads = (long)a.Hk * a.n_seqs;
+  w.few = a.total_q <= (long)a.n_seqs * (CH / (a.Hq / a.Hk));
+  w.key_tiles = tiles > 0 ? (int)tiles : 1;
+  w.n_splits = 1;
+  if (!w.few) return;
+  long splits = (4L * sm_count() + heads - 1) / heads;
+  if (splits > tiles / 4) splits = tiles / 4;
+  if (splits < 1) splits = 1;
+  const long per = (tiles + splits - 1) / splits;
+  w.key_tiles = per > 0 ? (int)per : 1;
+  w.n_splits = (int)(per > 0 ? (tiles + per - 1) / per : 1);
+}
+
+int gdn_attn_paged_weights(const void* q, const void* k_pages, const float* lse, const int* page_table,
+                           const int* k_len, const int* cu_q, float* weights, int n_seqs, int total_q, int max_k,
+                           int n_pages, int page_size, int max_pages, int Hq, int Hk, int d, float scale,
+                           long long q_stride, const gdn_page_strides* k_strides, long long table_stride, void* ws,
+                           size_t ws_bytes, void* stream) {
+  int rc = paged_check(n_seqs, total_q, max_k, n_pages, page_size, max_pages, Hq, Hk, d, cu_q, page_table, table_stride,
+                       k_len, scale, q_stride, k_strides);
+  if (rc) return rc;
+  const void* ptrs[] = {q, k_pages, ws};
+  for (const void* p : ptrs)
+    if (p && !aligned(p, 16)) return GDN_ERR_ARG;
+  if (!aligned(lse, 4) || !aligned(weights, 4)) return GDN_ERR_ARG;
+  if (!workspace_ok(ws, ws_bytes, STATUS_BYTES)) return GDN_ERR_WORKSPACE;
+  if (n_seqs == 0 || total_q == 0 || n_pages == 0 || max_pages == 0) return GDN_OK;
+  if (!q || !k_pages || !lse || !page_table || !k_len || !weights) return GDN_ERR_ARG;
+  WeighArgs w;
+  memset(&w, 0, sizeof w);
+  if ((rc = attn_args(w.at, q, nullptr, nullptr, cu_q, nullptr, n_seqs, total_q, 0, Hq, Hk, scale, q_stride,
+                      (long long)Hk * HD, (long long)Hk * HD)))
+    return rc;
+  w.at.table = page_table;
+  w.at.k_len = k_len;
+  w.at.status = static_cast<int*>(ws);
+  w.at.pages = page_args(n_pages, page_size, max_pages, table_stride, CH);
+  if (!tmap_pages(&w.at.k, k_pages, n_pages, page_size, Hk, HD, (uint64_t)k_strides->page * 2,
+                  (uint64_t)k_strides->row * 2, (uint64_t)k_strides->head * 2, w.at.pages.box))
+    return GDN_ERR_CUDA;
+  w.lse = lse;
+  w.weights = weights;
+  weigh_plan(w, max_k < w.at.pages.capacity ? max_k : w.at.pages.capacity);
+  // (blocks of one launch in one grid dimension; a key tile takes them where they do not suffice)
+  const long long most = (1LL << 30) / ((long long)Hk * n_seqs);
+  if (!w.few && w.key_tiles > most) w.key_tiles = (int)(most > 0 ? most : 1);
+  return cuda_status(launch_weigh(w, static_cast<cudaStream_t>(stream)));
+}
+
+size_t gdn_cache_evict_workspace_bytes(int n_seqs, int max_rows, int budget, int Hk) {
+  if (n_seqs < 0 || max_rows < 0 || budget < 0 || Hk <= 0) return 0;
+  return up((size_t)n_seqs * Hk * (size_t)(budget < max_rows ? budget : max_rows) * sizeof(int));
+}
+
+int gdn_cache_evict(void* k_pages, void* v_pages, float* weights, const int* page_table, const int* to_table,
+                    const int* k_len, int* new_len, int n_seqs, int n_pages, int page_size, int max_pages,
+                    int to_pages, int Hk, int d, int budget, int recent, const gdn_page_strides* k_strides,
+                    const gdn_page_strides* v_strides, long long table_stride, long long to_stride, void* ws,
+                    size_t ws_bytes, void* stream) {
+  int rc;
+  if (n_seqs < 0 || Hk <= 0 || budget < 0 || recent < 0) return GDN_ERR_ARG;
+  if (d != HD) return GDN_ERR_SHAPE;
+  if ((rc = pages_check(n_pages, page_size))) return rc;
+  if (max_pages < 0 || table_stride < max_pages || (long long)max_pages * page_size > (1LL << 30)) return GDN_ERR_ARG;
+  if ((long long)n_seqs * Hk > (1LL << 30)) return GDN_ERR_ARG;
+  if (!page_strides_ok(k_strides) || !page_strides_ok(v_strides)) return GDN_ERR_ARG;
+  const int capacity = max_pages * page_size, keep = budget < capacity ? budget : capacity;
+  if (to_table && (to_pages < 0 || to_stride < to_pages || (long long)to_pages * page_size < keep)) return GDN_ERR_ARG;
+  const void* ptrs[] = {k_pages, v_pages, ws};
+  for (const void* p : ptrs)
+    if (p && !aligned(p, 16)) return GDN_ERR_ARG;
+  if (!aligned(weights, 4) || !aligned(page_table, 4) || !aligned(to_table, 4) || !aligned(k_len, 4) ||
+      !aligned(new_len, 4))
+    return GDN_ERR_ARG;
+  if (n_seqs == 0) return GDN_OK;
+  if (!new_len) return GDN_ERR_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (n_pages == 0 || max_pages == 0) return cuda_status(cudaMemsetAsync(new_len, 0, (size_t)n_seqs * sizeof(int), s));
+  if (!k_pages || !v_pages || !weights || !page_table || !k_len) return GDN_ERR_ARG;
+  const size_t need = gdn_cache_evict_workspace_bytes(n_seqs, capacity, budget, Hk);
+  if (need > 0 && (!ws || ws_bytes < need)) return GDN_ERR_WORKSPACE;
+  EvictArgs a;
+  memset(&a, 0, sizeof a);
+  a.k = static_cast<bf16*>(k_pages);
+  a.v = static_cast<bf16*>(v_pages);
+  a.weights = weights;
+  a.table = page_table;
+  // (the table itself as target, named or not: the copies keep an order)
+  a.to = to_table == page_table ? nullptr : to_table;
+  a.k_len = k_len;
+  a.new_len = new_len;
+  a.list = static_cast<int*>(ws);
+  a.pages = page_args(n_pages, page_size, max_pages, table_stride, PAGE_PIECE);
+  a.to_stride = to_stride;
+  a.sk_page = k_strides->page;
+  a.sk_row = k_strides->row;
+  a.sk_head = k_strides->head;
+  a.sv_page = v_strides->page;
+  a.sv_row = v_strides->row;
+  a.sv_head = v_strides->head;
+  a.n_seqs = n_seqs;
+  a.Hk = Hk;
+  a.budget = budget;
+  a.recent = recent;
+  a.keep = keep;
+  return cuda_status(launch_evict(a, s));
 }
 
 int gdn_attn_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dO,

@@ -100,4 +100,20 @@ inline bool tmap_rows(CUtensorMap* m, const void* base, uint64_t N, int H, int D
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// bf16 pages [n_pages][page][H][D] with any strides (bytes, multiples of 16); box = 64
+// columns of one head over box_rows rows of one page (128-byte swizzle); a page outside
+// reads as zero.
+inline bool tmap_pages(CUtensorMap* m, const void* base, uint64_t n_pages, uint64_t page, int H, int D,
+                       uint64_t page_bytes, uint64_t row_bytes, uint64_t head_bytes, uint32_t box_rows) {
+  auto enc = tmap_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)H, page, n_pages};
+  cuuint64_t strides[3] = {head_bytes, row_bytes, page_bytes};
+  cuuint32_t box[4] = {64, 1, box_rows, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace gdn
