@@ -9,7 +9,7 @@
 // by its digits: weights are mapped to unsigned numbers of the same order, the digits
 // that all share are passed over, and each further digit of 8 bits takes one count over
 // the candidates.  The weights are held in shared memory where they fit.  A last pass in
-// index order writes the list of rows that stay: a warp counts over its own range of
+// index order writes the list of rows that stay (as places in the cache): a warp counts over its own range of
 // keys, a scan over the warps gives each its place.
 //
 // k_evict_move copies the rows of the lists, 16 lanes to a row.  Into other pages any
@@ -51,7 +51,7 @@ __device__ __forceinline__ uint32_t rank_of(float w) {
 }
 
 __global__ void __launch_bounds__(SELECT_THREADS, 1) k_evict_select(const __grid_constant__ EvictArgs a) {
-  extern __shared__ uint32_t held[];
+  extern __shared__ __align__(16) uint32_t held[];
   __shared__ uint32_t hist[256];
   __shared__ uint32_t least, most;
   __shared__ int present[2];          // of the candidates, of the last ones
@@ -64,13 +64,19 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1) k_evict_select(const __grid
   const Cut c = cut_of(a, seq);
   const int* table = a.table + (long)seq * a.pages.table_stride;
   const bool fits = c.old <= SELECT_HELD;
-  // rank of key j (0: on an absent page)
-  auto fetch = [&](int j) -> uint32_t {
-    const int e = table[j / a.pages.page];
-    if ((unsigned)e >= (unsigned)a.pages.n_pages) return 0u;
-    return rank_of(a.weights[((long)e * a.Hk + kh) * a.pages.page + j % a.pages.page]);
+  // ranks of the candidates j .. j + 3 (j a multiple of 4: one page); 0: none, or on an absent page
+  auto fetch = [&](int j) -> uint4 {
+    const int t = j / a.pages.page, e = table[t];
+    if ((unsigned)e >= (unsigned)a.pages.n_pages) return make_uint4(0u, 0u, 0u, 0u);
+    const float4 w = *reinterpret_cast<const float4*>(a.weights + ((long)e * a.Hk + kh) * a.pages.page + (j - t * a.pages.page));
+    return make_uint4(rank_of(w.x), j + 1 < c.old ? rank_of(w.y) : 0u, j + 2 < c.old ? rank_of(w.z) : 0u,
+                      j + 3 < c.old ? rank_of(w.w) : 0u);
   };
-  auto rank = [&](int j) { return fits ? held[j] : fetch(j); };
+  auto single = [&](int j) -> uint32_t {
+    const uint4 r = fetch(j & ~3);
+    return (j & 3) == 0 ? r.x : (j & 3) == 1 ? r.y : (j & 3) == 2 ? r.z : r.w;
+  };
+  auto ranks = [&](int j) { return fits ? *reinterpret_cast<const uint4*>(held + j) : fetch(j); };
 
   if (tid == 0) {
     least = 0xffffffffu;
@@ -80,14 +86,18 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1) k_evict_select(const __grid
   __syncthreads();
   uint32_t lo = 0xffffffffu, hi = 0u;
   int n0 = 0, n1 = 0;
-  for (int j = tid; j < c.old; j += SELECT_THREADS) {
-    const uint32_t r = fetch(j);
-    if (fits) held[j] = r;
-    if (r) {
-      lo = min(lo, r);
-      hi = max(hi, r);
-      ++n0;
-    }
+#pragma unroll 4
+  for (int j = 4 * tid; j < c.old; j += 4 * SELECT_THREADS) {
+    const uint4 r = fetch(j);
+    if (fits) *reinterpret_cast<uint4*>(held + j) = r;
+    const uint32_t x[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (x[i]) {
+        lo = min(lo, x[i]);
+        hi = max(hi, x[i]);
+        ++n0;
+      }
   }
   for (int j = c.old + tid; j < c.kl; j += SELECT_THREADS)
     n1 += (unsigned)table[j / a.pages.page] < (unsigned)a.pages.n_pages;
@@ -105,21 +115,26 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1) k_evict_select(const __grid
   const int take = min(present[0], a.budget - present[1]);  // of the candidates (recent <= budget)
   if (kh == 0 && tid == 0) a.new_len[seq] = take + present[1];
   // The candidates that stay: ranks above `edge`, and the first `ties` of rank `edge`.
-  uint32_t edge = 0u;
+  uint32_t edge = 0u;  // (all of them)
   int ties = 0;
-  if (take > 0 && take < present[0]) {
-    // the digits below the highest one in which candidates differ
-    int shift = 32 - __clz(least ^ most);       // bits that differ
+  if (take == 0) {
+    edge = 0xffffffffu;  // none: no rank is above it, and no number has it
+  } else if (take < present[0]) {
+    // the digits below the highest bit in which candidates differ
+    int shift = 32 - __clz(least ^ most);
     edge = shift < 32 ? most >> shift << shift : 0u;
     ties = take;
     while (shift > 0) {
       const int bits = min(shift, 8), low = shift - bits;
-      for (int i = tid; i < 256; i += SELECT_THREADS) hist[i] = 0u;
+      if (tid < 256) hist[tid] = 0u;
       __syncthreads();
       const uint32_t mask = shift < 32 ? ~0u << shift : 0u;
-      for (int j = tid; j < c.old; j += SELECT_THREADS) {
-        const uint32_t r = rank(j);
-        if (r && (r & mask) == edge) atomicAdd(&hist[r >> low & ((1u << bits) - 1u)], 1u);
+      for (int j = 4 * tid; j < c.old; j += 4 * SELECT_THREADS) {
+        const uint4 r = ranks(j);
+        const uint32_t x[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (x[i] && (x[i] & mask) == edge) atomicAdd(&hist[x[i] >> low & ((1u << bits) - 1u)], 1u);
       }
       __syncthreads();
       // the digit at which the count from the top reaches what is still to take
@@ -146,24 +161,21 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1) k_evict_select(const __grid
       ties -= above;
       shift = low;
     }
-  } else if (take > 0) {
-    edge = 0u;  // all of them
-  } else {
-    edge = 0xffffffffu;  // none (no rank is above it)
   }
 
   // the list, in index order: warp w's range of keys, counted first
   const int per = ((c.kl + SELECT_WARPS - 1) / SELECT_WARPS + 31) & ~31;
   const int j0 = min(warp * per, c.kl), j1 = min(j0 + per, c.kl);
-  auto kind = [&](int j) -> int {  // 1: stays, 2: stays if it is among the first ties
+  auto kind = [&](int j, int e) -> int {  // 1: stays, 2: stays if it is among the first ties
     if (j >= j1) return 0;
-    if (j >= c.old) return (unsigned)table[j / a.pages.page] < (unsigned)a.pages.n_pages ? 1 : 0;
-    const uint32_t r = rank(j);
+    if (j >= c.old) return (unsigned)e < (unsigned)a.pages.n_pages ? 1 : 0;
+    const uint32_t r = fits ? held[j] : single(j);
     return r > edge ? 1 : r == edge && r ? 2 : 0;
   };
   int stay = 0, tied = 0;
+#pragma unroll 4
   for (int j = j0; j < j1; j += 32) {
-    const int k = kind(j + lane);
+    const int k = kind(j + lane, j + lane >= c.old && j + lane < c.kl ? table[(j + lane) / a.pages.page] : 0);
     stay += __popc(__ballot_sync(0xffffffffu, k == 1));
     tied += __popc(__ballot_sync(0xffffffffu, k == 2));
   }
@@ -179,69 +191,76 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1) k_evict_select(const __grid
   }
   out += min(seen, ties);
   int* list = a.list + ((long)seq * a.Hk + kh) * a.keep;
+#pragma unroll 4
   for (int j = j0; j < j1; j += 32) {
-    const int k = kind(j + lane);
+    const int t = min(j + lane, c.kl - 1) / a.pages.page, e = table[t];
+    const int k = kind(j + lane, e);
     const uint32_t below = (1u << lane) - 1u, tie = __ballot_sync(0xffffffffu, k == 2);
     const bool keep = k == 1 || (k == 2 && seen + __popc(tie & below) < ties);
     const uint32_t kept = __ballot_sync(0xffffffffu, keep);
-    if (keep) list[out + __popc(kept & below)] = j + lane;
+    if (keep) list[out + __popc(kept & below)] = e * a.pages.page + (j + lane - t * a.pages.page);
     out += __popc(kept);
     seen += __popc(tie);
   }
 }
 
-// A row's halves of 16 lanes: the places of key j among keys, values and weights.
-struct Place {
-  long k, v, w;
+// Keys, values and weight of row `row` (page * page size + row in it), one lane's share of 16.
+struct Row {
+  uint4 k, v;
+  float w;
+  __device__ __forceinline__ void read(const EvictArgs& a, int kh, int l, int row) {
+    const int e = row / a.pages.page, i = row - e * a.pages.page;
+    k = *reinterpret_cast<const uint4*>(a.k + e * a.sk_page + i * a.sk_row + kh * a.sk_head + 8 * l);
+    v = *reinterpret_cast<const uint4*>(a.v + e * a.sv_page + i * a.sv_row + kh * a.sv_head + 8 * l);
+    w = a.weights[((long)e * a.Hk + kh) * a.pages.page + i];
+  }
+  __device__ __forceinline__ void write(const EvictArgs& a, int kh, int l, int row) const {
+    const int e = row / a.pages.page, i = row - e * a.pages.page;
+    *reinterpret_cast<uint4*>(a.k + e * a.sk_page + i * a.sk_row + kh * a.sk_head + 8 * l) = k;
+    *reinterpret_cast<uint4*>(a.v + e * a.sv_page + i * a.sv_row + kh * a.sv_head + 8 * l) = v;
+    if (l == 0) a.weights[((long)e * a.Hk + kh) * a.pages.page + i] = w;
+  }
 };
-__device__ __forceinline__ bool place_of(const EvictArgs& a, const int* table, int kh, int j, Place& p) {
-  const int t = j / a.pages.page, row = j - t * a.pages.page, e = table[t];
-  if ((unsigned)e >= (unsigned)a.pages.n_pages) return false;
-  p.k = e * a.sk_page + row * a.sk_row + kh * a.sk_head;
-  p.v = e * a.sv_page + row * a.sv_row + kh * a.sv_head;
-  p.w = ((long)e * a.Hk + kh) * a.pages.page + row;
-  return true;
+// Row i of the pages that `table` lists (-1: on an absent page).
+__device__ __forceinline__ int row_at(const EvictArgs& a, const int* table, int i) {
+  const int t = i / a.pages.page, e = table[t];
+  return (unsigned)e < (unsigned)a.pages.n_pages ? e * a.pages.page + (i - t * a.pages.page) : -1;
 }
 
 __global__ void __launch_bounds__(MOVE_THREADS) k_evict_move(const __grid_constant__ EvictArgs a) {
   const int kh = blockIdx.x % a.Hk, seq = blockIdx.x / a.Hk;
-  const int l = threadIdx.x & 15;
+  const int l = threadIdx.x & 15, i0 = threadIdx.x >> 4;
   pdl_wait();
   pdl_release();
   const int n = a.new_len[seq];
-  const int* from = a.table + (long)seq * a.pages.table_stride;
   const int* to = a.to + (long)seq * a.to_stride;
   const int* list = a.list + ((long)seq * a.Hk + kh) * a.keep;
   constexpr int R = MOVE_ROWS / (MOVE_THREADS / 16);
-  for (long base = (long)blockIdx.y * MOVE_ROWS; base < n; base += (long)gridDim.y * MOVE_ROWS) {
-    uint4 k[R], v[R];
-    float w[R];
-    Place d[R];
-    bool ok[R];
+  for (long base = (long)blockIdx.y * MOVE_ROWS; base < a.keep; base += (long)gridDim.y * MOVE_ROWS) {
+    int from[R], dst[R];
+    Row x[R];
+    // (the list, the target's page and the length are asked for at once: what lies behind the length is not used)
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int i = (int)base + (threadIdx.x >> 4) + r * (MOVE_THREADS / 16);
-      Place s;
-      ok[r] = i < n && place_of(a, from, kh, list[i], s) && place_of(a, to, kh, i, d[r]);
-      if (ok[r]) {
-        k[r] = *reinterpret_cast<const uint4*>(a.k + s.k + 8 * l);
-        v[r] = *reinterpret_cast<const uint4*>(a.v + s.v + 8 * l);
-        w[r] = a.weights[s.w];
-      }
+      const int i = min((int)base + i0 + r * (MOVE_THREADS / 16), a.keep - 1);
+      from[r] = list[i];
+      dst[r] = row_at(a, to, i);
+    }
+    if (base >= n) return;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if ((int)base + i0 + r * (MOVE_THREADS / 16) >= n) dst[r] = -1;
+      if (dst[r] >= 0) x[r].read(a, kh, l, from[r]);
     }
 #pragma unroll
     for (int r = 0; r < R; ++r)
-      if (ok[r]) {
-        *reinterpret_cast<uint4*>(a.k + d[r].k + 8 * l) = k[r];
-        *reinterpret_cast<uint4*>(a.v + d[r].v + 8 * l) = v[r];
-        if (l == 0) a.weights[d[r].w] = w[r];
-      }
+      if (dst[r] >= 0) x[r].write(a, kh, l, dst[r]);
   }
 }
 
 __global__ void __launch_bounds__(WALK_THREADS) k_evict_walk(const __grid_constant__ EvictArgs a) {
   const int kh = blockIdx.x % a.Hk, seq = blockIdx.x / a.Hk;
-  const int l = threadIdx.x & 15;
+  const int l = threadIdx.x & 15, i0 = threadIdx.x >> 4;
   pdl_wait();
   pdl_release();
   const int n = a.new_len[seq];
@@ -249,31 +268,23 @@ __global__ void __launch_bounds__(WALK_THREADS) k_evict_walk(const __grid_consta
   const int* list = a.list + ((long)seq * a.Hk + kh) * a.keep;
   constexpr int R = WALK_ROWS / (WALK_THREADS / 16);
   for (int base = 0; base < n; base += WALK_ROWS) {
-    uint4 k[R], v[R];
-    float w[R];
-    Place d[R];
-    bool ok[R];
+    int dst[R];
+    Row x[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int i = base + (threadIdx.x >> 4) + r * (WALK_THREADS / 16);
-      const int j = i < n ? list[i] : 0;
-      Place s;
-      // (a row that stays where it is needs no copy)
-      ok[r] = i < n && j != i && place_of(a, table, kh, j, s) && place_of(a, table, kh, i, d[r]);
-      if (ok[r]) {
-        k[r] = *reinterpret_cast<const uint4*>(a.k + s.k + 8 * l);
-        v[r] = *reinterpret_cast<const uint4*>(a.v + s.v + 8 * l);
-        w[r] = a.weights[s.w];
+      const int i = base + i0 + r * (WALK_THREADS / 16);
+      dst[r] = -1;
+      if (i < n) {
+        const int from = list[i];
+        dst[r] = row_at(a, table, i);
+        if (dst[r] == from) dst[r] = -1;  // it stays where it is
+        if (dst[r] >= 0) x[r].read(a, kh, l, from);
       }
     }
     __syncthreads();  // the round's rows have been read
 #pragma unroll
     for (int r = 0; r < R; ++r)
-      if (ok[r]) {
-        *reinterpret_cast<uint4*>(a.k + d[r].k + 8 * l) = k[r];
-        *reinterpret_cast<uint4*>(a.v + d[r].v + 8 * l) = v[r];
-        if (l == 0) a.weights[d[r].w] = w[r];
-      }
+      if (dst[r] >= 0) x[r].write(a, kh, l, dst[r]);
   }
 }
 
@@ -281,6 +292,7 @@ __global__ void __launch_bounds__(WALK_THREADS) k_evict_walk(const __grid_consta
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s) {
   const unsigned rows = (unsigned)a.n_seqs * (unsigned)a.Hk;
+  // (whole vectors of 4: a capacity is a multiple of 16)
   const size_t smem = sizeof(uint32_t) * (size_t)(a.pages.capacity < SELECT_HELD ? a.pages.capacity : SELECT_HELD);
   cudaError_t e = cudaFuncSetAttribute(k_evict_select, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)(SELECT_HELD * sizeof(uint32_t)));

@@ -237,13 +237,14 @@ struct AttnArgs {
 };
 
 // The weight that attention gives to each key in pages (gdn_weigh.cu).
+constexpr int WEIGH_FEW_ROWS = 64;  // rows of a query tile in the kernel for few of them
 struct WeighArgs {
   AttnArgs at;          // q, k, cu_q, k_len, table and sizes
   const float* lse;     // [total_q][Hq]
   float* weights;       // [n_pages][Hk][page], added to
   int few;              // tokens over caches: the kernel that streams keys
-  int key_tiles;        // many queries: key tiles of a sequence, foreseen; few: key tiles to a split
-  int n_splits;         // few
+  int key_tiles;        // many queries: key tiles of a sequence, foreseen
+  int ctas;             // few
 };
 
 // Eviction of the lightest keys from pages (gdn_evict.cu).
@@ -255,7 +256,7 @@ struct EvictArgs {
   const int* to;        // [n_seqs][..] target pages (null: the sequences' own)
   const int* k_len;
   int* new_len;         // [n_seqs]
-  int* list;            // [n_seqs][Hk][keep] keys that stay
+  int* list;            // [n_seqs][Hk][keep] rows that stay: page * page size + row
   PageArgs pages;       // (box unused)
   long to_stride;       // entries between sequences
   long sk_page, sk_row, sk_head, sv_page, sv_row, sv_head;  // elements
@@ -340,6 +341,7 @@ cudaError_t launch_weigh(const WeighArgs& a, cudaStream_t s);
 // the keys that stay and their lengths, then the copies
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s);
 int rope_tokens(int H);  // tokens that a block takes of a part with H heads
+int rope_resident(int backward);  // blocks to an SM
 cudaError_t launch_rope_fwd(const RopeArgs& a, cudaStream_t s);
 cudaError_t launch_rope_bwd(const RopeArgs& a, cudaStream_t s);
 cudaError_t launch_attn_fwd(const AttnArgs& a, cudaStream_t s);

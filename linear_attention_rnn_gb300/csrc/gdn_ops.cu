@@ -574,25 +574,6 @@ int gdn_attn_paged(const void* q, const void* k_pages, const void* v_pages, cons
   return cuda_status(p.few ? launch_attn_split(a, s) : launch_attn_fwd(a, s));
 }
 
-// The weights' kernel and its share of the keys.  Few rows to a sequence (one query tile
-// on average): two CTAs to an SM stream the keys of a sequence and head; with fewer such
-// pairs than that the keys are split.  A split's start and end take some 3 us, in which
-// an SM would take in 32 key tiles of 32 KiB: a split has at least 4 tiles.
-static void weigh_plan(WeighArgs& w, int max_k) {
-  const AttnArgs& a = w.at;
-  const long tiles = ((long)max_k + CH - 1) / CH, heads = (long)a.Hk * a.n_seqs;
-  w.few = a.total_q <= (long)a.n_seqs * (CH / (a.Hq / a.Hk));
-  w.key_tiles = tiles > 0 ? (int)tiles : 1;
-  w.n_splits = 1;
-  if (!w.few) return;
-  long splits = (4L * sm_count() + heads - 1) / heads;
-  if (splits > tiles / 4) splits = tiles / 4;
-  if (splits < 1) splits = 1;
-  const long per = (tiles + splits - 1) / splits;
-  w.key_tiles = per > 0 ? (int)per : 1;
-  w.n_splits = (int)(per > 0 ? (tiles + per - 1) / per : 1);
-}
-
 int gdn_attn_paged_weights(const void* q, const void* k_pages, const float* lse, const int* page_table,
                            const int* k_len, const int* cu_q, float* weights, int n_seqs, int total_q, int max_k,
                            int n_pages, int page_size, int max_pages, int Hq, int Hk, int d, float scale,
@@ -610,6 +591,9 @@ int gdn_attn_paged_weights(const void* q, const void* k_pages, const float* lse,
   if (!q || !k_pages || !lse || !page_table || !k_len || !weights) return GDN_ERR_ARG;
   WeighArgs w;
   memset(&w, 0, sizeof w);
+  const int G = Hq / Hk;
+  // one query tile of the kernel for few rows to a sequence, on average
+  w.few = G <= WEIGH_FEW_ROWS && total_q <= (long long)n_seqs * (WEIGH_FEW_ROWS / G);
   if ((rc = attn_args(w.at, q, nullptr, nullptr, cu_q, nullptr, n_seqs, total_q, 0, Hq, Hk, scale, q_stride,
                       (long long)Hk * HD, (long long)Hk * HD)))
     return rc;
@@ -622,10 +606,14 @@ int gdn_attn_paged_weights(const void* q, const void* k_pages, const float* lse,
     return GDN_ERR_CUDA;
   w.lse = lse;
   w.weights = weights;
-  weigh_plan(w, max_k < w.at.pages.capacity ? max_k : w.at.pages.capacity);
-  // (blocks of one launch in one grid dimension; a key tile takes them where they do not suffice)
-  const long long most = (1LL << 30) / ((long long)Hk * n_seqs);
-  if (!w.few && w.key_tiles > most) w.key_tiles = (int)(most > 0 ? most : 1);
+  if (w.few && !tmap_rows(&w.at.q, q, total_q, Hq, HD, (uint64_t)q_stride * 2, G, WEIGH_FEW_ROWS / G)) return GDN_ERR_CUDA;
+  w.ctas = 2 * sm_count();
+  // key tiles of the longest sequence, or as many as one grid dimension has blocks for (a
+  // sequence's last block takes the rest)
+  const long long longest = max_k < w.at.pages.capacity ? max_k : w.at.pages.capacity;
+  long long tiles = (longest + CH - 1) / CH;
+  if (tiles > (1LL << 30) / ((long long)Hk * n_seqs)) tiles = (1LL << 30) / ((long long)Hk * n_seqs);
+  w.key_tiles = tiles > 0 ? (int)tiles : 1;
   return cuda_status(launch_weigh(w, static_cast<cudaStream_t>(stream)));
 }
 
@@ -648,10 +636,10 @@ int gdn_cache_evict(void* k_pages, void* v_pages, float* weights, const int* pag
   if (!page_strides_ok(k_strides) || !page_strides_ok(v_strides)) return GDN_ERR_ARG;
   const int capacity = max_pages * page_size, keep = budget < capacity ? budget : capacity;
   if (to_table && (to_pages < 0 || to_stride < to_pages || (long long)to_pages * page_size < keep)) return GDN_ERR_ARG;
-  const void* ptrs[] = {k_pages, v_pages, ws};
+  const void* ptrs[] = {k_pages, v_pages, weights, ws};
   for (const void* p : ptrs)
     if (p && !aligned(p, 16)) return GDN_ERR_ARG;
-  if (!aligned(weights, 4) || !aligned(page_table, 4) || !aligned(to_table, 4) || !aligned(k_len, 4) ||
+  if (!aligned(page_table, 4) || !aligned(to_table, 4) || !aligned(k_len, 4) ||
       !aligned(new_len, 4))
     return GDN_ERR_ARG;
   if (n_seqs == 0) return GDN_OK;

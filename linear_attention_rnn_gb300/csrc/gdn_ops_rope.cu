@@ -55,13 +55,15 @@ RopePart part(const void* x, void* y, const float* w, long long sx, long long sy
   return p;
 }
 
-// Blocks of the backward's two parts: each adds up its share of the weights' gradients,
-// so no more than stay resident, shared out by the parts' rows.
-void backward_blocks(RopePart& q, RopePart& k) {
-  const long most = 4L * sm_count(), all = q.H + k.H;
-  const long nq = (most * q.H + all - 1) / all, nk = (most * k.H + all - 1) / all;
-  if (q.blocks > nq) q.blocks = (int)nq;
-  if (k.blocks > nk) k.blocks = (int)nk;
+// Blocks of the parts: no more than stay resident, shared out by the parts' rows.
+void share_blocks(RopeArgs& a, int parts, int backward) {
+  const long most = (long)rope_resident(backward) * sm_count();
+  long all = 0;
+  for (int i = 0; i < parts; ++i) all += a.part[i].H;
+  for (int i = 0; i < parts; ++i) {
+    const long n = (most * a.part[i].H + all - 1) / all;
+    if (a.part[i].blocks > n) a.part[i].blocks = (int)n;
+  }
 }
 
 }  // namespace
@@ -84,14 +86,17 @@ int gdn_rope_fwd(const void* q, const void* k, const float* q_weight, const floa
   RopeArgs a = rope_args(n, n_pairs, pair_axis, positions, inv_freq, interleaved, eps);
   a.part[0] = part(q, q_out, q_weight, q_stride, qo_stride, Hq, n_pairs, n);
   a.part[1] = part(k, k_out, k_weight, k_stride, ko_stride, Hk, n_pairs, n);
+  share_blocks(a, 2, 0);
   return cuda_status(launch_rope_fwd(a, static_cast<cudaStream_t>(stream)));
 }
 
 size_t gdn_rope_workspace_bytes(int n, int Hq, int Hk, int d) {
   if (rope_check(n, Hq, Hk, d, 1, 0, nullptr, nullptr, nullptr, nullptr, nullptr, 0.f) != GDN_OK) return 0;
-  RopePart q = part(nullptr, nullptr, nullptr, 0, 0, Hq, 0, n), k = part(nullptr, nullptr, nullptr, 0, 0, Hk, 0, n);
-  backward_blocks(q, k);
-  return up((size_t)(q.blocks + k.blocks) * HD * sizeof(float));
+  RopeArgs a;
+  a.part[0] = part(nullptr, nullptr, nullptr, 0, 0, Hq, 0, n);
+  a.part[1] = part(nullptr, nullptr, nullptr, 0, 0, Hk, 0, n);
+  share_blocks(a, 2, 1);
+  return up((size_t)(a.part[0].blocks + a.part[1].blocks) * HD * sizeof(float));
 }
 
 int gdn_rope_bwd(const void* q, const void* k, const float* q_weight, const float* k_weight, const int* positions,
@@ -126,7 +131,7 @@ int gdn_rope_bwd(const void* q, const void* k, const float* q_weight, const floa
   a.part[1].sg = dko_stride;
   a.part[0].dw = dq_weight;
   a.part[1].dw = dk_weight;
-  backward_blocks(a.part[0], a.part[1]);
+  share_blocks(a, 2, 1);
   if (dq_weight || dk_weight) {
     if (!ws || ws_bytes < gdn_rope_workspace_bytes(n, Hq, Hk, d)) return GDN_ERR_WORKSPACE;
     a.partial = static_cast<float*>(ws);
@@ -166,6 +171,7 @@ int gdn_rope_append(const void* q, const void* k, const void* v, const float* q_
   a.part[2].sy_row = v_strides->row;
   a.part[2].sy_head = v_strides->head;
   a.part[1].paged = a.part[2].paged = 1;
+  share_blocks(a, 3, 0);
   return cuda_status(launch_rope_fwd(a, static_cast<cudaStream_t>(stream)));
 }
 

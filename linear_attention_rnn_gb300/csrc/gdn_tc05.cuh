@@ -525,16 +525,18 @@ __device__ __forceinline__ void gemm128x64_by(uint32_t leader, uint32_t tmem_d, 
            idesc_bf16(128, 64), k > 0 ? 1u : 0u);
   }
 }
-// D[128 x N] = A B^T of K-major SW128 tiles of 128 rows each, the first N rows of B (a
-// multiple of 16), by a warp
+// D[128 x N] = A B^T of K-major SW128 tiles of 128 and B_ROWS rows, the first N rows of B
+// (a multiple of 16), by a warp
+template <int B_ROWS>
 __device__ __forceinline__ void gemm128xN_by(uint32_t leader, uint32_t tmem_d, uint32_t a_smem, uint32_t b_smem,
                                              int N) {
   const uint32_t idesc = idesc_bf16(128, N);
   const uint64_t da0 = desc_sw128(a_smem), db0 = desc_sw128(b_smem);
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    const uint32_t kmaj = (uint32_t)(k >> 2) * 128u * 128u + (uint32_t)(k & 3) * 32u;
-    mma_by(leader, tmem_d, da0 + (kmaj >> 4), db0 + (kmaj >> 4), idesc, k > 0 ? 1u : 0u);
+    const uint32_t in = (uint32_t)(k & 3) * 32u, half = (uint32_t)(k >> 2);
+    mma_by(leader, tmem_d, da0 + ((half * 128u * 128u + in) >> 4), db0 + ((half * B_ROWS * 128u + in) >> 4), idesc,
+           k > 0 ? 1u : 0u);
   }
 }
 // 64 of the K-values: A in tensor memory from tmem_a on (32 columns), B from the row

@@ -8,9 +8,10 @@
 // time; the other columns take one fma, one exponential and one addition each, in pairs.
 //
 // Many queries (prompts): a CTA keeps one tile of 128 keys and streams the query tiles
-// that see it through a ring; two groups of four warps take them in turn.
+// that see it through a ring; four groups of four warps take them in turn.
 // Few queries (tokens over caches): a CTA keeps the query tile and streams key tiles;
-// only as many columns are formed as there are rows, two CTAs to an SM.
+// only as many columns are formed as there are rows, two CTAs to an SM, each with an
+// equal run of all sequences' key tiles.
 //
 // A key's sum is formed by one thread in a fixed order and added once to its place
 // (by an atomic addition: sequences that share a page each add theirs).
@@ -26,12 +27,13 @@ using namespace attn;
 
 // What a query tile's columns need: the negative log-sum in base 2, and the last key that
 // the row sees (-1: none, or no row).
+template <int N>
 struct Columns {
-  float nl[CH];
-  int lim[CH];
+  float nl[N];
+  int lim[N];
 };
 
-// Column r of the query tile from token tok0 on.
+// Column r of the query tile of TT tokens from token tok0 on.
 __device__ __forceinline__ void column(const WeighArgs& a, const Seq& sq, int kh, int G, int TT, int tok0, int r,
                                        float& nl, int& lim) {
   const int tok = tok0 + r / G;
@@ -43,7 +45,8 @@ __device__ __forceinline__ void column(const WeighArgs& a, const Seq& sq, int kh
 }
 
 // Sum of the key's exponentials over 32 columns.  All rows see every key up to `clean`.
-__device__ __forceinline__ float sum32(uint32_t S, const Columns& c, int c0, int key, int tile_end, int clean, float sc) {
+template <int N>
+__device__ __forceinline__ float sum32(uint32_t S, const Columns<N>& c, int c0, int key, int tile_end, int clean, float sc) {
   float v[32];
   tc::ld32(S + c0, v);
   float sum[4] = {0.f, 0.f, 0.f, 0.f};
@@ -78,16 +81,16 @@ __device__ __forceinline__ float* place(const WeighArgs& a, const Paged<CH>& pg,
 }
 
 // ---- many queries ----------------------------------------------------------------------
-constexpr int MANY_THREADS = 320, MANY_SLOTS = 5;
+constexpr int MANY_GROUPS = 4, MANY_THREADS = 128 * MANY_GROUPS + 64, MANY_SLOTS = 5;
 
 struct ManySmem {
   unsigned char k[TILE];
   unsigned char slot[MANY_SLOTS][TILE];
-  Columns cols[2];
-  int clean[2][4];  // of 32 columns: the last key that all of their rows see
-  float sums[CH];
+  Columns<CH> cols[MANY_GROUPS];
+  int clean[MANY_GROUPS][4];  // of 32 columns: the last key that all of their rows see
+  float sums[MANY_GROUPS - 1][CH];
   uint64_t full[MANY_SLOTS], empty[MANY_SLOTS];
-  uint64_t barK, barS[4], barE[4];
+  uint64_t barK, barS[MANY_GROUPS], barE[MANY_GROUPS];
   uint32_t tmem;
 };
 
@@ -95,6 +98,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) k_weigh_many(const __grid_con
   extern __shared__ unsigned char raw[];
   ManySmem& sm = *reinterpret_cast<ManySmem*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
   const int tid = threadIdx.x, lane = tid & 31, warp = tc::warp_index();
+  constexpr int ISSUES = 4 * MANY_GROUPS, LOADS = ISSUES + 1, NG = MANY_GROUPS;
   pdl_wait();
   pdl_release();
   clear_status(a.at.status);
@@ -115,13 +119,13 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) k_weigh_many(const __grid_con
   const int tiles = (sq.kl + CH - 1) / CH, tile1 = tile0 == a.key_tiles - 1 ? tiles : min(tile0 + 1, tiles);
   if (tile0 >= tile1 || nq == 0) return;
 
-  if (warp == 9 && lane == 0) {
+  if (warp == LOADS && lane == 0) {
     for (int k = 0; k < MANY_SLOTS; ++k) {
       tc::mbar_init(&sm.full[k], 1);
       tc::mbar_init(&sm.empty[k], 1);
     }
     tc::mbar_init(&sm.barK, 1);
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < NG; ++k) {
       tc::mbar_init(&sm.barS[k], 1);
       tc::mbar_init(&sm.barE[k], 128);
     }
@@ -140,7 +144,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) k_weigh_many(const __grid_con
   int t = 0, done = 0;
   for (int tile = tile0; tile < tile1; ++tile, ++done) {
     const int q0 = first(tile);
-    if (warp == 9) {
+    if (warp == LOADS) {
       // (the sums' barrier at a tile's end orders this load behind the last product of the tile before)
       pg.load(a.at.pages, sm.k, &a.at.k, kh, tile * CH, pg.entry(a.at.pages, tile * CH), &sm.barK);
       if (lane == 0) {
@@ -159,15 +163,15 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) k_weigh_many(const __grid_con
         }
       }
       __syncwarp();
-    } else if (warp == 8) {
+    } else if (warp == ISSUES) {
       const uint32_t lead = tc::elect_leader();
       w.warp_on(&sm.barK, done);
       for (int i = q0; i < nq; ++i, ++t) {
         w.warp_on(&sm.full[t % MANY_SLOTS], t / MANY_SLOTS);
-        if (t >= 4) w.warp_on(&sm.barE[t & 3], t / 4 - 1);
+        if (t >= NG) w.warp_on(&sm.barE[t % NG], t / NG - 1);
         tc::fence_after();
-        tc::gemm128_by<false>(lead, sm.tmem + 128 * (t & 3), smem_u32(sm.k), smem_u32(sm.slot[t % MANY_SLOTS]), false);
-        tc::commit_by(lead, &sm.barS[t & 3]);
+        tc::gemm128_by<false>(lead, sm.tmem + 128 * (t % NG), smem_u32(sm.k), smem_u32(sm.slot[t % MANY_SLOTS]), false);
+        tc::commit_by(lead, &sm.barS[t % NG]);
         if (tile + 1 < tile1 || i + MANY_SLOTS < nq) tc::commit_by(lead, &sm.empty[t % MANY_SLOTS]);
       }
     } else {
@@ -177,10 +181,10 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) k_weigh_many(const __grid_con
       float* at = x == 0 ? place(a, pg, kh, key) : nullptr;
       float sum = 0.f, nl = 0.f;
       int lim = -1;
-      // the group's tiles: those of its parity, counted over the whole CTA
-      int i = q0 + ((t ^ x) & 1);
+      // the group's tiles: every fourth one, counted over the whole CTA
+      int i = q0 + (x + NG - t % NG) % NG;
       if (i < nq) column(a, sq, kh, G, TT, i * TT, r, nl, lim);
-      for (; i < nq; i += 2) {
+      for (; i < nq; i += NG) {
         const int u = t + i - q0;
         // the group's columns: all of its threads have read the ones before
         asm volatile("bar.sync %0, 128;" ::"r"(1 + x) : "memory");
@@ -189,22 +193,25 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) k_weigh_many(const __grid_con
         const int least = __reduce_min_sync(0xffffffffu, lim);
         if (lane == 0) sm.clean[x][warp & 3] = least;
         asm volatile("bar.sync %0, 128;" ::"r"(1 + x) : "memory");
-        if (i + 2 < nq) column(a, sq, kh, G, TT, (i + 2) * TT, r, nl, lim);
-        w.warp_on(&sm.barS[u & 3], u / 4);
+        if (i + NG < nq) column(a, sq, kh, G, TT, (i + NG) * TT, r, nl, lim);
+        w.warp_on(&sm.barS[x], u / NG);
         tc::fence_after();
-        const uint32_t S = sm.tmem + 128 * (u & 3) + lane_base;
+        const uint32_t S = sm.tmem + 128 * x + lane_base;
         float part[4];
 #pragma unroll
         for (int g = 0; g < 4; ++g) part[g] = sum32(S, sm.cols[x], 32 * g, key, tile * CH + CH - 1, sm.clean[x][g], sc);
         tc::fence_before();
-        tc::mbar_arrive(&sm.barE[u & 3]);
+        tc::mbar_arrive(&sm.barE[x]);
         sum += (part[0] + part[1]) + (part[2] + part[3]);
       }
       t += nq - q0;
-      if (x == 1) sm.sums[r] = sum;
-      asm volatile("bar.sync 3, 256;" ::: "memory");
-      sum += x == 0 ? sm.sums[r] : 0.f;
-      if (at && sum != 0.f) atomicAdd(at, sum);
+      if (x > 0) sm.sums[x - 1][r] = sum;
+      asm volatile("bar.sync %0, %1;" ::"n"(1 + NG), "n"(128 * NG) : "memory");
+      if (x == 0) {
+#pragma unroll
+        for (int g = 0; g < NG - 1; ++g) sum += sm.sums[g][r];
+        if (at && sum != 0.f) atomicAdd(at, sum);
+      }
     }
     if (tile + 1 < tile1) __syncthreads();
   }
@@ -216,16 +223,95 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) k_weigh_many(const __grid_con
 }
 
 // ---- few queries -------------------------------------------------------------------------
-constexpr int FEW_THREADS = 192, FEW_SLOTS = 2;
+// A query tile has 64 rows here.  The key tiles of all sequences and heads, one behind
+// another, are cut into equal runs, one to a CTA.
+constexpr int FEW_THREADS = 192, FEW_SLOTS = 2, FEW_ROWS = WEIGH_FEW_ROWS, FEW_S = 4;
+constexpr uint32_t QTILE = FEW_ROWS * HD * 2;
 
 struct FewSmem {
-  unsigned char q[TILE];
+  unsigned char q[2][QTILE];
   unsigned char slot[FEW_SLOTS][TILE];
-  Columns cols;
-  int clean[4];
+  Columns<FEW_ROWS> cols;
+  int clean[FEW_ROWS / 32];
   uint64_t full[FEW_SLOTS], empty[FEW_SLOTS];
-  uint64_t barQ, barS[2], barE[2];
+  uint64_t qfull[2], qempty[2], barS[FEW_S], barE[FEW_S];
   uint32_t tmem;
+};
+
+// A CTA's run over (sequence, head, key tile), which every warp walks by itself: the
+// lengths of 32 sequences lie in its lanes.
+struct Run {
+  const WeighArgs& a;
+  int left;           // units of the run that are left, this one included
+  int s0, lane_ql, lane_q0, lane_kl;
+  int seq, kh, tile, tiles;
+  Seq sq;
+
+  __device__ __forceinline__ int count(int ql, int kl) const { return ql > 0 ? (kl + CH - 1) / CH : 0; }
+  __device__ __forceinline__ void read(int from) {
+    s0 = from;
+    const int s = s0 + (threadIdx.x & 31);
+    lane_ql = lane_q0 = lane_kl = 0;
+    if (s < a.at.n_seqs) {
+      const int2 q = rows_of(a.at.cu_q, s, a.at.n_seqs, a.at.total_q);
+      lane_q0 = q.x;
+      lane_ql = q.y;
+      lane_kl = min(max(a.at.k_len[s], 0), a.at.pages.capacity);
+    }
+  }
+  __device__ __forceinline__ void take() {  // the numbers of sequence `seq`, which lies in the lanes
+    sq.q0 = __shfl_sync(0xffffffffu, lane_q0, seq - s0);
+    sq.ql = __shfl_sync(0xffffffffu, lane_ql, seq - s0);
+    sq.kl = __shfl_sync(0xffffffffu, lane_kl, seq - s0);
+    sq.k0 = 0;
+    tiles = count(sq.ql, sq.kl);
+  }
+  __device__ __forceinline__ explicit Run(const WeighArgs& args) : a(args), left(0) {
+    const int lane = threadIdx.x & 31;
+    long total = 0;
+    for (int s = 0; s < a.at.n_seqs; s += 32) {
+      read(s);
+      total += __reduce_add_sync(0xffffffffu, count(lane_ql, lane_kl));
+    }
+    total *= a.at.Hk;
+    const long lo = total * blockIdx.x / gridDim.x, hi = total * (blockIdx.x + 1) / gridDim.x;
+    left = (int)(hi - lo);
+    if (left == 0) return;
+    long before = 0;  // units ahead of the 32 sequences
+    for (int s = 0; s < a.at.n_seqs; s += 32) {
+      if (s != s0) read(s);
+      const int mine = count(lane_ql, lane_kl);
+      int upto = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, before + (long)upto * a.at.Hk > lo);
+      if (past) {
+        const int l = __ffs((int)past) - 1;
+        seq = s + l;
+        const long start = before + (long)__shfl_sync(0xffffffffu, upto - mine, l) * a.at.Hk;
+        take();
+        kh = (int)((lo - start) / tiles);
+        tile = (int)(lo - start - (long)kh * tiles);
+        return;
+      }
+      before += (long)__shfl_sync(0xffffffffu, upto, 31) * a.at.Hk;
+    }
+  }
+  __device__ __forceinline__ bool last_of_head() const { return left == 1 || tile + 1 == tiles; }
+  __device__ __forceinline__ void next() {
+    if (--left == 0) return;
+    if (++tile < tiles) return;
+    tile = 0;
+    if (++kh < a.at.Hk) return;
+    kh = 0;
+    do {  // (a later sequence has units, since some are left)
+      if (++seq == s0 + 32) read(seq);
+      take();
+    } while (tiles == 0);
+  }
 };
 
 __global__ void __launch_bounds__(FEW_THREADS, 2) k_weigh_few(const __grid_constant__ WeighArgs a) {
@@ -234,32 +320,21 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) k_weigh_few(const __grid_const
   const int tid = threadIdx.x, lane = tid & 31, warp = tc::warp_index();
   pdl_wait();
   pdl_release();
-  if (blockIdx.y == 0) clear_status(a.at.status);
-  const int G = a.at.Hq / a.at.Hk, TT = CH / G;
-  const int kh = blockIdx.x % a.at.Hk, seq = blockIdx.x / a.at.Hk;
-  Seq sq;
-  {
-    const int2 q = rows_of(a.at.cu_q, seq, a.at.n_seqs, a.at.total_q);
-    sq.q0 = q.x;
-    sq.ql = q.y;
-    sq.k0 = 0;
-    sq.kl = min(max(a.at.k_len[seq], 0), a.at.pages.capacity);
-  }
-  const int nq = (sq.ql + TT - 1) / TT, tiles = (sq.kl + CH - 1) / CH;
-  const int tile0 = min((int)blockIdx.y * a.key_tiles, tiles);
-  const int n = (blockIdx.y == gridDim.y - 1 ? tiles : min(tile0 + a.key_tiles, tiles)) - tile0;
-  if (n == 0 || nq == 0) return;
-  const Paged<CH> pg(a.at, seq, sq.kl);
+  clear_status(a.at.status);
+  const int G = a.at.Hq / a.at.Hk, TT = FEW_ROWS / G;
+  Run run(a);
+  if (run.left == 0) return;
 
-  int entry = -1;
-  if (warp == 5) entry = pg.entry(a.at.pages, tile0 * CH);
   if (warp == 5 && lane == 0) {
     for (int k = 0; k < FEW_SLOTS; ++k) {
       tc::mbar_init(&sm.full[k], 1);
       tc::mbar_init(&sm.empty[k], 1);
     }
-    tc::mbar_init(&sm.barQ, 1);
     for (int k = 0; k < 2; ++k) {
+      tc::mbar_init(&sm.qfull[k], 1);
+      tc::mbar_init(&sm.qempty[k], 1);
+    }
+    for (int k = 0; k < FEW_S; ++k) {
       tc::mbar_init(&sm.barS[k], 1);
       tc::mbar_init(&sm.barE[k], 128);
     }
@@ -271,71 +346,109 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) k_weigh_few(const __grid_const
   tc::fence_after();
   tc::Wait w;
 
-  // `t` counts key tiles over all query tiles (mostly one)
-  int t = 0;
-  for (int i = 0; i < nq; ++i) {
-    const int tok0 = i * TT, rows = min(TT, sq.ql - tok0) * G, N = (rows + 15) & ~15;
-    if (warp == 5) {
-      if (lane == 0) load_group(sm.q, &a.at.q, kh, G, sq.q0 + tok0, &sm.barQ);
-      __syncwarp();
-      const int t0 = t;
-      for (; t < t0 + n && w.ok; ++t) {
-        const int key0 = (tile0 + t - t0) * CH;
-        if (t >= FEW_SLOTS) w.on(&sm.empty[t % FEW_SLOTS], t / FEW_SLOTS - 1);
-        w.ok = __all_sync(0xffffffffu, w.ok);
-        if (w.ok) pg.load(a.at.pages, sm.slot[t % FEW_SLOTS], &a.at.k, kh, key0, entry, &sm.full[t % FEW_SLOTS]);
-        // (behind the last tile the next query tile begins with the first)
-        entry = pg.entry(a.at.pages, t + 1 < t0 + n ? key0 + CH : tile0 * CH);
-      }
-      if (lane == 0) {  // no copy is in flight when the CTA ends
-        if (w.ok) {
-          w.on(&sm.barQ, i);
-          for (int u = max(0, t - FEW_SLOTS); u < t; ++u) w.on(&sm.full[u % FEW_SLOTS], u / FEW_SLOTS);
+  // A query tile stays for all key tiles of a head where the sequence has one; else each key
+  // tile goes through all of them.  t counts key tiles, i query tiles, u products.
+  int t = 0, i = 0, u = 0;
+  if (warp == 5) {
+    bool fresh = true;  // the query tile of the head is not there yet
+    for (; run.left > 0 && w.ok; run.next(), ++t) {
+      const int nq = (run.sq.ql + TT - 1) / TT;
+      const Paged<CH> pg(a.at, run.seq, run.sq.kl);
+      const int entry = pg.entry(a.at.pages, run.tile * CH);
+      for (int qt = 0; qt < nq && w.ok; ++qt) {
+        if (nq > 1 || fresh) {
+          if (i >= 2) w.on(&sm.qempty[i & 1], i / 2 - 1);
+          w.ok = __all_sync(0xffffffffu, w.ok);
+          if (w.ok && lane == 0) {
+            tc::arrive_expect_tx(&sm.qfull[i & 1], 2u * 128u * (uint32_t)(TT * G));
+            tc::tma_load_3d(sm.q[i & 1], &a.at.q, 0, run.kh * G, run.sq.q0 + qt * TT, &sm.qfull[i & 1]);
+            tc::tma_load_3d(sm.q[i & 1] + QTILE / 2, &a.at.q, 64, run.kh * G, run.sq.q0 + qt * TT, &sm.qfull[i & 1]);
+          }
+          ++i;
         }
-        if (!w.ok) {
-          tc::mbar_wait_sleep(&sm.barQ, i & 1, 4000000LL);
-          for (int k = 0; k < FEW_SLOTS; ++k) tc::mbar_wait_sleep(&sm.full[k], 0, 4000000LL);
+        if (qt == 0) {
+          if (t >= FEW_SLOTS) w.on(&sm.empty[t % FEW_SLOTS], t / FEW_SLOTS - 1);
+          w.ok = __all_sync(0xffffffffu, w.ok);
+          if (w.ok) pg.load(a.at.pages, sm.slot[t % FEW_SLOTS], &a.at.k, run.kh, run.tile * CH, entry, &sm.full[t % FEW_SLOTS]);
         }
       }
-      __syncwarp();
-    } else if (warp == 4) {
-      const uint32_t lead = tc::elect_leader();
-      w.warp_on(&sm.barQ, i);
-      for (int u = t + n; t < u; ++t) {
-        w.warp_on(&sm.full[t % FEW_SLOTS], t / FEW_SLOTS);
-        if (t >= 2) w.warp_on(&sm.barE[t & 1], t / 2 - 1);
-        tc::fence_after();
-        tc::gemm128xN_by(lead, sm.tmem + 128 * (t & 1), smem_u32(sm.slot[t % FEW_SLOTS]), smem_u32(sm.q), N);
-        tc::commit_by(lead, &sm.barS[t & 1]);
-        if (i + 1 < nq || t + FEW_SLOTS < u) tc::commit_by(lead, &sm.empty[t % FEW_SLOTS]);
+      fresh = run.last_of_head();
+    }
+    if (lane == 0) {  // no copy is in flight when the CTA ends
+      if (w.ok) {
+        for (int k = max(0, i - 2); k < i; ++k) w.on(&sm.qfull[k & 1], k / 2);
+        for (int k = max(0, t - FEW_SLOTS); k < t; ++k) w.on(&sm.full[k % FEW_SLOTS], k / FEW_SLOTS);
       }
-    } else {
-      const int r = tid;
-      const uint32_t lane_base = (uint32_t)(32 * warp) << 16;
-      const float sc = a.at.scale * LOG2E;
-      float nl;
-      int lim;
-      column(a, sq, kh, G, TT, tok0, r, nl, lim);
-      sm.cols.nl[r] = nl;
-      sm.cols.lim[r] = lim;
-      const int least = __reduce_min_sync(0xffffffffu, lim);
-      if (lane == 0) sm.clean[warp] = least;
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-      for (int u = t + n, tile = tile0; t < u; ++t, ++tile) {
-        const int key = tile * CH + r;
-        float* at = place(a, pg, kh, key);
-        w.warp_on(&sm.barS[t & 1], t / 2);
-        tc::fence_after();
-        const uint32_t S = sm.tmem + 128 * (t & 1) + lane_base;
-        float sum = 0.f;
-        // (columns past N hold what earlier products left; no row there sees a key)
-        for (int g = 0; 32 * g < N; ++g) sum += sum32(S, sm.cols, 32 * g, key, tile * CH + CH - 1, sm.clean[g], sc);
-        tc::fence_before();
-        tc::mbar_arrive(&sm.barE[t & 1]);
-        if (at && sum != 0.f) atomicAdd(at, sum);
+      if (!w.ok) {
+        for (int k = 0; k < 2; ++k) tc::mbar_wait_sleep(&sm.qfull[k], 0, 4000000LL);
+        for (int k = 0; k < FEW_SLOTS; ++k) tc::mbar_wait_sleep(&sm.full[k], 0, 4000000LL);
       }
     }
-    if (i + 1 < nq) __syncthreads();  // the query tile and its columns have been read
+    __syncwarp();
+  } else if (warp == 4) {
+    const uint32_t lead = tc::elect_leader();
+    bool fresh = true;
+    for (; run.left > 0; run.next(), ++t) {
+      const int nq = (run.sq.ql + TT - 1) / TT;
+      const bool last = run.last_of_head();
+      for (int qt = 0; qt < nq; ++qt, ++u) {
+        if (nq > 1 || fresh) {
+          w.warp_on(&sm.qfull[i & 1], i / 2);
+          ++i;
+        }
+        if (qt == 0) w.warp_on(&sm.full[t % FEW_SLOTS], t / FEW_SLOTS);
+        if (u >= FEW_S) w.warp_on(&sm.barE[u % FEW_S], u / FEW_S - 1);
+        tc::fence_after();
+        const int N = (min(TT, run.sq.ql - qt * TT) * G + 15) & ~15;
+        tc::gemm128xN_by<FEW_ROWS>(lead, sm.tmem + FEW_ROWS * (u % FEW_S), smem_u32(sm.slot[t % FEW_SLOTS]),
+                                   smem_u32(sm.q[(i - 1) & 1]), N);
+        tc::commit_by(lead, &sm.barS[u % FEW_S]);
+        if (nq > 1 || last) tc::commit_by(lead, &sm.qempty[(i - 1) & 1]);
+        if (qt + 1 == nq) tc::commit_by(lead, &sm.empty[t % FEW_SLOTS]);
+      }
+      fresh = last;
+    }
+    // every commit has arrived before the CTA ends
+    for (int k = max(0, i - 2); k < i; ++k) w.warp_on(&sm.qempty[k & 1], k / 2);
+    for (int k = max(0, t - FEW_SLOTS); k < t; ++k) w.warp_on(&sm.empty[k % FEW_SLOTS], k / FEW_SLOTS);
+  } else {
+    const int r = tid;
+    const uint32_t lane_base = (uint32_t)(32 * warp) << 16;
+    const float sc = a.at.scale * LOG2E;
+    bool fresh = true;
+    for (; run.left > 0; run.next(), ++t) {
+      const int nq = (run.sq.ql + TT - 1) / TT;
+      const Paged<CH> pg(a.at, run.seq, run.sq.kl);
+      const int key = run.tile * CH + r;
+      float* at = place(a, pg, run.kh, key);
+      float sum = 0.f;
+      for (int qt = 0; qt < nq; ++qt, ++u) {
+        const int rows = min(TT, run.sq.ql - qt * TT) * G;
+        if (nq > 1 || fresh) {
+          float nl = 0.f;
+          int lim = -1;
+          if (r < FEW_ROWS) column(a, run.sq, run.kh, G, TT, qt * TT, r, nl, lim);
+          asm volatile("bar.sync 1, 128;" ::: "memory");  // the columns before have been read
+          if (r < FEW_ROWS) {
+            sm.cols.nl[r] = nl;
+            sm.cols.lim[r] = lim;
+            const int least = __reduce_min_sync(0xffffffffu, lim);
+            if (lane == 0) sm.clean[warp] = least;
+          }
+          asm volatile("bar.sync 1, 128;" ::: "memory");
+        }
+        w.warp_on(&sm.barS[u % FEW_S], u / FEW_S);
+        tc::fence_after();
+        const uint32_t S = sm.tmem + FEW_ROWS * (u % FEW_S) + lane_base;
+        // (columns past the product's hold what earlier ones left; no row there sees a key)
+        for (int g = 0; 32 * g < rows; ++g)
+          sum += sum32(S, sm.cols, 32 * g, key, run.tile * CH + CH - 1, sm.clean[g], sc);
+        tc::fence_before();
+        tc::mbar_arrive(&sm.barE[u % FEW_S]);
+      }
+      if (at && sum != 0.f) atomicAdd(at, sum);
+      fresh = run.last_of_head();
+    }
   }
   if (!w.ok && a.at.status) atomicOr(a.at.status, 1);
   tc::fence_before();
@@ -352,8 +465,7 @@ cudaError_t launch_weigh(const WeighArgs& a, cudaStream_t s) {
   static_assert(sizeof(ManySmem) + 1024 <= 227 * 1024 && 2 * (sizeof(FewSmem) + 2048) <= 228 * 1024, "shared memory");
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  const unsigned rows = (unsigned)a.at.Hk * (unsigned)a.at.n_seqs;
-  const dim3 grid = a.few ? dim3(rows, (unsigned)a.n_splits) : dim3(rows * (unsigned)a.key_tiles);
+  const dim3 grid = dim3(a.few ? (unsigned)a.ctas : (unsigned)a.at.Hk * (unsigned)a.at.n_seqs * (unsigned)a.key_tiles);
   return launch_pdl(kernel, grid, dim3(a.few ? FEW_THREADS : MANY_THREADS), smem, s, a);
 }
 
