@@ -407,6 +407,10 @@ def _check_rows(t, name, H, d, n=None):
     tokens."""
     if t.dtype is torch.bfloat16 and t.is_cuda and t.is_contiguous() and t.shape == (n, H, d):
         return H * d  # (the usual case, at a third of what the checks below take)
+    if t.dtype is torch.bfloat16 and t.is_cuda and t.dim() == 3 and t.shape == (n, H, d) and H > 1 < n:
+        st = t.stride()  # (a part of a wider buffer, likewise)
+        if st[2] == 1 and st[1] == d and st[0] >= H * d and not st[0] % 8:
+            return st[0]
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != torch.bfloat16:
@@ -759,11 +763,13 @@ def _pair_axes(pair_axis, n_pairs):
 
 def _rope_dims(q, k, positions, inv_freq, q_weight, k_weight, pair_axis):
     """Rows [n, H, d] or [B, T, H, d]; returns the sizes and the row strides of q and k."""
-    if q.dim() < 3 or k.dim() != q.dim() or q.shape[:-2] != k.shape[:-2] or q.shape[-1] != k.shape[-1]:
-        raise ValueError(f"q and k must be [.., H, d] with equal rows, got {tuple(q.shape)} and {tuple(k.shape)}")
-    Hq, d = q.shape[-2:]
-    Hk = k.shape[-2]
-    n = q.shape[:-2].numel()
+    qs, ks = q.shape, k.shape
+    rows = qs[:-2]
+    if len(qs) < 3 or rows != ks[:-2] or qs[-1] != ks[-1]:
+        raise ValueError(f"q and k must be [.., H, d] with equal rows, got {tuple(qs)} and {tuple(ks)}")
+    Hq, d = qs[-2:]
+    Hk = ks[-2]
+    n = qs[0] if len(qs) == 3 else rows.numel()
     sq, sk = _check_rows(q, "q", Hq, d, n), _check_rows(k, "k", Hk, d, n)
     _check(q_weight, "q_weight", torch.float32, (d,))
     _check(k_weight, "k_weight", torch.float32, (d,))
@@ -776,7 +782,6 @@ def _rope_dims(q, k, positions, inv_freq, q_weight, k_weight, pair_axis):
         if positions is None:
             raise ValueError("inv_freq needs positions")
         _check(positions, "positions", torch.int32)
-        rows = q.shape[:-2]
         if positions.shape != rows:
             if positions.dim() != len(rows) + 1 or positions.shape[1:] != rows or positions.shape[0] < 1:
                 raise ValueError(f"positions has shape {tuple(positions.shape)}, expected {tuple(rows)} "

@@ -133,7 +133,7 @@ struct Paged {
   __device__ __forceinline__ int entry(const PageArgs& p, int key0) const {
     const int lane = threadIdx.x & 31, key = key0 + lane * p.box;
     if (lane >= KEYS / p.box || key >= kl) return -1;
-    const int e = row[key / p.page];
+    const int e = row[p.page_of(key)];
     return (unsigned)e < (unsigned)p.n_pages ? e : -1;
   }
   // by a whole warp
@@ -143,7 +143,7 @@ struct Paged {
     if (lane == 0) tc::arrive_expect_tx(bar, KEYS * HD * 2);
     __syncwarp();
     if (lane < KEYS / p.box) {
-      const int y = (key0 + lane * p.box) % p.page;
+      const int key = key0 + lane * p.box, y = key - p.page_of(key) * p.page;
       unsigned char* d = dst + lane * p.box * 128;
       tc::tma_load_4d(d, m, 0, head, y, entry, bar);
       tc::tma_load_4d(d + KEYS * 128, m, 64, head, y, entry, bar);
@@ -153,7 +153,7 @@ struct Paged {
   // lanes; ask() reads the table, absent() a tile later so that nobody waits for it
   __device__ __forceinline__ int ask(const PageArgs& p, int key0) const {
     const int lane = threadIdx.x & 31, key = key0 + lane * 16;
-    return lane < KEYS / 16 && key < kl ? row[key / p.page] : 0;
+    return lane < KEYS / 16 && key < kl ? row[p.page_of(key)] : 0;
   }
   __device__ __forceinline__ uint32_t absent(const PageArgs& p, int asked) const {
     return __ballot_sync(0xffffffffu, (unsigned)asked >= (unsigned)p.n_pages);

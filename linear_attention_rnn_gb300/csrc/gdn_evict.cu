@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1) k_evict_select(const __grid
   const bool fits = c.old <= SELECT_HELD;
   // ranks of the candidates j .. j + 3 (j a multiple of 4: one page); 0: none, or on an absent page
   auto fetch = [&](int j) -> uint4 {
-    const int t = j / a.pages.page, e = table[t];
+    const int t = a.pages.page_of(j), e = table[t];
     if ((unsigned)e >= (unsigned)a.pages.n_pages) return make_uint4(0u, 0u, 0u, 0u);
     const float4 w = *reinterpret_cast<const float4*>(a.weights + ((long)e * a.Hk + kh) * a.pages.page + (j - t * a.pages.page));
     return make_uint4(rank_of(w.x), j + 1 < c.old ? rank_of(w.y) : 0u, j + 2 < c.old ? rank_of(w.z) : 0u,
@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1) k_evict_select(const __grid
       }
   }
   for (int j = c.old + tid; j < c.kl; j += SELECT_THREADS)
-    n1 += (unsigned)table[j / a.pages.page] < (unsigned)a.pages.n_pages;
+    n1 += (unsigned)table[a.pages.page_of(j)] < (unsigned)a.pages.n_pages;
   lo = __reduce_min_sync(0xffffffffu, lo);
   hi = __reduce_max_sync(0xffffffffu, hi);
   n0 = __reduce_add_sync(0xffffffffu, n0);
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1) k_evict_select(const __grid
   int stay = 0, tied = 0;
 #pragma unroll 4
   for (int j = j0; j < j1; j += 32) {
-    const int k = kind(j + lane, j + lane >= c.old && j + lane < c.kl ? table[(j + lane) / a.pages.page] : 0);
+    const int k = kind(j + lane, j + lane >= c.old && j + lane < c.kl ? table[a.pages.page_of(j + lane)] : 0);
     stay += __popc(__ballot_sync(0xffffffffu, k == 1));
     tied += __popc(__ballot_sync(0xffffffffu, k == 2));
   }
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1) k_evict_select(const __grid
   int* list = a.list + ((long)seq * a.Hk + kh) * a.keep;
 #pragma unroll 4
   for (int j = j0; j < j1; j += 32) {
-    const int t = min(j + lane, c.kl - 1) / a.pages.page, e = table[t];
+    const int t = a.pages.page_of(min(j + lane, c.kl - 1)), e = table[t];
     const int k = kind(j + lane, e);
     const uint32_t below = (1u << lane) - 1u, tie = __ballot_sync(0xffffffffu, k == 2);
     const bool keep = k == 1 || (k == 2 && seen + __popc(tie & below) < ties);
@@ -209,13 +209,13 @@ struct Row {
   uint4 k, v;
   float w;
   __device__ __forceinline__ void read(const EvictArgs& a, int kh, int l, int row) {
-    const int e = row / a.pages.page, i = row - e * a.pages.page;
+    const int e = a.pages.page_of(row), i = row - e * a.pages.page;
     k = *reinterpret_cast<const uint4*>(a.k + e * a.sk_page + i * a.sk_row + kh * a.sk_head + 8 * l);
     v = *reinterpret_cast<const uint4*>(a.v + e * a.sv_page + i * a.sv_row + kh * a.sv_head + 8 * l);
     w = a.weights[((long)e * a.Hk + kh) * a.pages.page + i];
   }
   __device__ __forceinline__ void write(const EvictArgs& a, int kh, int l, int row) const {
-    const int e = row / a.pages.page, i = row - e * a.pages.page;
+    const int e = a.pages.page_of(row), i = row - e * a.pages.page;
     *reinterpret_cast<uint4*>(a.k + e * a.sk_page + i * a.sk_row + kh * a.sk_head + 8 * l) = k;
     *reinterpret_cast<uint4*>(a.v + e * a.sv_page + i * a.sv_row + kh * a.sv_head + 8 * l) = v;
     if (l == 0) a.weights[((long)e * a.Hk + kh) * a.pages.page + i] = w;
@@ -223,11 +223,11 @@ struct Row {
 };
 // Row i of the pages that `table` lists (-1: on an absent page).
 __device__ __forceinline__ int row_at(const EvictArgs& a, const int* table, int i) {
-  const int t = i / a.pages.page, e = table[t];
+  const int t = a.pages.page_of(i), e = table[t];
   return (unsigned)e < (unsigned)a.pages.n_pages ? e * a.pages.page + (i - t * a.pages.page) : -1;
 }
 
-__global__ void __launch_bounds__(MOVE_THREADS) k_evict_move(const __grid_constant__ EvictArgs a) {
+__global__ void __launch_bounds__(MOVE_THREADS, 4) k_evict_move(const __grid_constant__ EvictArgs a) {
   const int kh = blockIdx.x % a.Hk, seq = blockIdx.x / a.Hk;
   const int l = threadIdx.x & 15, i0 = threadIdx.x >> 4;
   pdl_wait();

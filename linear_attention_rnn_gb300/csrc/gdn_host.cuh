@@ -6,6 +6,7 @@
 
 #include "gdn.h"
 #include "gdn_common.cuh"
+#include "gdn_kernels.cuh"
 
 namespace gdn {
 
@@ -42,6 +43,22 @@ inline int pages_check(int n_pages, int page_size) {
   if (n_pages < 0 || page_size <= 0) return GDN_ERR_ARG;
   if (page_size % PAGE_PIECE != 0) return GDN_ERR_SHAPE;
   return (long long)n_pages * page_size <= INT32_MAX ? GDN_OK : GDN_ERR_ARG;  // (rows are counted in 32 bits)
+}
+// Pages whose rows are loaded in boxes of at most `tile` rows (a power of two).
+inline PageArgs page_args(int n_pages, int page_size, int max_pages, long long table_stride, int tile) {
+  PageArgs p;
+  p.page = page_size;
+  p.n_pages = n_pages;
+  p.box = tile;
+  while (page_size % p.box != 0) p.box /= 2;  // (16 divides it)
+  p.capacity = n_pages > 0 ? max_pages * page_size : 0;
+  p.table_stride = table_stride;
+  // division by multiplication with 2^32 (2^shift - page) / page + 1 (Granlund and Montgomery,
+  // "Division by invariant integers using multiplication", 1994)
+  p.shift = 0;
+  while ((1LL << p.shift) < page_size) ++p.shift;
+  p.mul = (uint32_t)((((1ULL << p.shift) - (uint64_t)page_size) << 32) / (uint64_t)page_size + 1);
+  return p;
 }
 // Strides in elements: whole 16-byte pieces, at least a row apart, within what a tensor map holds.
 inline bool page_strides_ok(const gdn_page_strides* s) {

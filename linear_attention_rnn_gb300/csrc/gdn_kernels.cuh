@@ -155,6 +155,18 @@ struct StepArgs {
   int Hk, Hv;
 };
 
+// A cache in pages.
+struct PageArgs {
+  int page, n_pages;  // rows of a page, pages
+  int box;            // rows of a load (divides page and the key tile)
+  int capacity;       // rows that a sequence's part of the table covers
+  long table_stride;  // entries between sequences
+  uint32_t mul, shift; // row / page = (umulhi(mul, row) + row) >> shift for rows below 2^31
+  __device__ __forceinline__ int page_of(int row) const {
+    return (int)((__umulhi(mul, (uint32_t)row) + (uint32_t)row) >> shift);
+  }
+};
+
 // Linear attention with a decay for each head (gdn_decay.cu): one pass of the
 // chunk walk over rows a, b, c with entering state X0.
 struct DecayRole {
@@ -197,14 +209,6 @@ struct DecayFoldArgs {
   int slots;             // segment slots: n_seqs with nseg = 1, else total / (128 seg_chunks) + n_seqs
   int beside;            // the launch before it is the call's walk, which it need not wait for
   int behind;            // the launch before it is the call's walk, which reads the states that it writes
-};
-
-// A cache in pages.
-struct PageArgs {
-  int page, n_pages;  // rows of a page, pages
-  int box;            // rows of a load (divides page and the key tile)
-  int capacity;       // rows that a sequence's part of the table covers
-  long table_stride;  // entries between sequences
 };
 
 // Causal softmax attention over packed sequences (gdn_attn_fwd.cu, gdn_attn_bwd.cu).
@@ -273,17 +277,19 @@ struct RopePart {
   float* dw;            // backward (nullable)
   long sx, sg, sy;      // elements between tokens (paged y: between pages)
   long sy_row, sy_head; // paged y: between a page's rows, between heads
-  int H, turned, paged;
-  int tokens, blocks;   // tokens of a block, blocks of this part
+  int H;                // (v: 0 where there is none; then k's y is not paged either)
 };
 struct RopeArgs {
   RopePart part[3];
   const int* pos;       // [axes][n]
   const float* freq;    // [P]
   const int* slots;     // [n] rows of the cache (paged parts)
-  float* partial;       // [blocks][HD] (backward with weights)
-  long n, cache_rows;
-  int page, P, interleaved;
+  float* partial;       // [blocks][2][HD] (backward with weights)
+  long n;
+  PageArgs pages;       // (paged parts)
+  int cache_rows;
+  int P, axes, interleaved;
+  int blocks, run, longer;  // steps of a warp, warps that take one more
   float eps;
   unsigned char axis[HD / 2];
 };
@@ -340,8 +346,7 @@ cudaError_t launch_decay_fold(const DecayFoldArgs& a, cudaStream_t s);
 cudaError_t launch_weigh(const WeighArgs& a, cudaStream_t s);
 // the keys that stay and their lengths, then the copies
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s);
-int rope_tokens(int H);  // tokens that a block takes of a part with H heads
-int rope_resident(int backward);  // blocks to an SM
+int rope_blocks(int backward, long n, int H, int sms);  // blocks for n tokens of H heads in all
 cudaError_t launch_rope_fwd(const RopeArgs& a, cudaStream_t s);
 cudaError_t launch_rope_bwd(const RopeArgs& a, cudaStream_t s);
 cudaError_t launch_attn_fwd(const AttnArgs& a, cudaStream_t s);

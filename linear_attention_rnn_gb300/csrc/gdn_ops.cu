@@ -519,17 +519,6 @@ static int paged_check(int n_seqs, int total_q, int max_k, int n_pages, int page
   return GDN_OK;
 }
 
-static PageArgs page_args(int n_pages, int page_size, int max_pages, long long table_stride, int tile) {
-  PageArgs p;
-  p.page = page_size;
-  p.n_pages = n_pages;
-  p.box = tile;
-  while (page_size % p.box != 0) p.box /= 2;  // (16 divides it)
-  p.capacity = n_pages > 0 ? max_pages * page_size : 0;
-  p.table_stride = table_stride;
-  return p;
-}
-
 int gdn_attn_paged(const void* q, const void* k_pages, const void* v_pages, const int* page_table, const int* k_len,
                    const int* cu_q, void* o, float* lse, int n_seqs, int total_q, int max_k, int n_pages, int page_size,
                    int max_pages, int Hq, int Hk, int d, float scale, long long q_stride,

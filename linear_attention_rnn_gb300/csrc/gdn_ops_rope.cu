@@ -15,8 +15,7 @@ int rope_check(int n, int Hq, int Hk, int d, int n_axes, int n_pairs, const unsi
   if (n < 0 || Hq <= 0 || Hk <= 0 || n_axes < 1) return GDN_ERR_ARG;
   if (d != HD || n_pairs < 0 || n_pairs > HD / 2 || n_pairs % 8 != 0) return GDN_ERR_SHAPE;
   if (!(eps >= 0.f) || isinf(eps)) return GDN_ERR_ARG;
-  // (offsets of a part's blocks and rows stay within 32 bits)
-  if ((long long)n * (Hq > Hk ? Hq : Hk) > (1LL << 30)) return GDN_ERR_ARG;
+  if ((long long)n * ((long long)Hq + 2LL * Hk + 3) > (1LL << 32)) return GDN_ERR_ARG;  // (steps of four heads in 32 bits)
   if (n_axes > 1 && n_pairs > 0 && !pair_axis) return GDN_ERR_ARG;
   if (pair_axis)
     for (int j = 0; j < n_pairs; ++j)
@@ -26,12 +25,13 @@ int rope_check(int n, int Hq, int Hk, int d, int n_axes, int n_pairs, const unsi
   return GDN_OK;
 }
 
-RopeArgs rope_args(int n, int n_pairs, const unsigned char* pair_axis, const int* pos, const float* freq,
+RopeArgs rope_args(int n, int n_axes, int n_pairs, const unsigned char* pair_axis, const int* pos, const float* freq,
                    int interleaved, float eps) {
   RopeArgs a;
   memset(&a, 0, sizeof a);
   a.n = n;
   a.P = n_pairs;
+  a.axes = n_axes;
   a.pos = pos;
   a.freq = freq;
   a.interleaved = interleaved != 0;
@@ -40,7 +40,7 @@ RopeArgs rope_args(int n, int n_pairs, const unsigned char* pair_axis, const int
   return a;
 }
 
-RopePart part(const void* x, void* y, const float* w, long long sx, long long sy, int H, int n_pairs, int n) {
+RopePart part(const void* x, void* y, const float* w, long long sx, long long sy, int H) {
   RopePart p;
   memset(&p, 0, sizeof p);
   p.x = static_cast<const bf16*>(x);
@@ -49,21 +49,7 @@ RopePart part(const void* x, void* y, const float* w, long long sx, long long sy
   p.sx = sx;
   p.sy = sy;
   p.H = H;
-  p.turned = n_pairs > 0;
-  p.tokens = rope_tokens(H);
-  p.blocks = (n + p.tokens - 1) / p.tokens;
   return p;
-}
-
-// Blocks of the parts: no more than stay resident, shared out by the parts' rows.
-void share_blocks(RopeArgs& a, int parts, int backward) {
-  const long most = (long)rope_resident(backward) * sm_count();
-  long all = 0;
-  for (int i = 0; i < parts; ++i) all += a.part[i].H;
-  for (int i = 0; i < parts; ++i) {
-    const long n = (most * a.part[i].H + all - 1) / all;
-    if (a.part[i].blocks > n) a.part[i].blocks = (int)n;
-  }
 }
 
 }  // namespace
@@ -83,20 +69,16 @@ int gdn_rope_fwd(const void* q, const void* k, const float* q_weight, const floa
   for (const void* p : ptrs)
     if (!aligned(p, 16) || (n > 0 && !p)) return GDN_ERR_ARG;
   if (n == 0) return GDN_OK;
-  RopeArgs a = rope_args(n, n_pairs, pair_axis, positions, inv_freq, interleaved, eps);
-  a.part[0] = part(q, q_out, q_weight, q_stride, qo_stride, Hq, n_pairs, n);
-  a.part[1] = part(k, k_out, k_weight, k_stride, ko_stride, Hk, n_pairs, n);
-  share_blocks(a, 2, 0);
+  RopeArgs a = rope_args(n, n_axes, n_pairs, pair_axis, positions, inv_freq, interleaved, eps);
+  a.part[0] = part(q, q_out, q_weight, q_stride, qo_stride, Hq);
+  a.part[1] = part(k, k_out, k_weight, k_stride, ko_stride, Hk);
+  a.blocks = rope_blocks(0, n, Hq + Hk, sm_count());
   return cuda_status(launch_rope_fwd(a, static_cast<cudaStream_t>(stream)));
 }
 
 size_t gdn_rope_workspace_bytes(int n, int Hq, int Hk, int d) {
   if (rope_check(n, Hq, Hk, d, 1, 0, nullptr, nullptr, nullptr, nullptr, nullptr, 0.f) != GDN_OK) return 0;
-  RopeArgs a;
-  a.part[0] = part(nullptr, nullptr, nullptr, 0, 0, Hq, 0, n);
-  a.part[1] = part(nullptr, nullptr, nullptr, 0, 0, Hk, 0, n);
-  share_blocks(a, 2, 1);
-  return up((size_t)(a.part[0].blocks + a.part[1].blocks) * HD * sizeof(float));
+  return up((size_t)rope_blocks(1, n, Hq + Hk, sm_count()) * 2 * HD * sizeof(float));
 }
 
 int gdn_rope_bwd(const void* q, const void* k, const float* q_weight, const float* k_weight, const int* positions,
@@ -122,16 +104,16 @@ int gdn_rope_bwd(const void* q, const void* k, const float* q_weight, const floa
     if (dq_weight && (rc = cuda_status(cudaMemsetAsync(dq_weight, 0, HD * sizeof(float), s)))) return rc;
     return dk_weight ? cuda_status(cudaMemsetAsync(dk_weight, 0, HD * sizeof(float), s)) : GDN_OK;
   }
-  RopeArgs a = rope_args(n, n_pairs, pair_axis, positions, inv_freq, interleaved, eps);
-  a.part[0] = part(q, dq, q_weight, q_stride, dq_stride, Hq, n_pairs, n);
-  a.part[1] = part(k, dk, k_weight, k_stride, dk_stride, Hk, n_pairs, n);
+  RopeArgs a = rope_args(n, n_axes, n_pairs, pair_axis, positions, inv_freq, interleaved, eps);
+  a.part[0] = part(q, dq, q_weight, q_stride, dq_stride, Hq);
+  a.part[1] = part(k, dk, k_weight, k_stride, dk_stride, Hk);
   a.part[0].g = static_cast<const bf16*>(dq_out);
   a.part[1].g = static_cast<const bf16*>(dk_out);
   a.part[0].sg = dqo_stride;
   a.part[1].sg = dko_stride;
   a.part[0].dw = dq_weight;
   a.part[1].dw = dk_weight;
-  share_blocks(a, 2, 1);
+  a.blocks = rope_blocks(1, n, Hq + Hk, sm_count());
   if (dq_weight || dk_weight) {
     if (!ws || ws_bytes < gdn_rope_workspace_bytes(n, Hq, Hk, d)) return GDN_ERR_WORKSPACE;
     a.partial = static_cast<float*>(ws);
@@ -159,19 +141,18 @@ int gdn_rope_append(const void* q, const void* k, const void* v, const float* q_
     return GDN_ERR_ARG;
   if (!aligned(slots, 4) || (n > 0 && !slots)) return GDN_ERR_ARG;
   if (n == 0) return GDN_OK;
-  RopeArgs a = rope_args(n, n_pairs, pair_axis, positions, inv_freq, interleaved, eps);
+  RopeArgs a = rope_args(n, n_axes, n_pairs, pair_axis, positions, inv_freq, interleaved, eps);
   a.slots = slots;
-  a.page = page_size;
-  a.cache_rows = (long)n_pages * page_size;
-  a.part[0] = part(q, q_out, q_weight, q_stride, qo_stride, Hq, n_pairs, n);
-  a.part[1] = part(k, k_pages, k_weight, k_stride, k_strides->page, Hk, n_pairs, n);
-  a.part[2] = part(v, v_pages, nullptr, v_stride, v_strides->page, Hk, 0, n);
+  a.pages = page_args(n_pages, page_size, 0, 0, PAGE_PIECE);
+  a.cache_rows = n_pages * page_size;
+  a.part[0] = part(q, q_out, q_weight, q_stride, qo_stride, Hq);
+  a.part[1] = part(k, k_pages, k_weight, k_stride, k_strides->page, Hk);
+  a.part[2] = part(v, v_pages, nullptr, v_stride, v_strides->page, Hk);
   a.part[1].sy_row = k_strides->row;
   a.part[1].sy_head = k_strides->head;
   a.part[2].sy_row = v_strides->row;
   a.part[2].sy_head = v_strides->head;
-  a.part[1].paged = a.part[2].paged = 1;
-  share_blocks(a, 3, 0);
+  a.blocks = rope_blocks(0, n, Hq + 2 * Hk, sm_count());
   return cuda_status(launch_rope_fwd(a, static_cast<cudaStream_t>(stream)));
 }
 

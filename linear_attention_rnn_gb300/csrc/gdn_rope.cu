@@ -17,9 +17,9 @@
 //
 // Layout.  Eight lanes hold a head, 16 values each in two 16-byte pieces that hold
 // whole pairs in either order of pairs, so that only the norm's sum crosses lanes.  A
-// block takes the heads of q, of k or of v for some tokens and forms the tokens' cosines
-// and sines once, a token block ahead; as many blocks as stay resident walk over the
-// tokens.
+// warp takes four heads at a time, first those of q, then those of k (then those of v),
+// token by token, forms a token's cosines and sines once, and has three steps' rows on
+// their way.  The warps that stay resident share all steps equally.
 //
 // Bound: HBM.
 #include "gdn_kernels.cuh"
@@ -28,23 +28,24 @@ namespace gdn {
 
 namespace {
 
-constexpr int LANES = 8;                          // to a head
-constexpr int ROPE_THREADS = 256;
-constexpr int GROUPS = ROPE_THREADS / LANES;      // heads side by side
-constexpr int PAIRS = HD / 2;                     // at most
-constexpr int TOKENS = 16;                        // of a block, at most
-constexpr int PER = 2;                            // heads of a group in one round
-constexpr int ROUND = PER * GROUPS;
+constexpr int LANES = 8, SIDE = 32 / LANES;  // to a head; heads side by side in a warp
+constexpr int ROPE_THREADS = 256, WARPS = ROPE_THREADS / 32;
+constexpr int PAIRS = HD / 2;                // at most
+constexpr int AHEAD = 3;                     // steps (of four heads) whose rows are on their way
 
-// Rows on their way: each thread fetches its own pieces rounds ahead and alone reads them,
-// so that no barrier comes between a load and its use.
-template <bool BACK>
-struct Ring {
-  static constexpr int ROUNDS = BACK ? 3 : 3, SRC = BACK ? 2 : 1;
-  uint4 row[ROUNDS][SRC][PER][2][ROPE_THREADS];
-};
+// Cosines and sines of a warp's token, in the order in which the lanes of a head read them:
+// four values of each lane (pairs 8 l ..), then the next four (no two lanes on one bank).
 struct Turns {
   float cos[PAIRS], sin[PAIRS];
+  static __device__ __forceinline__ int at(int j) { return (j >> 2 & 1) * (PAIRS / 2) + (j >> 3) * 4 + (j & 3); }
+};
+// Rows on their way: each lane fetches its own pieces and alone reads them, so that no
+// barrier comes between a load and its use.
+template <bool BACK>
+struct RopeSmem {
+  float w[2][4][LANES][4];  // the weights of q and k, in the lanes' order likewise
+  Turns turns[WARPS];
+  uint4 row[WARPS][AHEAD + 1][BACK ? 2 : 1][2][32];
 };
 
 __device__ __forceinline__ void fetch16(void* dst, const void* src) {
@@ -56,57 +57,105 @@ __device__ __forceinline__ void fetch_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A thread's share of a block's angles: pair tid % 64 of every fourth token.  The
-// positions are read a block ahead.
+// A frequency as the fraction of a turn that a position adds, in 2^-64 of a turn: the 24
+// bits of its significand times 2^64 / (2 pi), shifted by its exponent.
+__device__ __forceinline__ unsigned long long turn_step(float f) {
+  constexpr unsigned long long PER_RADIAN = 0x28BE60DB9391054Aull;  // 2^64 / (2 pi)
+  const uint32_t u = __float_as_uint(f), e = u >> 23 & 255u;
+  const unsigned long long m = e ? (u & 0x7fffffu) | 0x800000u : (u & 0x7fffffu);
+  const unsigned long long lo = m * PER_RADIAN, hi = __umul64hi(m, PER_RADIAN);
+  const int right = 150 - (int)(e ? e : 1u);  // the value is m 2^-right
+  unsigned long long r;
+  if (right <= 0)
+    r = right > -64 ? lo << -right : 0ull;
+  else if (right < 64)
+    r = lo >> right | hi << (64 - right);
+  else
+    r = right < 128 ? hi >> (right - 64) : 0ull;
+  return u >> 31 ? 0ull - r : r;
+}
+
+// A lane's two pairs of its warp's token: lane and lane + 32.
 struct Angles {
-  static constexpr int N = TOKENS * PAIRS / ROPE_THREADS;
-  unsigned long long step;  // a position's step, in 2^-64 of a turn
-  const int* pos;
-  int at[N];
-  __device__ __forceinline__ Angles(const RopeArgs& a) {
-    const int j = threadIdx.x & (PAIRS - 1);
-    pos = nullptr;
-    step = 0;
-    if (j >= a.P) return;
-    double turns = (double)a.freq[j] * 0.15915494309189535;  // 1 / (2 pi)
-    turns -= floor(turns);
-    step = (unsigned long long)(turns * 18446744073709551616.0);
-    pos = a.pos + (long)a.axis[j] * a.n;
-  }
-  __device__ __forceinline__ void read(const RopeArgs& a, long t0, int tokens) {
+  unsigned long long step[2];
+  const int* pos[2];
+  int at[2];  // their positions for the next token
+  __device__ __forceinline__ explicit Angles(const RopeArgs& a) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int t = threadIdx.x / PAIRS + i * (ROPE_THREADS / PAIRS);
-      at[i] = pos && t < tokens && t0 + t < a.n ? pos[t0 + t] : 0;
+    for (int i = 0; i < 2; ++i) {
+      const int j = (threadIdx.x & 31) + 32 * i;
+      pos[i] = j < a.P ? a.pos + (a.axes > 1 ? (long)a.axis[j] * a.n : 0) : nullptr;
+      step[i] = j < a.P ? turn_step(a.freq[j]) : 0ull;
+      at[i] = 0;
     }
   }
-  __device__ __forceinline__ void form(Turns* to, int tokens) const {
-    if (!pos) return;
-    const int j = threadIdx.x & (PAIRS - 1);
+  __device__ __forceinline__ void read(int t) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int t = threadIdx.x / PAIRS + i * (ROPE_THREADS / PAIRS);
-      if (t >= tokens) break;
-      const unsigned long long turn = step * (unsigned long long)(long long)at[i];
-      sincospif((float)(int)(turn >> 32) * 0x1p-31f, &to[t].sin[j], &to[t].cos[j]);
+    for (int i = 0; i < 2; ++i)
+      if (pos[i]) at[i] = pos[i][t];
+  }
+  __device__ __forceinline__ void form(Turns& to) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int j = (threadIdx.x & 31) + 32 * i;
+      const unsigned long long turn = step[i] * (unsigned long long)(long long)at[i];
+      sincospif((float)(int)(turn >> 32) * 0x1p-31f, &to.sin[Turns::at(j)], &to.cos[Turns::at(j)]);
     }
   }
 };
 
-__device__ __forceinline__ void unpack16(const uint4 (&u)[2], float (&x)[16]) {
+// Two fp32 values, for the instructions that work on pairs.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 pair(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 parts(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
+// a head's 16 values of a lane, piece by piece
+__device__ __forceinline__ void unpack16(const uint4 (&u)[2], F2 (&x)[8]) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const uint32_t w[4] = {u[h].x, u[h].y, u[h].z, u[h].w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = unpack_bf16(w[i]);
-      x[8 * h + 2 * i] = f.x;
-      x[8 * h + 2 * i + 1] = f.y;
-    }
+    for (int i = 0; i < 4; ++i) x[4 * h + i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
   }
 }
-__device__ __forceinline__ uint4 pack8(const float* x) {
-  return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+__device__ __forceinline__ uint4 pack8(const F2* x) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = parts(x[i]);
+    w[i] = pack_bf16(f.x, f.y);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ float dot(const F2 (&x)[8], const F2 (&y)[8]) {
+  F2 s = x[0] * y[0], t = x[1] * y[1];
+#pragma unroll
+  for (int i = 2; i < 8; i += 2) {
+    s = fma(x[i], y[i], s);
+    t = fma(x[i + 1], y[i + 1], t);
+  }
+  const float2 a = parts(s), b = parts(t);
+  return (a.x + a.y) + (b.x + b.y);
 }
 
 // Where lane `l` of a head's eight finds its two pieces: pairs 8 l .. 8 l + 7, or
@@ -122,26 +171,32 @@ __device__ __forceinline__ void pieces(const RopeArgs& a, int l, int& p0, int& p
 }
 
 // The lane's pairs turned by the token's angles (back: by the opposite ones).
-template <bool BACK>
-__device__ __forceinline__ void turn(const RopeArgs& a, const Turns& s, int l, float (&x)[16]) {
+template <bool BACK, bool INTER>
+__device__ __forceinline__ void turn(const RopeArgs& a, const Turns& s, int l, F2 (&x)[8]) {
   if (8 * l >= a.P) return;
-  float c[8], d[8];
+  F2 c[4], d[4];  // of two pairs each
 #pragma unroll
-  for (int i = 0; i < 8; i += 4) {
-    *reinterpret_cast<float4*>(c + i) = *reinterpret_cast<const float4*>(&s.cos[8 * l + i]);
-    *reinterpret_cast<float4*>(d + i) = *reinterpret_cast<const float4*>(&s.sin[8 * l + i]);
+  for (int i = 0; i < 2; ++i) {
+    const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(&s.cos[4 * l + (PAIRS / 2) * i]);
+    const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(&s.sin[4 * l + (PAIRS / 2) * i]);
+    c[2 * i].v = u.x, c[2 * i + 1].v = u.y;
+    d[2 * i].v = v.x, d[2 * i + 1].v = v.y;
   }
+  const F2 minus = pair(-1.f, -1.f);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float sn = BACK ? -d[i] : d[i];
-    if (a.interleaved) {
-      const float p = x[2 * i], q = x[2 * i + 1];
-      x[2 * i] = p * c[i] - q * sn;
-      x[2 * i + 1] = q * c[i] + p * sn;
+  for (int i = 0; i < 4; ++i) {
+    if (INTER) {
+      const float2 cc = parts(c[i]), ss = parts(d[i]);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float cs = k ? cc.y : cc.x, sn = BACK ? -(k ? ss.y : ss.x) : (k ? ss.y : ss.x);
+        const float2 v = parts(x[2 * i + k]);
+        x[2 * i + k] = fma(pair(v.y, v.x), pair(-sn, sn), x[2 * i + k] * pair(cs, cs));
+      }
     } else {
-      const float p = x[i], q = x[8 + i];
-      x[i] = p * c[i] - q * sn;
-      x[8 + i] = q * c[i] + p * sn;
+      const F2 p = x[i], q = x[4 + i];
+      x[i] = fma(BACK ? q : q * minus, d[i], p * c[i]);
+      x[4 + i] = fma(BACK ? p * minus : p, d[i], q * c[i]);
     }
   }
 }
@@ -153,189 +208,211 @@ __device__ __forceinline__ float head_sum(float v) {
   return v;
 }
 
-// The block's part: its rows (q, k or v) and its place among the blocks of that part.
-__device__ __forceinline__ int part_of(const RopeArgs& a, int& block) {
-  block = blockIdx.x;
-  int r = 0;
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    if (r == i && block >= a.part[i].blocks) {
-      block -= a.part[i].blocks;
-      r = i + 1;
-    }
-  return r;
-}
-
-// A block walks token blocks t0 = tokens * (block, block + blocks, ..) of its part, each
-// in rounds of 64 heads, eight lanes to a head and two heads to a group of lanes.
-template <bool BACK>
+// A step is four heads of a token, side by side: those of q, then those of k (then those
+// of v).  Every warp walks an equal run of all tokens' steps.
+template <bool BACK, bool INTER, bool PAGED>
 __global__ void __launch_bounds__(ROPE_THREADS, BACK ? 2 : 3) k_rope(const __grid_constant__ RopeArgs a) {
   extern __shared__ __align__(16) unsigned char raw[];
-  Ring<BACK>& ring = *reinterpret_cast<Ring<BACK>*>(raw);
-  Turns* turns = reinterpret_cast<Turns*>(raw + sizeof(Ring<BACK>));  // [2][tokens]
-  constexpr int ROUNDS = Ring<BACK>::ROUNDS;
-  int block;
-  const RopePart& p = a.part[part_of(a, block)];
-  const int tid = threadIdx.x, l = tid & (LANES - 1), group = tid / LANES;
+  RopeSmem<BACK>& sm = *reinterpret_cast<RopeSmem<BACK>*>(raw);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, l = lane & (LANES - 1), side = lane / LANES;
   pdl_wait();
   pdl_release();
+  const RopePart &q = a.part[0], &k = a.part[1], &v = a.part[2];
+  const int Hqk = q.H + k.H, H = PAGED ? Hqk + v.H : Hqk, steps = (H + SIDE - 1) / SIDE;
+  const int me = (int)blockIdx.x * WARPS + warp, count = a.run + (me < a.longer ? 1 : 0);
+  const unsigned first = (unsigned)me * (unsigned)a.run + (unsigned)min(me, a.longer);
   int c0, c1;
   pieces(a, l, c0, c1);
-  const long step = (long)p.blocks * p.tokens;
-  const int H = p.H, most = p.tokens * H;
+  const int hop = c1 - c0;
+  const int t0 = (int)(first / (unsigned)steps), i0 = (int)(first - (unsigned)t0 * (unsigned)steps);
 
-  // the rounds ahead: token block f0, its round from head f_i on
-  long f0 = (long)block * p.tokens;
-  int fi = 0, fslot = 0;
+  // the rows ahead: the lane's place in the token's rows of q and of k (and of v), as if
+  // each had all heads
+  const int at = side * HD + c0;
+  const bf16* qx = q.x + (t0 * q.sx + at);
+  const bf16* kx = k.x + (t0 * k.sx + at - q.H * HD);
+  const bf16* vx = PAGED ? v.x + (t0 * v.sx + at - Hqk * HD) : nullptr;
+  const bf16* qg = BACK ? q.g + (t0 * q.sg + at) : nullptr;
+  const bf16* kg = BACK ? k.g + (t0 * k.sg + at - q.H * HD) : nullptr;
+  const bool normed = q.w || k.w;
+  int fi = i0, fleft = count, fslot = 0;
   auto fetch = [&] {
-    if (f0 < a.n) {
-      const int rows = (int)min((long)p.tokens, a.n - f0) * H;
-#pragma unroll
-      for (int u = 0; u < PER; ++u) {
-        const int i = fi + group + u * GROUPS;
-        if (i < rows) {
-          const int t = i / H, h = i - t * H;
-          if (!BACK || p.w) {
-            const bf16* x = p.x + (f0 + t) * p.sx + h * HD;
-            fetch16(&ring.row[fslot][0][u][0][tid], x + c0);
-            fetch16(&ring.row[fslot][0][u][1][tid], x + c1);
-          }
-          if (BACK) {
-            const bf16* g = p.g + (f0 + t) * p.sg + h * HD;
-            fetch16(&ring.row[fslot][Ring<BACK>::SRC - 1][u][0][tid], g + c0);
-            fetch16(&ring.row[fslot][Ring<BACK>::SRC - 1][u][1][tid], g + c1);
-          }
+    if (fleft > 0) {
+      const int h = SIDE * fi + side, off = fi * (SIDE * HD);
+      if (h < H) {
+        if (!BACK || normed) {
+          const bf16* x = (h < q.H ? qx : !PAGED || h < Hqk ? kx : vx) + off;
+          fetch16(&sm.row[warp][fslot][0][0][lane], x);
+          fetch16(&sm.row[warp][fslot][0][1][lane], x + hop);
+        }
+        if (BACK) {
+          const bf16* g = (h < q.H ? qg : kg) + off;
+          fetch16(&sm.row[warp][fslot][BACK][0][lane], g);
+          fetch16(&sm.row[warp][fslot][BACK][1][lane], g + hop);
         }
       }
-      fi += ROUND;
-      if (fi >= most) {
+      --fleft;
+      if (++fi == steps) {
         fi = 0;
-        f0 += step;
+        qx += q.sx;
+        kx += k.sx;
+        if (PAGED) vx += v.sx;
+        if (BACK) {
+          qg += q.sg;
+          kg += k.sg;
+        }
       }
-      fslot = fslot + 1 == ROUNDS ? 0 : fslot + 1;
+      fslot = (fslot + 1) & AHEAD;
     }
     fetch_commit();
   };
+  static_assert((AHEAD & (AHEAD + 1)) == 0, "slots in turn");
 #pragma unroll
-  for (int k = 0; k < ROUNDS - 1; ++k) fetch();
+  for (int u = 0; u < AHEAD; ++u) fetch();
 
-  float w[16], dw[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) w[i] = 1.f, dw[i] = 0.f;
-  if (p.w) {
-#pragma unroll
-    for (int i = 0; i < 8; i += 4) {
-      *reinterpret_cast<float4*>(w + i) = *reinterpret_cast<const float4*>(p.w + c0 + i);
-      *reinterpret_cast<float4*>(w + 8 + i) = *reinterpret_cast<const float4*>(p.w + c1 + i);
-    }
+  for (int e = warp; e < 32; e += WARPS) {  // four of a lane's values at a time
+    const float* w = a.part[e / 16].w;
+    const int piece = e / 4 % 4, from = (piece < 2 ? c0 : c1) + 4 * (piece & 1) + (e & 3);
+    if (lane < LANES) sm.w[e / 16][piece][lane][e & 3] = w ? w[from] : 1.f;
   }
   Angles angles(a);
-  const long first = (long)block * p.tokens;
-  int buf = 0, slot = 0;
-  if (p.turned) {
-    angles.read(a, first, p.tokens);
-    angles.form(turns, p.tokens);
-    angles.read(a, first + step, p.tokens);
+  int row = 0;  // of the next token in the cache
+  if (count > 0) {
+    angles.read(t0);
+    if (PAGED) row = a.slots[t0];
   }
-  for (long t0 = first; t0 < a.n; t0 += step) {
-    const int rows = (int)min((long)p.tokens, a.n - t0) * H;
-    if (p.turned) {
-      __syncthreads();  // this block's turns are there, the last block's have been read
-      if (t0 + step < a.n) angles.form(turns + (buf ^ 1) * p.tokens, p.tokens);
-      angles.read(a, t0 + 2 * step, p.tokens);
-    }
-    for (int i0 = 0; i0 < most; i0 += ROUND) {
-      fetch();
-      fetch_wait<ROUNDS - 1>();
+  F2 dq[8], dk[8];
 #pragma unroll
-      for (int u = 0; u < PER; ++u) {
-        const int i = i0 + group + u * GROUPS, t = i / H, h = i - t * H;
-        const bool own = i < rows;  // (the lanes of a head agree; others go along for the sums)
-        if (!__any_sync(0xffffffffu, own)) break;
-        const Turns& turn_of = turns[buf * p.tokens + (own ? t : 0)];
-        uint4 v[2] = {ring.row[slot][0][u][0][tid], ring.row[slot][0][u][1][tid]};
-        float x[16], y[16];
-        if (!BACK) {
-          if (p.turned || p.w) {
-            unpack16(v, x);
-            if (p.w) {
-              float ss = 0.f;
-#pragma unroll
-              for (int j = 0; j < 16; ++j) ss += x[j] * x[j];
-              const float r = rsqrtf(head_sum(ss) * (1.f / HD) + a.eps);
-#pragma unroll
-              for (int j = 0; j < 16; ++j) x[j] *= r * w[j];
-            }
-            if (p.turned) turn<false>(a, turn_of, l, x);
-            v[0] = pack8(x);
-            v[1] = pack8(x + 8);
-          }
-        } else {
-          const uint4 g[2] = {ring.row[slot][Ring<BACK>::SRC - 1][u][0][tid], ring.row[slot][Ring<BACK>::SRC - 1][u][1][tid]};
-          unpack16(g, y);
-          if (p.turned) turn<true>(a, turn_of, l, y);
-          if (p.w) {
-            unpack16(v, x);
-            float ss = 0.f;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) ss += x[j] * x[j];
-            const float r = rsqrtf(head_sum(ss) * (1.f / HD) + a.eps);
-            float gu = 0.f;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              x[j] *= r;
-              if (own) dw[j] += y[j] * x[j];
-              y[j] *= w[j];
-              gu += y[j] * x[j];
-            }
-            gu = head_sum(gu) * (1.f / HD);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) y[j] = r * (y[j] - x[j] * gu);
-          }
-          v[0] = pack8(y);
-          v[1] = pack8(y + 8);
-        }
-        if (!own) continue;
-        bf16* dst;
-        if (!BACK && p.paged) {
-          const long row = a.slots[t0 + t];
-          if (row < 0 || row >= a.cache_rows) continue;  // a padded token of the batch
-          const long page = row / a.page;
-          dst = p.y + page * p.sy + (row - page * a.page) * p.sy_row + h * p.sy_head;
-        } else {
-          dst = p.y + (t0 + t) * p.sy + h * HD;
-        }
-        *reinterpret_cast<uint4*>(dst + c0) = v[0];
-        *reinterpret_cast<uint4*>(dst + c1) = v[1];
+  for (int j = 0; j < 8; ++j) dq[j] = dk[j] = pair(0.f, 0.f);
+  __syncthreads();
+
+  int t = t0, slot = 0, i = i0;
+  bf16* qy = q.y + (t0 * q.sy + at);
+  bf16* ky = PAGED ? nullptr : k.y + (t0 * k.sy + at - q.H * HD);
+  bf16* vy = nullptr;
+  bool placed = !PAGED;  // (paged: the token has a row)
+  Turns& turns = sm.turns[warp];
+  for (int u = 0; u < count; ++u) {
+    fetch();
+    if (u == 0 || i == steps) {  // a new token
+      if (u > 0) {
+        i = 0;
+        ++t;
+        qy += q.sy;
+        if (!PAGED) ky += k.sy;
       }
-      slot = slot + 1 == ROUNDS ? 0 : slot + 1;
+      __syncwarp();  // (the last one's turns have been read)
+      if (a.P > 0) angles.form(turns);
+      if (PAGED) {
+        placed = row >= 0 && row < a.cache_rows;  // (else a padded token of the batch)
+        const int page = placed ? a.pages.page_of(row) : 0;
+        const long in = row - page * a.pages.page;
+        ky = k.y + (page * k.sy + in * k.sy_row + side * k.sy_head + c0);
+        vy = v.y + (page * v.sy + in * v.sy_row + side * v.sy_head + c0);
+      }
+      if (t + 1 < a.n) {
+        angles.read(t + 1);
+        if (PAGED) row = a.slots[t + 1];
+      }
+      __syncwarp();
     }
-    buf ^= 1;
+    fetch_wait<AHEAD>();
+    const int h = SIDE * i + side;
+    const bool own = h < H, is_k = h >= q.H;
+    const uint4* from = &sm.row[warp][slot][0][0][lane];
+    uint4 o[2] = {from[0], from[32]};
+    F2 x[8], y[8];
+    if (!BACK) {
+      if (!PAGED || h < Hqk) {
+        unpack16(o, x);
+        if (normed) {
+          float r = rsqrtf(head_sum(dot(x, x)) * (1.f / HD) + a.eps);
+          if (!(is_k ? k.w : q.w)) r = 1.f;
+          const F2 rr = pair(r, r);
+#pragma unroll
+          for (int j = 0; j < 8; j += 2) {
+            const ulonglong2 ww = *reinterpret_cast<const ulonglong2*>(sm.w[is_k][j / 2][l]);
+            x[j] = x[j] * (rr * F2{ww.x});
+            x[j + 1] = x[j + 1] * (rr * F2{ww.y});
+          }
+        }
+        turn<false, INTER>(a, turns, l, x);
+        o[0] = pack8(x);
+        o[1] = pack8(x + 4);
+      }
+    } else {
+      const uint4 g[2] = {from[64], from[96]};
+      unpack16(g, y);
+      turn<true, INTER>(a, turns, l, y);
+      if (normed) {
+        unpack16(o, x);
+        const float r = rsqrtf(head_sum(dot(x, x)) * (1.f / HD) + a.eps);
+        const F2 rr = pair(r, r);
+        F2 gx[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = x[j] * rr;
+        if (own && !is_k) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) dq[j] = fma(y[j], x[j], dq[j]);
+        } else if (own) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) dk[j] = fma(y[j], x[j], dk[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          const ulonglong2 ww = *reinterpret_cast<const ulonglong2*>(sm.w[is_k][j / 2][l]);
+          gx[j] = y[j] * F2{ww.x};
+          gx[j + 1] = y[j + 1] * F2{ww.y};
+        }
+        // r (g - u mean(g u))
+        const float gu = -r * (head_sum(dot(gx, x)) * (1.f / HD));
+        const F2 mean = pair(gu, gu);
+        if (is_k ? k.w : q.w) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) y[j] = fma(x[j], mean, gx[j] * rr);
+        }
+      }
+      o[0] = pack8(y);
+      o[1] = pack8(y + 4);
+    }
+    bf16* dst;
+    if (!PAGED || !is_k)
+      dst = (is_k ? ky : qy) + i * (SIDE * HD);
+    else if (h < Hqk)
+      dst = ky + (SIDE * i - q.H) * k.sy_head;
+    else
+      dst = vy + (SIDE * i - Hqk) * v.sy_head;
+    if (own && (placed || !is_k)) {
+      *reinterpret_cast<uint4*>(dst) = o[0];
+      *reinterpret_cast<uint4*>(dst + hop) = o[1];
+    }
+    slot = (slot + 1) & AHEAD;
+    ++i;
   }
   if constexpr (BACK) {
-  if (!p.dw) return;
-  // the block's sum of dw: over the warp's four heads, then over the warps
+    if (!q.dw && !k.dw) return;
+    // the block's sums: over the warp's four heads, then over the warps
+    __syncthreads();
+    float* red = reinterpret_cast<float*>(&sm.row[0][0][0][0][0]);  // [warps][2][HD]
+    static_assert(sizeof(sm.row) >= WARPS * 2 * HD * sizeof(float), "room for the sums");
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    dw[j] += __shfl_xor_sync(0xffffffffu, dw[j], 8);
-    dw[j] += __shfl_xor_sync(0xffffffffu, dw[j], 16);
-  }
-  __syncthreads();
-  float* red = reinterpret_cast<float*>(raw);  // [warps][HD]
-  if ((tid & 31) < LANES) {
+    for (int w = 0; w < 2; ++w) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      red[(tid >> 5) * HD + c0 + j] = dw[j];
-      red[(tid >> 5) * HD + c1 + j] = dw[8 + j];
+      for (int j = 0; j < 8; ++j) {
+        float2 d = parts(w ? dk[j] : dq[j]);
+#pragma unroll
+        for (int o = LANES; o < 32; o <<= 1) {
+          d.x += __shfl_xor_sync(0xffffffffu, d.x, o);
+          d.y += __shfl_xor_sync(0xffffffffu, d.y, o);
+        }
+        if (lane < LANES) *reinterpret_cast<float2*>(red + (2 * warp + w) * HD + (j < 4 ? c0 + 2 * j : c1 + 2 * j - 8)) = d;
+      }
     }
-  }
-  __syncthreads();
-  if (tid < HD) {
+    __syncthreads();
     float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < ROPE_THREADS / 32; ++i) sum += red[i * HD + tid];
-    a.partial[(long)blockIdx.x * HD + tid] = sum;
-  }
+    for (int w = 0; w < WARPS; ++w) sum += red[2 * w * HD + tid];
+    a.partial[(long)blockIdx.x * 2 * HD + tid] = sum;
   }
 }
 
@@ -348,11 +425,11 @@ __global__ void __launch_bounds__(DW_THREADS) k_rope_dw(const __grid_constant__ 
   const RopePart& p = a.part[blockIdx.x];
   if (!p.dw) return;
   const int c = 4 * (threadIdx.x % (HD / 4)), s = threadIdx.x / (HD / 4);
-  const float* from = a.partial + (blockIdx.x ? (long)a.part[0].blocks * HD : 0) + c;
+  const float* from = a.partial + blockIdx.x * HD + c;
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-  for (int i = s; i < p.blocks; i += DW_ROWS) {
-    const float4 v = *reinterpret_cast<const float4*>(from + (long)i * HD);
+  for (int i = s; i < a.blocks; i += DW_ROWS) {
+    const float4 v = *reinterpret_cast<const float4*>(from + (long)i * 2 * HD);
     sum.x += v.x;
     sum.y += v.y;
     sum.z += v.z;
@@ -368,30 +445,32 @@ __global__ void __launch_bounds__(DW_THREADS) k_rope_dw(const __grid_constant__ 
   }
 }
 
-template <bool BACK>
-cudaError_t launch(const RopeArgs& a, int parts, cudaStream_t s) {
-  int tokens = 0;
-  unsigned blocks = 0;
-  for (int i = 0; i < parts; ++i) {
-    blocks += (unsigned)a.part[i].blocks;
-    if (a.part[i].turned && a.part[i].tokens > tokens) tokens = a.part[i].tokens;
-  }
-  const size_t smem = sizeof(Ring<BACK>) + 2 * sizeof(Turns) * (size_t)tokens;
-  static_assert(sizeof(Ring<true>) + 2 * TOKENS * sizeof(Turns) <= 113 * 1024, "two blocks to an SM");
-  cudaError_t e = cudaFuncSetAttribute(k_rope<BACK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)(sizeof(Ring<BACK>) + 2 * TOKENS * sizeof(Turns)));
-  return e != cudaSuccess ? e : launch_pdl(k_rope<BACK>, dim3(blocks), dim3(ROPE_THREADS), smem, s, a);
+template <bool BACK, bool PAGED>
+cudaError_t launch(RopeArgs a, cudaStream_t s) {
+  const int H = a.part[0].H + a.part[1].H + a.part[2].H;
+  const long steps = a.n * ((H + SIDE - 1) / SIDE), warps = (long)a.blocks * WARPS;
+  a.run = (int)(steps / warps);
+  a.longer = (int)(steps % warps);
+  const auto kernel = a.interleaved ? k_rope<BACK, true, PAGED> : k_rope<BACK, false, PAGED>;
+  constexpr size_t smem = sizeof(RopeSmem<BACK>);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  return e != cudaSuccess ? e : launch_pdl(kernel, dim3((unsigned)a.blocks), dim3(ROPE_THREADS), smem, s, a);
 }
 
 }  // namespace
 
-int rope_tokens(int H) { return H >= ROUND ? 1 : H * TOKENS > ROUND ? ROUND / H : TOKENS; }
-int rope_resident(int backward) { return backward ? 2 : 3; }
+int rope_blocks(int backward, long n, int H, int sms) {
+  const long steps = n * ((H + SIDE - 1) / SIDE), need = (steps + WARPS - 1) / WARPS;
+  const long most = (long)(backward ? 2 : 3) * sms;
+  return (int)(need < most ? need : most);
+}
 
-cudaError_t launch_rope_fwd(const RopeArgs& a, cudaStream_t s) { return launch<false>(a, 3, s); }
+cudaError_t launch_rope_fwd(const RopeArgs& a, cudaStream_t s) {
+  return a.part[2].H > 0 ? launch<false, true>(a, s) : launch<false, false>(a, s);
+}
 
 cudaError_t launch_rope_bwd(const RopeArgs& a, cudaStream_t s) {
-  cudaError_t e = launch<true>(a, 2, s);
+  cudaError_t e = launch<true, false>(a, s);
   if (e != cudaSuccess || (!a.part[0].dw && !a.part[1].dw)) return e;
   return launch_pdl(k_rope_dw, dim3(2), dim3(DW_THREADS), 0, s, a);
 }

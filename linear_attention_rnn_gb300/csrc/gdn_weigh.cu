@@ -75,9 +75,9 @@ __device__ __forceinline__ float sum32(uint32_t S, const Columns<N>& c, int c0, 
 // The key's place among the weights, or null: behind the keys, or on no page.
 __device__ __forceinline__ float* place(const WeighArgs& a, const Paged<CH>& pg, int kh, int key) {
   if (key >= pg.kl) return nullptr;
-  const int e = pg.row[key / a.at.pages.page];
+  const int t = a.at.pages.page_of(key), e = pg.row[t];
   if ((unsigned)e >= (unsigned)a.at.pages.n_pages) return nullptr;
-  return a.weights + ((long)e * a.at.Hk + kh) * a.at.pages.page + key % a.at.pages.page;
+  return a.weights + ((long)e * a.at.Hk + kh) * a.at.pages.page + (key - t * a.at.pages.page);
 }
 
 // ---- many queries ----------------------------------------------------------------------
