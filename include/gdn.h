@@ -499,8 +499,11 @@ int gdn_rope_append(const void* q, const void* k, const void* v, const float* q_
  * outside 0 .. n_pages - 1 is an absent page, whose keys nobody sees (a row that sees no
  * other has o = 0, lse = -inf).  k_len is held within max_pages * page_size (at most
  * 2^30).  Rows past k_len may hold anything.  Sequences may share pages.  q [total_q, Hq,
- * d], cu_q, o, lse, scale, max_k, status and non-finite scores as for gdn_attn_fwd; ws of
- * gdn_attn_workspace_bytes(0, n_seqs, total_q, max_pages * page_size, max_k, Hq, Hk, d).
+ * d], cu_q, o, lse, scale, max_k, status and non-finite scores as for gdn_attn_fwd; max_q
+ * bounds a sequence's new tokens as max_k does its keys (0: not known; up to 128 / (Hq/Hk)
+ * it says that a kernel for few rows suits, which takes longer sequences too).  ws: at least
+ * gdn_attn_paged_workspace_bytes(n_seqs, total_q, max_pages * page_size, max_q, max_k, Hq, Hk,
+ * d) bytes, never NULL where there are queries.
  *
  * gdn_attn_paged_weights adds to each key the attention weight that it receives from the
  * same queries,
@@ -526,10 +529,12 @@ int gdn_rope_append(const void* q, const void* k, const void* v, const float* q_
  * sequence of the call.  ws: gdn_cache_evict_workspace_bytes(n_seqs, max_pages *
  * page_size, budget, Hk) bytes, without a status word (no kernel of it waits).
  */
+size_t gdn_attn_paged_workspace_bytes(int n_seqs, int total_q, int max_rows, int max_q, int max_k,
+                                      int Hq, int Hk, int d);
 int gdn_attn_paged(const void* q, const void* k_pages, const void* v_pages, const int* page_table,
                    const int* k_len, const int* cu_q, void* o, float* lse, int n_seqs, int total_q,
-                   int max_k, int n_pages, int page_size, int max_pages, int Hq, int Hk, int d,
-                   float scale, long long q_stride, const gdn_page_strides* k_strides,
+                   int max_q, int max_k, int n_pages, int page_size, int max_pages, int Hq, int Hk,
+                   int d, float scale, long long q_stride, const gdn_page_strides* k_strides,
                    const gdn_page_strides* v_strides, long long table_stride, void* ws,
                    size_t ws_bytes, void* stream);
 int gdn_attn_paged_weights(const void* q, const void* k_pages, const float* lse,

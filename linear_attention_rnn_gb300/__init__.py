@@ -135,7 +135,9 @@ def lib():
         L.gdn_rope_bwd.restype = I
         L.gdn_rope_append.argtypes = [P] * 12 + [I] * 9 + [F] + [LL] * 4 + [P] * 3
         L.gdn_rope_append.restype = I
-        L.gdn_attn_paged.argtypes = [P] * 8 + [I] * 9 + [F, LL, P, P, LL, P, Z, P]
+        L.gdn_attn_paged_workspace_bytes.argtypes = [I] * 8
+        L.gdn_attn_paged_workspace_bytes.restype = Z
+        L.gdn_attn_paged.argtypes = [P] * 8 + [I] * 10 + [F, LL, P, P, LL, P, Z, P]
         L.gdn_attn_paged.restype = I
         L.gdn_attn_paged_weights.argtypes = [P] * 7 + [I] * 9 + [F, LL, P, LL, P, Z, P]
         L.gdn_attn_paged_weights.restype = I
@@ -703,6 +705,13 @@ def attn_bwd(q, k, v, o, lse, dO, *, cu_q=None, cu_k=None, max_q=None, max_k=Non
     return dq, dk, dv
 
 
+def _scratch_all(nbytes, device, ws):
+    """As _scratch, for workspaces without a status word: none is made where none is needed."""
+    if ws is None and nbytes:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return _scratch(nbytes, device, ws)
+
+
 # ---- heads' norms and rotation, and the paged cache that they feed -----------------------
 class _PageStrides(ctypes.Structure):
     _fields_ = [("page", ctypes.c_longlong), ("row", ctypes.c_longlong), ("head", ctypes.c_longlong)]
@@ -882,13 +891,6 @@ def rope_append(q, k, v, positions, inv_freq, k_pages, v_pages, slots, *, q_weig
     return q_out
 
 
-def _scratch_all(nbytes, device, ws):
-    """As _scratch, for workspaces without a status word: none is made where none is needed."""
-    if ws is None and nbytes:
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    return _scratch(nbytes, device, ws)
-
-
 def _paged_dims(q, k_pages, page_table, k_len, cu_q, max_k, scale):
     """New tokens packed [total, H, D] with cu_q, or [B, T, H, D] without, over pages."""
     if q.dim() != (4 if cu_q is None else 3):
@@ -914,14 +916,20 @@ def _paged_dims(q, k_pages, page_table, k_len, cu_q, max_k, scale):
     return n, total, longest, P, page, pages, Hq, Hk, d, d ** -0.5 if scale is None else float(scale), sq, ks, st
 
 
+def attn_paged_workspace_bytes(n_seqs, total_q, max_rows, max_q, max_k, Hq, Hk, d=128) -> int:
+    return _planned_bytes("gdn_attn_paged_workspace_bytes", _current_device(), n_seqs, total_q, max_rows, max_q, max_k,
+                          Hq, Hk, d)
+
+
 def attn_paged(q, k_pages, v_pages, page_table, k_len, *, cu_q=None, max_q=None, max_k=None, scale=None,
                want_lse: bool = True, o=None, lse=None, workspace=None
                ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """attn_fwd of new tokens over a paged cache: q [total_q, Hq, 128] with cu_q, or [B, T, Hq,
     128]; k_pages, v_pages [pages, page_size, Hk, 128] as for rope_append; page_table int32
     [n, ..], the pages of each sequence (an entry outside the cache is an absent page, whose
-    keys nobody sees); k_len int32 [n], their used rows, the new tokens' own among them.  max_k
-    bounds them and steers how they are split over the SMs (without it: the table's rows).  Returns (o, lse)."""
+    keys nobody sees); k_len int32 [n], their used rows, the new tokens' own among them.  max_q
+    and max_k bound a sequence's new tokens and its keys; they steer what is started, not what is
+    computed.  Returns (o, lse)."""
     n, total, longest, P, page, pages, Hq, Hk, d, scale, sq, ks, st = _paged_dims(q, k_pages, page_table, k_len, cu_q,
                                                                                   max_k, scale)
     vs = _check_pages(v_pages, "v_pages", Hk, k_pages)
@@ -936,11 +944,12 @@ def attn_paged(q, k_pages, v_pages, page_table, k_len, *, cu_q=None, max_q=None,
         lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
     if _several_devices:
         _check_devices(q, k_pages, v_pages, page_table, k_len, cu_q, o, lse, workspace)
-    wp, wn, ws = _scratch(_planned_bytes("gdn_attn_workspace_bytes", dev.index, 0, n, total, pages * page, longest,
-                                         Hq, Hk, d), dev, workspace)  # (ws: kept alive over the call)
+    most = q.shape[1] if cu_q is None else 0 if max_q is None else int(max_q)
+    wp, wn, ws = _scratch_all(_planned_bytes("gdn_attn_paged_workspace_bytes", dev.index, n, total, pages * page, most,
+                                             longest, Hq, Hk, d), dev, workspace)  # (ws: kept alive over the call)
     rc = lib().gdn_attn_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
-                              k_len.data_ptr(), _ptr(cu_q), o.data_ptr(), _ptr(lse), n, total, longest, P, page, pages,
-                              Hq, Hk, d, scale, sq, ctypes.byref(ks), ctypes.byref(vs), st, wp, wn, _stream(dev))
+                              k_len.data_ptr(), _ptr(cu_q), o.data_ptr(), _ptr(lse), n, total, most, longest, P, page,
+                              pages, Hq, Hk, d, scale, sq, ctypes.byref(ks), ctypes.byref(vs), st, wp, wn, _stream(dev))
     if rc != GDN_OK:
         raise GDNError(rc, "gdn_attn_paged")
     return o, lse
@@ -1061,5 +1070,5 @@ __all__ = ["build", "lib", "chunk_fwd", "chunk_bwd", "layer_fwd", "layer_bwd",
            "fwd_workspace_bytes", "bwd_workspace_bytes", "default_segments", "GDNError",
            "header_functions", "delta_step", "decay_step", "decay_fwd", "decay_bwd",
            "decay_workspace_bytes", "attn_fwd", "attn_bwd", "attn_workspace_bytes", "rope_fwd", "rope_bwd",
-           "rope_workspace_bytes", "rope_append", "attn_paged", "attn_paged_weights", "cache_evict",
+           "rope_workspace_bytes", "rope_append", "attn_paged", "attn_paged_workspace_bytes", "attn_paged_weights", "cache_evict",
            "cache_evict_workspace_bytes", "workspace_status", "selftest_wait_timeout"]

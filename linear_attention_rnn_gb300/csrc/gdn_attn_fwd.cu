@@ -57,7 +57,6 @@ struct FwdSmem {
   uint32_t tmem;
 };
 
-template <bool PAGED>
 __global__ void __launch_bounds__(FWD_THREADS, 1) k_attn_fwd(const __grid_constant__ AttnArgs a) {
   extern __shared__ unsigned char raw[];
   FwdSmem& sm = *reinterpret_cast<FwdSmem*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
@@ -94,18 +93,9 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) k_attn_fwd(const __grid_consta
   const float sc = a.scale * LOG2E;
 
   const int nt = 2 * nmax;  // ring tiles: K, V of every key tile
-  const Paged<CH> pg(a, at.x, sq.kl);
-  int entry = -1;  // pages of the loading warp's tile
   auto load = [&](int t) {
-    if constexpr (PAGED) {
-      const int key0 = (kb + t / 2) * CH;
-      pg.load(a.pages, sm.slot[t % NSLOT], (t & 1) ? &a.v : &a.k, kh, key0, entry, &sm.full[t % NSLOT]);
-      if (t & 1) entry = pg.entry(a.pages, key0 + CH);
-      return;
-    }
     load_rows(sm.slot[t % NSLOT], (t & 1) ? &a.v : &a.k, kh, sq.k0 + (kb + t / 2) * CH, &sm.full[t % NSLOT]);
   };
-  if (PAGED && warp == 9) entry = pg.entry(a.pages, kb * CH);
   if (warp == 9 && lane == 0) {
     for (int k = 0; k < NSLOT; ++k) {
       tc::mbar_init(&sm.full[k], 1);
@@ -121,9 +111,6 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) k_attn_fwd(const __grid_consta
     tc::mbar_fence_init();
     for (int x = 0; x < (dual ? 1 : 2); ++x)  // the first loads at once
       if (n[x] > 0) load_group(sm.q[x], &a.q, kh, G, sq.q0 + tok0 + x * TT, &sm.barQ[x]);
-  }
-  if (warp == 9 && (PAGED || lane == 0)) {  // (pages are loaded by the whole warp)
-    __syncwarp(PAGED ? 0xffffffffu : 1u);
     for (int t = 0; t < min(nt, NSLOT); ++t) load(t);
   }
   if (warp == 0) tc::alloc(&sm.tmem, 512);
@@ -136,10 +123,9 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) k_attn_fwd(const __grid_consta
   if (warp >= 8) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_ISSUE));
   if (warp == 9) {
-    if ((PAGED || lane == 0) && nmax > 0) {
+    if (lane == 0 && nmax > 0) {
       for (int t = NSLOT; t < nt && w.ok; ++t) {
         w.on(&sm.empty[t % NSLOT], t / NSLOT - 1);
-        if (PAGED) w.ok = __all_sync(0xffffffffu, w.ok);
         if (w.ok) load(t);
       }
       if (w.ok)  // no copy is in flight when the CTA ends
@@ -220,17 +206,9 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) k_attn_fwd(const __grid_consta
     const int lim = valid ? tok + off : -1;  // the last key that the row sees
     const bool any = __any_sync(0xffffffffu, valid);
     float m = -INFINITY, l = 0.f;
-    const int step = dual ? 2 * CH : CH;
-    int asked = 0;
-    if (PAGED) asked = pg.ask(a.pages, (kb + (dual ? x : 0)) * CH);
     for (int i = 0; i < n[x]; ++i) {
       const int tile = dual ? 2 * i + x : i;  // of the CTA's key tiles
       const int key0 = (kb + tile) * CH;
-      uint32_t absent = 0;  // 16 keys to a bit
-      if (PAGED) {
-        absent = pg.absent(a.pages, asked);
-        asked = pg.ask(a.pages, key0 + step);
-      }
       if (key0 + CH > sq.kl) {  // rows past the keys: whatever they hold, they count as zero
         const int t = 2 * tile + 1;
         w.warp_on(&sm.full[t % NSLOT], t / NSLOT);
@@ -246,10 +224,6 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) k_attn_fwd(const __grid_consta
         if (key0 + CH - 1 > lim) {
 #pragma unroll
           for (int j = 0; j < 128; ++j) v[j] = key0 + j <= lim ? v[j] : -INFINITY;
-        }
-        if (PAGED && absent) {
-#pragma unroll
-          for (int j = 0; j < 128; ++j) v[j] = absent >> (j / 16) & 1u ? -INFINITY : v[j];
         }
         float mt[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
@@ -404,16 +378,15 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ AttnA
 cudaError_t launch_attn_fwd(const AttnArgs& a, cudaStream_t s) {
   constexpr size_t smem = sizeof(FwdSmem) + 1024;
   static_assert(smem <= 227 * 1024, "shared memory");
-  const auto kernel = a.table ? k_attn_fwd<true> : k_attn_fwd<false>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = cudaFuncSetAttribute(k_attn_fwd, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   // (the register hand-over waits for ever where the block was launched with fewer)
   cudaFuncAttributes fa;
-  if ((e = cudaFuncGetAttributes(&fa, kernel)) != cudaSuccess) return e;
+  if ((e = cudaFuncGetAttributes(&fa, k_attn_fwd)) != cudaSuccess) return e;
   if (fa.numRegs < REGS_LAUNCH) return cudaErrorInvalidConfiguration;
   const int K = 2 * (CH / (a.Hq / a.Hk));
   const dim3 grid((unsigned)a.Hk * (unsigned)(a.total_q / K + a.n_seqs), (unsigned)a.n_splits);
-  e = launch_pdl(kernel, grid, dim3(FWD_THREADS), smem, s, a);
+  e = launch_pdl(k_attn_fwd, grid, dim3(FWD_THREADS), smem, s, a);
   return e != cudaSuccess || a.n_splits == 1 ? e : launch_attn_join(a, s);
 }
 

@@ -36,7 +36,6 @@ struct SplitSmem {
   uint32_t tmem;
 };
 
-template <bool PAGED>
 __global__ void __launch_bounds__(SPLIT_THREADS, 2) k_attn_split(const __grid_constant__ AttnArgs a) {
   extern __shared__ unsigned char raw[];
   SplitSmem& sm = *reinterpret_cast<SplitSmem*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
@@ -60,15 +59,7 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 2) k_attn_split(const __grid_co
   const int n = (ke - kb + KEYS - 1) / KEYS;
 
   const int nt = 2 * n;
-  const Paged<KEYS> pg(a, at.x, sq.kl);
-  int entry = -1;  // pages of the loading warp's tile
   auto load = [&](int t) {
-    if constexpr (PAGED) {
-      const int key0 = kb + (t / 2) * KEYS;
-      pg.load(a.pages, sm.slot[t % NSLOT], (t & 1) ? &a.v : &a.k, kh, key0, entry, &sm.full[t % NSLOT]);
-      if (t & 1) entry = pg.entry(a.pages, key0 + KEYS);
-      return;
-    }
     uint64_t* bar = &sm.full[t % NSLOT];
     const CUtensorMap* m = (t & 1) ? &a.v : &a.k;
     unsigned char* dst = sm.slot[t % NSLOT];
@@ -77,7 +68,6 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 2) k_attn_split(const __grid_co
     tc::tma_load_3d(dst, m, 0, kh, row, bar);
     tc::tma_load_3d(dst + KTILE / 2, m, 64, kh, row, bar);
   };
-  if (PAGED && warp == 5) entry = pg.entry(a.pages, kb);
   if (warp == 5 && lane == 0) {
     for (int k = 0; k < NSLOT; ++k) {
       tc::mbar_init(&sm.full[k], 1);
@@ -89,9 +79,6 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 2) k_attn_split(const __grid_co
     tc::mbar_init(&sm.barP, 128);
     tc::mbar_fence_init();
     if (n > 0) load_group(sm.q, &a.q, kh, G, sq.q0 + tok0, &sm.barQ);  // the first loads at once
-  }
-  if (warp == 5 && (PAGED || lane == 0)) {  // (pages are loaded by the whole warp)
-    __syncwarp(PAGED ? 0xffffffffu : 1u);
     for (int t = 0; t < min(nt, NSLOT); ++t) load(t);
   }
   if (warp == 0) tc::alloc(&sm.tmem, 256);
@@ -102,10 +89,9 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 2) k_attn_split(const __grid_co
   tc::Wait w;
 
   if (warp == 5) {
-    if ((PAGED || lane == 0) && n > 0) {
+    if (lane == 0 && n > 0) {
       for (int t = NSLOT; t < nt && w.ok; ++t) {
         w.on(&sm.empty[t % NSLOT], t / NSLOT - 1);
-        if (PAGED) w.ok = __all_sync(0xffffffffu, w.ok);
         if (w.ok) load(t);
       }
       if (w.ok)  // no copy is in flight when the CTA ends
@@ -149,15 +135,8 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 2) k_attn_split(const __grid_co
     const bool any = __any_sync(0xffffffffu, valid);
     const float sc = a.scale * LOG2E;
     float m = -INFINITY, l = 0.f;
-    int asked = 0;
-    if (PAGED) asked = pg.ask(a.pages, kb);
     for (int i = 0; i < n; ++i) {
       const int key0 = kb + i * KEYS;
-      uint32_t absent = 0;  // 16 keys to a bit
-      if (PAGED) {
-        absent = pg.absent(a.pages, asked);
-        asked = pg.ask(a.pages, key0 + KEYS);
-      }
       if (key0 + KEYS > sq.kl) {  // rows past the keys: whatever they hold, they count as zero
         const int t = 2 * i + 1;
         w.warp_on(&sm.full[t % NSLOT], t / NSLOT);
@@ -173,10 +152,6 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 2) k_attn_split(const __grid_co
         if (key0 + KEYS - 1 > lim) {
 #pragma unroll
           for (int j = 0; j < 64; ++j) v[j] = key0 + j <= lim ? v[j] : -INFINITY;
-        }
-        if (PAGED && absent) {
-#pragma unroll
-          for (int j = 0; j < 64; ++j) v[j] = absent >> (j / 16) & 1u ? -INFINITY : v[j];
         }
         float mt[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
@@ -266,11 +241,10 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 2) k_attn_split(const __grid_co
 cudaError_t launch_attn_split(const AttnArgs& a, cudaStream_t s) {
   constexpr size_t smem = sizeof(SplitSmem) + 1024;
   static_assert(2 * (smem + 1024) <= 228 * 1024, "shared memory of two CTAs");
-  const auto kernel = a.table ? k_attn_split<true> : k_attn_split<false>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = cudaFuncSetAttribute(k_attn_split, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)a.Hk * (unsigned)(a.total_q / (CH / (a.Hq / a.Hk)) + a.n_seqs), (unsigned)a.n_splits);
-  e = launch_pdl(kernel, grid, dim3(SPLIT_THREADS), smem, s, a);
+  e = launch_pdl(k_attn_split, grid, dim3(SPLIT_THREADS), smem, s, a);
   return e != cudaSuccess || a.n_splits == 1 ? e : launch_attn_join(a, s);
 }
 

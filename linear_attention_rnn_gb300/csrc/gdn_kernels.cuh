@@ -240,6 +240,17 @@ struct AttnArgs {
   int n_parts;                // 2 to a split (k_attn_fwd) or 1 (k_attn_split)
 };
 
+// Attention over keys in pages (gdn_attn_paged.cu).
+namespace attn {
+struct Join;
+}
+constexpr int PAGED_KEYS = 64;  // most rows of a load
+struct PagedArgs {
+  AttnArgs at;          // part, part_lse: two slots to a CTA, of 128 rows (few) or 256
+  attn::Join* joins;    // one to a CTA
+  int ctas, few;        // few: k_paged_few, whose sequences are best of one query tile
+};
+
 // The weight that attention gives to each key in pages (gdn_weigh.cu).
 constexpr int WEIGH_FEW_ROWS = 64;  // rows of a query tile in the kernel for few of them
 struct WeighArgs {
@@ -352,6 +363,8 @@ cudaError_t launch_rope_bwd(const RopeArgs& a, cudaStream_t s);
 cudaError_t launch_attn_fwd(const AttnArgs& a, cudaStream_t s);
 cudaError_t launch_attn_split(const AttnArgs& a, cudaStream_t s);  // keys in maps of 64 rows
 cudaError_t launch_attn_join(const AttnArgs& a, cudaStream_t s);
+cudaError_t launch_attn_paged(const PagedArgs& a, cudaStream_t s);
+size_t paged_join_bytes();  // of a CTA's entry in the joins
 // dO . o per row, then the gradients of k and v, then that of q
 cudaError_t launch_attn_bwd(const AttnArgs& a, cudaStream_t s);
 // (A, B) = (I, 0) for n [HD x HD] fp32 pairs (A nullable).

@@ -519,15 +519,52 @@ static int paged_check(int n_seqs, int total_q, int max_k, int n_pages, int page
   return GDN_OK;
 }
 
+// The kernel for attention over pages: k_paged_few where all sequences fit one query tile (it
+// takes longer ones too, tile by tile), which the totals or max_q say; else k_paged_many.  CTAs: two to an
+// SM, or one, but no more than there can be tiles of 128 keys.
+struct PagedPlan {
+  int ctas, few;
+  size_t status, joins, part, part_lse, total;
+};
+static PagedPlan paged_plan(int n_seqs, int total_q, long long max_q, long long max_k, int Hq, int Hk) {
+  PagedPlan p;
+  const long long TT = CH / (Hq / Hk), tiles = max_k > CH ? (max_k + CH - 1) / CH : 1;
+  p.few = total_q <= TT || (max_q > 0 && max_q <= TT);
+  const long long items = (total_q / (p.few ? TT : 2 * TT) + n_seqs) * Hk, most = (p.few ? 2 : 1) * sm_count();
+  p.ctas = (int)(items < most && items * tiles < most ? items * tiles : most);
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off += up(bytes);
+    return o;
+  };
+  const size_t rows = p.ctas > 1 ? (size_t)p.ctas * 2 * (p.few ? CH : 2 * CH) : 0;
+  p.status = take(sizeof(int));
+  p.joins = take(p.ctas * paged_join_bytes());
+  p.part_lse = take(rows * sizeof(float));
+  p.part = take(rows * HD * sizeof(float));
+  p.total = off;
+  return p;
+}
+
+size_t gdn_attn_paged_workspace_bytes(int n_seqs, int total_q, int max_rows, int max_q, int max_k, int Hq, int Hk,
+                                      int d) {
+  const int* some = reinterpret_cast<const int*>(4);
+  if (max_rows < 0 || max_q < 0 || attn_check(n_seqs, total_q, 0, max_k, Hq, Hk, d, some, some, 1.f, (long long)Hq * HD,
+                                 (long long)Hk * HD, (long long)Hk * HD) != GDN_OK)
+    return 0;
+  return paged_plan(n_seqs, total_q, max_q, max_k < max_rows ? max_k : max_rows, Hq, Hk).total;
+}
+
 int gdn_attn_paged(const void* q, const void* k_pages, const void* v_pages, const int* page_table, const int* k_len,
-                   const int* cu_q, void* o, float* lse, int n_seqs, int total_q, int max_k, int n_pages, int page_size,
-                   int max_pages, int Hq, int Hk, int d, float scale, long long q_stride,
+                   const int* cu_q, void* o, float* lse, int n_seqs, int total_q, int max_q, int max_k, int n_pages,
+                   int page_size, int max_pages, int Hq, int Hk, int d, float scale, long long q_stride,
                    const gdn_page_strides* k_strides, const gdn_page_strides* v_strides, long long table_stride,
                    void* ws, size_t ws_bytes, void* stream) {
   int rc = paged_check(n_seqs, total_q, max_k, n_pages, page_size, max_pages, Hq, Hk, d, cu_q, page_table, table_stride,
                        k_len, scale, q_stride, k_strides);
   if (rc) return rc;
-  if (!page_strides_ok(v_strides)) return GDN_ERR_ARG;
+  if (!page_strides_ok(v_strides) || max_q < 0) return GDN_ERR_ARG;
   const void* ptrs[] = {q, k_pages, v_pages, o, ws};
   for (const void* p : ptrs)
     if (p && !aligned(p, 16)) return GDN_ERR_ARG;
@@ -535,15 +572,16 @@ int gdn_attn_paged(const void* q, const void* k_pages, const void* v_pages, cons
   if (n_seqs == 0 || total_q == 0) return GDN_OK;
   if (!q || !o || !page_table || !k_len || (n_pages > 0 && (!k_pages || !v_pages))) return GDN_ERR_ARG;
   const long long capacity = (long long)max_pages * page_size;
-  const AttnPlan p = attn_plan(0, n_seqs, total_q, max_k < capacity ? max_k : (int)capacity, Hq, Hk);
-  if (!workspace_ok(ws, ws_bytes, p.total)) return GDN_ERR_WORKSPACE;
-  AttnArgs a;
+  const PagedPlan p = paged_plan(n_seqs, total_q, max_q, max_k < capacity ? max_k : capacity, Hq, Hk);
+  if (!ws || ws_bytes < p.total) return GDN_ERR_WORKSPACE;
+  PagedArgs pa;
+  memset(&pa, 0, sizeof pa);
+  AttnArgs& a = pa.at;
   if ((rc = attn_args(a, q, nullptr, nullptr, cu_q, nullptr, n_seqs, total_q, 0, Hq, Hk, scale, q_stride,
                       (long long)Hk * HD, (long long)Hk * HD)))
     return rc;
   a.table = page_table;
-  a.pages = page_args(n_pages, page_size, max_pages, table_stride, p.few ? CH / 2 : CH);
-  if (!tmap_rows(&a.mo, o, total_q, Hq, HD, (uint64_t)Hq * HD * 2, Hq / Hk, CH / (Hq / Hk))) return GDN_ERR_CUDA;
+  a.pages = page_args(n_pages, page_size, max_pages, table_stride, PAGED_KEYS);
   if (n_pages > 0 &&  // (without pages no tile is ever loaded)
       (!tmap_pages(&a.k, k_pages, n_pages, page_size, Hk, HD, (uint64_t)k_strides->page * 2, (uint64_t)k_strides->row * 2,
                    (uint64_t)k_strides->head * 2, a.pages.box) ||
@@ -553,14 +591,13 @@ int gdn_attn_paged(const void* q, const void* k_pages, const void* v_pages, cons
   a.k_len = k_len;
   a.o = static_cast<bf16*>(o);
   a.lse = lse;
-  a.status = ws ? at<int>(ws, p.status) : nullptr;
-  a.split_tiles = p.split_tiles;
-  a.n_splits = p.n_splits;
-  a.n_parts = p.n_parts;
+  a.status = at<int>(ws, p.status);
   a.part = at<float>(ws, p.part);
   a.part_lse = at<float>(ws, p.part_lse);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return cuda_status(p.few ? launch_attn_split(a, s) : launch_attn_fwd(a, s));
+  pa.joins = at<attn::Join>(ws, p.joins);
+  pa.ctas = p.ctas;
+  pa.few = p.few;
+  return cuda_status(launch_attn_paged(pa, static_cast<cudaStream_t>(stream)));
 }
 
 int gdn_attn_paged_weights(const void* q, const void* k_pages, const float* lse, const int* page_table,

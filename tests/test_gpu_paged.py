@@ -18,10 +18,10 @@ def eps_of(x, scale):
     return float(scale * x["q"].float().norm(dim=-1).max() * k.norm(dim=-1).max() * 136 * 2.0 ** -23)
 
 
-def both(gdn, x, ql, kl, scale=None, most=None, weights=True, d=None):
+def both(gdn, x, ql, kl, scale=None, most=None, weights=True, d=None, most_q="exact"):
     sc = 128 ** -0.5 if scale is None else scale
     d = paged.cuda(x) if d is None else d
-    args = dict(cu_q=d["cu"], max_q=max(ql + [0]), max_k=most, scale=scale)
+    args = dict(cu_q=d["cu"], max_q=max(ql + [0]) if most_q == "exact" else most_q, max_k=most, scale=scale)
     o, lse = gdn.attn_paged(d["q"], d["kp"], d["vp"], d["table"], d["k_len"], **args)
     eps = eps_of(x, sc)
     r = ops.attn_paged(x["q"], x["kp"], x["vp"], x["table"], ql, kl, sc, eps)
@@ -59,11 +59,25 @@ def test_chunks_over_pages(gdn_lib, ql, kl, Hq, Hk, page):
 
 @pytest.mark.parametrize("page", [32, 80, 112, 128, 1024])
 @pytest.mark.parametrize("most", [None, 1, 3000, 100000])
-def test_bounds_only_steer(gdn_lib, page, most):
-    """max_k, too small or too large, and page sizes with other powers of two."""
+@pytest.mark.parametrize("most_q", [None, 1, 100000])
+def test_bounds_only_steer(gdn_lib, page, most, most_q):
+    """max_q and max_k, too small or too large, and page sizes with other powers of two."""
     for ql, kl in (([1, 2, 1], [2999, 1500, 17]), ([300, 5], [1300, 2000])):
         x = paged.cache(ql, kl, 4, 2, page, seed=page)
-        both(gdn_lib, x, ql, kl, most=most)
+        both(gdn_lib, x, ql, kl, most=most, most_q=most_q)
+
+
+@pytest.mark.parametrize("Hq,Hk", [(8, 8), (8, 2), (6, 2), (16, 1)])
+def test_many_sequences_of_any_length(gdn_lib, Hq, Hk):
+    """More items than are planned at a time, tokens and prompts and sequences without either, in any order."""
+    gen = torch.Generator().manual_seed(Hq + Hk)
+    n = 150
+    ql = torch.where(torch.rand(n, generator=gen) < 0.7, 1, torch.randint(0, 90, (n,), generator=gen)).tolist()
+    kl = [max(0, q + int(k)) for q, k in zip(ql, torch.randint(-40, 160, (n,), generator=gen))]
+    kl[7], kl[90] = 3000, 0
+    x = paged.cache(ql, kl, Hq, Hk, 16, seed=2)
+    for most_q in (None, 1):
+        both(gdn_lib, x, ql, kl, most_q=most_q, weights=most_q is None)
 
 
 @pytest.mark.parametrize("scale,spread", [(1.0, 1.0), (0.02, 1.0), (None, 8.0)])
@@ -140,18 +154,6 @@ def test_lengths_beyond_the_table(gdn_lib):
     d = paged.cuda(x)
     d["k_len"] = torch.tensor([1000, -4], dtype=torch.int32).cuda()
     both(gdn_lib, x, [2, 1], [64, 0], d=d)
-
-
-@pytest.mark.parametrize("ql", [[1, 1], [150, 20]])
-def test_as_over_packed_keys(gdn_lib, ql):
-    """The same keys in one piece and in pages: the same kernels but for the loads, so equal bits."""
-    kl = [1200, 333]
-    x = paged.cuda(paged.cache(ql, kl, 8, 2, 64, seed=10, nan=False))
-    flat = lambda p: torch.cat([p[x["table"][s, :-(-m // 64)].long()].flatten(0, 1)[:m] for s, m in enumerate(kl)])
-    for most in (1200, 64):
-        a = gdn_lib.attn_paged(x["q"], x["kp"], x["vp"], x["table"], x["k_len"], cu_q=x["cu"], max_k=most)
-        b = gdn_lib.attn_fwd(x["q"], flat(x["kp"]), flat(x["vp"]), cu_q=x["cu"], cu_k=paged.cu(kl).cuda(), max_k=most)
-        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
 @pytest.mark.parametrize("ql,kl", [([1, 1], [700, 90]), ([150, 140], [700, 140])])
@@ -231,7 +233,7 @@ def test_status_words(gdn_lib):
     """The workspaces' status words read clean after calls of each kernel."""
     for ql, kl in (([300, 1], [900, 500]), ([1, 2], [5000, 100])):
         d = paged.cuda(paged.cache(ql, kl, 4, 2, 16, seed=17))
-        ws = torch.full((gdn_lib.attn_workspace_bytes(0, 2, sum(ql), d["table"].shape[1] * 16, max(kl), 4, 2) + 256,), 255,
+        ws = torch.full((gdn_lib.attn_paged_workspace_bytes(2, sum(ql), d["table"].shape[1] * 16, 0, max(kl), 4, 2),), 255,
                         dtype=torch.uint8, device="cuda")
         o, lse = gdn_lib.attn_paged(d["q"], d["kp"], d["vp"], d["table"], d["k_len"], cu_q=d["cu"], max_k=max(kl), workspace=ws)
         assert gdn_lib.workspace_status(ws) == 0

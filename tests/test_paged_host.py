@@ -68,15 +68,18 @@ def test_rope_argument_errors(L):
 
 
 def test_paged_argument_errors(L):
-    need = gdn.attn_workspace_bytes(0, 2, 2, 20000, 10000, 4, 2)
+    need = gdn.attn_paged_workspace_bytes(2, 2, 313 * 64, 0, 10000, 4, 2)
+    assert need > gdn.attn_paged_workspace_bytes(1, 1, 313 * 64, 0, 100, 4, 2) > 0
+    assert gdn.attn_paged_workspace_bytes(1, 1, 64, 0, 64, 4, 2, d=64) == 0
 
-    def fwd(q=FAKE, kp=FAKE, table=FAKE, klen=FAKE, cu=FAKE, o=FAKE, lse=None, n=2, nq=2, most=10000, pages=400, page=64, wide=313,
+    def fwd(q=FAKE, kp=FAKE, table=FAKE, klen=FAKE, cu=FAKE, o=FAKE, lse=None, n=2, nq=2, mq=0, most=10000, pages=400, page=64, wide=313,
             Hq=4, Hk=2, d=128, scale=0.1, sq=512, ks=strides(), vs=strides(), st=313, ws=FAKE, nbytes=1 << 40):
-        return L.gdn_attn_paged(q, kp, FAKE, table, klen, cu, o, lse, n, nq, most, pages, page, wide, Hq, Hk, d, scale, sq, ks, vs,
+        return L.gdn_attn_paged(q, kp, FAKE, table, klen, cu, o, lse, n, nq, mq, most, pages, page, wide, Hq, Hk, d, scale, sq, ks, vs,
                                 st, ws, nbytes, None)
     assert fwd(n=0) == OK and fwd(nq=0) == OK
     assert fwd(d=64) == SHAPE and fwd(page=40) == SHAPE and fwd(Hq=258, Hk=2, sq=258 * 128) == SHAPE
-    assert fwd(Hk=3) == ARG and fwd(nq=-1) == ARG and fwd(most=-1) == ARG and fwd(pages=-1) == ARG and fwd(wide=-1) == ARG
+    assert fwd(Hk=3) == ARG and fwd(nq=-1) == ARG and fwd(most=-1) == ARG and fwd(mq=-1) == ARG
+    assert fwd(pages=-1) == ARG and fwd(wide=-1) == ARG
     assert fwd(st=312) == ARG and fwd(wide=1 << 25, st=1 << 25) == ARG
     for scale in (0.0, -1.0, float("nan"), float("inf")):
         assert fwd(scale=scale) == ARG
@@ -143,7 +146,7 @@ def calls(monkeypatch):
             calls.append(name)
             return 0
         return f
-    sizes = ["gdn_rope_workspace_bytes", "gdn_attn_workspace_bytes", "gdn_cache_evict_workspace_bytes"]
+    sizes = ["gdn_rope_workspace_bytes", "gdn_attn_paged_workspace_bytes", "gdn_cache_evict_workspace_bytes"]
     monkeypatch.setattr(gdn, "lib", lambda: types.SimpleNamespace(**{n: stand_in(n) for n in ["gdn_" + n for n in NAMES] + sizes}))
     monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
