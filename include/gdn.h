@@ -512,8 +512,8 @@ int gdn_rope_append(const void* q, const void* k, const void* v, const float* q_
  * [total_q, Hq] as gdn_attn_paged returned it (a row with lse = -inf adds nothing).
  * weights: fp32 [n_pages, Hk, page_size], contiguous.  A sequence's sum is formed in a
  * fixed order and added at once; where sequences share a page, or a table names one twice,
- * each adds its own, in no fixed order.  max_k bounds the keys of a sequence (a value that
- * is too small costs speed, not correctness).  ws: 256 bytes whose first word is the status
+ * each adds its own, in no fixed order.  max_q and max_k bound a sequence's queries (0: not
+ * known) and keys; they steer, as above.  ws: 256 bytes whose first word is the status
  * word, or NULL.  A call that has nothing to add starts no kernel.
  *
  * gdn_cache_evict drops the lightest keys.  Per sequence and key head the last min(recent,
@@ -539,7 +539,7 @@ int gdn_attn_paged(const void* q, const void* k_pages, const void* v_pages, cons
                    size_t ws_bytes, void* stream);
 int gdn_attn_paged_weights(const void* q, const void* k_pages, const float* lse,
                            const int* page_table, const int* k_len, const int* cu_q, float* weights,
-                           int n_seqs, int total_q, int max_k, int n_pages, int page_size,
+                           int n_seqs, int total_q, int max_q, int max_k, int n_pages, int page_size,
                            int max_pages, int Hq, int Hk, int d, float scale, long long q_stride,
                            const gdn_page_strides* k_strides, long long table_stride, void* ws,
                            size_t ws_bytes, void* stream);

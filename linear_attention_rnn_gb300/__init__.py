@@ -139,7 +139,7 @@ def lib():
         L.gdn_attn_paged_workspace_bytes.restype = Z
         L.gdn_attn_paged.argtypes = [P] * 8 + [I] * 10 + [F, LL, P, P, LL, P, Z, P]
         L.gdn_attn_paged.restype = I
-        L.gdn_attn_paged_weights.argtypes = [P] * 7 + [I] * 9 + [F, LL, P, LL, P, Z, P]
+        L.gdn_attn_paged_weights.argtypes = [P] * 7 + [I] * 10 + [F, LL, P, LL, P, Z, P]
         L.gdn_attn_paged_weights.restype = I
         L.gdn_cache_evict_workspace_bytes.argtypes = [I] * 4
         L.gdn_cache_evict_workspace_bytes.restype = Z
@@ -966,9 +966,10 @@ def attn_paged_weights(q, k_pages, lse, page_table, k_len, weights, *, cu_q=None
     _check(weights, "weights", torch.float32, (P, Hk, page))
     if _several_devices:
         _check_devices(q, k_pages, lse, page_table, k_len, weights, cu_q, workspace)
+    most = q.shape[1] if cu_q is None else 0 if max_q is None else int(max_q)
     wp, wn, ws = _scratch(_STATUS_BYTES, q.device, workspace)
     rc = lib().gdn_attn_paged_weights(q.data_ptr(), k_pages.data_ptr(), lse.data_ptr(), page_table.data_ptr(),
-                                      k_len.data_ptr(), _ptr(cu_q), weights.data_ptr(), n, total, longest, P, page,
+                                      k_len.data_ptr(), _ptr(cu_q), weights.data_ptr(), n, total, most, longest, P, page,
                                       pages, Hq, Hk, d, scale, sq, ctypes.byref(ks), st, wp, wn, _stream(q.device))
     if rc != GDN_OK:
         raise GDNError(rc, "gdn_attn_paged_weights")

@@ -63,15 +63,14 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs& a, const Lanes& l, int s) 
   return r;
 }
 
-// The rank-th tile of all sequences' tiles of K rows, those with the highest index
-// in their sequence first (the work of a tile grows with it, and CTAs start in
-// order of rank); sequence -1: there are fewer.  Every warp finds it for itself: a
-// lane counts for every 32nd sequence (lane_rows: its first one's rows), and the
-// index of rank's tile is found by bisection.
-__device__ __forceinline__ int2 find_tile(const int* cu, int lane_rows, int n_seqs, int total, int K, int rank) {
+// The rank-th of all sequences' tiles, those with the highest index in their sequence first
+// (the work of a tile grows with it, and CTAs start in order of rank); sequence -1: there
+// are fewer.  tiles(s): those of sequence s, n0: of the lane's own, the first 32.  Every warp
+// finds it for itself: a lane counts for every 32nd sequence, and the index of rank's
+// tile is found by bisection.
+template <typename F>
+__device__ __forceinline__ int2 find_nth(F tiles, int n0, int n_seqs, int rank) {
   const int lane = threadIdx.x & 31;
-  auto tiles = [&](int s) { return (rows_of(cu, s, n_seqs, total).y + K - 1) / K; };
-  const int n0 = lane < n_seqs ? (lane_rows + K - 1) / K : 0;  // (the first 32 stay in registers)
   auto count_above = [&](int t) {                  // tiles of index t or more
     int c = max(n0 - t, 0);
     for (int s = lane + 32; s < n_seqs; s += 32) c += max(tiles(s) - t, 0);
@@ -101,6 +100,11 @@ __device__ __forceinline__ int2 find_tile(const int* cu, int lane_rows, int n_se
     k -= c;
   }
   return make_int2(-1, 0);
+}
+// The same for tiles of K rows (lane_rows: the rows of the lane's own sequence).
+__device__ __forceinline__ int2 find_tile(const int* cu, int lane_rows, int n_seqs, int total, int K, int rank) {
+  return find_nth([&](int s) { return (rows_of(cu, s, n_seqs, total).y + K - 1) / K; },
+                  (int)(threadIdx.x & 31) < n_seqs ? (lane_rows + K - 1) / K : 0, n_seqs, rank);
 }
 
 // 128 rows of one head

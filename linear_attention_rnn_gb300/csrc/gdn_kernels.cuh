@@ -258,8 +258,8 @@ struct WeighArgs {
   const float* lse;     // [total_q][Hq]
   float* weights;       // [n_pages][Hk][page], added to
   int few;              // tokens over caches: the kernel that streams keys
-  int key_tiles;        // many queries: key tiles of a sequence, foreseen
-  int ctas;             // few
+  int ctas;             // of them; many: teams of `split` CTAs
+  int split;            // many: CTAs that share the queries of a key tile, 1 or 2
 };
 
 // Eviction of the lightest keys from pages (gdn_evict.cu).

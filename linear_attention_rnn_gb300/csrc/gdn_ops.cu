@@ -601,13 +601,14 @@ int gdn_attn_paged(const void* q, const void* k_pages, const void* v_pages, cons
 }
 
 int gdn_attn_paged_weights(const void* q, const void* k_pages, const float* lse, const int* page_table,
-                           const int* k_len, const int* cu_q, float* weights, int n_seqs, int total_q, int max_k,
-                           int n_pages, int page_size, int max_pages, int Hq, int Hk, int d, float scale,
+                           const int* k_len, const int* cu_q, float* weights, int n_seqs, int total_q, int max_q,
+                           int max_k, int n_pages, int page_size, int max_pages, int Hq, int Hk, int d, float scale,
                            long long q_stride, const gdn_page_strides* k_strides, long long table_stride, void* ws,
                            size_t ws_bytes, void* stream) {
   int rc = paged_check(n_seqs, total_q, max_k, n_pages, page_size, max_pages, Hq, Hk, d, cu_q, page_table, table_stride,
                        k_len, scale, q_stride, k_strides);
   if (rc) return rc;
+  if (max_q < 0) return GDN_ERR_ARG;
   const void* ptrs[] = {q, k_pages, ws};
   for (const void* p : ptrs)
     if (p && !aligned(p, 16)) return GDN_ERR_ARG;
@@ -633,13 +634,16 @@ int gdn_attn_paged_weights(const void* q, const void* k_pages, const float* lse,
   w.lse = lse;
   w.weights = weights;
   if (w.few && !tmap_rows(&w.at.q, q, total_q, Hq, HD, (uint64_t)q_stride * 2, G, WEIGH_FEW_ROWS / G)) return GDN_ERR_CUDA;
-  w.ctas = 2 * sm_count();
-  // key tiles of the longest sequence, or as many as one grid dimension has blocks for (a
-  // sequence's last block takes the rest)
+  // CTAs: two to an SM (few), or one, but no more than there can be key tiles.
   const long long longest = max_k < w.at.pages.capacity ? max_k : w.at.pages.capacity;
-  long long tiles = (longest + CH - 1) / CH;
-  if (tiles > (1LL << 30) / ((long long)Hk * n_seqs)) tiles = (1LL << 30) / ((long long)Hk * n_seqs);
-  w.key_tiles = tiles > 0 ? (int)tiles : 1;
+  const long long tiles = longest > CH ? (longest + CH - 1) / CH : 1, sms = sm_count();
+  // Pairs share a key tile where one CTA would still be at the first, which sees all queries of
+  // its sequence, long after the others are done (in query tiles; a causal prompt has half of all).
+  const long long TT = CH / G, first = (max_q > 0 && max_q < total_q ? max_q : total_q) / TT;
+  const long long each = total_q / TT * tiles * Hk / 2 / sms;
+  w.split = !w.few && first - each > 32 ? 2 : 1;
+  const long long most = w.few ? 2 * sms : sms / w.split, units = tiles * Hk;
+  w.ctas = (int)(units < most && units * n_seqs < most ? units * n_seqs : most);
   return cuda_status(launch_weigh(w, static_cast<cudaStream_t>(stream)));
 }
 

@@ -7,8 +7,8 @@
 // threads.  Keys that a tile's queries do not all see take a masked sum, 32 columns at a
 // time; the other columns take one fma, one exponential and one addition each, in pairs.
 //
-// Many queries (prompts): a CTA keeps one tile of 128 keys and streams the query tiles
-// that see it through a ring; four groups of four warps take them in turn.
+// Many queries (prompts): a CTA, or a pair of them, keeps one tile of 128 keys; it streams the query tiles
+// that see it through a ring; three groups of four warps take them in turn.
 // Few queries (tokens over caches): a CTA keeps the query tile and streams key tiles;
 // only as many columns are formed as there are rows, two CTAs to an SM, each with an
 // equal run of all sequences' key tiles.
@@ -44,12 +44,11 @@ __device__ __forceinline__ void column(const WeighArgs& a, const Seq& sq, int kh
   lim = sees ? tok + sq.kl - sq.ql : -1;
 }
 
-// Sum of the key's exponentials over 32 columns.  All rows see every key up to `clean`.
+// Adds the key's exponentials over the 32 columns v from column c0 on to sum.  All rows see
+// every key up to `clean`.
 template <int N>
-__device__ __forceinline__ float sum32(uint32_t S, const Columns<N>& c, int c0, int key, int tile_end, int clean, float sc) {
-  float v[32];
-  tc::ld32(S + c0, v);
-  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+__device__ __forceinline__ void add32(const float (&v)[32], const Columns<N>& c, int c0, int key, int tile_end, int clean,
+                                      float sc, float (&sum)[4]) {
   if (tile_end <= clean) {
 #pragma unroll
     for (int j = 0; j < 32; j += 4) {
@@ -69,7 +68,6 @@ __device__ __forceinline__ float sum32(uint32_t S, const Columns<N>& c, int c0, 
       if (key <= c.lim[c0 + j]) sum[j & 3] += p;
     }
   }
-  return (sum[0] + sum[1]) + (sum[2] + sum[3]);
 }
 
 // The key's place among the weights, or null: behind the keys, or on no page.
@@ -81,16 +79,22 @@ __device__ __forceinline__ float* place(const WeighArgs& a, const Paged<CH>& pg,
 }
 
 // ---- many queries ----------------------------------------------------------------------
-constexpr int MANY_GROUPS = 4, MANY_THREADS = 128 * MANY_GROUPS + 64, MANY_SLOTS = 5;
+// Two warps issue in turn: a product holds its issuer for the time that it takes, and the two
+// waits before the next one would come on top of that (a prompt of 8192 tokens: 131 us with
+// one, 114 with two).  An even number of slots and of S buffers, so that a barrier's phases
+// are one issuer's, in their order.
+constexpr int MANY_GROUPS = 4, MANY_THREADS = 128 * MANY_GROUPS + 96, MANY_SLOTS = 4, MANY_S = 4;
+static_assert(MANY_SLOTS % 2 == 0 && MANY_S % 2 == 0, "each issuer's own");
 
 struct ManySmem {
   unsigned char k[TILE];
   unsigned char slot[MANY_SLOTS][TILE];
-  Columns<CH> cols[MANY_GROUPS];
-  int clean[MANY_GROUPS][4];  // of 32 columns: the last key that all of their rows see
+  Columns<CH> cols[MANY_GROUPS][2];
+  int clean[MANY_GROUPS][2][4];  // of 32 columns: the last key that all of their rows see
   float sums[MANY_GROUPS - 1][CH];
+  float other[CH];  // the other CTA's sums
   uint64_t full[MANY_SLOTS], empty[MANY_SLOTS];
-  uint64_t barK, barS[MANY_GROUPS], barE[MANY_GROUPS];
+  uint64_t barK, barS[MANY_S], barE[MANY_S];
   uint32_t tmem;
 };
 
@@ -98,26 +102,17 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) k_weigh_many(const __grid_con
   extern __shared__ unsigned char raw[];
   ManySmem& sm = *reinterpret_cast<ManySmem*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
   const int tid = threadIdx.x, lane = tid & 31, warp = tc::warp_index();
-  constexpr int ISSUES = 4 * MANY_GROUPS, LOADS = ISSUES + 1, NG = MANY_GROUPS;
+  constexpr int ISSUES = 4 * MANY_GROUPS, LOADS = ISSUES + 2, NG = MANY_GROUPS, NS = MANY_S;
   pdl_wait();
   pdl_release();
   clear_status(a.at.status);
   const int G = a.at.Hq / a.at.Hk, TT = CH / G;
-  // heads run fastest, then sequences, then key tiles: the first ones see the most queries
-  const int kh = blockIdx.x % a.at.Hk, seq = blockIdx.x / a.at.Hk % a.at.n_seqs;
-  const int tile0 = blockIdx.x / a.at.Hk / a.at.n_seqs;
-  Seq sq;
-  {
-    const int2 q = rows_of(a.at.cu_q, seq, a.at.n_seqs, a.at.total_q);
-    sq.q0 = q.x;
-    sq.ql = q.y;
-    sq.k0 = 0;
-    sq.kl = min(max(a.at.k_len[seq], 0), a.at.pages.capacity);
-  }
-  const int off = sq.kl - sq.ql, nq = (sq.ql + TT - 1) / TT;
-  // the last CTA of a sequence takes the key tiles that are left, where there are more than foreseen
-  const int tiles = (sq.kl + CH - 1) / CH, tile1 = tile0 == a.key_tiles - 1 ? tiles : min(tile0 + 1, tiles);
-  if (tile0 >= tile1 || nq == 0) return;
+  const int split = a.split, rank = blockIdx.x % split, team = blockIdx.x / split, teams = gridDim.x / split;
+  // the lengths of a sequence, and its key tiles (none without queries)
+  auto rows = [&](int s) { return rows_of(a.at.cu_q, s, a.at.n_seqs, a.at.total_q); };
+  auto keys = [&](int s) { return min(max(a.at.k_len[s], 0), a.at.pages.capacity); };
+  auto tiles = [&](int s) { return rows(s).y > 0 ? (keys(s) + CH - 1) / CH : 0; };
+  const int own = lane < a.at.n_seqs ? tiles(lane) : 0;
 
   if (warp == LOADS && lane == 0) {
     for (int k = 0; k < MANY_SLOTS; ++k) {
@@ -125,7 +120,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) k_weigh_many(const __grid_con
       tc::mbar_init(&sm.empty[k], 1);
     }
     tc::mbar_init(&sm.barK, 1);
-    for (int k = 0; k < NG; ++k) {
+    for (int k = 0; k < NS; ++k) {
       tc::mbar_init(&sm.barS[k], 1);
       tc::mbar_init(&sm.barE[k], 128);
     }
@@ -136,21 +131,42 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) k_weigh_many(const __grid_con
   __syncthreads();
   tc::fence_after();
   tc::Wait w;
-  const Paged<CH> pg(a.at, seq, sq.kl);
-  // the first query tile that sees the key tile
-  auto first = [&](int tile) { return max(0, tile * CH - off) / TT; };
 
-  // `t` counts query tiles over all of the CTA's key tiles
-  int t = 0, done = 0;
-  for (int tile = tile0; tile < tile1; ++tile, ++done) {
-    const int q0 = first(tile);
+  // Units of a key tile and head, those with the most queries first, to the teams there and
+  // back again.  `t` counts query tiles over all of the CTA's units.
+  int t = 0, done = 0, buf = 0;
+  const int cr = tid & 127, tok = cr / G;  // column cr of a query tile: its token there
+  const bool row_ok = cr < TT * G;
+  for (int n = 0;; ++n, ++done) {
+    const int unit = n * teams + (n & 1 ? teams - 1 - team : team);
+    const int kh = unit % a.at.Hk;
+    // (a tile's index from its sequence's end)
+    const int2 from_end = find_nth(tiles, own, a.at.n_seqs, unit / a.at.Hk);
+    if (from_end.x < 0) break;
+    const int seq = from_end.x;
+    Seq sq;
+    {
+      const int2 q = rows(seq);
+      sq.q0 = q.x;
+      sq.ql = q.y;
+      sq.k0 = 0;
+      sq.kl = keys(seq);
+    }
+    const int off = sq.kl - sq.ql, nq = (sq.ql + TT - 1) / TT, tile = (sq.kl + CH - 1) / CH - 1 - from_end.y;
+    const Paged<CH> pg(a.at, seq, sq.kl);
+    const long row = ((long)sq.q0 + tok) * a.at.Hq + kh * G + cr - tok * G;  // of the log-sums, in the first tile
+    // the CTA's query tiles, of those that see the key tile: q0 + split j
+    const int q0 = max(0, tile * CH - off) / TT + rank, mine = max(0, nq - q0 + split - 1) / split;
+    float all = 0.f;
+    float* at = nullptr;
     if (warp == LOADS) {
-      // (the sums' barrier at a tile's end orders this load behind the last product of the tile before)
+      // (the barrier at a unit's end orders this load behind the last product of the unit before)
       pg.load(a.at.pages, sm.k, &a.at.k, kh, tile * CH, pg.entry(a.at.pages, tile * CH), &sm.barK);
       if (lane == 0) {
-        for (int i = q0; i < nq && w.ok; ++i, ++t) {
+        for (int j = 0; j < mine && w.ok; ++j, ++t) {
           if (t >= MANY_SLOTS) w.on(&sm.empty[t % MANY_SLOTS], t / MANY_SLOTS - 1);
-          if (w.ok) load_group(sm.slot[t % MANY_SLOTS], &a.at.q, kh, G, sq.q0 + i * TT, &sm.full[t % MANY_SLOTS]);
+          if (w.ok)
+            load_group(sm.slot[t % MANY_SLOTS], &a.at.q, kh, G, sq.q0 + (q0 + split * j) * TT, &sm.full[t % MANY_SLOTS]);
         }
         // no copy is in flight when the CTA ends
         if (w.ok) {
@@ -163,58 +179,86 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) k_weigh_many(const __grid_con
         }
       }
       __syncwarp();
-    } else if (warp == ISSUES) {
+    } else if (warp >= ISSUES) {
       const uint32_t lead = tc::elect_leader();
       w.warp_on(&sm.barK, done);
-      for (int i = q0; i < nq; ++i, ++t) {
+      for (int j = 0; j < mine; ++j, ++t) {
+        if ((t ^ warp) & 1) continue;  // the other issuer's
         w.warp_on(&sm.full[t % MANY_SLOTS], t / MANY_SLOTS);
-        if (t >= NG) w.warp_on(&sm.barE[t % NG], t / NG - 1);
+        if (t >= NS) w.warp_on(&sm.barE[t % NS], t / NS - 1);
         tc::fence_after();
-        tc::gemm128_by<false>(lead, sm.tmem + 128 * (t % NG), smem_u32(sm.k), smem_u32(sm.slot[t % MANY_SLOTS]), false);
-        tc::commit_by(lead, &sm.barS[t % NG]);
-        if (tile + 1 < tile1 || i + MANY_SLOTS < nq) tc::commit_by(lead, &sm.empty[t % MANY_SLOTS]);
+        tc::gemm128_by<false>(lead, sm.tmem + 128 * (t % NS), smem_u32(sm.k), smem_u32(sm.slot[t % MANY_SLOTS]), false);
+        tc::commit_by(lead, &sm.barS[t % NS]);
+        tc::commit_by(lead, &sm.empty[t % MANY_SLOTS]);
       }
     } else {
       const int x = warp >> 2, r = tid & 127, key = tile * CH + r;
       const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
       const float sc = a.at.scale * LOG2E;
-      float* at = x == 0 ? place(a, pg, kh, key) : nullptr;
-      float sum = 0.f, nl = 0.f;
-      int lim = -1;
-      // the group's tiles: every fourth one, counted over the whole CTA
-      int i = q0 + (x + NG - t % NG) % NG;
-      if (i < nq) column(a, sq, kh, G, TT, i * TT, r, nl, lim);
-      for (; i < nq; i += NG) {
-        const int u = t + i - q0;
-        // the group's columns: all of its threads have read the ones before
-        asm volatile("bar.sync %0, 128;" ::"r"(1 + x) : "memory");
-        sm.cols[x].nl[r] = nl;
-        sm.cols[x].lim[r] = lim;
+      if (x == 0 && rank == 0) at = place(a, pg, kh, key);
+      float sum[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
+      // the group's: every fourth one, counted over all of the CTA's key tiles
+      int j = (x + NG - t % NG) % NG;
+      auto read = [&](int j) {
+        const int i = q0 + split * j;
+        l = row_ok && i * TT + tok < sq.ql ? a.lse[row + (long)i * TT * a.at.Hq] : -INFINITY;
+      };
+      if (j < mine) read(j);
+      for (; j < mine; j += NG) {
+        const int u = t + j;
+        Columns<CH>& cols = sm.cols[x][buf];
+        const bool sees = l != -INFINITY;  // (a log-sum of NaN makes the keys' weights NaN)
+        const int lim = sees ? (q0 + split * j) * TT + tok + off : -1;
+        cols.nl[r] = sees ? -l * LOG2E : 0.f;
+        cols.lim[r] = lim;
         const int least = __reduce_min_sync(0xffffffffu, lim);
-        if (lane == 0) sm.clean[x][warp & 3] = least;
+        if (lane == 0) sm.clean[x][buf][warp & 3] = least;
+        // (two sets of columns in turn: whoever writes one again has met the others here since)
         asm volatile("bar.sync %0, 128;" ::"r"(1 + x) : "memory");
-        if (i + NG < nq) column(a, sq, kh, G, TT, (i + NG) * TT, r, nl, lim);
-        w.warp_on(&sm.barS[x], u / NG);
+        if (j + NG < mine) read(j + NG);
+        const int* clean = sm.clean[x][buf];
+        buf ^= 1;
+        w.warp_on(&sm.barS[u % NS], u / NS);
         tc::fence_after();
-        const uint32_t S = sm.tmem + 128 * x + lane_base;
-        float part[4];
-#pragma unroll
-        for (int g = 0; g < 4; ++g) part[g] = sum32(S, sm.cols[x], 32 * g, key, tile * CH + CH - 1, sm.clean[x][g], sc);
+        const uint32_t S = sm.tmem + 128 * (u % NS) + lane_base;
+        const int end = tile * CH + CH - 1;
+        float v[32];
+        tc::ld32(S, v);
+        add32(v, cols, 0, key, end, clean[0], sc, sum);
+        tc::ld32(S + 32, v);
+        add32(v, cols, 32, key, end, clean[1], sc, sum);
+        tc::ld32(S + 64, v);
+        add32(v, cols, 64, key, end, clean[2], sc, sum);
+        tc::ld32(S + 96, v);
         tc::fence_before();
-        tc::mbar_arrive(&sm.barE[x]);
-        sum += (part[0] + part[1]) + (part[2] + part[3]);
+        tc::mbar_arrive(&sm.barE[u % NS]);
+        add32(v, cols, 96, key, end, clean[3], sc, sum);
       }
-      t += nq - q0;
-      if (x > 0) sm.sums[x - 1][r] = sum;
+      t += mine;
+      all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      if (x > 0) sm.sums[x - 1][r] = all;
       asm volatile("bar.sync %0, %1;" ::"n"(1 + NG), "n"(128 * NG) : "memory");
       if (x == 0) {
 #pragma unroll
-        for (int g = 0; g < NG - 1; ++g) sum += sm.sums[g][r];
-        if (at && sum != 0.f) atomicAdd(at, sum);
+        for (int g = 0; g < NG - 1; ++g) all += sm.sums[g][r];
+        if (rank == 1) tc::st_cluster(&sm.other[r], 0, all);
       }
     }
-    if (tile + 1 < tile1) __syncthreads();
+    if (split > 1) tc::cluster_sync();
+    if (at) {
+      if (split > 1) all += sm.other[tid];
+      if (all != 0.f) atomicAdd(at, all);
+    }
+    // the sums have been read, and every warp is done with the unit
+    if (split > 1)
+      tc::cluster_sync();
+    else
+      __syncthreads();
   }
+  // every commit has arrived before the CTA ends
+  if (warp >= ISSUES && warp < LOADS)
+    for (int u = max(0, t - MANY_SLOTS); u < t; ++u)
+      if (((u ^ warp) & 1) == 0) w.warp_on(&sm.empty[u % MANY_SLOTS], u / MANY_SLOTS);
   if (!w.ok && a.at.status) atomicOr(a.at.status, 1);
   tc::fence_before();
   __syncthreads();
@@ -421,7 +465,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) k_weigh_few(const __grid_const
       const Paged<CH> pg(a.at, run.seq, run.sq.kl);
       const int key = run.tile * CH + r;
       float* at = place(a, pg, run.kh, key);
-      float sum = 0.f;
+      float part[4] = {0.f, 0.f, 0.f, 0.f};
       for (int qt = 0; qt < nq; ++qt, ++u) {
         const int rows = min(TT, run.sq.ql - qt * TT) * G;
         if (nq > 1 || fresh) {
@@ -441,11 +485,15 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) k_weigh_few(const __grid_const
         tc::fence_after();
         const uint32_t S = sm.tmem + FEW_ROWS * (u % FEW_S) + lane_base;
         // (columns past the product's hold what earlier ones left; no row there sees a key)
-        for (int g = 0; 32 * g < rows; ++g)
-          sum += sum32(S, sm.cols, 32 * g, key, run.tile * CH + CH - 1, sm.clean[g], sc);
+        for (int g = 0; 32 * g < rows; ++g) {
+          float v[32];
+          tc::ld32(S + 32 * g, v);
+          add32(v, sm.cols, 32 * g, key, run.tile * CH + CH - 1, sm.clean[g], sc, part);
+        }
         tc::fence_before();
         tc::mbar_arrive(&sm.barE[u % FEW_S]);
       }
+      const float sum = (part[0] + part[1]) + (part[2] + part[3]);
       if (at && sum != 0.f) atomicAdd(at, sum);
       fresh = run.last_of_head();
     }
@@ -465,8 +513,21 @@ cudaError_t launch_weigh(const WeighArgs& a, cudaStream_t s) {
   static_assert(sizeof(ManySmem) + 1024 <= 227 * 1024 && 2 * (sizeof(FewSmem) + 2048) <= 228 * 1024, "shared memory");
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  const dim3 grid = dim3(a.few ? (unsigned)a.ctas : (unsigned)a.at.Hk * (unsigned)a.at.n_seqs * (unsigned)a.key_tiles);
-  return launch_pdl(kernel, grid, dim3(a.few ? FEW_THREADS : MANY_THREADS), smem, s, a);
+  if (a.few) return launch_pdl(kernel, dim3((unsigned)a.ctas), dim3(FEW_THREADS), smem, s, a);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.split * a.ctas));
+  cfg.blockDim = dim3(MANY_THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)a.split;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 }  // namespace gdn

@@ -90,15 +90,15 @@ def test_paged_argument_errors(L):
         assert fwd(ks=bad) == ARG and fwd(vs=bad) == ARG
     assert fwd(nbytes=need - 1) == WS and fwd(ws=None) == WS
 
-    def weigh(q=FAKE, kp=FAKE, lse=FAKE, table=FAKE, klen=FAKE, w=FAKE, n=2, nq=2, pages=400, page=64, wide=313, Hk=2, d=128,
+    def weigh(q=FAKE, kp=FAKE, lse=FAKE, table=FAKE, klen=FAKE, w=FAKE, n=2, nq=2, mq=0, pages=400, page=64, wide=313, Hk=2, d=128,
               scale=0.1, sq=512, ks=strides(), st=313, ws=FAKE, nbytes=256):
-        return L.gdn_attn_paged_weights(q, kp, lse, table, klen, FAKE, w, n, nq, 10000, pages, page, wide, 4, Hk, d, scale, sq, ks,
+        return L.gdn_attn_paged_weights(q, kp, lse, table, klen, FAKE, w, n, nq, mq, 10000, pages, page, wide, 4, Hk, d, scale, sq, ks,
                                         st, ws, nbytes, None)
     assert weigh(n=0) == OK and weigh(nq=0) == OK and weigh(pages=0) == OK and weigh(wide=0) == OK
     assert weigh(d=64) == SHAPE and weigh(page=24) == SHAPE and weigh(Hk=3) == ARG and weigh(st=312) == ARG
     assert weigh(lse=None) == ARG and weigh(w=None) == ARG and weigh(table=None) == ARG and weigh(q=None) == ARG
     assert weigh(lse=MISAL) == ARG and weigh(w=MISAL) == ARG and weigh(kp=MISAL) == ARG and weigh(ks=strides(row=64)) == ARG
-    assert weigh(scale=-1.0) == ARG and weigh(nbytes=255) == WS
+    assert weigh(scale=-1.0) == ARG and weigh(mq=-1) == ARG and weigh(nbytes=255) == WS
 
     keep = gdn.cache_evict_workspace_bytes(2, 313 * 64, 1000, 2)
     assert keep >= 2 * 2 * 1000 * 4 and gdn.cache_evict_workspace_bytes(2, 100, 1000, 2) < keep
