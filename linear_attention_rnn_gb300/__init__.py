@@ -763,8 +763,6 @@ def _check_table(t, name, n):
 
 @functools.lru_cache(maxsize=64)
 def _pair_axes(pair_axis, n_pairs):
-    if pair_axis is None:
-        return None
     if len(pair_axis) != n_pairs or not all(0 <= a < 256 for a in pair_axis):
         raise ValueError(f"pair_axis must name an axis for each of the {n_pairs} pairs")
     return bytes(pair_axis)
@@ -780,14 +778,16 @@ def _rope_dims(q, k, positions, inv_freq, q_weight, k_weight, pair_axis):
     Hk = ks[-2]
     n = qs[0] if len(qs) == 3 else rows.numel()
     sq, sk = _check_rows(q, "q", Hq, d, n), _check_rows(k, "k", Hk, d, n)
-    _check(q_weight, "q_weight", torch.float32, (d,))
-    _check(k_weight, "k_weight", torch.float32, (d,))
-    axes, pairs = 1, 0
+    if q_weight is not None:
+        _check(q_weight, "q_weight", torch.float32, (d,))
+    if k_weight is not None:
+        _check(k_weight, "k_weight", torch.float32, (d,))
+    axes, pairs, table = 1, 0, None
     if inv_freq is not None:
         _check(inv_freq, "inv_freq", torch.float32)
         if inv_freq.dim() != 1:
             raise ValueError("inv_freq must hold a frequency for each pair")
-        pairs = inv_freq.numel()
+        pairs = inv_freq.shape[0]
         if positions is None:
             raise ValueError("inv_freq needs positions")
         _check(positions, "positions", torch.int32)
@@ -796,15 +796,15 @@ def _rope_dims(q, k, positions, inv_freq, q_weight, k_weight, pair_axis):
                 raise ValueError(f"positions has shape {tuple(positions.shape)}, expected {tuple(rows)} "
                                  f"or an axis more in front")
             axes = positions.shape[0]
-    if pair_axis is not None and pair_axis.__class__ is not tuple:
-        pair_axis = tuple(int(x) for x in pair_axis)
-    return n, Hq, Hk, d, axes, pairs, _pair_axes(pair_axis, pairs), sq, sk
+    if pair_axis is not None:
+        table = _pair_axes(pair_axis if pair_axis.__class__ is tuple else tuple(int(x) for x in pair_axis), pairs)
+    return n, Hq, Hk, d, axes, pairs, table, sq, sk
 
 
 def _rows_out(t, name, like, n, H, d):
     """An output's rows: contiguous ones made here, or the caller's (a part of a wider buffer)."""
     if t is None:
-        return torch.empty(like.shape, dtype=torch.bfloat16, device=like.device), H * d
+        return torch.empty_like(like, memory_format=torch.contiguous_format), H * d
     if t.shape != like.shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(like.shape)}")
     return t, _check_rows(t, name, H, d, n)

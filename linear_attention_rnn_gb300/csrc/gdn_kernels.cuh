@@ -357,7 +357,7 @@ cudaError_t launch_decay_fold(const DecayFoldArgs& a, cudaStream_t s);
 cudaError_t launch_weigh(const WeighArgs& a, cudaStream_t s);
 // the keys that stay and their lengths, then the copies
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s);
-int rope_blocks(int backward, long n, int H, int sms);  // blocks for n tokens of H heads in all
+int rope_blocks(int backward, long n, int H, int (*sms)());  // blocks for n tokens of H heads in all
 cudaError_t launch_rope_fwd(const RopeArgs& a, cudaStream_t s);
 cudaError_t launch_rope_bwd(const RopeArgs& a, cudaStream_t s);
 cudaError_t launch_attn_fwd(const AttnArgs& a, cudaStream_t s);

@@ -72,13 +72,13 @@ int gdn_rope_fwd(const void* q, const void* k, const float* q_weight, const floa
   RopeArgs a = rope_args(n, n_axes, n_pairs, pair_axis, positions, inv_freq, interleaved, eps);
   a.part[0] = part(q, q_out, q_weight, q_stride, qo_stride, Hq);
   a.part[1] = part(k, k_out, k_weight, k_stride, ko_stride, Hk);
-  a.blocks = rope_blocks(0, n, Hq + Hk, sm_count());
+  a.blocks = rope_blocks(0, n, Hq + Hk, sm_count);
   return cuda_status(launch_rope_fwd(a, static_cast<cudaStream_t>(stream)));
 }
 
 size_t gdn_rope_workspace_bytes(int n, int Hq, int Hk, int d) {
   if (rope_check(n, Hq, Hk, d, 1, 0, nullptr, nullptr, nullptr, nullptr, nullptr, 0.f) != GDN_OK) return 0;
-  return up((size_t)rope_blocks(1, n, Hq + Hk, sm_count()) * 2 * HD * sizeof(float));
+  return up((size_t)rope_blocks(1, n, Hq + Hk, sm_count) * 2 * HD * sizeof(float));
 }
 
 int gdn_rope_bwd(const void* q, const void* k, const float* q_weight, const float* k_weight, const int* positions,
@@ -113,7 +113,7 @@ int gdn_rope_bwd(const void* q, const void* k, const float* q_weight, const floa
   a.part[1].sg = dko_stride;
   a.part[0].dw = dq_weight;
   a.part[1].dw = dk_weight;
-  a.blocks = rope_blocks(1, n, Hq + Hk, sm_count());
+  a.blocks = rope_blocks(1, n, Hq + Hk, sm_count);
   if (dq_weight || dk_weight) {
     if (!ws || ws_bytes < gdn_rope_workspace_bytes(n, Hq, Hk, d)) return GDN_ERR_WORKSPACE;
     a.partial = static_cast<float*>(ws);
@@ -152,7 +152,7 @@ int gdn_rope_append(const void* q, const void* k, const void* v, const float* q_
   a.part[1].sy_head = k_strides->head;
   a.part[2].sy_row = v_strides->row;
   a.part[2].sy_head = v_strides->head;
-  a.blocks = rope_blocks(0, n, Hq + 2 * Hk, sm_count());
+  a.blocks = rope_blocks(0, n, Hq + 2 * Hk, sm_count);
   return cuda_status(launch_rope_fwd(a, static_cast<cudaStream_t>(stream)));
 }
 

@@ -453,15 +453,19 @@ cudaError_t launch(RopeArgs a, cudaStream_t s) {
   a.longer = (int)(steps % warps);
   const auto kernel = a.interleaved ? k_rope<BACK, true, PAGED> : k_rope<BACK, false, PAGED>;
   constexpr size_t smem = sizeof(RopeSmem<BACK>);
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  return e != cudaSuccess ? e : launch_pdl(kernel, dim3((unsigned)a.blocks), dim3(ROPE_THREADS), smem, s, a);
+  if (smem > 48 * 1024) {  // (what a block may have without being asked)
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(kernel, dim3((unsigned)a.blocks), dim3(ROPE_THREADS), smem, s, a);
 }
 
 }  // namespace
 
-int rope_blocks(int backward, long n, int H, int sms) {
+int rope_blocks(int backward, long n, int H, int (*sms)()) {
   const long steps = n * ((H + SIDE - 1) / SIDE), need = (steps + WARPS - 1) / WARPS;
-  const long most = (long)(backward ? 2 : 3) * sms;
+  if (need <= 64) return (int)need;  // (fewer than any device has SMs for: not worth the question)
+  const long most = (long)(backward ? 2 : 3) * sms();
   return (int)(need < most ? need : most);
 }
 
