@@ -762,10 +762,10 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) k_paged_few(const __grid_const
 }
 
 // ---- the items that were cut ------------------------------------------------------------------
-// o = sum_s e^{lse_s - lse} o_s over the parts in their order.  Blocks (c, y): rows 8 y .. of the
-// item that begins in run c and is cut, one to a warp.  A part of NaN makes
-// the row NaN, as it would be in one piece.
-constexpr int JOIN_ROWS = 8;
+// o = sum_s e^{lse_s - lse} o_s over the parts, in a fixed order.  Blocks (c, y): 32 / P rows of
+// the item that begins in run c and is cut, 8 P lanes to a row: eight have 16 columns each of
+// every P-th part.  A part of NaN makes the row NaN, as it would be in one piece.
+template <int P>
 __global__ void __launch_bounds__(256) k_paged_join(const __grid_constant__ PagedArgs pa) {
   pdl_wait();
   pdl_release();
@@ -773,47 +773,66 @@ __global__ void __launch_bounds__(256) k_paged_join(const __grid_constant__ Page
   const int cta = blockIdx.x, rows = pa.few ? CH : 2 * CH;
   const Join j = pa.joins[cta];
   if (j.last < 0) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = a.Hq / a.Hk, TT = CH / G;
+  const int l = threadIdx.x & 7, g = (threadIdx.x >> 3) & (P - 1), G = a.Hq / a.Hk, TT = CH / G, n = j.last - cta + 1;
+  const int rr = (blockIdx.y * 256 + threadIdx.x) / (8 * P), r = rr & (CH - 1), tok = (rr / CH) * TT + r / G;
+  if (r >= TT * G || tok >= j.toks) return;  // (the lanes of a row together)
+  const unsigned mask = P == 4 ? 0xffffffffu : 0xffu << (threadIdx.x & 24);
   // part s: the last slot of the run in which the item begins, then the first ones of the others
-  auto at = [&](int s, int r) { return (long)(s == 0 ? 2 * cta + 1 : 2 * (cta + s)) * rows + r; };
-  const int n = j.last - cta + 1, rr = blockIdx.y * JOIN_ROWS + warp, r = rr & (CH - 1), tok = (rr / CH) * TT + r / G;
-  if (rr >= rows || r >= TT * G || tok >= j.toks) return;
+  auto at = [&](int s) { return (long)(s == 0 ? 2 * cta + 1 : 2 * (cta + s)) * rows + rr; };
   float top = -INFINITY;
   bool nan = false;  // (which fmaxf passes over)
-  for (int s = lane; s < n; s += 32) {
-    const float l = a.part_lse[at(s, rr)];
-    nan |= isnan(l);
-    top = fmaxf(top, l);
+  for (int s = 8 * g + l; s < n; s += 8 * P) {
+    const float x = a.part_lse[at(s)];
+    nan |= isnan(x);
+    top = fmaxf(top, x);
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (__any_sync(0xffffffffu, nan)) top = NAN;
-  float total = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
-  if (top != -INFINITY)
-    for (int s0 = 0; s0 < n; s0 += 4) {  // four parts at a time
-      float f[4];
-      float4 p[4];
+  for (int o = 4 * P; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(mask, top, o));
+  if (__any_sync(mask, nan)) top = NAN;
+  float total = 0.f, y[16];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        f[u] = s0 + u < n ? a.part_lse[at(s0 + u, rr)] : -INFINITY;
-        p[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (f[u] != -INFINITY) p[u] = *reinterpret_cast<const float4*>(a.part + at(s0 + u, rr) * HD + 4 * lane);
+  for (int k = 0; k < 16; ++k) y[k] = 0.f;
+  if (top != -INFINITY) {
+    for (int s0 = g; s0 < n; s0 += 2 * P) {  // two parts at a time
+      float f[2];
+      float4 v[2][4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int s = s0 + u * P;
+        f[u] = s < n ? a.part_lse[at(s)] : -INFINITY;
+        const float* p = a.part + at(s < n ? s : s0) * HD + 4 * l;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[u][k] = *reinterpret_cast<const float4*>(p + 32 * k);
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float e = f[u] != -INFINITY ? expf(f[u] - top) : 0.f;
+      for (int u = 0; u < 2; ++u) {
+        if (f[u] == -INFINITY) continue;  // (a part without keys for the row has not been written)
+        const float e = expf(f[u] - top);
         total += e;
-        y[0] += e * p[u].x;
-        y[1] += e * p[u].y;
-        y[2] += e * p[u].z;
-        y[3] += e * p[u].w;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          y[4 * k] += e * v[u][k].x;
+          y[4 * k + 1] += e * v[u][k].y;
+          y[4 * k + 2] += e * v[u][k].z;
+          y[4 * k + 3] += e * v[u][k].w;
+        }
       }
     }
+  }
+#pragma unroll
+  for (int o = 8; o < 8 * P; o <<= 1) {
+    total += __shfl_xor_sync(mask, total, o);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) y[k] += __shfl_xor_sync(mask, y[k], o);
+  }
   const float inv = total != 0.f ? 1.f / total : 0.f;
   const long row = ((long)j.row + tok) * a.Hq + j.kh * G + r % G;
-  *reinterpret_cast<uint2*>(a.o + row * HD + 4 * lane) =
-      make_uint2(pack_bf16(inv * y[0], inv * y[1]), pack_bf16(inv * y[2], inv * y[3]));
-  if (a.lse && lane == 0) a.lse[row] = total != 0.f ? top + logf(total) : -INFINITY;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (k % P == g)
+      *reinterpret_cast<uint2*>(a.o + row * HD + 32 * k + 4 * l) =
+          make_uint2(pack_bf16(inv * y[4 * k], inv * y[4 * k + 1]), pack_bf16(inv * y[4 * k + 2], inv * y[4 * k + 3]));
+  if (a.lse && l == 0 && g == 0) a.lse[row] = total != 0.f ? top + logf(total) : -INFINITY;
 }
 
 }  // namespace
@@ -834,7 +853,9 @@ cudaError_t launch_attn_paged(const PagedArgs& a, cudaStream_t s) {
   }
   e = launch_pdl(kernel, dim3((unsigned)a.ctas), dim3(a.few ? FEW_THREADS : MANY_THREADS), smem, s, a);
   if (e != cudaSuccess || a.ctas <= 1) return e;
-  return launch_pdl(k_paged_join, dim3((unsigned)a.ctas, (a.few ? 1 : 2) * CH / JOIN_ROWS), dim3(256), 0, s, a);
+  const unsigned rows = (a.few ? 1 : 2) * CH;
+  return a.many_parts ? launch_pdl(k_paged_join<4>, dim3((unsigned)a.ctas, rows / 8), dim3(256), 0, s, a)
+                      : launch_pdl(k_paged_join<1>, dim3((unsigned)a.ctas, rows / 32), dim3(256), 0, s, a);
 }
 
 }  // namespace gdn

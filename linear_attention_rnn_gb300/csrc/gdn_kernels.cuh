@@ -249,6 +249,7 @@ struct PagedArgs {
   AttnArgs at;          // part, part_lse: two slots to a CTA, of 128 rows (few) or 256
   attn::Join* joins;    // one to a CTA
   int ctas, few;        // few: k_paged_few, whose sequences are best of one query tile
+  int many_parts;       // items that are cut have several parts, as far as the host knows
 };
 
 // The weight that attention gives to each key in pages (gdn_weigh.cu).

@@ -523,7 +523,7 @@ static int paged_check(int n_seqs, int total_q, int max_k, int n_pages, int page
 // takes longer ones too, tile by tile), which the totals or max_q say; else k_paged_many.  CTAs: two to an
 // SM, or one, but no more than there can be tiles of 128 keys.
 struct PagedPlan {
-  int ctas, few;
+  int ctas, few, many_parts;
   size_t status, joins, part, part_lse, total;
 };
 static PagedPlan paged_plan(int n_seqs, int total_q, long long max_q, long long max_k, int Hq, int Hk) {
@@ -532,6 +532,7 @@ static PagedPlan paged_plan(int n_seqs, int total_q, long long max_q, long long 
   p.few = total_q <= TT || (max_q > 0 && max_q <= TT);
   const long long items = (total_q / (p.few ? TT : 2 * TT) + n_seqs) * Hk, most = (p.few ? 2 : 1) * sm_count();
   p.ctas = (int)(items < most && items * tiles < most ? items * tiles : most);
+  p.many_parts = p.ctas >= 4 * items;
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t o = off;
@@ -597,6 +598,7 @@ int gdn_attn_paged(const void* q, const void* k_pages, const void* v_pages, cons
   pa.joins = at<attn::Join>(ws, p.joins);
   pa.ctas = p.ctas;
   pa.few = p.few;
+  pa.many_parts = p.many_parts;
   return cuda_status(launch_attn_paged(pa, static_cast<cudaStream_t>(stream)));
 }
 
