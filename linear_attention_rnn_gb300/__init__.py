@@ -997,6 +997,7 @@ def cache_evict(k_pages, v_pages, weights, page_table, k_len, budget: int, *, re
     n = k_len.shape[0]
     _check(k_len, "k_len", torch.int32)
     pages, st = _check_table(page_table, "page_table", n)
+    budget, recent = min(int(budget), 2 ** 31 - 1), min(int(recent), 2 ** 31 - 1)
     to_pages, sto = _check_table(to_table, "to_table", n) if to_table is not None else (0, 0)
     if new_len is None:
         new_len = torch.empty(n, dtype=torch.int32, device=k_len.device)
@@ -1004,10 +1005,10 @@ def cache_evict(k_pages, v_pages, weights, page_table, k_len, budget: int, *, re
         _check(new_len, "new_len", torch.int32, (n,))
     if _several_devices:
         _check_devices(k_pages, v_pages, weights, page_table, k_len, to_table, new_len, workspace)
-    wp, wn, ws = _scratch_all(cache_evict_workspace_bytes(n, pages * page, int(budget), Hk), k_len.device, workspace)
+    wp, wn, ws = _scratch_all(cache_evict_workspace_bytes(n, pages * page, budget, Hk), k_len.device, workspace)
     rc = lib().gdn_cache_evict(k_pages.data_ptr(), v_pages.data_ptr(), weights.data_ptr(), page_table.data_ptr(),
                                _ptr(to_table), k_len.data_ptr(), new_len.data_ptr(), n, P, page, pages, to_pages, Hk, d,
-                               int(budget), int(recent), ctypes.byref(ks), ctypes.byref(vs), st, sto, wp, wn,
+                               budget, recent, ctypes.byref(ks), ctypes.byref(vs), st, sto, wp, wn,
                                _stream(k_len.device))
     if rc != GDN_OK:
         raise GDNError(rc, "gdn_cache_evict")

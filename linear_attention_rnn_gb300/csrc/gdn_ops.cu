@@ -675,7 +675,7 @@ int gdn_cache_evict(void* k_pages, void* v_pages, float* weights, const int* pag
       !aligned(new_len, 4))
     return GDN_ERR_ARG;
   if (n_seqs == 0) return GDN_OK;
-  if (!new_len) return GDN_ERR_ARG;
+  if (!new_len || new_len == k_len) return GDN_ERR_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (n_pages == 0 || max_pages == 0) return cuda_status(cudaMemsetAsync(new_len, 0, (size_t)n_seqs * sizeof(int), s));
   if (!k_pages || !v_pages || !weights || !page_table || !k_len) return GDN_ERR_ARG;

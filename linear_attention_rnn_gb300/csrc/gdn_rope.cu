@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(ROPE_THREADS, BACK ? 2 : 3) k_rope(const __gri
     if (fleft > 0) {
       const int h = SIDE * fi + side, off = fi * (SIDE * HD);
       if (h < H) {
-        if (!BACK || normed) {
+        if (!BACK || (h < q.H ? q.w : k.w)) {
           const bf16* x = (h < q.H ? qx : !PAGED || h < Hqk ? kx : vx) + off;
           fetch16(&sm.row[warp][fslot][0][0][lane], x);
           fetch16(&sm.row[warp][fslot][0][1][lane], x + hop);

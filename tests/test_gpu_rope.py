@@ -72,6 +72,33 @@ def test_one_of_the_norms(gdn_lib):
     check(gdn_lib, dict(x, wk=None))
 
 
+def test_rows_that_are_not_read(gdn_lib):
+    """Without its weight a part's rows are not read in the backward, and may be left out in C."""
+    d = cuda(make(40, 4, 2, 64, seed=5))
+    want = gdn_lib.rope_bwd(d["q"], d["k"], d["pos"], d["freq"], d["gq"], d["gk"], q_weight=d["wq"])
+    got = [torch.empty_like(t) for t in want[:3]]
+    ws = torch.empty(gdn_lib.rope_workspace_bytes(40, 4, 2), dtype=torch.uint8, device="cuda")
+    p = lambda t: t.data_ptr()
+    rc = gdn_lib.lib().gdn_rope_bwd(p(d["q"]), None, p(d["wq"]), None, p(d["pos"]), p(d["freq"]), None, p(d["gq"]), p(d["gk"]),
+                                    p(got[0]), p(got[1]), p(got[2]), None, 40, 4, 2, 128, 1, 64, 0, EPS, 512, 256, 512, 256, 512,
+                                    256, p(ws), ws.numel(), torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert rc == 0 and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_infinities_stay_where_they_are(gdn_lib):
+    """What is not turned passes as it is, and an infinity reaches its pair alone."""
+    x = make(6, 2, 1, 32, seed=6, norm=False)
+    x["q"][2, 1, 100], x["q"][3, 0, 7] = float("inf"), float("-inf")
+    d = cuda(x)
+    q, _ = gdn_lib.rope_fwd(d["q"], d["k"], d["pos"], d["freq"])
+    assert torch.equal(q[..., 64:], d["q"][..., 64:])
+    bad = ~torch.isfinite(q[..., :64])
+    where = torch.zeros_like(bad)
+    where[3, 0, 7] = where[3, 0, 39] = True
+    assert not (bad & ~where).any()
+
+
 @pytest.mark.parametrize("axis", [(0,) * 16 + (1,) * 24 + (2,) * 24, tuple(j % 3 for j in range(64)), (1,) * 64])
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_several_axes(gdn_lib, axis, interleaved):

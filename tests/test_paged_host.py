@@ -103,7 +103,7 @@ def test_paged_argument_errors(L):
     keep = gdn.cache_evict_workspace_bytes(2, 313 * 64, 1000, 2)
     assert keep >= 2 * 2 * 1000 * 4 and gdn.cache_evict_workspace_bytes(2, 100, 1000, 2) < keep
 
-    def evict(kp=FAKE, w=FAKE, table=FAKE, to=None, klen=FAKE, new=FAKE, n=2, pages=400, page=64, wide=313, to_wide=16, Hk=2, d=128,
+    def evict(kp=FAKE, w=FAKE, table=FAKE, to=None, klen=FAKE, new=P(1 << 22), n=2, pages=400, page=64, wide=313, to_wide=16, Hk=2, d=128,
               budget=1000, recent=10, vs=strides(), st=313, sto=16, ws=FAKE, nbytes=1 << 30):
         return L.gdn_cache_evict(kp, FAKE, w, table, to, klen, new, n, pages, page, wide, to_wide, Hk, d, budget, recent, strides(),
                                  vs, st, sto, ws, nbytes, None)
@@ -111,6 +111,7 @@ def test_paged_argument_errors(L):
     assert evict(d=96) == SHAPE and evict(page=17) == SHAPE
     assert evict(Hk=0) == ARG and evict(budget=-1) == ARG and evict(recent=-1) == ARG and evict(wide=-1) == ARG and evict(st=1) == ARG
     assert evict(kp=None) == ARG and evict(w=None) == ARG and evict(table=None) == ARG and evict(klen=None) == ARG
+    assert evict(klen=P(1 << 21), new=P(1 << 21)) == ARG     # lengths read and written at once
     assert evict(new=None) == ARG and evict(new=MISAL) == ARG and evict(to=MISAL) == ARG and evict(vs=None) == ARG
     # target pages for fewer keys than may stay
     assert evict(to=P(1 << 21), to_wide=15) == ARG and evict(to=P(1 << 21), sto=15) == ARG
