@@ -28,7 +28,7 @@ namespace {
 
 constexpr int SELECT_THREADS = 1024, SELECT_WARPS = SELECT_THREADS / 32;
 constexpr int SELECT_HELD = 49152;  // weights that shared memory holds
-constexpr int MOVE_THREADS = 256, MOVE_ROWS = 64;  // rows of a list to a block (16 side by side)
+constexpr int MOVE_THREADS = 256, MOVE_ROWS = 32;  // rows of a list to a block (16 side by side)
 constexpr int WALK_THREADS = 1024, WALK_ROWS = 128;
 
 // The sequence's keys, and where the ones that always stay begin.
@@ -227,7 +227,7 @@ __device__ __forceinline__ int row_at(const EvictArgs& a, const int* table, int 
   return (unsigned)e < (unsigned)a.pages.n_pages ? e * a.pages.page + (i - t * a.pages.page) : -1;
 }
 
-__global__ void __launch_bounds__(MOVE_THREADS, 4) k_evict_move(const __grid_constant__ EvictArgs a) {
+__global__ void __launch_bounds__(MOVE_THREADS, 8) k_evict_move(const __grid_constant__ EvictArgs a) {
   const int kh = blockIdx.x % a.Hk, seq = blockIdx.x / a.Hk;
   const int l = threadIdx.x & 15, i0 = threadIdx.x >> 4;
   pdl_wait();
