@@ -7,8 +7,10 @@
 // threads.  Keys that a tile's queries do not all see take a masked sum, 32 columns at a
 // time; the other columns take one fma, one exponential and one addition each, in pairs.
 //
-// Many queries (prompts): a CTA, or a pair of them, keeps one tile of 128 keys; it streams the query tiles
-// that see it through a ring; three groups of four warps take them in turn.
+// Many queries (prompts): a CTA, or a pair of them, takes one tile of 128 keys after another and
+// streams the query tiles that see it through a ring; four groups of four warps take them in
+// turn.  One warp plans the key tiles and loads them, one loads the queries; the loads and
+// products of a key tile begin while the one before is summed up.
 // Few queries (tokens over caches): a CTA keeps the query tile and streams key tiles;
 // only as many columns are formed as there are rows, two CTAs to an SM, each with an
 // equal run of all sequences' key tiles.
@@ -32,6 +34,18 @@ struct Columns {
   float nl[N];
   int lim[N];
 };
+
+// Whether all 128 threads of named barrier `id` say so.
+__device__ __forceinline__ bool all128(int id, bool ok) {
+  uint32_t y;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.and.pred q, %2, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(y)
+      : "r"((uint32_t)ok), "r"(id)
+      : "memory");
+  return y != 0;
+}
 
 // Column r of the query tile of TT tokens from token tok0 on.
 __device__ __forceinline__ void column(const WeighArgs& a, const Seq& sq, int kh, int G, int TT, int tok0, int r,
@@ -83,18 +97,29 @@ __device__ __forceinline__ float* place(const WeighArgs& a, const Paged<CH>& pg,
 // waits before the next one would come on top of that (a prompt of 8192 tokens: 131 us with
 // one, 114 with two).  An even number of slots and of S buffers, so that a barrier's phases
 // are one issuer's, in their order.
-constexpr int MANY_GROUPS = 4, MANY_THREADS = 128 * MANY_GROUPS + 96, MANY_SLOTS = 4, MANY_S = 4;
+constexpr int MANY_GROUPS = 4, MANY_THREADS = 128 * MANY_GROUPS + 128, MANY_SLOTS = 4, MANY_S = 4;
 static_assert(MANY_SLOTS % 2 == 0 && MANY_S % 2 == 0, "each issuer's own");
+static_assert(MANY_GROUPS == MANY_S, "a group's scores lie in one buffer");
+
+// A unit of work: a key tile and head, and the CTA's share of the query tiles that see it.
+struct Unit {
+  int kh, tile, kl, off;  // off: keys ahead of the first query
+  int row, ql;            // the sequence's rows of q
+  int q0, mine;           // the first of the CTA's query tiles, and how many
+  const int* table;
+};
 
 struct ManySmem {
-  unsigned char k[TILE];
+  unsigned char k[2][TILE];
   unsigned char slot[MANY_SLOTS][TILE];
   Columns<CH> cols[MANY_GROUPS][2];
   int clean[MANY_GROUPS][2][4];  // of 32 columns: the last key that all of their rows see
-  float sums[MANY_GROUPS - 1][CH];
-  float other[CH];  // the other CTA's sums
+  float sums[2][MANY_GROUPS - 1][CH];
+  float other[2][CH];  // the other CTA's sums
+  Unit unit[2];
   uint64_t full[MANY_SLOTS], empty[MANY_SLOTS];
-  uint64_t barK, barS[MANY_S], barE[MANY_S];
+  // the unit there, its keys there, both free again
+  uint64_t barU[2], barK[2], barF[2], barS[MANY_S], barE[MANY_S];
   uint32_t tmem;
 };
 
@@ -102,7 +127,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) k_weigh_many(const __grid_con
   extern __shared__ unsigned char raw[];
   ManySmem& sm = *reinterpret_cast<ManySmem*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
   const int tid = threadIdx.x, lane = tid & 31, warp = tc::warp_index();
-  constexpr int ISSUES = 4 * MANY_GROUPS, LOADS = ISSUES + 2, NG = MANY_GROUPS, NS = MANY_S;
+  constexpr int ISSUES = 4 * MANY_GROUPS, LOADS = ISSUES + 2, PLANS = ISSUES + 3, NG = MANY_GROUPS, NS = MANY_S;
   pdl_wait();
   pdl_release();
   clear_status(a.at.status);
@@ -112,14 +137,24 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) k_weigh_many(const __grid_con
   auto rows = [&](int s) { return rows_of(a.at.cu_q, s, a.at.n_seqs, a.at.total_q); };
   auto keys = [&](int s) { return min(max(a.at.k_len[s], 0), a.at.pages.capacity); };
   auto tiles = [&](int s) { return rows(s).y > 0 ? (keys(s) + CH - 1) / CH : 0; };
-  const int own = lane < a.at.n_seqs ? tiles(lane) : 0;
+  int2 lane_q = make_int2(0, 0);  // of the first 32 sequences
+  int lane_kl = 0;
+  if (lane < a.at.n_seqs) {
+    lane_q = rows(lane);
+    lane_kl = keys(lane);
+  }
+  const int own = lane_q.y > 0 ? (lane_kl + CH - 1) / CH : 0;
 
   if (warp == LOADS && lane == 0) {
     for (int k = 0; k < MANY_SLOTS; ++k) {
       tc::mbar_init(&sm.full[k], 1);
       tc::mbar_init(&sm.empty[k], 1);
     }
-    tc::mbar_init(&sm.barK, 1);
+    for (int k = 0; k < 2; ++k) {
+      tc::mbar_init(&sm.barU[k], 1);
+      tc::mbar_init(&sm.barK[k], 1);
+      tc::mbar_init(&sm.barF[k], 4 * NG + 3);
+    }
     for (int k = 0; k < NS; ++k) {
       tc::mbar_init(&sm.barS[k], 1);
       tc::mbar_init(&sm.barE[k], 128);
@@ -127,101 +162,172 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) k_weigh_many(const __grid_con
     tc::mbar_fence_init();
   }
   if (warp == 0) tc::alloc(&sm.tmem, 512);
+  // Units, those with the most queries first, to the teams there and back again.  Every warp
+  // knows how many are the team's, whatever its waits come to.
+  int n_units;
+  {
+    long all = __reduce_add_sync(0xffffffffu, own);
+    for (int s = 32; s < a.at.n_seqs; s += 32) all += __reduce_add_sync(0xffffffffu, s + lane < a.at.n_seqs ? tiles(s + lane) : 0);
+    all *= a.at.Hk;
+    const long rounds = all / teams, rest = all - rounds * teams;
+    n_units = (int)rounds + ((rounds & 1 ? teams - 1 - team : team) < rest ? 1 : 0);
+  }
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
   tc::Wait w;
 
-  // Units of a key tile and head, those with the most queries first, to the teams there and
-  // back again.  `t` counts query tiles over all of the CTA's units.
-  int t = 0, done = 0, buf = 0;
-  const int cr = tid & 127, tok = cr / G;  // column cr of a query tile: its token there
-  const bool row_ok = cr < TT * G;
-  for (int n = 0;; ++n, ++done) {
-    const int unit = n * teams + (n & 1 ? teams - 1 - team : team);
-    const int kh = unit % a.at.Hk;
-    // (a tile's index from its sequence's end)
-    const int2 from_end = find_nth(tiles, own, a.at.n_seqs, unit / a.at.Hk);
-    if (from_end.x < 0) break;
-    const int seq = from_end.x;
-    Seq sq;
-    {
-      const int2 q = rows(seq);
-      sq.q0 = q.x;
-      sq.ql = q.y;
-      sq.k0 = 0;
-      sq.kl = keys(seq);
+  // t counts query tiles over all of the CTA's units.
+  int t = 0;
+  if (warp == PLANS) {
+    for (int n = 0; n < n_units; ++n) {
+      const int b = n & 1;
+      const long unit = (long)n * teams + (n & 1 ? teams - 1 - team : team);
+      // (a tile's index from its sequence's end)
+      const int2 from_end = find_nth(tiles, own, a.at.n_seqs, (int)(unit / a.at.Hk));
+      const int seq = max(from_end.x, 0);
+      int2 q;
+      Unit u;
+      if (seq < 32) {
+        q = make_int2(__shfl_sync(0xffffffffu, lane_q.x, seq), __shfl_sync(0xffffffffu, lane_q.y, seq));
+        u.kl = __shfl_sync(0xffffffffu, lane_kl, seq);
+      } else {
+        q = rows(seq);
+        u.kl = keys(seq);
+      }
+      u.kh = (int)(unit % a.at.Hk);
+      u.off = u.kl - q.y;
+      u.tile = (u.kl + CH - 1) / CH - 1 - from_end.y;
+      u.row = q.x;
+      u.ql = q.y;
+      u.table = a.at.table + (long)seq * a.at.pages.table_stride;
+      // the CTA's query tiles, of those that see the key tile: q0 + split j
+      u.q0 = max(0, u.tile * CH - u.off) / TT + rank;
+      u.mine = max(0, (q.y + TT - 1) / TT - u.q0 + split - 1) / split;
+      const Paged<CH> pg(a.at, seq, u.kl);
+      const int entry = pg.entry(a.at.pages, u.tile * CH);
+      if (n >= 2) w.on(&sm.barF[b], n / 2 - 1);
+      w.ok = __all_sync(0xffffffffu, w.ok);
+      if (w.ok) {
+        if (lane == 0) {
+          sm.unit[b] = u;
+          tc::mbar_arrive(&sm.barU[b]);
+        }
+        pg.load(a.at.pages, sm.k[b], &a.at.k, u.kh, u.tile * CH, entry, &sm.barK[b]);
+      }
+      if (split > 1) {  // (in step with the groups, a unit later)
+        if (n > 0) tc::cluster_wait();
+        tc::cluster_arrive();
+      }
     }
-    const int off = sq.kl - sq.ql, nq = (sq.ql + TT - 1) / TT, tile = (sq.kl + CH - 1) / CH - 1 - from_end.y;
-    const Paged<CH> pg(a.at, seq, sq.kl);
-    const long row = ((long)sq.q0 + tok) * a.at.Hq + kh * G + cr - tok * G;  // of the log-sums, in the first tile
-    // the CTA's query tiles, of those that see the key tile: q0 + split j
-    const int q0 = max(0, tile * CH - off) / TT + rank, mine = max(0, nq - q0 + split - 1) / split;
-    float all = 0.f;
-    float* at = nullptr;
-    if (warp == LOADS) {
-      // (the barrier at a unit's end orders this load behind the last product of the unit before)
-      pg.load(a.at.pages, sm.k, &a.at.k, kh, tile * CH, pg.entry(a.at.pages, tile * CH), &sm.barK);
+    if (lane == 0) {  // no copy is in flight when the CTA ends
+      if (w.ok)
+        for (int n = max(0, n_units - 2); n < n_units; ++n) w.on(&sm.barK[n & 1], n / 2);
+      if (!w.ok)
+        for (int k = 0; k < 2; ++k) tc::mbar_wait_sleep(&sm.barK[k], 0, 4000000LL);
+    }
+    __syncwarp();
+    if (split > 1 && n_units > 0) tc::cluster_wait();
+  } else if (warp == LOADS) {
+    for (int n = 0; n < n_units; ++n) {
       if (lane == 0) {
-        for (int j = 0; j < mine && w.ok; ++j, ++t) {
+        w.on(&sm.barU[n & 1], n / 2);
+        const Unit u = sm.unit[n & 1];
+        tc::mbar_arrive(&sm.barF[n & 1]);
+        for (int j = 0; w.ok && j < u.mine; ++j, ++t) {
           if (t >= MANY_SLOTS) w.on(&sm.empty[t % MANY_SLOTS], t / MANY_SLOTS - 1);
           if (w.ok)
-            load_group(sm.slot[t % MANY_SLOTS], &a.at.q, kh, G, sq.q0 + (q0 + split * j) * TT, &sm.full[t % MANY_SLOTS]);
-        }
-        // no copy is in flight when the CTA ends
-        if (w.ok) {
-          w.on(&sm.barK, done);
-          for (int u = max(0, t - MANY_SLOTS); u < t; ++u) w.on(&sm.full[u % MANY_SLOTS], u / MANY_SLOTS);
-        }
-        if (!w.ok) {
-          tc::mbar_wait_sleep(&sm.barK, done & 1, 4000000LL);
-          for (int k = 0; k < MANY_SLOTS; ++k) tc::mbar_wait_sleep(&sm.full[k], 0, 4000000LL);
+            load_group(sm.slot[t % MANY_SLOTS], &a.at.q, u.kh, G, u.row + (u.q0 + split * j) * TT, &sm.full[t % MANY_SLOTS]);
         }
       }
       __syncwarp();
-    } else if (warp >= ISSUES) {
-      const uint32_t lead = tc::elect_leader();
-      w.warp_on(&sm.barK, done);
+      if (split > 1) {
+        if (n > 0) tc::cluster_wait();
+        tc::cluster_arrive();
+      }
+    }
+    if (lane == 0) {  // no copy is in flight when the CTA ends
+      if (w.ok)
+        for (int u = max(0, t - MANY_SLOTS); u < t; ++u) w.on(&sm.full[u % MANY_SLOTS], u / MANY_SLOTS);
+      if (!w.ok)
+        for (int k = 0; k < MANY_SLOTS; ++k) tc::mbar_wait_sleep(&sm.full[k], 0, 4000000LL);
+    }
+    __syncwarp();
+    if (split > 1 && n_units > 0) tc::cluster_wait();
+  } else if (warp >= ISSUES) {
+    const uint32_t lead = tc::elect_leader();
+    for (int n = 0; n < n_units; ++n) {
+      const int b = n & 1;
+      w.warp_on(&sm.barU[b], n / 2);
+      w.ok = __all_sync(0xffffffffu, w.ok);
+      const int mine = w.ok ? sm.unit[b].mine : 0;
+      w.warp_on(&sm.barK[b], n / 2);
       for (int j = 0; j < mine; ++j, ++t) {
         if ((t ^ warp) & 1) continue;  // the other issuer's
         w.warp_on(&sm.full[t % MANY_SLOTS], t / MANY_SLOTS);
         if (t >= NS) w.warp_on(&sm.barE[t % NS], t / NS - 1);
         tc::fence_after();
-        tc::gemm128_by<false>(lead, sm.tmem + 128 * (t % NS), smem_u32(sm.k), smem_u32(sm.slot[t % MANY_SLOTS]), false);
+        tc::gemm128_by<false>(lead, sm.tmem + 128 * (t % NS), smem_u32(sm.k[b]), smem_u32(sm.slot[t % MANY_SLOTS]), false);
         tc::commit_by(lead, &sm.barS[t % NS]);
         tc::commit_by(lead, &sm.empty[t % MANY_SLOTS]);
       }
-    } else {
-      const int x = warp >> 2, r = tid & 127, key = tile * CH + r;
-      const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
-      const float sc = a.at.scale * LOG2E;
-      if (x == 0 && rank == 0) at = place(a, pg, kh, key);
-      float sum[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
-      // the group's: every fourth one, counted over all of the CTA's key tiles
-      int j = (x + NG - t % NG) % NG;
-      auto read = [&](int j) {
-        const int i = q0 + split * j;
-        l = row_ok && i * TT + tok < sq.ql ? a.lse[row + (long)i * TT * a.at.Hq] : -INFINITY;
-      };
-      if (j < mine) read(j);
-      for (; j < mine; j += NG) {
-        const int u = t + j;
+      tc::commit_by(lead, &sm.barF[b]);  // (at once where the unit had no product of this warp's)
+      if (split > 1) {
+        if (n > 0) tc::cluster_wait();
+        tc::cluster_arrive();
+      }
+    }
+    // every commit has arrived before the CTA ends
+    for (int u = max(0, t - MANY_SLOTS); u < t; ++u)
+      if (((u ^ warp) & 1) == 0) w.warp_on(&sm.empty[u % MANY_SLOTS], u / MANY_SLOTS);
+    for (int n = max(0, n_units - 2); n < n_units; ++n) w.warp_on(&sm.barF[n & 1], n / 2);
+    if (split > 1 && n_units > 0) tc::cluster_wait();
+  } else {
+    const int x = warp >> 2, r = tid & 127, tok = r / G;  // column r of a query tile: its token there
+    const bool row_ok = r < TT * G, adds = x == 0 && rank == 0;
+    const uint32_t S = sm.tmem + 128 * x + ((uint32_t)(32 * (warp & 3)) << 16);
+    const float sc = a.at.scale * LOG2E;
+    int buf = 0;
+    // the unit, the table's entry for the thread's key, and the first log-sum, which are asked for
+    // while the unit before is summed up
+    Unit u;
+    int entry, j;
+    float l;
+    auto read = [&](int i) {  // of the CTA's i-th query tile
+      const int at = (u.q0 + split * i) * TT + tok;
+      l = row_ok && at < u.ql ? a.lse[((long)u.row + at) * a.at.Hq + u.kh * G + r - tok * G] : -INFINITY;
+    };
+    auto take = [&](int n) {
+      w.warp_on(&sm.barU[n & 1], n / 2);
+      w.ok = all128(1 + x, w.ok);  // (the group takes as many steps in all of its threads)
+      u = sm.unit[n & 1];
+      if (!w.ok) u.mine = u.kl = 0;
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sm.barF[n & 1]);
+      const int key = u.tile * CH + r;
+      entry = adds && key < u.kl ? u.table[a.at.pages.page_of(key)] : -1;
+      j = (x + NG - t % NG) % NG;  // the group's: every fourth one, counted over all units
+      if (j < u.mine) read(j);
+    };
+    if (n_units > 0) take(0);
+    for (int n = 0; n < n_units; ++n) {
+      const int key = u.tile * CH + r, kh = u.kh, page = entry, end = u.tile * CH + CH - 1;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      for (; j < u.mine; j += NG) {
         Columns<CH>& cols = sm.cols[x][buf];
         const bool sees = l != -INFINITY;  // (a log-sum of NaN makes the keys' weights NaN)
-        const int lim = sees ? (q0 + split * j) * TT + tok + off : -1;
+        const int lim = sees ? (u.q0 + split * j) * TT + tok + u.off : -1;
         cols.nl[r] = sees ? -l * LOG2E : 0.f;
         cols.lim[r] = lim;
         const int least = __reduce_min_sync(0xffffffffu, lim);
         if (lane == 0) sm.clean[x][buf][warp & 3] = least;
         // (two sets of columns in turn: whoever writes one again has met the others here since)
         asm volatile("bar.sync %0, 128;" ::"r"(1 + x) : "memory");
-        if (j + NG < mine) read(j + NG);
+        if (j + NG < u.mine) read(j + NG);
         const int* clean = sm.clean[x][buf];
         buf ^= 1;
-        w.warp_on(&sm.barS[u % NS], u / NS);
+        w.warp_on(&sm.barS[x], (t + j) / NS);
         tc::fence_after();
-        const uint32_t S = sm.tmem + 128 * (u % NS) + lane_base;
-        const int end = tile * CH + CH - 1;
         float v[32];
         tc::ld32(S, v);
         add32(v, cols, 0, key, end, clean[0], sc, sum);
@@ -231,34 +337,29 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) k_weigh_many(const __grid_con
         add32(v, cols, 64, key, end, clean[2], sc, sum);
         tc::ld32(S + 96, v);
         tc::fence_before();
-        tc::mbar_arrive(&sm.barE[u % NS]);
+        tc::mbar_arrive(&sm.barE[x]);
         add32(v, cols, 96, key, end, clean[3], sc, sum);
       }
-      t += mine;
-      all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      if (x > 0) sm.sums[x - 1][r] = all;
+      t += u.mine;
+      if (n + 1 < n_units) take(n + 1);
+      // (two sets of sums in turn: whoever writes one again has met the reader here since)
+      float all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      if (x > 0) sm.sums[n & 1][x - 1][r] = all;
       asm volatile("bar.sync %0, %1;" ::"n"(1 + NG), "n"(128 * NG) : "memory");
       if (x == 0) {
 #pragma unroll
-        for (int g = 0; g < NG - 1; ++g) all += sm.sums[g][r];
-        if (rank == 1) tc::st_cluster(&sm.other[r], 0, all);
+        for (int g = 0; g < NG - 1; ++g) all += sm.sums[n & 1][g][r];
+        if (rank == 1) tc::st_cluster(&sm.other[n & 1][r], 0, all);
       }
+      if (split > 1) {
+        tc::cluster_arrive();
+        tc::cluster_wait();
+        if (adds) all += sm.other[n & 1][r];
+      }
+      if ((unsigned)page < (unsigned)a.at.pages.n_pages && all != 0.f)
+        atomicAdd(a.weights + ((long)page * a.at.Hk + kh) * a.at.pages.page + (key - a.at.pages.page_of(key) * a.at.pages.page), all);
     }
-    if (split > 1) tc::cluster_sync();
-    if (at) {
-      if (split > 1) all += sm.other[tid];
-      if (all != 0.f) atomicAdd(at, all);
-    }
-    // the sums have been read, and every warp is done with the unit
-    if (split > 1)
-      tc::cluster_sync();
-    else
-      __syncthreads();
   }
-  // every commit has arrived before the CTA ends
-  if (warp >= ISSUES && warp < LOADS)
-    for (int u = max(0, t - MANY_SLOTS); u < t; ++u)
-      if (((u ^ warp) & 1) == 0) w.warp_on(&sm.empty[u % MANY_SLOTS], u / MANY_SLOTS);
   if (!w.ok && a.at.status) atomicOr(a.at.status, 1);
   tc::fence_before();
   __syncthreads();

@@ -464,59 +464,81 @@ def test_one_query_tile_over_items():
         few_model([rnd.choice([0, 1, 1, 2, 3, 6]) for _ in range(rnd.randint(1, 8))], seed)
 
 
-def weigh_many_model(units, seed, slots=4, groups=4, buffers=4):
-    """k_weigh_many: units of that many query tiles, two issuers in turn, a unit's end meets all."""
+def weigh_many_model(units, seed, slots=4, groups=4, buffers=4, sets=2):
+    """k_weigh_many: units of that many query tiles, two issuers in turn; loads and products run on into
+    the next unit, the groups meet at a unit's end.  `sets`: of sums, in turn."""
     m = Loose(seed)
     r = Ring(m, slots)
-    barK, barS, barE = Bar(1), [Bar(1) for _ in range(buffers)], [Bar(2) for _ in range(buffers)]
-    K, S = [None], [None] * buffers
-    everyone, phases = Bar(3 + 2 * groups), [0] * (3 + 2 * groups)
+    barU, barK, barF = [Bar(1), Bar(1)], [Bar(1), Bar(1)], [Bar(2 * groups + 3), Bar(2 * groups + 3)]
+    barS, barE = [Bar(1) for _ in range(buffers)], [Bar(2) for _ in range(buffers)]
+    unit, K, S, sums_of = [None] * 2, [None] * 2, [None] * buffers, [[None] * groups for _ in range(sets)]
+    everyone, phases = Bar(2 * groups), [0] * (2 * groups)
 
-    def loads(me):
-        t = 0
+    def plans():
         for e, n in enumerate(units):
-            K[0] = None
-            barK.arrive(tx=1)
+            if e >= 2:
+                yield from wait(barF[e % 2], e // 2 - 1)
+            unit[e % 2] = e
+            barU[e % 2].arrive()
+            K[e % 2] = None
+            barK[e % 2].arrive(tx=1)
 
             def land(e=e):
-                K[0] = e
-                barK.complete(1)
+                K[e % 2] = e
+                barK[e % 2].complete(1)
             m.copy(land)
             yield
+        for e in range(max(0, len(units) - 2), len(units)):
+            yield from wait(barK[e % 2], e // 2)
+
+    def loads():
+        t = 0
+        for e, n in enumerate(units):
+            yield from wait(barU[e % 2], e // 2)
+            assert unit[e % 2] == e, "another unit"
+            barF[e % 2].arrive()
             for _ in range(n):
                 yield from r.load(t)
                 t += 1
-            yield from wait(barK, e)
-            for u in range(max(0, t - slots), t):
-                yield from r.landed(u)
-            yield from meet(everyone, phases, me)
+        for u in range(max(0, t - slots), t):
+            yield from r.landed(u)
 
-    def issues(w, me):
+    def issues(w):
         t = 0
         for e, n in enumerate(units):
-            yield from wait(barK, e)
+            yield from wait(barU[e % 2], e // 2)
+            assert unit[e % 2] == e, "another unit"
+            yield from wait(barK[e % 2], e // 2)
             for _ in range(n):
                 if t % 2 == w:
                     yield from r.landed(t)
                     if t >= buffers:
                         yield from wait(barE[t % buffers], t // buffers - 1)
-                    assert K[0] == e, "other keys"
 
-                    def done(over=r.use(t), t=t):
+                    def done(over=r.use(t), t=t, e=e):
+                        assert K[e % 2] == e, "other keys"
                         over()
                         S[t % buffers] = t
                     m.mma(done, barS[t % buffers].arrive)
                     r.release(t)
                     yield
                 t += 1
-            yield from meet(everyone, phases, me)
+            m.mma(barF[e % 2].arrive)
         for u in range(max(0, t - slots), t):
             if u % 2 == w:
                 yield from wait(r.empty[u % slots], u // slots)
+        for e in range(max(0, len(units) - 2), len(units)):
+            yield from wait(barF[e % 2], e // 2)
 
     def sums(x, me):
+        def take(e):
+            yield from wait(barU[e % 2], e // 2)
+            assert unit[e % 2] == e, "another unit"
+            yield
+            barF[e % 2].arrive()
         t = 0
-        for n in units:
+        yield from take(0)
+        for e, n in enumerate(units):
             j = (x + groups - t % groups) % groups
             while j < n:
                 u = t + j
@@ -527,8 +549,16 @@ def weigh_many_model(units, seed, slots=4, groups=4, buffers=4):
                 barE[u % buffers].arrive()
                 j += groups
             t += n
+            if e + 1 < len(units):
+                yield from take(e + 1)
+            if me % 2 == 0 and x > 0:
+                sums_of[e % sets][x] = e
             yield from meet(everyone, phases, me)
-    for a in [loads(0), issues(0, 1), issues(1, 2)] + [sums(x, 3 + 2 * x + i) for x in range(groups) for i in range(2)]:
+            if x == 0:
+                for g in range(1, groups):
+                    yield
+                    assert sums_of[e % sets][g] == e, "sums of another unit"
+    for a in [plans(), loads(), issues(0), issues(1)] + [sums(x, 2 * x + i) for x in range(groups) for i in range(2)]:
         m.add(a)
     m.run()
 
@@ -536,12 +566,17 @@ def weigh_many_model(units, seed, slots=4, groups=4, buffers=4):
 def test_weights_of_many_queries():
     for seed in range(150):
         rnd = random.Random(seed)
-        weigh_many_model([rnd.choice([0, 1, 2, 3, 5, 9]) for _ in range(rnd.randint(1, 5))], seed)
+        weigh_many_model([rnd.choice([0, 1, 2, 3, 5, 9]) for _ in range(rnd.randint(1, 7))], seed)
 
 
 def test_two_issuers_of_an_odd_ring_fail():
     """A slot's phases are then not one issuer's: it may ask for one that is two ahead."""
     assert fails(lambda seed: weigh_many_model([25], seed, slots=5), 400) > 0
+
+
+def test_one_set_of_sums_fails():
+    """A group that goes on writes its next sums while the last ones are read."""
+    assert fails(lambda seed: weigh_many_model([1, 0, 2, 1, 1, 0, 1], seed, sets=1), 400) > 0
 
 
 def weigh_few_model(run, seed):
