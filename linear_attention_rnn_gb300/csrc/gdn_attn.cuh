@@ -32,14 +32,11 @@ struct Lanes {
   int2 q, k;
   int used;
 };
-__device__ __forceinline__ int2 keys_of(const AttnArgs& a, int s) {
-  return a.table ? make_int2(0, a.pages.capacity) : rows_of(a.cu_k, s, a.n_seqs, a.total_k);
-}
 __device__ __forceinline__ Lanes read_lanes(const AttnArgs& a) {
   const int s = min((int)(threadIdx.x & 31), a.n_seqs - 1);
   Lanes l;
   l.q = rows_of(a.cu_q, s, a.n_seqs, a.total_q);
-  l.k = keys_of(a, s);
+  l.k = rows_of(a.cu_k, s, a.n_seqs, a.total_k);
   l.used = a.k_len ? min(max(a.k_len[s], 0), l.k.y) : l.k.y;
   return l;
 }
@@ -52,7 +49,7 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs& a, const Lanes& l, int s) 
     used = __shfl_sync(0xffffffffu, l.used, s);
   } else {
     q = rows_of(a.cu_q, s, a.n_seqs, a.total_q);
-    k = keys_of(a, s);
+    k = rows_of(a.cu_k, s, a.n_seqs, a.total_k);
     used = a.k_len ? min(max(a.k_len[s], 0), k.y) : k.y;
   }
   Seq r;

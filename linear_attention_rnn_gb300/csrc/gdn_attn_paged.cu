@@ -93,8 +93,8 @@ __device__ __forceinline__ void leave_whole(Stage& st, bf16* o, const int (&at)[
 // ---- sequences of more than one query tile ---------------------------------------------------
 constexpr int NSLOT = 4;
 constexpr int MANY_THREADS = 384;
-constexpr int MANY_EXTRA = 512;   // keys that an item's start and end take the time of
-constexpr int MANY_RUN = 768;     // width of a run, at least
+constexpr int MANY_EXTRA = 256;   // keys that an item's start and end take the time of
+constexpr int MANY_RUN = 512;     // width of a run, at least
 constexpr int REGS_LAUNCH = 168, REGS_SOFTMAX = 208, REGS_ISSUE = 88;  // (as in gdn_attn_fwd.cu)
 static_assert(2 * REGS_SOFTMAX + REGS_ISSUE <= 3 * REGS_LAUNCH, "the groups' registers come from the block's");
 
@@ -169,40 +169,40 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) k_paged_many(const __grid_con
     if (warp == 9) {
       int t = 0, qc[2] = {0, 0};  // ring tiles, query tiles so far
       for (;;) {
-      for (int e = 0; e < sm.runs.count && w.ok; ++e) {
-        const Item& it = sm.runs.item[e];
-        int n[2];
-        const int nmax = tiles(it, n), kb = it.kb, kh = it.kh, row = it.row;
-        const bool dual = it.toks <= TT;
-        if (nmax == 0) continue;
-        const Paged<CH> pg(a, it.seq, it.kl);
-        int entry = pg.entry(a.pages, kb * CH);
-        for (int i = 0; i < nmax && w.ok; ++i) {
-          const int key0 = (kb + i) * CH, now = entry;
-          if (i + 1 < nmax) entry = pg.entry(a.pages, key0 + CH);
+        for (int e = 0; e < sm.runs.count && w.ok; ++e) {
+          const Item& it = sm.runs.item[e];
+          int n[2];
+          const int nmax = tiles(it, n), kb = it.kb, kh = it.kh, row = it.row;
+          const bool dual = it.toks <= TT;
+          if (nmax == 0) continue;
+          const Paged<CH> pg(a, it.seq, it.kl);
+          int entry = pg.entry(a.pages, kb * CH);
+          for (int i = 0; i < nmax && w.ok; ++i) {
+            const int key0 = (kb + i) * CH, now = entry;
+            if (i + 1 < nmax) entry = pg.entry(a.pages, key0 + CH);
 #pragma unroll
-          for (int v = 0; v < 2; ++v, ++t) {
-            if (t >= NSLOT) w.on(&sm.empty[t % NSLOT], t / NSLOT - 1);
-            w.ok = __all_sync(0xffffffffu, w.ok);
-            if (w.ok) pg.load(a.pages, sm.slot[t % NSLOT], v ? &a.v : &a.k, kh, key0, now, &sm.full[t % NSLOT]);
-          }
-          if (i > 0) continue;
-          // (behind the first key tile, which needs no free query buffer)
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-            if (n[x] > 0 && !(dual && x)) {
-              if (qc[x] > 0) w.on(&sm.barQF[x], qc[x] - 1);
+            for (int v = 0; v < 2; ++v, ++t) {
+              if (t >= NSLOT) w.on(&sm.empty[t % NSLOT], t / NSLOT - 1);
               w.ok = __all_sync(0xffffffffu, w.ok);
-              if (w.ok && lane == 0)
-                load_group(sm.q[x], &a.q, kh, G, row + x * TT, &sm.barQ[x]);
-              ++qc[x];
+              if (w.ok) pg.load(a.pages, sm.slot[t % NSLOT], v ? &a.v : &a.k, kh, key0, now, &sm.full[t % NSLOT]);
             }
+            if (i > 0) continue;
+            // (behind the first key tile, which needs no free query buffer)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              if (n[x] > 0 && !(dual && x)) {
+                if (qc[x] > 0) w.on(&sm.barQF[x], qc[x] - 1);
+                w.ok = __all_sync(0xffffffffu, w.ok);
+                if (w.ok && lane == 0)
+                  load_group(sm.q[x], &a.q, kh, G, row + x * TT, &sm.barQ[x]);
+                ++qc[x];
+              }
+          }
         }
-      }
-      if (!sm.runs.more) break;
-      block_sync();  // the items have been read
-      plan.fill(sm.runs, pa.joins, (int)blockIdx.x);
-      block_sync();
+        if (!sm.runs.more) break;
+        block_sync();  // the items have been read
+        plan.fill(sm.runs, pa.joins, (int)blockIdx.x);
+        block_sync();
       }
       if (lane == 0) {  // no copy is in flight when the CTA ends
         if (w.ok) {
@@ -313,182 +313,182 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) k_paged_many(const __grid_con
     const float sc = a.scale * LOG2E;
     int t0 = 0, s0 = 0, items = 0;  // ring tiles, the group's key tiles and items so far
     for (;;) {
-    for (int e = 0; e < sm.runs.count; ++e) {
-      const Item& it = sm.runs.item[e];
-      int n[2];
-      const int nmax = tiles(it, n);
-      const bool dual = it.toks <= TT;
-      const int mine = n[x], kb = it.kb, kl = it.kl, step = dual ? 2 : 1, at0 = dual ? x : 0;  // the group's key tiles
-      const int tok = (dual ? 0 : x * TT) + r / G;
-      const bool valid = r < TT * G && tok < it.toks;
-      const int lim = valid ? it.lim + tok : -1;  // the last key that the row sees
-      const bool any = __any_sync(0xffffffffu, valid);
-      const Paged<CH> pg(a, it.seq, kl);
-      float m = -INFINITY, l = 0.f;
-      int asked = 0;
-      if (mine > 0) asked = pg.ask(a.pages, (kb + at0) * CH);
-      for (int i = 0; i < mine; ++i) {
-        const int tile = at0 + step * i, key0 = (kb + tile) * CH;
-        const uint32_t absent = pg.absent(a.pages, asked);  // 16 keys to a bit
-        asked = pg.ask(a.pages, key0 + step * CH);
-        w.warp_on(&sm.barS[x], s0 + i);
-        if (key0 + CH > kl) {  // rows past the keys: whatever they hold, they count as zero
-          // (behind S, which says that the issuer is at this item: a group whose part of the last one
-          // was short may be whole rounds of the ring ahead of it, where a phase's parity says nothing)
-          const int t = t0 + 2 * tile + 1;
-          w.warp_on(&sm.full[t % NSLOT], t / NSLOT);
-          zero_rows(sm.slot[t % NSLOT], kl - key0, tid & 127, 128);
-          tc::fence_proxy_async();
-        }
-        tc::fence_after();
-        if (any) {
-          float v[128];
-          tc::ld64(S, *reinterpret_cast<float(*)[64]>(v));
-          tc::ld64(S + 64, *reinterpret_cast<float(*)[64]>(v + 64));
-          if (key0 + CH - 1 > lim) {
-#pragma unroll
-            for (int j = 0; j < 128; ++j) v[j] = key0 + j <= lim ? v[j] : -INFINITY;
+      for (int e = 0; e < sm.runs.count; ++e) {
+        const Item& it = sm.runs.item[e];
+        int n[2];
+        const int nmax = tiles(it, n);
+        const bool dual = it.toks <= TT;
+        const int mine = n[x], kb = it.kb, kl = it.kl, step = dual ? 2 : 1, at0 = dual ? x : 0;  // the group's key tiles
+        const int tok = (dual ? 0 : x * TT) + r / G;
+        const bool valid = r < TT * G && tok < it.toks;
+        const int lim = valid ? it.lim + tok : -1;  // the last key that the row sees
+        const bool any = __any_sync(0xffffffffu, valid);
+        const Paged<CH> pg(a, it.seq, kl);
+        float m = -INFINITY, l = 0.f;
+        int asked = 0;
+        if (mine > 0) asked = pg.ask(a.pages, (kb + at0) * CH);
+        for (int i = 0; i < mine; ++i) {
+          const int tile = at0 + step * i, key0 = (kb + tile) * CH;
+          const uint32_t absent = pg.absent(a.pages, asked);  // 16 keys to a bit
+          asked = pg.ask(a.pages, key0 + step * CH);
+          w.warp_on(&sm.barS[x], s0 + i);
+          if (key0 + CH > kl) {  // rows past the keys: whatever they hold, they count as zero
+            // (behind S, which says that the issuer is at this item: a group whose part of the last one
+            // was short may be whole rounds of the ring ahead of it, where a phase's parity says nothing)
+            const int t = t0 + 2 * tile + 1;
+            w.warp_on(&sm.full[t % NSLOT], t / NSLOT);
+            zero_rows(sm.slot[t % NSLOT], kl - key0, tid & 127, 128);
+            tc::fence_proxy_async();
           }
-          if (absent) {
+          tc::fence_after();
+          if (any) {
+            float v[128];
+            tc::ld64(S, *reinterpret_cast<float(*)[64]>(v));
+            tc::ld64(S + 64, *reinterpret_cast<float(*)[64]>(v + 64));
+            if (key0 + CH - 1 > lim) {
 #pragma unroll
-            for (int j = 0; j < 128; ++j) v[j] = absent >> (j / 16) & 1u ? -INFINITY : v[j];
-          }
-          float mt[4] = {v[0], v[1], v[2], v[3]};
+              for (int j = 0; j < 128; ++j) v[j] = key0 + j <= lim ? v[j] : -INFINITY;
+            }
+            if (absent) {
 #pragma unroll
-          for (int j = 4; j < 124; j += 8) {
+              for (int j = 0; j < 128; ++j) v[j] = absent >> (j / 16) & 1u ? -INFINITY : v[j];
+            }
+            float mt[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-            for (int c = 0; c < 4; ++c) mt[c] = tc::max3(mt[c], v[j + c], v[j + 4 + c]);
-          }
-          const float mn = fmaxf(tc::max3(mt[0], mt[1], fmaxf(v[124], v[125])), tc::max3(mt[2], mt[3], fmaxf(v[126], v[127])));
-          // raise the maximum (a first one counts); O is idle: this S was issued after the last P V
-          if (__any_sync(0xffffffffu, mn > m && (mn - m) * sc > RAISE)) {
-            const float to = fmaxf(m, mn);
-            const float f = m == to ? 1.f : ex2((m - to) * sc);  // 0 for a first maximum
-            m = to;
-            l *= f;
-            if (i > 0) {
+            for (int j = 4; j < 124; j += 8) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c) mt[c] = tc::max3(mt[c], v[j + c], v[j + 4 + c]);
+            }
+            const float mn = fmaxf(tc::max3(mt[0], mt[1], fmaxf(v[124], v[125])), tc::max3(mt[2], mt[3], fmaxf(v[126], v[127])));
+            // raise the maximum (a first one counts); O is idle: this S was issued after the last P V
+            if (__any_sync(0xffffffffu, mn > m && (mn - m) * sc > RAISE)) {
+              const float to = fmaxf(m, mn);
+              const float f = m == to ? 1.f : ex2((m - to) * sc);  // 0 for a first maximum
+              m = to;
+              l *= f;
+              if (i > 0) {
 #pragma unroll 1
-              for (int g = 0; g < 4; ++g) {
-                float y[32];
-                tc::ld32(O + 32 * g, y);
+                for (int g = 0; g < 4; ++g) {
+                  float y[32];
+                  tc::ld32(O + 32 * g, y);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) y[j] *= f;
-                tc::st32(O + 32 * g, y);
+                  for (int j = 0; j < 32; ++j) y[j] *= f;
+                  tc::st32(O + 32 * g, y);
+                }
+                tc::wait_st();
+              }
+            }
+            const float ms = m == -INFINITY ? 0.f : -m * sc;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+              for (int g = 0; g < 2; ++g) {
+                float(&p)[32] = *reinterpret_cast<float(*)[32]>(v + 64 * h + 32 * g);
+#pragma unroll
+                for (int j = 0; j < 32; j += 2) {
+                  tc::fma2(p[j], p[j + 1], sc, sc, ms);
+                  p[j] = ex2(p[j]);
+                  p[j + 1] = ex2(p[j + 1]);
+                  tc::add2(sum[j & 2], sum[(j & 2) + 1], p[j], p[j + 1]);
+                }
+                tc::st16_bf16(S + 32 * h + 16 * g, p);
               }
               tc::wait_st();
+              tc::fence_before();
+              tc::mbar_arrive(&sm.barP[x][h]);
             }
-          }
-          const float ms = m == -INFINITY ? 0.f : -m * sc;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              float(&p)[32] = *reinterpret_cast<float(*)[32]>(v + 64 * h + 32 * g);
-#pragma unroll
-              for (int j = 0; j < 32; j += 2) {
-                tc::fma2(p[j], p[j + 1], sc, sc, ms);
-                p[j] = ex2(p[j]);
-                p[j + 1] = ex2(p[j + 1]);
-                tc::add2(sum[j & 2], sum[(j & 2) + 1], p[j], p[j + 1]);
-              }
-              tc::st16_bf16(S + 32 * h + 16 * g, p);
-            }
-            tc::wait_st();
-            tc::fence_before();
-            tc::mbar_arrive(&sm.barP[x][h]);
-          }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        } else {
-          tc::fence_before();
-          tc::mbar_arrive(&sm.barP[x][0]);
-          tc::mbar_arrive(&sm.barP[x][1]);
-        }
-      }
-      t0 += 2 * nmax;
-      s0 += mine;
-      if (mine > 0) {
-        w.warp_on(&sm.barO[x], items);
-        tc::fence_after();
-        ++items;
-      }
-      const int w4 = warp & 3;
-      float f = 1.f;  // what the group's own O counts for
-      if (dual) {
-        // the two groups' maxima and sums; group 1's part of O goes through its stage, 32 columns at a
-        // time, to the warp of group 0 that has the same rows
-        *reinterpret_cast<float2*>(&sm.stage[warp].v[lane][0]) = make_float2(m, l);
-        pair_sync(3 + w4);
-        const float2 other = *reinterpret_cast<const float2*>(&sm.stage[warp ^ 4].v[lane][0]);
-        pair_sync(3 + w4);
-        const float top = fmaxf(m, other.x);
-        f = m == top ? 1.f : ex2((m - top) * sc);
-        l = f * l + (other.x == top ? 1.f : ex2((other.x - top) * sc)) * other.y;  // (0 and 0: neither sees a key)
-        m = top;
-      }
-      if (any) {
-        // (a sum of zero: the row sees no key; one of NaN is neither greater nor equal, and goes on)
-        const bool none = nmax == 0 || l == 0.f;
-        const float inv = none ? 0.f : 1.f / l;
-        const float lse = none ? -INFINITY : m * a.scale + logf(l);
-        // (the join reads no part whose lse is minus infinity)
-        const uint32_t rows = __ballot_sync(0xffffffffu, valid && (it.whole || !none));
-        const long first = ((long)it.row + (dual ? 0 : x * TT)) * a.Hq + it.kh * G;  // row of the tile's first
-        const long part = (long)it.slot * 256 + (dual ? 0 : 128 * x) + 32 * w4;
-        int at[4];  // of the rows that are this lane's in the output
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int rr = 32 * w4 + 8 * k + (lane >> 2), t = rr / G;
-          at[k] = (t * a.Hq + rr - t * G) * HD;
-        }
-#pragma unroll 1
-        for (int g = 0; g < 4; ++g) {
-          float y[32];
-          if (mine > 0) tc::ld32(O + 32 * g, y);
-          if (none || mine == 0) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) y[j] = 0.f;
-          }
-          if (dual) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) y[j] *= f;
-            Stage& st = sm.stage[4 + w4];
-            if (x == 1) {
-#pragma unroll
-              for (int c = 0; c < 8; ++c) st.v[lane][c ^ (lane & 7)] = make_float4(y[4 * c], y[4 * c + 1], y[4 * c + 2], y[4 * c + 3]);
-            }
-            pair_sync(3 + w4);
-            if (x == 0) {
-#pragma unroll
-              for (int c = 0; c < 8; ++c) {
-                const float4 o = st.v[lane][c ^ (lane & 7)];
-                y[4 * c] += o.x, y[4 * c + 1] += o.y, y[4 * c + 2] += o.z, y[4 * c + 3] += o.w;
-              }
-            }
-            pair_sync(3 + w4);
-            if (x == 1) continue;
-          }
-          if (it.whole)
-            leave_whole(sm.stage[warp], a.o + first * HD + 32 * g, at, y, inv, rows);
-          else
-            leave_part(sm.stage[warp], a.part + part * HD + 32 * g, y, inv, rows);
-        }
-        if (valid && !(dual && x)) {
-          if (it.whole) {
-            if (a.lse) a.lse[first + r / G * a.Hq + r % G] = lse;
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           } else {
-            a.part_lse[part + lane] = lse;
+            tc::fence_before();
+            tc::mbar_arrive(&sm.barP[x][0]);
+            tc::mbar_arrive(&sm.barP[x][1]);
           }
         }
+        t0 += 2 * nmax;
+        s0 += mine;
+        if (mine > 0) {
+          w.warp_on(&sm.barO[x], items);
+          tc::fence_after();
+          ++items;
+        }
+        const int w4 = warp & 3;
+        float f = 1.f;  // what the group's own O counts for
+        if (dual) {
+          // the two groups' maxima and sums; group 1's part of O goes through its stage, 32 columns at a
+          // time, to the warp of group 0 that has the same rows
+          *reinterpret_cast<float2*>(&sm.stage[warp].v[lane][0]) = make_float2(m, l);
+          pair_sync(3 + w4);
+          const float2 other = *reinterpret_cast<const float2*>(&sm.stage[warp ^ 4].v[lane][0]);
+          pair_sync(3 + w4);
+          const float top = fmaxf(m, other.x);
+          f = m == top ? 1.f : ex2((m - top) * sc);
+          l = f * l + (other.x == top ? 1.f : ex2((other.x - top) * sc)) * other.y;  // (0 and 0: neither sees a key)
+          m = top;
+        }
+        if (any) {
+          // (a sum of zero: the row sees no key; one of NaN is neither greater nor equal, and goes on)
+          const bool none = nmax == 0 || l == 0.f;
+          const float inv = none ? 0.f : 1.f / l;
+          const float lse = none ? -INFINITY : m * a.scale + logf(l);
+          // (the join reads no part whose lse is minus infinity)
+          const uint32_t rows = __ballot_sync(0xffffffffu, valid && (it.whole || !none));
+          const long first = ((long)it.row + (dual ? 0 : x * TT)) * a.Hq + it.kh * G;  // row of the tile's first
+          const long part = (long)it.slot * 256 + (dual ? 0 : 128 * x) + 32 * w4;
+          int at[4];  // of the rows that are this lane's in the output
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int rr = 32 * w4 + 8 * k + (lane >> 2), t = rr / G;
+            at[k] = (t * a.Hq + rr - t * G) * HD;
+          }
+#pragma unroll 1
+          for (int g = 0; g < 4; ++g) {
+            float y[32];
+            if (mine > 0) tc::ld32(O + 32 * g, y);
+            if (none || mine == 0) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) y[j] = 0.f;
+            }
+            if (dual) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) y[j] *= f;
+              Stage& st = sm.stage[4 + w4];
+              if (x == 1) {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) st.v[lane][c ^ (lane & 7)] = make_float4(y[4 * c], y[4 * c + 1], y[4 * c + 2], y[4 * c + 3]);
+              }
+              pair_sync(3 + w4);
+              if (x == 0) {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                  const float4 o = st.v[lane][c ^ (lane & 7)];
+                  y[4 * c] += o.x, y[4 * c + 1] += o.y, y[4 * c + 2] += o.z, y[4 * c + 3] += o.w;
+                }
+              }
+              pair_sync(3 + w4);
+              if (x == 1) continue;
+            }
+            if (it.whole)
+              leave_whole(sm.stage[warp], a.o + first * HD + 32 * g, at, y, inv, rows);
+            else
+              leave_part(sm.stage[warp], a.part + part * HD + 32 * g, y, inv, rows);
+          }
+          if (valid && !(dual && x)) {
+            if (it.whole) {
+              if (a.lse) a.lse[first + r / G * a.Hq + r % G] = lse;
+            } else {
+              a.part_lse[part + lane] = lse;
+            }
+          }
+        }
+        if (mine > 0) {
+          tc::fence_before();
+          tc::mbar_arrive(&sm.barF[x]);
+        }
       }
-      if (mine > 0) {
-        tc::fence_before();
-        tc::mbar_arrive(&sm.barF[x]);
-      }
-    }
-    if (!sm.runs.more) break;
-    block_sync();
-    block_sync();
+      if (!sm.runs.more) break;
+      block_sync();
+      block_sync();
     }
   }
   if (!w.ok && a.status) atomicOr(a.status, 1);

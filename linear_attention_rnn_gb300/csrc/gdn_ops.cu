@@ -520,8 +520,14 @@ static int paged_check(int n_seqs, int total_q, int max_k, int n_pages, int page
 }
 
 // The kernel for attention over pages: k_paged_few where all sequences fit one query tile (it
-// takes longer ones too, tile by tile), which the totals or max_q say; else k_paged_many.  CTAs: two to an
-// SM, or one, but no more than there can be tiles of 128 keys.
+// takes longer ones too, tile by tile), which the totals or max_q say; else k_paged_many (16/4
+// heads: one token over 777 keys 16.6 us against 22.7, 8 x 16 tokens over 4096 keys each 25.9
+// against 27.4; 8 x 40 tokens 35.6 against 31.3, 2048 over 32768 keys 497 against 311).  Where
+// few items are cut into many long parts, k_paged_many has half as many to join (one token over
+// 16384 keys 24.7 against 26.9, over 32768 30.5 against 33.9; over 8192 22.7 against 20.7).
+// CTAs: two to an SM, or one, but no more than there can be tiles of 128 keys.
+// many_parts (four lanes' groups to a row of the join): 4 and more parts to an item, as far as
+// known (one token over 100000 keys 55 us against 75; 8 x 200 tokens 72 against 62).
 struct PagedPlan {
   int ctas, few, many_parts;
   size_t status, joins, part, part_lse, total;
@@ -529,8 +535,9 @@ struct PagedPlan {
 static PagedPlan paged_plan(int n_seqs, int total_q, long long max_q, long long max_k, int Hq, int Hk) {
   PagedPlan p;
   const long long TT = CH / (Hq / Hk), tiles = max_k > CH ? (max_k + CH - 1) / CH : 1;
-  p.few = total_q <= TT || (max_q > 0 && max_q <= TT);
-  const long long items = (total_q / (p.few ? TT : 2 * TT) + n_seqs) * Hk, most = (p.few ? 2 : 1) * sm_count();
+  const long long sms = sm_count();
+  p.few = (total_q <= TT || (max_q > 0 && max_q <= TT)) && !(n_seqs * (long long)Hk * 32 <= sms && tiles > 96);
+  const long long items = (total_q / (p.few ? TT : 2 * TT) + n_seqs) * Hk, most = (p.few ? 2 : 1) * sms;
   p.ctas = (int)(items < most && items * tiles < most ? items * tiles : most);
   p.many_parts = p.ctas >= 4 * items;
   size_t off = 0;
@@ -621,8 +628,10 @@ int gdn_attn_paged_weights(const void* q, const void* k_pages, const float* lse,
   WeighArgs w;
   memset(&w, 0, sizeof w);
   const int G = Hq / Hk;
-  // one query tile of the kernel for few rows to a sequence, on average
-  w.few = G <= WEIGH_FEW_ROWS && total_q <= (long long)n_seqs * (WEIGH_FEW_ROWS / G);
+  // Four of its query tiles to a sequence, on average, suit the kernel for few rows (16 caches of
+  // 4096 rows, 16/4 heads: 64 new tokens 31 us against 37 in the other, 128 53 against 41; one
+  // of 32768 rows: 22 against 25 and 33 against 27).
+  w.few = G <= WEIGH_FEW_ROWS && total_q <= (long long)n_seqs * (4 * WEIGH_FEW_ROWS / G);
   if ((rc = attn_args(w.at, q, nullptr, nullptr, cu_q, nullptr, n_seqs, total_q, 0, Hq, Hk, scale, q_stride,
                       (long long)Hk * HD, (long long)Hk * HD)))
     return rc;
@@ -640,10 +649,14 @@ int gdn_attn_paged_weights(const void* q, const void* k_pages, const float* lse,
   const long long longest = max_k < w.at.pages.capacity ? max_k : w.at.pages.capacity;
   const long long tiles = longest > CH ? (longest + CH - 1) / CH : 1, sms = sm_count();
   // Pairs share a key tile where one CTA would still be at the first, which sees all queries of
-  // its sequence, long after the others are done (in query tiles; a causal prompt has half of all).
+  // its sequence, when the others are done (in query tiles; a causal prompt has half of all): a
+  // prompt of 2500 tokens, 16/4 heads, 25 us against 39, four of 1024 18 against 21, of 2500
+  // 54 against 47.  With long units the smaller pieces alone win something (8192 + 640 + 77
+  // tokens: 105 against 109, 16384 with 16/2 heads: 382 against 412), with short ones the pair's
+  // meeting at each costs more (768 tokens, 16/16: 12.5 against 10.4).
   const long long TT = CH / G, first = (max_q > 0 && max_q < total_q ? max_q : total_q) / TT;
   const long long each = total_q / TT * tiles * Hk / 2 / sms;
-  w.split = !w.few && first - each > 32 ? 2 : 1;
+  w.split = !w.few && first >= 8 && (first > 2 * each || (first >= 64 && first > each)) ? 2 : 1;
   const long long most = w.few ? 2 * sms : sms / w.split, units = tiles * Hk;
   w.ctas = (int)(units < most && units * n_seqs < most ? units * n_seqs : most);
   return cuda_status(launch_weigh(w, static_cast<cudaStream_t>(stream)));
