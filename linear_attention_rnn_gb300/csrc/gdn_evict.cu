@@ -9,8 +9,8 @@
 // by its digits: weights are mapped to unsigned numbers of the same order, the digits
 // that all share are passed over, and each further digit of 8 bits takes one count over
 // the candidates.  The weights are held in shared memory where they fit.  A last pass in
-// index order writes the list of rows that stay (as places in the cache): a warp counts over its own range of
-// keys, a scan over the warps gives each its place.
+// index order writes the list of rows that stay (as places in the cache): a warp counts over
+// its own range of keys, scans over the warps and the lanes give each its place.
 //
 // k_evict_move copies the rows of the lists, 16 lanes to a row.  Into other pages any
 // block may take any part of a list.  In place (the target pages are the sequence's
@@ -71,10 +71,6 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1) k_evict_select(const __grid
     const float4 w = *reinterpret_cast<const float4*>(a.weights + ((long)e * a.Hk + kh) * a.pages.page + (j - t * a.pages.page));
     return make_uint4(rank_of(w.x), j + 1 < c.old ? rank_of(w.y) : 0u, j + 2 < c.old ? rank_of(w.z) : 0u,
                       j + 3 < c.old ? rank_of(w.w) : 0u);
-  };
-  auto single = [&](int j) -> uint32_t {
-    const uint4 r = fetch(j & ~3);
-    return (j & 3) == 0 ? r.x : (j & 3) == 1 ? r.y : (j & 3) == 2 ? r.z : r.w;
   };
   auto ranks = [&](int j) { return fits ? *reinterpret_cast<const uint4*>(held + j) : fetch(j); };
 
@@ -160,47 +156,78 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1) k_evict_select(const __grid
       edge |= (uint32_t)digit << low;
       ties -= above;
       shift = low;
+      if (ties == (int)hist[digit]) {  // all that have these digits: no need to tell them apart
+        edge = edge ? edge - 1u : 0u;
+        ties = 0;
+        break;
+      }
+      __syncthreads();  // (the counts have been read)
     }
   }
 
-  // the list, in index order: warp w's range of keys, counted first
-  const int per = ((c.kl + SELECT_WARPS - 1) / SELECT_WARPS + 31) & ~31;
+  // the list, in index order: warp w's range of keys, counted first; a lane has four at a time
+  const int per = ((c.kl + SELECT_WARPS - 1) / SELECT_WARPS + 127) & ~127;
   const int j0 = min(warp * per, c.kl), j1 = min(j0 + per, c.kl);
-  auto kind = [&](int j, int e) -> int {  // 1: stays, 2: stays if it is among the first ties
-    if (j >= j1) return 0;
-    if (j >= c.old) return (unsigned)e < (unsigned)a.pages.n_pages ? 1 : 0;
-    const uint32_t r = fits ? held[j] : single(j);
-    return r > edge ? 1 : r == edge && r ? 2 : 0;
+  // of the keys j .. j + 3 on page e: bits 0 to 3, those that stay, 4 to 7, those that stay if they are
+  // among the first ties
+  auto kinds = [&](int j, int e) -> uint32_t {
+    if (j >= j1 || (unsigned)e >= (unsigned)a.pages.n_pages) return 0u;
+    uint32_t y = 0u;
+    if (j < c.old) {
+      const uint4 r = ranks(j);
+      const uint32_t x[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y |= (x[i] > edge ? 1u : x[i] == edge ? 16u : 0u) << i;
+      if (edge == 0u) y &= 15u;  // (a rank of zero is no key)
+    }
+    if (j + 4 > c.old) {  // (the last ones begin here, or earlier)
+      const uint32_t last = 0xfu << max(c.old - j, 0) & 0xfu >> max(j + 4 - c.kl, 0);
+      y = (y & ~(last * 17u)) | last;
+    }
+    return y;
   };
+  auto page_at = [&](int j) { return j < j1 ? table[a.pages.page_of(j)] : -1; };
   int stay = 0, tied = 0;
-#pragma unroll 4
-  for (int j = j0; j < j1; j += 32) {
-    const int k = kind(j + lane, j + lane >= c.old && j + lane < c.kl ? table[a.pages.page_of(j + lane)] : 0);
-    stay += __popc(__ballot_sync(0xffffffffu, k == 1));
-    tied += __popc(__ballot_sync(0xffffffffu, k == 2));
+#pragma unroll 2
+  for (int j = j0 + 4 * lane; j < j1; j += 128) {
+    const uint32_t y = kinds(j, page_at(j));
+    stay += __popc(y & 15u);
+    tied += __popc(y >> 4);
   }
+  stay = __reduce_add_sync(0xffffffffu, stay);
+  tied = __reduce_add_sync(0xffffffffu, tied);
   if (lane == 0) {
     warps[warp][0] = stay;
     warps[warp][1] = tied;
   }
   __syncthreads();
-  int out = 0, seen = 0;
+  int out = 0, seen = 0;  // ahead of the warp's keys: those that stay, the tied ones
   for (int i = 0; i < warp; ++i) {
     out += warps[i][0];
     seen += warps[i][1];
   }
-  out += min(seen, ties);
   int* list = a.list + ((long)seq * a.Hk + kh) * a.keep;
-#pragma unroll 4
-  for (int j = j0; j < j1; j += 32) {
-    const int t = a.pages.page_of(min(j + lane, c.kl - 1)), e = table[t];
-    const int k = kind(j + lane, e);
-    const uint32_t below = (1u << lane) - 1u, tie = __ballot_sync(0xffffffffu, k == 2);
-    const bool keep = k == 1 || (k == 2 && seen + __popc(tie & below) < ties);
-    const uint32_t kept = __ballot_sync(0xffffffffu, keep);
-    if (keep) list[out + __popc(kept & below)] = e * a.pages.page + (j + lane - t * a.pages.page);
-    out += __popc(kept);
-    seen += __popc(tie);
+  for (int j = j0; j < j1; j += 128) {
+    const int key = j + 4 * lane, e = page_at(key);
+    const uint32_t y = kinds(key, e), mine = __popc(y & 15u) | __popc(y >> 4) << 16;
+    uint32_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t z = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += z;
+    }
+    int s = out + (int)((upto - mine) & 0xffffu), t = seen + (int)((upto - mine) >> 16);
+    const int row = e * a.pages.page + key - a.pages.page_of(key) * a.pages.page;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool stays = y >> i & 1u, tie = y >> (4 + i) & 1u;
+      if (stays || (tie && t < ties)) list[s + min(t, ties)] = row + i;
+      s += stays;
+      t += tie;
+    }
+    const uint32_t all = __shfl_sync(0xffffffffu, upto, 31);
+    out += (int)(all & 0xffffu);
+    seen += (int)(all >> 16);
   }
 }
 
