@@ -5,22 +5,27 @@
 // moves, in its order, to the first rows of the target pages (keys, values and weights).
 // Keys on absent pages are gone already and never stay.
 //
-// k_evict_select, one block to a sequence and head, finds the smallest weight that stays
-// by its digits: weights are mapped to unsigned numbers of the same order, the digits
-// that all share are passed over, and each further digit of 8 bits takes one count over
-// the candidates.  The weights are held in shared memory where they fit.  A last pass in
-// index order writes the list of rows that stay (as places in the cache): a warp counts over
-// its own range of keys, scans over the warps and the lanes give each its place.
+// k_evict_select, a block or a cluster of them to a sequence and head, finds the smallest
+// weight that stays by its digits: weights are mapped to unsigned numbers of the same
+// order, the digits that all share are passed over, and each further digit of 11 bits takes
+// one count over the candidates, until all that have the digits so far stay.  The weights
+// are held in shared memory where they fit.  A last pass in index order writes the list of
+// rows that stay (as places in the cache): a warp counts over its own range of keys, scans
+// over blocks, warps and lanes give each its place.
 //
 // k_evict_move copies the rows of the lists, 16 lanes to a row.  Into other pages any
 // block may take any part of a list.  In place (the target pages are the sequence's
 // own) one block walks a list in its order: a row's target never lies behind it, so
 // what a round writes are rows that this round and the earlier ones have read.
 //
-// Bound: HBM, 4 bytes a key and head and 1,024 a row that stays.
+// Bound: HBM, 4 bytes a key and head and 1,024 a row that stays.  32 caches of 1 to 16214 keys,
+// 4096 kept of 4 heads: 92 us, the copies 71 (424 MB of traffic, 6.0 TB/s; a plain copy with as
+// much 65), the lists some 20, by the longest cache's block.  1024 keys, 512 kept: 10 us,
+// latencies.  In place, where one block walks a list, the 32 caches take 117 us.
 #include <stdint.h>
 
 #include "gdn_kernels.cuh"
+#include "gdn_tc05.cuh"
 
 namespace gdn {
 
@@ -28,7 +33,14 @@ namespace {
 
 constexpr int SELECT_THREADS = 1024, SELECT_WARPS = SELECT_THREADS / 32;
 constexpr int SELECT_HELD = 49152;  // weights that shared memory holds
-constexpr int MOVE_THREADS = 256, MOVE_ROWS = 32;  // rows of a list to a block (16 side by side)
+// Bits of a digit.  With eight, weights of few binades meet in a few dozen places, and a warp's
+// additions there wait for one another (32 caches in all 94 us, with eleven 92).
+constexpr int DIGIT = 11;
+constexpr int PASSES = (32 + DIGIT - 1) / DIGIT;
+static_assert(1 << DIGIT == 2 * SELECT_THREADS, "two digits to a thread");
+// Rows of a list to a block, 16 side by side: 32 caches in all 98 us, with 64 rows 111, with 128
+// 156 (fewer blocks to an SM; with six of 32 rows instead of eight 103).
+constexpr int MOVE_THREADS = 256, MOVE_ROWS = 32;
 constexpr int WALK_THREADS = 1024, WALK_ROWS = 128;
 
 // The sequence's keys, and where the ones that always stay begin.
@@ -50,42 +62,62 @@ __device__ __forceinline__ uint32_t rank_of(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+// A value of CTA `rank` of the cluster, where p points in this one's shared memory.
+__device__ __forceinline__ uint2 ld_cluster(const uint32_t* p, int rank) {
+  uint32_t at;
+  uint2 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+  return v;
+}
+
 __global__ void __launch_bounds__(SELECT_THREADS, 1) k_evict_select(const __grid_constant__ EvictArgs a) {
   extern __shared__ __align__(16) uint32_t held[];
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t least, most;
-  __shared__ int present[2];          // of the candidates, of the last ones
-  __shared__ int digit, above;
+  __shared__ __align__(16) uint32_t hist[PASSES][1 << DIGIT];
+  __shared__ __align__(8) uint32_t range[2];    // complement of the least rank, the highest one
+  __shared__ __align__(8) uint32_t present[2];  // of the candidates, of the last ones
+  __shared__ __align__(8) uint32_t total[2];    // that stay, tied
+  __shared__ int digit, above, same;
   __shared__ int warps[SELECT_WARPS][2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int kh = blockIdx.x % a.Hk, seq = blockIdx.x / a.Hk;
+  const int C = a.split, rank = blockIdx.x % C, kh = blockIdx.x / C % a.Hk, seq = blockIdx.x / C / a.Hk;
+  auto meet = [&] {  // the threads of all CTAs of the list
+    if (C > 1) {
+      tc::cluster_arrive();
+      tc::cluster_wait();
+    } else {
+      __syncthreads();
+    }
+  };
   pdl_wait();
   pdl_release();
   const Cut c = cut_of(a, seq);
   const int* table = a.table + (long)seq * a.pages.table_stride;
-  const bool fits = c.old <= SELECT_HELD;
+  // this CTA's keys, and the candidates among them
+  const int span = ((c.kl + C - 1) / C + 127) & ~127;
+  const int b0 = min(rank * span, c.kl), b1 = min(b0 + span, c.kl), old1 = min(b1, c.old);
+  const bool fits = span <= SELECT_HELD;
   // ranks of the candidates j .. j + 3 (j a multiple of 4: one page); 0: none, or on an absent page
   auto fetch = [&](int j) -> uint4 {
     const int t = a.pages.page_of(j), e = table[t];
     if ((unsigned)e >= (unsigned)a.pages.n_pages) return make_uint4(0u, 0u, 0u, 0u);
-    const float4 w = *reinterpret_cast<const float4*>(a.weights + ((long)e * a.Hk + kh) * a.pages.page + (j - t * a.pages.page));
+    const float* at = a.weights + ((long)e * a.Hk + kh) * a.pages.page + (j - t * a.pages.page);
+    const float4 w = *reinterpret_cast<const float4*>(at);
     return make_uint4(rank_of(w.x), j + 1 < c.old ? rank_of(w.y) : 0u, j + 2 < c.old ? rank_of(w.z) : 0u,
                       j + 3 < c.old ? rank_of(w.w) : 0u);
   };
-  auto ranks = [&](int j) { return fits ? *reinterpret_cast<const uint4*>(held + j) : fetch(j); };
+  auto ranks = [&](int j) { return fits ? *reinterpret_cast<const uint4*>(held + (j - b0)) : fetch(j); };
 
-  if (tid == 0) {
-    least = 0xffffffffu;
-    most = 0u;
-    present[0] = present[1] = 0;
-  }
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p) hist[p][tid] = hist[p][tid + SELECT_THREADS] = 0u;
+  if (tid < 2) range[tid] = present[tid] = 0u;
   __syncthreads();
   uint32_t lo = 0xffffffffu, hi = 0u;
   int n0 = 0, n1 = 0;
 #pragma unroll 4
-  for (int j = 4 * tid; j < c.old; j += 4 * SELECT_THREADS) {
+  for (int j = b0 + 4 * tid; j < old1; j += 4 * SELECT_THREADS) {
     const uint4 r = fetch(j);
-    if (fits) *reinterpret_cast<uint4*>(held + j) = r;
+    if (fits) *reinterpret_cast<uint4*>(held + (j - b0)) = r;
     const uint32_t x[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -95,79 +127,83 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1) k_evict_select(const __grid
         ++n0;
       }
   }
-  for (int j = c.old + tid; j < c.kl; j += SELECT_THREADS)
+  for (int j = max(b0, c.old) + tid; j < b1; j += SELECT_THREADS)
     n1 += (unsigned)table[a.pages.page_of(j)] < (unsigned)a.pages.n_pages;
   lo = __reduce_min_sync(0xffffffffu, lo);
   hi = __reduce_max_sync(0xffffffffu, hi);
   n0 = __reduce_add_sync(0xffffffffu, n0);
   n1 = __reduce_add_sync(0xffffffffu, n1);
   if (lane == 0) {
-    atomicMin(&least, lo);
-    atomicMax(&most, hi);
-    atomicAdd(&present[0], n0);
-    atomicAdd(&present[1], n1);
+    atomicMax(&range[0], ~lo);
+    atomicMax(&range[1], hi);
+    atomicAdd(&present[0], (uint32_t)n0);
+    atomicAdd(&present[1], (uint32_t)n1);
   }
-  __syncthreads();
-  const int take = min(present[0], a.budget - present[1]);  // of the candidates (recent <= budget)
-  if (kh == 0 && tid == 0) a.new_len[seq] = take + present[1];
+  meet();
+  const uint2 ends = lane < C ? ld_cluster(range, lane) : make_uint2(0u, 0u);
+  const uint2 counts = lane < C ? ld_cluster(present, lane) : make_uint2(0u, 0u);
+  const uint32_t least = ~__reduce_max_sync(0xffffffffu, ends.x), most = __reduce_max_sync(0xffffffffu, ends.y);
+  const int candidates = __reduce_add_sync(0xffffffffu, counts.x), recent = __reduce_add_sync(0xffffffffu, counts.y);
+  const int take = min(candidates, a.budget - recent);  // of the candidates (recent <= budget)
+  if (kh == 0 && rank == 0 && tid == 0) a.new_len[seq] = take + recent;
   // The candidates that stay: ranks above `edge`, and the first `ties` of rank `edge`.
   uint32_t edge = 0u;  // (all of them)
   int ties = 0;
   if (take == 0) {
     edge = 0xffffffffu;  // none: no rank is above it, and no number has it
-  } else if (take < present[0]) {
+  } else if (take < candidates) {
     // the digits below the highest bit in which candidates differ
     int shift = 32 - __clz(least ^ most);
     edge = shift < 32 ? most >> shift << shift : 0u;
     ties = take;
-    while (shift > 0) {
-      const int bits = min(shift, 8), low = shift - bits;
-      if (tid < 256) hist[tid] = 0u;
-      __syncthreads();
+    for (int p = 0; shift > 0; ++p) {
+      const int bits = min(shift, DIGIT), low = shift - bits;
       const uint32_t mask = shift < 32 ? ~0u << shift : 0u;
-      for (int j = 4 * tid; j < c.old; j += 4 * SELECT_THREADS) {
+      for (int j = b0 + 4 * tid; j < old1; j += 4 * SELECT_THREADS) {
         const uint4 r = ranks(j);
         const uint32_t x[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (x[i] && (x[i] & mask) == edge) atomicAdd(&hist[x[i] >> low & ((1u << bits) - 1u)], 1u);
+          if (x[i] && (x[i] & mask) == edge) atomicAdd(&hist[p][x[i] >> low & ((1u << bits) - 1u)], 1u);
       }
+      meet();
+      // the digit at which the count from the top reaches what is still to take: a warp has 64 of them
+      int d0 = 0, d1 = 0;
+      for (int r = 0; r < C; ++r) {
+        const uint2 n = ld_cluster(&hist[p][2 * tid], r);
+        d0 += (int)n.x;
+        d1 += (int)n.y;
+      }
+      int from = d0 + d1;  // in this lane's digits and those above in the warp
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_down_sync(0xffffffffu, from, o);
+        if (lane + o < 32) from += y;
+      }
+      if (lane == 0) warps[warp][0] = from;
       __syncthreads();
-      // the digit at which the count from the top reaches what is still to take
-      if (warp == 0) {
-        int mine = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) mine += hist[8 * lane + i];
-        int from = mine;  // in this lane's digits and above
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_down_sync(0xffffffffu, from, o);
-          if (lane + o < 32) from += y;
-        }
-        int over = from - mine;  // above this lane's digits
-        if (over < ties && from >= ties) {
-          int d = 8 * lane + 7;
-          while (over + (int)hist[d] < ties) over += hist[d--];
-          digit = d;
-          above = over;
-        }
+      const int over = __reduce_add_sync(0xffffffffu, lane > warp ? warps[lane][0] : 0) + from - d0 - d1;  // above them
+      if (over < ties && over + d0 + d1 >= ties) {
+        const bool upper = over + d1 >= ties;
+        digit = 2 * tid + upper;
+        above = upper ? over : over + d1;
+        same = upper ? d1 : d0;
       }
       __syncthreads();
       edge |= (uint32_t)digit << low;
       ties -= above;
       shift = low;
-      if (ties == (int)hist[digit]) {  // all that have these digits: no need to tell them apart
+      if (ties == same) {  // all that have these digits: no need to tell them apart
         edge = edge ? edge - 1u : 0u;
         ties = 0;
         break;
       }
-      __syncthreads();  // (the counts have been read)
     }
   }
 
   // the list, in index order: warp w's range of keys, counted first; a lane has four at a time
-  const int per = ((c.kl + SELECT_WARPS - 1) / SELECT_WARPS + 127) & ~127;
-  const int j0 = min(warp * per, c.kl), j1 = min(j0 + per, c.kl);
+  const int per = ((b1 - b0 + SELECT_WARPS - 1) / SELECT_WARPS + 127) & ~127;
+  const int j0 = min(b0 + warp * per, b1), j1 = min(j0 + per, b1);
   // of the keys j .. j + 3 on page e: bits 0 to 3, those that stay, 4 to 7, those that stay if they are
   // among the first ties
   auto kinds = [&](int j, int e) -> uint32_t {
@@ -202,6 +238,19 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1) k_evict_select(const __grid
   }
   __syncthreads();
   int out = 0, seen = 0;  // ahead of the warp's keys: those that stay, the tied ones
+  if (C > 1) {
+    if (warp == 0) {
+      const int x = __reduce_add_sync(0xffffffffu, warps[lane][0]), y = __reduce_add_sync(0xffffffffu, warps[lane][1]);
+      if (lane == 0) {
+        total[0] = (uint32_t)x;
+        total[1] = (uint32_t)y;
+      }
+    }
+    meet();
+    const uint2 ahead = lane < rank ? ld_cluster(total, lane) : make_uint2(0u, 0u);
+    out = __reduce_add_sync(0xffffffffu, ahead.x);
+    seen = __reduce_add_sync(0xffffffffu, ahead.y);
+  }
   for (int i = 0; i < warp; ++i) {
     out += warps[i][0];
     seen += warps[i][1];
@@ -228,7 +277,7 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1) k_evict_select(const __grid
     const uint32_t all = __shfl_sync(0xffffffffu, upto, 31);
     out += (int)(all & 0xffffu);
     seen += (int)(all >> 16);
-  }
+  }  if (C > 1) meet();  // no CTA ends while another reads its counts
 }
 
 // Keys, values and weight of row `row` (page * page size + row in it), one lane's share of 16.
@@ -319,12 +368,25 @@ __global__ void __launch_bounds__(WALK_THREADS) k_evict_walk(const __grid_consta
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s) {
   const unsigned rows = (unsigned)a.n_seqs * (unsigned)a.Hk;
-  // (whole vectors of 4: a capacity is a multiple of 16)
-  const size_t smem = sizeof(uint32_t) * (size_t)(a.pages.capacity < SELECT_HELD ? a.pages.capacity : SELECT_HELD);
+  const long span = (((long)a.pages.capacity + a.split - 1) / a.split + 127) & ~127L;  // as in the kernel, at most
+  const size_t smem = sizeof(uint32_t) * (size_t)(span < SELECT_HELD ? span : SELECT_HELD);
   cudaError_t e = cudaFuncSetAttribute(k_evict_select, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)(SELECT_HELD * sizeof(uint32_t)));
   if (e != cudaSuccess) return e;
-  if ((e = launch_pdl(k_evict_select, dim3(rows), dim3(SELECT_THREADS), smem, s, a)) != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(rows * (unsigned)a.split);
+  cfg.blockDim = dim3(SELECT_THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)a.split;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if ((e = cudaLaunchKernelEx(&cfg, k_evict_select, a)) != cudaSuccess) return e;
   if (a.keep == 0) return cudaSuccess;
   if (!a.to) return launch_pdl(k_evict_walk, dim3(rows), dim3(WALK_THREADS), 0, s, a);
   const long parts = ((long)a.keep + MOVE_ROWS - 1) / MOVE_ROWS;

@@ -74,6 +74,34 @@ def test_long_caches(gdn_lib, kind, kl, budget):
     check(gdn_lib, x, kl, budget, budget // 3)
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("kl,Hk,page,budget,recent", [([9000, 4100, 3], 2, 64, 3000, 1000), ([20001], 1, 48, 777, 0),
+                                                      ([16500, 40000], 1, 16, 16000, 15990)])
+def test_lists_of_several_blocks(gdn_lib, kind, kl, Hk, page, budget, recent):
+    """Caches whose keys are shared out, ties and the last ones across the cuts."""
+    x = weights(paged.cache([1] * len(kl), kl, Hk, Hk, page, seed=budget), budget, kind)
+    check(gdn_lib, x, kl, budget, recent)
+
+
+@pytest.mark.parametrize("kind", ["spread", "ties"])
+def test_short_sequences_of_a_wide_table(gdn_lib, kind):
+    """A table for 65536 keys and few of them there: most of the blocks have none."""
+    kl = [300, 0, 130, 2500]
+    x = weights(paged.cache([1] * 4, kl, 1, 1, 64, seed=3, wide=1000), 3, kind)
+    check(gdn_lib, x, kl, 120, 20)
+
+
+def test_many_long_lists(gdn_lib):
+    """More keys than shared memory holds, in more lists than are shared out: 80 over the same pages."""
+    n, m, budget = 20, 49300, 16
+    x = weights(paged.cache([1], [m], 4, 4, 64, seed=12, spare=n), 12, "ties")
+    free = sorted(set(range(x["kp"].shape[0])) - set(x["table"].flatten().tolist()))
+    x["table"] = x["table"].repeat(n, 1)
+    kl = [m - 3 * s for s in range(n)]
+    x["k_len"] = paged.ints(kl)
+    check(gdn_lib, x, kl, budget, 5, torch.tensor([[f] for f in free[:n]], dtype=torch.int32))
+
+
 def test_nothing_to_drop_leaves_everything(gdn_lib):
     x = paged.cache([1, 1], [77, 33], 2, 2, 16, seed=4)
     d = paged.cuda(x)
