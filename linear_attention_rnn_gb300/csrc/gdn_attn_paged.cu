@@ -13,7 +13,13 @@
 // tiles its two groups of warps take in turn; k_paged_few (for calls whose sequences are
 // known to fit one query tile) holds one against tiles of 64 keys, two CTAs to an SM.
 //
-#include <limits.h>
+// Bounds.  Chunks of prompts: the tensor rate, 2048 tokens over 32768 keys with 16/4 heads take
+// 308 us, 1.73 PFLOP/s (tensor pipe 77% busy; CTAs that each took one item 367).  Tokens: HBM,
+// 32 of them over 1 to 16214 keys take 92 us for 532 MB, 5.8 TB/s (an equal number of key tiles
+// of each item to a CTA: 98).  A mixed step (512 + 300 + 129 tokens and 20 single ones, 16/2
+// heads): 55 us (82 before), of which some 20 are the start, the plan and the join, and single
+// tokens fill 8 of a tile's 128 rows.  One token over 777 keys: 16.5 us, latencies alone.
+//
 #include <math.h>
 
 #include "gdn_attn_runs.cuh"
@@ -53,8 +59,8 @@ __device__ __forceinline__ void leave(const Item& it, bf16* o, float* part, floa
 
 // 32 columns of a warp's 32 rows, through shared memory, so that whole lines leave: a store of
 // every lane's own row touches 32 lines at a time, and a part of 256 rows took some 8 us.
-// `rows`: those that are written; `o` and `part`: of the warp's first row, `at`: elements from
-// there to the row that is the lane's in step k of the output's (its four lanes have 64 bytes).
+// `rows`: those that are written; `part`: the warp's first row, `o`: the tile's first, `at`: elements
+// from there to the row that is the lane's in step k (its four lanes have 64 bytes).
 struct alignas(16) Stage {
   float4 v[32][8];
 };
@@ -93,8 +99,10 @@ __device__ __forceinline__ void leave_whole(Stage& st, bf16* o, const int (&at)[
 // ---- sequences of more than one query tile ---------------------------------------------------
 constexpr int NSLOT = 4;
 constexpr int MANY_THREADS = 384;
-constexpr int MANY_EXTRA = 256;   // keys that an item's start and end take the time of
-constexpr int MANY_RUN = 512;     // width of a run, at least
+// Keys that an item's start and end take the time of, and a run's width, at least.  Measured in us
+// for a mixed step, 2048 tokens over 32768 keys, 40 over 16384: 55, 308, 28; without extra and 128
+// at least 90, 309, 29; 1024 and 1536 61, 315, 35.
+constexpr int MANY_EXTRA = 256, MANY_RUN = 512;
 constexpr int REGS_LAUNCH = 168, REGS_SOFTMAX = 208, REGS_ISSUE = 88;  // (as in gdn_attn_fwd.cu)
 static_assert(2 * REGS_SOFTMAX + REGS_ISSUE <= 3 * REGS_LAUNCH, "the groups' registers come from the block's");
 
@@ -218,7 +226,8 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) k_paged_many(const __grid_con
       __syncwarp();
     } else if (warp == 8) {
       const uint32_t lead = tc::elect_leader();
-      int t0 = 0, qc[2] = {0, 0}, oc[2] = {0, 0}, sc[2] = {0, 0};  // ring tiles, query tiles, a group's items and key tiles so far
+      // ring tiles, query tiles, a group's items and key tiles so far
+      int t0 = 0, qc[2] = {0, 0}, oc[2] = {0, 0}, sc[2] = {0, 0};
       for (;;) {
         for (int e = 0; e < sm.runs.count; ++e) {
           const Item& it = sm.runs.item[e];
@@ -359,7 +368,8 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) k_paged_many(const __grid_con
 #pragma unroll
               for (int c = 0; c < 4; ++c) mt[c] = tc::max3(mt[c], v[j + c], v[j + 4 + c]);
             }
-            const float mn = fmaxf(tc::max3(mt[0], mt[1], fmaxf(v[124], v[125])), tc::max3(mt[2], mt[3], fmaxf(v[126], v[127])));
+            const float mn =
+                fmaxf(tc::max3(mt[0], mt[1], fmaxf(v[124], v[125])), tc::max3(mt[2], mt[3], fmaxf(v[126], v[127])));
             // raise the maximum (a first one counts); O is idle: this S was issued after the last P V
             if (__any_sync(0xffffffffu, mn > m && (mn - m) * sc > RAISE)) {
               const float to = fmaxf(m, mn);
@@ -455,7 +465,8 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) k_paged_many(const __grid_con
               Stage& st = sm.stage[4 + w4];
               if (x == 1) {
 #pragma unroll
-                for (int c = 0; c < 8; ++c) st.v[lane][c ^ (lane & 7)] = make_float4(y[4 * c], y[4 * c + 1], y[4 * c + 2], y[4 * c + 3]);
+                for (int c = 0; c < 8; ++c)
+                  st.v[lane][c ^ (lane & 7)] = make_float4(y[4 * c], y[4 * c + 1], y[4 * c + 2], y[4 * c + 3]);
               }
               pair_sync(3 + w4);
               if (x == 0) {
@@ -500,8 +511,9 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) k_paged_many(const __grid_con
 
 // ---- sequences of one query tile ---------------------------------------------------------------
 constexpr int KEYS = 64, FEW_SLOTS = 4;
-constexpr int FEW_EXTRA = 128;    // keys that an item's start and end take the time of
-constexpr int FEW_RUN = 256;      // width of a run, at least
+// As above: one token over 777 keys, 32 over 1 to 16214, in us: 16.5, 94; without extra and 128 at
+// least 15.6, 102; 128 and 1024 29, 94; 512 and 1024 23, 95.
+constexpr int FEW_EXTRA = 128, FEW_RUN = 256;
 constexpr int FEW_THREADS = 192;  // four warps of softmax, one that issues, one that plans and loads
 
 struct FewSmem {
@@ -764,7 +776,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) k_paged_few(const __grid_const
 // ---- the items that were cut ------------------------------------------------------------------
 // o = sum_s e^{lse_s - lse} o_s over the parts, in a fixed order.  Blocks (c, y): 32 / P rows of
 // the item that begins in run c and is cut, 8 P lanes to a row: eight have 16 columns each of
-// every P-th part.  A part of NaN makes the row NaN, as it would be in one piece.
+// every P-th part.  A part of NaN makes the row NaN, as it would be in one piece.  Bound by the
+// latency of its loads: 9 us for 32 tokens' parts, 14 for the 36 MB of a chunk's.
 template <int P>
 __global__ void __launch_bounds__(256) k_paged_join(const __grid_constant__ PagedArgs pa) {
   pdl_wait();

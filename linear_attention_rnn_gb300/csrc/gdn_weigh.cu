@@ -17,6 +17,13 @@
 //
 // A key's sum is formed by one thread in a fixed order and added once to its place
 // (by an atomic addition: sequences that share a page each add theirs).
+//
+// Bounds.  Prompts: the exponentials, a tile of 128 x 128 takes an SM 0.27 us of its 32 a clock,
+// whose issue the fma and the addition share: 8192 + 640 + 77 tokens with 16/4 heads take 105 us
+// (138 GFLOP, 1.3 PFLOP/s; 115 where a key tile began behind the last one's end).  Chunks over
+// caches: the same (2048 over 32768 keys 192 us), short ones the latency of a key tile's start, some
+// 2.5 us (16 x 128 tokens over 4096 keys 41 us).  Tokens: HBM, 32 over 1 to 16214 keys 47 us for
+// 274 MB, 5.8 TB/s.
 #include <math.h>
 
 #include "gdn_attn.cuh"
@@ -167,7 +174,8 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) k_weigh_many(const __grid_con
   int n_units;
   {
     long all = __reduce_add_sync(0xffffffffu, own);
-    for (int s = 32; s < a.at.n_seqs; s += 32) all += __reduce_add_sync(0xffffffffu, s + lane < a.at.n_seqs ? tiles(s + lane) : 0);
+    for (int s = 32; s < a.at.n_seqs; s += 32)
+      all += __reduce_add_sync(0xffffffffu, s + lane < a.at.n_seqs ? tiles(s + lane) : 0);
     all *= a.at.Hk;
     const long rounds = all / teams, rest = all - rounds * teams;
     n_units = (int)rounds + ((rounds & 1 ? teams - 1 - team : team) < rest ? 1 : 0);
@@ -237,7 +245,8 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) k_weigh_many(const __grid_con
         for (int j = 0; w.ok && j < u.mine; ++j, ++t) {
           if (t >= MANY_SLOTS) w.on(&sm.empty[t % MANY_SLOTS], t / MANY_SLOTS - 1);
           if (w.ok)
-            load_group(sm.slot[t % MANY_SLOTS], &a.at.q, u.kh, G, u.row + (u.q0 + split * j) * TT, &sm.full[t % MANY_SLOTS]);
+            load_group(sm.slot[t % MANY_SLOTS], &a.at.q, u.kh, G, u.row + (u.q0 + split * j) * TT,
+                       &sm.full[t % MANY_SLOTS]);
         }
       }
       __syncwarp();
