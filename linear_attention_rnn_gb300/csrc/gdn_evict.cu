@@ -15,13 +15,15 @@
 //
 // k_evict_move copies the rows of the lists, 16 lanes to a row.  Into other pages any
 // block may take any part of a list.  In place (the target pages are the sequence's
-// own) one block walks a list in its order: a row's target never lies behind it, so
-// what a round writes are rows that this round and the earlier ones have read.
+// own) a block or a cluster walks a list in its order: a row's target never lies behind it, so
+// what a round writes are rows that this round and the earlier ones have read, and the next
+// round's rows are on their way meanwhile.
 //
 // Bound: HBM, 4 bytes a key and head and 1,024 a row that stays.  32 caches of 1 to 16214 keys,
 // 4096 kept of 4 heads: 92 us, the copies 71 (424 MB of traffic, 6.0 TB/s; a plain copy with as
 // much 65), the lists some 20, by the longest cache's block.  1024 keys, 512 kept: 10 us,
-// latencies.  In place, where one block walks a list, the 32 caches take 117 us.
+// latencies.  In place the walk's rounds bound: the 32 caches, with a block to a list, 105 us,
+// one of 65536 keys, half of them kept, by clusters of eight 115 (into other pages 46).
 #include <stdint.h>
 
 #include "gdn_kernels.cuh"
@@ -41,7 +43,7 @@ static_assert(1 << DIGIT == 2 * SELECT_THREADS, "two digits to a thread");
 // Rows of a list to a block, 16 side by side: 32 caches in all 98 us, with 64 rows 111, with 128
 // 156 (fewer blocks to an SM; with six of 32 rows instead of eight 103).
 constexpr int MOVE_THREADS = 256, MOVE_ROWS = 32;
-constexpr int WALK_THREADS = 1024, WALK_ROWS = 128;
+constexpr int WALK_THREADS = 1024, WALK_ROWS = 128;  // (64 rows to a round 160 us for 131, 256 149)
 
 // The sequence's keys, and where the ones that always stay begin.
 struct Cut {
@@ -335,32 +337,58 @@ __global__ void __launch_bounds__(MOVE_THREADS, 8) k_evict_move(const __grid_con
 }
 
 __global__ void __launch_bounds__(WALK_THREADS) k_evict_walk(const __grid_constant__ EvictArgs a) {
-  const int kh = blockIdx.x % a.Hk, seq = blockIdx.x / a.Hk;
-  const int l = threadIdx.x & 15, i0 = threadIdx.x >> 4;
+  const int C = a.walks, rank = blockIdx.x % C, kh = blockIdx.x / C % a.Hk, seq = blockIdx.x / C / a.Hk;
+  const int l = threadIdx.x & 15, i0 = rank * WALK_ROWS + (threadIdx.x >> 4);
   pdl_wait();
   pdl_release();
-  const int n = a.new_len[seq];
+  const int n = a.new_len[seq], step = C * WALK_ROWS;
   const int* table = a.table + (long)seq * a.pages.table_stride;
   const int* list = a.list + ((long)seq * a.Hk + kh) * a.keep;
   constexpr int R = WALK_ROWS / (WALK_THREADS / 16);
-  for (int base = 0; base < n; base += WALK_ROWS) {
+  struct Round {
     int dst[R];
     Row x[R];
+  };
+  int from[R], to[R];  // the places of the round whose rows are read next
+  auto ask = [&](int base) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int i = base + i0 + r * (WALK_THREADS / 16);
-      dst[r] = -1;
-      if (i < n) {
-        const int from = list[i];
-        dst[r] = row_at(a, table, i);
-        if (dst[r] == from) dst[r] = -1;  // it stays where it is
-        if (dst[r] >= 0) x[r].read(a, kh, l, from);
+      const int i = i0 + r * (WALK_THREADS / 16);
+      from[r] = to[r] = -1;
+      if (base < n && i < n - base) {
+        from[r] = list[base + i];
+        to[r] = row_at(a, table, base + i);
       }
     }
-    __syncthreads();  // the round's rows have been read
+  };
+  auto read = [&](Round& t) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      t.dst[r] = to[r] == from[r] ? -1 : to[r];  // (it stays where it is)
+      if (t.dst[r] >= 0) t.x[r].read(a, kh, l, from[r]);
+    }
+  };
+  auto round = [&](int base, const Round& now, Round& next) {
+    read(next);  // (rows behind all that this round writes)
+    ask(base + 2 * step);
+    if (C > 1) {  // the round's rows have been read
+      tc::cluster_arrive();
+      tc::cluster_wait();
+    } else {
+      __syncthreads();
+    }
 #pragma unroll
     for (int r = 0; r < R; ++r)
-      if (dst[r] >= 0) x[r].write(a, kh, l, dst[r]);
+      if (now.dst[r] >= 0) now.x[r].write(a, kh, l, now.dst[r]);
+  };
+  Round even, odd;
+  ask(0);
+  read(even);
+  ask(step);
+  for (int base = 0; base < n; base += 2 * step) {
+    round(base, even, odd);
+    if (n - base <= step) break;
+    round(base + step, odd, even);
   }
 }
 
@@ -373,22 +401,25 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(k_evict_select, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)(SELECT_HELD * sizeof(uint32_t)));
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(rows * (unsigned)a.split);
-  cfg.blockDim = dim3(SELECT_THREADS);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)a.split;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  if ((e = cudaLaunchKernelEx(&cfg, k_evict_select, a)) != cudaSuccess) return e;
+  auto launch = [&](auto kernel, int ctas, int threads, size_t bytes) {  // `ctas` to a list
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(rows * (unsigned)ctas);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+  };
+  if ((e = launch(k_evict_select, a.split, SELECT_THREADS, smem)) != cudaSuccess) return e;
   if (a.keep == 0) return cudaSuccess;
-  if (!a.to) return launch_pdl(k_evict_walk, dim3(rows), dim3(WALK_THREADS), 0, s, a);
+  if (!a.to) return launch(k_evict_walk, a.walks, WALK_THREADS, 0);
   const long parts = ((long)a.keep + MOVE_ROWS - 1) / MOVE_ROWS;
   return launch_pdl(k_evict_move, dim3(rows, (unsigned)(parts < 65535 ? parts : 65535)), dim3(MOVE_THREADS), 0, s, a);
 }

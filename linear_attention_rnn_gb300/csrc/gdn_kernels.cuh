@@ -278,7 +278,7 @@ struct EvictArgs {
   long sk_page, sk_row, sk_head, sv_page, sv_row, sv_head;  // elements
   int n_seqs, Hk, budget, recent;
   int keep;             // most keys that stay: the smaller of budget and the table's rows
-  int split;            // CTAs that choose a list's keys, 1 to 8
+  int split, walks;     // CTAs that choose a list's keys, that move them in place: 1 to 8
 };
 
 // Norms and rotation of heads (gdn_rope.cu): the rows of q, of k or of v (v: copied into pages).

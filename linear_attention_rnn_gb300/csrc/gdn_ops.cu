@@ -720,11 +720,12 @@ int gdn_cache_evict(void* k_pages, void* v_pages, float* weights, const int* pag
   a.keep = keep;
   // CTAs to a list, as far as half the device holds them (clusters of eight fill no more), of 6144
   // keys and more.  Four lists of 65536 keys 73 us with one each, 33, 27 and 25 with two, four and
-  // eight, of 4096 12.5, 14.3, 14.5 and 16.6; 16 lists of 65536 96, 54, 45 and 58.
-  a.split = 1;
-  for (const long long lists = (long long)n_seqs * Hk, most = sm_count();
-       a.split < 8 && 4 * a.split * lists <= most && capacity >= 12288 * a.split;)
-    a.split *= 2;
+  // eight, of 4096 12.5, 14.3, 14.5 and 16.6; 16 lists of 65536 96, 54, 45 and 58.  Moving rows in
+  // place, of 256 rows and more: 16 lists of 16384 keys, half kept, 122 us by one each, 64 by four.
+  const long long lists = (long long)n_seqs * Hk, most = sm_count();
+  a.split = a.walks = 1;
+  while (a.split < 8 && 4 * a.split * lists <= most && capacity >= 12288 * a.split) a.split *= 2;
+  while (a.walks < 8 && 4 * a.walks * lists <= most && keep >= 256 * a.walks) a.walks *= 2;
   return cuda_status(launch_evict(a, s));
 }
 
