@@ -512,7 +512,8 @@ int gdn_rope_append(const void* q, const void* k, const void* v, const float* q_
  * [total_q, Hq] as gdn_attn_paged returned it (a row with lse = -inf adds nothing).
  * weights: fp32 [n_pages, Hk, page_size], contiguous.  A sequence's sum is formed in a
  * fixed order and added at once; where sequences share a page, or a table names one twice,
- * each adds its own, in no fixed order.  max_q and max_k bound a sequence's queries (0: not
+ * each adds its own, in no fixed order.  A row that a new key takes keeps the weight that it
+ * had (of a key that was evicted, say): set it to zero where it is to count anew.  max_q and max_k bound a sequence's queries (0: not
  * known) and keys; they steer, as above.  ws: 256 bytes whose first word is the status
  * word, or NULL.  A call that has nothing to add starts no kernel.
  *
@@ -525,8 +526,8 @@ int gdn_rope_append(const void* q, const void* k, const void* v, const float* q_
  * the sequence's own pages, in place.  Other rows keep what they hold.  new_len [n_seqs] receives
  * the keys that stay of each sequence (the same for all heads); it must not be k_len.
  * Keys on absent pages never stay; a row whose target page is absent is not written.  In
- * place, sequences must not share pages; otherwise no target page may hold a key of any
- * sequence of the call.  ws: gdn_cache_evict_workspace_bytes(n_seqs, max_pages *
+ * place, no page may occur twice in the tables; otherwise no target page may, nor may one
+ * hold a key of any sequence of the call.  ws: gdn_cache_evict_workspace_bytes(n_seqs, max_pages *
  * page_size, budget, Hk) bytes, without a status word (no kernel of it waits).
  */
 size_t gdn_attn_paged_workspace_bytes(int n_seqs, int total_q, int max_rows, int max_q, int max_k,

@@ -397,7 +397,8 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// All threads of a cluster's CTAs; what they wrote before is visible to all of them behind it.
+// A barrier of all threads of a cluster's CTAs, in two halves: what they wrote ahead of the first is
+// visible to all of them behind the second.
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 // v to where p lies in the shared memory of CTA `rank` of the cluster

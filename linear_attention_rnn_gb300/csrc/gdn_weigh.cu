@@ -181,7 +181,12 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) k_weigh_many(const __grid_con
     n_units = (int)rounds + ((rounds & 1 ? teams - 1 - team : team) < rest ? 1 : 0);
   }
   tc::fence_before();
-  __syncthreads();
+  if (split > 1) {  // (the other CTA's shared memory is there from here on)
+    tc::cluster_arrive();
+    tc::cluster_wait();
+  } else {
+    __syncthreads();
+  }
   tc::fence_after();
   tc::Wait w;
 

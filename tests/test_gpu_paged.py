@@ -57,6 +57,17 @@ def test_chunks_over_pages(gdn_lib, ql, kl, Hq, Hk, page):
     both(gdn_lib, x, ql, kl, most=max(kl))
 
 
+@pytest.mark.parametrize("ql,kl,Hq,Hk", [
+    ([1300], [1300], 16, 8),                                         # pairs of CTAs with several key tiles each
+    ([1100, 900], [1100, 3001], 16, 8), ([70] * 6, list(range(1990, 2014, 4)), 8, 2),   # CTAs with several
+    ([64, 60, 65], [1000, 64, 2500], 4, 1), ([200, 1, 1, 1, 1, 1], [777, 500, 1, 0, 1111, 40], 8, 2),  # several query tiles
+])
+def test_several_tiles_each(gdn_lib, ql, kl, Hq, Hk):
+    """CTAs that take one key tile, or one query tile, after another."""
+    x = paged.cache(ql, kl, Hq, Hk, 32, seed=len(ql))
+    both(gdn_lib, x, ql, kl, most=max(kl))
+
+
 @pytest.mark.parametrize("page", [32, 80, 112, 128, 1024])
 @pytest.mark.parametrize("most", [None, 1, 3000, 100000])
 @pytest.mark.parametrize("most_q", [None, 1, 100000])
