@@ -578,7 +578,7 @@ int gdn_attn_paged(const void* q, const void* k_pages, const void* v_pages, cons
     if (p && !aligned(p, 16)) return GDN_ERR_ARG;
   if (!aligned(lse, 4)) return GDN_ERR_ARG;
   if (n_seqs == 0 || total_q == 0) return GDN_OK;
-  if (!q || !o || !page_table || !k_len || (n_pages > 0 && (!k_pages || !v_pages))) return GDN_ERR_ARG;
+  if (!q || !o || !k_len || (max_pages > 0 && !page_table) || (n_pages > 0 && (!k_pages || !v_pages))) return GDN_ERR_ARG;
   const long long capacity = (long long)max_pages * page_size;
   const PagedPlan p = paged_plan(n_seqs, total_q, max_q, max_k < capacity ? max_k : capacity, Hq, Hk);
   if (!ws || ws_bytes < p.total) return GDN_ERR_WORKSPACE;

@@ -44,7 +44,7 @@ CASES = [
     ([513], [700], 3, 1), ([100, 260], [100, 1260], 6, 2),           # groups of 3: 126 rows to a tile
     ([64, 130, 3], [2700, 131, 3], 8, 2),                            # continuing cached keys
     ([50, 200, 3], [20, 130, 0], 4, 2),                              # more queries than keys: rows that see none
-    ([0, 0], [5, 300], 2, 1), ([0, 2], [40, 0], 2, 1),
+    ([0, 0], [5, 300], 2, 1), ([0, 2], [40, 0], 2, 1), ([0, 3], [0, 0], 8, 2), ([200], [0], 4, 2),  # (no table at all)
     ([40], [333], 16, 1), ([9], [260], 128, 1), ([7], [140], 100, 1),
     ([1, 1, 1, 2, 1], [4000, 1, 0, 129, 2048], 8, 2), ([1] * 40, list(range(0, 400, 10)), 4, 4),
 ]
