@@ -18,12 +18,14 @@
 // A key's sum is formed by one thread in a fixed order and added once to its place
 // (by an atomic addition: sequences that share a page each add theirs).
 //
-// Bounds.  Prompts: the exponentials, a tile of 128 x 128 takes an SM 0.27 us of its 32 a clock,
-// whose issue the fma and the addition share: 8192 + 640 + 77 tokens with 16/4 heads take 105 us
-// (138 GFLOP, 1.3 PFLOP/s; 115 where a key tile began behind the last one's end).  Chunks over
-// caches: the same (2048 over 32768 keys 192 us), short ones the latency of a key tile's start, some
-// 2.5 us (16 x 128 tokens over 4096 keys 41 us).  Tokens: HBM, 32 over 1 to 16214 keys 47 us for
-// 274 MB, 5.8 TB/s.
+// Bounds.  Prompts: shared memory, where a tile's product of 128 x 128 reads 64 KB beside the 32
+// that the load writes, 768 clocks; a tile takes 0.41 us (its product alone 0.33, its
+// exponentials 0.27).  8192 + 640 + 77 tokens with 16/4 heads: 105 us (138 GFLOP, 1.3 PFLOP/s; 115
+// where a key tile began behind the last one's end).  With the keys in tensor memory there is
+// room for three S buffers only, whose way round is then longer: 120 us, handed back by halves
+// 114.  Chunks over caches: the same (2048 over 32768 keys 192 us), short ones the latency of a key
+// tile's start, some 2.5 us (16 x 128 tokens over 4096 keys 41 us).  Tokens: HBM, 32 over 1 to
+// 16214 keys 47 us for 274 MB, 5.8 TB/s.
 #include <math.h>
 
 #include "gdn_attn.cuh"
