@@ -15,6 +15,8 @@
 // only as many columns are formed as there are rows, two CTAs to an SM, each with an
 // equal run of all sequences' key tiles.
 //
+// Where lengths may differ both are started, and each takes the sequences that suit it.
+//
 // A key's sum is formed by one thread in a fixed order and added once to its place
 // (by an atomic addition: sequences that share a page each add theirs).
 //
@@ -139,20 +141,23 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) k_weigh_many(const __grid_con
   constexpr int ISSUES = 4 * MANY_GROUPS, LOADS = ISSUES + 2, PLANS = ISSUES + 3, NG = MANY_GROUPS, NS = MANY_S;
   pdl_wait();
   pdl_release();
-  clear_status(a.at.status);
+  if (!a.few) clear_status(a.at.status);  // (the kernel ahead has)
   const int G = a.at.Hq / a.at.Hk, TT = CH / G;
   const int split = a.split, rank = blockIdx.x % split, team = blockIdx.x / split, teams = gridDim.x / split;
-  // the lengths of a sequence, and its key tiles (none without queries)
+  // the lengths of a sequence, and its key tiles (none without queries, or where it is not this kernel's)
   auto rows = [&](int s) { return rows_of(a.at.cu_q, s, a.at.n_seqs, a.at.total_q); };
   auto keys = [&](int s) { return min(max(a.at.k_len[s], 0), a.at.pages.capacity); };
-  auto tiles = [&](int s) { return rows(s).y > 0 ? (keys(s) + CH - 1) / CH : 0; };
+  auto count = [&](int ql, int kl) {
+    return ql > 0 && (a.many == WeighArgs::ALL || !WeighArgs::small(ql, G)) ? (kl + CH - 1) / CH : 0;
+  };
+  auto tiles = [&](int s) { return count(rows(s).y, keys(s)); };
   int2 lane_q = make_int2(0, 0);  // of the first 32 sequences
   int lane_kl = 0;
   if (lane < a.at.n_seqs) {
     lane_q = rows(lane);
     lane_kl = keys(lane);
   }
-  const int own = lane_q.y > 0 ? (lane_kl + CH - 1) / CH : 0;
+  const int own = count(lane_q.y, lane_kl);
 
   if (warp == LOADS && lane == 0) {
     for (int k = 0; k < MANY_SLOTS; ++k) {
@@ -408,7 +413,10 @@ struct Run {
   int seq, kh, tile, tiles;
   Seq sq;
 
-  __device__ __forceinline__ int count(int ql, int kl) const { return ql > 0 ? (kl + CH - 1) / CH : 0; }
+  __device__ __forceinline__ int count(int ql, int kl) const {
+    const bool mine = a.few == WeighArgs::ALL || WeighArgs::small(ql, a.at.Hq / a.at.Hk);
+    return ql > 0 && mine ? (kl + CH - 1) / CH : 0;
+  }
   __device__ __forceinline__ void read(int from) {
     s0 = from;
     const int s = s0 + (threadIdx.x & 31);
@@ -522,8 +530,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) k_weigh_few(const __grid_const
           w.ok = __all_sync(0xffffffffu, w.ok);
           if (w.ok && lane == 0) {
             tc::arrive_expect_tx(&sm.qfull[i & 1], 2u * 128u * (uint32_t)(TT * G));
-            tc::tma_load_3d(sm.q[i & 1], &a.at.q, 0, run.kh * G, run.sq.q0 + qt * TT, &sm.qfull[i & 1]);
-            tc::tma_load_3d(sm.q[i & 1] + QTILE / 2, &a.at.q, 64, run.kh * G, run.sq.q0 + qt * TT, &sm.qfull[i & 1]);
+            tc::tma_load_3d(sm.q[i & 1], &a.q, 0, run.kh * G, run.sq.q0 + qt * TT, &sm.qfull[i & 1]);
+            tc::tma_load_3d(sm.q[i & 1] + QTILE / 2, &a.q, 64, run.kh * G, run.sq.q0 + qt * TT, &sm.qfull[i & 1]);
           }
           ++i;
         }
@@ -625,12 +633,17 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) k_weigh_few(const __grid_const
 }  // namespace
 
 cudaError_t launch_weigh(const WeighArgs& a, cudaStream_t s) {
-  const auto kernel = a.few ? k_weigh_few : k_weigh_many;
-  const size_t smem = (a.few ? sizeof(FewSmem) : sizeof(ManySmem)) + 1024;
   static_assert(sizeof(ManySmem) + 1024 <= 227 * 1024 && 2 * (sizeof(FewSmem) + 2048) <= 228 * 1024, "shared memory");
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = cudaSuccess;
+  if (a.few) {
+    const size_t smem = sizeof(FewSmem) + 1024;
+    e = cudaFuncSetAttribute(k_weigh_few, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess) e = launch_pdl(k_weigh_few, dim3((unsigned)a.few_ctas), dim3(FEW_THREADS), smem, s, a);
+  }
+  if (e != cudaSuccess || !a.many) return e;
+  const size_t smem = sizeof(ManySmem) + 1024;
+  e = cudaFuncSetAttribute(k_weigh_many, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  if (a.few) return launch_pdl(kernel, dim3((unsigned)a.ctas), dim3(FEW_THREADS), smem, s, a);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.split * a.ctas));
   cfg.blockDim = dim3(MANY_THREADS);
@@ -644,7 +657,7 @@ cudaError_t launch_weigh(const WeighArgs& a, cudaStream_t s) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, a);
+  return cudaLaunchKernelEx(&cfg, k_weigh_many, a);
 }
 
 }  // namespace gdn

@@ -60,6 +60,7 @@ def test_chunks_over_pages(gdn_lib, ql, kl, Hq, Hk, page):
 @pytest.mark.parametrize("ql,kl,Hq,Hk", [
     ([1300], [1300], 16, 8),                                         # pairs of CTAs with several key tiles each
     ([1100, 900], [1100, 3001], 16, 8), ([70] * 6, list(range(1990, 2014, 4)), 8, 2),   # CTAs with several
+    ([400, 1, 64, 3, 65, 1, 0, 1], [500, 3000, 3000, 2900, 3000, 1, 7, 2800], 8, 4),    # long ones beside short ones
     ([64, 60, 65], [1000, 64, 2500], 4, 1), ([200, 1, 1, 1, 1, 1], [777, 500, 1, 0, 1111, 40], 8, 2),  # several query tiles
 ])
 def test_several_tiles_each(gdn_lib, ql, kl, Hq, Hk):
