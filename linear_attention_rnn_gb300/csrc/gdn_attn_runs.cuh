@@ -71,6 +71,7 @@ struct Planner {
 
   __device__ __forceinline__ Planner(const AttnArgs& args, int s) : a(args), S(s), s0(-32) {}
   __device__ __forceinline__ long begin(int c) const { return each * c + min((long)c, longer); }
+  __device__ __forceinline__ int keys(int s) const { return min(max(a.k_len[s], 0), a.pages.capacity); }
   __device__ __forceinline__ void read(int from) {
     s0 = from;
     const int s = s0 + (threadIdx.x & 31);
@@ -79,7 +80,7 @@ struct Planner {
       const int2 q = rows_of(a.cu_q, s, a.n_seqs, a.total_q);
       lane_q0 = q.x;
       lane_ql = q.y;
-      lane_kl = min(max(a.k_len[s], 0), a.pages.capacity);
+      lane_kl = keys(s);
     }
   }
   __device__ __forceinline__ void take() {
@@ -99,52 +100,70 @@ struct Planner {
   static __device__ __forceinline__ long from(long v, int lane) {
     return (long)__shfl_sync(0xffffffffu, (unsigned long long)v, lane);
   }
-  // The run of CTA `cta` of `most`; fewer have one where it would be narrower than `narrow`.
+  // The run of CTA `cta` of `most`; fewer have one where it would be narrower than `narrow`.  A lane
+  // adds up a 32nd of the sequences, one behind another, so that their lengths are asked for at
+  // once (32 at a time, one after another, 256 tokens over 1024 keys each took 104 us for 98, 1000
+  // over 300 153 for 129).
   __device__ __forceinline__ void start(int cta, int most_ctas, int narrow) {
-    long all = 0;
-    for (int s = 0; s < a.n_seqs; s += 32) {
-      read(s);
-      all += from(sums(Seqs(lane_ql, lane_kl, S).total()), 31);
+    const int lane = threadIdx.x & 31, block = (a.n_seqs + 31) / 32;
+    long mine = 0;
+    if (block == 1) {
+      read(0);
+      mine = Seqs(lane_ql, lane_kl, S).total();
+    } else {
+#pragma unroll 4
+      for (int i = 0; i < block; ++i) {
+        const int s = min(lane * block + i, a.n_seqs - 1);
+        const int ql = rows_of(a.cu_q, s, a.n_seqs, a.total_q).y, kl = keys(s);
+        if (lane * block + i < a.n_seqs) mine += Seqs(ql, kl, S).total();
+      }
     }
-    all *= a.Hk;
+    long upto = sums(mine * a.Hk);
+    const long all = from(upto, 31);
     ctas = all >= (long)narrow * most_ctas ? most_ctas : max(1, (int)((unsigned)all / (unsigned)narrow));
     each = all >> 32 ? all / ctas : (long)((unsigned)all / (unsigned)ctas);  // (the short division where it does)
     longer = all - each * ctas;
     const long lo = begin(cta);
     left = cta < ctas ? begin(cta + 1) - lo : 0;
     if (left <= 0) return;
-    long ahead = 0;
-    for (int s = 0; s < a.n_seqs; s += 32) {
-      if (s != s0) read(s);
-      const long mine = Seqs(lane_ql, lane_kl, S).total() * a.Hk, upto = sums(mine);
-      const unsigned past = __ballot_sync(0xffffffffu, ahead + upto > lo);
-      if (past) {
-        const int l = __ffs((int)past) - 1;
-        seq = s + l;
-        take();
-        const Seqs it(ql, kl, S);
-        const long one = it.total();
-        long in = lo - ahead - from(upto - mine, l);
-        kh = 0;
-        while (in >= one) {  // (a few heads)
-          in -= one;
-          ++kh;
+    // the lane, or behind it the sequence of its block, in which the run begins
+    int l = __ffs((int)__ballot_sync(0xffffffffu, upto > lo)) - 1;
+    long ahead = from(upto - mine * a.Hk, l);
+    seq = l;
+    if (block > 1) {
+      for (int s = l * block;; s += 32) {
+        read(s);
+        mine = s + lane < a.n_seqs ? Seqs(lane_ql, lane_kl, S).total() : 0;
+        upto = ahead + sums(mine * a.Hk);
+        const unsigned past = __ballot_sync(0xffffffffu, upto > lo);
+        if (past) {
+          l = __ffs((int)past) - 1;
+          ahead = from(upto - mine * a.Hk, l);
+          seq = s + l;
+          break;
         }
-        int b = 0, e = it.n;  // before(b) <= in < before(e)
-        while (e - b > 1) {
-          const int m = (b + e) >> 1;
-          if (it.before(m) <= in)
-            b = m;
-          else
-            e = m;
-        }
-        i = b;
-        x0 = (int)(in - it.before(b));
-        return;
+        ahead = from(upto, 31);
       }
-      ahead += from(upto, 31);
     }
-    left = 0;
+    take();
+    const Seqs it(ql, kl, S);
+    const long one = it.total();
+    long in = lo - ahead;
+    kh = 0;
+    while (in >= one) {  // (a few heads)
+      in -= one;
+      ++kh;
+    }
+    int b = 0, e = it.n;  // before(b) <= in < before(e)
+    while (e - b > 1) {
+      const int m = (b + e) >> 1;
+      if (it.before(m) <= in)
+        b = m;
+      else
+        e = m;
+    }
+    i = b;
+    x0 = (int)(in - it.before(b));
   }
   // The next N items of the run (or those that are left); those without work for this CTA are
   // left out.

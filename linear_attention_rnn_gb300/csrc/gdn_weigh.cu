@@ -58,6 +58,19 @@ __device__ __forceinline__ bool all128(int id, bool ok) {
   return y != 0;
 }
 
+// Inclusive sums over the lanes of a warp, and one lane's value.
+__device__ __forceinline__ long sums(long v) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long y = (long)__shfl_up_sync(0xffffffffu, (unsigned long long)v, o);
+    if ((threadIdx.x & 31) >= o) v += y;
+  }
+  return v;
+}
+__device__ __forceinline__ long from(long v, int lane) {
+  return (long)__shfl_sync(0xffffffffu, (unsigned long long)v, lane);
+}
+
 // Column r of the query tile of TT tokens from token tok0 on.
 __device__ __forceinline__ void column(const WeighArgs& a, const Seq& sq, int kh, int G, int TT, int tok0, int r,
                                        float& nl, int& lim) {
@@ -176,13 +189,15 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) k_weigh_many(const __grid_con
     tc::mbar_fence_init();
   }
   if (warp == 0) tc::alloc(&sm.tmem, 512);
-  // Units, those with the most queries first, to the teams there and back again.  Every warp
-  // knows how many are the team's, whatever its waits come to.
+  // Units, of up to 32 sequences those with the most queries first, to the teams there and back again.
+  // Every warp knows how many are the team's, whatever its waits come to.
   int n_units;
   {
-    long all = __reduce_add_sync(0xffffffffu, own);
-    for (int s = 32; s < a.at.n_seqs; s += 32)
-      all += __reduce_add_sync(0xffffffffu, s + lane < a.at.n_seqs ? tiles(s + lane) : 0);
+    long all = own;
+#pragma unroll 4
+    for (int s = 32 + lane; s < a.at.n_seqs; s += 32) all += tiles(s);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) all += (long)__shfl_xor_sync(0xffffffffu, (unsigned long long)all, o);
     all *= a.at.Hk;
     const long rounds = all / teams, rest = all - rounds * teams;
     n_units = (int)rounds + ((rounds & 1 ? teams - 1 - team : team) < rest ? 1 : 0);
@@ -200,12 +215,41 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) k_weigh_many(const __grid_con
   // t counts query tiles over all of the CTA's units.
   int t = 0;
   if (warp == PLANS) {
+    // of more sequences than lanes a lane adds up a 32nd, one behind another
+    const int block = (a.at.n_seqs + 31) / 32;
+    long mine = 0, upto = 0;
+    if (block > 1) {
+#pragma unroll 4
+      for (int i = 0; i < block; ++i) {
+        const int s = lane * block + i, k = tiles(min(s, a.at.n_seqs - 1));
+        if (s < a.at.n_seqs) mine += k;
+      }
+      upto = sums(mine);
+    }
     for (int n = 0; n < n_units; ++n) {
       const int b = n & 1;
-      const long unit = (long)n * teams + (n & 1 ? teams - 1 - team : team);
-      // (a tile's index from its sequence's end)
-      const int2 from_end = find_nth(tiles, own, a.at.n_seqs, (int)(unit / a.at.Hk));
-      const int seq = max(from_end.x, 0);
+      const long unit = (long)n * teams + (n & 1 ? teams - 1 - team : team), rank_of = unit / a.at.Hk;
+      int seq, from_end = 0, from_start = 0;
+      if (block == 1) {  // (a tile's index from its sequence's end)
+        const int2 at = find_nth(tiles, own, a.at.n_seqs, (int)rank_of);
+        seq = max(at.x, 0);
+        from_end = at.y;
+      } else {  // one sequence behind another: enough of them to even out (sorted, by a search over all
+                // sequences for each unit, 1000 prompts of 100 tokens took 509 us for 113)
+        int l = __ffs((int)__ballot_sync(0xffffffffu, upto > rank_of)) - 1;
+        long before = from(upto - mine, l);
+        for (int s = l * block;; s += 32) {
+          const long k = s + lane < a.at.n_seqs ? tiles(s + lane) : 0, in = before + sums(k);
+          const unsigned past = __ballot_sync(0xffffffffu, in > rank_of);
+          if (past) {
+            l = __ffs((int)past) - 1;
+            seq = s + l;
+            from_start = (int)(rank_of - from(in - k, l));
+            break;
+          }
+          before = from(in, 31);
+        }
+      }
       int2 q;
       Unit u;
       if (seq < 32) {
@@ -217,7 +261,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) k_weigh_many(const __grid_con
       }
       u.kh = (int)(unit % a.at.Hk);
       u.off = u.kl - q.y;
-      u.tile = (u.kl + CH - 1) / CH - 1 - from_end.y;
+      u.tile = block == 1 ? (u.kl + CH - 1) / CH - 1 - from_end : from_start;
       u.row = q.x;
       u.ql = q.y;
       u.table = a.at.table + (long)seq * a.at.pages.table_stride;
@@ -435,39 +479,51 @@ struct Run {
     sq.k0 = 0;
     tiles = count(sq.ql, sq.kl);
   }
+  // A lane counts for a 32nd of the sequences, one behind another, so that their lengths are asked for
+  // at once.
   __device__ __forceinline__ explicit Run(const WeighArgs& args) : a(args), left(0) {
-    const int lane = threadIdx.x & 31;
-    long total = 0;
-    for (int s = 0; s < a.at.n_seqs; s += 32) {
-      read(s);
-      total += __reduce_add_sync(0xffffffffu, count(lane_ql, lane_kl));
+    const int lane = threadIdx.x & 31, block = (a.at.n_seqs + 31) / 32;
+    int mine = 0;
+    if (block == 1) {
+      read(0);
+      mine = count(lane_ql, lane_kl);
+    } else {
+#pragma unroll 4
+      for (int i = 0; i < block; ++i) {
+        const int s = min(lane * block + i, a.at.n_seqs - 1);
+        const int ql = rows_of(a.at.cu_q, s, a.at.n_seqs, a.at.total_q).y;
+        const int kl = min(max(a.at.k_len[s], 0), a.at.pages.capacity);
+        if (lane * block + i < a.at.n_seqs) mine += count(ql, kl);
+      }
     }
-    total *= a.at.Hk;
+    long upto = sums(mine);
+    const long total = from(upto, 31) * a.at.Hk;
     const long lo = total * blockIdx.x / gridDim.x, hi = total * (blockIdx.x + 1) / gridDim.x;
     left = (int)(hi - lo);
     if (left == 0) return;
-    long before = 0;  // units ahead of the 32 sequences
-    for (int s = 0; s < a.at.n_seqs; s += 32) {
-      if (s != s0) read(s);
-      const int mine = count(lane_ql, lane_kl);
-      int upto = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += y;
+    // the lane, or behind it the sequence of its block, in which the run begins
+    int l = __ffs((int)__ballot_sync(0xffffffffu, upto * a.at.Hk > lo)) - 1;
+    long before = from(upto - mine, l);  // key tiles ahead of it
+    seq = l;
+    if (block > 1) {
+      for (int s = l * block;; s += 32) {
+        read(s);
+        mine = count(lane_ql, lane_kl);
+        upto = before + sums(mine);
+        const unsigned past = __ballot_sync(0xffffffffu, upto * a.at.Hk > lo);
+        if (past) {
+          l = __ffs((int)past) - 1;
+          before = from(upto - mine, l);
+          seq = s + l;
+          break;
+        }
+        before = from(upto, 31);
       }
-      const unsigned past = __ballot_sync(0xffffffffu, before + (long)upto * a.at.Hk > lo);
-      if (past) {
-        const int l = __ffs((int)past) - 1;
-        seq = s + l;
-        const long start = before + (long)__shfl_sync(0xffffffffu, upto - mine, l) * a.at.Hk;
-        take();
-        kh = (int)((lo - start) / tiles);
-        tile = (int)(lo - start - (long)kh * tiles);
-        return;
-      }
-      before += (long)__shfl_sync(0xffffffffu, upto, 31) * a.at.Hk;
     }
+    take();
+    const long in = lo - before * a.at.Hk;
+    kh = (int)(in / tiles);
+    tile = (int)(in - (long)kh * tiles);
   }
   __device__ __forceinline__ bool last_of_head() const { return left == 1 || tile + 1 == tiles; }
   __device__ __forceinline__ void next() {

@@ -92,6 +92,17 @@ def test_many_sequences_of_any_length(gdn_lib, Hq, Hk):
         both(gdn_lib, x, ql, kl, most_q=most_q, weights=most_q is None)
 
 
+@pytest.mark.parametrize("n,most", [(33, 400), (64, 300), (1030, 20)])
+def test_prompts_of_many_sequences(gdn_lib, n, most):
+    """More sequences than a warp has lanes, a few of them long beside short ones."""
+    gen = torch.Generator().manual_seed(n)
+    ql = torch.randint(0, most, (n,), generator=gen).tolist()
+    ql[n // 2], ql[n - 1] = 500, 1
+    kl = [q + int(k) for q, k in zip(ql, torch.randint(0, 60, (n,), generator=gen))]
+    x = paged.cache(ql, kl, 4, 1, 32, seed=n)
+    both(gdn_lib, x, ql, kl, most=max(kl))
+
+
 @pytest.mark.parametrize("scale,spread", [(1.0, 1.0), (0.02, 1.0), (None, 8.0)])
 def test_sharp_and_flat_rows(gdn_lib, scale, spread):
     x = paged.cache([300], [700], 2, 1, 64, seed=3, spread=spread)
