@@ -724,7 +724,7 @@ def _page_layout(shape, strides):
     return _PageStrides(st[0], st[1], st[2])
 
 
-def _check_pages(t, name, Hk=None, like=None):
+def _check_pages(t, name, Hk=None, like=None, d=None):
     """A cache [pages, page_size, Hk, d] in bf16 whose rows of d values are contiguous and
     lie multiples of 8 elements apart; returns its strides as the C struct."""
     if not t.is_cuda:
@@ -735,6 +735,8 @@ def _check_pages(t, name, Hk=None, like=None):
         raise ValueError(f"{name} must be [pages, page_size, {'Hk' if Hk is None else Hk}, d], got {tuple(t.shape)}")
     if like is not None and t.shape != like.shape:
         raise ValueError(f"k_pages and v_pages have shapes {tuple(like.shape)} and {tuple(t.shape)}")
+    if d is not None and t.shape[3] != d:
+        raise ValueError(f"{name} has heads of {t.shape[3]}, expected {d}")
     d = t.shape[3]
     strides = t.stride()
     if t.numel():
@@ -875,7 +877,7 @@ def rope_append(q, k, v, positions, inv_freq, k_pages, v_pages, slots, *, q_weig
     if v.shape != k.shape:
         raise ValueError(f"k and v have shapes {tuple(k.shape)} and {tuple(v.shape)}")
     sv = _check_rows(v, "v", Hk, d, n)
-    ks = _check_pages(k_pages, "k_pages", Hk)
+    ks = _check_pages(k_pages, "k_pages", Hk, d=d)
     vs = _check_pages(v_pages, "v_pages", Hk, k_pages)
     _check(slots, "slots", torch.int32, q.shape[:-2])
     q_out, so = _rows_out(q_out, "q_out", q, n, Hq, d)
@@ -904,9 +906,7 @@ def _paged_dims(q, k_pages, page_table, k_len, cu_q, max_k, scale):
         n, total = q.shape[0], q.shape[0] * q.shape[1]
     Hq, d = q.shape[-2:]
     sq = _check_rows(q, "q", Hq, d, total)
-    ks = _check_pages(k_pages, "k_pages")
-    if k_pages.shape[3] != d:
-        raise ValueError(f"q and k_pages have heads of {d} and {k_pages.shape[3]}")
+    ks = _check_pages(k_pages, "k_pages", d=d)
     P, page, Hk = k_pages.shape[:3]
     pages, st = _check_table(page_table, "page_table", n)
     _check(k_len, "k_len", torch.int32, (n,))
