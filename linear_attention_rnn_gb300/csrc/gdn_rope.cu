@@ -327,10 +327,13 @@ __global__ void __launch_bounds__(ROPE_THREADS, BACK ? 2 : 3) k_rope(const __gri
     uint4 o[2] = {from[0], from[32]};
     F2 x[8], y[8];
     if (!BACK) {
+      unpack16(o, x);
+      // (the sums cross heads of keys and of values, which a step may have side by side: the whole warp forms
+      // them where one of its heads has a norm, and those of values are not used)
+      float r = 1.f;
+      if (normed && (!PAGED || SIDE * i < Hqk)) r = rsqrtf(head_sum(dot(x, x)) * (1.f / HD) + a.eps);
       if (!PAGED || h < Hqk) {
-        unpack16(o, x);
         if (normed) {
-          float r = rsqrtf(head_sum(dot(x, x)) * (1.f / HD) + a.eps);
           if (!(is_k ? k.w : q.w)) r = 1.f;
           const F2 rr = pair(r, r);
 #pragma unroll
