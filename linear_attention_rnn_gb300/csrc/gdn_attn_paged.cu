@@ -33,8 +33,12 @@ using namespace attn;
 constexpr float RAISE = 8.f;  // base-2 headroom before the running maximum is raised
 constexpr int BATCH = 16;     // items that are planned at a time
 
-// all threads of the block, from wherever their role has taken them
-__device__ __forceinline__ void block_sync() { asm volatile("bar.sync 0;" ::: "memory"); }
+// The N threads that have a role: they meet around a new plan, twice.  (Not at the block's barrier, where
+// warps without a role may be already, which go straight to the kernel's end.)
+template <int N>
+__device__ __forceinline__ void roles_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
+}
 
 // two warps that have the same rows
 __device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
@@ -98,7 +102,7 @@ __device__ __forceinline__ void leave_whole(Stage& st, bf16* o, const int (&at)[
 
 // ---- sequences of more than one query tile ---------------------------------------------------
 constexpr int NSLOT = 4;
-constexpr int MANY_THREADS = 384;
+constexpr int MANY_THREADS = 384, MANY_ROLES = 320;  // (two groups of softmax, one warp that issues, one that plans and loads)
 // Keys that an item's start and end take the time of, and a run's width, at least.  Measured in us
 // for a mixed step, 2048 tokens over 32768 keys, 40 over 16384: 55, 308, 28; without extra and 128
 // at least 90, 309, 29; 1024 and 1536 61, 315, 35.
@@ -208,9 +212,9 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) k_paged_many(const __grid_con
           }
         }
         if (!sm.runs.more) break;
-        block_sync();  // the items have been read
+        roles_sync<MANY_ROLES>();  // the items have been read
         plan.fill(sm.runs, pa.joins, (int)blockIdx.x);
-        block_sync();
+        roles_sync<MANY_ROLES>();
       }
       if (lane == 0) {  // no copy is in flight when the CTA ends
         if (w.ok) {
@@ -305,8 +309,8 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) k_paged_many(const __grid_con
           }
         }
         if (!sm.runs.more) break;
-        block_sync();
-        block_sync();
+        roles_sync<MANY_ROLES>();
+        roles_sync<MANY_ROLES>();
       }
       // every commit has arrived before the CTA ends
       for (int u = max(0, t0 - NSLOT); u < t0; ++u) w.warp_on(&sm.empty[u % NSLOT], u / NSLOT);
@@ -498,8 +502,8 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) k_paged_many(const __grid_con
         }
       }
       if (!sm.runs.more) break;
-      block_sync();
-      block_sync();
+      roles_sync<MANY_ROLES>();
+      roles_sync<MANY_ROLES>();
     }
   }
   if (!w.ok && a.status) atomicOr(a.status, 1);
@@ -593,9 +597,9 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) k_paged_few(const __grid_const
         }
       }
       if (!sm.runs.more) break;
-      block_sync();  // the items have been read
+      roles_sync<FEW_THREADS>();  // the items have been read
       plan.fill(sm.runs, pa.joins, (int)blockIdx.x);
-      block_sync();
+      roles_sync<FEW_THREADS>();
     }
     if (lane == 0) {  // no copy is in flight when the CTA ends
       if (w.ok) {
@@ -642,8 +646,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) k_paged_few(const __grid_const
         ++qc;
       }
       if (!sm.runs.more) break;
-      block_sync();
-      block_sync();
+      roles_sync<FEW_THREADS>();
+      roles_sync<FEW_THREADS>();
     }
     // every commit has arrived before the CTA ends
     for (int u = max(0, t0 - FEW_SLOTS); u < t0; ++u) w.warp_on(&sm.empty[u % FEW_SLOTS], u / FEW_SLOTS);
@@ -762,8 +766,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) k_paged_few(const __grid_const
         }
       }
       if (!sm.runs.more) break;
-      block_sync();
-      block_sync();
+      roles_sync<FEW_THREADS>();
+      roles_sync<FEW_THREADS>();
     }
   }
   if (!w.ok && a.status) atomicOr(a.status, 1);
