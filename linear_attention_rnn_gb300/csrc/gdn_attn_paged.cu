@@ -53,11 +53,8 @@ __device__ __forceinline__ void leave(const Item& it, bf16* o, float* part, floa
     store32(o, y, inv);
   } else if (!none) {  // (the join reads no part whose lse is minus infinity)
 #pragma unroll
-    for (int j = 0; j < 32; j += 8)  // 32 bytes, a whole sector
-      asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(part + j), "f"(inv * y[j]),
-                   "f"(inv * y[j + 1]), "f"(inv * y[j + 2]), "f"(inv * y[j + 3]), "f"(inv * y[j + 4]),
-                   "f"(inv * y[j + 5]), "f"(inv * y[j + 6]), "f"(inv * y[j + 7])
-                   : "memory");
+    for (int j = 0; j < 32; j += 4)  // (16 bytes: a workspace need not lie at a multiple of more)
+      *reinterpret_cast<float4*>(part + j) = make_float4(inv * y[j], inv * y[j + 1], inv * y[j + 2], inv * y[j + 3]);
   }
 }
 
