@@ -6,6 +6,7 @@
 #include <stddef.h>
 
 #include "gdn_common.cuh"
+#include "gdn_weigh_rule.cuh"
 
 namespace gdn {
 
@@ -253,23 +254,12 @@ struct PagedArgs {
 };
 
 // The weight that attention gives to each key in pages (gdn_weigh.cu).
-constexpr int WEIGH_FEW_ROWS = 64;  // rows of a query tile in the kernel for few of them
-constexpr int WEIGH_FEW_TILES = 4;  // to a sequence, at most
 struct WeighArgs {
   AttnArgs at;          // q, k, cu_q, k_len, table and sizes
   CUtensorMap q;        // few: boxes of its query tiles
   const float* lse;     // [total_q][Hq]
   float* weights;       // [n_pages][Hk][page], added to
-  // Which sequences k_weigh_few takes, and which k_weigh_many: all, none, or (BY_SIZE, both) those of up
-  // to WEIGH_FEW_TILES query tiles of the former and the others.
-  int few, many;
-  int few_ctas;
-  int ctas;             // many: teams of `split` CTAs
-  int split;            // CTAs that share the queries of a key tile, 1 or 2
-  enum { NONE, ALL, BY_SIZE };
-  __host__ __device__ __forceinline__ static bool small(int ql, int G) {
-    return G <= WEIGH_FEW_ROWS && ql <= WEIGH_FEW_TILES * WEIGH_FEW_ROWS / G;
-  }
+  WeighRule rule;
 };
 
 // Eviction of the lightest keys from pages (gdn_evict.cu).

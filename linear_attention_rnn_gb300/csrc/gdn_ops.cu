@@ -627,24 +627,9 @@ int gdn_attn_paged_weights(const void* q, const void* k_pages, const float* lse,
   if (!q || !k_pages || !lse || !page_table || !k_len || !weights) return GDN_ERR_ARG;
   WeighArgs w;
   memset(&w, 0, sizeof w);
-  const int G = Hq / Hk;
-  const long long capacity = n_pages > 0 ? (long long)max_pages * page_size : 0, sms = sm_count();
-  const long long longest = max_k < capacity ? max_k : capacity, tiles = longest > CH ? (longest + CH - 1) / CH : 1;
-  const long long TT = CH / G, most_q = max_q > 0 && max_q < total_q ? max_q : total_q;
-  // Sequences of up to four of its query tiles suit the kernel for few rows (16 caches of 4096 rows,
-  // 16/4 heads: 64 new tokens 31 us against 37 in the other, 128 53 against 41; one of 32768 rows:
-  // 22 against 25 and 33 against 27).  Where lengths may differ both are started, and each takes its
-  // own (a prompt of 2048 tokens and 64 single tokens over 3000 keys: 67 us; in the kernel for few rows
-  // alone 2039, in the other 474), unless so few can be short that the other kernel's start
-  // takes longer (3 to 4 us; a key tile in the kernel for many rows 2.5 an SM).
-  const bool alike = !cu_q || n_seqs == 1;
-  const long long few_q = G <= WEIGH_FEW_ROWS ? WEIGH_FEW_TILES * WEIGH_FEW_ROWS / G : 0;
-  const bool small = WeighArgs::small((int)(alike ? total_q / n_seqs : most_q), G);
-  long long shorts = n_seqs;  // at most: the others have no more than most_q
-  if (!small && total_q > n_seqs * few_q) shorts -= (total_q - n_seqs * few_q + most_q - few_q - 1) / (most_q - few_q);
-  const bool none = alike || few_q == 0 || shorts * tiles * Hk <= 2 * sms;
-  w.few = small ? WeighArgs::ALL : none ? WeighArgs::NONE : WeighArgs::BY_SIZE;
-  w.many = small ? WeighArgs::NONE : none ? WeighArgs::ALL : WeighArgs::BY_SIZE;
+  const long long capacity = (long long)max_pages * page_size;
+  w.rule = weigh_rule(n_seqs, total_q, max_q, max_k < capacity ? max_k : capacity, !cu_q || n_seqs == 1, Hq, Hk, CH,
+                      sm_count());
   if ((rc = attn_args(w.at, q, nullptr, nullptr, cu_q, nullptr, n_seqs, total_q, 0, Hq, Hk, scale, q_stride,
                       (long long)Hk * HD, (long long)Hk * HD)))
     return rc;
@@ -657,20 +642,8 @@ int gdn_attn_paged_weights(const void* q, const void* k_pages, const float* lse,
     return GDN_ERR_CUDA;
   w.lse = lse;
   w.weights = weights;
-  if (w.few && !tmap_rows(&w.q, q, total_q, Hq, HD, (uint64_t)q_stride * 2, G, WEIGH_FEW_ROWS / G)) return GDN_ERR_CUDA;
-  // Pairs share a key tile where one CTA would still be at the first, which sees all queries of
-  // its sequence, when the others are done (in query tiles; a causal prompt has half of all): a
-  // prompt of 2500 tokens, 16/4 heads, 25 us against 39, four of 1024 18 against 21, of 2500
-  // 54 against 47.  With long units the smaller pieces alone win something (8192 + 640 + 77
-  // tokens: 105 against 109, 16384 with 16/2 heads: 382 against 412), with short ones the pair's
-  // meeting at each costs more (768 tokens, 16/16: 12.5 against 10.4).
-  const long long first = most_q / TT, each = total_q / TT * tiles * Hk / 2 / sms;
-  w.split = first >= 8 && (first > 2 * each || (first >= 64 && first > each)) ? 2 : 1;
-  const long long units = tiles * Hk;
-  // two CTAs to an SM (few), or one, but no more than there can be key tiles
-  auto ctas = [&](long long most) { return (int)(units < most && units * n_seqs < most ? units * n_seqs : most); };
-  w.few_ctas = ctas(2 * sms);
-  w.ctas = ctas(sms / w.split);
+  const int G = Hq / Hk;
+  if (w.rule.few && !tmap_rows(&w.q, q, total_q, Hq, HD, (uint64_t)q_stride * 2, G, WEIGH_FEW_ROWS / G)) return GDN_ERR_CUDA;
   return cuda_status(launch_weigh(w, static_cast<cudaStream_t>(stream)));
 }
 

@@ -154,14 +154,14 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) k_weigh_many(const __grid_con
   constexpr int ISSUES = 4 * MANY_GROUPS, LOADS = ISSUES + 2, PLANS = ISSUES + 3, NG = MANY_GROUPS, NS = MANY_S;
   pdl_wait();
   pdl_release();
-  if (!a.few) clear_status(a.at.status);  // (the kernel ahead has)
+  if (!a.rule.few) clear_status(a.at.status);  // (the kernel ahead has)
   const int G = a.at.Hq / a.at.Hk, TT = CH / G;
-  const int split = a.split, rank = blockIdx.x % split, team = blockIdx.x / split, teams = gridDim.x / split;
+  const int split = a.rule.split, rank = blockIdx.x % split, team = blockIdx.x / split, teams = gridDim.x / split;
   // the lengths of a sequence, and its key tiles (none without queries, or where it is not this kernel's)
   auto rows = [&](int s) { return rows_of(a.at.cu_q, s, a.at.n_seqs, a.at.total_q); };
   auto keys = [&](int s) { return min(max(a.at.k_len[s], 0), a.at.pages.capacity); };
   auto count = [&](int ql, int kl) {
-    return ql > 0 && (a.many == WeighArgs::ALL || !WeighArgs::small(ql, G)) ? (kl + CH - 1) / CH : 0;
+    return ql > 0 && (a.rule.many == WeighRule::ALL || !WeighRule::small(ql, G)) ? (kl + CH - 1) / CH : 0;
   };
   auto tiles = [&](int s) { return count(rows(s).y, keys(s)); };
   int2 lane_q = make_int2(0, 0);  // of the first 32 sequences
@@ -458,7 +458,7 @@ struct Run {
   Seq sq;
 
   __device__ __forceinline__ int count(int ql, int kl) const {
-    const bool mine = a.few == WeighArgs::ALL || WeighArgs::small(ql, a.at.Hq / a.at.Hk);
+    const bool mine = a.rule.few == WeighRule::ALL || WeighRule::small(ql, a.at.Hq / a.at.Hk);
     return ql > 0 && mine ? (kl + CH - 1) / CH : 0;
   }
   __device__ __forceinline__ void read(int from) {
@@ -691,17 +691,17 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) k_weigh_few(const __grid_const
 cudaError_t launch_weigh(const WeighArgs& a, cudaStream_t s) {
   static_assert(sizeof(ManySmem) + 1024 <= 227 * 1024 && 2 * (sizeof(FewSmem) + 2048) <= 228 * 1024, "shared memory");
   cudaError_t e = cudaSuccess;
-  if (a.few) {
+  if (a.rule.few) {
     const size_t smem = sizeof(FewSmem) + 1024;
     e = cudaFuncSetAttribute(k_weigh_few, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess) e = launch_pdl(k_weigh_few, dim3((unsigned)a.few_ctas), dim3(FEW_THREADS), smem, s, a);
+    if (e == cudaSuccess) e = launch_pdl(k_weigh_few, dim3((unsigned)a.rule.few_ctas), dim3(FEW_THREADS), smem, s, a);
   }
-  if (e != cudaSuccess || !a.many) return e;
+  if (e != cudaSuccess || !a.rule.many) return e;
   const size_t smem = sizeof(ManySmem) + 1024;
   e = cudaFuncSetAttribute(k_weigh_many, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.split * a.ctas));
+  cfg.gridDim = dim3((unsigned)(a.rule.split * a.rule.ctas));
   cfg.blockDim = dim3(MANY_THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -709,7 +709,7 @@ cudaError_t launch_weigh(const WeighArgs& a, cudaStream_t s) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)a.split;
+  attr[1].val.clusterDim.x = (unsigned)a.rule.split;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
