@@ -524,7 +524,7 @@ int gdn_rope_append(const void* q, const void* k, const void* v, const float* q_
  * to_stride entries between sequences, with to_pages * page_size rows for min(budget,
  * max_pages * page_size) keys): keys, values and weights.  to_table NULL or page_table:
  * the sequence's own pages, in place.  Other rows keep what they hold.  new_len [n_seqs] receives
- * the keys that stay of each sequence (the same for all heads); it must not be k_len.
+ * the keys that stay of each sequence (the same for all heads); it must not overlap k_len.
  * Keys on absent pages never stay; a row whose target page is absent is not written.  In
  * place, no page may occur twice in the tables; otherwise no target page may, nor may one
  * hold a key of any sequence of the call.  ws: gdn_cache_evict_workspace_bytes(n_seqs, max_pages *

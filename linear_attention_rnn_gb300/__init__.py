@@ -987,7 +987,7 @@ def cache_evict(k_pages, v_pages, weights, page_table, k_len, budget: int, *, re
     lowest index), `budget` in all.  What stays moves in its order, with its values and weights, to
     the first rows of the pages that to_table [n, ..] lists (None: the sequence's own, in place;
     no page may occur twice then; other target pages may not either, nor hold a key of the call).
-    Returns the new lengths, int32 [n] (new_len, if given; it must not be k_len)."""
+    Returns the new lengths, int32 [n] (new_len, if given; it must not overlap k_len)."""
     ks = _check_pages(k_pages, "k_pages")
     P, page, Hk, d = k_pages.shape
     vs = _check_pages(v_pages, "v_pages", Hk, k_pages)

@@ -88,7 +88,7 @@ bool one_launch(const DecayArgs& a) {
   return a.seg_chunks <= 6 && (long)(a.n_roles + 1) * a.slots * a.Hv <= sm_count();
 }
 
-// Whether two states' buffers of `bytes` share any of them.
+// Whether two buffers of `bytes` share any of them.
 inline bool overlap(const void* a, const void* b, size_t bytes) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return a && b && (x < y ? y - x : x - y) < bytes;
@@ -673,7 +673,7 @@ int gdn_cache_evict(void* k_pages, void* v_pages, float* weights, const int* pag
       !aligned(new_len, 4))
     return GDN_ERR_ARG;
   if (n_seqs == 0) return GDN_OK;
-  if (!new_len || new_len == k_len) return GDN_ERR_ARG;
+  if (!new_len || overlap(new_len, k_len, (size_t)n_seqs * sizeof(int))) return GDN_ERR_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (n_pages == 0 || max_pages == 0) return cuda_status(cudaMemsetAsync(new_len, 0, (size_t)n_seqs * sizeof(int), s));
   if (!k_pages || !v_pages || !weights || !page_table || !k_len) return GDN_ERR_ARG;
