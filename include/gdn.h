@@ -522,8 +522,8 @@ int gdn_rope_append(const void* q, const void* k, const void* v, const float* q_
  * equal weights the lowest index stays, NaN weighs least.  What stays moves in its order
  * into rows 0, 1, .. of the sequence's target pages to_table [n_seqs, to_pages] (int32,
  * to_stride entries between sequences, with to_pages * page_size rows for min(budget,
- * max_pages * page_size) keys): keys, values and weights.  to_table NULL or page_table:
- * the sequence's own pages, in place.  Other rows keep what they hold.  new_len [n_seqs] receives
+ * max_pages * page_size) keys): keys, values and weights.  to_table NULL or page_table (with
+ * its stride): the sequence's own pages, in place.  Other rows keep what they hold.  new_len [n_seqs] receives
  * the keys that stay of each sequence (the same for all heads); it must not overlap k_len.
  * Keys on absent pages never stay; a row whose target page is absent is not written.  In
  * place, no page may occur twice in the tables; otherwise no target page may, nor may one

@@ -666,6 +666,7 @@ int gdn_cache_evict(void* k_pages, void* v_pages, float* weights, const int* pag
   if (!page_strides_ok(k_strides) || !page_strides_ok(v_strides)) return GDN_ERR_ARG;
   const int capacity = max_pages * page_size, keep = budget < capacity ? budget : capacity;
   if (to_table && (to_pages < 0 || to_stride < to_pages || (long long)to_pages * page_size < keep)) return GDN_ERR_ARG;
+  if (to_table == page_table && to_table && n_seqs > 1 && to_stride != table_stride) return GDN_ERR_ARG;  // (other sequences' pages)
   const void* ptrs[] = {k_pages, v_pages, weights, ws};
   for (const void* p : ptrs)
     if (p && !aligned(p, 16)) return GDN_ERR_ARG;

@@ -30,3 +30,14 @@ def test_lengths_that_overlap(evict):
     for shift in (12, -12, 1 << 20):
         assert evict(k_len=at, new=at + shift) == WS
     assert evict(n=1, k_len=at, new=at) == ARG and evict(n=1, k_len=at, new=at + 4) == WS
+
+
+def test_the_table_as_target_with_other_rows(evict):
+    """The table itself as target means in place, row by row; other rows of the same memory are other
+    sequences' pages."""
+    at = 1 << 21
+    assert evict(table=at, to=at, to_wide=20, sto=20) == WS
+    assert evict(table=at, to=at, to_wide=16, sto=20) == WS         # the first columns of it
+    for sto in (16, 19, 21, 40):
+        assert evict(table=at, to=at, to_wide=16, sto=sto) == ARG
+    assert evict(n=1, table=at, to=at, to_wide=16, sto=16) == WS    # (one row: no distance between rows)
