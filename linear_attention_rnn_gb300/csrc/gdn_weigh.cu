@@ -17,8 +17,9 @@
 //
 // Where lengths may differ both are started, and each takes the sequences that suit it.
 //
-// A key's sum is formed by one thread in a fixed order and added once to its place
-// (by an atomic addition: sequences that share a page each add theirs).
+// A key's sum is formed by one thread in a fixed order (a query tile's terms in four chains, then
+// tile by tile, so that no chain is longer than some 64 additions and one to 128 terms) and added once to
+// its place (by an atomic addition: sequences that share a page each add theirs).
 //
 // Bounds.  Prompts: shared memory, where a tile's product of 128 x 128 reads 64 KB beside the 32
 // that the load writes, 768 clocks; a tile takes 0.41 us (its product alone 0.33, its
@@ -377,8 +378,9 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) k_weigh_many(const __grid_con
     if (n_units > 0) take(0);
     for (int n = 0; n < n_units; ++n) {
       const int key = u.tile * CH + r, kh = u.kh, page = entry, end = u.tile * CH + CH - 1;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      float all = 0.f;  // (tile by tile: a chain over all of a long prompt's terms rounds them all)
       for (; j < u.mine; j += NG) {
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
         Columns<CH>& cols = sm.cols[x][buf];
         const bool sees = l != -INFINITY;  // (a log-sum of NaN makes the keys' weights NaN)
         const int lim = sees ? (u.q0 + split * j) * TT + tok + u.off : -1;
@@ -404,11 +406,11 @@ __global__ void __launch_bounds__(MANY_THREADS, 1) k_weigh_many(const __grid_con
         tc::fence_before();
         tc::mbar_arrive(&sm.barE[x]);
         add32(v, cols, 96, key, end, clean[3], sc, sum);
+        all += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       }
       t += u.mine;
       if (n + 1 < n_units) take(n + 1);
       // (two sets of sums in turn: whoever writes one again has met the reader here since)
-      float all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
       if (x > 0) sm.sums[n & 1][x - 1][r] = all;
       asm volatile("bar.sync %0, %1;" ::"n"(1 + NG), "n"(128 * NG) : "memory");
       if (x == 0) {
@@ -646,7 +648,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) k_weigh_few(const __grid_const
       const Paged<CH> pg(a.at, run.seq, run.sq.kl);
       const int key = run.tile * CH + r;
       float* at = place(a, pg, run.kh, key);
-      float part[4] = {0.f, 0.f, 0.f, 0.f};
+      float even = 0.f, odd = 0.f;  // of the query tiles
       for (int qt = 0; qt < nq; ++qt, ++u) {
         const int rows = min(TT, run.sq.ql - qt * TT) * G;
         if (nq > 1 || fresh) {
@@ -665,6 +667,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) k_weigh_few(const __grid_const
         w.warp_on(&sm.barS[u % FEW_S], u / FEW_S);
         tc::fence_after();
         const uint32_t S = sm.tmem + FEW_ROWS * (u % FEW_S) + lane_base;
+        float part[4] = {0.f, 0.f, 0.f, 0.f};
         // (columns past the product's hold what earlier ones left; no row there sees a key)
         for (int g = 0; 32 * g < rows; ++g) {
           float v[32];
@@ -673,8 +676,13 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) k_weigh_few(const __grid_const
         }
         tc::fence_before();
         tc::mbar_arrive(&sm.barE[u % FEW_S]);
+        const float tile = (part[0] + part[1]) + (part[2] + part[3]);
+        if (qt & 1)
+          odd += tile;
+        else
+          even += tile;
       }
-      const float sum = (part[0] + part[1]) + (part[2] + part[3]);
+      const float sum = even + odd;
       if (at && sum != 0.f) atomicAdd(at, sum);
       fresh = run.last_of_head();
     }

@@ -251,7 +251,8 @@ def attn_paged_weights(q, k_pages, lse, table, ql, kl, weights, scale, eps=0.0):
             l = lse[rows, h, None]
             z = scale * (q[rows, h] @ kp.reshape(-1, Hk, d)[flat, kh].T)
             p = torch.where(hidden | (l == -math.inf), 0.0, torch.exp(z - l))
-            # of each term: the score, the exponent's two roundings, ex2; and a chain of additions
+            # of each term: the score, the exponent's two roundings, ex2; and chains of at most 64 + n G / 128
+            # additions (a query tile's terms in four, 32 each, or 16; then tile by tile, joins)
             off = p * (eps + (z.abs() + torch.where(l.isinf(), 0.0, l.abs())) * 2.0 ** -22 + 2.0 ** -21
                        + (64 + n * G / 128) * 2.0 ** -24)
             for x, y in ((w, p), (tol, off)):
