@@ -20,10 +20,10 @@
 // round's rows are on their way meanwhile.
 //
 // Bound: HBM, 4 bytes a key and head and 1,024 a row that stays.  32 caches of 1 to 16214 keys,
-// 4096 kept of 4 heads: 92 us, the copies 71 (424 MB of traffic, 6.0 TB/s; a plain copy with as
-// much 65), the lists some 20, by the longest cache's block.  1024 keys, 512 kept: 10 us,
-// latencies.  In place the walk's rounds bound: the 32 caches, with a block to a list, 105 us,
-// one of 65536 keys, half of them kept, by clusters of eight 115 (into other pages 46).
+// 4096 kept of 4 heads: 89 us, the copies some 70 (424 MB of traffic, 6.0 TB/s; a plain copy with as
+// much 65), the lists some 20, by the longest cache's block.  1024 keys, 512 kept: 9 us,
+// latencies.  In place the walk's rounds bound: the 32 caches, with a block to a list, 100 us,
+// one of 65536 keys, half of them kept, by clusters of eight 113 (into other pages 43).
 #include <stdint.h>
 
 #include "gdn_kernels.cuh"
@@ -36,14 +36,16 @@ namespace {
 constexpr int SELECT_THREADS = 1024, SELECT_WARPS = SELECT_THREADS / 32;
 constexpr int SELECT_HELD = 49152;  // weights that shared memory holds
 // Bits of a digit.  With eight, weights of few binades meet in a few dozen places, and a warp's
-// additions there wait for one another (32 caches in all 94 us, with eleven 92).
+// additions there wait for one another (the 32 caches 2 us more).
 constexpr int DIGIT = 11;
 constexpr int PASSES = (32 + DIGIT - 1) / DIGIT;
 static_assert(1 << DIGIT == 2 * SELECT_THREADS, "two digits to a thread");
-// Rows of a list to a block, 16 side by side: 32 caches in all 98 us, with 64 rows 111, with 128
-// 156 (fewer blocks to an SM; with six of 32 rows instead of eight 103).
+// Rows of a list to a block, 16 side by side: the 32 caches into other pages 89 us, with 64 rows 101,
+// with 128 124 (fewer blocks to an SM; with six of 32 rows instead of eight 94).
 constexpr int MOVE_THREADS = 256, MOVE_ROWS = 32;
-constexpr int WALK_THREADS = 1024, WALK_ROWS = 128;  // (64 rows to a round 160 us for 131, 256 149)
+// Rows to a round of a block in place: 65536 keys, half kept, 113 us, the 32 caches 100; with 64 rows 147 and
+// 109, with 256, which spill, 176 and 276.
+constexpr int WALK_THREADS = 1024, WALK_ROWS = 128;
 
 // The sequence's keys, and where the ones that always stay begin.
 struct Cut {
@@ -279,7 +281,8 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1) k_evict_select(const __grid
     const uint32_t all = __shfl_sync(0xffffffffu, upto, 31);
     out += (int)(all & 0xffffu);
     seen += (int)(all >> 16);
-  }  if (C > 1) meet();  // no CTA ends while another reads its counts
+  }
+  if (C > 1) meet();  // no CTA ends while another reads its counts
 }
 
 // Keys, values and weight of row `row` (page * page size + row in it), one lane's share of 16.
