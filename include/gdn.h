@@ -398,6 +398,8 @@ int gdn_decay_bwd(const void* q, const void* k, const void* v, const float* deca
  * keys.  A query that sees no key (n > m, or m = 0) has o = 0, lse = -inf and
  * passes no gradient.  One that sees a score of NaN or plus infinity (or one too large
  * for fp32) has o and lse NaN, however the keys are split.
+ * Values of v are finite: a row of v that is not may make o NaN of queries that do not
+ * see it, too (they count it zero times; lse is right).
  * q, o [total_q, Hq, d], k, v [total_k, Hk, d] bf16, d = 128, Hq a multiple of
  * Hk, at most 128 query heads to a key head (q_stride, k_stride, v_stride as for
  * the single-token forms); lse [total_q, Hq] fp32 (NULL = not written);
@@ -499,7 +501,7 @@ int gdn_rope_append(const void* q, const void* k, const void* v, const float* q_
  * outside 0 .. n_pages - 1 is an absent page, whose keys nobody sees (a row that sees no
  * other has o = 0, lse = -inf).  k_len is held within max_pages * page_size (at most
  * 2^30).  Rows past k_len may hold anything.  Sequences may share pages.  q [total_q, Hq,
- * d], cu_q, o, lse, scale, max_k, status and non-finite scores as for gdn_attn_fwd; max_q
+ * d], cu_q, o, lse, scale, max_k, status, scores and values that are not finite as for gdn_attn_fwd; max_q
  * bounds a sequence's new tokens as max_k does its keys (0: not known; up to 128 / (Hq/Hk)
  * it says that a kernel for few rows suits, which takes longer sequences too).  ws: at least
  * gdn_attn_paged_workspace_bytes(n_seqs, total_q, max_pages * page_size, max_q, max_k, Hq, Hk,
@@ -527,7 +529,8 @@ int gdn_rope_append(const void* q, const void* k, const void* v, const float* q_
  * the keys that stay of each sequence (the same for all heads); it must not overlap k_len.
  * Keys on absent pages never stay; a row whose target page is absent is not written.  In
  * place, no page may occur twice in the tables; otherwise no target page may, nor may one
- * hold a key of any sequence of the call.  ws: gdn_cache_evict_workspace_bytes(n_seqs, max_pages *
+ * hold a key of any sequence of the call.  (A copy of page_table as to_table is such a case: rows
+ * would be overwritten that others still read.)  ws: gdn_cache_evict_workspace_bytes(n_seqs, max_pages *
  * page_size, budget, Hk) bytes, without a status word (no kernel of it waits).
  */
 size_t gdn_attn_paged_workspace_bytes(int n_seqs, int total_q, int max_rows, int max_q, int max_k,

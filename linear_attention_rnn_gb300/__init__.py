@@ -985,8 +985,10 @@ def cache_evict(k_pages, v_pages, weights, page_table, k_len, budget: int, *, re
     """Drops the lightest keys of a paged cache: of each sequence and key head the last `recent`
     keys stay and of the others those with the largest weights [pages, Hk, page_size] (ties: the
     lowest index), `budget` in all.  What stays moves in its order, with its values and weights, to
-    the first rows of the pages that to_table [n, ..] lists (None: the sequence's own, in place;
-    no page may occur twice then; other target pages may not either, nor hold a key of the call).
+    the first rows of the pages that to_table [n, ..] lists (None, or page_table itself: the
+    sequence's own, in place; no page may occur twice then).  Other target pages may not occur twice
+    either, nor hold a key of the call: a copy of page_table is such a target, whose rows would be
+    written while others still read them; leave to_table out instead.
     Returns the new lengths, int32 [n] (new_len, if given; it must not overlap k_len)."""
     ks = _check_pages(k_pages, "k_pages")
     P, page, Hk, d = k_pages.shape
