@@ -13,6 +13,10 @@
 // tiles its two groups of warps take in turn; k_paged_few (for calls whose sequences are
 // known to fit one query tile) holds one against tiles of 64 keys, two CTAs to an SM.
 //
+// P meets V rounded once to bf16, the only type that the product takes beside V's; scores, maxima, sums (of
+// the p as they were), O and parts are fp32.  The rounding is as large as that of the result: o is off by
+// 2.3e-3 in the 2-norm, where the exact result in bf16 is by 1.7e-3.
+//
 // Bounds.  Chunks of prompts: the tensor rate, 2048 tokens over 32768 keys with 16/4 heads take
 // 308 us, 1.73 PFLOP/s (tensor pipe 77% busy; CTAs that each took one item 367).  Tokens: HBM,
 // 32 of them over 1 to 16214 keys take 92 us for 532 MB, 5.8 TB/s (an equal number of key tiles

@@ -20,7 +20,7 @@
 // round's rows are on their way meanwhile.
 //
 // Bound: HBM, 4 bytes a key and head and 1,024 a row that stays.  32 caches of 1 to 16214 keys,
-// 4096 kept of 4 heads: 89 us, the copies some 70 (424 MB of traffic, 6.0 TB/s; a plain copy with as
+// 4096 kept of 4 heads: 89 us in a row of calls, the copies some 70 (424 MB of traffic, 6.0 TB/s; a plain copy with as
 // much 65), the lists some 20, by the longest cache's block.  1024 keys, 512 kept: 9 us,
 // latencies.  In place the walk's rounds bound: the 32 caches, with a block to a list, 100 us,
 // one of 65536 keys, half of them kept, by clusters of eight 113 (into other pages 43).
